@@ -56,7 +56,8 @@ typedef enum {
   MIS_ERR_WORKSPACE = 4,      /* workspace missing, misaligned or too small    */
   MIS_ERR_CUDA = 5,           /* a CUDA runtime/driver call failed             */
   MIS_ERR_DEVICE_TIMEOUT = 6, /* a kernel wait ran out of time and bailed out  */
-  MIS_ERR_DEVICE_INDEX = 7    /* a device-side index was out of range          */
+  MIS_ERR_DEVICE_INDEX = 7,   /* a device-side index was out of range          */
+  MIS_ERR_DEVICE_PAGES = 8    /* the free list of a paged cache ran out        */
 } mis_status_t;
 
 const char* mis_status_string(int status);
@@ -409,6 +410,155 @@ mis_status_t mis_label_scores(const void* hidden, int64_t hidden_row_stride, int
                               const int32_t* delim_positions, int32_t M,
                               const int32_t* label_token_ids, int32_t K, float* out_logprobs,
                               float* out_renorm, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged K/V cache. The cache of the knock-knock second request
+ * ("Turbocharging LinkedIn's recommendation systems with SGLang") kept in
+ * pages of page_size rows that requests take from a free list as they grow.
+ * mis_paged_extend() gives a batch's new rows their pages and slots,
+ * mis_paged_write_kv() stores K/V rows at slots, and
+ * mis_tree_attention_fwd() attends from drafted tokens (or single tokens) to
+ * the cache and to each other. Lengths, tables and maps stay on the device,
+ * so a step of any lengths can be captured into a graph and replayed.
+ *   k, v        — device bf16. Row r of page p, head h starts at element
+ *                 p*page_stride + r*row_stride + h*head_stride of either
+ *                 buffer; its D elements are contiguous
+ *   page_size   — 16, 32, 64, 128 or 256 rows; n_pages * page_size < 2^31
+ *   D           — 64 or 128
+ *   strides     — in elements, multiples of 8, K and V alike; no two rows
+ *                 may overlap (a stride whose extent is 1 is not used). Both
+ *                 [page][row][head] and [page][head][row] orders, and K and V
+ *                 interleaved in one buffer, fit. k and v 16-byte aligned
+ * "Slot" s is row s % page_size of page s / page_size. A request's row at
+ * position p lies in page block_table[p / page_size] of its table row.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  void* k;
+  void* v;
+  int32_t n_pages, page_size, Hkv, D;
+  int64_t page_stride, row_stride, head_stride;
+} mis_paged_cache;
+
+/* Block tables and slot maps from request lengths, on the device. Request b
+ * holds cache_len[b] rows and gains new_len[b]; the pages it still needs,
+ *     need_b = ceil((cache_len[b] + new_len[b]) / page_size)
+ *            - ceil(cache_len[b] / page_size),
+ * come from the free list in request order: free_pages[free_head + need_0 +
+ * ... + need_(b-1)] onwards.
+ *   B, T          — requests (>= 1); rows of slot_map / position_ids (>= 0)
+ *   page_size, n_pages — of the cache
+ *   new_len, cache_len — device int32 [B]
+ *   cache_len_out — device int32 [B]: cache_len + new_len
+ *   block_table   — device int32 [B, max_pages], row stride
+ *                   block_table_stride (elements, >= max_pages): the old
+ *                   pages' entries are read, the new pages' entries written,
+ *                   nothing else changes
+ *   free_pages    — device int32 [n_free]; free_head device int32 [1], the
+ *                   entries taken so far; free_head_out [1] the same after
+ *                   this call
+ *   cu_new        — device int32 [B+1] out: request b's new rows are
+ *                   [cu_new[b], cu_new[b+1])
+ *   slot_map      — device int32 [T] out: the slot of every new row, -1 for
+ *                   rows from cu_new[B] on
+ *   position_ids  — device int32 [T] out or NULL: the row's position in its
+ *                   request (cache_len[b] + d), 0 for rows from cu_new[B] on
+ * cache_len_out may be cache_len and free_head_out free_head (in place);
+ * other overlaps are not allowed. All pointers 4-byte aligned.
+ * Refused requests gain no rows and no pages (their lengths stay, cu_new
+ * gives them no rows), the others are served:
+ *   - a negative length, or one past max_pages * page_size rows, and a
+ *     request whose rows (counted over all requests of valid length) pass T:
+ *     MIS_ERR_DEVICE_INDEX in the workspace status
+ *   - a request that needs pages when the free list has fewer left than it
+ *     and the requests before it need: MIS_ERR_DEVICE_PAGES. A later request
+ *     that needs no page is still served.
+ * A page id outside [0, n_pages) gives its rows the slot -1 (and, fresh, the
+ * table entry -1) and MIS_ERR_DEVICE_INDEX.
+ * Workspace: device, 256-byte aligned, >= mis_paged_extend_workspace_size(B)
+ * (0 for an invalid B). One call at a time may use a workspace. */
+size_t mis_paged_extend_workspace_size(int32_t B);
+mis_status_t mis_paged_extend(int32_t B, int32_t T, int32_t page_size, int32_t n_pages,
+                              const int32_t* new_len, const int32_t* cache_len,
+                              int32_t* cache_len_out, int32_t* block_table, int32_t max_pages,
+                              int64_t block_table_stride, const int32_t* free_pages,
+                              int32_t n_free, const int32_t* free_head, int32_t* free_head_out,
+                              int32_t* cu_new, int32_t* slot_map, int32_t* position_ids,
+                              void* workspace, size_t ws_bytes, void* stream);
+
+/* Store K/V rows at cache slots, K rotated on the way if asked:
+ *     cache row slot_map[i] = (rope(k[s_i], position_ids[i]), v[s_i]),
+ *     s_i = src_rows[i], or i when src_rows is NULL,  i = 0 .. n-1.
+ *   k, v          — device bf16 [T, Hkv, D], row strides in elements (>=
+ *                   Hkv*D, multiples of 8), 16-byte aligned; not the cache
+ *   slot_map      — device int32 [n]; a negative slot skips its row (the
+ *                   padding of mis_paged_extend). Slots must differ: two rows
+ *                   at one slot leave pieces of either
+ *   src_rows      — device int32 [n] or NULL (then n <= T): the rows to
+ *                   store, e.g. the accepted nodes of a drafted tree; repeats ok
+ *   position_ids  — device int32 [n] or NULL for no rotation. Rotate-half
+ *                   form of mis_rope_qk: the pair (x[i], x[i + D/2]) turns by
+ *                   p * rope_base^(-2i/D); the angle is kept as a 64-bit
+ *                   fraction of a turn, so far positions lose nothing
+ *   rope_base     — > 1, read only with position_ids
+ * A slot past the cache or a source row outside [0, T) stores nothing and
+ * sets MIS_ERR_DEVICE_INDEX. One kernel; n = 0 enqueues nothing and leaves
+ * the status word. Workspace: device, 256-byte aligned, >=
+ * mis_paged_write_workspace_size(). */
+size_t mis_paged_write_workspace_size(void);
+mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const void* k, const void* v,
+                                int64_t k_row_stride, int64_t v_row_stride, int32_t T,
+                                const int32_t* src_rows, const int32_t* slot_map, int32_t n,
+                                const int32_t* position_ids, double rope_base, void* workspace,
+                                size_t ws_bytes, void* stream);
+
+/* Attention of drafted token trees over a paged cache. Request b brings the
+ * rows [cu_nodes[b], cu_nodes[b+1]) of q, k, v: the nodes of a tree (a chain,
+ * or one decoded token) that continues its cached rows. A node sees every
+ * cached row of its request, its ancestors and itself:
+ *     o_i = sum_j p_ij v_j,  p_ij = softmax_j(scale * q_i k_j),
+ *     j in [0, cache_len[b]) (cached) and j on the path from i to its root.
+ * The nodes' own K/V are read from k and v (already rotated), not from the
+ * cache; mis_paged_write_kv() stores the ones that were accepted.
+ *   B, T      — requests, rows of q, k, v, o (>= 0); Hq a multiple of Hkv
+ *   max_nodes — upper bound on a request's nodes, 1 .. MIS_TREE_MAX_NODES
+ *   scale     — softmax scale, finite; 0 selects 1/sqrt(D)
+ *   q, k, v, o, lse, row strides — as in mis_attention_fwd_plan (lse fp32
+ *               [Hq, T] or NULL). Rows from cu_nodes[B] on are not written
+ *   block_table — device int32 [B, max_pages], row stride in elements
+ *   cache_len — device int32 [B], 0 .. max_pages * page_size
+ *   cu_nodes  — device int32 [B+1], non-decreasing, within [0, T]
+ *   parents   — device int32 [T]: the parent's index inside the request
+ *               (below the node's own), MIS_TREE_ROOT (-1), or
+ *               MIS_TREE_UNUSED (-2): the row sees nothing (o = 0, lse =
+ *               -inf) and no row sees it, its children count as roots.
+ *               NULL: every request is a chain (node i's parent is i - 1)
+ * What a node does not see never reaches it, whatever its value (NaN and
+ * infinities in unused cache rows or in other branches included). A row none
+ * of whose visible scores is above -inf gets o = 0 and lse = -inf.
+ * Found on the device, reported as MIS_ERR_DEVICE_INDEX: a request with a
+ * bad cache_len, more than max_nodes rows, or a bad cu_nodes range is
+ * skipped (its rows are not written); a page id outside the cache hides its
+ * rows; a parent out of range counts as MIS_TREE_ROOT.
+ * fp32 scores, statistics and accumulation; probabilities are rounded to
+ * bf16 for the second product, o to bf16. The same call gives the same bits.
+ * Workspace: device, 256-byte aligned, >= mis_tree_attention_workspace_size()
+ * (0 for an invalid descriptor); one call at a time may use it. */
+#define MIS_TREE_MAX_NODES 256
+#define MIS_TREE_ROOT (-1)
+#define MIS_TREE_UNUSED (-2)
+typedef struct {
+  int32_t B, T, Hq, max_nodes;
+  float scale;
+} mis_tree_desc;
+size_t mis_tree_attention_workspace_size(const mis_tree_desc* desc, const mis_paged_cache* cache);
+mis_status_t mis_tree_attention_fwd(const mis_tree_desc* desc, const mis_paged_cache* cache,
+                                    const void* q, const void* k, const void* v, void* o,
+                                    float* lse, int64_t q_row_stride, int64_t k_row_stride,
+                                    int64_t v_row_stride, int64_t o_row_stride,
+                                    const int32_t* block_table, int32_t max_pages,
+                                    int64_t block_table_stride, const int32_t* cache_len,
+                                    const int32_t* cu_nodes, const int32_t* parents,
+                                    void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Device status of the last call that used `workspace` (a plan workspace or

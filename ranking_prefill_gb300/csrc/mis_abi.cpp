@@ -191,6 +191,7 @@ const char* mis_status_string(int status) {
     case MIS_ERR_CUDA: return "CUDA call failed";
     case MIS_ERR_DEVICE_TIMEOUT: return "a device wait ran out of time";
     case MIS_ERR_DEVICE_INDEX: return "a device-side index was out of range";
+    case MIS_ERR_DEVICE_PAGES: return "the free list of a paged cache ran out";
     default: return "unknown status";
   }
 }
@@ -583,6 +584,7 @@ mis_status_t mis_get_device_status(const void* workspace, void* stream) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return MIS_ERR_CUDA;
   if (w[0] & kDevTimeout) return MIS_ERR_DEVICE_TIMEOUT;
   if (w[0] & kDevIndex) return MIS_ERR_DEVICE_INDEX;
+  if (w[0] & kDevPages) return MIS_ERR_DEVICE_PAGES;
   return MIS_OK;
 }
 

@@ -22,6 +22,7 @@ constexpr size_t kStatusBytes = 256;
 // Bits of the device status word (workspace offset 0).
 constexpr uint32_t kDevTimeout = 1u;
 constexpr uint32_t kDevIndex = 2u;
+constexpr uint32_t kDevPages = 4u;
 
 // Key-tile list entry: absolute first key row | (needs element mask << 31).
 constexpr uint32_t kNeedMask = 0x80000000u;
@@ -120,6 +121,9 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 
 // Raise a kernel's dynamic shared-memory limit once per device.
 bool kernel_attr_once(const void* kernel, int smem_bytes);
+
+// Host-side checks of a paged cache's descriptor (mis_paged.cu).
+mis_status_t check_paged_cache(const mis_paged_cache* c);
 
 // Process-wide wait limit for the kernels' bounded waits.
 uint64_t wait_limit_ns();

@@ -1,0 +1,422 @@
+// Paged K/V cache for sm_103a: block tables and slot maps from request
+// lengths, and K/V rows stored at slots (K rotated on the way).
+//
+// mis_paged_extend. need_b = ceil((L_b + n_b) / ps) - ceil(L_b / ps) pages of
+// request b are the run of the free list that starts at the exclusive sum of
+// need; its rows start at the exclusive sum of n. One block takes both sums
+// over the batch and leaves a record per request; the rows' slots follow from
+// the record of their request (found by bisection of cu_new) and one page id.
+//
+// mis_paged_write_kv is a copy: every kept row is read and written once, so
+// HBM bounds it (a decoding step: the launch).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "mis_internal.h"
+#include "mis_ptx.cuh"
+
+namespace mis {
+namespace {
+
+using namespace dev;
+
+constexpr int kPlanThreads = 1024;
+constexpr int kFillThreads = 256;
+
+// What the rows of a request need to find their slots.
+struct ExtendRec {
+  int32_t len;    // rows cached before the call
+  int32_t have;   // pages held before the call
+  int32_t first;  // free-list index of its first fresh page
+  int32_t pad;
+};
+
+struct ExtendParams {
+  int32_t B, T, page_size, n_pages, max_pages, n_free;
+  const int32_t* new_len;
+  const int32_t* cache_len;
+  int32_t* cache_len_out;
+  int32_t* table;
+  int64_t table_stride;
+  const int32_t* free_pages;
+  const int32_t* free_head;
+  int32_t* free_head_out;
+  int32_t* cu_new;
+  int32_t* slot_map;
+  int32_t* position_ids;
+  uint32_t* status;
+  ExtendRec* rec;
+};
+
+// Inclusive sum over the block's threads; *total = the sum of all.
+__device__ int64_t block_sum(int64_t x, int64_t* total, int64_t* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();                       // the previous call's readers are done
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  *total = warp_sums[31];
+  return x + (warp ? warp_sums[warp - 1] : 0);
+}
+
+// Slot and position of row t (and the table entry of a page that starts there).
+__device__ __forceinline__ void fill_row(const ExtendParams& p, int t, int total) {
+  int slot = -1, pos = 0;
+  if (t < total) {
+    int lo = 0, hi = p.B - 1;            // first b with cu_new[b + 1] > t
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (p.cu_new[mid + 1] > t) hi = mid; else lo = mid + 1;
+    }
+    const ExtendRec r = p.rec[lo];
+    pos = r.len + (t - p.cu_new[lo]);
+    const int col = pos / p.page_size, off = pos % p.page_size;
+    int32_t* entry = p.table + (int64_t)lo * p.table_stride + col;
+    const bool fresh = col >= r.have;
+    int page = fresh ? p.free_pages[r.first + (col - r.have)] : *entry;
+    if (page < 0 || page >= p.n_pages) {
+      page = -1;
+      raise_status(p.status, kDevIndex, 0x21);
+    }
+    if (fresh && off == 0) *entry = page;
+    if (page >= 0) slot = page * p.page_size + off;
+  }
+  p.slot_map[t] = slot;
+  if (p.position_ids) p.position_ids[t] = pos;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+mis_paged_extend_kernel(const ExtendParams p) {
+  __shared__ int64_t warp_sums[32];
+  __shared__ int s_head;
+  __shared__ uint32_t s_bits, s_taken;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (threadIdx.x == 0) {
+    s_head = *p.free_head;
+    s_bits = s_taken = 0;
+  }
+  __syncthreads();
+  const int head = s_head;
+  const bool head_ok = head >= 0 && head <= p.n_free;
+  const int64_t avail = head_ok ? p.n_free - head : 0;
+  const int64_t cap = (int64_t)p.max_pages * p.page_size;
+  uint32_t bits = head_ok ? 0u : kDevIndex;
+  int64_t pages0 = 0, rows0 = 0, cu0 = 0, taken = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    int64_t len = 0, n = 0, need = 0;
+    int have = 0;
+    if (b < p.B) {
+      len = p.cache_len[b];
+      n = p.new_len[b];
+      if (len < 0 || n < 0 || len + n > cap) {
+        bits |= kDevIndex;
+        n = 0;
+      } else {
+        have = (int)((len + p.page_size - 1) / p.page_size);
+        need = (len + n + p.page_size - 1) / p.page_size - have;
+      }
+    }
+    int64_t pages, rows, granted;
+    const int64_t pend = pages0 + block_sum(need, &pages, warp_sums);
+    const int64_t rend = rows0 + block_sum(n, &rows, warp_sums);
+    bool ok = true;
+    if (need > 0 && pend > avail) { bits |= kDevPages; ok = false; }
+    if (n > 0 && rend > p.T) { bits |= kDevIndex; ok = false; }
+    const int64_t g = ok ? n : 0;
+    const int64_t gend = cu0 + block_sum(g, &granted, warp_sums);
+    if (ok && need > 0 && pend > taken) taken = pend;
+    if (b < p.B) {
+      ExtendRec r;
+      r.len = (int32_t)len;
+      r.have = have;
+      r.first = (int32_t)(ok ? head + pend - need : 0);
+      r.pad = 0;
+      p.rec[b] = r;
+      p.cu_new[b + 1] = (int32_t)gend;
+      p.cache_len_out[b] = (int32_t)(len + g);
+    }
+    pages0 += pages;
+    rows0 += rows;
+    cu0 += granted;
+  }
+  // granted requests that took pages are a prefix of those that need any, so
+  // the furthest end of a granted run is where the list continues
+  if (bits) atomicOr(&s_bits, bits);
+  if (taken) atomicMax(&s_taken, (uint32_t)taken);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    p.cu_new[0] = 0;
+    *p.free_head_out = head + (int)s_taken;
+    p.status[0] = s_bits;
+    p.status[1] = s_bits ? 0x20u : 0u;
+  }
+}
+
+__global__ void __launch_bounds__(kFillThreads)
+mis_paged_fill_kernel(const ExtendParams p) {
+  griddep_wait();
+  const int total = p.cu_new[p.B];
+  for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < p.T;
+       t += (int64_t)gridDim.x * blockDim.x)
+    fill_row(p, (int)t, total);
+}
+
+// ------------------------------------------------------------------- write
+struct WriteParams {
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* kc;
+  __nv_bfloat16* vc;
+  int64_t ks, vs;                    // source row strides, elements
+  int64_t page_stride, row_stride, head_stride;
+  const int32_t* src;                // or null
+  const int32_t* slot;
+  const int32_t* pos;                // or null: no rotation
+  int32_t n, T, Hkv;
+  int32_t page_shift;
+  int64_t n_slots;
+  uint32_t* status;
+  uint64_t turn[64];                 // base^(-2i/D) / (2 pi) as a 64-bit fraction of a turn
+};
+
+__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// sin and cos of position p times a frequency given as a 64-bit fraction of a
+// turn: the product modulo 2^64 is the fraction of a turn left after whole
+// turns, exact up to p * 2^-64, whatever p. Its top 32 bits, read as signed,
+// are an angle in [-pi, pi), where the SFU approximations are good to 2^-21.
+__device__ __forceinline__ void sincos_turn(int32_t p, uint64_t f, float& sn, float& cs) {
+  const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32), up = (uint32_t)p;
+  uint32_t frac = __umulhi(up, lo) + up * hi;
+  if (p < 0) frac -= lo;
+  const float x = (float)(int32_t)frac * 1.46291807926715968e-9f;   // 2 pi / 2^32
+  asm("sin.approx.f32 %0, %1;" : "=f"(sn) : "f"(x));
+  asm("cos.approx.f32 %0, %1;" : "=f"(cs) : "f"(x));
+}
+
+template <int D>
+__global__ void __launch_bounds__(256)
+mis_paged_write_kernel(const WriteParams p) {
+  constexpr int HALF = D / 2, NC = HALF / 8;
+  griddep_wait();
+  if (blockIdx.x == 0) {
+    // one block looks over every index and writes the status word
+    uint32_t bad = 0;
+    for (int i = threadIdx.x; i < p.n; i += blockDim.x) {
+      const int s = p.slot[i];
+      if (s < 0) continue;
+      if (s >= p.n_slots) bad = 1;
+      const int r = p.src ? p.src[i] : i;
+      if (r < 0 || r >= p.T) bad = 1;
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) {
+      p.status[0] = bad ? kDevIndex : 0u;
+      p.status[1] = bad ? 0x30u : 0u;
+    }
+    return;
+  }
+  const int64_t gid = (int64_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x;
+  const int c = (int)(gid % NC);
+  const int64_t cell = gid / NC;
+  const int h = (int)(cell % p.Hkv);
+  const int64_t i = cell / p.Hkv;
+  if (i >= p.n) return;
+  const int s = p.slot[i];
+  const int r = p.src ? p.src[i] : (int)i;
+  if (s < 0 || s >= p.n_slots || r < 0 || r >= p.T) return;
+  const int64_t at = (int64_t)(s >> p.page_shift) * p.page_stride +
+                     (int64_t)(s & ((1 << p.page_shift) - 1)) * p.row_stride +
+                     (int64_t)h * p.head_stride + c * 8;
+  const __nv_bfloat16* ks = p.k + (int64_t)r * p.ks + (int64_t)h * D + c * 8;
+  const __nv_bfloat16* vs = p.v + (int64_t)r * p.vs + (int64_t)h * D + c * 8;
+  uint4 a = *reinterpret_cast<const uint4*>(ks), b = *reinterpret_cast<const uint4*>(ks + HALF);
+  const uint4 va = *reinterpret_cast<const uint4*>(vs), vb = *reinterpret_cast<const uint4*>(vs + HALF);
+  if (p.pos) {
+    const int pos = p.pos[i];
+    float x[8], y[8];
+    unpack8(a, x);
+    unpack8(b, y);
+    uint32_t wa[4], wb[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float s0, c0, s1, c1;
+      sincos_turn(pos, p.turn[c * 8 + 2 * e], s0, c0);
+      sincos_turn(pos, p.turn[c * 8 + 2 * e + 1], s1, c1);
+      const float x0 = x[2 * e], x1 = x[2 * e + 1], y0 = y[2 * e], y1 = y[2 * e + 1];
+      wa[e] = pack_bf16(x0 * c0 - y0 * s0, x1 * c1 - y1 * s1);
+      wb[e] = pack_bf16(y0 * c0 + x0 * s0, y1 * c1 + x1 * s1);
+    }
+    a = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+    b = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+  }
+  *reinterpret_cast<uint4*>(p.kc + at) = a;
+  *reinterpret_cast<uint4*>(p.kc + at + HALF) = b;
+  *reinterpret_cast<uint4*>(p.vc + at) = va;
+  *reinterpret_cast<uint4*>(p.vc + at + HALF) = vb;
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+bool page_size_ok(int32_t ps) {
+  return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256;
+}
+
+mis_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MIS_OK : MIS_ERR_CUDA; }
+
+}  // namespace
+
+mis_status_t check_paged_cache(const mis_paged_cache* c) {
+  if (!c || !c->k || !c->v) return MIS_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return MIS_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->Hkv < 1) return MIS_ERR_INVALID_ARG;
+  if (!page_size_ok(c->page_size) || (c->D != 64 && c->D != 128)) return MIS_ERR_UNSUPPORTED;
+  if ((int64_t)c->n_pages * c->page_size > 0x7fffffff) return MIS_ERR_SHAPE;
+  // the strides in use, smallest first, each past the extent of the ones below
+  int64_t st[3] = {c->row_stride, c->page_stride, c->head_stride};
+  int64_t ex[3] = {c->page_size, c->n_pages, c->Hkv};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (st[j] < st[i]) { std::swap(st[i], st[j]); std::swap(ex[i], ex[j]); }
+  int64_t width = c->D;
+  for (int i = 0; i < 3; ++i) {
+    if (ex[i] == 1) continue;
+    if (st[i] < width || (st[i] & 7) || st[i] >= (int64_t)1 << 38) return MIS_ERR_SHAPE;
+    width = st[i] * (ex[i] - 1) + width;
+  }
+  return MIS_OK;
+}
+
+}  // namespace mis
+
+using namespace mis;
+
+extern "C" size_t mis_paged_extend_workspace_size(int32_t B) {
+  return B < 1 ? 0 : kStatusBytes + (((size_t)B * sizeof(ExtendRec) + 255) & ~(size_t)255);
+}
+
+extern "C" mis_status_t mis_paged_extend(
+    int32_t B, int32_t T, int32_t page_size, int32_t n_pages, const int32_t* new_len,
+    const int32_t* cache_len, int32_t* cache_len_out, int32_t* block_table, int32_t max_pages,
+    int64_t block_table_stride, const int32_t* free_pages, int32_t n_free,
+    const int32_t* free_head, int32_t* free_head_out, int32_t* cu_new, int32_t* slot_map,
+    int32_t* position_ids, void* workspace, size_t ws_bytes, void* stream) {
+  if (B < 1 || T < 0 || n_pages < 1 || max_pages < 1 || n_free < 0) return MIS_ERR_INVALID_ARG;
+  if (!page_size_ok(page_size)) return MIS_ERR_UNSUPPORTED;
+  if ((int64_t)n_pages * page_size > 0x7fffffff || (int64_t)max_pages * page_size > 0x7fffffff ||
+      block_table_stride < max_pages)
+    return MIS_ERR_SHAPE;
+  if (!new_len || !cache_len || !cache_len_out || !block_table || !free_head || !free_head_out ||
+      !cu_new || (T > 0 && !slot_map) || (n_free > 0 && !free_pages))
+    return MIS_ERR_INVALID_ARG;
+  for (const void* ptr : {(const void*)new_len, (const void*)cache_len, (const void*)cache_len_out,
+                          (const void*)block_table, (const void*)free_pages,
+                          (const void*)free_head, (const void*)free_head_out, (const void*)cu_new,
+                          (const void*)slot_map, (const void*)position_ids})
+    if (!aligned(ptr, 4)) return MIS_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < mis_paged_extend_workspace_size(B))
+    return MIS_ERR_WORKSPACE;
+  ExtendParams p;
+  p.B = B; p.T = T; p.page_size = page_size; p.n_pages = n_pages; p.max_pages = max_pages;
+  p.n_free = n_free;
+  p.new_len = new_len; p.cache_len = cache_len; p.cache_len_out = cache_len_out;
+  p.table = block_table; p.table_stride = block_table_stride;
+  p.free_pages = free_pages; p.free_head = free_head; p.free_head_out = free_head_out;
+  p.cu_new = cu_new; p.slot_map = slot_map; p.position_ids = position_ids;
+  p.status = static_cast<uint32_t*>(workspace);
+  p.rec = reinterpret_cast<ExtendRec*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  try {
+    mis_status_t r = cuda_status(
+        launch_pdl(mis_paged_extend_kernel, dim3(1), dim3(kPlanThreads), 0, st, p));
+    if (r != MIS_OK || T == 0) return r;
+    const int64_t blocks = std::min<int64_t>(((int64_t)T + kFillThreads - 1) / kFillThreads,
+                                             8 * (int64_t)num_sms());
+    return cuda_status(launch_pdl(mis_paged_fill_kernel, dim3((unsigned)blocks),
+                                  dim3(kFillThreads), 0, st, p));
+  } catch (...) {
+    return MIS_ERR_CUDA;
+  }
+}
+
+extern "C" size_t mis_paged_write_workspace_size(void) { return kStatusBytes; }
+
+extern "C" mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const void* k,
+                                           const void* v, int64_t k_row_stride,
+                                           int64_t v_row_stride, int32_t T,
+                                           const int32_t* src_rows, const int32_t* slot_map,
+                                           int32_t n, const int32_t* position_ids,
+                                           double rope_base, void* workspace, size_t ws_bytes,
+                                           void* stream) {
+  const mis_status_t cs = check_paged_cache(cache);
+  if (cs != MIS_OK) return cs;
+  if (T < 0 || n < 0) return MIS_ERR_INVALID_ARG;
+  if (position_ids && (!(rope_base > 1.0) || !std::isfinite(rope_base))) return MIS_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < mis_paged_write_workspace_size())
+    return MIS_ERR_WORKSPACE;
+  if (!src_rows && n > T) return MIS_ERR_SHAPE;
+  const int64_t w = (int64_t)cache->Hkv * cache->D;
+  if (k_row_stride < w || v_row_stride < w || ((k_row_stride | v_row_stride) & 7))
+    return MIS_ERR_SHAPE;
+  if (n == 0) return MIS_OK;
+  if (!slot_map || !aligned(slot_map, 4) || !aligned(src_rows, 4) || !aligned(position_ids, 4))
+    return MIS_ERR_INVALID_ARG;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return MIS_ERR_INVALID_ARG;
+  WriteParams p;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.kc = static_cast<__nv_bfloat16*>(cache->k);
+  p.vc = static_cast<__nv_bfloat16*>(cache->v);
+  p.ks = k_row_stride; p.vs = v_row_stride;
+  p.page_stride = cache->page_stride; p.row_stride = cache->row_stride;
+  p.head_stride = cache->head_stride;
+  p.src = src_rows; p.slot = slot_map; p.pos = position_ids;
+  p.n = n; p.T = T; p.Hkv = cache->Hkv;
+  p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
+  p.n_slots = (int64_t)cache->n_pages * cache->page_size;
+  p.status = static_cast<uint32_t*>(workspace);
+  const int D = cache->D;
+  for (int i = 0; i < 64; ++i)
+    p.turn[i] = (position_ids && i < D / 2)
+                    ? (uint64_t)(std::pow(rope_base, -2.0 * i / D) / 6.283185307179586476925 *
+                                 18446744073709551616.0)
+                    : 0;
+  const int64_t threads = (int64_t)n * cache->Hkv * (D / 16);
+  const int64_t blocks = 1 + (threads + 255) / 256;
+  if (blocks > 0x7fffffff) return MIS_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  try {
+    return cuda_status(D == 128 ? launch_pdl(mis_paged_write_kernel<128>, dim3((unsigned)blocks),
+                                             dim3(256), 0, st, p)
+                                : launch_pdl(mis_paged_write_kernel<64>, dim3((unsigned)blocks),
+                                             dim3(256), 0, st, p));
+  } catch (...) {
+    return MIS_ERR_CUDA;
+  }
+}

@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(_HERE, "libmis_gb300.so")
 
 STATUS = {0: "MIS_OK", 1: "MIS_ERR_INVALID_ARG", 2: "MIS_ERR_SHAPE", 3: "MIS_ERR_UNSUPPORTED",
           4: "MIS_ERR_WORKSPACE", 5: "MIS_ERR_CUDA", 6: "MIS_ERR_DEVICE_TIMEOUT",
-          7: "MIS_ERR_DEVICE_INDEX"}
+          7: "MIS_ERR_DEVICE_INDEX", 8: "MIS_ERR_DEVICE_PAGES"}
 for _v, _n in STATUS.items():
     globals()[_n] = _v
 
@@ -37,7 +37,9 @@ EXPORTS = ["mis_status_string", "mis_abi_version", "mis_layout_size", "mis_build
            "mis_set_schedule", "mis_setwise_layout_size", "mis_build_setwise_layout",
            "mis_rope_qk", "mis_cached_plan_workspace_size", "mis_cached_plan_create",
            "mis_attention_fwd_cached", "mis_attention_fwd_plan_rope", "mis_rope_k_plan",
-           "mis_plan_exec_tiles"]
+           "mis_plan_exec_tiles", "mis_paged_extend_workspace_size", "mis_paged_extend",
+           "mis_paged_write_workspace_size", "mis_paged_write_kv",
+           "mis_tree_attention_workspace_size", "mis_tree_attention_fwd"]
 
 
 class MisError(RuntimeError):
@@ -59,6 +61,17 @@ class mis_cached_desc(C.Structure):
                 ("D", C.c_int32), ("scale", C.c_float),
                 ("cu_seqlens", C.c_void_p), ("item_ptr", C.c_void_p), ("item_offsets", C.c_void_p),
                 ("cache_start", C.c_void_p), ("cache_len", C.c_void_p), ("cache_T", C.c_int32)]
+
+
+class mis_paged_cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("n_pages", C.c_int32),
+                ("page_size", C.c_int32), ("Hkv", C.c_int32), ("D", C.c_int32),
+                ("page_stride", C.c_int64), ("row_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class mis_tree_desc(C.Structure):
+    _fields_ = [("B", C.c_int32), ("T", C.c_int32), ("Hq", C.c_int32), ("max_nodes", C.c_int32),
+                ("scale", C.c_float)]
 
 
 class mis_plan_stats(C.Structure):
@@ -126,6 +139,16 @@ def load(path: str = LIB_PATH):
         "mis_planner_destroy": (C.c_int, [vp]),
         "mis_label_scores_noalloc": (C.c_int, [vp, i64, C.c_int32, vp, C.c_int32, C.c_int32, vp,
                                                C.c_int32, i32p, C.c_int32, vp, vp, vp, vp]),
+        "mis_paged_extend_workspace_size": (sz, [C.c_int32]),
+        "mis_paged_extend": (C.c_int, [C.c_int32] * 4 + [vp] * 4 + [C.c_int32, i64, vp, C.c_int32] +
+                             [vp] * 6 + [sz, vp]),
+        "mis_paged_write_workspace_size": (sz, []),
+        "mis_paged_write_kv": (C.c_int, [C.POINTER(mis_paged_cache), vp, vp, i64, i64, C.c_int32, vp,
+                                         vp, C.c_int32, vp, C.c_double, vp, sz, vp]),
+        "mis_tree_attention_workspace_size": (sz, [C.POINTER(mis_tree_desc),
+                                                   C.POINTER(mis_paged_cache)]),
+        "mis_tree_attention_fwd": (C.c_int, [C.POINTER(mis_tree_desc), C.POINTER(mis_paged_cache)] +
+                                   [vp] * 5 + [i64] * 4 + [vp, C.c_int32, i64] + [vp] * 4 + [sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -547,6 +570,180 @@ def mis_label_scores_noalloc(hidden, w_lm, delim_positions, label_token_ids: Seq
                                       _dptr(delim_positions), M, _ptr_i32(labels), len(labels),
                                       _dptr(out_logprobs), _dptr(out_renorm), _dptr(device_status),
                                       _stream(stream)), "mis_label_scores_noalloc")
+
+
+# --------------------------------------------------------------- paged cache
+
+TREE_MAX_NODES, TREE_ROOT, TREE_UNUSED = 256, -1, -2
+
+
+def _require(ok, status: int, where: str):
+    if not ok:
+        raise MisError(status, where)
+
+
+def _on_device(where: str, dtype, *tensors):
+    """Every tensor (None passes) is of `dtype` on the current CUDA device."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for t in tensors:
+        if t is not None and (t.dtype != dtype or t.get_device() != dev):
+            raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+
+
+def _flat_i32(where: str, n: int, *tensors):
+    """Contiguous int32 vectors (None passes) of at least n elements on the current device."""
+    import torch
+    _on_device(where, torch.int32, *tensors)
+    for t in tensors:
+        if t is not None and (t.dim() != 1 or t.numel() < n or (t.numel() > 1 and t.stride(0) != 1)):
+            raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+
+
+def _rows_bf16(where: str, heads: int, D: int, *tensors):
+    """[T, heads, D] bf16 rows, heads packed inside a row, on the current device."""
+    import torch
+    _on_device(where, torch.bfloat16, *tensors)
+    for t in tensors:
+        if (t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.stride(2) != 1 or
+                (heads > 1 and t.stride(1) != D)):
+            raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+
+
+def _table(where: str, t):
+    import torch
+    _on_device(where, torch.int32, t)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _row_stride(t, width: int) -> int:
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _workspace(where: str, t) -> int:
+    import torch
+    _on_device(where, torch.uint8, t)
+    if not t.is_contiguous():
+        raise MisError(MIS_ERR_WORKSPACE, where)  # noqa: F821
+    return t.numel()
+
+
+class PagedCache:
+    """A paged K/V cache: k and v bf16 [n_pages, page_size, Hkv, D] with equal
+    strides and contiguous head rows (a [n_pages, Hkv, page_size, D] buffer
+    passes as its transpose(1, 2)). Keeps the tensors alive."""
+
+    def __init__(self, k, v):
+        import torch
+        where = "PagedCache"
+        _on_device(where, torch.bfloat16, k, v)
+        _require(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and
+                 k.stride(3) == 1, MIS_ERR_SHAPE, where)  # noqa: F821
+        self.k, self.v = k, v
+        self.n_pages, self.page_size, self.Hkv, self.D = k.shape
+        self.desc = mis_paged_cache(_dptr(k), _dptr(v), self.n_pages, self.page_size, self.Hkv, self.D,
+                                    k.stride(0), k.stride(1), k.stride(2))
+        self.ref = C.byref(self.desc)
+        self.device = k.get_device()
+
+
+class TreeDesc:
+    """Sizes of a mis_tree_attention_fwd call over `cache`."""
+
+    def __init__(self, cache: PagedCache, B: int, T: int, Hq: int, max_nodes: int, scale: float = 0.0):
+        self.cache, self.B, self.T, self.Hq, self.max_nodes = cache, B, T, Hq, max_nodes
+        self.desc = mis_tree_desc(B, T, Hq, max_nodes, scale)
+        self.ref = C.byref(self.desc)
+
+    def workspace_size(self) -> int:
+        n = int(load().mis_tree_attention_workspace_size(self.ref, self.cache.ref))
+        if n == 0:   # ask the call itself for the reason (no pointer is looked at before it)
+            L = load()
+            st = L.mis_tree_attention_fwd(self.ref, self.cache.ref, *([None] * 5), 0, 0, 0, 0, None, 0, 0,
+                                          *([None] * 4), 0, None)
+            _check(st or lib_status_unknown(), "mis_tree_attention_workspace_size")
+        return n
+
+
+def mis_paged_extend_workspace_size(B: int) -> int:
+    return int(load().mis_paged_extend_workspace_size(B))
+
+
+def mis_paged_extend(new_len, cache_len, cache_len_out, block_table, free_pages, free_head,
+                     free_head_out, cu_new, slot_map, position_ids, page_size: int, n_pages: int,
+                     workspace, stream=None):
+    """Pages and slots of a batch's new rows (all int32 device tensors): new_len,
+    cache_len, cache_len_out [B] (the last two may be one tensor), block_table
+    [B, max_pages], free_pages, free_head, free_head_out [1] (may be one),
+    cu_new [B+1], slot_map [T], position_ids [T] or None."""
+    L = load()
+    where = "mis_paged_extend"
+    B, T = new_len.numel(), slot_map.numel()
+    _flat_i32(where, 0, new_len, slot_map, free_pages)
+    _flat_i32(where, B, cache_len, cache_len_out)
+    _flat_i32(where, B + 1, cu_new)
+    _flat_i32(where, 1, free_head, free_head_out)
+    _flat_i32(where, T, position_ids)
+    stride = _table(where, block_table)
+    _require(block_table.shape[0] >= B, MIS_ERR_SHAPE, where)  # noqa: F821
+    _check(L.mis_paged_extend(B, T, page_size, n_pages, _dptr(new_len), _dptr(cache_len),
+                              _dptr(cache_len_out), _dptr(block_table), block_table.shape[1], stride,
+                              _dptr(free_pages), free_pages.numel(), _dptr(free_head),
+                              _dptr(free_head_out), _dptr(cu_new), _dptr(slot_map), _dptr(position_ids),
+                              _dptr(workspace), _workspace(where, workspace), _stream(stream)), where)
+
+
+def mis_paged_write_workspace_size() -> int:
+    return int(load().mis_paged_write_workspace_size())
+
+
+def mis_paged_write_kv(cache: PagedCache, k, v, slot_map, workspace, position_ids=None,
+                       base: float = 1.0e6, src_rows=None, stream=None):
+    """Store rows of k, v [T, Hkv, D] at the slots of slot_map [n] (negative: skip);
+    row src_rows[i], or i; K rotated at position_ids[i] if given."""
+    L = load()
+    where = "mis_paged_write_kv"
+    n, w = slot_map.numel(), cache.Hkv * cache.D
+    _rows_bf16(where, cache.Hkv, cache.D, k, v)
+    _require(k.shape[0] == v.shape[0], MIS_ERR_SHAPE, where)  # noqa: F821
+    _require(cache.device == k.get_device(), MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    _flat_i32(where, n, slot_map, position_ids, src_rows)
+    _check(L.mis_paged_write_kv(cache.ref, _dptr(k), _dptr(v), _row_stride(k, w), _row_stride(v, w),
+                                k.shape[0], _dptr(src_rows), _dptr(slot_map), n, _dptr(position_ids),
+                                float(base), _dptr(workspace), _workspace(where, workspace),
+                                _stream(stream)), where)
+
+
+def mis_tree_attention_fwd(desc: TreeDesc, q, k, v, o, lse, block_table, cache_len, cu_nodes, parents,
+                           workspace, stream=None):
+    """Attention of q [T, Hq, D] over the cached rows of block_table [B, max_pages]
+    up to cache_len [B] and over the ancestors among the request's own rows of
+    k, v [T, Hkv, D], [cu_nodes[b], cu_nodes[b+1]); parents [T] or None (chains);
+    o like q, lse fp32 [Hq, T] or None."""
+    import torch
+    L = load()
+    where = "mis_tree_attention_fwd"
+    c, T = desc.cache, desc.T
+    _rows_bf16(where, desc.Hq, c.D, q, o)
+    _rows_bf16(where, c.Hkv, c.D, k, v)
+    _require(c.device == q.get_device(), MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    _require(min(q.shape[0], k.shape[0], v.shape[0], o.shape[0]) >= T, MIS_ERR_SHAPE, where)  # noqa: F821
+    if lse is not None:
+        _on_device(where, torch.float32, lse)
+        _require(lse.is_contiguous() and lse.shape == (desc.Hq, T), MIS_ERR_SHAPE, where)  # noqa: F821
+    _flat_i32(where, desc.B, cache_len)
+    _flat_i32(where, desc.B + 1, cu_nodes)
+    _flat_i32(where, T, parents)
+    stride = _table(where, block_table)
+    _require(block_table.shape[0] >= desc.B, MIS_ERR_SHAPE, where)  # noqa: F821
+    wq, wk = desc.Hq * c.D, c.Hkv * c.D
+    _check(L.mis_tree_attention_fwd(desc.ref, c.ref, _dptr(q), _dptr(k), _dptr(v), _dptr(o), _dptr(lse),
+                                    _row_stride(q, wq), _row_stride(k, wk), _row_stride(v, wk),
+                                    _row_stride(o, wq), _dptr(block_table), block_table.shape[1], stride,
+                                    _dptr(cache_len), _dptr(cu_nodes), _dptr(parents), _dptr(workspace),
+                                    _workspace(where, workspace), _stream(stream)), where)
 
 
 def mis_get_device_status(workspace, stream=None) -> int:
