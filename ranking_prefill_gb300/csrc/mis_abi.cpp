@@ -62,8 +62,8 @@ namespace {
 struct TmapKey {
   const void* base;
   int rank;
-  uint64_t dims[3], strides[2];
-  uint32_t box[3];
+  uint64_t dims[4], strides[3];
+  uint32_t box[4];
   bool operator==(const TmapKey& o) const {
     return base == o.base && rank == o.rank && std::memcmp(dims, o.dims, sizeof(dims)) == 0 &&
            std::memcmp(strides, o.strides, sizeof(strides)) == 0 &&
@@ -87,8 +87,8 @@ CUtensorMap make_tmap_bf16(const void* base, int rank, const uint64_t* dims,
   std::memset(&key, 0, sizeof(key));
   key.base = base;
   key.rank = rank;
-  for (int i = 0; i < rank && i < 3; ++i) { key.dims[i] = dims[i]; key.box[i] = box[i]; }
-  for (int i = 0; i + 1 < rank && i < 2; ++i) key.strides[i] = strides_bytes[i];
+  for (int i = 0; i < rank && i < 4; ++i) { key.dims[i] = dims[i]; key.box[i] = box[i]; }
+  for (int i = 0; i + 1 < rank && i < 3; ++i) key.strides[i] = strides_bytes[i];
   {
     std::lock_guard<std::mutex> lock(g_tmap_mu);
     for (int i = 0; i < g_tmap_n; ++i)

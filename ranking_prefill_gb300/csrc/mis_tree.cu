@@ -3,8 +3,30 @@
 // Row i of request b sees the cached rows [0, L_b) and, among the request's
 // own new rows, its ancestors and itself:
 //     o_i = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  s_ij = scale q_i k_j.
-// One warp per (row, query head) walks the visible keys with a running
-// maximum and sum; a lane owns D / 32 elements of the head.
+//
+// The n_b * G rows of a request that share a kv head (G query heads each) are
+// few, the keys many, so the tensor-core products are taken with the keys on
+// the wide side:
+//     S^T [128 keys x N rows] = K Q^T        (A = K tile, B = Q rows)
+//     O^T [D x N rows]       += V^T P^T      (A = V tile, MN-major, B = P)
+// with N = 16, 32, 64 or 128 rows a tile: a decoded token costs N = 16
+// columns of softmax instead of 128 rows, and one pass over K and V serves
+// every row of the tile.
+//
+// Work is cut evenly: the (request, kv head, row tile) units are laid end to
+// end in 128-key steps and every block takes the same number of consecutive
+// steps, found on the device from the lengths (no host plan). A block that
+// holds a whole unit writes O; the pieces of a unit that several blocks share
+// leave (max, sum, unnormalised O) in the workspace and a second kernel adds
+// them in block order, so the same call gives the same bits.
+//
+// Warp roles: 0 TMA producer (pages of the cache, 8-row groups of the new
+// rows), 1 MMA issue, 2-3 load Q and build the tree's masks, then one or two
+// softmax warpgroups (a thread is a key, it owns N or N / 2 columns) and an
+// epilogue warpgroup (a thread is an element of the head).
+// The running maximum of a column is common to the block's keys. It is moved
+// only when a score passes it by 2^8: one vote per tile replaces the exchange
+// of maxima, and O in tensor memory is rescaled only then.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -15,93 +37,943 @@
 #include "mis_ptx.cuh"
 
 namespace mis {
+
+CUtensorMap make_tmap_bf16(const void* base, int rank, const uint64_t* dims,
+                           const uint64_t* strides_bytes, const uint32_t* box, bool* ok);
+
 namespace {
 
 using namespace dev;
 
+constexpr int kKeys = 128;                       // keys of a step
+constexpr float kGrow = 8.0f;                    // log2 units a score may pass the maximum by
+constexpr float kEmpty = -1.0e30f;               // maximum of a column that has seen nothing
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <int D, int N>
+struct TreeCfg {
+  static constexpr int kNB = D / 64;             // 64-column boxes of a row
+  static constexpr int kWG = N == 16 ? 1 : 2;    // softmax warpgroups
+  static constexpr int kNC = N / kWG;            // columns of a softmax thread
+  static constexpr int kThreads = 256 + 128 * kWG;
+  static constexpr int kBox = kKeys * 128;       // 64 columns of a 128-key tile
+  static constexpr int kTile = kNB * kBox;
+  static constexpr int kQ = N * D * 2;
+  static constexpr int kQBox = N * 128;
+  static constexpr int kQS = (N == 128 && D == 128) ? 1 : 2;
+  static constexpr int kP = kKeys * 128 * (N > 64 ? 2 : 1);
+  static constexpr int kK = D == 128 ? (N == 128 ? 2 : 3) : (N == 128 ? 4 : 5);
+  static constexpr int kV = D == 128 ? (N == 16 ? 3 : 2) : (N == 128 ? 4 : 5);
+  static constexpr int kMW = N == 128 ? MIS_TREE_MAX_NODES / 32 : 2;   // mask words of a column
+  static constexpr int kTmem = N == 16 ? 64 : 4 * N;    // S_0 | S_1 | O_0 | O_1
+  // floats / words behind the tiles
+  static constexpr int oMask = 0;                       // [2][N][kMW]
+  static constexpr int oDead = oMask + 2 * N * kMW;     // [2][4] unused rows of the tile
+  static constexpr int oNf = oDead + 8;                 // [2][8] keys with a non-finite value
+  static constexpr int oM = oNf + 16;                   // [2][N] maxima
+  static constexpr int oL = oM + 2 * N;                 // [2][4][N] sums of each softmax warp
+  static constexpr int oMax = oL + 8 * N;               // [4][N] maxima of a tile
+  static constexpr int oAl = oMax + 4 * N;              // [N] factors
+  static constexpr int kWords = oAl + N;
+  static constexpr int kData = kQS * kQ + kP + (kK + kV) * kTile;
+  static constexpr int kSmem = kData + 4 * kWords + 512 + 1024;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+// Register budgets of the warpgroups where N = 128 needs more than 128 in the
+// softmax: 128 * (88 + 72) + 256 * 176 = 512 * 128, the launch's own.
+constexpr int kRegCtl = 88, kRegEpi = 72, kRegSoft = 176;
+
 struct TreeParams {
   const __nv_bfloat16* q;
-  const __nv_bfloat16* k;
   const __nv_bfloat16* v;
   __nv_bfloat16* o;
   float* lse;
-  int64_t qs, ks, vs, os;
-  const __nv_bfloat16* kc;
-  const __nv_bfloat16* vc;
-  int64_t page_stride, row_stride, head_stride;
-  int32_t n_pages, page_size, max_pages;
+  int64_t qs, vs, os;
+  int32_t n_pages, page_shift, max_pages;
   const int32_t* table;
   int64_t table_stride;
   const int32_t* cache_len;
   const int32_t* cu;
   const int32_t* parents;
-  int32_t B, T, Hq, group, max_nodes;
-  float scale;
-  uint32_t* status;
+  int32_t B, T, Hq, Hkv, G, max_nodes;
+  float scale_log2;
+  uint32_t* cta_status;    // [blocks][2]
+  int4* meta;              // [blocks] the split unit that starts in the block: b, h, row tile, pieces
+  float2* ml;              // [2 * blocks][N] (max, sum) of a piece
+  float* part;             // [2 * blocks][N][D]
+  uint64_t wait_ns;
+  uint32_t stall;
 };
 
-template <int D>
-__global__ void __launch_bounds__(128) mis_tree_attn_kernel(const TreeParams p) {
+struct Req {               // one request, checked
+  int r0, n, L;
+  int nct;                 // steps of the cache
+  int nkt;                 // steps in all
+  int nrt;                 // row tiles
+  bool bad;
+};
+
+template <int N>
+__device__ __forceinline__ Req load_req(const TreeParams& p, int b) {
+  const int64_t r0 = p.cu[b], r1 = p.cu[b + 1], L = p.cache_len[b];
+  Req R;
+  R.bad = r0 < 0 || r1 < r0 || r1 > p.T || r1 - r0 > p.max_nodes || L < 0 ||
+          L > ((int64_t)p.max_pages << p.page_shift);
+  R.r0 = (int)r0;
+  R.n = R.bad ? 0 : (int)(r1 - r0);
+  R.L = (int)L;
+  R.nct = (int)((L + kKeys - 1) / kKeys);
+  R.nkt = R.nct + (R.n + kKeys - 1) / kKeys;
+  R.nrt = (R.n * p.G + N - 1) / N;
+  return R;
+}
+
+// The units of a block, in order: unit (b, h, rt), steps [k0, k1).
+template <int N>
+struct Walk {
+  const TreeParams& p;
+  Req R;
+  int64_t left;
+  int b, h, rt, k0, k1;
+  bool fresh;
+
+  __device__ __forceinline__ Walk(const TreeParams& prm, int b0, int64_t off, int64_t steps)
+      : p(prm), left(steps), b(b0), h(0), rt(0), k0(0), k1(0), fresh(true) {
+    if (left <= 0) return;
+    R = load_req<N>(p, b);
+    const int64_t u = off / R.nkt;
+    k0 = (int)(off - u * R.nkt);
+    h = (int)(u / R.nrt);
+    rt = (int)(u - (int64_t)h * R.nrt);
+  }
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    if (!fresh) {
+      k0 = 0;
+      if (++rt == R.nrt) {
+        rt = 0;
+        if (++h == p.Hkv) {
+          h = 0;
+          do {
+            if (++b >= p.B) return false;
+            R = load_req<N>(p, b);
+          } while (R.n == 0);
+        }
+      }
+    }
+    fresh = false;
+    k1 = (int)min((int64_t)R.nkt, k0 + left);
+    left -= k1 - k0;
+    return true;
+  }
+  // valid keys of step k
+  __device__ __forceinline__ int keys(int k) const {
+    return k < R.nct ? min(kKeys, R.L - k * kKeys) : min(kKeys, R.n - (k - R.nct) * kKeys);
+  }
+};
+
+// The parent of node j, as the mask uses it: its index, or -1.
+__device__ __forceinline__ int parent_of(const TreeParams& p, int r0, int j, bool* bad) {
+  if (!p.parents) return j - 1;
+  const int up = p.parents[r0 + j];
+  if (up >= j || up < MIS_TREE_UNUSED) { *bad = true; return -1; }
+  return (up >= 0 && p.parents[r0 + up] != MIS_TREE_UNUSED) ? up : -1;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+template <int NC>
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t* r) {
+  if constexpr (NC == 8) {
+    tmem_ld8(taddr, r);
+    tmem_ld_wait();
+    reg_fence8(r);
+  } else if constexpr (NC == 16) {
+    tmem_ld16(taddr, r);
+    tmem_ld_wait();
+    reg_fence16(r);
+  } else {
+#pragma unroll
+    for (int c = 0; c < NC; c += 32) tmem_ld32(taddr + c, r + c);
+    tmem_ld_wait();
+#pragma unroll
+    for (int c = 0; c < NC; c += 32) reg_fence32(r + c);
+  }
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(TreeCfg<D, N>::kThreads, 1)
+mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
+                     const __grid_constant__ CUtensorMap vcmap,
+                     const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
+  using C = TreeCfg<D, N>;
+  constexpr int NB = C::kNB, NC = C::kNC, WG = C::kWG, KS = C::kK, VS = C::kV, QS = C::kQS;
+  constexpr int MW = C::kMW;
+  // barriers
+  constexpr int bQF = 0, bQE = bQF + 2, bKF = bQE + 2, bKE = bKF + KS, bVF = bKE + KS,
+                bVE = bVF + VS, bSF = bVE + VS, bPF = bSF + 2, bPV = bPF + 1, bOF = bPV + 1,
+                bOE = bOF + 2, bST = bOE + 2, bSE = bST + 2, bMF = bSE + 2, bDR = bMF + 2,
+                nBar = bDR + 1;
+  static_assert(nBar * 8 + 64 <= 512, "barrier space");
+
+  griddep_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* sQ = smem;
+  uint8_t* sP = sQ + QS * C::kQ;
+  uint8_t* sK = sP + C::kP;
+  uint8_t* sV = sK + KS * C::kTile;
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem + C::kData);
+  uint32_t* sMask = words + C::oMask;
+  uint32_t* sDead = words + C::oDead;
+  uint32_t* sNf = words + C::oNf;
+  float* sM = reinterpret_cast<float*>(words + C::oM);
+  float* sL = reinterpret_cast<float*>(words + C::oL);
+  float* sMax = reinterpret_cast<float*>(words + C::oMax);
+  float* sAl = reinterpret_cast<float*>(words + C::oAl);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(words + C::kWords);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + nBar);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  // the block's share: first request, offset of its first step there
+  __shared__ int s_b0;
+  __shared__ int64_t s_off, s_sums[C::kThreads / 32];
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(bQF + s), 2);
+      mbar_init(bar(bQE + s), 1);
+      mbar_init(bar(bSF + s), 1);
+      mbar_init(bar(bOF + s), 1);
+      mbar_init(bar(bOE + s), 4);
+      mbar_init(bar(bST + s), 4 * WG);
+      mbar_init(bar(bSE + s), 4);
+      mbar_init(bar(bMF + s), 2);
+    }
+    for (int s = 0; s < KS; ++s) { mbar_init(bar(bKF + s), 1); mbar_init(bar(bKE + s), 1); }
+    for (int s = 0; s < VS; ++s) { mbar_init(bar(bVF + s), 1); mbar_init(bar(bVE + s), 1); }
+    mbar_init(bar(bPF), 4 * WG);
+    mbar_init(bar(bPV), 1);
+    mbar_init(bar(bDR), 1);
+    fence_mbar_init();
+    fence_proxy_async();
+    tma_prefetch_desc(&kcmap); tma_prefetch_desc(&vcmap);
+    tma_prefetch_desc(&kmap); tma_prefetch_desc(&vmap);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmem);
+    tmem_relinquish();
+  }
   griddep_wait();
-  constexpr int E = D / 32;
+
+  // ------------------------------------------------ this block's share of the steps
+  uint32_t* status = p.cta_status + 2 * blockIdx.x;
+  const int per = (p.B + C::kThreads - 1) / C::kThreads;
+  const int rb0 = min(p.B, (int)threadIdx.x * per), rb1 = min(p.B, rb0 + per);
+  int64_t mine = 0;
+  bool bad_req = false;
+  for (int b = rb0; b < rb1; ++b) {
+    const Req R = load_req<N>(p, b);
+    bad_req |= R.bad;
+    if (R.n) mine += (int64_t)p.Hkv * R.nrt * R.nkt;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_sums[warp] = incl;
+  if (threadIdx.x == 0) {
+    status[0] = 0;
+    status[1] = 0;
+    p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+  tc_fence_before();
+  const bool any_bad = __syncthreads_or(bad_req);
+  tc_fence_after();
+  int64_t total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < C::kThreads / 32; ++w) {
+    if (w == warp) before = total;
+    total += s_sums[w];
+  }
+  if (any_bad && blockIdx.x == 0 && threadIdx.x == 0) raise_status(status, kDevIndex, 0x40);
+  const int64_t blocks = min((int64_t)gridDim.x, total);
+  int64_t f0 = 0, f1 = 0;
+  if (blockIdx.x < blocks) {
+    f0 = blockIdx.x * total / blocks;
+    f1 = (blockIdx.x + 1) * total / blocks;
+    int64_t at = before + incl - mine;
+    if (f0 >= at && f0 < at + mine) {
+      for (int b = rb0; b < rb1; ++b) {
+        const Req R = load_req<N>(p, b);
+        const int64_t c = R.n ? (int64_t)p.Hkv * R.nrt * R.nkt : 0;
+        if (f0 < at + c) { s_b0 = b; s_off = f0 - at; break; }
+        at += c;
+      }
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = *tmem_slot;
+  const int b0 = s_b0;
+  const int64_t off0 = s_off, steps = f1 - f0;
+  const Waiter W{abort_flag, status, p.wait_ns};
+  auto colS = [](int s) { return (uint32_t)(s * N); };
+  auto colO = [](int s) { return (uint32_t)((2 + s) * N); };
+
+  if (warp < 4) {
+    if constexpr (N == 128) regs_dec<kRegCtl>();
+    Walk<N> w(p, b0, off0, steps);
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      const int box_shift = min(p.page_shift, 7), box_rows = 1 << box_shift;
+      int t = 0, k_issued = 0, v_issued = 0;
+      bool ok = true;
+      while (ok && w.next()) {
+        const int32_t* row = p.table + (int64_t)w.b * p.table_stride;
+        for (int k = w.k0; ok && k < w.k1; ++k, ++t) {
+          const int kv = w.keys(k), sk = t % KS, sv = t % VS;
+          const bool cached = k < w.R.nct;
+          // copies of this step: box x of page (or 8-row group) g by lane g * NB + x
+          const int g = lane / NB, x = lane % NB;
+          int page = 0, prow = 0;
+          bool mine_ok;
+          uint32_t each, dst;
+          if (cached) {
+            mine_ok = (g << box_shift) < kv;
+            if (mine_ok) {
+              const int key = k * kKeys + (g << box_shift);
+              page = row[key >> p.page_shift];
+              prow = key & ((1 << p.page_shift) - 1);
+              if (page < 0 || page >= p.n_pages) {
+                mine_ok = false;
+                raise_status(status, kDevIndex, 0x41);
+              }
+            }
+            each = (uint32_t)box_rows * 128u;
+            dst = (uint32_t)(x * C::kBox + (g << box_shift) * 128);
+          } else {
+            mine_ok = g * 8 < kv;
+            prow = w.R.r0 + (k - w.R.nct) * kKeys + g * 8;
+            each = 1024u;
+            dst = (uint32_t)(x * C::kBox + g * 1024);
+          }
+          const uint32_t bytes = each * __popc(__ballot_sync(0xffffffffu, mine_ok));
+          if (t >= KS) {
+            ok = wait<true>(bar(bKE + sk), ((t / KS) - 1) & 1, W, 0x100);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(bKF + sk), bytes);
+          __syncwarp();
+          if (mine_ok) {
+            const uint32_t d = smem_u32(sK + sk * C::kTile) + dst;
+            if (cached) tma_load_4d(d, &kcmap, bar(bKF + sk), x * 64, w.h, prow, page);
+            else tma_load_3d(d, &kmap, bar(bKF + sk), x * 64, w.h, prow);
+          }
+          k_issued = t + 1;
+          if (t >= VS) {
+            ok = wait<true>(bar(bVE + sv), ((t / VS) - 1) & 1, W, 0x180);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(bVF + sv), bytes);
+          __syncwarp();
+          if (mine_ok) {
+            const uint32_t d = smem_u32(sV + sv * C::kTile) + dst;
+            if (cached) tma_load_4d(d, &vcmap, bar(bVF + sv), x * 64, w.h, prow, page);
+            else tma_load_3d(d, &vmap, bar(bVF + sv), x * 64, w.h, prow);
+          }
+          v_issued = t + 1;
+        }
+      }
+      __syncwarp();
+      // drain: every copy has landed before the block exits
+      for (int i = max(0, k_issued - KS); i < k_issued; ++i) wait_drain(bar(bKF + i % KS), (i / KS) & 1);
+      for (int i = max(0, v_issued - VS); i < v_issued; ++i) wait_drain(bar(bVF + i % VS), (i / VS) & 1);
+    } else if (warp == 1) {
+      // --------------------------------------------------------------- MMA
+      if (lane == 0) {
+        constexpr uint32_t idS = idesc_bf16(128, N, false);
+        constexpr uint32_t idO = idesc_bf16(128, N, true) | (1u << 15);   // A MN-major too
+        bool ok = true;
+        if (p.stall) ok = wait<true>(bar(bDR), 0, W, 0x7ff);   // nothing arrives before the drain
+        struct Step { int lu, kv; bool first, last; };
+        int k = 0, lu = -1;
+        auto fetch = [&](Step& s) -> bool {                    // the block's next step
+          if (lu < 0 || k >= w.k1) {
+            if (!w.next()) return false;
+            ++lu;
+            k = w.k0;
+          }
+          s.lu = lu;
+          s.kv = w.keys(k);
+          s.first = k == w.k0;
+          s.last = k + 1 == w.k1;
+          ++k;
+          return true;
+        };
+        auto s_ready = [&](const Step& s, int t) -> bool {
+          return mbar_test_wait(bar(bKF + t % KS), (t / KS) & 1) &&
+                 (!s.first || mbar_test_wait(bar(bQF + s.lu % QS), (s.lu / QS) & 1));
+        };
+        auto issue_s = [&](const Step& s, int t) -> bool {
+          if (s.first && !wait<true>(bar(bQF + s.lu % QS), (s.lu / QS) & 1, W, 0x200)) return false;
+          if (!wait<true>(bar(bKF + t % KS), (t / KS) & 1, W, 0x300)) return false;
+          tc_fence_after();
+          const uint32_t aK = smem_u32(sK + (t % KS) * C::kTile);
+          const uint32_t aQ = smem_u32(sQ + (s.lu % QS) * C::kQ);
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss(tmem + colS(t & 1), sdesc_sw128(aK + b * C::kBox + ks * 32, 16, 1024),
+                     sdesc_sw128(aQ + b * C::kQBox + ks * 32, 16, 1024), idS, (b | ks) != 0);
+          mma_commit(bar(bSF + (t & 1)));
+          mma_commit(bar(bKE + t % KS));
+          if (s.last) mma_commit(bar(bQE + s.lu % QS));
+          return true;
+        };
+        Step cur, nxt;
+        int t = 0;
+        bool have = ok && fetch(cur);
+        if (have) ok = issue_s(cur, 0);
+        while (ok && have) {
+          const bool more = fetch(nxt);
+          // the next S runs during this step's softmax, if its operands are there
+          bool early = false;
+          if (more && s_ready(nxt, t + 1)) {
+            if (!(ok = issue_s(nxt, t + 1))) break;
+            early = true;
+          }
+          if (!(ok = wait<true>(bar(bPF), t & 1, W, 0x400))) break;
+          if (!(ok = wait<true>(bar(bVF + t % VS), (t / VS) & 1, W, 0x480))) break;
+          if (cur.first && cur.lu >= 2 &&
+              !(ok = wait<true>(bar(bOE + (cur.lu & 1)), ((cur.lu >> 1) - 1) & 1, W, 0x500)))
+            break;
+          tc_fence_after();
+          const uint32_t aV = smem_u32(sV + (t % VS) * C::kTile), aP = smem_u32(sP);
+          const int nks = (cur.kv + 15) >> 4;
+          for (int ks = 0; ks < nks; ++ks)
+            // V [key][d] and P [key][row], both MN-major: 8-key groups 1024 B
+            // apart, 64-column boxes kBox apart. D = 64 repeats its one box
+            // (stride 0): rows 64..127 of O^T equal rows 0..63.
+            mma_ss(tmem + colO(cur.lu & 1),
+                   sdesc_sw128(aV + ks * 2048, D == 128 ? C::kBox : 0, 1024),
+                   sdesc_sw128(aP + ks * 2048, C::kBox, 1024), idO, (!cur.first || ks != 0) ? 1u : 0u);
+          mma_commit(bar(bVE + t % VS));
+          mma_commit(bar(bPV));
+          if (cur.last) mma_commit(bar(bOF + (cur.lu & 1)));
+          if (more && !early && !(ok = issue_s(nxt, t + 1))) break;
+          cur = nxt;
+          have = more;
+          ++t;
+        }
+        // drain: all tensor-core work of this thread completes before dealloc
+        mma_commit(bar(bDR));
+        wait_drain(bar(bDR), 0);
+      }
+    } else {
+      // --------------------------------------------- Q rows and the tree's masks
+      const int th = threadIdx.x - 64;
+      int lu = 0;
+      bool ok = true, bad = false;
+      while (ok && w.next()) {
+        const int rows = min(N, w.R.n * p.G - w.rt * N), rbase = w.rt * N;
+        const int sq = lu % QS, sm = lu & 1;
+        if (lu >= QS) ok = wait<true>(bar(bQE + sq), ((lu / QS) - 1) & 1, W, 0x600);
+        if (ok && lu >= 2) ok = wait<true>(bar(bSE + sm), ((lu >> 1) - 1) & 1, W, 0x610);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t aQ = smem_u32(sQ + sq * C::kQ);
+        constexpr int CH = D / 8;
+#pragma unroll 4
+        for (int x = th; x < N * CH; x += 64) {
+          const int n = x / CH, c = x % CH;
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (n < rows) {
+            const int r = rbase + n, i = r / p.G, g = r - i * p.G;
+            u = *reinterpret_cast<const uint4*>(p.q + (int64_t)(w.R.r0 + i) * p.qs +
+                                                (int64_t)(w.h * p.G + g) * D + c * 8);
+          }
+          st_shared_v4(aQ + (c >> 3) * C::kQBox + n * 128 + (((c & 7) ^ (n & 7)) << 4), u.x, u.y,
+                       u.z, u.w);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bQF + sq));
+        // columns of unused nodes, and who sees which new key
+        const bool tree = w.k1 > w.R.nct;
+        if (th < 8) sNf[sm * 8 + th] = 0;
+#pragma unroll
+        for (int c0 = 0; c0 < N; c0 += 64) {
+          const int n = c0 + th;
+          const int i = (rbase + n) / p.G;
+          const bool live = n < rows;
+          const bool dead = live && p.parents && p.parents[w.R.r0 + i] == MIS_TREE_UNUSED;
+          const uint32_t dw = __ballot_sync(0xffffffffu, dead);
+          if (n < N) {
+            if (lane == 0) sDead[sm * 4 + (n >> 5)] = dw;
+            uint32_t* m = sMask + (sm * N + n) * MW;
+            if (tree) {
+              if (p.parents) {
+#pragma unroll
+                for (int x = 0; x < MW; ++x) m[x] = 0;
+                for (int j = (live && !dead) ? i : -1; j >= 0; j = parent_of(p, w.R.r0, j, &bad))
+                  m[j >> 5] |= 1u << (j & 31);
+              } else {
+#pragma unroll
+                for (int x = 0; x < MW; ++x) m[x] = live ? bit_range(0, i + 1 - 32 * x) : 0u;
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bMF + sm));
+        ++lu;
+      }
+      if (bad) raise_status(status, kDevIndex, 0x42);
+    }
+  } else if (warp < 4 + 4 * WG) {
+    // --------------------------------------------------------------- softmax
+    if constexpr (N == 128) regs_inc<kRegSoft>();
+    const int wg = (warp - 4) >> 2, sw = warp & 3, r = sw * 32 + lane;
+    const int c0 = wg * NC, id = 1 + wg;
+    const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
+    const float sl2 = p.scale_log2;
+    const uint32_t hidden = sl2 < 0.f ? 0x7f800000u : 0xff800000u;     // scales to -inf
+    // this thread's row of P: chunk c of its columns
+    const uint32_t aP = smem_u32(sP) + (N == 128 ? wg * C::kBox : 0) + r * 128;
+    const int cP = (N == 128 ? 0 : c0) / 8;
+    Walk<N> w(p, b0, off0, steps);
+    int t = 0, lu = 0;
+    bool ok = true, gone = false;
+    while (!gone && w.next()) {
+      const int slot = lu & 1;
+      float l[NC];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) l[n] = 0.f;
+      float* m = sM + slot * N + c0;
+      if (ok && lu >= 2) {
+        ok = wait<true>(bar(bSE + slot), ((lu >> 1) - 1) & 1, W, 0x700);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      const int32_t* row = p.table + (int64_t)w.b * p.table_stride;
+      for (int k = w.k0; k < w.k1; ++k, ++t) {
+        const int kv = w.keys(k), kv16 = (kv + 15) & ~15;
+        const bool first = k == w.k0, cached = k < w.R.nct;
+        const bool active = sw * 32 < kv16;              // this warp holds keys of the product
+        bool seen = r < kv;
+        if (cached && seen) {
+          const int page = row[(k * kKeys + r) >> p.page_shift];
+          seen = page >= 0 && page < p.n_pages;
+        }
+        if (ok) {
+          ok = wait<true>(bar(bSF + (t & 1)), (t >> 1) & 1, W, 0x710);
+          if (ok && !cached) ok = wait<true>(bar(bMF + slot), (lu >> 1) & 1, W, 0x720);
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        tc_fence_after();
+        uint32_t s[NC];
+        bool over = first || !ok;
+        if (ok && active) {
+          ld_cols<NC>(tl + colS(t & 1) + c0, s);
+          if (!cached) {
+            const int wd = (k - w.R.nct) * 4 + sw;
+            const uint32_t* mk = sMask + (slot * N + c0) * MW + wd;
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+              const uint32_t bits = wd < MW ? mk[n * MW] : 0u;
+              if (!seen || !((bits >> lane) & 1u)) s[n] = hidden;
+            }
+          } else if (!seen) {
+#pragma unroll
+            for (int n = 0; n < NC; ++n) s[n] = hidden;
+          }
+          if (!first) {
+            float mx = kEmpty;
+#pragma unroll
+            for (int n = 0; n < NC; n += 4) {
+              const float4 mm = *reinterpret_cast<const float4*>(m + n);
+              mx = fmaxf(mx, fmaf(__uint_as_float(s[n]), sl2, -mm.x));
+              mx = fmaxf(mx, fmaf(__uint_as_float(s[n + 1]), sl2, -mm.y));
+              mx = fmaxf(mx, fmaf(__uint_as_float(s[n + 2]), sl2, -mm.z));
+              mx = fmaxf(mx, fmaf(__uint_as_float(s[n + 3]), sl2, -mm.w));
+            }
+            over = mx > kGrow;
+          }
+        }
+        if (bar_any128(id, over)) {
+          // a score passed its column's maximum (or a unit begins, or a wait
+          // gave up: then every warp of the warpgroup leaves here)
+          if (bar_any128(id, !ok)) { gone = true; break; }
+#pragma unroll
+          for (int n = 0; n < NC; ++n) {
+            float x = active ? __uint_as_float(s[n]) * sl2 : -INFINITY;
+            x = warp_max(x);
+            if (lane == 0) sMax[sw * N + c0 + n] = x;
+          }
+          bar_sync128(id);
+          if (r < NC) {
+            const float old = first ? kEmpty : m[r];
+            float x = old;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x = fmaxf(x, sMax[q * N + c0 + r]);
+            sAl[c0 + r] = ex2(old - x);
+            m[r] = x;
+          }
+          bar_sync128(id);
+          if (!first) {
+            ok = wait<true>(bar(bPV), (t - 1) & 1, W, 0x730);    // O holds every step before
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            if (ok) {
+              const uint32_t tO = tl + colO(slot) + c0;
+              constexpr int Q = NC > 32 ? 32 : NC;
+#pragma unroll
+              for (int q = 0; q < NC; q += Q) {
+                uint32_t ov[Q];
+                ld_cols<Q>(tO + q, ov);
+#pragma unroll
+                for (int n = 0; n < Q; ++n) {
+                  const float a = sAl[c0 + q + n];
+                  ov[n] = __float_as_uint(__uint_as_float(ov[n]) * a);
+                  l[q + n] *= a;
+                }
+                if constexpr (Q == 16) tmem_st16(tO + q, ov);
+                else tmem_st32(tO + q, ov);
+              }
+              tmem_st_wait();
+            }
+          }
+        }
+        // P of the step before has been read
+        if (ok && t > 0) {
+          ok = wait<true>(bar(bPV), (t - 1) & 1, W, 0x740);
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        if (ok && active) {
+#pragma unroll
+          for (int n = 0; n < NC; n += 8) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+              const float4 mm = *reinterpret_cast<const float4*>(m + n + e);
+              const float p0 = ex2(fmaf(__uint_as_float(s[n + e]), sl2, -mm.x));
+              const float p1 = ex2(fmaf(__uint_as_float(s[n + e + 1]), sl2, -mm.y));
+              const float p2 = ex2(fmaf(__uint_as_float(s[n + e + 2]), sl2, -mm.z));
+              const float p3 = ex2(fmaf(__uint_as_float(s[n + e + 3]), sl2, -mm.w));
+              l[n + e] += p0; l[n + e + 1] += p1; l[n + e + 2] += p2; l[n + e + 3] += p3;
+              pk[e / 2] = pack_bf16(p0, p1);
+              pk[e / 2 + 1] = pack_bf16(p2, p3);
+            }
+            st_shared_v4(aP + (((cP + n / 8) ^ (r & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+          }
+          // a V row that no row of the tile sees must not meet a zero
+          // probability with a NaN or an infinity; one that some rows see
+          // leaves its non-finite elements to the epilogue
+          if (wg == 0 && r < kv16 && (!seen || !cached)) {
+            ok = wait<true>(bar(bVF + t % VS), (t / VS) & 1, W, 0x750);
+            if (ok) {
+              const uint32_t aV = smem_u32(sV + (t % VS) * C::kTile) + r * 128;
+              bool nf = false;
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                for (int c = 0; c < 8; ++c) {
+                  const uint32_t a = aV + b * C::kBox + c * 16;
+                  if (!seen) { st_shared_v4(a, 0, 0, 0, 0); continue; }
+                  uint32_t x[4];
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(a) : "memory");
+                  bool any = false;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    if ((x[e] & 0x7f80u) == 0x7f80u) { x[e] &= 0xffff0000u; any = true; }
+                    if ((x[e] & 0x7f800000u) == 0x7f800000u) { x[e] &= 0x0000ffffu; any = true; }
+                  }
+                  if (any) { st_shared_v4(a, x[0], x[1], x[2], x[3]); nf = true; }
+                }
+              if (nf) atomicOr(&sNf[slot * 8 + (k - w.R.nct) * 4 + sw], 1u << lane);
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar(bPF));
+      }
+      if (gone) break;
+      // the columns' sums over this warp's keys: halve the columns, fold the lanes
+      int cnt = NC, col = 0;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        if (cnt > 1) {
+          const int hf = cnt / 2;
+          const bool up = (lane & o) != 0;
+#pragma unroll
+          for (int n = 0; n < NC / 2; ++n) {
+            if (n >= hf) break;
+            const float give = up ? l[n] : l[n + hf], keep = up ? l[n + hf] : l[n];
+            l[n] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+          col += up ? hf : 0;
+          cnt = hf;
+        } else {
+          l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < (NC > 32 ? NC / 32 : 1); ++n) sL[(slot * 4 + sw) * N + c0 + col + n] = l[n];
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(bar(bST + slot));
+      ++lu;
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    if constexpr (N == 128) regs_dec<kRegEpi>();
+    const int sw = warp & 3;
+    const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
+    // D = 128: a lane is element d, all columns. D = 64: the two copies of
+    // O^T share the columns.
+    const int d = (D == 128 ? sw * 32 : (sw & 1) * 32) + lane;
+    constexpr int NE = D == 128 ? N : N / 2;            // columns of a warp
+    constexpr int CH = NE < 16 ? 8 : 16;
+    const int e0 = D == 128 ? 0 : (sw >> 1) * NE;
+    Walk<N> w(p, b0, off0, steps);
+    int lu = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      const int slot = lu & 1;
+      const int rows = min(N, w.R.n * p.G - w.rt * N);
+      const bool whole = w.k0 == 0 && w.k1 == w.R.nkt;
+      ok = wait<true>(bar(bST + slot), (lu >> 1) & 1, W, 0x800) &&
+           wait<true>(bar(bMF + slot), (lu >> 1) & 1, W, 0x801);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      // maximum and sum of columns lane, lane + 32, ...
+      constexpr int NL = (N + 31) / 32;
+      float mx[NL], sum[NL];
+#pragma unroll
+      for (int x = 0; x < NL; ++x) {
+        const int n = x * 32 + lane;
+        mx[x] = kEmpty;
+        sum[x] = 0.f;
+        if (n < N) {
+          const float* l = sL + slot * 4 * N + n;
+          const bool dead = (sDead[slot * 4 + x] >> lane) & 1u;
+          if (!dead) {
+            mx[x] = sM[slot * N + n];
+            sum[x] = (l[0] + l[N]) + (l[2 * N] + l[3 * N]);
+          }
+        }
+      }
+      const int piece = 2 * blockIdx.x + (w.k0 == 0 ? 1 : 0);
+      if (sw == 0) {
+#pragma unroll
+        for (int x = 0; x < NL; ++x) {
+          const int n = x * 32 + lane;
+          if (n < rows) {
+            if (!whole) {
+              p.ml[(int64_t)piece * N + n] = make_float2(mx[x], sum[x]);
+            } else if (p.lse) {
+              const int r = w.rt * N + n, i = r / p.G, g = r - i * p.G;
+              p.lse[(int64_t)(w.h * p.G + g) * p.T + w.R.r0 + i] =
+                  sum[x] != 0.f ? (mx[x] + log2f(sum[x])) * kLn2 : -INFINITY;
+            }
+          }
+        }
+        if (!whole && w.k0 == 0 && lane == 0) {
+          // the unit starts here at f1 - k1 and reaches into later blocks
+          const int64_t end = f1 - w.k1 + w.R.nkt;
+          const int64_t lastb = (end * blocks - 1) / total;
+          p.meta[blockIdx.x] = make_int4(w.b, w.h, w.rt, (int)(lastb - blockIdx.x + 1));
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < NL; ++x) sum[x] = sum[x] != 0.f ? 1.f / sum[x] : 0.f;   // NaN stays
+      ok = wait<true>(bar(bOF + slot), (lu >> 1) & 1, W, 0x810);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      // non-finite values of the new rows, by key
+      uint32_t nf = 0;
+      if (w.k1 > w.R.nct)
+        for (int x = 0; x < MW; ++x) nf |= sNf[slot * 8 + x];
+#pragma unroll
+      for (int q = 0; q < NE; q += CH) {
+        uint32_t ov[CH];
+        ld_cols<CH>(tl + colO(slot) + e0 + q, ov);
+        if (q + CH == NE) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(bOE + slot));
+        }
+        if (e0 + q >= rows) continue;
+        if (nf) {
+          for (int x = 0; x < MW; ++x)
+            for (uint32_t bits = sNf[slot * 8 + x]; bits; bits &= bits - 1) {
+              const int j = x * 32 + __ffs(bits) - 1;
+              if (j < (w.k0 - w.R.nct) * kKeys || j >= (w.k1 - w.R.nct) * kKeys) continue;
+              const float val = __bfloat162float(p.v[(int64_t)(w.R.r0 + j) * p.vs + w.h * D + d]);
+              if (isfinite(val)) continue;
+#pragma unroll
+              for (int n = 0; n < CH; ++n)
+                if ((sMask[(slot * N + e0 + q + n) * MW + x] >> (j & 31)) & 1u)
+                  ov[n] = __float_as_uint(__uint_as_float(ov[n]) + val);
+            }
+        }
+        if (!whole) {
+          float* dst = p.part + ((int64_t)piece * N + e0 + q) * D + d;
+#pragma unroll
+          for (int n = 0; n < CH; ++n)
+            if (e0 + q + n < rows) dst[n * D] = __uint_as_float(ov[n]);
+          continue;
+        }
+        // neighbours exchange one of two rows: an even lane stores elements
+        // d, d + 1 of row n, the odd one d - 1, d of row n + 1
+        const bool odd = lane & 1;
+#pragma unroll
+        for (int n = 0; n < CH; n += 2) {
+          float v2[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int c = e0 + q + n + e;
+            float inv = 0.f;
+#pragma unroll
+            for (int x = 0; x < NL; ++x) {
+              const float y = __shfl_sync(0xffffffffu, sum[x], c & 31);
+              if ((c >> 5) == x) inv = y;
+            }
+            // an empty row is zero, whatever its accumulator holds
+            v2[e] = inv != 0.f ? __uint_as_float(ov[n + e]) * inv : 0.f;
+          }
+          const float other = __shfl_xor_sync(0xffffffffu, odd ? v2[0] : v2[1], 1);
+          const int c = e0 + q + n + (odd ? 1 : 0);
+          if (c < rows) {
+            const int r = w.rt * N + c, i = r / p.G, g = r - i * p.G;
+            const uint32_t u = odd ? pack_bf16(other, v2[1]) : pack_bf16(v2[0], other);
+            *reinterpret_cast<uint32_t*>(p.o + (int64_t)(w.R.r0 + i) * p.os +
+                                         (int64_t)(w.h * p.G + g) * D + (d & ~1)) = u;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bSE + slot));
+      ++lu;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmem);
+  }
+}
+
+// Adds the pieces of split units in block order: block (c, y) takes rows 4y ..
+// 4y + 3 of the unit whose first piece block c of the attention left, a warp
+// a row. Block (0, 0) gathers the blocks' status words.
+struct CombineParams {
+  const uint32_t* cta_status;
+  const int4* meta;
+  const float2* ml;
+  const float* part;
+  uint32_t* status;
+  __nv_bfloat16* o;
+  float* lse;
+  int64_t os;
+  const int32_t* cu;
+  int32_t T, G, blocks;
+};
+
+template <int D, int N>
+__global__ void __launch_bounds__(128) mis_tree_combine_kernel(const CombineParams p) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.y, h = blockIdx.x * 4 + warp;
-  if (h >= p.Hq) return;
-  const int i = blockIdx.z, r0 = p.cu[b], n = p.cu[b + 1] - r0, L = p.cache_len[b];
-  if (r0 < 0 || n < 0 || n > p.max_nodes || r0 + n > p.T || L < 0 ||
-      L > (int64_t)p.max_pages * p.page_size) {
-    if (lane == 0) raise_status(p.status, kDevIndex, 0x40);
-    return;
-  }
-  if (i >= n) return;
-  const int kvh = h / p.group;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(p.q[(int64_t)(r0 + i) * p.qs + h * D + lane * E + e]);
-    o[e] = 0.f;
-  }
-  auto key = [&](const __nv_bfloat16* kr, const __nv_bfloat16* vr) {
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(kr[lane * E + e]), s);
-#pragma unroll
-    for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    s *= p.scale;
-    const float mn = fmaxf(m, s);
-    if (mn == -INFINITY && s == s) return;
-    const float a = m == -INFINITY ? 0.f : expf(m - mn), pr = expf(s - mn);
-    m = mn;
-    l = l * a + pr;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * a + pr * __bfloat162float(vr[lane * E + e]);
-  };
-  auto parent = [&](int j) { return p.parents ? p.parents[r0 + j] : j - 1; };
-  if (parent(i) != MIS_TREE_UNUSED) {
-    for (int j = 0; j < L; ++j) {
-      const int page = p.table[b * p.table_stride + j / p.page_size];
-      if (page < 0 || page >= p.n_pages) {
-        if (lane == 0) raise_status(p.status, kDevIndex, 0x41);
-        continue;
-      }
-      const int64_t at = page * p.page_stride + (j % p.page_size) * p.row_stride + kvh * p.head_stride;
-      key(p.kc + at, p.vc + at);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+    uint32_t bits = 0, where = 0;
+    for (int c = lane; c < p.blocks; c += 32) {
+      const uint32_t s = p.cta_status[2 * c];
+      if (s && !bits) where = p.cta_status[2 * c + 1];
+      bits |= s;
     }
-    for (int j = i; j >= 0;) {
-      key(p.k + (int64_t)(r0 + j) * p.ks + kvh * D, p.v + (int64_t)(r0 + j) * p.vs + kvh * D);
-      int up = parent(j);
-      if (up >= j || up < MIS_TREE_UNUSED) {
-        if (lane == 0) raise_status(p.status, kDevIndex, 0x42);
-        up = MIS_TREE_ROOT;
-      }
-      j = up >= 0 && parent(up) != MIS_TREE_UNUSED ? up : -1;
+    const uint32_t any = __ballot_sync(0xffffffffu, bits != 0);
+    where = __shfl_sync(0xffffffffu, where, any ? __ffs(any) - 1 : 0);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+    if (lane == 0) {
+      p.status[0] = bits;
+      p.status[1] = where;
     }
   }
-  const float inv = l != 0.f ? 1.f / l : 0.f;   // NaN stays
+  const int c = blockIdx.x;
+  const int4 u = p.meta[c];
+  if (u.w < 2) return;
+  const int n = blockIdx.y * 4 + warp, r = u.z * N + n;
+  const int r0 = p.cu[u.x], rows = (p.cu[u.x + 1] - r0) * p.G;
+  if (r >= rows) return;
+  // piece s: the first lies in block c's second slot, the others in the first
+  // slots of the blocks that follow
+  auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
+  float m = kEmpty;
+  bool stuck = false;
+  for (int s = lane; s < u.w; s += 32) {
+    m = fmaxf(m, p.ml[(int64_t)slot(s) * N + n].x);
+    stuck |= (p.cta_status[2 * (c + s)] & kDevTimeout) != 0;
+  }
+  if (__any_sync(0xffffffffu, stuck)) return;          // a piece is missing
+  m = warp_max(m);
+  float l = 0.f;
+  for (int s = lane; s < u.w; s += 32) {
+    const float2 x = p.ml[(int64_t)slot(s) * N + n];
+    l += x.y * ex2(x.x - m);
+  }
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    p.o[(int64_t)(r0 + i) * p.os + h * D + lane * E + e] = __float2bfloat16(o[e] * inv);
-  if (p.lse && lane == 0) p.lse[(int64_t)h * p.T + r0 + i] = l != 0.f ? m + logf(l) : -INFINITY;
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  constexpr int E = D / 32;
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < u.w; ++s) {
+    const int64_t at = (int64_t)slot(s) * N + n;
+    const float a = ex2(p.ml[at].x - m);
+    const float* src = p.part + at * D + lane * E;
+    float x[E];
+    if constexpr (E == 4) {
+      const float4 y = *reinterpret_cast<const float4*>(src);
+      x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+    } else {
+      const float2 y = *reinterpret_cast<const float2*>(src);
+      x[0] = y.x; x[1] = y.y;
+    }
+    // a piece that saw nothing weighs nothing, whatever it holds
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = a != 0.f ? fmaf(a, x[e], acc[e]) : acc[e];
+  }
+  const int i = r / p.G, h = u.y * p.G + r - i * p.G;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  uint32_t w[E / 2];
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    w[e / 2] = inv != 0.f ? pack_bf16(acc[e] * inv, acc[e + 1] * inv) : 0u;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (int64_t)(r0 + i) * p.os + (int64_t)h * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) dst[e] = w[e];
+  if (p.lse && lane == 0)
+    p.lse[(int64_t)h * p.T + r0 + i] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -112,9 +984,45 @@ mis_status_t check_desc(const mis_tree_desc* d, const mis_paged_cache* c) {
   if (cs != MIS_OK) return cs;
   if (d->B < 1 || d->T < 0 || d->Hq < 1 || d->max_nodes < 1 || !std::isfinite(d->scale))
     return MIS_ERR_INVALID_ARG;
-  if (d->max_nodes > MIS_TREE_MAX_NODES) return MIS_ERR_UNSUPPORTED;
+  if (d->max_nodes > MIS_TREE_MAX_NODES || d->Hq > 65535) return MIS_ERR_UNSUPPORTED;
   if (d->Hq % c->Hkv) return MIS_ERR_SHAPE;
   return MIS_OK;
+}
+
+// Rows of a tile: the smallest that holds all rows of a request's kv head.
+int tile_rows(const mis_tree_desc* d, const mis_paged_cache* c) {
+  const int64_t rows = (int64_t)d->max_nodes * (d->Hq / c->Hkv);
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
+
+struct TreeWs { size_t status, meta, ml, part, total; };
+
+TreeWs workspace_of(const mis_tree_desc* d, const mis_paged_cache* c) {
+  const size_t G = (size_t)num_sms(), N = (size_t)tile_rows(d, c);
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  TreeWs w;
+  w.status = kStatusBytes;
+  w.meta = w.status + up(G * 8);
+  w.ml = w.meta + up(G * sizeof(int4));
+  w.part = w.ml + up(2 * G * N * sizeof(float2));
+  w.total = w.part + 2 * G * N * (size_t)c->D * sizeof(float);
+  return w;
+}
+
+template <int D, int N>
+mis_status_t launch_tree(const CUtensorMap& kc, const CUtensorMap& vc, const CUtensorMap& k,
+                         const CUtensorMap& v, const TreeParams& p, const CombineParams& c,
+                         cudaStream_t st) {
+  using Cf = TreeCfg<D, N>;
+  auto kern = mis_tree_attn_kernel<D, N>;
+  if (!kernel_attr_once(reinterpret_cast<const void*>(kern), Cf::kSmem)) return MIS_ERR_CUDA;
+  if (launch_pdl(kern, dim3((unsigned)c.blocks), dim3(Cf::kThreads), Cf::kSmem, st, kc, vc, k, v, p) !=
+      cudaSuccess)
+    return MIS_ERR_CUDA;
+  return launch_pdl(mis_tree_combine_kernel<D, N>, dim3((unsigned)c.blocks, N / 4), dim3(128), 0, st,
+                    c) == cudaSuccess
+             ? MIS_OK
+             : MIS_ERR_CUDA;
 }
 
 }  // namespace
@@ -124,7 +1032,7 @@ using namespace mis;
 
 extern "C" size_t mis_tree_attention_workspace_size(const mis_tree_desc* desc,
                                                     const mis_paged_cache* cache) {
-  return check_desc(desc, cache) == MIS_OK ? kStatusBytes : 0;
+  return check_desc(desc, cache) == MIS_OK ? workspace_of(desc, cache).total : 0;
 }
 
 extern "C" mis_status_t mis_tree_attention_fwd(
@@ -151,36 +1059,71 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16))
       return MIS_ERR_INVALID_ARG;
   }
-  if (!workspace || !aligned(workspace, 256) ||
-      ws_bytes < mis_tree_attention_workspace_size(desc, cache))
-    return MIS_ERR_WORKSPACE;
+  const TreeWs ws = workspace_of(desc, cache);
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < ws.total) return MIS_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, 8, st) != cudaSuccess) return MIS_ERR_CUDA;
-  if (desc->T == 0) return MIS_OK;
-  TreeParams p;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k = static_cast<const __nv_bfloat16*>(k);
-  p.v = static_cast<const __nv_bfloat16*>(v);
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.qs = q_row_stride; p.ks = k_row_stride; p.vs = v_row_stride; p.os = o_row_stride;
-  p.kc = static_cast<const __nv_bfloat16*>(cache->k);
-  p.vc = static_cast<const __nv_bfloat16*>(cache->v);
-  p.page_stride = cache->page_stride; p.row_stride = cache->row_stride;
-  p.head_stride = cache->head_stride;
-  p.n_pages = cache->n_pages; p.page_size = cache->page_size; p.max_pages = max_pages;
-  p.table = block_table; p.table_stride = block_table_stride;
-  p.cache_len = cache_len; p.cu = cu_nodes; p.parents = parents;
-  p.B = desc->B; p.T = desc->T; p.Hq = desc->Hq; p.group = desc->Hq / cache->Hkv;
-  p.max_nodes = desc->max_nodes;
-  p.scale = desc->scale != 0.f ? desc->scale : 1.f / std::sqrt((float)D);
-  p.status = static_cast<uint32_t*>(workspace);
-  const dim3 grid((unsigned)(desc->Hq + 3) / 4, (unsigned)desc->B, (unsigned)desc->max_nodes);
-  if (desc->B > 65535) return MIS_ERR_UNSUPPORTED;
+  if (desc->T == 0)
+    return cudaMemsetAsync(workspace, 0, 8, st) == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
   try {
-    const cudaError_t e = D == 128 ? launch_pdl(mis_tree_attn_kernel<128>, grid, dim3(128), 0, st, p)
-                                   : launch_pdl(mis_tree_attn_kernel<64>, grid, dim3(128), 0, st, p);
-    return e == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
+    // the cache as (element, head, row, page), boxes of 64 elements by the
+    // rows of a page (128 at most); the new rows in groups of 8, so that a
+    // short request copies little more than its own rows. Strides of extents
+    // of one are never used, but have to be valid.
+    bool ok = true;
+    const uint64_t cd[4] = {(uint64_t)D, (uint64_t)cache->Hkv, (uint64_t)cache->page_size,
+                            (uint64_t)cache->n_pages};
+    auto stride = [&](int64_t s, int64_t extent) { return (uint64_t)(extent > 1 ? s : D) * 2; };
+    const uint64_t cs[3] = {stride(cache->head_stride, cache->Hkv),
+                            stride(cache->row_stride, cache->page_size),
+                            stride(cache->page_stride, cache->n_pages)};
+    const uint32_t cb[4] = {64, 1, (uint32_t)std::min(cache->page_size, kKeys), 1};
+    const CUtensorMap kcm = make_tmap_bf16(cache->k, 4, cd, cs, cb, &ok);
+    const CUtensorMap vcm = make_tmap_bf16(cache->v, 4, cd, cs, cb, &ok);
+    const uint64_t nd[3] = {(uint64_t)D, (uint64_t)cache->Hkv, (uint64_t)desc->T};
+    const uint64_t nk[2] = {(uint64_t)D * 2, (uint64_t)k_row_stride * 2};
+    const uint64_t nv[2] = {(uint64_t)D * 2, (uint64_t)v_row_stride * 2};
+    const uint32_t nb[3] = {64, 1, 8};
+    const CUtensorMap km = make_tmap_bf16(k, 3, nd, nk, nb, &ok);
+    const CUtensorMap vm = make_tmap_bf16(v, 3, nd, nv, nb, &ok);
+    if (!ok) return MIS_ERR_CUDA;
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    TreeParams p;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.qs = q_row_stride; p.vs = v_row_stride; p.os = o_row_stride;
+    p.n_pages = cache->n_pages;
+    p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
+    p.max_pages = max_pages;
+    p.table = block_table; p.table_stride = block_table_stride;
+    p.cache_len = cache_len; p.cu = cu_nodes; p.parents = parents;
+    p.B = desc->B; p.T = desc->T; p.Hq = desc->Hq; p.Hkv = cache->Hkv;
+    p.G = desc->Hq / cache->Hkv;
+    p.max_nodes = desc->max_nodes;
+    p.scale_log2 = (desc->scale != 0.f ? desc->scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
+    p.cta_status = reinterpret_cast<uint32_t*>(base + ws.status);
+    p.meta = reinterpret_cast<int4*>(base + ws.meta);
+    p.ml = reinterpret_cast<float2*>(base + ws.ml);
+    p.part = reinterpret_cast<float*>(base + ws.part);
+    p.wait_ns = wait_limit_ns();
+    p.stall = inject_stall_mask() & 1u;
+    CombineParams c;
+    c.cta_status = p.cta_status; c.meta = p.meta; c.ml = p.ml; c.part = p.part;
+    c.status = reinterpret_cast<uint32_t*>(base);
+    c.o = p.o; c.lse = lse; c.os = o_row_stride; c.cu = cu_nodes;
+    c.T = desc->T; c.G = p.G; c.blocks = num_sms();
+    const int N = tile_rows(desc, cache);
+    if (D == 128) {
+      if (N == 16) return launch_tree<128, 16>(kcm, vcm, km, vm, p, c, st);
+      if (N == 32) return launch_tree<128, 32>(kcm, vcm, km, vm, p, c, st);
+      if (N == 64) return launch_tree<128, 64>(kcm, vcm, km, vm, p, c, st);
+      return launch_tree<128, 128>(kcm, vcm, km, vm, p, c, st);
+    }
+    if (N == 16) return launch_tree<64, 16>(kcm, vcm, km, vm, p, c, st);
+    if (N == 32) return launch_tree<64, 32>(kcm, vcm, km, vm, p, c, st);
+    if (N == 64) return launch_tree<64, 64>(kcm, vcm, km, vm, p, c, st);
+    return launch_tree<64, 128>(kcm, vcm, km, vm, p, c, st);
   } catch (...) {
     return MIS_ERR_CUDA;
   }

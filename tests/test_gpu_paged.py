@@ -672,6 +672,23 @@ def test_rows_beyond_32_bit_element_offsets():
     torch.cuda.empty_cache()
 
 
+def test_wait_timeout_is_reported_and_the_workspace_survives():
+    t = Tree([300, 20], [4, 2], 8, 2, 128, 16, None, seed=17).prepare()
+    old = lib.mis_set_wait_limit_ns(2_000_000)
+    lib.mis_inject_stall(1)
+    try:
+        t.call()
+        torch.cuda.synchronize()
+        assert lib.mis_get_device_status(t.ws) == lib.MIS_ERR_DEVICE_TIMEOUT
+        assert bool((t.o == 7.0).all())
+    finally:
+        lib.mis_inject_stall(0)
+        lib.mis_set_wait_limit_ns(old)
+    t.call()
+    assert lib.mis_get_device_status(t.ws) == lib.MIS_OK
+    t.compare(t.oracle())
+
+
 def test_python_refusals():
     t = Tree([30], [2], 4, 2, 64, 16, None, seed=18).prepare()
     ok = dict(q=t.q, k=t.k, v=t.v, o=t.o, lse=t.lse, table=t.d_table, n=t.d_len, cu=t.d_cu, par=None, ws=t.ws)
