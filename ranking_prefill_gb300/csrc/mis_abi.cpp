@@ -56,9 +56,10 @@ int num_sms() {
 
 namespace {
 
-// A few recently encoded tensor maps (the LM head, a layer's Q/K/V buffers
-// are reused call after call); encoding is pure host work, so a hit only
-// saves time and a miss re-encodes.
+// Recently encoded tensor maps (the LM head, a layer's Q/K/V buffers, a paged
+// cache are used call after call), in small sets found by a hash of the
+// description; encoding is pure host work, so a hit only saves time and a
+// miss re-encodes.
 struct TmapKey {
   const void* base;
   int rank;
@@ -69,12 +70,17 @@ struct TmapKey {
            std::memcmp(strides, o.strides, sizeof(strides)) == 0 &&
            std::memcmp(box, o.box, sizeof(box)) == 0;
   }
+  unsigned set() const {
+    uint64_t h = reinterpret_cast<uintptr_t>(base) >> 4;
+    for (int i = 0; i < 4; ++i) h = h * 31 + dims[i] + 7 * box[i];
+    return (unsigned)((h * 0x9E3779B97F4A7C15ull) >> 60);
+  }
 };
-constexpr int kTmapCache = 16;
+constexpr int kTmapSets = 16, kTmapWays = 8;
 std::mutex g_tmap_mu;
-TmapKey g_tmap_key[kTmapCache];
-CUtensorMap g_tmap_val[kTmapCache];
-int g_tmap_n = 0, g_tmap_next = 0;
+TmapKey g_tmap_key[kTmapSets][kTmapWays];
+CUtensorMap g_tmap_val[kTmapSets][kTmapWays];
+int g_tmap_n[kTmapSets], g_tmap_next[kTmapSets];
 
 }  // namespace
 
@@ -89,10 +95,11 @@ CUtensorMap make_tmap_bf16(const void* base, int rank, const uint64_t* dims,
   key.rank = rank;
   for (int i = 0; i < rank && i < 4; ++i) { key.dims[i] = dims[i]; key.box[i] = box[i]; }
   for (int i = 0; i + 1 < rank && i < 3; ++i) key.strides[i] = strides_bytes[i];
+  const unsigned set = key.set();
   {
     std::lock_guard<std::mutex> lock(g_tmap_mu);
-    for (int i = 0; i < g_tmap_n; ++i)
-      if (g_tmap_key[i] == key) return g_tmap_val[i];
+    for (int i = 0; i < g_tmap_n[set]; ++i)
+      if (g_tmap_key[set][i] == key) return g_tmap_val[set][i];
   }
   auto fn = encode_fn();
   if (!fn) { *ok = false; return m; }
@@ -109,10 +116,11 @@ CUtensorMap make_tmap_bf16(const void* base, int rank, const uint64_t* dims,
     return m;
   }
   std::lock_guard<std::mutex> lock(g_tmap_mu);
-  g_tmap_key[g_tmap_next] = key;
-  g_tmap_val[g_tmap_next] = m;
-  g_tmap_next = (g_tmap_next + 1) % kTmapCache;
-  if (g_tmap_n < kTmapCache) ++g_tmap_n;
+  int& next = g_tmap_next[set];
+  g_tmap_key[set][next] = key;
+  g_tmap_val[set][next] = m;
+  next = (next + 1) % kTmapWays;
+  if (g_tmap_n[set] < kTmapWays) ++g_tmap_n[set];
   return m;
 }
 

@@ -70,19 +70,21 @@ struct TreeCfg {
   static constexpr int oMask = 0;                       // [2][N][kMW]
   static constexpr int oDead = oMask + 2 * N * kMW;     // [2][4] unused rows of the tile
   static constexpr int oNf = oDead + 8;                 // [2][8] keys with a non-finite value
-  static constexpr int oM = oNf + 16;                   // [2][N] maxima
+  static constexpr int oM = oNf + 16;                   // [2][N] maxima, negated
   static constexpr int oL = oM + 2 * N;                 // [2][4][N] sums of each softmax warp
   static constexpr int oMax = oL + 8 * N;               // [4][N] maxima of a tile
   static constexpr int oAl = oMax + 4 * N;              // [N] factors
-  static constexpr int kWords = oAl + N;
+  static constexpr int oInv = oAl + N;                  // [4][N] an epilogue warp's 1 / sum
+  static constexpr int oPar = oInv + 4 * N;             // [2][256] int16: a loader warp's parents
+  static constexpr int kWords = oPar + MIS_TREE_MAX_NODES;
   static constexpr int kData = kQS * kQ + kP + (kK + kV) * kTile;
   static constexpr int kSmem = kData + 4 * kWords + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
-// Register budgets of the warpgroups where N = 128 needs more than 128 in the
-// softmax: 128 * (88 + 72) + 256 * 176 = 512 * 128, the launch's own.
-constexpr int kRegCtl = 88, kRegEpi = 72, kRegSoft = 176;
+// Register budgets of the warpgroups where N >= 64 needs more than 128 in the
+// softmax: 128 * (64 + 64) + 256 * 192 = 512 * 128, the launch's own.
+constexpr int kRegCtl = 64, kRegEpi = 64, kRegSoft = 192;
 
 struct TreeParams {
   const __nv_bfloat16* q;
@@ -97,6 +99,7 @@ struct TreeParams {
   const int32_t* cu;
   const int32_t* parents;
   int32_t B, T, Hq, Hkv, G, max_nodes;
+  uint32_t g_magic;        // ceil(2^32 / G): r / G = umulhi(r, magic) for r < 2^20, G <= 4096
   float scale_log2;
   uint32_t* cta_status;    // [blocks][2]
   int4* meta;              // [blocks] the split unit that starts in the block: b, h, row tile, pieces
@@ -106,10 +109,15 @@ struct TreeParams {
   uint32_t stall;
 };
 
-struct Req {               // one request, checked
+// One request, checked. Its steps are the 128-key tiles of its cached rows,
+// then those of its new rows. When the new rows fit behind the last, partial
+// cache tile (from the next multiple of 8 rows, a copy's granularity) they
+// share its step: a decoded token costs no step of its own.
+struct Req {
   int r0, n, L;
-  int nct;                 // steps of the cache
   int nkt;                 // steps in all
+  int kt;                  // first step with new rows
+  int a;                   // their first key row in that step (0 unless it is shared)
   int nrt;                 // row tiles
   bool bad;
 };
@@ -123,11 +131,21 @@ __device__ __forceinline__ Req load_req(const TreeParams& p, int b) {
   R.r0 = (int)r0;
   R.n = R.bad ? 0 : (int)(r1 - r0);
   R.L = (int)L;
-  R.nct = (int)((L + kKeys - 1) / kKeys);
-  R.nkt = R.nct + (R.n + kKeys - 1) / kKeys;
+  const int nct = (int)((L + kKeys - 1) / kKeys);
+  const int off = (int)L & (kKeys - 1), a = (off + 7) & ~7;
+  const bool share = off > 0 && a + R.n <= kKeys;
+  R.a = share ? a : 0;
+  R.kt = share ? nct - 1 : nct;
+  R.nkt = share ? nct : nct + (R.n + kKeys - 1) / kKeys;
   R.nrt = (R.n * p.G + N - 1) / N;
   return R;
 }
+
+// Where a block starts: found by one thread, read by every role.
+struct Start {
+  Req R;
+  int b, h, rt, k0;
+};
 
 // The units of a block, in order: unit (b, h, rt), steps [k0, k1).
 template <int N>
@@ -138,15 +156,8 @@ struct Walk {
   int b, h, rt, k0, k1;
   bool fresh;
 
-  __device__ __forceinline__ Walk(const TreeParams& prm, int b0, int64_t off, int64_t steps)
-      : p(prm), left(steps), b(b0), h(0), rt(0), k0(0), k1(0), fresh(true) {
-    if (left <= 0) return;
-    R = load_req<N>(p, b);
-    const int64_t u = off / R.nkt;
-    k0 = (int)(off - u * R.nkt);
-    h = (int)(u / R.nrt);
-    rt = (int)(u - (int64_t)h * R.nrt);
-  }
+  __device__ __forceinline__ Walk(const TreeParams& prm, const Start& s, int64_t steps)
+      : p(prm), R(s.R), left(steps), b(s.b), h(s.h), rt(s.rt), k0(s.k0), k1(0), fresh(true) {}
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
     if (!fresh) {
@@ -167,24 +178,20 @@ struct Walk {
     left -= k1 - k0;
     return true;
   }
-  // valid keys of step k
+  // key rows of step k: the products run over them, the rest of the tile is void
   __device__ __forceinline__ int keys(int k) const {
-    return k < R.nct ? min(kKeys, R.L - k * kKeys) : min(kKeys, R.n - (k - R.nct) * kKeys);
+    return k < R.kt ? min(kKeys, R.L - k * kKeys) : min(kKeys, R.a + R.n - (k - R.kt) * kKeys);
   }
 };
 
-// The parent of node j, as the mask uses it: its index, or -1.
-__device__ __forceinline__ int parent_of(const TreeParams& p, int r0, int j, bool* bad) {
-  if (!p.parents) return j - 1;
-  const int up = p.parents[r0 + j];
-  if (up >= j || up < MIS_TREE_UNUSED) { *bad = true; return -1; }
-  return (up >= 0 && p.parents[r0 + up] != MIS_TREE_UNUSED) ? up : -1;
+__device__ __forceinline__ int over_g(const TreeParams& p, int r) {
+  return p.G == 1 ? r : (int)__umulhi((uint32_t)r, p.g_magic);
 }
 
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 template <int NC>
@@ -210,6 +217,8 @@ template <int D, int N>
 __global__ void __launch_bounds__(TreeCfg<D, N>::kThreads, 1)
 mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
                      const __grid_constant__ CUtensorMap vcmap,
+                     const __grid_constant__ CUtensorMap kc8map,
+                     const __grid_constant__ CUtensorMap vc8map,
                      const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
   using C = TreeCfg<D, N>;
@@ -237,12 +246,13 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
   float* sL = reinterpret_cast<float*>(words + C::oL);
   float* sMax = reinterpret_cast<float*>(words + C::oMax);
   float* sAl = reinterpret_cast<float*>(words + C::oAl);
+  float* sInv = reinterpret_cast<float*>(words + C::oInv);
+  int16_t* sPar = reinterpret_cast<int16_t*>(words + C::oPar);
   uint64_t* bars = reinterpret_cast<uint64_t*>(words + C::kWords);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + nBar);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  // the block's share: first request, offset of its first step there
-  __shared__ int s_b0;
-  __shared__ int64_t s_off, s_sums[C::kThreads / 32];
+  __shared__ Start s_start;
+  __shared__ int64_t s_sums[C::kThreads / 32];
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -280,8 +290,9 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
   const int rb0 = min(p.B, (int)threadIdx.x * per), rb1 = min(p.B, rb0 + per);
   int64_t mine = 0;
   bool bad_req = false;
+  Req R;
   for (int b = rb0; b < rb1; ++b) {
-    const Req R = load_req<N>(p, b);
+    R = load_req<N>(p, b);
     bad_req |= R.bad;
     if (R.n) mine += (int64_t)p.Hkv * R.nrt * R.nkt;
   }
@@ -310,63 +321,76 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
   const int64_t blocks = min((int64_t)gridDim.x, total);
   int64_t f0 = 0, f1 = 0;
   if (blockIdx.x < blocks) {
-    f0 = blockIdx.x * total / blocks;
-    f1 = (blockIdx.x + 1) * total / blocks;
+    if (total < (1 << 24)) {                    // products below 2^32: short division
+      f0 = blockIdx.x * (uint32_t)total / (uint32_t)blocks;
+      f1 = (blockIdx.x + 1) * (uint32_t)total / (uint32_t)blocks;
+    } else {
+      f0 = blockIdx.x * total / blocks;
+      f1 = (blockIdx.x + 1) * total / blocks;
+    }
     int64_t at = before + incl - mine;
     if (f0 >= at && f0 < at + mine) {
       for (int b = rb0; b < rb1; ++b) {
-        const Req R = load_req<N>(p, b);
+        if (per > 1) R = load_req<N>(p, b);
         const int64_t c = R.n ? (int64_t)p.Hkv * R.nrt * R.nkt : 0;
-        if (f0 < at + c) { s_b0 = b; s_off = f0 - at; break; }
-        at += c;
+        if (f0 >= at + c) { at += c; continue; }
+        Start s;
+        s.R = R;
+        s.b = b;
+        const int64_t off = f0 - at;
+        const int64_t u = (off >> 31) == 0 ? (uint32_t)off / (uint32_t)R.nkt : off / R.nkt;
+        s.k0 = (int)(off - u * R.nkt);
+        s.h = (int)((u >> 31) == 0 ? (uint32_t)u / (uint32_t)R.nrt : u / R.nrt);
+        s.rt = (int)(u - (int64_t)s.h * R.nrt);
+        s_start = s;
+        break;
       }
     }
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  const int b0 = s_b0;
-  const int64_t off0 = s_off, steps = f1 - f0;
+  const int64_t steps = f1 - f0;
   const Waiter W{abort_flag, status, p.wait_ns};
   auto colS = [](int s) { return (uint32_t)(s * N); };
   auto colO = [](int s) { return (uint32_t)((2 + s) * N); };
 
   if (warp < 4) {
-    if constexpr (N == 128) regs_dec<kRegCtl>();
-    Walk<N> w(p, b0, off0, steps);
+    if constexpr (N >= 64) regs_dec<kRegCtl>();
+    Walk<N> w(p, s_start, steps);
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      const int box_shift = min(p.page_shift, 7), box_rows = 1 << box_shift;
+      const int box_shift = min(p.page_shift, 7);
       int t = 0, k_issued = 0, v_issued = 0;
       bool ok = true;
       while (ok && w.next()) {
         const int32_t* row = p.table + (int64_t)w.b * p.table_stride;
         for (int k = w.k0; ok && k < w.k1; ++k, ++t) {
           const int kv = w.keys(k), sk = t % KS, sv = t % VS;
-          const bool cached = k < w.R.nct;
-          // copies of this step: box x of page (or 8-row group) g by lane g * NB + x
+          // copies of this step: box x of key-row group g by lane g * NB + x.
+          // Groups are whole boxes of a page, or 8 rows where new rows follow
           const int g = lane / NB, x = lane % NB;
+          const bool fresh = k >= w.R.kt;
+          const int shift = fresh ? 3 : box_shift;
+          const int key = g << shift;
+          const bool cached = !fresh || key < w.R.a;
+          bool mine_ok = key < kv;
           int page = 0, prow = 0;
-          bool mine_ok;
-          uint32_t each, dst;
-          if (cached) {
-            mine_ok = (g << box_shift) < kv;
-            if (mine_ok) {
-              const int key = k * kKeys + (g << box_shift);
-              page = row[key >> p.page_shift];
-              prow = key & ((1 << p.page_shift) - 1);
+          if (mine_ok) {
+            if (cached) {
+              const int at = k * kKeys + key;
+              page = row[at >> p.page_shift];
+              prow = at & ((1 << p.page_shift) - 1);
               if (page < 0 || page >= p.n_pages) {
                 mine_ok = false;
                 raise_status(status, kDevIndex, 0x41);
               }
+            } else {
+              prow = w.R.r0 + (k - w.R.kt) * kKeys + key - w.R.a;
             }
-            each = (uint32_t)box_rows * 128u;
-            dst = (uint32_t)(x * C::kBox + (g << box_shift) * 128);
-          } else {
-            mine_ok = g * 8 < kv;
-            prow = w.R.r0 + (k - w.R.nct) * kKeys + g * 8;
-            each = 1024u;
-            dst = (uint32_t)(x * C::kBox + g * 1024);
           }
+          const CUtensorMap* km = !cached ? &kmap : fresh ? &kc8map : &kcmap;
+          const CUtensorMap* vm = !cached ? &vmap : fresh ? &vc8map : &vcmap;
+          const uint32_t each = 128u << shift, dst = (uint32_t)(x * C::kBox + key * 128);
           const uint32_t bytes = each * __popc(__ballot_sync(0xffffffffu, mine_ok));
           if (t >= KS) {
             ok = wait<true>(bar(bKE + sk), ((t / KS) - 1) & 1, W, 0x100);
@@ -377,8 +401,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
           __syncwarp();
           if (mine_ok) {
             const uint32_t d = smem_u32(sK + sk * C::kTile) + dst;
-            if (cached) tma_load_4d(d, &kcmap, bar(bKF + sk), x * 64, w.h, prow, page);
-            else tma_load_3d(d, &kmap, bar(bKF + sk), x * 64, w.h, prow);
+            if (cached) tma_load_4d(d, km, bar(bKF + sk), x * 64, w.h, prow, page);
+            else tma_load_3d(d, km, bar(bKF + sk), x * 64, w.h, prow);
           }
           k_issued = t + 1;
           if (t >= VS) {
@@ -390,8 +414,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
           __syncwarp();
           if (mine_ok) {
             const uint32_t d = smem_u32(sV + sv * C::kTile) + dst;
-            if (cached) tma_load_4d(d, &vcmap, bar(bVF + sv), x * 64, w.h, prow, page);
-            else tma_load_3d(d, &vmap, bar(bVF + sv), x * 64, w.h, prow);
+            if (cached) tma_load_4d(d, vm, bar(bVF + sv), x * 64, w.h, prow, page);
+            else tma_load_3d(d, vm, bar(bVF + sv), x * 64, w.h, prow);
           }
           v_issued = t + 1;
         }
@@ -494,6 +518,19 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
         if (ok && lu >= 2) ok = wait<true>(bar(bSE + sm), ((lu >> 1) - 1) & 1, W, 0x610);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        // parents as the masks use them (each warp keeps its own copy): the
+        // index, or -1 for roots, for children of unused nodes, and for what
+        // is no index; unused nodes themselves -2
+        const bool tree = w.k1 > w.R.kt;
+        int16_t* par = sPar + (warp - 2) * MIS_TREE_MAX_NODES;
+        if (p.parents) {
+          for (int j = lane; j < w.R.n; j += 32) {
+            int up = p.parents[w.R.r0 + j];
+            if (up >= j || up < MIS_TREE_UNUSED) { up = -1; bad = true; }
+            if (up >= 0 && p.parents[w.R.r0 + up] == MIS_TREE_UNUSED) up = -1;
+            par[j] = (int16_t)up;
+          }
+        }
         const uint32_t aQ = smem_u32(sQ + sq * C::kQ);
         constexpr int CH = D / 8;
 #pragma unroll 4
@@ -501,7 +538,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
           const int n = x / CH, c = x % CH;
           uint4 u = make_uint4(0, 0, 0, 0);
           if (n < rows) {
-            const int r = rbase + n, i = r / p.G, g = r - i * p.G;
+            const int r = rbase + n, i = over_g(p, r), g = r - i * p.G;
             u = *reinterpret_cast<const uint4*>(p.q + (int64_t)(w.R.r0 + i) * p.qs +
                                                 (int64_t)(w.h * p.G + g) * D + c * 8);
           }
@@ -512,14 +549,13 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bQF + sq));
         // columns of unused nodes, and who sees which new key
-        const bool tree = w.k1 > w.R.nct;
         if (th < 8) sNf[sm * 8 + th] = 0;
 #pragma unroll
         for (int c0 = 0; c0 < N; c0 += 64) {
           const int n = c0 + th;
-          const int i = (rbase + n) / p.G;
+          const int i = over_g(p, rbase + n);
           const bool live = n < rows;
-          const bool dead = live && p.parents && p.parents[w.R.r0 + i] == MIS_TREE_UNUSED;
+          const bool dead = live && p.parents && par[i] == MIS_TREE_UNUSED;
           const uint32_t dw = __ballot_sync(0xffffffffu, dead);
           if (n < N) {
             if (lane == 0) sDead[sm * 4 + (n >> 5)] = dw;
@@ -528,8 +564,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
               if (p.parents) {
 #pragma unroll
                 for (int x = 0; x < MW; ++x) m[x] = 0;
-                for (int j = (live && !dead) ? i : -1; j >= 0; j = parent_of(p, w.R.r0, j, &bad))
-                  m[j >> 5] |= 1u << (j & 31);
+                for (int j = (live && !dead) ? i : -1; j >= 0; j = par[j]) m[j >> 5] |= 1u << (j & 31);
               } else {
 #pragma unroll
                 for (int x = 0; x < MW; ++x) m[x] = live ? bit_range(0, i + 1 - 32 * x) : 0u;
@@ -545,24 +580,28 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
     }
   } else if (warp < 4 + 4 * WG) {
     // --------------------------------------------------------------- softmax
-    if constexpr (N == 128) regs_inc<kRegSoft>();
+    if constexpr (N >= 64) regs_inc<kRegSoft>();
     const int wg = (warp - 4) >> 2, sw = warp & 3, r = sw * 32 + lane;
     const int c0 = wg * NC, id = 1 + wg;
     const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
     const float sl2 = p.scale_log2;
     const uint32_t hidden = sl2 < 0.f ? 0x7f800000u : 0xff800000u;     // scales to -inf
+    const uint64_t sl2x2 = f2_pack(__float_as_uint(sl2), __float_as_uint(sl2));
+    // columns in registers at a time. Two pieces (N = 128) are read from
+    // tensor memory twice, once for the maximum and once for P.
+    constexpr int CC = NC > 32 ? 32 : NC, NP = NC / CC;
     // this thread's row of P: chunk c of its columns
     const uint32_t aP = smem_u32(sP) + (N == 128 ? wg * C::kBox : 0) + r * 128;
     const int cP = (N == 128 ? 0 : c0) / 8;
-    Walk<N> w(p, b0, off0, steps);
+    Walk<N> w(p, s_start, steps);
     int t = 0, lu = 0;
     bool ok = true, gone = false;
     while (!gone && w.next()) {
       const int slot = lu & 1;
-      float l[NC];
+      uint64_t l2[NC / 2];
 #pragma unroll
-      for (int n = 0; n < NC; ++n) l[n] = 0.f;
-      float* m = sM + slot * N + c0;
+      for (int n = 0; n < NC / 2; ++n) l2[n] = 0ull;
+      float* nm = sM + slot * N + c0;                    // negated maxima
       if (ok && lu >= 2) {
         ok = wait<true>(bar(bSE + slot), ((lu >> 1) - 1) & 1, W, 0x700);
         ok = __all_sync(0xffffffffu, ok);
@@ -570,66 +609,94 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
       const int32_t* row = p.table + (int64_t)w.b * p.table_stride;
       for (int k = w.k0; k < w.k1; ++k, ++t) {
         const int kv = w.keys(k), kv16 = (kv + 15) & ~15;
-        const bool first = k == w.k0, cached = k < w.R.nct;
+        const bool first = k == w.k0, fresh = k >= w.R.kt;
         const bool active = sw * 32 < kv16;              // this warp holds keys of the product
-        bool seen = r < kv;
-        if (cached && seen) {
+        // what this thread's key row holds: a cached row, new row j, or nothing
+        const int j = fresh ? (k - w.R.kt) * kKeys + r - w.R.a : -1;
+        const bool node = fresh && j >= 0 && r < kv;
+        bool seen = node;
+        if (!node && r < kv && k * kKeys + r < w.R.L) {
           const int page = row[(k * kKeys + r) >> p.page_shift];
           seen = page >= 0 && page < p.n_pages;
         }
         if (ok) {
           ok = wait<true>(bar(bSF + (t & 1)), (t >> 1) & 1, W, 0x710);
-          if (ok && !cached) ok = wait<true>(bar(bMF + slot), (lu >> 1) & 1, W, 0x720);
+          if (ok && fresh) ok = wait<true>(bar(bMF + slot), (lu >> 1) & 1, W, 0x720);
           ok = __all_sync(0xffffffffu, ok);
         }
         tc_fence_after();
-        uint32_t s[NC];
-        bool over = first || !ok;
-        if (ok && active) {
-          ld_cols<NC>(tl + colS(t & 1) + c0, s);
-          if (!cached) {
-            const int wd = (k - w.R.nct) * 4 + sw;
-            const uint32_t* mk = sMask + (slot * N + c0) * MW + wd;
+        uint32_t s[CC];
+        // columns q .. q + CC - 1 of the scores; what a row does not see is -inf
+        auto load = [&](int q) {
+          ld_cols<CC>(tl + colS(t & 1) + c0 + q, s);
+          if (node) {
+            const uint32_t* mk = sMask + (slot * N + c0 + q) * MW + (j >> 5);
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-              const uint32_t bits = wd < MW ? mk[n * MW] : 0u;
-              if (!seen || !((bits >> lane) & 1u)) s[n] = hidden;
-            }
+            for (int n = 0; n < CC; ++n)
+              if (!((mk[n * MW] >> (j & 31)) & 1u)) s[n] = hidden;
           } else if (!seen) {
 #pragma unroll
-            for (int n = 0; n < NC; ++n) s[n] = hidden;
+            for (int n = 0; n < CC; ++n) s[n] = hidden;
           }
-          if (!first) {
+          __syncwarp();
+        };
+        // s = scaled scores less the maxima, in log2 units; their largest
+        auto shift = [&](int q) -> float {
+          float x0 = kEmpty, x1 = kEmpty;
+#pragma unroll
+          for (int n = 0; n < CC; n += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(nm + q + n);
+            float a0, a1, a2, a3;
+            f2_unpack(f2_fma(f2_pack(s[n], s[n + 1]), sl2x2,
+                             f2_pack(__float_as_uint(b.x), __float_as_uint(b.y))), a0, a1);
+            f2_unpack(f2_fma(f2_pack(s[n + 2], s[n + 3]), sl2x2,
+                             f2_pack(__float_as_uint(b.z), __float_as_uint(b.w))), a2, a3);
+            x0 = max3(x0, a0, a1);
+            x1 = max3(x1, a2, a3);
+            s[n] = __float_as_uint(a0); s[n + 1] = __float_as_uint(a1);
+            s[n + 2] = __float_as_uint(a2); s[n + 3] = __float_as_uint(a3);
+          }
+          return fmaxf(x0, x1);
+        };
+        bool move = first;
+        if (!first) {
+          bool over = !ok;
+          if (ok && active) {
             float mx = kEmpty;
 #pragma unroll
-            for (int n = 0; n < NC; n += 4) {
-              const float4 mm = *reinterpret_cast<const float4*>(m + n);
-              mx = fmaxf(mx, fmaf(__uint_as_float(s[n]), sl2, -mm.x));
-              mx = fmaxf(mx, fmaf(__uint_as_float(s[n + 1]), sl2, -mm.y));
-              mx = fmaxf(mx, fmaf(__uint_as_float(s[n + 2]), sl2, -mm.z));
-              mx = fmaxf(mx, fmaf(__uint_as_float(s[n + 3]), sl2, -mm.w));
+            for (int q = 0; q < NC; q += CC) {
+              load(q);
+              mx = fmaxf(mx, shift(q));
             }
             over = mx > kGrow;
           }
+          move = bar_any128(id, over);
         }
-        if (bar_any128(id, over)) {
-          // a score passed its column's maximum (or a unit begins, or a wait
+        if (move) {
+          // a unit begins or a score passed its column's maximum (or a wait
           // gave up: then every warp of the warpgroup leaves here)
           if (bar_any128(id, !ok)) { gone = true; break; }
 #pragma unroll
-          for (int n = 0; n < NC; ++n) {
-            float x = active ? __uint_as_float(s[n]) * sl2 : -INFINITY;
-            x = warp_max(x);
-            if (lane == 0) sMax[sw * N + c0 + n] = x;
+          for (int q = 0; q < NC; q += CC) {
+            float mine = -INFINITY;
+            if (active) {
+              load(q);
+#pragma unroll
+              for (int n = 0; n < CC; ++n) {
+                const float x = warp_max(__uint_as_float(s[n]) * sl2);
+                if (lane == n) mine = x;
+              }
+            }
+            if (lane < CC) sMax[sw * N + c0 + q + lane] = mine;
           }
           bar_sync128(id);
           if (r < NC) {
-            const float old = first ? kEmpty : m[r];
+            const float old = first ? kEmpty : -nm[r];
             float x = old;
 #pragma unroll
             for (int q = 0; q < 4; ++q) x = fmaxf(x, sMax[q * N + c0 + r]);
             sAl[c0 + r] = ex2(old - x);
-            m[r] = x;
+            nm[r] = -x;
           }
           bar_sync128(id);
           if (!first) {
@@ -638,73 +705,89 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
             tc_fence_after();
             if (ok) {
               const uint32_t tO = tl + colO(slot) + c0;
-              constexpr int Q = NC > 32 ? 32 : NC;
 #pragma unroll
-              for (int q = 0; q < NC; q += Q) {
-                uint32_t ov[Q];
-                ld_cols<Q>(tO + q, ov);
+              for (int q = 0; q < NC; q += 16) {
+                uint32_t ov[16];
+                ld_cols<16>(tO + q, ov);
 #pragma unroll
-                for (int n = 0; n < Q; ++n) {
-                  const float a = sAl[c0 + q + n];
-                  ov[n] = __float_as_uint(__uint_as_float(ov[n]) * a);
-                  l[q + n] *= a;
+                for (int n = 0; n < 16; n += 2) {
+                  const float2 a = *reinterpret_cast<const float2*>(sAl + c0 + q + n);
+                  ov[n] = __float_as_uint(__uint_as_float(ov[n]) * a.x);
+                  ov[n + 1] = __float_as_uint(__uint_as_float(ov[n + 1]) * a.y);
+                  l2[(q + n) / 2] = f2_fma(l2[(q + n) / 2], f2_pack(__float_as_uint(a.x), __float_as_uint(a.y)), 0ull);
                 }
-                if constexpr (Q == 16) tmem_st16(tO + q, ov);
-                else tmem_st32(tO + q, ov);
+                tmem_st16(tO + q, ov);
               }
               tmem_st_wait();
             }
           }
-        }
-        // P of the step before has been read
-        if (ok && t > 0) {
-          ok = wait<true>(bar(bPV), (t - 1) & 1, W, 0x740);
-          ok = __all_sync(0xffffffffu, ok);
+          if (NP == 1 && active) shift(0);               // the raw scores are still there
         }
         if (ok && active) {
 #pragma unroll
-          for (int n = 0; n < NC; n += 8) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              const float4 mm = *reinterpret_cast<const float4*>(m + n + e);
-              const float p0 = ex2(fmaf(__uint_as_float(s[n + e]), sl2, -mm.x));
-              const float p1 = ex2(fmaf(__uint_as_float(s[n + e + 1]), sl2, -mm.y));
-              const float p2 = ex2(fmaf(__uint_as_float(s[n + e + 2]), sl2, -mm.z));
-              const float p3 = ex2(fmaf(__uint_as_float(s[n + e + 3]), sl2, -mm.w));
-              l[n + e] += p0; l[n + e + 1] += p1; l[n + e + 2] += p2; l[n + e + 3] += p3;
-              pk[e / 2] = pack_bf16(p0, p1);
-              pk[e / 2 + 1] = pack_bf16(p2, p3);
+          for (int q = 0; q < NC; q += CC) {
+            if (NP > 1) {
+              load(q);
+              shift(q);
             }
-            st_shared_v4(aP + (((cP + n / 8) ^ (r & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+            uint32_t pk[CC / 2];
+#pragma unroll
+            for (int n = 0; n < CC; n += 2) {
+              const float p0 = ex2(__uint_as_float(s[n])), p1 = ex2(__uint_as_float(s[n + 1]));
+              l2[(q + n) / 2] = f2_add(l2[(q + n) / 2], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
+              pk[n / 2] = pack_bf16(p0, p1);
+            }
+            if (q == 0 && t > 0) {                       // P of the step before has been read
+              ok = wait<true>(bar(bPV), (t - 1) & 1, W, 0x740);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+            }
+#pragma unroll
+            for (int c = 0; c < CC / 8; ++c)
+              st_shared_v4(aP + (((cP + q / 8 + c) ^ (r & 7)) << 4), pk[4 * c], pk[4 * c + 1],
+                           pk[4 * c + 2], pk[4 * c + 3]);
           }
           // a V row that no row of the tile sees must not meet a zero
           // probability with a NaN or an infinity; one that some rows see
           // leaves its non-finite elements to the epilogue
-          if (wg == 0 && r < kv16 && (!seen || !cached)) {
+          if (ok && wg == 0 && r < kv16 && (!seen || node)) {
             ok = wait<true>(bar(bVF + t % VS), (t / VS) & 1, W, 0x750);
             if (ok) {
               const uint32_t aV = smem_u32(sV + (t % VS) * C::kTile) + r * 128;
               bool nf = false;
 #pragma unroll
-              for (int b = 0; b < NB; ++b)
-                for (int c = 0; c < 8; ++c) {
-                  const uint32_t a = aV + b * C::kBox + c * 16;
+              for (int c = 0; c < 8 * NB; c += 4) {
+                uint32_t x[4][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t a = aV + (c >> 3) * C::kBox + ((c & 7) + e) * 16;
                   if (!seen) { st_shared_v4(a, 0, 0, 0, 0); continue; }
-                  uint32_t x[4];
                   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(a) : "memory");
+                               : "=r"(x[e][0]), "=r"(x[e][1]), "=r"(x[e][2]), "=r"(x[e][3])
+                               : "r"(a) : "memory");
+                }
+                if (!seen) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
                   bool any = false;
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    if ((x[e] & 0x7f80u) == 0x7f80u) { x[e] &= 0xffff0000u; any = true; }
-                    if ((x[e] & 0x7f800000u) == 0x7f800000u) { x[e] &= 0x0000ffffu; any = true; }
+                  for (int y = 0; y < 4; ++y) {
+                    if ((x[e][y] & 0x7f80u) == 0x7f80u) { x[e][y] &= 0xffff0000u; any = true; }
+                    if ((x[e][y] & 0x7f800000u) == 0x7f800000u) { x[e][y] &= 0x0000ffffu; any = true; }
                   }
-                  if (any) { st_shared_v4(a, x[0], x[1], x[2], x[3]); nf = true; }
+                  if (any) {
+                    st_shared_v4(aV + (c >> 3) * C::kBox + ((c & 7) + e) * 16, x[e][0], x[e][1], x[e][2], x[e][3]);
+                    nf = true;
+                  }
                 }
-              if (nf) atomicOr(&sNf[slot * 8 + (k - w.R.nct) * 4 + sw], 1u << lane);
+              }
+              if (nf) atomicOr(&sNf[slot * 8 + (j >> 5)], 1u << (j & 31));
             }
           }
+          ok = __all_sync(0xffffffffu, ok);
+        } else if (ok && t > 0) {
+          // a warp without keys still keeps step with the products
+          ok = wait<true>(bar(bPV), (t - 1) & 1, W, 0x741);
           ok = __all_sync(0xffffffffu, ok);
         }
         fence_proxy_async();
@@ -714,6 +797,9 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
       }
       if (gone) break;
       // the columns' sums over this warp's keys: halve the columns, fold the lanes
+      float l[NC];
+#pragma unroll
+      for (int n = 0; n < NC / 2; ++n) f2_unpack(l2[n], l[2 * n], l[2 * n + 1]);
       int cnt = NC, col = 0;
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
@@ -740,7 +826,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    if constexpr (N == 128) regs_dec<kRegEpi>();
+    if constexpr (N >= 64) regs_dec<kRegEpi>();
     const int sw = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
     // D = 128: a lane is element d, all columns. D = 64: the two copies of
@@ -749,7 +835,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
     constexpr int NE = D == 128 ? N : N / 2;            // columns of a warp
     constexpr int CH = NE < 16 ? 8 : 16;
     const int e0 = D == 128 ? 0 : (sw >> 1) * NE;
-    Walk<N> w(p, b0, off0, steps);
+    Walk<N> w(p, s_start, steps);
     int lu = 0;
     bool ok = true;
     while (ok && w.next()) {
@@ -772,7 +858,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
           const float* l = sL + slot * 4 * N + n;
           const bool dead = (sDead[slot * 4 + x] >> lane) & 1u;
           if (!dead) {
-            mx[x] = sM[slot * N + n];
+            mx[x] = -sM[slot * N + n];
             sum[x] = (l[0] + l[N]) + (l[2 * N] + l[3 * N]);
           }
         }
@@ -786,7 +872,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
             if (!whole) {
               p.ml[(int64_t)piece * N + n] = make_float2(mx[x], sum[x]);
             } else if (p.lse) {
-              const int r = w.rt * N + n, i = r / p.G, g = r - i * p.G;
+              const int r = w.rt * N + n, i = over_g(p, r), g = r - i * p.G;
               p.lse[(int64_t)(w.h * p.G + g) * p.T + w.R.r0 + i] =
                   sum[x] != 0.f ? (mx[x] + log2f(sum[x])) * kLn2 : -INFINITY;
             }
@@ -799,15 +885,18 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
           p.meta[blockIdx.x] = make_int4(w.b, w.h, w.rt, (int)(lastb - blockIdx.x + 1));
         }
       }
+      float* inv = sInv + sw * N;
 #pragma unroll
-      for (int x = 0; x < NL; ++x) sum[x] = sum[x] != 0.f ? 1.f / sum[x] : 0.f;   // NaN stays
+      for (int x = 0; x < NL; ++x)
+        if (x * 32 + lane < N) inv[x * 32 + lane] = sum[x] != 0.f ? 1.f / sum[x] : 0.f;   // NaN stays
+      __syncwarp();
       ok = wait<true>(bar(bOF + slot), (lu >> 1) & 1, W, 0x810);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       // non-finite values of the new rows, by key
       uint32_t nf = 0;
-      if (w.k1 > w.R.nct)
+      if (w.k1 > w.R.kt)
         for (int x = 0; x < MW; ++x) nf |= sNf[slot * 8 + x];
 #pragma unroll
       for (int q = 0; q < NE; q += CH) {
@@ -823,7 +912,6 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
           for (int x = 0; x < MW; ++x)
             for (uint32_t bits = sNf[slot * 8 + x]; bits; bits &= bits - 1) {
               const int j = x * 32 + __ffs(bits) - 1;
-              if (j < (w.k0 - w.R.nct) * kKeys || j >= (w.k1 - w.R.nct) * kKeys) continue;
               const float val = __bfloat162float(p.v[(int64_t)(w.R.r0 + j) * p.vs + w.h * D + d]);
               if (isfinite(val)) continue;
 #pragma unroll
@@ -844,23 +932,14 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
         const bool odd = lane & 1;
 #pragma unroll
         for (int n = 0; n < CH; n += 2) {
-          float v2[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = e0 + q + n + e;
-            float inv = 0.f;
-#pragma unroll
-            for (int x = 0; x < NL; ++x) {
-              const float y = __shfl_sync(0xffffffffu, sum[x], c & 31);
-              if ((c >> 5) == x) inv = y;
-            }
-            // an empty row is zero, whatever its accumulator holds
-            v2[e] = inv != 0.f ? __uint_as_float(ov[n + e]) * inv : 0.f;
-          }
+          // an empty row is zero, whatever its accumulator holds
+          const float2 iv = *reinterpret_cast<const float2*>(inv + e0 + q + n);
+          const float v2[2] = {iv.x != 0.f ? __uint_as_float(ov[n]) * iv.x : 0.f,
+                               iv.y != 0.f ? __uint_as_float(ov[n + 1]) * iv.y : 0.f};
           const float other = __shfl_xor_sync(0xffffffffu, odd ? v2[0] : v2[1], 1);
           const int c = e0 + q + n + (odd ? 1 : 0);
           if (c < rows) {
-            const int r = w.rt * N + c, i = r / p.G, g = r - i * p.G;
+            const int r = w.rt * N + c, i = over_g(p, r), g = r - i * p.G;
             const uint32_t u = odd ? pack_bf16(other, v2[1]) : pack_bf16(v2[0], other);
             *reinterpret_cast<uint32_t*>(p.o + (int64_t)(w.R.r0 + i) * p.os +
                                          (int64_t)(w.h * p.G + g) * D + (d & ~1)) = u;
@@ -984,8 +1063,9 @@ mis_status_t check_desc(const mis_tree_desc* d, const mis_paged_cache* c) {
   if (cs != MIS_OK) return cs;
   if (d->B < 1 || d->T < 0 || d->Hq < 1 || d->max_nodes < 1 || !std::isfinite(d->scale))
     return MIS_ERR_INVALID_ARG;
-  if (d->max_nodes > MIS_TREE_MAX_NODES || d->Hq > 65535) return MIS_ERR_UNSUPPORTED;
+  if (d->max_nodes > MIS_TREE_MAX_NODES) return MIS_ERR_UNSUPPORTED;
   if (d->Hq % c->Hkv) return MIS_ERR_SHAPE;
+  if (d->Hq / c->Hkv > 4096) return MIS_ERR_UNSUPPORTED;
   return MIS_OK;
 }
 
@@ -1010,14 +1090,13 @@ TreeWs workspace_of(const mis_tree_desc* d, const mis_paged_cache* c) {
 }
 
 template <int D, int N>
-mis_status_t launch_tree(const CUtensorMap& kc, const CUtensorMap& vc, const CUtensorMap& k,
-                         const CUtensorMap& v, const TreeParams& p, const CombineParams& c,
+mis_status_t launch_tree(const CUtensorMap* m, const TreeParams& p, const CombineParams& c,
                          cudaStream_t st) {
   using Cf = TreeCfg<D, N>;
   auto kern = mis_tree_attn_kernel<D, N>;
   if (!kernel_attr_once(reinterpret_cast<const void*>(kern), Cf::kSmem)) return MIS_ERR_CUDA;
-  if (launch_pdl(kern, dim3((unsigned)c.blocks), dim3(Cf::kThreads), Cf::kSmem, st, kc, vc, k, v, p) !=
-      cudaSuccess)
+  if (launch_pdl(kern, dim3((unsigned)c.blocks), dim3(Cf::kThreads), Cf::kSmem, st, m[0],
+                 m[1], m[2], m[3], m[4], m[5], p) != cudaSuccess)
     return MIS_ERR_CUDA;
   return launch_pdl(mis_tree_combine_kernel<D, N>, dim3((unsigned)c.blocks, N / 4), dim3(128), 0, st,
                     c) == cudaSuccess
@@ -1066,9 +1145,10 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     return cudaMemsetAsync(workspace, 0, 8, st) == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
   try {
     // the cache as (element, head, row, page), boxes of 64 elements by the
-    // rows of a page (128 at most); the new rows in groups of 8, so that a
-    // short request copies little more than its own rows. Strides of extents
-    // of one are never used, but have to be valid.
+    // rows of a page (128 at most), and by 8 rows for the step that new rows
+    // share; the new rows in groups of 8, so that a short request copies
+    // little more than its own rows. Strides of extents of one are never
+    // used, but have to be valid.
     bool ok = true;
     const uint64_t cd[4] = {(uint64_t)D, (uint64_t)cache->Hkv, (uint64_t)cache->page_size,
                             (uint64_t)cache->n_pages};
@@ -1077,14 +1157,15 @@ extern "C" mis_status_t mis_tree_attention_fwd(
                             stride(cache->row_stride, cache->page_size),
                             stride(cache->page_stride, cache->n_pages)};
     const uint32_t cb[4] = {64, 1, (uint32_t)std::min(cache->page_size, kKeys), 1};
-    const CUtensorMap kcm = make_tmap_bf16(cache->k, 4, cd, cs, cb, &ok);
-    const CUtensorMap vcm = make_tmap_bf16(cache->v, 4, cd, cs, cb, &ok);
+    const uint32_t c8[4] = {64, 1, 8, 1};
     const uint64_t nd[3] = {(uint64_t)D, (uint64_t)cache->Hkv, (uint64_t)desc->T};
     const uint64_t nk[2] = {(uint64_t)D * 2, (uint64_t)k_row_stride * 2};
     const uint64_t nv[2] = {(uint64_t)D * 2, (uint64_t)v_row_stride * 2};
     const uint32_t nb[3] = {64, 1, 8};
-    const CUtensorMap km = make_tmap_bf16(k, 3, nd, nk, nb, &ok);
-    const CUtensorMap vm = make_tmap_bf16(v, 3, nd, nv, nb, &ok);
+    const CUtensorMap maps[6] = {
+        make_tmap_bf16(cache->k, 4, cd, cs, cb, &ok), make_tmap_bf16(cache->v, 4, cd, cs, cb, &ok),
+        make_tmap_bf16(cache->k, 4, cd, cs, c8, &ok), make_tmap_bf16(cache->v, 4, cd, cs, c8, &ok),
+        make_tmap_bf16(k, 3, nd, nk, nb, &ok), make_tmap_bf16(v, 3, nd, nv, nb, &ok)};
     if (!ok) return MIS_ERR_CUDA;
     uint8_t* base = static_cast<uint8_t*>(workspace);
     TreeParams p;
@@ -1100,6 +1181,7 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     p.cache_len = cache_len; p.cu = cu_nodes; p.parents = parents;
     p.B = desc->B; p.T = desc->T; p.Hq = desc->Hq; p.Hkv = cache->Hkv;
     p.G = desc->Hq / cache->Hkv;
+    p.g_magic = (uint32_t)((0xffffffffull + (uint64_t)p.G) / (uint64_t)p.G);
     p.max_nodes = desc->max_nodes;
     p.scale_log2 = (desc->scale != 0.f ? desc->scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
     p.cta_status = reinterpret_cast<uint32_t*>(base + ws.status);
@@ -1115,15 +1197,15 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     c.T = desc->T; c.G = p.G; c.blocks = num_sms();
     const int N = tile_rows(desc, cache);
     if (D == 128) {
-      if (N == 16) return launch_tree<128, 16>(kcm, vcm, km, vm, p, c, st);
-      if (N == 32) return launch_tree<128, 32>(kcm, vcm, km, vm, p, c, st);
-      if (N == 64) return launch_tree<128, 64>(kcm, vcm, km, vm, p, c, st);
-      return launch_tree<128, 128>(kcm, vcm, km, vm, p, c, st);
+      if (N == 16) return launch_tree<128, 16>(maps, p, c, st);
+      if (N == 32) return launch_tree<128, 32>(maps, p, c, st);
+      if (N == 64) return launch_tree<128, 64>(maps, p, c, st);
+      return launch_tree<128, 128>(maps, p, c, st);
     }
-    if (N == 16) return launch_tree<64, 16>(kcm, vcm, km, vm, p, c, st);
-    if (N == 32) return launch_tree<64, 32>(kcm, vcm, km, vm, p, c, st);
-    if (N == 64) return launch_tree<64, 64>(kcm, vcm, km, vm, p, c, st);
-    return launch_tree<64, 128>(kcm, vcm, km, vm, p, c, st);
+    if (N == 16) return launch_tree<64, 16>(maps, p, c, st);
+    if (N == 32) return launch_tree<64, 32>(maps, p, c, st);
+    if (N == 64) return launch_tree<64, 64>(maps, p, c, st);
+    return launch_tree<64, 128>(maps, p, c, st);
   } catch (...) {
     return MIS_ERR_CUDA;
   }

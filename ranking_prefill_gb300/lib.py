@@ -582,50 +582,59 @@ def _require(ok, status: int, where: str):
         raise MisError(status, where)
 
 
-def _on_device(where: str, dtype, *tensors):
-    """Every tensor (None passes) is of `dtype` on the current CUDA device."""
+def _here(stream):
+    """(current device, stream address). One look at the runtime per call: the
+    checks below compare every tensor's device with it."""
     import torch
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    if not torch.cuda.is_initialized() and not torch.cuda.is_available():
+        return -1, None
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _vectors(where: str, dev: int, *pairs):
+    """(tensor or None, n): contiguous int32 vectors of at least n elements on `dev`."""
+    import torch
+    i32 = torch.int32
+    for t, n in pairs:
+        if t is not None:
+            if t.dtype is not i32 or t.get_device() != dev:
+                raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+            if t.dim() != 1 or t.numel() < n or not t.is_contiguous():
+                raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+
+
+def _rows(where: str, dev: int, T: int, heads: int, D: int, *tensors):
+    """Row strides of bf16 [>= T, heads, D] tensors on `dev`, heads packed inside a row."""
+    import torch
+    bf16 = torch.bfloat16
+    out = []
     for t in tensors:
-        if t is not None and (t.dtype != dtype or t.get_device() != dev):
+        if t.dtype is not bf16 or t.get_device() != dev:
             raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
-
-
-def _flat_i32(where: str, n: int, *tensors):
-    """Contiguous int32 vectors (None passes) of at least n elements on the current device."""
-    import torch
-    _on_device(where, torch.int32, *tensors)
-    for t in tensors:
-        if t is not None and (t.dim() != 1 or t.numel() < n or (t.numel() > 1 and t.stride(0) != 1)):
+        st, sh = t.stride(), t.shape
+        if (len(sh) != 3 or sh[0] < T or sh[1] != heads or sh[2] != D or st[2] != 1 or
+                (heads > 1 and st[1] != D)):
             raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+        out.append(st[0] if sh[0] > 1 else heads * D)
+    return out
 
 
-def _rows_bf16(where: str, heads: int, D: int, *tensors):
-    """[T, heads, D] bf16 rows, heads packed inside a row, on the current device."""
+def _table(where: str, dev: int, t, B: int) -> int:
+    """Row stride of an int32 [>= B, pages] table on `dev`."""
     import torch
-    _on_device(where, torch.bfloat16, *tensors)
-    for t in tensors:
-        if (t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.stride(2) != 1 or
-                (heads > 1 and t.stride(1) != D)):
-            raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
-
-
-def _table(where: str, t):
-    import torch
-    _on_device(where, torch.int32, t)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dtype is not torch.int32 or t.get_device() != dev:
+        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    if t.dim() != 2 or t.shape[0] < B or (t.shape[1] > 1 and t.stride(1) != 1):
         raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
-def _row_stride(t, width: int) -> int:
-    return t.stride(0) if t.shape[0] > 1 else width
-
-
-def _workspace(where: str, t) -> int:
+def _workspace(where: str, dev: int, t) -> int:
     import torch
-    _on_device(where, torch.uint8, t)
-    if not t.is_contiguous():
+    if t.dtype is not torch.uint8 or t.get_device() != dev or not t.is_contiguous():
         raise MisError(MIS_ERR_WORKSPACE, where)  # noqa: F821
     return t.numel()
 
@@ -638,7 +647,9 @@ class PagedCache:
     def __init__(self, k, v):
         import torch
         where = "PagedCache"
-        _on_device(where, torch.bfloat16, k, v)
+        dev, _ = _here(0)
+        _require(k.dtype == v.dtype == torch.bfloat16 and k.get_device() == v.get_device() == dev,
+                 MIS_ERR_INVALID_ARG, where)  # noqa: F821
         _require(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and
                  k.stride(3) == 1, MIS_ERR_SHAPE, where)  # noqa: F821
         self.k, self.v = k, v
@@ -678,21 +689,21 @@ def mis_paged_extend(new_len, cache_len, cache_len_out, block_table, free_pages,
     cache_len, cache_len_out [B] (the last two may be one tensor), block_table
     [B, max_pages], free_pages, free_head, free_head_out [1] (may be one),
     cu_new [B+1], slot_map [T], position_ids [T] or None."""
-    L = load()
+    L = _lib or load()
     where = "mis_paged_extend"
-    B, T = new_len.numel(), slot_map.numel()
-    _flat_i32(where, 0, new_len, slot_map, free_pages)
-    _flat_i32(where, B, cache_len, cache_len_out)
-    _flat_i32(where, B + 1, cu_new)
-    _flat_i32(where, 1, free_head, free_head_out)
-    _flat_i32(where, T, position_ids)
-    stride = _table(where, block_table)
-    _require(block_table.shape[0] >= B, MIS_ERR_SHAPE, where)  # noqa: F821
-    _check(L.mis_paged_extend(B, T, page_size, n_pages, _dptr(new_len), _dptr(cache_len),
-                              _dptr(cache_len_out), _dptr(block_table), block_table.shape[1], stride,
-                              _dptr(free_pages), free_pages.numel(), _dptr(free_head),
-                              _dptr(free_head_out), _dptr(cu_new), _dptr(slot_map), _dptr(position_ids),
-                              _dptr(workspace), _workspace(where, workspace), _stream(stream)), where)
+    dev, st = _here(stream)
+    B, T, n_free = new_len.numel(), slot_map.numel(), free_pages.numel()
+    _vectors(where, dev, (new_len, B), (cache_len, B), (cache_len_out, B), (cu_new, B + 1), (slot_map, T),
+             (position_ids, T), (free_pages, n_free), (free_head, 1), (free_head_out, 1))
+    stride = _table(where, dev, block_table, B)
+    st = L.mis_paged_extend(B, T, page_size, n_pages, new_len.data_ptr(), cache_len.data_ptr(),
+                            cache_len_out.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+                            stride, free_pages.data_ptr(), n_free, free_head.data_ptr(),
+                            free_head_out.data_ptr(), cu_new.data_ptr(), slot_map.data_ptr(),
+                            None if position_ids is None else position_ids.data_ptr(),
+                            workspace.data_ptr(), _workspace(where, dev, workspace), st)
+    if st:
+        raise MisError(st, where)
 
 
 def mis_paged_write_workspace_size() -> int:
@@ -703,17 +714,20 @@ def mis_paged_write_kv(cache: PagedCache, k, v, slot_map, workspace, position_id
                        base: float = 1.0e6, src_rows=None, stream=None):
     """Store rows of k, v [T, Hkv, D] at the slots of slot_map [n] (negative: skip);
     row src_rows[i], or i; K rotated at position_ids[i] if given."""
-    L = load()
+    L = _lib or load()
     where = "mis_paged_write_kv"
-    n, w = slot_map.numel(), cache.Hkv * cache.D
-    _rows_bf16(where, cache.Hkv, cache.D, k, v)
-    _require(k.shape[0] == v.shape[0], MIS_ERR_SHAPE, where)  # noqa: F821
-    _require(cache.device == k.get_device(), MIS_ERR_INVALID_ARG, where)  # noqa: F821
-    _flat_i32(where, n, slot_map, position_ids, src_rows)
-    _check(L.mis_paged_write_kv(cache.ref, _dptr(k), _dptr(v), _row_stride(k, w), _row_stride(v, w),
-                                k.shape[0], _dptr(src_rows), _dptr(slot_map), n, _dptr(position_ids),
-                                float(base), _dptr(workspace), _workspace(where, workspace),
-                                _stream(stream)), where)
+    dev, st = _here(stream)
+    n = slot_map.numel()
+    _require(cache.device == dev, MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    T = k.shape[0]
+    ks, vs = _rows(where, dev, T, cache.Hkv, cache.D, k, v)
+    _vectors(where, dev, (slot_map, n), (position_ids, n), (src_rows, n))
+    st = L.mis_paged_write_kv(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs, T,
+                              None if src_rows is None else src_rows.data_ptr(), slot_map.data_ptr(), n,
+                              None if position_ids is None else position_ids.data_ptr(), base,
+                              workspace.data_ptr(), _workspace(where, dev, workspace), st)
+    if st:
+        raise MisError(st, where)
 
 
 def mis_tree_attention_fwd(desc: TreeDesc, q, k, v, o, lse, block_table, cache_len, cu_nodes, parents,
@@ -722,28 +736,27 @@ def mis_tree_attention_fwd(desc: TreeDesc, q, k, v, o, lse, block_table, cache_l
     up to cache_len [B] and over the ancestors among the request's own rows of
     k, v [T, Hkv, D], [cu_nodes[b], cu_nodes[b+1]); parents [T] or None (chains);
     o like q, lse fp32 [Hq, T] or None."""
-    import torch
-    L = load()
+    L = _lib or load()
     where = "mis_tree_attention_fwd"
-    c, T = desc.cache, desc.T
-    _rows_bf16(where, desc.Hq, c.D, q, o)
-    _rows_bf16(where, c.Hkv, c.D, k, v)
-    _require(c.device == q.get_device(), MIS_ERR_INVALID_ARG, where)  # noqa: F821
-    _require(min(q.shape[0], k.shape[0], v.shape[0], o.shape[0]) >= T, MIS_ERR_SHAPE, where)  # noqa: F821
+    dev, st = _here(stream)
+    c, T, B, Hq = desc.cache, desc.T, desc.B, desc.Hq
+    _require(c.device == dev, MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    qs, os_ = _rows(where, dev, T, Hq, c.D, q, o)
+    ks, vs = _rows(where, dev, T, c.Hkv, c.D, k, v)
     if lse is not None:
-        _on_device(where, torch.float32, lse)
-        _require(lse.is_contiguous() and lse.shape == (desc.Hq, T), MIS_ERR_SHAPE, where)  # noqa: F821
-    _flat_i32(where, desc.B, cache_len)
-    _flat_i32(where, desc.B + 1, cu_nodes)
-    _flat_i32(where, T, parents)
-    stride = _table(where, block_table)
-    _require(block_table.shape[0] >= desc.B, MIS_ERR_SHAPE, where)  # noqa: F821
-    wq, wk = desc.Hq * c.D, c.Hkv * c.D
-    _check(L.mis_tree_attention_fwd(desc.ref, c.ref, _dptr(q), _dptr(k), _dptr(v), _dptr(o), _dptr(lse),
-                                    _row_stride(q, wq), _row_stride(k, wk), _row_stride(v, wk),
-                                    _row_stride(o, wq), _dptr(block_table), block_table.shape[1], stride,
-                                    _dptr(cache_len), _dptr(cu_nodes), _dptr(parents), _dptr(workspace),
-                                    _workspace(where, workspace), _stream(stream)), where)
+        import torch
+        _require(lse.dtype is torch.float32 and lse.get_device() == dev, MIS_ERR_INVALID_ARG, where)  # noqa: F821
+        _require(lse.shape == (Hq, T) and lse.is_contiguous(), MIS_ERR_SHAPE, where)  # noqa: F821
+        lse = lse.data_ptr()
+    _vectors(where, dev, (cache_len, B), (cu_nodes, B + 1), (parents, T))
+    stride = _table(where, dev, block_table, B)
+    st = L.mis_tree_attention_fwd(desc.ref, c.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                  lse, qs, ks, vs, os_, block_table.data_ptr(), block_table.shape[1],
+                                  stride, cache_len.data_ptr(), cu_nodes.data_ptr(),
+                                  None if parents is None else parents.data_ptr(), workspace.data_ptr(),
+                                  _workspace(where, dev, workspace), st)
+    if st:
+        raise MisError(st, where)
 
 
 def mis_get_device_status(workspace, stream=None) -> int:
