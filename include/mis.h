@@ -519,7 +519,8 @@ mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const void* k, con
  *     j in [0, cache_len[b]) (cached) and j on the path from i to its root.
  * The nodes' own K/V are read from k and v (already rotated), not from the
  * cache; mis_paged_write_kv() stores the ones that were accepted.
- *   B, T      — requests, rows of q, k, v, o (>= 0); Hq a multiple of Hkv
+ *   B, T      — requests, rows of q, k, v, o (>= 0); Hq a multiple of Hkv, at
+ *               most 128 query heads a kv head
  *   max_nodes — upper bound on a request's nodes, 1 .. MIS_TREE_MAX_NODES
  *   scale     — softmax scale, finite; 0 selects 1/sqrt(D)
  *   q, k, v, o, lse, row strides — as in mis_attention_fwd_plan (lse fp32

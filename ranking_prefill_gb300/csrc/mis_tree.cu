@@ -13,6 +13,8 @@
 // columns of softmax instead of 128 rows, and one pass over K and V serves
 // every row of the tile.
 //
+// A tile holds the G rows of N / G nodes (rounded down), so one TMA box loads
+// its Q.
 // Work is cut evenly: the (request, kv head, row tile) units are laid end to
 // end in 128-key steps and every block takes the same number of consecutive
 // steps, found on the device from the lengths (no host plan). A block that
@@ -20,13 +22,18 @@
 // leave (max, sum, unnormalised O) in the workspace and a second kernel adds
 // them in block order, so the same call gives the same bits.
 //
-// Warp roles: 0 TMA producer (pages of the cache, 8-row groups of the new
-// rows), 1 MMA issue, 2-3 load Q and build the tree's masks, then one or two
-// softmax warpgroups (a thread is a key, it owns N or N / 2 columns) and an
-// epilogue warpgroup (a thread is an element of the head).
-// The running maximum of a column is common to the block's keys. It is moved
-// only when a score passes it by 2^8: one vote per tile replaces the exchange
-// of maxima, and O in tensor memory is rescaled only then.
+// Warp roles: 0 TMA producer of K and V (pages of the cache, 8-row groups of
+// the new rows), 1 MMA issue, 2-3 Q's copies and the tree's masks, then one or
+// two softmax warpgroups (a thread is a key, it owns N or N / 2 columns) and
+// an epilogue warpgroup (a thread is an element of the head).
+//
+// Any reference serves a column's softmax as long as its scores stay within
+// the exponent's reach of it. One reference for all columns of a warpgroup
+// stays in a register: it is the largest maximum, taken when the columns'
+// maxima lie within 2^40 of each other (else every column has its own, read
+// from shared memory). It is moved only when a score passes it by 2^8: one
+// vote per step replaces the exchange of maxima, and O in tensor memory is
+// rescaled only then.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -46,7 +53,8 @@ namespace {
 using namespace dev;
 
 constexpr int kKeys = 128;                       // keys of a step
-constexpr float kGrow = 8.0f;                    // log2 units a score may pass the maximum by
+constexpr float kGrow = 8.0f;                    // log2 units a score may pass the reference by
+constexpr float kSpread = 40.0f;                 // ... and maxima may differ under one reference
 constexpr float kEmpty = -1.0e30f;               // maximum of a column that has seen nothing
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -70,11 +78,12 @@ struct TreeCfg {
   static constexpr int oMask = 0;                       // [2][N][kMW]
   static constexpr int oDead = oMask + 2 * N * kMW;     // [2][4] unused rows of the tile
   static constexpr int oNf = oDead + 8;                 // [2][8] keys with a non-finite value
-  static constexpr int oM = oNf + 16;                   // [2][N] maxima, negated
+  static constexpr int oM = oNf + 16;                   // [2][N] references, negated, for the epilogue
   static constexpr int oL = oM + 2 * N;                 // [2][4][N] sums of each softmax warp
-  static constexpr int oMax = oL + 8 * N;               // [4][N] maxima of a tile
-  static constexpr int oAl = oMax + 4 * N;              // [N] factors
-  static constexpr int oInv = oAl + N;                  // [4][N] an epilogue warp's 1 / sum
+  static constexpr int oMax = oL + 8 * N;               // [4][N] maxima of a step by warp
+  static constexpr int oRef = oMax + 4 * N;             // [4][N] a warp's copy of the negated references
+  static constexpr int oAl = oRef + 4 * N;              // [4][N] ... of the factors of a move
+  static constexpr int oInv = oAl + 4 * N;              // [4][N] an epilogue warp's 1 / sum
   static constexpr int oPar = oInv + 4 * N;             // [2][256] int16: a loader warp's parents
   static constexpr int kWords = oPar + MIS_TREE_MAX_NODES;
   static constexpr int kData = kQS * kQ + kP + (kK + kV) * kTile;
@@ -87,19 +96,19 @@ struct TreeCfg {
 constexpr int kRegCtl = 64, kRegEpi = 64, kRegSoft = 192;
 
 struct TreeParams {
-  const __nv_bfloat16* q;
   const __nv_bfloat16* v;
   __nv_bfloat16* o;
   float* lse;
-  int64_t qs, vs, os;
+  int64_t vs, os;
   int32_t n_pages, page_shift, max_pages;
   const int32_t* table;
   int64_t table_stride;
   const int32_t* cache_len;
   const int32_t* cu;
   const int32_t* parents;
-  int32_t B, T, Hq, Hkv, G, max_nodes;
-  uint32_t g_magic;        // ceil(2^32 / G): r / G = umulhi(r, magic) for r < 2^20, G <= 4096
+  int32_t B, T, Hkv, G, max_nodes;
+  int32_t npt;             // nodes of a row tile, N / G
+  uint32_t g_magic;        // ceil(2^32 / G): n / G = umulhi(n, magic) for n < N, 1 < G <= 128
   float scale_log2;
   uint32_t* cta_status;    // [blocks][2]
   int4* meta;              // [blocks] the split unit that starts in the block: b, h, row tile, pieces
@@ -137,7 +146,7 @@ __device__ __forceinline__ Req load_req(const TreeParams& p, int b) {
   R.a = share ? a : 0;
   R.kt = share ? nct - 1 : nct;
   R.nkt = share ? nct : nct + (R.n + kKeys - 1) / kKeys;
-  R.nrt = (R.n * p.G + N - 1) / N;
+  R.nrt = N < 128 ? 1 : (R.n + p.npt - 1) / p.npt;
   return R;
 }
 
@@ -152,11 +161,11 @@ template <int N>
 struct Walk {
   const TreeParams& p;
   Req R;
-  int64_t left;
+  int left;
   int b, h, rt, k0, k1;
   bool fresh;
 
-  __device__ __forceinline__ Walk(const TreeParams& prm, const Start& s, int64_t steps)
+  __device__ __forceinline__ Walk(const TreeParams& prm, const Start& s, int steps)
       : p(prm), R(s.R), left(steps), b(s.b), h(s.h), rt(s.rt), k0(s.k0), k1(0), fresh(true) {}
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
@@ -174,7 +183,7 @@ struct Walk {
       }
     }
     fresh = false;
-    k1 = (int)min((int64_t)R.nkt, k0 + left);
+    k1 = min(R.nkt, k0 + left);
     left -= k1 - k0;
     return true;
   }
@@ -184,13 +193,19 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ int over_g(const TreeParams& p, int r) {
-  return p.G == 1 ? r : (int)__umulhi((uint32_t)r, p.g_magic);
+// Node (in its tile) of column n.
+__device__ __forceinline__ int over_g(const TreeParams& p, int n) {
+  return p.G == 1 ? n : (int)__umulhi((uint32_t)n, p.g_magic);
 }
 
-__device__ __forceinline__ float warp_max(float x) {
+__device__ __forceinline__ float warp_max(float x) {       // NaN only if all are
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float warp_min(float x) {
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -215,7 +230,8 @@ __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t* r) {
 
 template <int D, int N>
 __global__ void __launch_bounds__(TreeCfg<D, N>::kThreads, 1)
-mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
+mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ CUtensorMap kcmap,
                      const __grid_constant__ CUtensorMap vcmap,
                      const __grid_constant__ CUtensorMap kc8map,
                      const __grid_constant__ CUtensorMap vc8map,
@@ -245,6 +261,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
   float* sM = reinterpret_cast<float*>(words + C::oM);
   float* sL = reinterpret_cast<float*>(words + C::oL);
   float* sMax = reinterpret_cast<float*>(words + C::oMax);
+  float* sRef = reinterpret_cast<float*>(words + C::oRef);
   float* sAl = reinterpret_cast<float*>(words + C::oAl);
   float* sInv = reinterpret_cast<float*>(words + C::oInv);
   int16_t* sPar = reinterpret_cast<int16_t*>(words + C::oPar);
@@ -252,14 +269,14 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + nBar);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   __shared__ Start s_start;
-  __shared__ int64_t s_sums[C::kThreads / 32];
+  __shared__ int s_sums[C::kThreads / 32];
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(bQF + s), 2);
+      mbar_init(bar(bQF + s), 1);
       mbar_init(bar(bQE + s), 1);
       mbar_init(bar(bSF + s), 1);
       mbar_init(bar(bOF + s), 1);
@@ -275,7 +292,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
     mbar_init(bar(bDR), 1);
     fence_mbar_init();
     fence_proxy_async();
-    tma_prefetch_desc(&kcmap); tma_prefetch_desc(&vcmap);
+    tma_prefetch_desc(&qmap); tma_prefetch_desc(&kcmap); tma_prefetch_desc(&vcmap);
+    tma_prefetch_desc(&kc8map); tma_prefetch_desc(&vc8map);
     tma_prefetch_desc(&kmap); tma_prefetch_desc(&vmap);
   }
   if (warp == 1) {
@@ -288,18 +306,19 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
   uint32_t* status = p.cta_status + 2 * blockIdx.x;
   const int per = (p.B + C::kThreads - 1) / C::kThreads;
   const int rb0 = min(p.B, (int)threadIdx.x * per), rb1 = min(p.B, rb0 + per);
-  int64_t mine = 0;
+  int mine = 0;                                  // the host bounds the total below 2^31
   bool bad_req = false;
   Req R;
+#pragma unroll 1
   for (int b = rb0; b < rb1; ++b) {
     R = load_req<N>(p, b);
     bad_req |= R.bad;
-    if (R.n) mine += (int64_t)p.Hkv * R.nrt * R.nkt;
+    if (R.n) mine += p.Hkv * R.nrt * R.nkt;
   }
-  int64_t incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) s_sums[warp] = incl;
@@ -311,37 +330,32 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
   tc_fence_before();
   const bool any_bad = __syncthreads_or(bad_req);
   tc_fence_after();
-  int64_t total = 0, before = 0;
+  int total = 0, before = 0;
 #pragma unroll
   for (int w = 0; w < C::kThreads / 32; ++w) {
     if (w == warp) before = total;
     total += s_sums[w];
   }
   if (any_bad && blockIdx.x == 0 && threadIdx.x == 0) raise_status(status, kDevIndex, 0x40);
-  const int64_t blocks = min((int64_t)gridDim.x, total);
-  int64_t f0 = 0, f1 = 0;
-  if (blockIdx.x < blocks) {
-    if (total < (1 << 24)) {                    // products below 2^32: short division
-      f0 = blockIdx.x * (uint32_t)total / (uint32_t)blocks;
-      f1 = (blockIdx.x + 1) * (uint32_t)total / (uint32_t)blocks;
-    } else {
-      f0 = blockIdx.x * total / blocks;
-      f1 = (blockIdx.x + 1) * total / blocks;
-    }
-    int64_t at = before + incl - mine;
-    if (f0 >= at && f0 < at + mine) {
+  // blocks [0, rem) take quo + 1 steps, the others quo
+  const int quo = total / (int)gridDim.x, rem = total - quo * (int)gridDim.x;
+  const int blk = (int)blockIdx.x;
+  const int f0 = blk * quo + min(blk, rem), steps = quo + (blk < rem ? 1 : 0);
+  {
+    int at = before + incl - mine;
+    if (steps > 0 && f0 >= at && f0 < at + mine) {
+#pragma unroll 1
       for (int b = rb0; b < rb1; ++b) {
         if (per > 1) R = load_req<N>(p, b);
-        const int64_t c = R.n ? (int64_t)p.Hkv * R.nrt * R.nkt : 0;
+        const int c = R.n ? p.Hkv * R.nrt * R.nkt : 0;
         if (f0 >= at + c) { at += c; continue; }
         Start s;
         s.R = R;
         s.b = b;
-        const int64_t off = f0 - at;
-        const int64_t u = (off >> 31) == 0 ? (uint32_t)off / (uint32_t)R.nkt : off / R.nkt;
-        s.k0 = (int)(off - u * R.nkt);
-        s.h = (int)((u >> 31) == 0 ? (uint32_t)u / (uint32_t)R.nrt : u / R.nrt);
-        s.rt = (int)(u - (int64_t)s.h * R.nrt);
+        const int off = f0 - at, u = off / R.nkt;
+        s.k0 = off - u * R.nkt;
+        s.h = N < 128 ? u : u / R.nrt;
+        s.rt = u - s.h * R.nrt;
         s_start = s;
         break;
       }
@@ -349,7 +363,6 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  const int64_t steps = f1 - f0;
   const Waiter W{abort_flag, status, p.wait_ns};
   auto colS = [](int s) { return (uint32_t)(s * N); };
   auto colO = [](int s) { return (uint32_t)((2 + s) * N); };
@@ -507,15 +520,29 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
         wait_drain(bar(bDR), 0);
       }
     } else {
-      // --------------------------------------------- Q rows and the tree's masks
+      // ------------------------------------------ Q's copies and the tree's masks
       const int th = threadIdx.x - 64;
-      int lu = 0;
+      int lu = 0, q_issued = 0;
       bool ok = true, bad = false;
       while (ok && w.next()) {
-        const int rows = min(N, w.R.n * p.G - w.rt * N), rbase = w.rt * N;
+        const int node0 = w.rt * p.npt, rows = min(p.npt, w.R.n - node0) * p.G;
         const int sq = lu % QS, sm = lu & 1;
-        if (lu >= QS) ok = wait<true>(bar(bQE + sq), ((lu / QS) - 1) & 1, W, 0x600);
-        if (ok && lu >= 2) ok = wait<true>(bar(bSE + sm), ((lu >> 1) - 1) & 1, W, 0x610);
+        if (warp == 2) {
+          if (lu >= QS) ok = wait<true>(bar(bQE + sq), ((lu / QS) - 1) & 1, W, 0x600);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          // the rows of npt nodes (nodes behind the request's are columns that
+          // nobody reads)
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(bQF + sq), (uint32_t)(NB * p.npt * p.G * 128));
+            for (int x = 0; x < NB; ++x)
+              tma_load_3d(smem_u32(sQ + sq * C::kQ) + x * C::kQBox, &qmap, bar(bQF + sq), x * 64,
+                          w.h * p.G, w.R.r0 + node0);
+          }
+          q_issued = lu + 1;
+          __syncwarp();
+        }
+        if (lu >= 2) ok = wait<true>(bar(bSE + sm), ((lu >> 1) - 1) & 1, W, 0x610);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         // parents as the masks use them (each warp keeps its own copy): the
@@ -524,36 +551,21 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
         const bool tree = w.k1 > w.R.kt;
         int16_t* par = sPar + (warp - 2) * MIS_TREE_MAX_NODES;
         if (p.parents) {
+#pragma unroll 2
           for (int j = lane; j < w.R.n; j += 32) {
             int up = p.parents[w.R.r0 + j];
             if (up >= j || up < MIS_TREE_UNUSED) { up = -1; bad = true; }
             if (up >= 0 && p.parents[w.R.r0 + up] == MIS_TREE_UNUSED) up = -1;
             par[j] = (int16_t)up;
           }
+          __syncwarp();
         }
-        const uint32_t aQ = smem_u32(sQ + sq * C::kQ);
-        constexpr int CH = D / 8;
-#pragma unroll 4
-        for (int x = th; x < N * CH; x += 64) {
-          const int n = x / CH, c = x % CH;
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (n < rows) {
-            const int r = rbase + n, i = over_g(p, r), g = r - i * p.G;
-            u = *reinterpret_cast<const uint4*>(p.q + (int64_t)(w.R.r0 + i) * p.qs +
-                                                (int64_t)(w.h * p.G + g) * D + c * 8);
-          }
-          st_shared_v4(aQ + (c >> 3) * C::kQBox + n * 128 + (((c & 7) ^ (n & 7)) << 4), u.x, u.y,
-                       u.z, u.w);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bQF + sq));
         // columns of unused nodes, and who sees which new key
         if (th < 8) sNf[sm * 8 + th] = 0;
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < N; c0 += 64) {
           const int n = c0 + th;
-          const int i = over_g(p, rbase + n);
+          const int i = node0 + over_g(p, n);
           const bool live = n < rows;
           const bool dead = live && p.parents && par[i] == MIS_TREE_UNUSED;
           const uint32_t dw = __ballot_sync(0xffffffffu, dead);
@@ -561,14 +573,11 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
             if (lane == 0) sDead[sm * 4 + (n >> 5)] = dw;
             uint32_t* m = sMask + (sm * N + n) * MW;
             if (tree) {
-              if (p.parents) {
+              const bool chain = !p.parents;
 #pragma unroll
-                for (int x = 0; x < MW; ++x) m[x] = 0;
-                for (int j = (live && !dead) ? i : -1; j >= 0; j = par[j]) m[j >> 5] |= 1u << (j & 31);
-              } else {
-#pragma unroll
-                for (int x = 0; x < MW; ++x) m[x] = live ? bit_range(0, i + 1 - 32 * x) : 0u;
-              }
+              for (int x = 0; x < MW; ++x) m[x] = chain && live ? bit_range(0, i + 1 - 32 * x) : 0u;
+              for (int j = (live && !dead && !chain) ? i : -1; j >= 0; j = par[j])
+                m[j >> 5] |= 1u << (j & 31);
             }
           }
         }
@@ -576,6 +585,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
         if (lane == 0) mbar_arrive(bar(bMF + sm));
         ++lu;
       }
+      __syncwarp();
+      for (int i = max(0, q_issued - QS); i < q_issued; ++i) wait_drain(bar(bQF + i % QS), (i / QS) & 1);
       if (bad) raise_status(status, kDevIndex, 0x42);
     }
   } else if (warp < 4 + 4 * WG) {
@@ -587,26 +598,30 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
     const float sl2 = p.scale_log2;
     const uint32_t hidden = sl2 < 0.f ? 0x7f800000u : 0xff800000u;     // scales to -inf
     const uint64_t sl2x2 = f2_pack(__float_as_uint(sl2), __float_as_uint(sl2));
-    // columns in registers at a time. Two pieces (N = 128) are read from
-    // tensor memory twice, once for the maximum and once for P.
-    constexpr int CC = NC > 32 ? 32 : NC, NP = NC / CC;
+    // columns in registers at a time: two pieces (N = 128) are read from
+    // tensor memory twice, once for the maximum and once for P
+    constexpr int CC = NC > 32 ? 32 : NC;
     // this thread's row of P: chunk c of its columns
     const uint32_t aP = smem_u32(sP) + (N == 128 ? wg * C::kBox : 0) + r * 128;
     const int cP = (N == 128 ? 0 : c0) / 8;
+    float* ref = sRef + sw * N + c0;                     // negated references, if not one for all
+    float* al = sAl + sw * N + c0;
     Walk<N> w(p, s_start, steps);
     int t = 0, lu = 0;
     bool ok = true, gone = false;
     while (!gone && w.next()) {
-      const int slot = lu & 1;
+      const int slot = lu & 1, rows = min(p.npt, w.R.n - w.rt * p.npt) * p.G;
       uint64_t l2[NC / 2];
 #pragma unroll
       for (int n = 0; n < NC / 2; ++n) l2[n] = 0ull;
-      float* nm = sM + slot * N + c0;                    // negated maxima
+      bool one = true;                                   // one reference, -base, for all columns
+      float base = 0.f;
       if (ok && lu >= 2) {
         ok = wait<true>(bar(bSE + slot), ((lu >> 1) - 1) & 1, W, 0x700);
         ok = __all_sync(0xffffffffu, ok);
       }
       const int32_t* row = p.table + (int64_t)w.b * p.table_stride;
+#pragma unroll 1
       for (int k = w.k0; k < w.k1; ++k, ++t) {
         const int kv = w.keys(k), kv16 = (kv + 15) & ~15;
         const bool first = k == w.k0, fresh = k >= w.R.kt;
@@ -625,115 +640,139 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
           ok = __all_sync(0xffffffffu, ok);
         }
         tc_fence_after();
-        uint32_t s[CC];
+        const uint32_t tS = tl + colS(t & 1) + c0;
+        const uint32_t* mk = sMask + (slot * N + c0) * MW + (node ? j >> 5 : 0);
+        const bool plain = __all_sync(0xffffffffu, seen && !node);
         // columns q .. q + CC - 1 of the scores; what a row does not see is -inf
+        uint32_t s[CC];
         auto load = [&](int q) {
-          ld_cols<CC>(tl + colS(t & 1) + c0 + q, s);
-          if (node) {
-            const uint32_t* mk = sMask + (slot * N + c0 + q) * MW + (j >> 5);
+          ld_cols<CC>(tS + q, s);
+          if (!plain) {
 #pragma unroll
             for (int n = 0; n < CC; ++n)
-              if (!((mk[n * MW] >> (j & 31)) & 1u)) s[n] = hidden;
-          } else if (!seen) {
-#pragma unroll
-            for (int n = 0; n < CC; ++n) s[n] = hidden;
+              if (!seen || (node && !((mk[(q + n) * MW] >> (j & 31)) & 1u))) s[n] = hidden;
+            __syncwarp();
           }
-          __syncwarp();
         };
-        // s = scaled scores less the maxima, in log2 units; their largest
-        auto shift = [&](int q) -> float {
-          float x0 = kEmpty, x1 = kEmpty;
-#pragma unroll
-          for (int n = 0; n < CC; n += 4) {
-            const float4 b = *reinterpret_cast<const float4*>(nm + q + n);
-            float a0, a1, a2, a3;
-            f2_unpack(f2_fma(f2_pack(s[n], s[n + 1]), sl2x2,
-                             f2_pack(__float_as_uint(b.x), __float_as_uint(b.y))), a0, a1);
-            f2_unpack(f2_fma(f2_pack(s[n + 2], s[n + 3]), sl2x2,
-                             f2_pack(__float_as_uint(b.z), __float_as_uint(b.w))), a2, a3);
-            x0 = max3(x0, a0, a1);
-            x1 = max3(x1, a2, a3);
-            s[n] = __float_as_uint(a0); s[n + 1] = __float_as_uint(a1);
-            s[n + 2] = __float_as_uint(a2); s[n + 3] = __float_as_uint(a3);
-          }
-          return fmaxf(x0, x1);
-        };
+        if (CC == NC && ok && active) load(0);
         bool move = first;
         if (!first) {
           bool over = !ok;
           if (ok && active) {
-            float mx = kEmpty;
+            float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
             for (int q = 0; q < NC; q += CC) {
-              load(q);
-              mx = fmaxf(mx, shift(q));
+              if (CC < NC) load(q);
+              if (one) {
+#pragma unroll
+                for (int n = 0; n < CC; n += 4) {
+                  x0 = max3(x0, __uint_as_float(s[n]), __uint_as_float(s[n + 1]));
+                  x1 = max3(x1, __uint_as_float(s[n + 2]), __uint_as_float(s[n + 3]));
+                }
+              } else {
+#pragma unroll
+                for (int n = 0; n < CC; n += 2) {
+                  const float2 b = *reinterpret_cast<const float2*>(ref + q + n);
+                  x0 = max3(x0, fmaf(__uint_as_float(s[n]), sl2, b.x), fmaf(__uint_as_float(s[n + 1]), sl2, b.y));
+                }
+              }
             }
-            over = mx > kGrow;
+            over = (one ? fmaf(fmaxf(x0, x1), sl2, base) : x0) > kGrow;
           }
           move = bar_any128(id, over);
         }
         if (move) {
-          // a unit begins or a score passed its column's maximum (or a wait
-          // gave up: then every warp of the warpgroup leaves here)
+          // a unit begins or a score passed its reference (or a wait gave up:
+          // then every warp of the warpgroup leaves here)
           if (bar_any128(id, !ok)) { gone = true; break; }
-#pragma unroll
-          for (int q = 0; q < NC; q += CC) {
+          // the step's maximum of every column over this warp's keys; rolled,
+          // since straight code that runs once is paid in instruction fetches
+#pragma unroll 1
+          for (int q = 0; q < NC; q += 8) {
             float mine = -INFINITY;
             if (active) {
-              load(q);
+              uint32_t x[8];
+              ld_cols<8>(tS + q, x);
 #pragma unroll
-              for (int n = 0; n < CC; ++n) {
-                const float x = warp_max(__uint_as_float(s[n]) * sl2);
-                if (lane == n) mine = x;
+              for (int n = 0; n < 8; ++n) {
+                if (!seen || (node && !((mk[(q + n) * MW] >> (j & 31)) & 1u))) x[n] = hidden;
+                __syncwarp();
+                const float y = warp_max(__uint_as_float(x[n]) * sl2);
+                if (lane == n) mine = y;
               }
             }
-            if (lane < CC) sMax[sw * N + c0 + q + lane] = mine;
+            if (lane < 8) sMax[sw * N + c0 + q + lane] = mine;
           }
           bar_sync128(id);
-          if (r < NC) {
-            const float old = first ? kEmpty : -nm[r];
-            float x = old;
+          // every warp draws the same conclusion from the four warps' maxima
+          constexpr int NL = (NC + 31) / 32;
+          float old[NL], top[NL], hi = kEmpty, lo = INFINITY;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x = fmaxf(x, sMax[q * N + c0 + r]);
-            sAl[c0 + r] = ex2(old - x);
-            nm[r] = -x;
+          for (int x = 0; x < NL; ++x) {
+            const int n = min(x * 32 + lane, NC - 1);
+            old[x] = first ? kEmpty : one ? -base : -ref[n];
+            top[x] = old[x];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top[x] = fmaxf(top[x], sMax[q * N + c0 + n]);
+            hi = fmaxf(hi, top[x]);
+            // columns without a row only count upwards, so that they never
+            // make the reference move step after step
+            if (c0 + n < rows) lo = fminf(lo, top[x]);
           }
-          bar_sync128(id);
+          hi = warp_max(hi);
+          lo = warp_min(lo);
+          one = sl2 > 0.f && (hi - lo <= kSpread || lo == INFINITY);
+          base = -hi;
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < NL; ++x) {
+            const int n = x * 32 + lane;
+            if (n < NC) {
+              const float to = one ? hi : top[x];
+              ref[n] = -to;
+              al[n] = ex2(old[x] - to);
+            }
+          }
+          __syncwarp();
           if (!first) {
             ok = wait<true>(bar(bPV), (t - 1) & 1, W, 0x730);    // O holds every step before
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             if (ok) {
               const uint32_t tO = tl + colO(slot) + c0;
-#pragma unroll
+#pragma unroll 1
               for (int q = 0; q < NC; q += 16) {
                 uint32_t ov[16];
                 ld_cols<16>(tO + q, ov);
 #pragma unroll
-                for (int n = 0; n < 16; n += 2) {
-                  const float2 a = *reinterpret_cast<const float2*>(sAl + c0 + q + n);
-                  ov[n] = __float_as_uint(__uint_as_float(ov[n]) * a.x);
-                  ov[n + 1] = __float_as_uint(__uint_as_float(ov[n + 1]) * a.y);
-                  l2[(q + n) / 2] = f2_fma(l2[(q + n) / 2], f2_pack(__float_as_uint(a.x), __float_as_uint(a.y)), 0ull);
-                }
+                for (int n = 0; n < 16; ++n) ov[n] = __float_as_uint(__uint_as_float(ov[n]) * al[q + n]);
                 tmem_st16(tO + q, ov);
               }
               tmem_st_wait();
+#pragma unroll
+              for (int n = 0; n < NC; n += 2) {
+                const float2 a = *reinterpret_cast<const float2*>(al + n);
+                l2[n / 2] = f2_fma(l2[n / 2], f2_pack(__float_as_uint(a.x), __float_as_uint(a.y)), 0ull);
+              }
             }
           }
-          if (NP == 1 && active) shift(0);               // the raw scores are still there
         }
         if (ok && active) {
+          const uint64_t basex2 = f2_pack(__float_as_uint(base), __float_as_uint(base));
 #pragma unroll
           for (int q = 0; q < NC; q += CC) {
-            if (NP > 1) {
-              load(q);
-              shift(q);
-            }
+            if (CC < NC) load(q);
             uint32_t pk[CC / 2];
 #pragma unroll
             for (int n = 0; n < CC; n += 2) {
-              const float p0 = ex2(__uint_as_float(s[n])), p1 = ex2(__uint_as_float(s[n + 1]));
+              uint64_t b2 = basex2;
+              if (!one) {
+                const float2 b = *reinterpret_cast<const float2*>(ref + q + n);
+                b2 = f2_pack(__float_as_uint(b.x), __float_as_uint(b.y));
+              }
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(s[n], s[n + 1]), sl2x2, b2), x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
               l2[(q + n) / 2] = f2_add(l2[(q + n) / 2], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
               pk[n / 2] = pack_bf16(p0, p1);
             }
@@ -750,38 +789,37 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
           // a V row that no row of the tile sees must not meet a zero
           // probability with a NaN or an infinity; one that some rows see
           // leaves its non-finite elements to the epilogue
-          if (ok && wg == 0 && r < kv16 && (!seen || node)) {
+          if (ok && !plain && wg == 0 && r < kv16 && (!seen || node)) {
             ok = wait<true>(bar(bVF + t % VS), (t / VS) & 1, W, 0x750);
             if (ok) {
               const uint32_t aV = smem_u32(sV + (t % VS) * C::kTile) + r * 128;
               bool nf = false;
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < 8 * NB; c += 4) {
+                const uint32_t a = aV + (c >> 3) * C::kBox + (c & 7) * 16;
                 uint32_t x[4][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t a = aV + (c >> 3) * C::kBox + ((c & 7) + e) * 16;
-                  if (!seen) { st_shared_v4(a, 0, 0, 0, 0); continue; }
+                for (int e = 0; e < 4; ++e)
                   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                : "=r"(x[e][0]), "=r"(x[e][1]), "=r"(x[e][2]), "=r"(x[e][3])
-                               : "r"(a) : "memory");
-                }
-                if (!seen) continue;
+                               : "r"(a + e * 16) : "memory");
+                bool any = !seen;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  bool any = false;
+                for (int e = 0; e < 4; ++e)
 #pragma unroll
                   for (int y = 0; y < 4; ++y) {
-                    if ((x[e][y] & 0x7f80u) == 0x7f80u) { x[e][y] &= 0xffff0000u; any = true; }
-                    if ((x[e][y] & 0x7f800000u) == 0x7f800000u) { x[e][y] &= 0x0000ffffu; any = true; }
+                    uint32_t keep = 0xffffffffu;
+                    if ((x[e][y] & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
+                    if ((x[e][y] & 0x7f800000u) == 0x7f800000u) keep &= 0x0000ffffu;
+                    nf |= keep != 0xffffffffu;
+                    x[e][y] = seen ? x[e][y] & keep : 0u;
                   }
-                  if (any) {
-                    st_shared_v4(aV + (c >> 3) * C::kBox + ((c & 7) + e) * 16, x[e][0], x[e][1], x[e][2], x[e][3]);
-                    nf = true;
-                  }
-                }
+                if (any || nf)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    st_shared_v4(a + e * 16, x[e][0], x[e][1], x[e][2], x[e][3]);
               }
-              if (nf) atomicOr(&sNf[slot * 8 + (j >> 5)], 1u << (j & 31));
+              if (nf && node) atomicOr(&sNf[slot * 8 + (j >> 5)], 1u << (j & 31));
             }
           }
           ok = __all_sync(0xffffffffu, ok);
@@ -820,6 +858,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
       }
 #pragma unroll
       for (int n = 0; n < (NC > 32 ? NC / 32 : 1); ++n) sL[(slot * 4 + sw) * N + c0 + col + n] = l[n];
+      if (sw == 0)
+        for (int n = lane; n < NC; n += 32) sM[slot * N + c0 + n] = ref[n];
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(bar(bST + slot));
       ++lu;
@@ -840,7 +880,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
     bool ok = true;
     while (ok && w.next()) {
       const int slot = lu & 1;
-      const int rows = min(N, w.R.n * p.G - w.rt * N);
+      const int node0 = w.rt * p.npt, rows = min(p.npt, w.R.n - node0) * p.G;
       const bool whole = w.k0 == 0 && w.k1 == w.R.nkt;
       ok = wait<true>(bar(bST + slot), (lu >> 1) & 1, W, 0x800) &&
            wait<true>(bar(bMF + slot), (lu >> 1) & 1, W, 0x801);
@@ -872,16 +912,16 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
             if (!whole) {
               p.ml[(int64_t)piece * N + n] = make_float2(mx[x], sum[x]);
             } else if (p.lse) {
-              const int r = w.rt * N + n, i = over_g(p, r), g = r - i * p.G;
-              p.lse[(int64_t)(w.h * p.G + g) * p.T + w.R.r0 + i] =
+              const int i = over_g(p, n), g = n - i * p.G;
+              p.lse[(int64_t)(w.h * p.G + g) * p.T + w.R.r0 + node0 + i] =
                   sum[x] != 0.f ? (mx[x] + log2f(sum[x])) * kLn2 : -INFINITY;
             }
           }
         }
         if (!whole && w.k0 == 0 && lane == 0) {
           // the unit starts here at f1 - k1 and reaches into later blocks
-          const int64_t end = f1 - w.k1 + w.R.nkt;
-          const int64_t lastb = (end * blocks - 1) / total;
+          const int last = f0 + steps - w.k1 + w.R.nkt - 1, cut = rem * (quo + 1);
+          const int lastb = last < cut ? last / (quo + 1) : rem + (last - cut) / quo;
           p.meta[blockIdx.x] = make_int4(w.b, w.h, w.rt, (int)(lastb - blockIdx.x + 1));
         }
       }
@@ -898,7 +938,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
       uint32_t nf = 0;
       if (w.k1 > w.R.kt)
         for (int x = 0; x < MW; ++x) nf |= sNf[slot * 8 + x];
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < NE; q += CH) {
         uint32_t ov[CH];
         ld_cols<CH>(tl + colO(slot) + e0 + q, ov);
@@ -939,9 +979,9 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap kcmap,
           const float other = __shfl_xor_sync(0xffffffffu, odd ? v2[0] : v2[1], 1);
           const int c = e0 + q + n + (odd ? 1 : 0);
           if (c < rows) {
-            const int r = w.rt * N + c, i = over_g(p, r), g = r - i * p.G;
+            const int i = over_g(p, c), g = c - i * p.G;
             const uint32_t u = odd ? pack_bf16(other, v2[1]) : pack_bf16(v2[0], other);
-            *reinterpret_cast<uint32_t*>(p.o + (int64_t)(w.R.r0 + i) * p.os +
+            *reinterpret_cast<uint32_t*>(p.o + (int64_t)(w.R.r0 + node0 + i) * p.os +
                                          (int64_t)(w.h * p.G + g) * D + (d & ~1)) = u;
           }
         }
@@ -973,7 +1013,7 @@ struct CombineParams {
   float* lse;
   int64_t os;
   const int32_t* cu;
-  int32_t T, G, blocks;
+  int32_t T, G, npt, blocks;
 };
 
 template <int D, int N>
@@ -1000,9 +1040,8 @@ __global__ void __launch_bounds__(128) mis_tree_combine_kernel(const CombinePara
   const int c = blockIdx.x;
   const int4 u = p.meta[c];
   if (u.w < 2) return;
-  const int n = blockIdx.y * 4 + warp, r = u.z * N + n;
-  const int r0 = p.cu[u.x], rows = (p.cu[u.x + 1] - r0) * p.G;
-  if (r >= rows) return;
+  const int n = blockIdx.y * 4 + warp, r0 = p.cu[u.x] + u.z * p.npt;
+  if (n >= min(p.npt, p.cu[u.x + 1] - r0) * p.G) return;
   // piece s: the first lies in block c's second slot, the others in the first
   // slots of the blocks that follow
   auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
@@ -1042,7 +1081,7 @@ __global__ void __launch_bounds__(128) mis_tree_combine_kernel(const CombinePara
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = a != 0.f ? fmaf(a, x[e], acc[e]) : acc[e];
   }
-  const int i = r / p.G, h = u.y * p.G + r - i * p.G;
+  const int i = n / p.G, h = u.y * p.G + n - i * p.G;
   const float inv = l != 0.f ? 1.f / l : 0.f;
   uint32_t w[E / 2];
 #pragma unroll
@@ -1065,7 +1104,7 @@ mis_status_t check_desc(const mis_tree_desc* d, const mis_paged_cache* c) {
     return MIS_ERR_INVALID_ARG;
   if (d->max_nodes > MIS_TREE_MAX_NODES) return MIS_ERR_UNSUPPORTED;
   if (d->Hq % c->Hkv) return MIS_ERR_SHAPE;
-  if (d->Hq / c->Hkv > 4096) return MIS_ERR_UNSUPPORTED;
+  if (d->Hq / c->Hkv > 128) return MIS_ERR_UNSUPPORTED;
   return MIS_OK;
 }
 
@@ -1096,7 +1135,7 @@ mis_status_t launch_tree(const CUtensorMap* m, const TreeParams& p, const Combin
   auto kern = mis_tree_attn_kernel<D, N>;
   if (!kernel_attr_once(reinterpret_cast<const void*>(kern), Cf::kSmem)) return MIS_ERR_CUDA;
   if (launch_pdl(kern, dim3((unsigned)c.blocks), dim3(Cf::kThreads), Cf::kSmem, st, m[0],
-                 m[1], m[2], m[3], m[4], m[5], p) != cudaSuccess)
+                 m[1], m[2], m[3], m[4], m[5], m[6], p) != cudaSuccess)
     return MIS_ERR_CUDA;
   return launch_pdl(mis_tree_combine_kernel<D, N>, dim3((unsigned)c.blocks, N / 4), dim3(128), 0, st,
                     c) == cudaSuccess
@@ -1141,6 +1180,11 @@ extern "C" mis_status_t mis_tree_attention_fwd(
   const TreeWs ws = workspace_of(desc, cache);
   if (!workspace || !aligned(workspace, 256) || ws_bytes < ws.total) return MIS_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // steps are counted in 32 bits
+  const int64_t tiles = ((int64_t)max_pages * cache->page_size + kKeys - 1) / kKeys + 2;
+  const int64_t rows = (int64_t)desc->max_nodes * (desc->Hq / cache->Hkv);
+  if ((double)tiles * desc->B * cache->Hkv * (rows > 128 ? 2.0 * ((rows + 127) / 128) : 1.0) >= 2147483648.0)
+    return MIS_ERR_UNSUPPORTED;
   if (desc->T == 0)
     return cudaMemsetAsync(workspace, 0, 8, st) == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
   try {
@@ -1162,25 +1206,30 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     const uint64_t nk[2] = {(uint64_t)D * 2, (uint64_t)k_row_stride * 2};
     const uint64_t nv[2] = {(uint64_t)D * 2, (uint64_t)v_row_stride * 2};
     const uint32_t nb[3] = {64, 1, 8};
-    const CUtensorMap maps[6] = {
+    // Q by the rows of a tile's nodes
+    const uint64_t qd[3] = {(uint64_t)D, (uint64_t)desc->Hq, (uint64_t)desc->T};
+    const uint64_t qst[2] = {(uint64_t)D * 2, (uint64_t)q_row_stride * 2};
+    const int N = tile_rows(desc, cache), G = desc->Hq / cache->Hkv, npt = N / G;
+    const uint32_t qb[3] = {64, (uint32_t)G, (uint32_t)npt};
+    const CUtensorMap maps[7] = {
+        make_tmap_bf16(q, 3, qd, qst, qb, &ok),
         make_tmap_bf16(cache->k, 4, cd, cs, cb, &ok), make_tmap_bf16(cache->v, 4, cd, cs, cb, &ok),
         make_tmap_bf16(cache->k, 4, cd, cs, c8, &ok), make_tmap_bf16(cache->v, 4, cd, cs, c8, &ok),
         make_tmap_bf16(k, 3, nd, nk, nb, &ok), make_tmap_bf16(v, 3, nd, nv, nb, &ok)};
     if (!ok) return MIS_ERR_CUDA;
     uint8_t* base = static_cast<uint8_t*>(workspace);
     TreeParams p;
-    p.q = static_cast<const __nv_bfloat16*>(q);
     p.v = static_cast<const __nv_bfloat16*>(v);
     p.o = static_cast<__nv_bfloat16*>(o);
     p.lse = lse;
-    p.qs = q_row_stride; p.vs = v_row_stride; p.os = o_row_stride;
+    p.vs = v_row_stride; p.os = o_row_stride;
     p.n_pages = cache->n_pages;
     p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
     p.max_pages = max_pages;
     p.table = block_table; p.table_stride = block_table_stride;
     p.cache_len = cache_len; p.cu = cu_nodes; p.parents = parents;
-    p.B = desc->B; p.T = desc->T; p.Hq = desc->Hq; p.Hkv = cache->Hkv;
-    p.G = desc->Hq / cache->Hkv;
+    p.B = desc->B; p.T = desc->T; p.Hkv = cache->Hkv;
+    p.G = G; p.npt = npt;
     p.g_magic = (uint32_t)((0xffffffffull + (uint64_t)p.G) / (uint64_t)p.G);
     p.max_nodes = desc->max_nodes;
     p.scale_log2 = (desc->scale != 0.f ? desc->scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
@@ -1194,8 +1243,7 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     c.cta_status = p.cta_status; c.meta = p.meta; c.ml = p.ml; c.part = p.part;
     c.status = reinterpret_cast<uint32_t*>(base);
     c.o = p.o; c.lse = lse; c.os = o_row_stride; c.cu = cu_nodes;
-    c.T = desc->T; c.G = p.G; c.blocks = num_sms();
-    const int N = tile_rows(desc, cache);
+    c.T = desc->T; c.G = G; c.npt = npt; c.blocks = num_sms();
     if (D == 128) {
       if (N == 16) return launch_tree<128, 16>(maps, p, c, st);
       if (N == 32) return launch_tree<128, 32>(maps, p, c, st);

@@ -419,7 +419,7 @@ def random_parents(rng, nodes, unused=0.0, reach=4):
 
 
 HEADS = [(16, 8, 128), (32, 8, 128), (4, 2, 64), (12, 4, 64), (6, 6, 128), (8, 1, 128), (20, 4, 128),
-         (7, 1, 64), (3, 3, 64), (40, 1, 128)]
+         (7, 1, 64), (3, 3, 64), (40, 1, 128), (128, 1, 64), (100, 1, 128)]
 
 
 @pytest.mark.parametrize("hq,hkv,D", HEADS)
@@ -476,6 +476,20 @@ def test_many_short_requests():
 @pytest.mark.parametrize("scale", [0.02, 1.0, -0.3])
 def test_scales_and_large_scores(scale):
     Tree([300, 20], [9, 4], 4, 2, 64, 32, None, seed=6, scale=scale, q_scale=4.0).check()
+
+
+@pytest.mark.parametrize("hq,hkv,D,n", [(4, 2, 64, 9), (8, 2, 128, 13), (16, 2, 128, 40), (8, 1, 64, 7)])
+def test_heads_and_nodes_of_very_different_size(hq, hkv, D, n):
+    # rows whose scores differ by hundreds share a tile, and scores that grow along
+    # the cache move the reference again and again
+    t = Tree([700, 90], [n, 3], hq, hkv, D, 16, None, seed=19, max_nodes=n)
+    size = torch.linspace(-4, 7, t.q.shape[0] * hq, device="cuda").exp2().view(t.q.shape[0], hq, 1)
+    t.q.copy_((t.q.float() * size).to(BF16))
+    grow = torch.linspace(0.2, 3, 700, device="cuda")
+    for j in range(700):
+        page, off = int(t.table[0, j // 16]), j % 16
+        t.kc[page, off] = (t.kc[page, off].float() * grow[j]).to(BF16)
+    t.check()
 
 
 def test_no_lse_and_more_rows_than_requests_have():
