@@ -522,7 +522,8 @@ mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const void* k, con
  *   B, T      — requests, rows of q, k, v, o (>= 0); Hq a multiple of Hkv, at
  *               most 128 query heads a kv head
  *   max_nodes — upper bound on a request's nodes, 1 .. MIS_TREE_MAX_NODES
- *   scale     — softmax scale, finite; 0 selects 1/sqrt(D)
+ *   scale     — softmax scale of size 1e-20 to 1e20, of either sign; 0 selects
+ *               1/sqrt(D)
  *   q, k, v, o, lse, row strides — as in mis_attention_fwd_plan (lse fp32
  *               [Hq, T] or NULL). Rows from cu_nodes[B] on are not written
  *   block_table — device int32 [B, max_pages], row stride in elements

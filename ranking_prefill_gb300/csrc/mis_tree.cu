@@ -439,86 +439,103 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       for (int i = max(0, v_issued - VS); i < v_issued; ++i) wait_drain(bar(bVF + i % VS), (i / VS) & 1);
     } else if (warp == 1) {
       // --------------------------------------------------------------- MMA
-      if (lane == 0) {
-        constexpr uint32_t idS = idesc_bf16(128, N, false);
-        constexpr uint32_t idO = idesc_bf16(128, N, true) | (1u << 15);   // A MN-major too
-        bool ok = true;
-        if (p.stall) ok = wait<true>(bar(bDR), 0, W, 0x7ff);   // nothing arrives before the drain
-        struct Step { int lu, kv; bool first, last; };
-        int k = 0, lu = -1;
-        auto fetch = [&](Step& s) -> bool {                    // the block's next step
-          if (lu < 0 || k >= w.k1) {
-            if (!w.next()) return false;
-            ++lu;
-            k = w.k0;
-          }
-          s.lu = lu;
-          s.kv = w.keys(k);
-          s.first = k == w.k0;
-          s.last = k + 1 == w.k1;
-          ++k;
-          return true;
-        };
-        auto s_ready = [&](const Step& s, int t) -> bool {
-          return mbar_test_wait(bar(bKF + t % KS), (t / KS) & 1) &&
-                 (!s.first || mbar_test_wait(bar(bQF + s.lu % QS), (s.lu / QS) & 1));
-        };
-        auto issue_s = [&](const Step& s, int t) -> bool {
-          if (s.first && !wait<true>(bar(bQF + s.lu % QS), (s.lu / QS) & 1, W, 0x200)) return false;
-          if (!wait<true>(bar(bKF + t % KS), (t / KS) & 1, W, 0x300)) return false;
-          tc_fence_after();
-          const uint32_t aK = smem_u32(sK + (t % KS) * C::kTile);
-          const uint32_t aQ = smem_u32(sQ + (s.lu % QS) * C::kQ);
+      // the warp walks together and one elected lane issues: loop state and
+      // descriptors then stay in uniform registers
+      constexpr uint32_t idS = idesc_bf16(128, N, false);
+      constexpr uint32_t idO = idesc_bf16(128, N, true) | (1u << 15);   // A MN-major too
+      bool ok = true;
+      auto wait_all = [&](int b, uint32_t parity, uint32_t where) -> bool {
+        const bool r = wait<true>(bar(b), parity, W, where);
+        return __all_sync(0xffffffffu, r);
+      };
+      if (p.stall) ok = wait_all(bDR, 0, 0x7ff);               // nothing arrives before the drain
+      struct Step { int lu, kv; bool first, last; };
+      int k = 0, lu = -1;
+      auto fetch = [&](Step& s) -> bool {                      // the block's next step
+        if (lu < 0 || k >= w.k1) {
+          if (!w.next()) return false;
+          ++lu;
+          k = w.k0;
+        }
+        s.lu = lu;
+        s.kv = w.keys(k);
+        s.first = k == w.k0;
+        s.last = k + 1 == w.k1;
+        ++k;
+        return true;
+      };
+      auto s_ready = [&](const Step& s, int t) -> bool {
+        const bool r = mbar_test_wait(bar(bKF + t % KS), (t / KS) & 1) &&
+                       (!s.first || mbar_test_wait(bar(bQF + s.lu % QS), (s.lu / QS) & 1));
+        return __all_sync(0xffffffffu, r);
+      };
+      const uint32_t dQ = smem_u32(sQ), dK = smem_u32(sK), dV = smem_u32(sV), dP = smem_u32(sP);
+      auto issue_s = [&](const Step& s, int t) -> bool {
+        if (s.first && !wait_all(bQF + s.lu % QS, (s.lu / QS) & 1, 0x200)) return false;
+        if (!wait_all(bKF + t % KS, (t / KS) & 1, 0x300)) return false;
+        tc_fence_after();
+        const uint32_t d = __shfl_sync(0xffffffffu, tmem + colS(t & 1), 0);
+        const uint64_t a = sdesc_sw128(__shfl_sync(0xffffffffu, dK + (t % KS) * C::kTile, 0), 16, 1024);
+        const uint64_t b = sdesc_sw128(__shfl_sync(0xffffffffu, dQ + (s.lu % QS) * C::kQ, 0), 16, 1024);
+        if (elect_uniform()) {
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
+          for (int x = 0; x < NB; ++x)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_ss(tmem + colS(t & 1), sdesc_sw128(aK + b * C::kBox + ks * 32, 16, 1024),
-                     sdesc_sw128(aQ + b * C::kQBox + ks * 32, 16, 1024), idS, (b | ks) != 0);
+              mma_ss(d, a + ((x * C::kBox + ks * 32) >> 4), b + ((x * C::kQBox + ks * 32) >> 4), idS,
+                     (x | ks) != 0);
           mma_commit(bar(bSF + (t & 1)));
           mma_commit(bar(bKE + t % KS));
           if (s.last) mma_commit(bar(bQE + s.lu % QS));
-          return true;
-        };
-        Step cur, nxt;
-        int t = 0;
-        bool have = ok && fetch(cur);
-        if (have) ok = issue_s(cur, 0);
-        while (ok && have) {
-          const bool more = fetch(nxt);
-          // the next S runs during this step's softmax, if its operands are there
-          bool early = false;
-          if (more && s_ready(nxt, t + 1)) {
-            if (!(ok = issue_s(nxt, t + 1))) break;
-            early = true;
-          }
-          if (!(ok = wait<true>(bar(bPF), t & 1, W, 0x400))) break;
-          if (!(ok = wait<true>(bar(bVF + t % VS), (t / VS) & 1, W, 0x480))) break;
-          if (cur.first && cur.lu >= 2 &&
-              !(ok = wait<true>(bar(bOE + (cur.lu & 1)), ((cur.lu >> 1) - 1) & 1, W, 0x500)))
-            break;
-          tc_fence_after();
-          const uint32_t aV = smem_u32(sV + (t % VS) * C::kTile), aP = smem_u32(sP);
-          const int nks = (cur.kv + 15) >> 4;
-          for (int ks = 0; ks < nks; ++ks)
-            // V [key][d] and P [key][row], both MN-major: 8-key groups 1024 B
-            // apart, 64-column boxes kBox apart. D = 64 repeats its one box
-            // (stride 0): rows 64..127 of O^T equal rows 0..63.
-            mma_ss(tmem + colO(cur.lu & 1),
-                   sdesc_sw128(aV + ks * 2048, D == 128 ? C::kBox : 0, 1024),
-                   sdesc_sw128(aP + ks * 2048, C::kBox, 1024), idO, (!cur.first || ks != 0) ? 1u : 0u);
+        }
+        __syncwarp();
+        return true;
+      };
+      Step cur, nxt;
+      int t = 0;
+      bool have = ok && fetch(cur);
+      if (have) ok = issue_s(cur, 0);
+      while (ok && have) {
+        const bool more = fetch(nxt);
+        // the next S runs during this step's softmax, if its operands are there
+        bool early = false;
+        if (more && s_ready(nxt, t + 1)) {
+          if (!(ok = issue_s(nxt, t + 1))) break;
+          early = true;
+        }
+        if (!(ok = wait_all(bPF, t & 1, 0x400))) break;
+        if (!(ok = wait_all(bVF + t % VS, (t / VS) & 1, 0x480))) break;
+        if (cur.first && cur.lu >= 2 &&
+            !(ok = wait_all(bOE + (cur.lu & 1), ((cur.lu >> 1) - 1) & 1, 0x500)))
+          break;
+        tc_fence_after();
+        // V [key][d] and P [key][row], both MN-major: 8-key groups 1024 B
+        // apart, 64-column boxes kBox apart. D = 64 repeats its one box
+        // (stride 0): rows 64..127 of O^T equal rows 0..63.
+        const uint32_t d = __shfl_sync(0xffffffffu, tmem + colO(cur.lu & 1), 0);
+        const uint64_t a = sdesc_sw128(__shfl_sync(0xffffffffu, dV + (t % VS) * C::kTile, 0),
+                                       D == 128 ? C::kBox : 0, 1024);
+        const uint64_t b = sdesc_sw128(dP, C::kBox, 1024);
+        const int nks = __shfl_sync(0xffffffffu, (cur.kv + 15) >> 4, 0);
+        const uint32_t acc = __shfl_sync(0xffffffffu, cur.first ? 0u : 1u, 0);
+        if (elect_uniform()) {
+#pragma unroll
+          for (int ks = 0; ks < kKeys / 16; ++ks)
+            if (ks < nks) mma_ss(d, a + ks * 128, b + ks * 128, idO, ks == 0 ? acc : 1u);
           mma_commit(bar(bVE + t % VS));
           mma_commit(bar(bPV));
           if (cur.last) mma_commit(bar(bOF + (cur.lu & 1)));
-          if (more && !early && !(ok = issue_s(nxt, t + 1))) break;
-          cur = nxt;
-          have = more;
-          ++t;
         }
-        // drain: all tensor-core work of this thread completes before dealloc
-        mma_commit(bar(bDR));
-        wait_drain(bar(bDR), 0);
+        __syncwarp();
+        if (more && !early && !(ok = issue_s(nxt, t + 1))) break;
+        cur = nxt;
+        have = more;
+        ++t;
       }
+      // drain: all tensor-core work of the elected lane completes before dealloc
+      if (elect_uniform()) mma_commit(bar(bDR));
+      __syncwarp();
+      wait_drain(bar(bDR), 0);
     } else {
       // ------------------------------------------ Q's copies and the tree's masks
       const int th = threadIdx.x - 64;
@@ -595,9 +612,10 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     const int wg = (warp - 4) >> 2, sw = warp & 3, r = sw * 32 + lane;
     const int c0 = wg * NC, id = 1 + wg;
     const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
-    const float sl2 = p.scale_log2;
-    const uint32_t hidden = sl2 < 0.f ? 0x7f800000u : 0xff800000u;     // scales to -inf
-    const uint64_t sl2x2 = f2_pack(__float_as_uint(sl2), __float_as_uint(sl2));
+    // scores are taken times the scale's sign, then scaled by its size: the
+    // largest score is the largest product
+    const float sa = fabsf(p.scale_log2), sign = p.scale_log2 < 0.f ? -1.f : 1.f, inv_sa = 1.f / sa;
+    const uint64_t sax2 = f2_pack(__float_as_uint(sa), __float_as_uint(sa));
     // columns in registers at a time: two pieces (N = 128) are read from
     // tensor memory twice, once for the maximum and once for P
     constexpr int CC = NC > 32 ? 32 : NC;
@@ -615,6 +633,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
       for (int n = 0; n < NC / 2; ++n) l2[n] = 0ull;
       bool one = true;                                   // one reference, -base, for all columns
+                                                         // (else their scores are shifted, base 0)
       float base = 0.f;
       if (ok && lu >= 2) {
         ok = wait<true>(bar(bSE + slot), ((lu >> 1) - 1) & 1, W, 0x700);
@@ -643,41 +662,51 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         const uint32_t tS = tl + colS(t & 1) + c0;
         const uint32_t* mk = sMask + (slot * N + c0) * MW + (node ? j >> 5 : 0);
         const bool plain = __all_sync(0xffffffffu, seen && !node);
-        // columns q .. q + CC - 1 of the scores; what a row does not see is -inf
-        uint32_t s[CC];
-        auto load = [&](int q) {
-          ld_cols<CC>(tS + q, s);
-          if (!plain) {
+        // Steps that are not plain (new rows, a partial tile, a negative scale,
+        // references by column) have their scores rewritten in tensor memory
+        // first, in a rolled loop: hidden ones -inf, the others times the
+        // scale's sign and less the column's reference. What follows is then
+        // the same short code for all steps; instruction fetches, not
+        // arithmetic, were what this kernel waited for when it was unrolled
+        // for each (256 rows a kv head: 335 -> see the table).
+        bool over = !ok || first;
+        if (ok && active && !(plain && one && sign > 0.f)) {
+#pragma unroll 1
+          for (int q = 0; q < NC; q += 8) {
+            uint32_t x[8];
+            ld_cols<8>(tS + q, x);
 #pragma unroll
-            for (int n = 0; n < CC; ++n)
-              if (!seen || (node && !((mk[(q + n) * MW] >> (j & 31)) & 1u))) s[n] = hidden;
-            __syncwarp();
+            for (int n = 0; n < 8; ++n) {
+              const bool hide = !seen || (node && !((mk[(q + n) * MW] >> (j & 31)) & 1u));
+              const float b = one ? 0.f : ref[q + n];
+              float y = __uint_as_float(x[n]) * sign;
+              // a column that saw nothing so far has no reference to be taken off
+              if (b >= -kEmpty) over |= !hide && y > -INFINITY;
+              else y = fmaf(b, inv_sa, y);
+              x[n] = __float_as_uint(hide ? -INFINITY : y);
+            }
+            tmem_st8(tS + q, x);
           }
-        };
-        if (CC == NC && ok && active) load(0);
+          tmem_st_wait();
+        }
+        __syncwarp();
+        // columns q .. q + CC - 1 of the scores
+        uint32_t s[CC];
+        if (CC == NC && ok && active) ld_cols<CC>(tS, s);
         bool move = first;
         if (!first) {
-          bool over = !ok;
           if (ok && active) {
             float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
             for (int q = 0; q < NC; q += CC) {
-              if (CC < NC) load(q);
-              if (one) {
+              if (CC < NC) ld_cols<CC>(tS + q, s);
 #pragma unroll
-                for (int n = 0; n < CC; n += 4) {
-                  x0 = max3(x0, __uint_as_float(s[n]), __uint_as_float(s[n + 1]));
-                  x1 = max3(x1, __uint_as_float(s[n + 2]), __uint_as_float(s[n + 3]));
-                }
-              } else {
-#pragma unroll
-                for (int n = 0; n < CC; n += 2) {
-                  const float2 b = *reinterpret_cast<const float2*>(ref + q + n);
-                  x0 = max3(x0, fmaf(__uint_as_float(s[n]), sl2, b.x), fmaf(__uint_as_float(s[n + 1]), sl2, b.y));
-                }
+              for (int n = 0; n < CC; n += 4) {
+                x0 = max3(x0, __uint_as_float(s[n]), __uint_as_float(s[n + 1]));
+                x1 = max3(x1, __uint_as_float(s[n + 2]), __uint_as_float(s[n + 3]));
               }
             }
-            over = (one ? fmaf(fmaxf(x0, x1), sl2, base) : x0) > kGrow;
+            over |= fmaf(fmaxf(x0, x1), sa, base) > kGrow;
           }
           move = bar_any128(id, over);
         }
@@ -685,8 +714,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           // a unit begins or a score passed its reference (or a wait gave up:
           // then every warp of the warpgroup leaves here)
           if (bar_any128(id, !ok)) { gone = true; break; }
-          // the step's maximum of every column over this warp's keys; rolled,
-          // since straight code that runs once is paid in instruction fetches
+          // the step's maximum of every column over this warp's keys
 #pragma unroll 1
           for (int q = 0; q < NC; q += 8) {
             float mine = -INFINITY;
@@ -695,11 +723,10 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
               ld_cols<8>(tS + q, x);
 #pragma unroll
               for (int n = 0; n < 8; ++n) {
-                if (!seen || (node && !((mk[(q + n) * MW] >> (j & 31)) & 1u))) x[n] = hidden;
-                __syncwarp();
-                const float y = warp_max(__uint_as_float(x[n]) * sl2);
+                const float y = warp_max(__uint_as_float(x[n])) * sa;
                 if (lane == n) mine = y;
               }
+              if (!one && lane < 8 && ref[q + lane] < -kEmpty) mine -= ref[q + lane];
             }
             if (lane < 8) sMax[sw * N + c0 + q + lane] = mine;
           }
@@ -721,9 +748,32 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           }
           hi = warp_max(hi);
           lo = warp_min(lo);
-          one = sl2 > 0.f && (hi - lo <= kSpread || lo == INFINITY);
-          base = -hi;
+          const bool was = one;
+          one = hi - lo <= kSpread || lo == INFINITY;
+          base = one ? -hi : 0.f;
           __syncwarp();
+          if (!(was && one)) {
+            // the scores in tensor memory go from the old references to the new
+#pragma unroll
+            for (int x = 0; x < NL; ++x) {
+              const float from = was || old[x] <= kEmpty ? 0.f : old[x];
+              const float to = one || top[x] <= kEmpty ? 0.f : top[x];
+              if (x * 32 + lane < NC) al[x * 32 + lane] = (from - to) * inv_sa;
+            }
+            __syncwarp();
+            if (active) {
+#pragma unroll 1
+              for (int q = 0; q < NC; q += 8) {
+                uint32_t x[8];
+                ld_cols<8>(tS + q, x);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) x[n] = __float_as_uint(__uint_as_float(x[n]) + al[q + n]);
+                tmem_st8(tS + q, x);
+              }
+              tmem_st_wait();
+            }
+            __syncwarp();
+          }
 #pragma unroll
           for (int x = 0; x < NL; ++x) {
             const int n = x * 32 + lane;
@@ -757,21 +807,17 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
             }
           }
         }
+        if (move && ok && active && CC == NC) ld_cols<CC>(tS, s);
         if (ok && active) {
           const uint64_t basex2 = f2_pack(__float_as_uint(base), __float_as_uint(base));
 #pragma unroll
           for (int q = 0; q < NC; q += CC) {
-            if (CC < NC) load(q);
+            if (CC < NC) ld_cols<CC>(tS + q, s);
             uint32_t pk[CC / 2];
 #pragma unroll
             for (int n = 0; n < CC; n += 2) {
-              uint64_t b2 = basex2;
-              if (!one) {
-                const float2 b = *reinterpret_cast<const float2*>(ref + q + n);
-                b2 = f2_pack(__float_as_uint(b.x), __float_as_uint(b.y));
-              }
               float x0, x1;
-              f2_unpack(f2_fma(f2_pack(s[n], s[n + 1]), sl2x2, b2), x0, x1);
+              f2_unpack(f2_fma(f2_pack(s[n], s[n + 1]), sax2, basex2), x0, x1);
               const float p0 = ex2(x0), p1 = ex2(x1);
               l2[(q + n) / 2] = f2_add(l2[(q + n) / 2], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
               pk[n / 2] = pack_bf16(p0, p1);
@@ -1100,8 +1146,9 @@ mis_status_t check_desc(const mis_tree_desc* d, const mis_paged_cache* c) {
   if (!d) return MIS_ERR_INVALID_ARG;
   const mis_status_t cs = check_paged_cache(c);
   if (cs != MIS_OK) return cs;
-  if (d->B < 1 || d->T < 0 || d->Hq < 1 || d->max_nodes < 1 || !std::isfinite(d->scale))
-    return MIS_ERR_INVALID_ARG;
+  if (d->B < 1 || d->T < 0 || d->Hq < 1 || d->max_nodes < 1) return MIS_ERR_INVALID_ARG;
+  const float size = std::fabs(d->scale);
+  if (!(size <= 1e20f) || (size != 0.f && size < 1e-20f)) return MIS_ERR_INVALID_ARG;
   if (d->max_nodes > MIS_TREE_MAX_NODES) return MIS_ERR_UNSUPPORTED;
   if (d->Hq % c->Hkv) return MIS_ERR_SHAPE;
   if (d->Hq / c->Hkv > 128) return MIS_ERR_UNSUPPORTED;

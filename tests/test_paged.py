@@ -160,7 +160,8 @@ TREE = dict(q=A, k=A, v=A, o=A, lse=A, qs=256, ks=128, vs=128, os=256, table=A, 
     (dict(max_nodes=0), {}, "MIS_ERR_INVALID_ARG"), (dict(max_nodes=257), {}, "MIS_ERR_UNSUPPORTED"),
     (dict(Hq=2 * 129), dict(qs=2 * 129 * 64, os=2 * 129 * 64), "MIS_ERR_UNSUPPORTED"),
     (dict(B=1 << 20), dict(max_pages=1 << 20, stride=1 << 20), "MIS_ERR_UNSUPPORTED"),   # steps pass 32 bits
-    (dict(scale=float("inf")), {}, "MIS_ERR_INVALID_ARG"),
+    (dict(scale=float("inf")), {}, "MIS_ERR_INVALID_ARG"), (dict(scale=float("nan")), {}, "MIS_ERR_INVALID_ARG"),
+    (dict(scale=1e-30), {}, "MIS_ERR_INVALID_ARG"),
     ({}, dict(q=None), "MIS_ERR_INVALID_ARG"), ({}, dict(o=A + 8), "MIS_ERR_INVALID_ARG"),
     ({}, dict(lse=A + 2), "MIS_ERR_INVALID_ARG"), ({}, dict(qs=248), "MIS_ERR_SHAPE"),
     ({}, dict(ks=132), "MIS_ERR_SHAPE"), ({}, dict(table=None), "MIS_ERR_INVALID_ARG"),
