@@ -401,36 +401,29 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
               prow = w.R.r0 + (k - w.R.kt) * kKeys + key - w.R.a;
             }
           }
-          const CUtensorMap* km = !cached ? &kmap : fresh ? &kc8map : &kcmap;
-          const CUtensorMap* vm = !cached ? &vmap : fresh ? &vc8map : &vcmap;
           const uint32_t each = 128u << shift, dst = (uint32_t)(x * C::kBox + key * 128);
           const uint32_t bytes = each * __popc(__ballot_sync(0xffffffffu, mine_ok));
-          if (t >= KS) {
-            ok = wait<true>(bar(bKE + sk), ((t / KS) - 1) & 1, W, 0x100);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+          // K, then V: one rolled body (see the note on instruction fetches)
+#pragma unroll 1
+          for (int y = 0; y < 2; ++y) {
+            const int depth = y ? VS : KS, sl = y ? sv : sk, full = (y ? bVF : bKF) + sl;
+            if (t >= depth) {
+              ok = wait<true>(bar((y ? bVE : bKE) + sl), ((t / depth) - 1) & 1, W, 0x100 + 0x80 * y);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
+            __syncwarp();
+            if (mine_ok) {
+              const uint32_t d = smem_u32((y ? sV : sK) + sl * C::kTile) + dst;
+              if (cached)
+                tma_load_4d(d, fresh ? (y ? &vc8map : &kc8map) : (y ? &vcmap : &kcmap), bar(full),
+                            x * 64, w.h, prow, page);
+              else
+                tma_load_3d(d, y ? &vmap : &kmap, bar(full), x * 64, w.h, prow);
+            }
+            if (y) v_issued = t + 1; else k_issued = t + 1;
           }
-          if (lane == 0) mbar_arrive_expect_tx(bar(bKF + sk), bytes);
-          __syncwarp();
-          if (mine_ok) {
-            const uint32_t d = smem_u32(sK + sk * C::kTile) + dst;
-            if (cached) tma_load_4d(d, km, bar(bKF + sk), x * 64, w.h, prow, page);
-            else tma_load_3d(d, km, bar(bKF + sk), x * 64, w.h, prow);
-          }
-          k_issued = t + 1;
-          if (t >= VS) {
-            ok = wait<true>(bar(bVE + sv), ((t / VS) - 1) & 1, W, 0x180);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(bar(bVF + sv), bytes);
-          __syncwarp();
-          if (mine_ok) {
-            const uint32_t d = smem_u32(sV + sv * C::kTile) + dst;
-            if (cached) tma_load_4d(d, vm, bar(bVF + sv), x * 64, w.h, prow, page);
-            else tma_load_3d(d, vm, bar(bVF + sv), x * 64, w.h, prow);
-          }
-          v_issued = t + 1;
         }
       }
       __syncwarp();
@@ -497,13 +490,21 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       if (have) ok = issue_s(cur, 0);
       while (ok && have) {
         const bool more = fetch(nxt);
-        // the next S runs during this step's softmax, if its operands are there
-        bool early = false;
-        if (more && s_ready(nxt, t + 1)) {
-          if (!(ok = issue_s(nxt, t + 1))) break;
-          early = true;
+        // the next S runs during this step's softmax: look for its operands
+        // and for P in turn (a look that came too early once would leave S
+        // behind this step's PV: attn of 256 rows a kv head 172 -> TTT us)
+        bool early = !more;
+        const uint64_t t0 = globaltimer();
+        for (uint32_t it = 1; !early; ++it) {
+          if (s_ready(nxt, t + 1)) {
+            if (!(ok = issue_s(nxt, t + 1))) break;
+            early = true;
+          } else if (__all_sync(0xffffffffu, mbar_test_wait(bar(bPF), t & 1)) ||
+                     ((it & 31) == 0 && __any_sync(0xffffffffu, *abort_flag || globaltimer() - t0 > p.wait_ns))) {
+            break;
+          }
         }
-        if (!(ok = wait_all(bPF, t & 1, 0x400))) break;
+        if (!ok || !(ok = wait_all(bPF, t & 1, 0x400))) break;
         if (!(ok = wait_all(bVF + t % VS, (t / VS) & 1, 0x480))) break;
         if (cur.first && cur.lu >= 2 &&
             !(ok = wait_all(bOE + (cur.lu & 1), ((cur.lu >> 1) - 1) & 1, 0x500)))
@@ -527,7 +528,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           if (cur.last) mma_commit(bar(bOF + (cur.lu & 1)));
         }
         __syncwarp();
-        if (more && !early && !(ok = issue_s(nxt, t + 1))) break;
+        if (!early && !(ok = issue_s(nxt, t + 1))) break;
         cur = nxt;
         have = more;
         ++t;
