@@ -22,8 +22,8 @@
 // leave (max, sum, unnormalised O) in the workspace and a second kernel adds
 // them in block order, so the same call gives the same bits.
 //
-// Warp roles: 0 TMA producer of K and V (pages of the cache, 8-row groups of
-// the new rows), 1 MMA issue, 2-3 Q's copies and the tree's masks, then one or
+// Warp roles: 0 and 3 TMA producers of K and of V (pages of the cache, 8-row
+// groups of the new rows), 1 MMA issue, 2 Q's copies and the tree's masks, then one or
 // two softmax warpgroups (a thread is a key, it owns N or N / 2 columns) and
 // an epilogue warpgroup (a thread is an element of the head).
 //
@@ -84,8 +84,8 @@ struct TreeCfg {
   static constexpr int oRef = oMax + 4 * N;             // [4][N] a warp's copy of the negated references
   static constexpr int oAl = oRef + 4 * N;              // [4][N] ... of the factors of a move
   static constexpr int oInv = oAl + 4 * N;              // [4][N] an epilogue warp's 1 / sum
-  static constexpr int oPar = oInv + 4 * N;             // [2][256] int16: a loader warp's parents
-  static constexpr int kWords = oPar + MIS_TREE_MAX_NODES;
+  static constexpr int oPar = oInv + 4 * N;             // [256] int16: parents
+  static constexpr int kWords = oPar + MIS_TREE_MAX_NODES / 2;
   static constexpr int kData = kQS * kQ + kP + (kK + kV) * kTile;
   static constexpr int kSmem = kData + 4 * kWords + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
@@ -283,7 +283,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       mbar_init(bar(bOE + s), 4);
       mbar_init(bar(bST + s), 4 * WG);
       mbar_init(bar(bSE + s), 4);
-      mbar_init(bar(bMF + s), 2);
+      mbar_init(bar(bMF + s), 1);
     }
     for (int s = 0; s < KS; ++s) { mbar_init(bar(bKF + s), 1); mbar_init(bar(bKE + s), 1); }
     for (int s = 0; s < VS; ++s) { mbar_init(bar(bVF + s), 1); mbar_init(bar(bVE + s), 1); }
@@ -370,66 +370,76 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   if (warp < 4) {
     if constexpr (N >= 64) regs_dec<kRegCtl>();
     Walk<N> w(p, s_start, steps);
-    if (warp == 0) {
-      // ---------------------------------------------------------- producer
+    if (warp == 0 || warp == 3) {
+      // ---------------------------------- producers: warp 0 of K, warp 3 of V.
+      // Each follows its own ring, so a K tile never waits behind a V tile
+      const int y = warp == 3;
+      const int depth = y ? VS : KS, full0 = y ? bVF : bKF, empty0 = y ? bVE : bKE;
+      const uint32_t ring = smem_u32(y ? sV : sK);
+      const CUtensorMap* const cmap = y ? &vcmap : &kcmap;
+      const CUtensorMap* const c8map = y ? &vc8map : &kc8map;
+      const CUtensorMap* const nmap = y ? &vmap : &kmap;
       const int box_shift = min(p.page_shift, 7);
-      int t = 0, k_issued = 0, v_issued = 0;
-      bool ok = true;
-      while (ok && w.next()) {
-        const int32_t* row = p.table + (int64_t)w.b * p.table_stride;
-        for (int k = w.k0; ok && k < w.k1; ++k, ++t) {
-          const int kv = w.keys(k), sk = t % KS, sv = t % VS;
-          // copies of this step: box x of key-row group g by lane g * NB + x.
-          // Groups are whole boxes of a page, or 8 rows where new rows follow
-          const int g = lane / NB, x = lane % NB;
-          const bool fresh = k >= w.R.kt;
-          const int shift = fresh ? 3 : box_shift;
-          const int key = g << shift;
-          const bool cached = !fresh || key < w.R.a;
-          bool mine_ok = key < kv;
-          int page = 0, prow = 0;
-          if (mine_ok) {
-            if (cached) {
-              const int at = k * kKeys + key;
-              page = row[at >> p.page_shift];
-              prow = at & ((1 << p.page_shift) - 1);
-              if (page < 0 || page >= p.n_pages) {
-                mine_ok = false;
-                raise_status(status, kDevIndex, 0x41);
-              }
-            } else {
-              prow = w.R.r0 + (k - w.R.kt) * kKeys + key - w.R.a;
-            }
-          }
-          const uint32_t each = 128u << shift, dst = (uint32_t)(x * C::kBox + key * 128);
-          const uint32_t bytes = each * __popc(__ballot_sync(0xffffffffu, mine_ok));
-          // K, then V: one rolled body (see the note on instruction fetches)
-#pragma unroll 1
-          for (int y = 0; y < 2; ++y) {
-            const int depth = y ? VS : KS, sl = y ? sv : sk, full = (y ? bVF : bKF) + sl;
-            if (t >= depth) {
-              ok = wait<true>(bar((y ? bVE : bKE) + sl), ((t / depth) - 1) & 1, W, 0x100 + 0x80 * y);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
-            __syncwarp();
-            if (mine_ok) {
-              const uint32_t d = smem_u32((y ? sV : sK) + sl * C::kTile) + dst;
-              if (cached)
-                tma_load_4d(d, fresh ? (y ? &vc8map : &kc8map) : (y ? &vcmap : &kcmap), bar(full),
-                            x * 64, w.h, prow, page);
-              else
-                tma_load_3d(d, y ? &vmap : &kmap, bar(full), x * 64, w.h, prow);
-            }
-            if (y) v_issued = t + 1; else k_issued = t + 1;
-          }
+      // a lane's copy of a step: box x of key-row group g by lane g * NB + x.
+      // Groups are whole boxes of a page, or 8 rows where new rows follow.
+      // The page id is asked for a step ahead of its use
+      const int g = lane / NB, x = lane % NB;
+      struct Copy { int page, row, h, key; bool fresh, cached, want; };
+      int k = 0;
+      bool open = false;
+      auto fetch = [&](Copy& c) -> bool {
+        if (!open || k >= w.k1) {
+          if (!w.next()) return false;
+          open = true;
+          k = w.k0;
         }
+        c.fresh = k >= w.R.kt;
+        c.h = w.h;
+        c.key = g << (c.fresh ? 3 : box_shift);
+        c.cached = !c.fresh || c.key < w.R.a;
+        c.want = c.key < w.keys(k);
+        c.page = 0;
+        c.row = w.R.r0 + (k - w.R.kt) * kKeys + c.key - w.R.a;
+        if (c.want && c.cached) {
+          const int at = k * kKeys + c.key;
+          c.page = p.table[(int64_t)w.b * p.table_stride + (at >> p.page_shift)];
+          c.row = at & ((1 << p.page_shift) - 1);
+        }
+        ++k;
+        return true;
+      };
+      Copy cur, nxt;
+      bool ok = true, have = fetch(cur);
+      int t = 0, issued = 0;
+      while (have) {
+        const bool more = fetch(nxt);
+        if (cur.cached && cur.want && (cur.page < 0 || cur.page >= p.n_pages)) {
+          cur.want = false;
+          raise_status(status, kDevIndex, 0x41);
+        }
+        const uint32_t each = 128u << (cur.fresh ? 3 : box_shift);
+        const uint32_t bytes = each * __popc(__ballot_sync(0xffffffffu, cur.want));
+        const int sl = t % depth;
+        if (t >= depth) {
+          ok = wait<true>(bar(empty0 + sl), ((t / depth) - 1) & 1, W, 0x100 + y);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bar(full0 + sl), bytes);
+        __syncwarp();
+        if (cur.want) {
+          const uint32_t d = ring + sl * C::kTile + (uint32_t)(x * C::kBox + cur.key * 128);
+          if (cur.cached) tma_load_4d(d, cur.fresh ? c8map : cmap, bar(full0 + sl), x * 64, cur.h, cur.row, cur.page);
+          else tma_load_3d(d, nmap, bar(full0 + sl), x * 64, cur.h, cur.row);
+        }
+        issued = ++t;
+        cur = nxt;
+        have = more;
       }
       __syncwarp();
       // drain: every copy has landed before the block exits
-      for (int i = max(0, k_issued - KS); i < k_issued; ++i) wait_drain(bar(bKF + i % KS), (i / KS) & 1);
-      for (int i = max(0, v_issued - VS); i < v_issued; ++i) wait_drain(bar(bVF + i % VS), (i / VS) & 1);
+      for (int i = max(0, issued - depth); i < issued; ++i)
+        wait_drain(bar(full0 + i % depth), (i / depth) & 1);
     } else if (warp == 1) {
       // --------------------------------------------------------------- MMA
       // the warp walks together and one elected lane issues: loop state and
@@ -539,35 +549,32 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       wait_drain(bar(bDR), 0);
     } else {
       // ------------------------------------------ Q's copies and the tree's masks
-      const int th = threadIdx.x - 64;
       int lu = 0, q_issued = 0;
       bool ok = true, bad = false;
       while (ok && w.next()) {
         const int node0 = w.rt * p.npt, rows = min(p.npt, w.R.n - node0) * p.G;
         const int sq = lu % QS, sm = lu & 1;
-        if (warp == 2) {
-          if (lu >= QS) ok = wait<true>(bar(bQE + sq), ((lu / QS) - 1) & 1, W, 0x600);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          // the rows of npt nodes (nodes behind the request's are columns that
-          // nobody reads)
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(bQF + sq), (uint32_t)(NB * p.npt * p.G * 128));
-            for (int x = 0; x < NB; ++x)
-              tma_load_3d(smem_u32(sQ + sq * C::kQ) + x * C::kQBox, &qmap, bar(bQF + sq), x * 64,
-                          w.h * p.G, w.R.r0 + node0);
-          }
-          q_issued = lu + 1;
-          __syncwarp();
+        if (lu >= QS) ok = wait<true>(bar(bQE + sq), ((lu / QS) - 1) & 1, W, 0x600);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        // the rows of npt nodes (nodes behind the request's are columns that
+        // nobody reads)
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(bQF + sq), (uint32_t)(NB * p.npt * p.G * 128));
+          for (int x = 0; x < NB; ++x)
+            tma_load_3d(smem_u32(sQ + sq * C::kQ) + x * C::kQBox, &qmap, bar(bQF + sq), x * 64,
+                        w.h * p.G, w.R.r0 + node0);
         }
+        q_issued = lu + 1;
+        __syncwarp();
         if (lu >= 2) ok = wait<true>(bar(bSE + sm), ((lu >> 1) - 1) & 1, W, 0x610);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        // parents as the masks use them (each warp keeps its own copy): the
-        // index, or -1 for roots, for children of unused nodes, and for what
-        // is no index; unused nodes themselves -2
+        // parents as the masks use them: the index, or -1 for roots, for
+        // children of unused nodes, and for what is no index; unused nodes
+        // themselves -2
         const bool tree = w.k1 > w.R.kt;
-        int16_t* par = sPar + (warp - 2) * MIS_TREE_MAX_NODES;
+        int16_t* par = sPar;
         if (p.parents) {
 #pragma unroll 2
           for (int j = lane; j < w.R.n; j += 32) {
@@ -579,10 +586,10 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           __syncwarp();
         }
         // columns of unused nodes, and who sees which new key
-        if (th < 8) sNf[sm * 8 + th] = 0;
+        if (lane < 8) sNf[sm * 8 + lane] = 0;
 #pragma unroll 1
-        for (int c0 = 0; c0 < N; c0 += 64) {
-          const int n = c0 + th;
+        for (int c0 = 0; c0 < N; c0 += 32) {
+          const int n = c0 + lane;
           const int i = node0 + over_g(p, n);
           const bool live = n < rows;
           const bool dead = live && p.parents && par[i] == MIS_TREE_UNUSED;
