@@ -442,8 +442,10 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         wait_drain(bar(full0 + i % depth), (i / depth) & 1);
     } else if (warp == 1) {
       // --------------------------------------------------------------- MMA
-      // the warp walks together and one elected lane issues: loop state and
-      // descriptors then stay in uniform registers
+      // the warp walks together and one elected lane issues, so loop state and
+      // descriptors stay in uniform registers. This warp's own instructions are
+      // the longest chain of a short step: slots and phases are counted along
+      // instead of divided out, and no clock is read while it looks around
       constexpr uint32_t idS = idesc_bf16(128, N, false);
       constexpr uint32_t idO = idesc_bf16(128, N, true) | (1u << 15);   // A MN-major too
       bool ok = true;
@@ -452,34 +454,45 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         return __all_sync(0xffffffffu, r);
       };
       if (p.stall) ok = wait_all(bDR, 0, 0x7ff);               // nothing arrives before the drain
-      struct Step { int lu, kv; bool first, last; };
-      int k = 0, lu = -1;
-      auto fetch = [&](Step& s) -> bool {                      // the block's next step
-        if (lu < 0 || k >= w.k1) {
-          if (!w.next()) return false;
-          ++lu;
-          k = w.k0;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      // the step whose S comes next: its key rows, place in the unit, K slot
+      // and phase, Q slot and phase, S buffer
+      struct Ring { int slot; uint32_t ph; };
+      auto turn = [](Ring& r, int depth) { if (++r.slot == depth) { r.slot = 0; r.ph ^= 1; } };
+      struct Step { int kv; bool first, last; } cur, nxt;
+      int k = 0, k1 = 0;
+      auto fetch = [&](Step& s) -> bool {
+        const bool first = k >= k1;
+        if (first) {
+          const bool more = w.next();
+          if (!__all_sync(0xffffffffu, more)) return false;
+          k = __shfl_sync(0xffffffffu, w.k0, 0);
+          k1 = __shfl_sync(0xffffffffu, w.k1, 0);
         }
-        s.lu = lu;
-        s.kv = w.keys(k);
-        s.first = k == w.k0;
-        s.last = k + 1 == w.k1;
-        ++k;
+        s.kv = __shfl_sync(0xffffffffu, w.keys(k), 0);
+        s.first = first;
+        s.last = ++k == k1;
         return true;
       };
-      auto s_ready = [&](const Step& s, int t) -> bool {
-        const bool r = mbar_test_wait(bar(bKF + t % KS), (t / KS) & 1) &&
-                       (!s.first || mbar_test_wait(bar(bQF + s.lu % QS), (s.lu / QS) & 1));
+      Ring rk{0, 0}, rv{0, 0}, rq{QS - 1, 1}, rs{0, 0}, ro{1, 1};
+      // rq, ro: the unit under way (they turn when one begins); rs.slot: S buffer
+      auto s_ready = [&](const Step& s) -> bool {
+        Ring q = rq;
+        if (s.first) turn(q, QS);
+        const bool r = mbar_test_wait(bar(bKF + rk.slot), rk.ph) &&
+                       (!s.first || mbar_test_wait(bar(bQF + q.slot), q.ph));
         return __all_sync(0xffffffffu, r);
       };
-      const uint32_t dQ = smem_u32(sQ), dK = smem_u32(sK), dV = smem_u32(sV), dP = smem_u32(sP);
-      auto issue_s = [&](const Step& s, int t) -> bool {
-        if (s.first && !wait_all(bQF + s.lu % QS, (s.lu / QS) & 1, 0x200)) return false;
-        if (!wait_all(bKF + t % KS, (t / KS) & 1, 0x300)) return false;
+      auto issue_s = [&](const Step& s) -> bool {
+        if (s.first) {
+          turn(rq, QS);
+          if (!wait_all(bQF + rq.slot, rq.ph, 0x200)) return false;
+        }
+        if (!wait_all(bKF + rk.slot, rk.ph, 0x300)) return false;
         tc_fence_after();
-        const uint32_t d = __shfl_sync(0xffffffffu, tmem + colS(t & 1), 0);
-        const uint64_t a = sdesc_sw128(__shfl_sync(0xffffffffu, dK + (t % KS) * C::kTile, 0), 16, 1024);
-        const uint64_t b = sdesc_sw128(__shfl_sync(0xffffffffu, dQ + (s.lu % QS) * C::kQ, 0), 16, 1024);
+        const uint32_t d = tm + colS(rs.slot);
+        const uint64_t a = sdesc_sw128(smem_u32(sK) + rk.slot * C::kTile, 16, 1024);
+        const uint64_t b = sdesc_sw128(smem_u32(sQ) + rq.slot * C::kQ, 16, 1024);
         if (elect_uniform()) {
 #pragma unroll
           for (int x = 0; x < NB; ++x)
@@ -487,61 +500,67 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
             for (int ks = 0; ks < 4; ++ks)
               mma_ss(d, a + ((x * C::kBox + ks * 32) >> 4), b + ((x * C::kQBox + ks * 32) >> 4), idS,
                      (x | ks) != 0);
-          mma_commit(bar(bSF + (t & 1)));
-          mma_commit(bar(bKE + t % KS));
-          if (s.last) mma_commit(bar(bQE + s.lu % QS));
+          mma_commit(bar(bSF + rs.slot));
+          mma_commit(bar(bKE + rk.slot));
+          if (s.last) mma_commit(bar(bQE + rq.slot));
         }
         __syncwarp();
+        turn(rk, KS);
+        turn(rs, 2);
         return true;
       };
-      Step cur, nxt;
-      int t = 0;
+      uint32_t pf = 0, units = 0;
       bool have = ok && fetch(cur);
-      if (have) ok = issue_s(cur, 0);
+      if (have) ok = issue_s(cur);
       while (ok && have) {
         const bool more = fetch(nxt);
         // the next S runs during this step's softmax: look for its operands
-        // and for P in turn (a look that came too early once would leave S
-        // behind this step's PV: attn of 256 rows a kv head 172 -> TTT us)
+        // and for P in turn (one look that came too early would leave S
+        // behind this step's PV)
         bool early = !more;
-        const uint64_t t0 = globaltimer();
         for (uint32_t it = 1; !early; ++it) {
-          if (s_ready(nxt, t + 1)) {
-            if (!(ok = issue_s(nxt, t + 1))) break;
+          if (s_ready(nxt)) {
+            if (!(ok = issue_s(nxt))) break;
             early = true;
-          } else if (__all_sync(0xffffffffu, mbar_test_wait(bar(bPF), t & 1)) ||
-                     ((it & 31) == 0 && __any_sync(0xffffffffu, *abort_flag || globaltimer() - t0 > p.wait_ns))) {
-            break;
+          } else if (__all_sync(0xffffffffu, mbar_test_wait(bar(bPF), pf)) || (it & 4095) == 0) {
+            break;                                             // P is there, or the bounded wait's turn
           }
         }
-        if (!ok || !(ok = wait_all(bPF, t & 1, 0x400))) break;
-        if (!(ok = wait_all(bVF + t % VS, (t / VS) & 1, 0x480))) break;
-        if (cur.first && cur.lu >= 2 &&
-            !(ok = wait_all(bOE + (cur.lu & 1), ((cur.lu >> 1) - 1) & 1, 0x500)))
-          break;
+        if (!ok || !(ok = wait_all(bPF, pf, 0x400))) break;
+        if (!(ok = wait_all(bVF + rv.slot, rv.ph, 0x480))) break;
+        if (cur.first) {
+          turn(ro, 2);
+          // O's buffer: the unit before the last must have been read out
+          if (units >= 2 && !(ok = wait_all(bOE + ro.slot, ro.ph ^ 1, 0x500))) break;
+          ++units;
+        }
         tc_fence_after();
         // V [key][d] and P [key][row], both MN-major: 8-key groups 1024 B
         // apart, 64-column boxes kBox apart. D = 64 repeats its one box
         // (stride 0): rows 64..127 of O^T equal rows 0..63.
-        const uint32_t d = __shfl_sync(0xffffffffu, tmem + colO(cur.lu & 1), 0);
-        const uint64_t a = sdesc_sw128(__shfl_sync(0xffffffffu, dV + (t % VS) * C::kTile, 0),
-                                       D == 128 ? C::kBox : 0, 1024);
-        const uint64_t b = sdesc_sw128(dP, C::kBox, 1024);
-        const int nks = __shfl_sync(0xffffffffu, (cur.kv + 15) >> 4, 0);
-        const uint32_t acc = __shfl_sync(0xffffffffu, cur.first ? 0u : 1u, 0);
+        const uint32_t d = tm + colO(ro.slot), acc = cur.first ? 0u : 1u;
+        const uint64_t a = sdesc_sw128(smem_u32(sV) + rv.slot * C::kTile, D == 128 ? C::kBox : 0, 1024);
+        const uint64_t b = sdesc_sw128(smem_u32(sP), C::kBox, 1024);
+        const int nks = (cur.kv + 15) >> 4;
         if (elect_uniform()) {
+          mma_ss(d, a, b, idO, acc);
+          if (nks == kKeys / 16) {
 #pragma unroll
-          for (int ks = 0; ks < kKeys / 16; ++ks)
-            if (ks < nks) mma_ss(d, a + ks * 128, b + ks * 128, idO, ks == 0 ? acc : 1u);
-          mma_commit(bar(bVE + t % VS));
+            for (int ks = 1; ks < kKeys / 16; ++ks) mma_ss(d, a + ks * 128, b + ks * 128, idO, 1u);
+          } else {
+#pragma unroll 1
+            for (int ks = 1; ks < nks; ++ks) mma_ss(d, a + ks * 128, b + ks * 128, idO, 1u);
+          }
+          mma_commit(bar(bVE + rv.slot));
           mma_commit(bar(bPV));
-          if (cur.last) mma_commit(bar(bOF + (cur.lu & 1)));
+          if (cur.last) mma_commit(bar(bOF + ro.slot));
         }
         __syncwarp();
-        if (!early && !(ok = issue_s(nxt, t + 1))) break;
+        turn(rv, VS);
+        pf ^= 1;
+        if (!early && !(ok = issue_s(nxt))) break;
         cur = nxt;
         have = more;
-        ++t;
       }
       // drain: all tensor-core work of the elected lane completes before dealloc
       if (elect_uniform()) mma_commit(bar(bDR));
@@ -647,7 +666,14 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         ok = wait<true>(bar(bSE + slot), ((lu >> 1) - 1) & 1, W, 0x700);
         ok = __all_sync(0xffffffffu, ok);
       }
+      // the page under this thread's key row, asked for a step ahead (0 where
+      // there is no cached row)
       const int32_t* row = p.table + (int64_t)w.b * p.table_stride;
+      auto page_of = [&](int k) {
+        const int at = k * kKeys + r;
+        return k < w.k1 && at < w.R.L ? row[at >> p.page_shift] : 0;
+      };
+      int page = page_of(w.k0);
 #pragma unroll 1
       for (int k = w.k0; k < w.k1; ++k, ++t) {
         const int kv = w.keys(k), kv16 = (kv + 15) & ~15;
@@ -656,11 +682,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         // what this thread's key row holds: a cached row, new row j, or nothing
         const int j = fresh ? (k - w.R.kt) * kKeys + r - w.R.a : -1;
         const bool node = fresh && j >= 0 && r < kv;
-        bool seen = node;
-        if (!node && r < kv && k * kKeys + r < w.R.L) {
-          const int page = row[(k * kKeys + r) >> p.page_shift];
-          seen = page >= 0 && page < p.n_pages;
-        }
+        const bool seen = node || (r < kv && k * kKeys + r < w.R.L && page >= 0 && page < p.n_pages);
+        page = page_of(k + 1);
         if (ok) {
           ok = wait<true>(bar(bSF + (t & 1)), (t >> 1) & 1, W, 0x710);
           if (ok && fresh) ok = wait<true>(bar(bMF + slot), (lu >> 1) & 1, W, 0x720);
