@@ -72,11 +72,13 @@ struct TreeCfg {
   static constexpr int kP = kKeys * 128 * (N > 64 ? 2 : 1);
   static constexpr int kK = D == 128 ? (N == 128 ? 2 : 3) : (N == 128 ? 4 : 5);
   static constexpr int kV = D == 128 ? (N == 16 ? 3 : 2) : (N == 128 ? 4 : 5);
-  static constexpr int kMW = N == 128 ? MIS_TREE_MAX_NODES / 32 : 2;   // mask words of a column
+  static constexpr int kNW = N < 32 ? 1 : N / 32;       // mask words of a key: which columns see it
+  static constexpr int kNodes = N == 128 ? MIS_TREE_MAX_NODES : 64;   // N >= max_nodes * G below 128
+  static constexpr int kLanes = N == 128 ? 4 : 1;       // see TreeParams::lanes
   static constexpr int kTmem = N == 16 ? 64 : 4 * N;    // S_0 | S_1 | O_0 | O_1
   // floats / words behind the tiles
-  static constexpr int oMask = 0;                       // [2][N][kMW]
-  static constexpr int oDead = oMask + 2 * N * kMW;     // [2][4] unused rows of the tile
+  static constexpr int oMask = 0;                       // [2][kNodes][kNW]
+  static constexpr int oDead = oMask + 2 * kNodes * kNW;   // [2][4] unused rows of the tile
   static constexpr int oNf = oDead + 8;                 // [2][8] keys with a non-finite value
   static constexpr int oM = oNf + 16;                   // [2][N] references, negated, for the epilogue
   static constexpr int oL = oM + 2 * N;                 // [2][4][N] sums of each softmax warp
@@ -92,8 +94,8 @@ struct TreeCfg {
 };
 
 // Register budgets of the warpgroups where N >= 64 needs more than 128 in the
-// softmax: 128 * (64 + 64) + 256 * 192 = 512 * 128, the launch's own.
-constexpr int kRegCtl = 64, kRegEpi = 64, kRegSoft = 192;
+// softmax: 128 * (80 + 80) + 256 * 176 = 512 * 128, the launch's own.
+constexpr int kRegCtl = 80, kRegEpi = 80, kRegSoft = 176;
 
 struct TreeParams {
   const __nv_bfloat16* v;
@@ -108,10 +110,14 @@ struct TreeParams {
   const int32_t* parents;
   int32_t B, T, Hkv, G, max_nodes;
   int32_t npt;             // nodes of a row tile, N / G
+  int32_t lanes;           // row tiles rt, rt + lanes, ... of all requests form a lane, and the lanes lie
+                           // end to end: tiles that share K and V are worked on at the same time, by
+                           // blocks that start a lane's length apart, and meet in L2
   uint32_t g_magic;        // ceil(2^32 / G): n / G = umulhi(n, magic) for n < N, 1 < G <= 128
   float scale_log2;
   uint32_t* cta_status;    // [blocks][2]
-  int4* meta;              // [blocks] the split unit that starts in the block: b, h, row tile, pieces
+  int4* meta;              // [blocks] the split unit that starts in the block: its first row of q,
+                           // columns, kv head, pieces
   float2* ml;              // [2 * blocks][N] (max, sum) of a piece
   float* part;             // [2 * blocks][N][D]
   uint64_t wait_ns;
@@ -153,32 +159,42 @@ __device__ __forceinline__ Req load_req(const TreeParams& p, int b) {
 // Where a block starts: found by one thread, read by every role.
 struct Start {
   Req R;
-  int b, h, rt, k0;
+  int z, b, h, rt, k0;
 };
 
-// The units of a block, in order: unit (b, h, rt), steps [k0, k1).
+// Row tiles of a request in lane z.
+__device__ __forceinline__ int lane_tiles(const TreeParams& p, const Req& R, int z) {
+  return R.n && R.nrt > z ? (R.nrt - z + p.lanes - 1) / p.lanes : 0;
+}
+
+// The units of a block, in order: lane z, unit (b, h, rt), steps [k0, k1).
 template <int N>
 struct Walk {
   const TreeParams& p;
   Req R;
   int left;
-  int b, h, rt, k0, k1;
+  int z, b, h, rt, k0, k1;
   bool fresh;
 
   __device__ __forceinline__ Walk(const TreeParams& prm, const Start& s, int steps)
-      : p(prm), R(s.R), left(steps), b(s.b), h(s.h), rt(s.rt), k0(s.k0), k1(0), fresh(true) {}
+      : p(prm), R(s.R), left(steps), z(s.z), b(s.b), h(s.h), rt(s.rt), k0(s.k0), k1(0), fresh(true) {}
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
     if (!fresh) {
       k0 = 0;
-      if (++rt == R.nrt) {
-        rt = 0;
+      rt += p.lanes;
+      if (rt >= R.nrt) {
+        rt = z;
         if (++h == p.Hkv) {
           h = 0;
           do {
-            if (++b >= p.B) return false;
+            if (++b >= p.B) {
+              b = 0;
+              rt = ++z;
+              if (z >= p.lanes) return false;
+            }
             R = load_req<N>(p, b);
-          } while (R.n == 0);
+          } while (R.n == 0 || R.nrt <= z);
         }
       }
     }
@@ -239,7 +255,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
   using C = TreeCfg<D, N>;
   constexpr int NB = C::kNB, NC = C::kNC, WG = C::kWG, KS = C::kK, VS = C::kV, QS = C::kQS;
-  constexpr int MW = C::kMW;
+  constexpr int NW = C::kNW, LM = C::kLanes;
   // barriers
   constexpr int bQF = 0, bQE = bQF + 2, bKF = bQE + 2, bKE = bKF + KS, bVF = bKE + KS,
                 bVE = bVF + VS, bSF = bVE + VS, bPF = bSF + 2, bPV = bPF + 1, bOF = bPV + 1,
@@ -269,7 +285,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + nBar);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   __shared__ Start s_start;
-  __shared__ int s_sums[C::kThreads / 32];
+  __shared__ int s_sums[C::kLanes][C::kThreads / 32];
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -306,22 +322,28 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   uint32_t* status = p.cta_status + 2 * blockIdx.x;
   const int per = (p.B + C::kThreads - 1) / C::kThreads;
   const int rb0 = min(p.B, (int)threadIdx.x * per), rb1 = min(p.B, rb0 + per);
-  int mine = 0;                                  // the host bounds the total below 2^31
+  int mine[LM], incl[LM];                        // the host bounds the total below 2^31
+#pragma unroll
+  for (int z = 0; z < LM; ++z) mine[z] = 0;
   bool bad_req = false;
   Req R;
 #pragma unroll 1
   for (int b = rb0; b < rb1; ++b) {
     R = load_req<N>(p, b);
     bad_req |= R.bad;
-    if (R.n) mine += p.Hkv * R.nrt * R.nkt;
-  }
-  int incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    for (int z = 0; z < LM; ++z) mine[z] += p.Hkv * lane_tiles(p, R, z) * R.nkt;
   }
-  if (lane == 31) s_sums[warp] = incl;
+#pragma unroll
+  for (int z = 0; z < LM; ++z) {
+    incl[z] = mine[z];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl[z], o);
+      if (lane >= o) incl[z] += y;
+    }
+    if (lane == 31) s_sums[z][warp] = incl[z];
+  }
   if (threadIdx.x == 0) {
     status[0] = 0;
     status[1] = 0;
@@ -330,32 +352,36 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   tc_fence_before();
   const bool any_bad = __syncthreads_or(bad_req);
   tc_fence_after();
-  int total = 0, before = 0;
+  int total = 0, before[LM];                     // before: steps ahead of this warp's, lane by lane
 #pragma unroll
-  for (int w = 0; w < C::kThreads / 32; ++w) {
-    if (w == warp) before = total;
-    total += s_sums[w];
-  }
+  for (int z = 0; z < LM; ++z)
+#pragma unroll
+    for (int w = 0; w < C::kThreads / 32; ++w) {
+      if (w == warp) before[z] = total;
+      total += s_sums[z][w];
+    }
   if (any_bad && blockIdx.x == 0 && threadIdx.x == 0) raise_status(status, kDevIndex, 0x40);
   // blocks [0, rem) take quo + 1 steps, the others quo
   const int quo = total / (int)gridDim.x, rem = total - quo * (int)gridDim.x;
   const int blk = (int)blockIdx.x;
   const int f0 = blk * quo + min(blk, rem), steps = quo + (blk < rem ? 1 : 0);
-  {
-    int at = before + incl - mine;
-    if (steps > 0 && f0 >= at && f0 < at + mine) {
+#pragma unroll
+  for (int z = 0; z < LM; ++z) {
+    int at = before[z] + incl[z] - mine[z];
+    if (steps > 0 && f0 >= at && f0 < at + mine[z]) {
 #pragma unroll 1
       for (int b = rb0; b < rb1; ++b) {
         if (per > 1) R = load_req<N>(p, b);
-        const int c = R.n ? p.Hkv * R.nrt * R.nkt : 0;
+        const int nt = lane_tiles(p, R, z), c = p.Hkv * nt * R.nkt;
         if (f0 >= at + c) { at += c; continue; }
         Start s;
         s.R = R;
+        s.z = z;
         s.b = b;
         const int off = f0 - at, u = off / R.nkt;
         s.k0 = off - u * R.nkt;
-        s.h = N < 128 ? u : u / R.nrt;
-        s.rt = u - s.h * R.nrt;
+        s.h = N < 128 ? u : u / nt;
+        s.rt = z + (u - s.h * nt) * p.lanes;
         s_start = s;
         break;
       }
@@ -604,25 +630,50 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           }
           __syncwarp();
         }
-        // columns of unused nodes, and who sees which new key
+        // columns of unused nodes
         if (lane < 8) sNf[sm * 8 + lane] = 0;
 #pragma unroll 1
         for (int c0 = 0; c0 < N; c0 += 32) {
           const int n = c0 + lane;
-          const int i = node0 + over_g(p, n);
-          const bool live = n < rows;
-          const bool dead = live && p.parents && par[i] == MIS_TREE_UNUSED;
+          const bool dead = n < rows && p.parents && par[node0 + over_g(p, n)] == MIS_TREE_UNUSED;
           const uint32_t dw = __ballot_sync(0xffffffffu, dead);
-          if (n < N) {
-            if (lane == 0) sDead[sm * 4 + (n >> 5)] = dw;
-            uint32_t* m = sMask + (sm * N + n) * MW;
-            if (tree) {
-              const bool chain = !p.parents;
-#pragma unroll
-              for (int x = 0; x < MW; ++x) m[x] = chain && live ? bit_range(0, i + 1 - 32 * x) : 0u;
-              for (int j = (live && !dead && !chain) ? i : -1; j >= 0; j = par[j])
-                m[j >> 5] |= 1u << (j & 31);
+          if (lane == 0) sDead[sm * 4 + (c0 >> 5)] = dw;
+        }
+        if (tree) {
+          // who sees new key j: a bit a column
+          uint32_t* m = sMask + sm * C::kNodes * NW;
+          if (!p.parents) {
+            for (int x = lane; x < w.R.n * NW; x += 32) {
+              const int j = x / NW, c0 = x % NW * 32;
+              m[x] = bit_range((j - node0) * p.G - c0, rows - c0);
             }
+          } else {
+            for (int x = lane; x < w.R.n * NW; x += 32) m[x] = 0;
+            __syncwarp();
+            for (int i = lane; i * p.G < rows; i += 32) {
+              const int lo = i * p.G, hi = lo + p.G;
+              if (par[node0 + i] == MIS_TREE_UNUSED) continue;
+              for (int j = node0 + i; j >= 0; j = par[j])
+                for (int x = lo >> 5; x <= (hi - 1) >> 5; ++x)
+                  atomicOr(&m[j * NW + x], bit_range(lo - 32 * x, hi - 32 * x));
+            }
+          }
+          __syncwarp();
+          // new rows whose V holds a NaN or an infinity (see the softmax)
+          constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes a row, rows at a time
+#pragma unroll 4
+          for (int j0 = 0; j0 < w.R.n; j0 += RPI) {
+            const int j = j0 + lane / LPR;
+            bool nf = false;
+            if (j < w.R.n) {
+              const uint4 u = *reinterpret_cast<const uint4*>(p.v + (int64_t)(w.R.r0 + j) * p.vs + w.h * D +
+                                                              lane % LPR * 8);
+              const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                nf |= (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
+            }
+            if (nf) atomicOr(&sNf[sm * 8 + (j >> 5)], 1u << (j & 31));
           }
         }
         __syncwarp();
@@ -691,32 +742,38 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         }
         tc_fence_after();
         const uint32_t tS = tl + colS(t & 1) + c0;
-        const uint32_t* mk = sMask + (slot * N + c0) * MW + (node ? j >> 5 : 0);
+        const uint32_t* mk = sMask + (slot * C::kNodes + (node ? j : 0)) * NW;
         const bool plain = __all_sync(0xffffffffu, seen && !node);
         // Steps that are not plain (new rows, a partial tile, a negative scale,
         // references by column) have their scores rewritten in tensor memory
-        // first, in a rolled loop: hidden ones -inf, the others times the
-        // scale's sign and less the column's reference. What follows is then
-        // the same short code for all steps; instruction fetches, not
-        // arithmetic, were what this kernel waited for when it was unrolled
-        // for each (256 rows a kv head: 335 -> see the table).
+        // first: hidden ones -inf, the others times the scale's sign and less
+        // the column's reference. What follows is then the same short code for
+        // every step; unrolled for each kind, the kernel waited for instruction
+        // fetches more than for anything else (256 rows a kv head: 335 us,
+        // with the elected issue below 185).
         bool over = !ok || first;
         if (ok && active && !(plain && one && sign > 0.f)) {
 #pragma unroll 1
-          for (int q = 0; q < NC; q += 8) {
-            uint32_t x[8];
-            ld_cols<8>(tS + q, x);
+          for (int q = 0; q < NC; q += CC) {
+            const int c = c0 + q;
+            const uint32_t bits = (node ? mk[c >> 5] : seen ? 0xffffffffu : 0u) >> (node ? c & 31 : 0);
+            __syncwarp();
+            uint32_t x[CC];
+            ld_cols<CC>(tS + q, x);
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              const bool hide = !seen || (node && !((mk[(q + n) * MW] >> (j & 31)) & 1u));
-              const float b = one ? 0.f : ref[q + n];
+            for (int n = 0; n < CC; ++n) {
+              const bool hide = !((bits >> n) & 1u);
               float y = __uint_as_float(x[n]) * sign;
-              // a column that saw nothing so far has no reference to be taken off
-              if (b >= -kEmpty) over |= !hide && y > -INFINITY;
-              else y = fmaf(b, inv_sa, y);
+              if (!one) {
+                // a column that saw nothing so far has no reference to be taken off
+                const float b = ref[q + n];
+                if (b >= -kEmpty) over |= !hide && y > -INFINITY;
+                else y = fmaf(b, inv_sa, y);
+              }
               x[n] = __float_as_uint(hide ? -INFINITY : y);
             }
-            tmem_st8(tS + q, x);
+            if constexpr (CC == 16) tmem_st16(tS + q, x);
+            else tmem_st32(tS + q, x);
           }
           tmem_st_wait();
         }
@@ -866,37 +923,26 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           // a V row that no row of the tile sees must not meet a zero
           // probability with a NaN or an infinity; one that some rows see
           // leaves its non-finite elements to the epilogue
-          if (ok && !plain && wg == 0 && r < kv16 && (!seen || node)) {
+          if (ok && !plain && wg == 0 && r < kv16 &&
+              (!seen || (node && ((sNf[slot * 8 + (j >> 5)] >> (j & 31)) & 1u)))) {
             ok = wait<true>(bar(bVF + t % VS), (t / VS) & 1, W, 0x750);
             if (ok) {
               const uint32_t aV = smem_u32(sV + (t % VS) * C::kTile) + r * 128;
-              bool nf = false;
-#pragma unroll 1
-              for (int c = 0; c < 8 * NB; c += 4) {
+#pragma unroll 2
+              for (int c = 0; c < 8 * NB; ++c) {
                 const uint32_t a = aV + (c >> 3) * C::kBox + (c & 7) * 16;
-                uint32_t x[4][4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
+                uint32_t x[4] = {0, 0, 0, 0};
+                if (seen) {
                   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                               : "=r"(x[e][0]), "=r"(x[e][1]), "=r"(x[e][2]), "=r"(x[e][3])
-                               : "r"(a + e * 16) : "memory");
-                bool any = !seen;
+                               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(a) : "memory");
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                  for (int y = 0; y < 4; ++y) {
-                    uint32_t keep = 0xffffffffu;
-                    if ((x[e][y] & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
-                    if ((x[e][y] & 0x7f800000u) == 0x7f800000u) keep &= 0x0000ffffu;
-                    nf |= keep != 0xffffffffu;
-                    x[e][y] = seen ? x[e][y] & keep : 0u;
+                  for (int e = 0; e < 4; ++e) {
+                    if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u;
+                    if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0x0000ffffu;
                   }
-                if (any || nf)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    st_shared_v4(a + e * 16, x[e][0], x[e][1], x[e][2], x[e][3]);
+                }
+                st_shared_v4(a, x[0], x[1], x[2], x[3]);
               }
-              if (nf && node) atomicOr(&sNf[slot * 8 + (j >> 5)], 1u << (j & 31));
             }
           }
           ok = __all_sync(0xffffffffu, ok);
@@ -999,7 +1045,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           // the unit starts here at f1 - k1 and reaches into later blocks
           const int last = f0 + steps - w.k1 + w.R.nkt - 1, cut = rem * (quo + 1);
           const int lastb = last < cut ? last / (quo + 1) : rem + (last - cut) / quo;
-          p.meta[blockIdx.x] = make_int4(w.b, w.h, w.rt, (int)(lastb - blockIdx.x + 1));
+          p.meta[blockIdx.x] = make_int4(w.R.r0 + node0, rows, w.h, (int)(lastb - blockIdx.x + 1));
         }
       }
       float* inv = sInv + sw * N;
@@ -1014,7 +1060,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       // non-finite values of the new rows, by key
       uint32_t nf = 0;
       if (w.k1 > w.R.kt)
-        for (int x = 0; x < MW; ++x) nf |= sNf[slot * 8 + x];
+        for (int x = 0; x < 8; ++x) nf |= sNf[slot * 8 + x];
 #pragma unroll 1
       for (int q = 0; q < NE; q += CH) {
         uint32_t ov[CH];
@@ -1026,16 +1072,18 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         }
         if (e0 + q >= rows) continue;
         if (nf) {
-          for (int x = 0; x < MW; ++x)
+          for (int x = 0; x < 8; ++x)
             for (uint32_t bits = sNf[slot * 8 + x]; bits; bits &= bits - 1) {
               const int j = x * 32 + __ffs(bits) - 1;
               const float val = __bfloat162float(p.v[(int64_t)(w.R.r0 + j) * p.vs + w.h * D + d]);
               if (isfinite(val)) continue;
+              const uint32_t* m = sMask + (slot * C::kNodes + j) * NW;
 #pragma unroll
               for (int n = 0; n < CH; ++n)
-                if ((sMask[(slot * N + e0 + q + n) * MW + x] >> (j & 31)) & 1u)
+                if ((m[(e0 + q + n) >> 5] >> ((e0 + q + n) & 31)) & 1u)
                   ov[n] = __float_as_uint(__uint_as_float(ov[n]) + val);
             }
+          __syncwarp();
         }
         if (!whole) {
           float* dst = p.part + ((int64_t)piece * N + e0 + q) * D + d;
@@ -1077,9 +1125,9 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   }
 }
 
-// Adds the pieces of split units in block order: block (c, y) takes rows 4y ..
-// 4y + 3 of the unit whose first piece block c of the attention left, a warp
-// a row. Block (0, 0) gathers the blocks' status words.
+// Adds the pieces of split units in block order: blocks (c, y) take the unit
+// whose first piece block c of the attention left, a warp a column. Block (0,
+// 0) gathers the blocks' status words.
 struct CombineParams {
   const uint32_t* cta_status;
   const int4* meta;
@@ -1089,86 +1137,96 @@ struct CombineParams {
   __nv_bfloat16* o;
   float* lse;
   int64_t os;
-  const int32_t* cu;
-  int32_t T, G, npt, blocks;
+  int32_t T, G, blocks;
 };
 
+constexpr int kCombineWarps = 8;
+
 template <int D, int N>
-__global__ void __launch_bounds__(128) mis_tree_combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(32 * kCombineWarps) mis_tree_combine_kernel(const CombineParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+  const int c = blockIdx.x;
+  const int4 u = p.meta[c];
+  if (c == 0 && blockIdx.y == 0 && warp == 0) {
     uint32_t bits = 0, where = 0;
-    for (int c = lane; c < p.blocks; c += 32) {
-      const uint32_t s = p.cta_status[2 * c];
-      if (s && !bits) where = p.cta_status[2 * c + 1];
+    for (int x = lane; x < p.blocks; x += 32) {
+      const uint32_t s = p.cta_status[2 * x];
+      if (s && !bits) where = p.cta_status[2 * x + 1];
       bits |= s;
     }
     const uint32_t any = __ballot_sync(0xffffffffu, bits != 0);
     where = __shfl_sync(0xffffffffu, where, any ? __ffs(any) - 1 : 0);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+    bits = __reduce_or_sync(0xffffffffu, bits);
     if (lane == 0) {
       p.status[0] = bits;
       p.status[1] = where;
     }
   }
-  const int c = blockIdx.x;
-  const int4 u = p.meta[c];
-  if (u.w < 2) return;
-  const int n = blockIdx.y * 4 + warp, r0 = p.cu[u.x] + u.z * p.npt;
-  if (n >= min(p.npt, p.cu[u.x + 1] - r0) * p.G) return;
+  const int n = blockIdx.y * kCombineWarps + warp, pieces = u.w;
+  if (pieces < 2 || n >= u.y) return;
   // piece s: the first lies in block c's second slot, the others in the first
-  // slots of the blocks that follow
-  auto slot = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
-  float m = kEmpty;
+  // slots of the blocks that follow. Lane s looks at piece s (of 32 at a
+  // time), while the first pieces' elements are on their way
+  auto at = [&](int s) { return (int64_t)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * N + n; };
+  constexpr int E = D / 32, A = 4;
+  auto load = [&](int s, float* y) {
+    const float* src = p.part + at(s) * D + lane * E;
+    if constexpr (E == 4) {
+      const float4 z = *reinterpret_cast<const float4*>(src);
+      y[0] = z.x; y[1] = z.y; y[2] = z.z; y[3] = z.w;
+    } else {
+      const float2 z = *reinterpret_cast<const float2*>(src);
+      y[0] = z.x; y[1] = z.y;
+    }
+  };
+  float y[A][E], acc[E];
+#pragma unroll
+  for (int s = 0; s < A; ++s) load(min(s, pieces - 1), y[s]);
   bool stuck = false;
-  for (int s = lane; s < u.w; s += 32) {
-    m = fmaxf(m, p.ml[(int64_t)slot(s) * N + n].x);
+  float m = kEmpty;
+  for (int s = lane; s < pieces; s += 32) {
+    m = fmaxf(m, p.ml[at(s)].x);
     stuck |= (p.cta_status[2 * (c + s)] & kDevTimeout) != 0;
   }
   if (__any_sync(0xffffffffu, stuck)) return;          // a piece is missing
   m = warp_max(m);
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
   float l = 0.f;
-  for (int s = lane; s < u.w; s += 32) {
-    const float2 x = p.ml[(int64_t)slot(s) * N + n];
-    l += x.y * ex2(x.x - m);
+  for (int s0 = 0; s0 < pieces; s0 += 32) {
+    float a = 0.f;
+    if (s0 + lane < pieces) {
+      const float2 x = p.ml[at(s0 + lane)];
+      a = ex2(x.x - m);
+      l += a * x.y;
+    }
+    __syncwarp();
+    // a piece that saw nothing weighs nothing, whatever it holds
+    for (int s1 = 0; s1 < min(32, pieces - s0); s1 += A) {
+      if (s0 + s1 > 0) {
+#pragma unroll
+        for (int s = 0; s < A; ++s) load(min(s0 + s1 + s, pieces - 1), y[s]);
+      }
+#pragma unroll
+      for (int s = 0; s < A; ++s) {
+        const float b = __shfl_sync(0xffffffffu, a, s1 + s);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = b != 0.f ? fmaf(b, y[s][e], acc[e]) : acc[e];
+      }
+    }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  constexpr int E = D / 32;
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 8
-  for (int s = 0; s < u.w; ++s) {
-    const int64_t at = (int64_t)slot(s) * N + n;
-    const float a = ex2(p.ml[at].x - m);
-    const float* src = p.part + at * D + lane * E;
-    float x[E];
-    if constexpr (E == 4) {
-      const float4 y = *reinterpret_cast<const float4*>(src);
-      x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-    } else {
-      const float2 y = *reinterpret_cast<const float2*>(src);
-      x[0] = y.x; x[1] = y.y;
-    }
-    // a piece that saw nothing weighs nothing, whatever it holds
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = a != 0.f ? fmaf(a, x[e], acc[e]) : acc[e];
-  }
-  const int i = n / p.G, h = u.y * p.G + n - i * p.G;
+  const int i = n / p.G, h = u.z * p.G + n - i * p.G;
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  uint32_t w[E / 2];
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (int64_t)(u.x + i) * p.os + (int64_t)h * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2)
-    w[e / 2] = inv != 0.f ? pack_bf16(acc[e] * inv, acc[e + 1] * inv) : 0u;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (int64_t)(r0 + i) * p.os + (int64_t)h * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E / 2; ++e) dst[e] = w[e];
+    dst[e / 2] = inv != 0.f ? pack_bf16(acc[e] * inv, acc[e + 1] * inv) : 0u;
   if (p.lse && lane == 0)
-    p.lse[(int64_t)h * p.T + r0 + i] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    p.lse[(int64_t)h * p.T + u.x + i] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -1215,8 +1273,8 @@ mis_status_t launch_tree(const CUtensorMap* m, const TreeParams& p, const Combin
   if (launch_pdl(kern, dim3((unsigned)c.blocks), dim3(Cf::kThreads), Cf::kSmem, st, m[0],
                  m[1], m[2], m[3], m[4], m[5], m[6], p) != cudaSuccess)
     return MIS_ERR_CUDA;
-  return launch_pdl(mis_tree_combine_kernel<D, N>, dim3((unsigned)c.blocks, N / 4), dim3(128), 0, st,
-                    c) == cudaSuccess
+  return launch_pdl(mis_tree_combine_kernel<D, N>, dim3((unsigned)c.blocks, N / kCombineWarps),
+                    dim3(32 * kCombineWarps), 0, st, c) == cudaSuccess
              ? MIS_OK
              : MIS_ERR_CUDA;
 }
@@ -1310,6 +1368,7 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     p.G = G; p.npt = npt;
     p.g_magic = (uint32_t)((0xffffffffull + (uint64_t)p.G) / (uint64_t)p.G);
     p.max_nodes = desc->max_nodes;
+    p.lanes = N < 128 ? 1 : std::min((desc->max_nodes + npt - 1) / npt, 4);
     p.scale_log2 = (desc->scale != 0.f ? desc->scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
     p.cta_status = reinterpret_cast<uint32_t*>(base + ws.status);
     p.meta = reinterpret_cast<int4*>(base + ws.meta);
@@ -1320,8 +1379,8 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     CombineParams c;
     c.cta_status = p.cta_status; c.meta = p.meta; c.ml = p.ml; c.part = p.part;
     c.status = reinterpret_cast<uint32_t*>(base);
-    c.o = p.o; c.lse = lse; c.os = o_row_stride; c.cu = cu_nodes;
-    c.T = desc->T; c.G = G; c.npt = npt; c.blocks = num_sms();
+    c.o = p.o; c.lse = lse; c.os = o_row_stride;
+    c.T = desc->T; c.G = G; c.blocks = num_sms();
     if (D == 128) {
       if (N == 16) return launch_tree<128, 16>(maps, p, c, st);
       if (N == 32) return launch_tree<128, 32>(maps, p, c, st);
