@@ -74,7 +74,7 @@ struct TreeCfg {
   static constexpr int kV = D == 128 ? (N == 16 ? 3 : 2) : (N == 128 ? 4 : 5);
   static constexpr int kNW = N < 32 ? 1 : N / 32;       // mask words of a key: which columns see it
   static constexpr int kNodes = N == 128 ? MIS_TREE_MAX_NODES : 64;   // N >= max_nodes * G below 128
-  static constexpr int kLanes = N == 128 ? 4 : 1;       // see TreeParams::lanes
+  static constexpr int kLanes = N == 128 ? 2 : 1;       // see TreeParams::lanes
   static constexpr int kTmem = N == 16 ? 64 : 4 * N;    // S_0 | S_1 | O_0 | O_1
   // floats / words behind the tiles
   static constexpr int oMask = 0;                       // [2][kNodes][kNW]
@@ -124,6 +124,24 @@ struct TreeParams {
   uint32_t stall;
 };
 
+// A bounded wait in few instructions (it stands at some thirty places): a wait
+// that runs out, or sees that another gave up, returns false. The site goes to
+// shared memory and to the status word when the block ends.
+struct Bound {
+  volatile uint32_t* gave_up;
+  uint64_t limit_ns;
+};
+__device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, const Bound& w, uint32_t where) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*w.gave_up) return false;
+  } while (globaltimer() - t0 <= w.limit_ns);
+  *w.gave_up = where;
+  return false;
+}
+
 // One request, checked. Its steps are the 128-key tiles of its cached rows,
 // then those of its new rows. When the new rows fit behind the last, partial
 // cache tile (from the next multiple of 8 rows, a copy's granularity) they
@@ -156,58 +174,48 @@ __device__ __forceinline__ Req load_req(const TreeParams& p, int b) {
   return R;
 }
 
-// Where a block starts: found by one thread, read by every role.
-struct Start {
-  Req R;
-  int z, b, h, rt, k0;
-};
-
 // Row tiles of a request in lane z.
 __device__ __forceinline__ int lane_tiles(const TreeParams& p, const Req& R, int z) {
   return R.n && R.nrt > z ? (R.nrt - z + p.lanes - 1) / p.lanes : 0;
 }
 
-// The units of a block, in order: lane z, unit (b, h, rt), steps [k0, k1).
-template <int N>
-struct Walk {
-  const TreeParams& p;
+// A unit of the block: request b's row tile rt for kv head h, steps [k0, k1);
+// k1 = 0 ends the list. at: the unit's first step here, counted over the batch.
+struct Unit {
   Req R;
-  int left;
-  int z, b, h, rt, k0, k1;
-  bool fresh;
-
-  __device__ __forceinline__ Walk(const TreeParams& prm, const Start& s, int steps)
-      : p(prm), R(s.R), left(steps), z(s.z), b(s.b), h(s.h), rt(s.rt), k0(s.k0), k1(0), fresh(true) {}
-  __device__ __forceinline__ bool next() {
-    if (left <= 0) return false;
-    if (!fresh) {
-      k0 = 0;
-      rt += p.lanes;
-      if (rt >= R.nrt) {
-        rt = z;
-        if (++h == p.Hkv) {
-          h = 0;
-          do {
-            if (++b >= p.B) {
-              b = 0;
-              rt = ++z;
-              if (z >= p.lanes) return false;
-            }
-            R = load_req<N>(p, b);
-          } while (R.n == 0 || R.nrt <= z);
-        }
-      }
-    }
-    fresh = false;
-    k1 = min(R.nkt, k0 + left);
-    left -= k1 - k0;
-    return true;
-  }
+  int z, b, h, rt, k0, k1, at;
   // key rows of step k: the products run over them, the rest of the tile is void
   __device__ __forceinline__ int keys(int k) const {
     return k < R.kt ? min(kKeys, R.L - k * kKeys) : min(kKeys, R.a + R.n - (k - R.kt) * kKeys);
   }
 };
+constexpr int kUnits = 4;      // units the K producer may be ahead of the last reader
+
+// The unit behind u; left: steps of the block not yet in a unit.
+template <int N>
+__device__ __forceinline__ bool next_unit(const TreeParams& p, Unit& u, int& left) {
+  if (left <= 0) return false;
+  u.at += u.k1 - u.k0;
+  u.k0 = 0;
+  u.rt += p.lanes;
+  if (u.rt >= u.R.nrt) {
+    u.rt = u.z;
+    if (++u.h == p.Hkv) {
+      u.h = 0;
+      do {
+        if (++u.b >= p.B) {
+          u.b = 0;
+          u.rt = ++u.z;
+          if (u.z >= p.lanes) return false;
+        }
+        u.R = load_req<N>(p, u.b);
+      } while (u.R.n == 0 || u.R.nrt <= u.z);
+    }
+  }
+  u.k1 = min(u.R.nkt, left);
+  left -= u.k1;
+  return true;
+}
 
 // Node (in its tile) of column n.
 __device__ __forceinline__ int over_g(const TreeParams& p, int n) {
@@ -259,8 +267,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   // barriers
   constexpr int bQF = 0, bQE = bQF + 2, bKF = bQE + 2, bKE = bKF + KS, bVF = bKE + KS,
                 bVE = bVF + VS, bSF = bVE + VS, bPF = bSF + 2, bPV = bPF + 1, bOF = bPV + 1,
-                bOE = bOF + 2, bST = bOE + 2, bSE = bST + 2, bMF = bSE + 2, bDR = bMF + 2,
-                nBar = bDR + 1;
+                bOE = bOF + 2, bST = bOE + 2, bSE = bST + 2, bMF = bSE + 2, bUF = bMF + 2,
+                bUE = bUF + kUnits, bDR = bUE + kUnits, nBar = bDR + 1;
   static_assert(nBar * 8 + 64 <= 512, "barrier space");
 
   griddep_launch_dependents();
@@ -284,7 +292,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   uint64_t* bars = reinterpret_cast<uint64_t*>(words + C::kWords);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + nBar);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  __shared__ Start s_start;
+  __shared__ Unit s_unit[kUnits];
   __shared__ int s_sums[C::kLanes][C::kThreads / 32];
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -306,6 +314,10 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     mbar_init(bar(bPF), 4 * WG);
     mbar_init(bar(bPV), 1);
     mbar_init(bar(bDR), 1);
+    for (int s = 0; s < kUnits; ++s) {
+      mbar_init(bar(bUF + s), 1);
+      mbar_init(bar(bUE + s), 7 + 4 * WG);               // every warp but the K producer
+    }
     fence_mbar_init();
     fence_proxy_async();
     tma_prefetch_desc(&qmap); tma_prefetch_desc(&kcmap); tma_prefetch_desc(&vcmap);
@@ -374,28 +386,43 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         if (per > 1) R = load_req<N>(p, b);
         const int nt = lane_tiles(p, R, z), c = p.Hkv * nt * R.nkt;
         if (f0 >= at + c) { at += c; continue; }
-        Start s;
-        s.R = R;
-        s.z = z;
-        s.b = b;
         const int off = f0 - at, u = off / R.nkt;
-        s.k0 = off - u * R.nkt;
-        s.h = N < 128 ? u : u / nt;
-        s.rt = z + (u - s.h * nt) * p.lanes;
-        s_start = s;
+        Unit v;
+        v.R = R;
+        v.z = z;
+        v.b = b;
+        v.k0 = off - u * R.nkt;
+        v.k1 = min(R.nkt, v.k0 + steps);
+        v.h = N < 128 ? u : u / nt;
+        v.rt = z + (u - v.h * nt) * p.lanes;
+        v.at = f0;
+        s_unit[0] = v;
         break;
       }
     }
   }
+  if (threadIdx.x == 0 && steps == 0) s_unit[0] = Unit{};
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
-  const Waiter W{abort_flag, status, p.wait_ns};
+  const Bound W{abort_flag, p.wait_ns};
   auto colS = [](int s) { return (uint32_t)(s * N); };
   auto colO = [](int s) { return (uint32_t)((2 + s) * N); };
 
+  // a reader's next unit, number lu: copied, and its place given back. The
+  // block's first unit is there from the start
+  auto take = [&](int lu, Unit& u) -> bool {
+    const int s = lu % kUnits;
+    bool ok = lu == 0 || spin(bar(bUF + s), (lu / kUnits) & 1, W, 0x900);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    u = s_unit[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(bUE + s));
+    return u.k1 > 0;
+  };
+
   if (warp < 4) {
     if constexpr (N >= 64) regs_dec<kRegCtl>();
-    Walk<N> w(p, s_start, steps);
     if (warp == 0 || warp == 3) {
       // ---------------------------------- producers: warp 0 of K, warp 3 of V.
       // Each follows its own ring, so a K tile never waits behind a V tile
@@ -411,14 +438,44 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       // The page id is asked for a step ahead of its use
       const int g = lane / NB, x = lane % NB;
       struct Copy { int page, row, h, key; bool fresh, cached, want; };
-      int k = 0;
-      bool open = false;
-      auto fetch = [&](Copy& c) -> bool {
-        if (!open || k >= w.k1) {
-          if (!w.next()) return false;
-          open = true;
-          k = w.k0;
+      bool ok = true;
+      Unit w;
+      int k = 0, lu = 0, left = 0;
+      if (y) {
+        w.k1 = 0;
+      } else {
+        // the K producer also lays out the block's units for the other warps
+        if (lane == 0) mbar_arrive(bar(bUF));
+        w = s_unit[0];                                   // all zero if there is none
+        left = steps - (w.k1 - w.k0);
+        k = w.k0;
+        lu = 1;
+      }
+      auto advance = [&]() -> bool {
+        if (y) {
+          if (!take(lu, w)) return false;
+        } else {
+          const bool more = next_unit<N>(p, w, left);
+          const int sl = lu % kUnits;
+          if (lu >= kUnits) {
+            ok = spin(bar(bUE + sl), ((lu / kUnits) - 1) & 1, W, 0x910);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return false;
+          }
+          if (lane == 0) {
+            if (more) s_unit[sl] = w;
+            else s_unit[sl].k1 = 0;
+            mbar_arrive(bar(bUF + sl));
+          }
+          __syncwarp();
+          if (!more) return false;
         }
+        k = w.k0;
+        ++lu;
+        return true;
+      };
+      auto fetch = [&](Copy& c) -> bool {
+        if (k >= w.k1 && !advance()) return false;
         c.fresh = k >= w.R.kt;
         c.h = w.h;
         c.key = g << (c.fresh ? 3 : box_shift);
@@ -434,11 +491,14 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         ++k;
         return true;
       };
+      // one copy is made while the next one's page id is on its way; the first
+      // round only asks
       Copy cur, nxt;
-      bool ok = true, have = fetch(cur);
+      cur.h = -1;
       int t = 0, issued = 0;
-      while (have) {
-        const bool more = fetch(nxt);
+      for (bool more = true; more;) {
+        more = fetch(nxt);
+        if (cur.h < 0) { cur = nxt; continue; }
         if (cur.cached && cur.want && (cur.page < 0 || cur.page >= p.n_pages)) {
           cur.want = false;
           raise_status(status, kDevIndex, 0x41);
@@ -447,7 +507,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         const uint32_t bytes = each * __popc(__ballot_sync(0xffffffffu, cur.want));
         const int sl = t % depth;
         if (t >= depth) {
-          ok = wait<true>(bar(empty0 + sl), ((t / depth) - 1) & 1, W, 0x100 + y);
+          ok = spin(bar(empty0 + sl), ((t / depth) - 1) & 1, W, 0x100 + y);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
@@ -460,7 +520,6 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         }
         issued = ++t;
         cur = nxt;
-        have = more;
       }
       __syncwarp();
       // drain: every copy has landed before the block exits
@@ -476,117 +535,116 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       constexpr uint32_t idO = idesc_bf16(128, N, true) | (1u << 15);   // A MN-major too
       bool ok = true;
       auto wait_all = [&](int b, uint32_t parity, uint32_t where) -> bool {
-        const bool r = wait<true>(bar(b), parity, W, where);
+        const bool r = spin(bar(b), parity, W, where);
         return __all_sync(0xffffffffu, r);
       };
       if (p.stall) ok = wait_all(bDR, 0, 0x7ff);               // nothing arrives before the drain
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      // the step whose S comes next: its key rows, place in the unit, K slot
-      // and phase, Q slot and phase, S buffer
+      // the next step with its S outstanding (nxt), the step whose S runs or
+      // has run and whose P is awaited (cur), the one behind it (aft). One loop
+      // looks for whatever can go next, each product at one place in the code
       struct Ring { int slot; uint32_t ph; };
       auto turn = [](Ring& r, int depth) { if (++r.slot == depth) { r.slot = 0; r.ph ^= 1; } };
-      struct Step { int kv; bool first, last; } cur, nxt;
-      int k = 0, k1 = 0;
-      auto fetch = [&](Step& s) -> bool {
-        const bool first = k >= k1;
-        if (first) {
-          const bool more = w.next();
-          if (!__all_sync(0xffffffffu, more)) return false;
-          k = __shfl_sync(0xffffffffu, w.k0, 0);
-          k1 = __shfl_sync(0xffffffffu, w.k1, 0);
-        }
-        s.kv = __shfl_sync(0xffffffffu, w.keys(k), 0);
-        s.first = first;
-        s.last = ++k == k1;
-        return true;
-      };
-      Ring rk{0, 0}, rv{0, 0}, rq{QS - 1, 1}, rs{0, 0}, ro{1, 1};
-      // rq, ro: the unit under way (they turn when one begins); rs.slot: S buffer
-      auto s_ready = [&](const Step& s) -> bool {
-        Ring q = rq;
-        if (s.first) turn(q, QS);
-        const bool r = mbar_test_wait(bar(bKF + rk.slot), rk.ph) &&
-                       (!s.first || mbar_test_wait(bar(bQF + q.slot), q.ph));
-        return __all_sync(0xffffffffu, r);
-      };
-      auto issue_s = [&](const Step& s) -> bool {
-        if (s.first) {
-          turn(rq, QS);
-          if (!wait_all(bQF + rq.slot, rq.ph, 0x200)) return false;
-        }
-        if (!wait_all(bKF + rk.slot, rk.ph, 0x300)) return false;
-        tc_fence_after();
-        const uint32_t d = tm + colS(rs.slot);
-        const uint64_t a = sdesc_sw128(smem_u32(sK) + rk.slot * C::kTile, 16, 1024);
-        const uint64_t b = sdesc_sw128(smem_u32(sQ) + rq.slot * C::kQ, 16, 1024);
-        if (elect_uniform()) {
-#pragma unroll
-          for (int x = 0; x < NB; ++x)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_ss(d, a + ((x * C::kBox + ks * 32) >> 4), b + ((x * C::kQBox + ks * 32) >> 4), idS,
-                     (x | ks) != 0);
-          mma_commit(bar(bSF + rs.slot));
-          mma_commit(bar(bKE + rk.slot));
-          if (s.last) mma_commit(bar(bQE + rq.slot));
-        }
-        __syncwarp();
-        turn(rk, KS);
-        turn(rs, 2);
-        return true;
-      };
-      uint32_t pf = 0, units = 0;
-      bool have = ok && fetch(cur);
-      if (have) ok = issue_s(cur);
-      while (ok && have) {
-        const bool more = fetch(nxt);
-        // the next S runs during this step's softmax: look for its operands
-        // and for P in turn (one look that came too early would leave S
-        // behind this step's PV)
-        bool early = !more;
-        for (uint32_t it = 1; !early; ++it) {
-          if (s_ready(nxt)) {
-            if (!(ok = issue_s(nxt))) break;
-            early = true;
-          } else if (__all_sync(0xffffffffu, mbar_test_wait(bar(bPF), pf)) || (it & 4095) == 0) {
-            break;                                             // P is there, or the bounded wait's turn
+      struct Step { int kv; bool first, last; } cur{0, false, false}, aft{0, false, false}, nxt;
+      Ring rk{0, 0}, rv{0, 0}, rq{0, 0}, rs{0, 0}, ro{1, 1};
+      Unit w;
+      int k = 0, k1 = 0, lu = 0, running = 0;            // running: S products without their PV
+      uint32_t pf = 0, units = 0, idle = 0;
+      bool have = false, more = ok;
+      uint64_t t0 = 0;
+      while (true) {
+        if (!have && more) {
+          const bool first = k >= k1;
+          if (first) {
+            more = take(lu++, w);
+            k = __shfl_sync(0xffffffffu, w.k0, 0);
+            k1 = __shfl_sync(0xffffffffu, w.k1, 0);
+          }
+          if (more) {
+            nxt.kv = __shfl_sync(0xffffffffu, w.keys(k), 0);
+            nxt.first = first;
+            nxt.last = ++k == k1;
+            have = true;
           }
         }
-        if (!ok || !(ok = wait_all(bPF, pf, 0x400))) break;
-        if (!(ok = wait_all(bVF + rv.slot, rv.ph, 0x480))) break;
-        if (cur.first) {
-          turn(ro, 2);
-          // O's buffer: the unit before the last must have been read out
-          if (units >= 2 && !(ok = wait_all(bOE + ro.slot, ro.ph ^ 1, 0x500))) break;
-          ++units;
-        }
-        tc_fence_after();
-        // V [key][d] and P [key][row], both MN-major: 8-key groups 1024 B
-        // apart, 64-column boxes kBox apart. D = 64 repeats its one box
-        // (stride 0): rows 64..127 of O^T equal rows 0..63.
-        const uint32_t d = tm + colO(ro.slot), acc = cur.first ? 0u : 1u;
-        const uint64_t a = sdesc_sw128(smem_u32(sV) + rv.slot * C::kTile, D == 128 ? C::kBox : 0, 1024);
-        const uint64_t b = sdesc_sw128(smem_u32(sP), C::kBox, 1024);
-        const int nks = (cur.kv + 15) >> 4;
-        if (elect_uniform()) {
-          mma_ss(d, a, b, idO, acc);
-          if (nks == kKeys / 16) {
+        if (!have && running == 0) break;
+        bool s_go = have && running < 2 && mbar_test_wait(bar(bKF + rk.slot), rk.ph) &&
+                    (!nxt.first || mbar_test_wait(bar(bQF + rq.slot), rq.ph));
+        bool p_go = running > 0 && mbar_test_wait(bar(bPF), pf) &&
+                    mbar_test_wait(bar(bVF + rv.slot), rv.ph) &&
+                    // O's buffer: the unit before the last must have been read out
+                    (!cur.first || units < 2 || mbar_test_wait(bar(bOE + (ro.slot ^ 1)), ro.ph ^ (ro.slot ^ 1)));
+        s_go = __all_sync(0xffffffffu, s_go);
+        p_go = __all_sync(0xffffffffu, p_go);
+        if (s_go) {
+          // S of the next step, during the softmax of the one before
+          tc_fence_after();
+          const uint32_t d = tm + colS(rs.slot);
+          const uint64_t a = sdesc_sw128(smem_u32(sK) + rk.slot * C::kTile, 16, 1024);
+          const uint64_t b = sdesc_sw128(smem_u32(sQ) + rq.slot * C::kQ, 16, 1024);
+          if (elect_uniform()) {
 #pragma unroll
-            for (int ks = 1; ks < kKeys / 16; ++ks) mma_ss(d, a + ks * 128, b + ks * 128, idO, 1u);
-          } else {
+            for (int x = 0; x < NB; ++x)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_ss(d, a + ((x * C::kBox + ks * 32) >> 4), b + ((x * C::kQBox + ks * 32) >> 4), idS,
+                       (x | ks) != 0);
+            mma_commit(bar(bSF + rs.slot));
+            mma_commit(bar(bKE + rk.slot));
+            if (nxt.last) mma_commit(bar(bQE + rq.slot));
+          }
+          __syncwarp();
+          turn(rk, KS);
+          turn(rs, 2);
+          if (nxt.last) turn(rq, QS);
+          (running ? aft : cur) = nxt;
+          ++running;
+          have = false;
+          idle = 0;
+        } else if (p_go) {
+          if (cur.first) {
+            turn(ro, 2);
+            ++units;
+          }
+          tc_fence_after();
+          // V [key][d] and P [key][row], both MN-major: 8-key groups 1024 B
+          // apart, 64-column boxes kBox apart. D = 64 repeats its one box
+          // (stride 0): rows 64..127 of O^T equal rows 0..63.
+          const uint32_t d = tm + colO(ro.slot), acc = cur.first ? 0u : 1u;
+          const uint64_t a = sdesc_sw128(smem_u32(sV) + rv.slot * C::kTile, D == 128 ? C::kBox : 0, 1024);
+          const uint64_t b = sdesc_sw128(smem_u32(sP), C::kBox, 1024);
+          const int nks = (cur.kv + 15) >> 4;
+          if (elect_uniform()) {
+            mma_ss(d, a, b, idO, acc);
+            if (nks == kKeys / 16) {
+#pragma unroll
+              for (int ks = 1; ks < kKeys / 16; ++ks) mma_ss(d, a + ks * 128, b + ks * 128, idO, 1u);
+            } else {
 #pragma unroll 1
-            for (int ks = 1; ks < nks; ++ks) mma_ss(d, a + ks * 128, b + ks * 128, idO, 1u);
+              for (int ks = 1; ks < nks; ++ks) mma_ss(d, a + ks * 128, b + ks * 128, idO, 1u);
+            }
+            mma_commit(bar(bVE + rv.slot));
+            mma_commit(bar(bPV));
+            if (cur.last) mma_commit(bar(bOF + ro.slot));
           }
-          mma_commit(bar(bVE + rv.slot));
-          mma_commit(bar(bPV));
-          if (cur.last) mma_commit(bar(bOF + ro.slot));
+          __syncwarp();
+          turn(rv, VS);
+          pf ^= 1;
+          cur = aft;
+          --running;
+          idle = 0;
+        } else {
+          // bounded: the clock is read every 64 fruitless rounds
+          if ((++idle & 63) == 0) {
+            const uint64_t now = globaltimer();
+            if (idle == 64) t0 = now;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            if (__any_sync(0xffffffffu, now - t0 > p.wait_ns && idle > 64)) {
+              if (lane == 0) *abort_flag = 0x400;
+              break;
+            }
+          }
         }
-        __syncwarp();
-        turn(rv, VS);
-        pf ^= 1;
-        if (!early && !(ok = issue_s(nxt))) break;
-        cur = nxt;
-        have = more;
       }
       // drain: all tensor-core work of the elected lane completes before dealloc
       if (elect_uniform()) mma_commit(bar(bDR));
@@ -596,10 +654,11 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       // ------------------------------------------ Q's copies and the tree's masks
       int lu = 0, q_issued = 0;
       bool ok = true, bad = false;
-      while (ok && w.next()) {
+      Unit w;
+      while (ok && take(lu, w)) {
         const int node0 = w.rt * p.npt, rows = min(p.npt, w.R.n - node0) * p.G;
         const int sq = lu % QS, sm = lu & 1;
-        if (lu >= QS) ok = wait<true>(bar(bQE + sq), ((lu / QS) - 1) & 1, W, 0x600);
+        if (lu >= QS) ok = spin(bar(bQE + sq), ((lu / QS) - 1) & 1, W, 0x600);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         // the rows of npt nodes (nodes behind the request's are columns that
@@ -612,7 +671,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         }
         q_issued = lu + 1;
         __syncwarp();
-        if (lu >= 2) ok = wait<true>(bar(bSE + sm), ((lu >> 1) - 1) & 1, W, 0x610);
+        if (lu >= 2) ok = spin(bar(bSE + sm), ((lu >> 1) - 1) & 1, W, 0x610);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         // parents as the masks use them: the index, or -1 for roots, for
@@ -702,10 +761,16 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     const int cP = (N == 128 ? 0 : c0) / 8;
     float* ref = sRef + sw * N + c0;                     // negated references, if not one for all
     float* al = sAl + sw * N + c0;
-    Walk<N> w(p, s_start, steps);
+    Unit w;
     int t = 0, lu = 0;
     bool ok = true, gone = false;
-    while (!gone && w.next()) {
+    while (!gone) {
+      // Every look at the list is followed by one vote of the warpgroup: here
+      // by a warp that leaves, at the unit's first step by one that goes on
+      if (!take(lu, w)) {
+        bar_any128(id, *abort_flag != 0);
+        break;
+      }
       const int slot = lu & 1, rows = min(p.npt, w.R.n - w.rt * p.npt) * p.G;
       uint64_t l2[NC / 2];
 #pragma unroll
@@ -714,7 +779,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                                                          // (else their scores are shifted, base 0)
       float base = 0.f;
       if (ok && lu >= 2) {
-        ok = wait<true>(bar(bSE + slot), ((lu >> 1) - 1) & 1, W, 0x700);
+        ok = spin(bar(bSE + slot), ((lu >> 1) - 1) & 1, W, 0x700);
         ok = __all_sync(0xffffffffu, ok);
       }
       // the page under this thread's key row, asked for a step ahead (0 where
@@ -736,8 +801,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         const bool seen = node || (r < kv && k * kKeys + r < w.R.L && page >= 0 && page < p.n_pages);
         page = page_of(k + 1);
         if (ok) {
-          ok = wait<true>(bar(bSF + (t & 1)), (t >> 1) & 1, W, 0x710);
-          if (ok && fresh) ok = wait<true>(bar(bMF + slot), (lu >> 1) & 1, W, 0x720);
+          ok = spin(bar(bSF + (t & 1)), (t >> 1) & 1, W, 0x710);
+          if (ok && fresh) ok = spin(bar(bMF + slot), (lu >> 1) & 1, W, 0x720);
           ok = __all_sync(0xffffffffu, ok);
         }
         tc_fence_after();
@@ -754,26 +819,23 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         bool over = !ok || first;
         if (ok && active && !(plain && one && sign > 0.f)) {
 #pragma unroll 1
-          for (int q = 0; q < NC; q += CC) {
+          for (int q = 0; q < NC; q += 8) {
             const int c = c0 + q;
-            const uint32_t bits = (node ? mk[c >> 5] : seen ? 0xffffffffu : 0u) >> (node ? c & 31 : 0);
+            const uint32_t bits = node ? mk[c >> 5] >> (c & 31) : seen ? 0xffu : 0u;
             __syncwarp();
-            uint32_t x[CC];
-            ld_cols<CC>(tS + q, x);
+            uint32_t x[8];
+            ld_cols<8>(tS + q, x);
 #pragma unroll
-            for (int n = 0; n < CC; ++n) {
+            for (int n = 0; n < 8; ++n) {
               const bool hide = !((bits >> n) & 1u);
+              const float b = one ? 0.f : ref[q + n];
               float y = __uint_as_float(x[n]) * sign;
-              if (!one) {
-                // a column that saw nothing so far has no reference to be taken off
-                const float b = ref[q + n];
-                if (b >= -kEmpty) over |= !hide && y > -INFINITY;
-                else y = fmaf(b, inv_sa, y);
-              }
+              // a column that saw nothing so far has no reference to be taken off
+              if (b >= -kEmpty) over |= !hide && y > -INFINITY;
+              else y = fmaf(b, inv_sa, y);
               x[n] = __float_as_uint(hide ? -INFINITY : y);
             }
-            if constexpr (CC == 16) tmem_st16(tS + q, x);
-            else tmem_st32(tS + q, x);
+            tmem_st8(tS + q, x);
           }
           tmem_st_wait();
         }
@@ -873,7 +935,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           }
           __syncwarp();
           if (!first) {
-            ok = wait<true>(bar(bPV), (t - 1) & 1, W, 0x730);    // O holds every step before
+            ok = spin(bar(bPV), (t - 1) & 1, W, 0x730);    // O holds every step before
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             if (ok) {
@@ -911,7 +973,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
               pk[n / 2] = pack_bf16(p0, p1);
             }
             if (q == 0 && t > 0) {                       // P of the step before has been read
-              ok = wait<true>(bar(bPV), (t - 1) & 1, W, 0x740);
+              ok = spin(bar(bPV), (t - 1) & 1, W, 0x740);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
             }
@@ -925,7 +987,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           // leaves its non-finite elements to the epilogue
           if (ok && !plain && wg == 0 && r < kv16 &&
               (!seen || (node && ((sNf[slot * 8 + (j >> 5)] >> (j & 31)) & 1u)))) {
-            ok = wait<true>(bar(bVF + t % VS), (t / VS) & 1, W, 0x750);
+            ok = spin(bar(bVF + t % VS), (t / VS) & 1, W, 0x750);
             if (ok) {
               const uint32_t aV = smem_u32(sV + (t % VS) * C::kTile) + r * 128;
 #pragma unroll 2
@@ -948,7 +1010,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           ok = __all_sync(0xffffffffu, ok);
         } else if (ok && t > 0) {
           // a warp without keys still keeps step with the products
-          ok = wait<true>(bar(bPV), (t - 1) & 1, W, 0x741);
+          ok = spin(bar(bPV), (t - 1) & 1, W, 0x741);
           ok = __all_sync(0xffffffffu, ok);
         }
         fence_proxy_async();
@@ -998,15 +1060,15 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     constexpr int NE = D == 128 ? N : N / 2;            // columns of a warp
     constexpr int CH = NE < 16 ? 8 : 16;
     const int e0 = D == 128 ? 0 : (sw >> 1) * NE;
-    Walk<N> w(p, s_start, steps);
+    Unit w;
     int lu = 0;
     bool ok = true;
-    while (ok && w.next()) {
+    while (ok && take(lu, w)) {
       const int slot = lu & 1;
       const int node0 = w.rt * p.npt, rows = min(p.npt, w.R.n - node0) * p.G;
       const bool whole = w.k0 == 0 && w.k1 == w.R.nkt;
-      ok = wait<true>(bar(bST + slot), (lu >> 1) & 1, W, 0x800) &&
-           wait<true>(bar(bMF + slot), (lu >> 1) & 1, W, 0x801);
+      ok = spin(bar(bST + slot), (lu >> 1) & 1, W, 0x800) &&
+           spin(bar(bMF + slot), (lu >> 1) & 1, W, 0x801);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       // maximum and sum of columns lane, lane + 32, ...
@@ -1053,7 +1115,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       for (int x = 0; x < NL; ++x)
         if (x * 32 + lane < N) inv[x * 32 + lane] = sum[x] != 0.f ? 1.f / sum[x] : 0.f;   // NaN stays
       __syncwarp();
-      ok = wait<true>(bar(bOF + slot), (lu >> 1) & 1, W, 0x810);
+      ok = spin(bar(bOF + slot), (lu >> 1) & 1, W, 0x810);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -1118,6 +1180,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) raise_status(status, kDevTimeout, *abort_flag);
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -1368,7 +1431,7 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     p.G = G; p.npt = npt;
     p.g_magic = (uint32_t)((0xffffffffull + (uint64_t)p.G) / (uint64_t)p.G);
     p.max_nodes = desc->max_nodes;
-    p.lanes = N < 128 ? 1 : std::min((desc->max_nodes + npt - 1) / npt, 4);
+    p.lanes = N < 128 ? 1 : std::min((desc->max_nodes + npt - 1) / npt, 2);
     p.scale_log2 = (desc->scale != 0.f ? desc->scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
     p.cta_status = reinterpret_cast<uint32_t*>(base + ws.status);
     p.meta = reinterpret_cast<int4*>(base + ws.meta);
