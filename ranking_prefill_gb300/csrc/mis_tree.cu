@@ -61,9 +61,15 @@ constexpr float kLn2 = 0.69314718055994530942f;
 template <int D, int N>
 struct TreeCfg {
   static constexpr int kNB = D / 64;             // 64-column boxes of a row
-  static constexpr int kWG = N == 16 ? 1 : 2;    // softmax warpgroups
+  static constexpr int kWG = N == 16 ? 1 : N == 128 ? 4 : 2;    // softmax warpgroups
   static constexpr int kNC = N / kWG;            // columns of a softmax thread
   static constexpr int kThreads = 256 + 128 * kWG;
+  // Register budgets of the warpgroups (N >= 64): their sum is the launch's,
+  // 512 threads x 128 or 768 x 80
+  static constexpr int kRegCtl = N == 128 ? 64 : 80, kRegEpi = N == 128 ? 64 : 80;
+  static constexpr int kRegSoft = N == 128 ? 88 : 176;
+  static_assert(N < 64 || 128 * (kRegCtl + kRegEpi + kWG * kRegSoft) <= kThreads * (N == 128 ? 80 : 128),
+                "register split exceeds the launch allocation");
   static constexpr int kBox = kKeys * 128;       // 64 columns of a 128-key tile
   static constexpr int kTile = kNB * kBox;
   static constexpr int kQ = N * D * 2;
@@ -92,10 +98,6 @@ struct TreeCfg {
   static constexpr int kSmem = kData + 4 * kWords + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
 };
-
-// Register budgets of the warpgroups where N >= 64 needs more than 128 in the
-// softmax: 128 * (80 + 80) + 256 * 176 = 512 * 128, the launch's own.
-constexpr int kRegCtl = 80, kRegEpi = 80, kRegSoft = 176;
 
 struct TreeParams {
   const __nv_bfloat16* v;
@@ -422,7 +424,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   };
 
   if (warp < 4) {
-    if constexpr (N >= 64) regs_dec<kRegCtl>();
+    if constexpr (N >= 64) regs_dec<C::kRegCtl>();
     if (warp == 0 || warp == 3) {
       // ---------------------------------- producers: warp 0 of K, warp 3 of V.
       // Each follows its own ring, so a K tile never waits behind a V tile
@@ -745,7 +747,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     }
   } else if (warp < 4 + 4 * WG) {
     // --------------------------------------------------------------- softmax
-    if constexpr (N >= 64) regs_inc<kRegSoft>();
+    if constexpr (N >= 64) regs_inc<C::kRegSoft>();
     const int wg = (warp - 4) >> 2, sw = warp & 3, r = sw * 32 + lane;
     const int c0 = wg * NC, id = 1 + wg;
     const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
@@ -755,10 +757,10 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     const uint64_t sax2 = f2_pack(__float_as_uint(sa), __float_as_uint(sa));
     // columns in registers at a time: two pieces (N = 128) are read from
     // tensor memory twice, once for the maximum and once for P
-    constexpr int CC = NC > 32 ? 32 : NC;
+    constexpr int CC = N == 128 ? 16 : NC;
     // this thread's row of P: chunk c of its columns
-    const uint32_t aP = smem_u32(sP) + (N == 128 ? wg * C::kBox : 0) + r * 128;
-    const int cP = (N == 128 ? 0 : c0) / 8;
+    const uint32_t aP = smem_u32(sP) + (c0 >> 6) * C::kBox + r * 128;
+    const int cP = (c0 & 63) / 8;
     float* ref = sRef + sw * N + c0;                     // negated references, if not one for all
     float* al = sAl + sw * N + c0;
     Unit w;
@@ -1051,7 +1053,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    if constexpr (N >= 64) regs_dec<kRegEpi>();
+    if constexpr (N >= 64) regs_dec<C::kRegEpi>();
     const int sw = warp & 3;
     const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
     // D = 128: a lane is element d, all columns. D = 64: the two copies of
