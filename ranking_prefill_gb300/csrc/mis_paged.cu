@@ -25,6 +25,11 @@ using namespace dev;
 
 constexpr int kPlanThreads = 1024;
 constexpr int kFillThreads = 256;
+constexpr int kFillRows = 4;            // consecutive rows of a thread
+constexpr int kCuShared = 2048;         // requests whose row starts a fill block keeps
+// Rows up to which the planning block fills the maps itself: a second launch
+// costs the host 3.2 us and the GPU about 2; eight rows a thread cost less
+constexpr int kFillInPlan = 8 * kPlanThreads;
 
 // What the rows of a request need to find their slots.
 struct ExtendRec {
@@ -35,7 +40,7 @@ struct ExtendRec {
 };
 
 struct ExtendParams {
-  int32_t B, T, page_size, n_pages, max_pages, n_free;
+  int32_t B, T, page_size, page_shift, n_pages, max_pages, n_free;
   const int32_t* new_len;
   const int32_t* cache_len;
   int32_t* cache_len_out;
@@ -49,62 +54,95 @@ struct ExtendParams {
   int32_t* position_ids;
   uint32_t* status;
   ExtendRec* rec;
+  int32_t vec;       // slot_map and position_ids take 16-byte stores
 };
 
-// Inclusive sum over the block's threads; *total = the sum of all.
-__device__ int64_t block_sum(int64_t x, int64_t* total, int64_t* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive sums of two values over the block's threads, and their totals.
+struct Pair {
+  int64_t x, y;
+};
+__device__ __forceinline__ Pair block_sum(Pair v, Pair* total, Pair* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int64_t x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
+    if (lane >= o) { v.x += x; v.y += y; }
   }
   __syncthreads();                       // the previous call's readers are done
-  if (lane == 31) warp_sums[warp] = x;
+  if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    int64_t s = warp_sums[lane];
+  // every warp adds up the warps' sums for itself
+  Pair w = lane < warps ? warp_sums[lane] : Pair{0, 0};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sums[lane] = s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, w.x, o), y = __shfl_up_sync(0xffffffffu, w.y, o);
+    if (lane >= o) { w.x += x; w.y += y; }
   }
-  __syncthreads();
-  *total = warp_sums[31];
-  return x + (warp ? warp_sums[warp - 1] : 0);
+  total->x = __shfl_sync(0xffffffffu, w.x, 31);
+  total->y = __shfl_sync(0xffffffffu, w.y, 31);
+  const int64_t bx = __shfl_sync(0xffffffffu, w.x, max(warp - 1, 0));
+  const int64_t by = __shfl_sync(0xffffffffu, w.y, max(warp - 1, 0));
+  return warp ? Pair{v.x + bx, v.y + by} : v;
 }
 
-// Slot and position of row t (and the table entry of a page that starts there).
-__device__ __forceinline__ void fill_row(const ExtendParams& p, int t, int total) {
-  int slot = -1, pos = 0;
+// Slots and positions of rows t .. t + kFillRows - 1 (and the table entries of
+// pages that start there). cu: cu_new, wherever it is read from.
+__device__ __forceinline__ void fill_rows(const ExtendParams& p, const int32_t* cu, int t, int total) {
+  int slot[kFillRows], pos[kFillRows];
+  int b = 0;
   if (t < total) {
-    int lo = 0, hi = p.B - 1;            // first b with cu_new[b + 1] > t
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (p.cu_new[mid + 1] > t) hi = mid; else lo = mid + 1;
+    int hi = p.B - 1;                    // first b with cu[b + 1] > t
+    while (b < hi) {
+      const int mid = (b + hi) >> 1;
+      if (cu[mid + 1] > t) hi = mid; else b = mid + 1;
     }
-    const ExtendRec r = p.rec[lo];
-    pos = r.len + (t - p.cu_new[lo]);
-    const int col = pos / p.page_size, off = pos % p.page_size;
-    int32_t* entry = p.table + (int64_t)lo * p.table_stride + col;
-    const bool fresh = col >= r.have;
-    int page = fresh ? p.free_pages[r.first + (col - r.have)] : *entry;
-    if (page < 0 || page >= p.n_pages) {
-      page = -1;
-      raise_status(p.status, kDevIndex, 0x21);
-    }
-    if (fresh && off == 0) *entry = page;
-    if (page >= 0) slot = page * p.page_size + off;
   }
-  p.slot_map[t] = slot;
-  if (p.position_ids) p.position_ids[t] = pos;
+  ExtendRec r{0, 0, 0, 0};
+  int start = 0, end = -1, col0 = -1, page = -1;
+#pragma unroll
+  for (int e = 0; e < kFillRows; ++e) {
+    slot[e] = -1;
+    pos[e] = 0;
+    if (t + e >= total) continue;
+    if (t + e >= end) {
+      while (cu[b + 1] <= t + e) ++b;
+      r = p.rec[b];
+      start = cu[b];
+      end = cu[b + 1];
+      col0 = -1;
+    }
+    pos[e] = r.len + (t + e - start);
+    const int col = pos[e] >> p.page_shift, off = pos[e] & ((1 << p.page_shift) - 1);
+    if (col != col0) {
+      int32_t* entry = p.table + (int64_t)b * p.table_stride + col;
+      const bool fresh = col >= r.have;
+      page = fresh ? p.free_pages[r.first + (col - r.have)] : *entry;
+      if (page < 0 || page >= p.n_pages) {
+        page = -1;
+        raise_status(p.status, kDevIndex, 0x21);
+      }
+      if (fresh && off == 0) *entry = page;
+      col0 = col;
+    }
+    if (page >= 0) slot[e] = (page << p.page_shift) + off;
+  }
+  if (p.vec && t + kFillRows <= p.T) {
+    *reinterpret_cast<int4*>(p.slot_map + t) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    if (p.position_ids)
+      *reinterpret_cast<int4*>(p.position_ids + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < kFillRows; ++e)
+    if (t + e < p.T) {
+      p.slot_map[t + e] = slot[e];
+      if (p.position_ids) p.position_ids[t + e] = pos[e];
+    }
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
 mis_paged_extend_kernel(const ExtendParams p) {
-  __shared__ int64_t warp_sums[32];
+  __shared__ Pair warp_sums[32];
   __shared__ int s_head;
   __shared__ uint32_t s_bits, s_taken;
   griddep_launch_dependents();
@@ -120,7 +158,7 @@ mis_paged_extend_kernel(const ExtendParams p) {
   const int64_t cap = (int64_t)p.max_pages * p.page_size;
   uint32_t bits = head_ok ? 0u : kDevIndex;
   int64_t pages0 = 0, rows0 = 0, cu0 = 0, taken = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < p.B; b0 += (int)blockDim.x) {
     const int b = b0 + threadIdx.x;
     int64_t len = 0, n = 0, need = 0;
     int have = 0;
@@ -135,14 +173,19 @@ mis_paged_extend_kernel(const ExtendParams p) {
         need = (len + n + p.page_size - 1) / p.page_size - have;
       }
     }
-    int64_t pages, rows, granted;
-    const int64_t pend = pages0 + block_sum(need, &pages, warp_sums);
-    const int64_t rend = rows0 + block_sum(n, &rows, warp_sums);
+    Pair sum;
+    const Pair end = block_sum(Pair{need, n}, &sum, warp_sums);
+    const int64_t pend = pages0 + end.x, rend = rows0 + end.y;
     bool ok = true;
     if (need > 0 && pend > avail) { bits |= kDevPages; ok = false; }
     if (n > 0 && rend > p.T) { bits |= kDevIndex; ok = false; }
     const int64_t g = ok ? n : 0;
-    const int64_t gend = cu0 + block_sum(g, &granted, warp_sums);
+    int64_t gend = cu0 + end.y, granted = sum.y;
+    if (__syncthreads_or(!ok)) {           // rows of refused requests close up
+      Pair gsum;
+      gend = cu0 + block_sum(Pair{g, 0}, &gsum, warp_sums).x;
+      granted = gsum.x;
+    }
     if (ok && need > 0 && pend > taken) taken = pend;
     if (b < p.B) {
       ExtendRec r;
@@ -154,8 +197,8 @@ mis_paged_extend_kernel(const ExtendParams p) {
       p.cu_new[b + 1] = (int32_t)gend;
       p.cache_len_out[b] = (int32_t)(len + g);
     }
-    pages0 += pages;
-    rows0 += rows;
+    pages0 += sum.x;
+    rows0 += sum.y;
     cu0 += granted;
   }
   // granted requests that took pages are a prefix of those that need any, so
@@ -169,15 +212,25 @@ mis_paged_extend_kernel(const ExtendParams p) {
     p.status[0] = s_bits;
     p.status[1] = s_bits ? 0x20u : 0u;
   }
+  if (p.T <= kFillInPlan) {
+    __syncthreads();                     // cu_new, records and status are written
+    for (int t = threadIdx.x * kFillRows; t < p.T; t += (int)blockDim.x * kFillRows)
+      fill_rows(p, p.cu_new, t, (int)cu0);
+  }
 }
 
 __global__ void __launch_bounds__(kFillThreads)
 mis_paged_fill_kernel(const ExtendParams p) {
   griddep_wait();
-  const int total = p.cu_new[p.B];
-  for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < p.T;
-       t += (int64_t)gridDim.x * blockDim.x)
-    fill_row(p, (int)t, total);
+  __shared__ int32_t s_cu[kCuShared + 1];
+  const int32_t* cu = p.cu_new;
+  if (p.B <= kCuShared) {
+    for (int b = threadIdx.x; b <= p.B; b += blockDim.x) s_cu[b] = p.cu_new[b];
+    __syncthreads();
+    cu = s_cu;
+  }
+  const int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * kFillRows;
+  if (t < p.T) fill_rows(p, cu, (int)t, cu[p.B]);
 }
 
 // ------------------------------------------------------------------- write
@@ -192,6 +245,7 @@ struct WriteParams {
   const int32_t* slot;
   const int32_t* pos;                // or null: no rotation
   int32_t n, T, Hkv;
+  int32_t hpt;                       // heads of a thread
   int32_t page_shift;
   int64_t n_slots;
   uint32_t* status;
@@ -220,20 +274,37 @@ __device__ __forceinline__ void sincos_turn(int32_t p, uint64_t f, float& sn, fl
   asm("cos.approx.f32 %0, %1;" : "=f"(cs) : "f"(x));
 }
 
+// A source row's 16 bytes, read once.
+__device__ __forceinline__ uint4 ld_once(const __nv_bfloat16* ptr) {
+  uint4 u;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(ptr));
+  return u;
+}
+
 template <int D>
 __global__ void __launch_bounds__(256)
 mis_paged_write_kernel(const WriteParams p) {
   constexpr int HALF = D / 2, NC = HALF / 8;
   griddep_wait();
   if (blockIdx.x == 0) {
-    // one block looks over every index and writes the status word
+    // one block looks over every index and writes the status word: 16 loads in
+    // flight a thread, so that it is through long before the copies are
+    // (128K rows: 330 us when it took them one by one)
+    constexpr int U = 16;
+    const int step = U * (int)blockDim.x;
     uint32_t bad = 0;
-    for (int i = threadIdx.x; i < p.n; i += blockDim.x) {
-      const int s = p.slot[i];
-      if (s < 0) continue;
-      if (s >= p.n_slots) bad = 1;
-      const int r = p.src ? p.src[i] : i;
-      if (r < 0 || r >= p.T) bad = 1;
+    for (int64_t i0 = threadIdx.x; i0 < p.n; i0 += step) {
+      int s[U], r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = i0 + u * (int)blockDim.x;
+        s[u] = i < p.n ? p.slot[i] : -1;
+        r[u] = p.src && i < p.n ? p.src[i] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (s[u] >= 0 && (s[u] >= p.n_slots || r[u] < 0 || r[u] >= p.T)) bad = 1;
     }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) {
@@ -245,47 +316,75 @@ mis_paged_write_kernel(const WriteParams p) {
   const int64_t gid = (int64_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x;
   const int c = (int)(gid % NC);
   const int64_t cell = gid / NC;
-  const int h = (int)(cell % p.Hkv);
-  const int64_t i = cell / p.Hkv;
+  const int groups = (p.Hkv + p.hpt - 1) / p.hpt;
+  const int grp = (int)(cell % groups);
+  const int64_t i = cell / groups;
   if (i >= p.n) return;
   const int s = p.slot[i];
   const int r = p.src ? p.src[i] : (int)i;
   if (s < 0 || s >= p.n_slots || r < 0 || r >= p.T) return;
+  const int h0 = grp * p.hpt, h1 = min(h0 + p.hpt, p.Hkv);
   const int64_t at = (int64_t)(s >> p.page_shift) * p.page_stride +
-                     (int64_t)(s & ((1 << p.page_shift) - 1)) * p.row_stride +
-                     (int64_t)h * p.head_stride + c * 8;
-  const __nv_bfloat16* ks = p.k + (int64_t)r * p.ks + (int64_t)h * D + c * 8;
-  const __nv_bfloat16* vs = p.v + (int64_t)r * p.vs + (int64_t)h * D + c * 8;
-  uint4 a = *reinterpret_cast<const uint4*>(ks), b = *reinterpret_cast<const uint4*>(ks + HALF);
-  const uint4 va = *reinterpret_cast<const uint4*>(vs), vb = *reinterpret_cast<const uint4*>(vs + HALF);
+                     (int64_t)(s & ((1 << p.page_shift) - 1)) * p.row_stride + c * 8;
+  const __nv_bfloat16* ks = p.k + (int64_t)r * p.ks + c * 8;
+  const __nv_bfloat16* vs = p.v + (int64_t)r * p.vs + c * 8;
+  float sn[8], cs[8];
   if (p.pos) {
     const int pos = p.pos[i];
-    float x[8], y[8];
-    unpack8(a, x);
-    unpack8(b, y);
-    uint32_t wa[4], wb[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float s0, c0, s1, c1;
-      sincos_turn(pos, p.turn[c * 8 + 2 * e], s0, c0);
-      sincos_turn(pos, p.turn[c * 8 + 2 * e + 1], s1, c1);
-      const float x0 = x[2 * e], x1 = x[2 * e + 1], y0 = y[2 * e], y1 = y[2 * e + 1];
-      wa[e] = pack_bf16(x0 * c0 - y0 * s0, x1 * c1 - y1 * s1);
-      wb[e] = pack_bf16(y0 * c0 + x0 * s0, y1 * c1 + x1 * s1);
-    }
-    a = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-    b = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+    for (int e = 0; e < 8; ++e) sincos_turn(pos, p.turn[c * 8 + e], sn[e], cs[e]);
   }
-  *reinterpret_cast<uint4*>(p.kc + at) = a;
-  *reinterpret_cast<uint4*>(p.kc + at + HALF) = b;
-  *reinterpret_cast<uint4*>(p.vc + at) = va;
-  *reinterpret_cast<uint4*>(p.vc + at + HALF) = vb;
+#pragma unroll 2
+  for (int h = h0; h < h1; ++h) {
+    const int64_t from = (int64_t)h * D, to = at + (int64_t)h * p.head_stride;
+    uint4 a = ld_once(ks + from), b = ld_once(ks + from + HALF);
+    const uint4 va = ld_once(vs + from), vb = ld_once(vs + from + HALF);
+    if (p.pos) {
+      float x[8], y[8];
+      unpack8(a, x);
+      unpack8(b, y);
+      uint32_t wa[4], wb[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = x[2 * e], x1 = x[2 * e + 1], y0 = y[2 * e], y1 = y[2 * e + 1];
+        const float s0 = sn[2 * e], s1 = sn[2 * e + 1], c0 = cs[2 * e], c1 = cs[2 * e + 1];
+        wa[e] = pack_bf16(x0 * c0 - y0 * s0, x1 * c1 - y1 * s1);
+        wb[e] = pack_bf16(y0 * c0 + x0 * s0, y1 * c1 + x1 * s1);
+      }
+      a = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+      b = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+    }
+    *reinterpret_cast<uint4*>(p.kc + to) = a;
+    *reinterpret_cast<uint4*>(p.kc + to + HALF) = b;
+    *reinterpret_cast<uint4*>(p.vc + to) = va;
+    *reinterpret_cast<uint4*>(p.vc + to + HALF) = vb;
+  }
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 bool page_size_ok(int32_t ps) {
   return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256;
+}
+
+// The frequencies of a (base, D), kept from call to call: 64 powers cost the
+// host 3 us.
+void fill_turns(double base, int D, uint64_t* turn) {
+  struct Kept {
+    double base = 0;
+    int D = 0;
+    uint64_t turn[64];
+  };
+  static thread_local Kept kept;
+  if (kept.base != base || kept.D != D) {
+    for (int i = 0; i < 64; ++i)
+      kept.turn[i] = i < D / 2 ? (uint64_t)(std::pow(base, -2.0 * i / D) / 6.283185307179586476925 *
+                                            18446744073709551616.0)
+                               : 0;
+    kept.base = base;
+    kept.D = D;
+  }
+  for (int i = 0; i < 64; ++i) turn[i] = kept.turn[i];
 }
 
 mis_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MIS_OK : MIS_ERR_CUDA; }
@@ -328,6 +427,7 @@ extern "C" mis_status_t mis_paged_extend(
     const int32_t* free_head, int32_t* free_head_out, int32_t* cu_new, int32_t* slot_map,
     int32_t* position_ids, void* workspace, size_t ws_bytes, void* stream) {
   if (B < 1 || T < 0 || n_pages < 1 || max_pages < 1 || n_free < 0) return MIS_ERR_INVALID_ARG;
+  if (T > 0x7ffffff0) return MIS_ERR_SHAPE;
   if (!page_size_ok(page_size)) return MIS_ERR_UNSUPPORTED;
   if ((int64_t)n_pages * page_size > 0x7fffffff || (int64_t)max_pages * page_size > 0x7fffffff ||
       block_table_stride < max_pages)
@@ -343,6 +443,8 @@ extern "C" mis_status_t mis_paged_extend(
   if (!workspace || !aligned(workspace, 256) || ws_bytes < mis_paged_extend_workspace_size(B))
     return MIS_ERR_WORKSPACE;
   ExtendParams p;
+  p.page_shift = 31 - __builtin_clz((unsigned)page_size);
+  p.vec = aligned(slot_map, 16) && aligned(position_ids, 16);
   p.B = B; p.T = T; p.page_size = page_size; p.n_pages = n_pages; p.max_pages = max_pages;
   p.n_free = n_free;
   p.new_len = new_len; p.cache_len = cache_len; p.cache_len_out = cache_len_out;
@@ -354,10 +456,10 @@ extern "C" mis_status_t mis_paged_extend(
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   try {
     mis_status_t r = cuda_status(
-        launch_pdl(mis_paged_extend_kernel, dim3(1), dim3(kPlanThreads), 0, st, p));
-    if (r != MIS_OK || T == 0) return r;
-    const int64_t blocks = std::min<int64_t>(((int64_t)T + kFillThreads - 1) / kFillThreads,
-                                             8 * (int64_t)num_sms());
+        launch_pdl(mis_paged_extend_kernel, dim3(1),
+                   dim3(B <= 256 && (T <= 1024 || T > kFillInPlan) ? 256 : kPlanThreads), 0, st, p));
+    if (r != MIS_OK || T <= kFillInPlan) return r;
+    const int64_t blocks = ((int64_t)T + kFillThreads * kFillRows - 1) / (kFillThreads * kFillRows);
     return cuda_status(launch_pdl(mis_paged_fill_kernel, dim3((unsigned)blocks),
                                   dim3(kFillThreads), 0, st, p));
   } catch (...) {
@@ -402,12 +504,13 @@ extern "C" mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const v
   p.n_slots = (int64_t)cache->n_pages * cache->page_size;
   p.status = static_cast<uint32_t*>(workspace);
   const int D = cache->D;
-  for (int i = 0; i < 64; ++i)
-    p.turn[i] = (position_ids && i < D / 2)
-                    ? (uint64_t)(std::pow(rope_base, -2.0 * i / D) / 6.283185307179586476925 *
-                                 18446744073709551616.0)
-                    : 0;
-  const int64_t threads = (int64_t)n * cache->Hkv * (D / 16);
+  if (position_ids) fill_turns(rope_base, D, p.turn);
+  // an angle serves all heads of a thread; a row's heads are split over
+  // threads only while its chunks alone would leave SMs idle
+  const int64_t cells = (int64_t)n * (D / 16), want = 1024 * (int64_t)num_sms();
+  const int64_t split = std::max<int64_t>(1, std::min<int64_t>(cache->Hkv, want / cells));
+  p.hpt = (int32_t)((cache->Hkv + split - 1) / split);
+  const int64_t threads = cells * ((cache->Hkv + p.hpt - 1) / p.hpt);
   const int64_t blocks = 1 + (threads + 255) / 256;
   if (blocks > 0x7fffffff) return MIS_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -420,3 +523,5 @@ extern "C" mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const v
     return MIS_ERR_CUDA;
   }
 }
+
+
