@@ -582,59 +582,60 @@ def _require(ok, status: int, where: str):
         raise MisError(status, where)
 
 
+_torch = None
+
+
 def _here(stream):
-    """(current device, stream address). One look at the runtime per call: the
-    checks below compare every tensor's device with it."""
-    import torch
-    if not torch.cuda.is_initialized() and not torch.cuda.is_available():
+    """(current device, stream address), one look at the runtime per call: the
+    checks below compare every tensor's device with it. (These calls run once
+    a layer and step, so they are kept short.)"""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    if not _torch.cuda.is_initialized() and not _torch.cuda.is_available():
         return -1, None
-    dev = torch.cuda.current_device()
+    dev = _torch.cuda.current_device()
     if stream is None:
-        return dev, torch._C._cuda_getCurrentRawStream(dev)
+        return dev, _torch._C._cuda_getCurrentRawStream(dev)
     return dev, stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _vectors(where: str, dev: int, *pairs):
-    """(tensor or None, n): contiguous int32 vectors of at least n elements on `dev`."""
-    import torch
-    i32 = torch.int32
+    """(tensor or None, n): contiguous int32 of at least n elements on `dev`."""
+    i32 = _torch.int32
     for t, n in pairs:
-        if t is not None:
-            if t.dtype is not i32 or t.get_device() != dev:
-                raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
-            if t.dim() != 1 or t.numel() < n or not t.is_contiguous():
-                raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
-
-
-def _rows(where: str, dev: int, T: int, heads: int, D: int, *tensors):
-    """Row strides of bf16 [>= T, heads, D] tensors on `dev`, heads packed inside a row."""
-    import torch
-    bf16 = torch.bfloat16
-    out = []
-    for t in tensors:
-        if t.dtype is not bf16 or t.get_device() != dev:
+        if t is None:
+            continue
+        if t.dtype is not i32 or t.get_device() != dev:
             raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
-        st, sh = t.stride(), t.shape
-        if (len(sh) != 3 or sh[0] < T or sh[1] != heads or sh[2] != D or st[2] != 1 or
-                (heads > 1 and st[1] != D)):
+        if t.numel() < n or not t.is_contiguous():
             raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
-        out.append(st[0] if sh[0] > 1 else heads * D)
-    return out
 
 
-def _table(where: str, dev: int, t, B: int) -> int:
-    """Row stride of an int32 [>= B, pages] table on `dev`."""
-    import torch
-    if t.dtype is not torch.int32 or t.get_device() != dev:
+def _rows(where: str, dev: int, T: int, heads: int, D: int, t) -> int:
+    """Row stride of bf16 [>= T, heads, D] on `dev`, heads packed inside a row."""
+    if t.dtype is not _torch.bfloat16 or t.get_device() != dev:
         raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
-    if t.dim() != 2 or t.shape[0] < B or (t.shape[1] > 1 and t.stride(1) != 1):
+    st, sh = t.stride(), t.shape
+    if (len(sh) != 3 or sh[0] < T or sh[1] != heads or sh[2] != D or st[2] != 1 or
+            (heads > 1 and st[1] != D)):
         raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    return st[0] if sh[0] > 1 else heads * D
+
+
+def _table(where: str, dev: int, t, B: int):
+    """(columns, row stride) of an int32 [>= B, pages] table on `dev`."""
+    if t.dtype is not _torch.int32 or t.get_device() != dev:
+        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    sh, st = t.shape, t.stride()
+    if len(sh) != 2 or sh[0] < B or (sh[1] > 1 and st[1] != 1):
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+    return sh[1], st[0] if sh[0] > 1 else max(sh[1], 1)
 
 
 def _workspace(where: str, dev: int, t) -> int:
-    import torch
-    if t.dtype is not torch.uint8 or t.get_device() != dev or not t.is_contiguous():
+    if t.dtype is not _torch.uint8 or t.get_device() != dev or not t.is_contiguous():
         raise MisError(MIS_ERR_WORKSPACE, where)  # noqa: F821
     return t.numel()
 
@@ -693,12 +694,11 @@ def mis_paged_extend(new_len, cache_len, cache_len_out, block_table, free_pages,
     where = "mis_paged_extend"
     dev, st = _here(stream)
     B, T, n_free = new_len.numel(), slot_map.numel(), free_pages.numel()
-    _vectors(where, dev, (new_len, B), (cache_len, B), (cache_len_out, B), (cu_new, B + 1), (slot_map, T),
-             (position_ids, T), (free_pages, n_free), (free_head, 1), (free_head_out, 1))
-    stride = _table(where, dev, block_table, B)
+    _vectors(where, dev, (new_len, 0), (cache_len, B), (cache_len_out, B), (cu_new, B + 1), (slot_map, 0),
+             (position_ids, T), (free_pages, 0), (free_head, 1), (free_head_out, 1))
+    cols, stride = _table(where, dev, block_table, B)
     st = L.mis_paged_extend(B, T, page_size, n_pages, new_len.data_ptr(), cache_len.data_ptr(),
-                            cache_len_out.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-                            stride, free_pages.data_ptr(), n_free, free_head.data_ptr(),
+                            cache_len_out.data_ptr(), block_table.data_ptr(), cols, stride, free_pages.data_ptr(), n_free, free_head.data_ptr(),
                             free_head_out.data_ptr(), cu_new.data_ptr(), slot_map.data_ptr(),
                             None if position_ids is None else position_ids.data_ptr(),
                             workspace.data_ptr(), _workspace(where, dev, workspace), st)
@@ -720,8 +720,9 @@ def mis_paged_write_kv(cache: PagedCache, k, v, slot_map, workspace, position_id
     n = slot_map.numel()
     _require(cache.device == dev, MIS_ERR_INVALID_ARG, where)  # noqa: F821
     T = k.shape[0]
-    ks, vs = _rows(where, dev, T, cache.Hkv, cache.D, k, v)
-    _vectors(where, dev, (slot_map, n), (position_ids, n), (src_rows, n))
+    ks = _rows(where, dev, T, cache.Hkv, cache.D, k)
+    vs = _rows(where, dev, T, cache.Hkv, cache.D, v)
+    _vectors(where, dev, (slot_map, 0), (position_ids, n), (src_rows, n))
     st = L.mis_paged_write_kv(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs, T,
                               None if src_rows is None else src_rows.data_ptr(), slot_map.data_ptr(), n,
                               None if position_ids is None else position_ids.data_ptr(), base,
@@ -741,18 +742,17 @@ def mis_tree_attention_fwd(desc: TreeDesc, q, k, v, o, lse, block_table, cache_l
     dev, st = _here(stream)
     c, T, B, Hq = desc.cache, desc.T, desc.B, desc.Hq
     _require(c.device == dev, MIS_ERR_INVALID_ARG, where)  # noqa: F821
-    qs, os_ = _rows(where, dev, T, Hq, c.D, q, o)
-    ks, vs = _rows(where, dev, T, c.Hkv, c.D, k, v)
+    H, D = c.Hkv, c.D
+    qs, os_ = _rows(where, dev, T, Hq, D, q), _rows(where, dev, T, Hq, D, o)
+    ks, vs = _rows(where, dev, T, H, D, k), _rows(where, dev, T, H, D, v)
     if lse is not None:
-        import torch
-        _require(lse.dtype is torch.float32 and lse.get_device() == dev, MIS_ERR_INVALID_ARG, where)  # noqa: F821
+        _require(lse.dtype is _torch.float32 and lse.get_device() == dev, MIS_ERR_INVALID_ARG, where)  # noqa: F821
         _require(lse.shape == (Hq, T) and lse.is_contiguous(), MIS_ERR_SHAPE, where)  # noqa: F821
         lse = lse.data_ptr()
     _vectors(where, dev, (cache_len, B), (cu_nodes, B + 1), (parents, T))
-    stride = _table(where, dev, block_table, B)
+    cols, stride = _table(where, dev, block_table, B)
     st = L.mis_tree_attention_fwd(desc.ref, c.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                  lse, qs, ks, vs, os_, block_table.data_ptr(), block_table.shape[1],
-                                  stride, cache_len.data_ptr(), cu_nodes.data_ptr(),
+                                  lse, qs, ks, vs, os_, block_table.data_ptr(), cols, stride, cache_len.data_ptr(), cu_nodes.data_ptr(),
                                   None if parents is None else parents.data_ptr(), workspace.data_ptr(),
                                   _workspace(where, dev, workspace), st)
     if st:
