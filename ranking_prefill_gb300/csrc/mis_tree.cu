@@ -235,6 +235,35 @@ __device__ __forceinline__ float warp_min(float x) {
   return r;
 }
 
+// Sums (or maxima) over the warp of NV columns, of which every lane brings one
+// value each: halve the columns lane bit by lane bit, then fold the lanes that
+// are left. Returns the first of the NV / 32 (at least one) columns that end up
+// in v[0], v[1], ... of this lane. (One redux a column took three times as long.)
+template <int NV, bool kMax>
+__device__ __forceinline__ int fold_cols(float* v, int lane) {
+  int cnt = NV, col = 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    if (cnt > 1) {
+      const int hf = cnt / 2;
+      const bool up = (lane & o) != 0;
+#pragma unroll
+      for (int n = 0; n < NV / 2; ++n) {
+        if (n >= hf) break;
+        const float give = up ? v[n] : v[n + hf], keep = up ? v[n + hf] : v[n];
+        const float got = __shfl_xor_sync(0xffffffffu, give, o);
+        v[n] = kMax ? fmaxf(keep, got) : keep + got;
+      }
+      col += up ? hf : 0;
+      cnt = hf;
+    } else {
+      const float got = __shfl_xor_sync(0xffffffffu, v[0], o);
+      v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+    }
+  }
+  return col;
+}
+
 template <int NC>
 __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t* r) {
   if constexpr (NC == 8) {
@@ -821,23 +850,27 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         bool over = !ok || first;
         if (ok && active && !(plain && one && sign > 0.f)) {
 #pragma unroll 1
-          for (int q = 0; q < NC; q += 8) {
+          for (int q = 0; q < NC; q += 16) {
             const int c = c0 + q;
-            const uint32_t bits = node ? mk[c >> 5] >> (c & 31) : seen ? 0xffu : 0u;
+            const uint32_t bits = node ? mk[c >> 5] >> (c & 31) : seen ? 0xffffu : 0u;
             __syncwarp();
-            uint32_t x[8];
-            ld_cols<8>(tS + q, x);
+            uint32_t x[16];
+            ld_cols<16>(tS + q, x);
+            if (!(one && sign > 0.f)) {
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              const bool hide = !((bits >> n) & 1u);
-              const float b = one ? 0.f : ref[q + n];
-              float y = __uint_as_float(x[n]) * sign;
-              // a column that saw nothing so far has no reference to be taken off
-              if (b >= -kEmpty) over |= !hide && y > -INFINITY;
-              else y = fmaf(b, inv_sa, y);
-              x[n] = __float_as_uint(hide ? -INFINITY : y);
+              for (int n = 0; n < 16; ++n) {
+                const float b = one ? 0.f : ref[q + n];
+                float y = __uint_as_float(x[n]) * sign;
+                // a column that saw nothing so far has no reference to be taken off
+                if (b >= -kEmpty) over |= ((bits >> n) & 1u) && y > -INFINITY;
+                else y = fmaf(b, inv_sa, y);
+                x[n] = __float_as_uint(y);
+              }
             }
-            tmem_st8(tS + q, x);
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+              if (!((bits >> n) & 1u)) x[n] = 0xff800000u;
+            tmem_st16(tS + q, x);
           }
           tmem_st_wait();
         }
@@ -868,19 +901,19 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           if (bar_any128(id, !ok)) { gone = true; break; }
           // the step's maximum of every column over this warp's keys
 #pragma unroll 1
-          for (int q = 0; q < NC; q += 8) {
-            float mine = -INFINITY;
-            if (active) {
-              uint32_t x[8];
-              ld_cols<8>(tS + q, x);
+          for (int q = 0; q < NC; q += CC) {
+            float v[CC];
 #pragma unroll
-              for (int n = 0; n < 8; ++n) {
-                const float y = warp_max(__uint_as_float(x[n])) * sa;
-                if (lane == n) mine = y;
-              }
-              if (!one && lane < 8 && ref[q + lane] < -kEmpty) mine -= ref[q + lane];
+            for (int n = 0; n < CC; ++n) v[n] = -INFINITY;
+            if (active) {
+              ld_cols<CC>(tS + q, s);
+#pragma unroll
+              for (int n = 0; n < CC; ++n) v[n] = __uint_as_float(s[n]);
             }
-            if (lane < 8) sMax[sw * N + c0 + q + lane] = mine;
+            const int n = q + fold_cols<CC, true>(v, lane);
+            float mine = v[0] * sa;
+            if (!one && ref[n] < -kEmpty) mine -= ref[n];
+            sMax[sw * N + c0 + n] = mine;
           }
           bar_sync128(id);
           // every warp draws the same conclusion from the four warps' maxima
@@ -1025,24 +1058,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       float l[NC];
 #pragma unroll
       for (int n = 0; n < NC / 2; ++n) f2_unpack(l2[n], l[2 * n], l[2 * n + 1]);
-      int cnt = NC, col = 0;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        if (cnt > 1) {
-          const int hf = cnt / 2;
-          const bool up = (lane & o) != 0;
-#pragma unroll
-          for (int n = 0; n < NC / 2; ++n) {
-            if (n >= hf) break;
-            const float give = up ? l[n] : l[n + hf], keep = up ? l[n + hf] : l[n];
-            l[n] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-          }
-          col += up ? hf : 0;
-          cnt = hf;
-        } else {
-          l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
-        }
-      }
+      const int col = fold_cols<NC, false>(l, lane);
 #pragma unroll
       for (int n = 0; n < (NC > 32 ? NC / 32 : 1); ++n) sL[(slot * 4 + sw) * N + c0 + col + n] = l[n];
       if (sw == 0)
