@@ -81,6 +81,11 @@ struct TreeCfg {
   static constexpr int kNW = N < 32 ? 1 : N / 32;       // mask words of a key: which columns see it
   static constexpr int kNodes = N == 128 ? MIS_TREE_MAX_NODES : 64;   // N >= max_nodes * G below 128
   static constexpr int kLanes = N == 128 ? 2 : 1;       // see TreeParams::lanes
+  // What a unit costs besides its steps (its first step, masks, epilogue), in
+  // steps: blocks are given equal shares of both. Measured as the time blocks
+  // took by their number of units: 8 us a unit at N = 128 (1.4 us a step), 2.8
+  // at 64, 0.3 at 16
+  static constexpr int kUnitCost = N == 128 ? 7 : N == 64 ? 3 : 0;
   static constexpr int kTmem = N == 16 ? 64 : 4 * N;    // S_0 | S_1 | O_0 | O_1
   // floats / words behind the tiles
   static constexpr int oMask = 0;                       // [2][kNodes][kNW]
@@ -182,10 +187,10 @@ __device__ __forceinline__ int lane_tiles(const TreeParams& p, const Req& R, int
 }
 
 // A unit of the block: request b's row tile rt for kv head h, steps [k0, k1);
-// k1 = 0 ends the list. at: the unit's first step here, counted over the batch.
+// k1 = 0 ends the list.
 struct Unit {
   Req R;
-  int z, b, h, rt, k0, k1, at;
+  int z, b, h, rt, k0, k1;
   // key rows of step k: the products run over them, the rest of the tile is void
   __device__ __forceinline__ int keys(int k) const {
     return k < R.kt ? min(kKeys, R.L - k * kKeys) : min(kKeys, R.a + R.n - (k - R.kt) * kKeys);
@@ -193,11 +198,10 @@ struct Unit {
 };
 constexpr int kUnits = 4;      // units the K producer may be ahead of the last reader
 
-// The unit behind u; left: steps of the block not yet in a unit.
-template <int N>
+// The unit behind u; left: the block's share not yet in a unit.
+template <int N, int kCost>
 __device__ __forceinline__ bool next_unit(const TreeParams& p, Unit& u, int& left) {
   if (left <= 0) return false;
-  u.at += u.k1 - u.k0;
   u.k0 = 0;
   u.rt += p.lanes;
   if (u.rt >= u.R.nrt) {
@@ -215,7 +219,7 @@ __device__ __forceinline__ bool next_unit(const TreeParams& p, Unit& u, int& lef
     }
   }
   u.k1 = min(u.R.nkt, left);
-  left -= u.k1;
+  left -= u.R.nkt + kCost;
   return true;
 }
 
@@ -323,7 +327,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   uint64_t* bars = reinterpret_cast<uint64_t*>(words + C::kWords);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + nBar);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  __shared__ Unit s_unit[kUnits];
+  __shared__ Unit s_start, s_unit[kUnits];
   __shared__ int s_sums[C::kLanes][C::kThreads / 32];
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -375,7 +379,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     R = load_req<N>(p, b);
     bad_req |= R.bad;
 #pragma unroll
-    for (int z = 0; z < LM; ++z) mine[z] += p.Hkv * lane_tiles(p, R, z) * R.nkt;
+    for (int z = 0; z < LM; ++z) mine[z] += p.Hkv * lane_tiles(p, R, z) * (R.nkt + C::kUnitCost);
   }
 #pragma unroll
   for (int z = 0; z < LM; ++z) {
@@ -415,35 +419,32 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
 #pragma unroll 1
       for (int b = rb0; b < rb1; ++b) {
         if (per > 1) R = load_req<N>(p, b);
-        const int nt = lane_tiles(p, R, z), c = p.Hkv * nt * R.nkt;
+        const int nt = lane_tiles(p, R, z), cost = R.nkt + C::kUnitCost, c = p.Hkv * nt * cost;
         if (f0 >= at + c) { at += c; continue; }
-        const int off = f0 - at, u = off / R.nkt;
+        const int off = f0 - at, u = off / cost;
         Unit v;
         v.R = R;
         v.z = z;
         v.b = b;
-        v.k0 = off - u * R.nkt;
+        v.k0 = off - u * cost;              // from nkt on: the unit's steps are all done
         v.k1 = min(R.nkt, v.k0 + steps);
         v.h = N < 128 ? u : u / nt;
         v.rt = z + (u - v.h * nt) * p.lanes;
-        v.at = f0;
-        s_unit[0] = v;
+        s_start = v;
         break;
       }
     }
   }
-  if (threadIdx.x == 0 && steps == 0) s_unit[0] = Unit{};
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
   const Bound W{abort_flag, p.wait_ns};
   auto colS = [](int s) { return (uint32_t)(s * N); };
   auto colO = [](int s) { return (uint32_t)((2 + s) * N); };
 
-  // a reader's next unit, number lu: copied, and its place given back. The
-  // block's first unit is there from the start
+  // a reader's next unit, number lu: copied, and its place given back
   auto take = [&](int lu, Unit& u) -> bool {
     const int s = lu % kUnits;
-    bool ok = lu == 0 || spin(bar(bUF + s), (lu / kUnits) & 1, W, 0x900);
+    bool ok = spin(bar(bUF + s), (lu / kUnits) & 1, W, 0x900);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) return false;
     u = s_unit[s];
@@ -471,22 +472,23 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       struct Copy { int page, row, h, key; bool fresh, cached, want; };
       bool ok = true;
       Unit w;
-      int k = 0, lu = 0, left = 0;
-      if (y) {
-        w.k1 = 0;
-      } else {
-        // the K producer also lays out the block's units for the other warps
-        if (lane == 0) mbar_arrive(bar(bUF));
-        w = s_unit[0];                                   // all zero if there is none
-        left = steps - (w.k1 - w.k0);
-        k = w.k0;
-        lu = 1;
-      }
+      // the K producer also lays out the block's units for the other warps
+      int k = 0, lu = 0, left = steps;
+      bool begun = y || steps == 0;
+      w.k1 = 0;
       auto advance = [&]() -> bool {
         if (y) {
           if (!take(lu, w)) return false;
         } else {
-          const bool more = next_unit<N>(p, w, left);
+          bool more;
+          if (!begun) {
+            begun = true;
+            w = s_start;
+            left -= w.R.nkt + C::kUnitCost - w.k0;
+            more = w.k1 > w.k0 || next_unit<N, C::kUnitCost>(p, w, left);
+          } else {
+            more = steps > 0 && next_unit<N, C::kUnitCost>(p, w, left);
+          }
           const int sl = lu % kUnits;
           if (lu >= kUnits) {
             ok = spin(bar(bUE + sl), ((lu / kUnits) - 1) & 1, W, 0x910);
@@ -1397,8 +1399,8 @@ extern "C" mis_status_t mis_tree_attention_fwd(
   const TreeWs ws = workspace_of(desc, cache);
   if (!workspace || !aligned(workspace, 256) || ws_bytes < ws.total) return MIS_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // steps are counted in 32 bits
-  const int64_t tiles = ((int64_t)max_pages * cache->page_size + kKeys - 1) / kKeys + 2;
+  // steps (with a unit's own cost) are counted in 32 bits
+  const int64_t tiles = ((int64_t)max_pages * cache->page_size + kKeys - 1) / kKeys + 16;
   const int64_t rows = (int64_t)desc->max_nodes * (desc->Hq / cache->Hkv);
   if ((double)tiles * desc->B * cache->Hkv * (rows > 128 ? 2.0 * ((rows + 127) / 128) : 1.0) >= 2147483648.0)
     return MIS_ERR_UNSUPPORTED;
