@@ -22,8 +22,8 @@
 // leave (max, sum, unnormalised O) in the workspace and a second kernel adds
 // them in block order, so the same call gives the same bits.
 //
-// Warp roles: 0 and 3 TMA producers of K and of V (pages of the cache, 8-row
-// groups of the new rows), 1 MMA issue, 2 Q's copies and the tree's masks, then one or
+// Warp roles: 0 and 3 TMA producers of K and of Q and V (pages of the cache,
+// 8-row groups of the new rows), 1 MMA issue, 2 the tree's masks, then one or
 // two softmax warpgroups (a thread is a key, it owns N or N / 2 columns) and
 // an epilogue warpgroup (a thread is an element of the head).
 //
@@ -456,7 +456,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   if (warp < 4) {
     if constexpr (N >= 64) regs_dec<C::kRegCtl>();
     if (warp == 0 || warp == 3) {
-      // ---------------------------------- producers: warp 0 of K, warp 3 of V.
+      // --------------------------- producers: warp 0 of K, warp 3 of Q and V.
       // Each follows its own ring, so a K tile never waits behind a V tile
       const int y = warp == 3;
       const int depth = y ? VS : KS, full0 = y ? bVF : bKF, empty0 = y ? bVE : bKE;
@@ -479,6 +479,19 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       auto advance = [&]() -> bool {
         if (y) {
           if (!take(lu, w)) return false;
+          // Q too, the rows of npt nodes (nodes behind the request's are
+          // columns that nobody reads)
+          const int sq = lu % QS;
+          if (lu >= QS) ok = spin(bar(bQE + sq), ((lu / QS) - 1) & 1, W, 0x600);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) return false;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(bQF + sq), (uint32_t)(NB * p.npt * p.G * 128));
+            for (int x = 0; x < NB; ++x)
+              tma_load_3d(smem_u32(sQ + sq * C::kQ) + x * C::kQBox, &qmap, bar(bQF + sq), x * 64,
+                          w.h * p.G, w.R.r0 + w.rt * p.npt);
+          }
+          __syncwarp();
         } else {
           bool more;
           if (!begun) {
@@ -558,6 +571,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       // drain: every copy has landed before the block exits
       for (int i = max(0, issued - depth); i < issued; ++i)
         wait_drain(bar(full0 + i % depth), (i / depth) & 1);
+      if (y)
+        for (int i = max(0, lu - QS); i < lu; ++i) wait_drain(bar(bQF + i % QS), (i / QS) & 1);
     } else if (warp == 1) {
       // --------------------------------------------------------------- MMA
       // the warp walks together and one elected lane issues, so loop state and
@@ -684,26 +699,13 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       __syncwarp();
       wait_drain(bar(bDR), 0);
     } else {
-      // ------------------------------------------ Q's copies and the tree's masks
-      int lu = 0, q_issued = 0;
+      // ------------------------------------------------------ the tree's masks
+      int lu = 0, t0 = 0;                                // t0: steps of the units before
       bool ok = true, bad = false;
       Unit w;
       while (ok && take(lu, w)) {
         const int node0 = w.rt * p.npt, rows = min(p.npt, w.R.n - node0) * p.G;
-        const int sq = lu % QS, sm = lu & 1;
-        if (lu >= QS) ok = spin(bar(bQE + sq), ((lu / QS) - 1) & 1, W, 0x600);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        // the rows of npt nodes (nodes behind the request's are columns that
-        // nobody reads)
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(bQF + sq), (uint32_t)(NB * p.npt * p.G * 128));
-          for (int x = 0; x < NB; ++x)
-            tma_load_3d(smem_u32(sQ + sq * C::kQ) + x * C::kQBox, &qmap, bar(bQF + sq), x * 64,
-                        w.h * p.G, w.R.r0 + node0);
-        }
-        q_issued = lu + 1;
-        __syncwarp();
+        const int sm = lu & 1;
         if (lu >= 2) ok = spin(bar(bSE + sm), ((lu >> 1) - 1) & 1, W, 0x610);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -750,30 +752,60 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                   atomicOr(&m[j * NW + x], bit_range(lo - 32 * x, hi - 32 * x));
             }
           }
-          __syncwarp();
-          // new rows whose V holds a NaN or an infinity (see the softmax)
-          constexpr int LPR = D / 8, RPI = 32 / LPR;     // lanes a row, rows at a time
-#pragma unroll 4
-          for (int j0 = 0; j0 < w.R.n; j0 += RPI) {
-            const int j = j0 + lane / LPR;
+          // New rows whose V holds a NaN or an infinity (see the softmax). A few
+          // are read from memory, one trip that is over before their tile is
+          // there; more than that from the tiles the producer brought, which
+          // stay until the softmax has used this unit's masks (64 rows from
+          // memory took 20 us of the loaded HBM's latency; one decoded row
+          // from its tile 0.8 us more than this)
+          auto odd = [](const uint32_t* x) {
             bool nf = false;
-            if (j < w.R.n) {
-              const uint4 u = *reinterpret_cast<const uint4*>(p.v + (int64_t)(w.R.r0 + j) * p.vs + w.h * D +
-                                                              lane % LPR * 8);
-              const uint32_t x[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                nf |= (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
+            for (int y = 0; y < 4; ++y)
+              nf |= (x[y] & 0x7f80u) == 0x7f80u || (x[y] & 0x7f800000u) == 0x7f800000u;
+            return nf;
+          };
+          constexpr int LPR = D / 8, RPI = 32 / LPR, U = 4;   // lanes a row, rows a load, loads in flight
+          const bool few = w.R.n <= U * RPI;
+          if (few) {
+            const __nv_bfloat16* src = p.v + (int64_t)w.R.r0 * p.vs + w.h * D + lane % LPR * 8;
+            uint4 u[U];
+#pragma unroll
+            for (int e = 0; e < U; ++e)
+              u[e] = *reinterpret_cast<const uint4*>(src + (int64_t)min(e * RPI + lane / LPR, w.R.n - 1) * p.vs);
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+              const uint32_t x[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
+              if (odd(x)) atomicOr(&sNf[sm * 8], 1u << min(e * RPI + lane / LPR, w.R.n - 1));
             }
-            if (nf) atomicOr(&sNf[sm * 8 + (j >> 5)], 1u << (j & 31));
           }
+          for (int k = max(w.k0, w.R.kt); ok && !few && k < w.k1; ++k) {
+            const int t = t0 + k - w.k0, kv = w.keys(k), a = k == w.R.kt ? w.R.a : 0;
+            ok = spin(bar(bVF + t % VS), (t / VS) & 1, W, 0x620);
+            ok = __all_sync(0xffffffffu, ok);
+            const uint32_t tile = smem_u32(sV + (t % VS) * C::kTile);
+            for (int r = a + lane; ok && r < kv; r += 32) {
+              bool nf = false;
+#pragma unroll 4
+              for (int c = 0; c < 8 * NB; ++c) {               // any order: lanes spread over the banks
+                uint32_t x[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                             : "r"(tile + (c >> 3) * C::kBox + r * 128 + (((c + r) & 7) << 4)) : "memory");
+                nf |= odd(x);
+              }
+              const int j = (k - w.R.kt) * kKeys + r - w.R.a;
+              if (nf) atomicOr(&sNf[sm * 8 + (j >> 5)], 1u << (j & 31));
+            }
+          }
+          if (!ok) break;
         }
+        t0 += w.k1 - w.k0;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bMF + sm));
         ++lu;
       }
       __syncwarp();
-      for (int i = max(0, q_issued - QS); i < q_issued; ++i) wait_drain(bar(bQF + i % QS), (i / QS) & 1);
       if (bad) raise_status(status, kDevIndex, 0x42);
     }
   } else if (warp < 4 + 4 * WG) {
