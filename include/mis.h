@@ -526,7 +526,8 @@ mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const void* k, con
  *               1/sqrt(D)
  *   q, k, v, o, lse, row strides — as in mis_attention_fwd_plan (lse fp32
  *               [Hq, T] or NULL). Rows from cu_nodes[B] on are not written
- *   block_table — device int32 [B, max_pages], row stride in elements
+ *   block_table — device int32 [B, max_pages], row stride in elements;
+ *               max_pages * page_size <= 2^31 - 256
  *   cache_len — device int32 [B], 0 .. max_pages * page_size
  *   cu_nodes  — device int32 [B+1], non-decreasing, within [0, T]
  *   parents   — device int32 [T]: the parent's index inside the request
@@ -541,8 +542,12 @@ mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const void* k, con
  * bad cache_len, more than max_nodes rows, or a bad cu_nodes range is
  * skipped (its rows are not written); a page id outside the cache hides its
  * rows; a parent out of range counts as MIS_TREE_ROOT.
- * fp32 scores, statistics and accumulation; probabilities are rounded to
- * bf16 for the second product, o to bf16. The same call gives the same bits.
+ * o and lse overlap no input. fp32 scores, statistics and accumulation;
+ * probabilities are rounded to bf16 for the second product, o to bf16. The
+ * same call gives the same bits. Two kernels. A wait inside the first can last
+ * as long as a block works on one request, about 1.5 us per 128 cached rows
+ * (see mis_set_wait_limit_ns()). MIS_ERR_UNSUPPORTED also where B * Hkv *
+ * max_pages * page_size / 128 steps would pass 32 bits.
  * Workspace: device, 256-byte aligned, >= mis_tree_attention_workspace_size()
  * (0 for an invalid descriptor); one call at a time may use it. */
 #define MIS_TREE_MAX_NODES 256

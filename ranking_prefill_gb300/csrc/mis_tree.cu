@@ -359,6 +359,13 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     tma_prefetch_desc(&kc8map); tma_prefetch_desc(&vc8map);
     tma_prefetch_desc(&kmap); tma_prefetch_desc(&vmap);
   }
+  // Q rows that no copy writes (G does not divide N): columns that nobody
+  // reads, but whose scores are looked at when references are drawn
+  for (int x = threadIdx.x; x < QS * NB * (N - p.npt * p.G) * 8; x += C::kThreads) {
+    const int row = x / 8 % (N - p.npt * p.G), box = x / 8 / (N - p.npt * p.G);
+    st_shared_v4(smem_u32(sQ) + box * C::kQBox + (p.npt * p.G + row) * 128 + x % 8 * 16, 0, 0, 0, 0);
+  }
+  fence_proxy_async();
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmem);
     tmem_relinquish();
@@ -1413,7 +1420,7 @@ extern "C" mis_status_t mis_tree_attention_fwd(
   const mis_status_t ds = check_desc(desc, cache);
   if (ds != MIS_OK) return ds;
   if (max_pages < 1) return MIS_ERR_INVALID_ARG;
-  if ((int64_t)max_pages * cache->page_size > 0x7fffffff || block_table_stride < max_pages)
+  if ((int64_t)max_pages * cache->page_size > 0x7fffff00 || block_table_stride < max_pages)
     return MIS_ERR_SHAPE;
   if (!block_table || !cache_len || !cu_nodes || !aligned(block_table, 4) ||
       !aligned(cache_len, 4) || !aligned(cu_nodes, 4) || !aligned(parents, 4) || !aligned(lse, 4))

@@ -439,7 +439,7 @@ def test_ragged_trees(hq, hkv, D, layout, ps):
          extra_cols=2).check()
 
 
-@pytest.mark.parametrize("hq,hkv,D,nodes", [(16, 8, 128, [64, 1, 63]), (32, 8, 128, [64, 40]),
+@pytest.mark.parametrize("hq,hkv,D,nodes", [(16, 8, 128, [64, 1, 63]), (32, 8, 128, [64, 40]), (28, 4, 128, [64, 9]),
                                             (8, 1, 128, [256, 129]), (4, 2, 64, [256, 200, 3]),
                                             (2, 2, 128, [128, 127, 129, 130])])
 @pytest.mark.parametrize("chain", [False, True])
@@ -644,6 +644,57 @@ def test_captured_and_replayed_with_other_lengths():
         t.compare(t.oracle())
 
 
+def test_two_graphs_share_a_workspace_in_turn():
+    a = Tree([700, 300], [8, 3], 8, 2, 128, 32, None, seed=20).prepare()
+    b = Tree([90, 1000, 3], [20, 5, 1], 16, 2, 128, 16, None, seed=21).prepare()
+    shared = torch.empty(max(a.ws.numel(), b.ws.numel()), dtype=torch.uint8, device="cuda").fill_(0x5A)
+    graphs = []
+    for t in (a, b):
+        t.ws = shared
+        t.call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            t.call()
+        graphs.append(g)
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    a.compare(a.oracle())
+    b.compare(b.oracle())
+
+
+def test_infinite_and_nan_queries_stay_in_their_rows():
+    # rows of other requests fill up a tile's columns; whatever they hold, this
+    # request's rows come out as without them
+    t = Tree([300, 200, 40], [2, 3, 1], 8, 2, 128, 16, None, seed=22).prepare()
+    want = t.oracle()
+    t.q[2] = float("inf")
+    t.q[4, :, ::2] = float("nan")
+    t.call()
+    assert lib.mis_get_device_status(t.ws) == lib.MIS_OK
+    want = [x.copy() for x in want]
+    for x in (want[0], want[2]):
+        x[[2, 4]] = np.nan
+    want[1][:, [2, 4]] = np.nan
+    t.compare(want)
+
+
+def test_nodes_at_the_edges_of_the_last_cache_tile():
+    # the new rows share the last cache tile when they fit behind it (from a
+    # multiple of 8 rows): both sides of that edge, for a few and for many nodes
+    lens, nodes = [], []
+    for n in (1, 2, 7, 8, 9, 56, 64):
+        for off in (0, 1, 7, 8, 9, 120 - n, 127 - n, 128 - n, 121, 127):
+            if off >= 0:
+                lens.append(128 + off)
+                nodes.append(n)
+    for hq, hkv, D in ((2, 2, 64), (4, 1, 128)):
+        rng = np.random.default_rng(hq)
+        Tree(lens, nodes, hq, hkv, D, 16, random_parents(rng, nodes), seed=23).check()
+
+
 def test_two_streams_with_their_own_workspaces():
     a = Tree([700, 300], [8, 3], 8, 2, 128, 32, None, seed=15).prepare()
     b = Tree([900, 100], [2, 5], 8, 2, 128, 32, None, seed=16).prepare()
@@ -686,8 +737,14 @@ def test_rows_beyond_32_bit_element_offsets():
     torch.cuda.empty_cache()
 
 
-def test_wait_timeout_is_reported_and_the_workspace_survives():
-    t = Tree([300, 20], [4, 2], 8, 2, 128, 16, None, seed=17).prepare()
+WIDTHS = [(8, 2, 128, [4, 2]), (8, 2, 64, [8, 3]), (16, 8, 128, [32, 5]), (8, 1, 128, [33, 40]),
+          (4, 2, 64, [64, 130])]          # 16, 32, 64, 128 and 2 x 128 rows a kv head
+
+
+@pytest.mark.parametrize("hq,hkv,D,nodes", WIDTHS)
+def test_wait_timeout_is_reported_and_the_workspace_survives(hq, hkv, D, nodes):
+    par = random_parents(np.random.default_rng(2), nodes)
+    t = Tree([300, 20], nodes, hq, hkv, D, 16, par, seed=17).prepare()
     old = lib.mis_set_wait_limit_ns(2_000_000)
     lib.mis_inject_stall(1)
     try:
@@ -698,6 +755,26 @@ def test_wait_timeout_is_reported_and_the_workspace_survives():
     finally:
         lib.mis_inject_stall(0)
         lib.mis_set_wait_limit_ns(old)
+    t.call()
+    assert lib.mis_get_device_status(t.ws) == lib.MIS_OK
+    t.compare(t.oracle())
+
+
+@pytest.mark.parametrize("hq,hkv,D,nodes", WIDTHS)
+def test_waits_that_run_out_anywhere_end_the_call(hq, hkv, D, nodes):
+    # a limit far below the time of a copy: waits give up in whatever role comes first,
+    # and every block still ends
+    par = random_parents(np.random.default_rng(3), nodes)
+    t = Tree([3000, 700], nodes, hq, hkv, D, 16, par, seed=18).prepare()
+    for limit in (0, 300, 1000, 3000, 10000):
+        old = lib.mis_set_wait_limit_ns(limit)
+        try:
+            for _ in range(3):
+                t.call()
+            torch.cuda.synchronize()
+            assert lib.mis_get_device_status(t.ws) in (lib.MIS_OK, lib.MIS_ERR_DEVICE_TIMEOUT)
+        finally:
+            lib.mis_set_wait_limit_ns(old)
     t.call()
     assert lib.mis_get_device_status(t.ws) == lib.MIS_OK
     t.compare(t.oracle())
