@@ -582,41 +582,32 @@ def _require(ok, status: int, where: str):
         raise MisError(status, where)
 
 
-_torch = None
+_torch = _bf16 = _i32 = _u8 = _f32 = _device = _raw_stream = None
 
 
 def _here(stream):
     """(current device, stream address), one look at the runtime per call: the
-    checks below compare every tensor's device with it. (These calls run once
-    a layer and step, so they are kept short.)"""
-    global _torch
+    checks below compare every tensor's device with it. (The paged calls run
+    once a layer and step; a look at a tensor costs 0.1 us and more, so each is
+    made once, and what they share is not put into functions.)"""
+    global _torch, _bf16, _i32, _u8, _f32, _device, _raw_stream
     if _torch is None:
         import torch
+        if torch.cuda.is_available():
+            torch.cuda.init()
+            _device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+        else:
+            _device, _raw_stream = (lambda: -1), (lambda dev: None)
+        _bf16, _i32, _u8, _f32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
         _torch = torch
-    if not _torch.cuda.is_initialized() and not _torch.cuda.is_available():
-        return -1, None
-    dev = _torch.cuda.current_device()
+    dev = _device()
     if stream is None:
-        return dev, _torch._C._cuda_getCurrentRawStream(dev)
+        return dev, _raw_stream(dev)
     return dev, stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _vectors(where: str, dev: int, *pairs):
-    """(tensor or None, n): contiguous int32 of at least n elements on `dev`."""
-    i32 = _torch.int32
-    for t, n in pairs:
-        if t is None:
-            continue
-        if t.dtype is not i32 or t.get_device() != dev:
-            raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
-        if t.numel() < n or not t.is_contiguous():
-            raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
-
-
-def _rows(where: str, dev: int, T: int, heads: int, D: int, t) -> int:
-    """Row stride of bf16 [>= T, heads, D] on `dev`, heads packed inside a row."""
-    if t.dtype is not _torch.bfloat16 or t.get_device() != dev:
-        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+def _row_stride(where: str, T: int, heads: int, D: int, t) -> int:
+    """Row stride of [>= T, heads, D] rows, heads packed inside a row."""
     st, sh = t.stride(), t.shape
     if (len(sh) != 3 or sh[0] < T or sh[1] != heads or sh[2] != D or st[2] != 1 or
             (heads > 1 and st[1] != D)):
@@ -624,20 +615,12 @@ def _rows(where: str, dev: int, T: int, heads: int, D: int, t) -> int:
     return st[0] if sh[0] > 1 else heads * D
 
 
-def _table(where: str, dev: int, t, B: int):
-    """(columns, row stride) of an int32 [>= B, pages] table on `dev`."""
-    if t.dtype is not _torch.int32 or t.get_device() != dev:
-        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+def _table(where: str, t, B: int):
+    """(columns, row stride) of a [>= B, pages] table."""
     sh, st = t.shape, t.stride()
     if len(sh) != 2 or sh[0] < B or (sh[1] > 1 and st[1] != 1):
         raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
     return sh[1], st[0] if sh[0] > 1 else max(sh[1], 1)
-
-
-def _workspace(where: str, dev: int, t) -> int:
-    if t.dtype is not _torch.uint8 or t.get_device() != dev or not t.is_contiguous():
-        raise MisError(MIS_ERR_WORKSPACE, where)  # noqa: F821
-    return t.numel()
 
 
 class PagedCache:
@@ -693,15 +676,34 @@ def mis_paged_extend(new_len, cache_len, cache_len_out, block_table, free_pages,
     L = _lib or load()
     where = "mis_paged_extend"
     dev, st = _here(stream)
+    if not (new_len.dtype is _i32 and cache_len.dtype is _i32 and cache_len_out.dtype is _i32 and
+            block_table.dtype is _i32 and free_pages.dtype is _i32 and free_head.dtype is _i32 and
+            free_head_out.dtype is _i32 and cu_new.dtype is _i32 and slot_map.dtype is _i32 and
+            workspace.dtype is _u8 and new_len.get_device() == dev and cache_len.get_device() == dev and
+            cache_len_out.get_device() == dev and block_table.get_device() == dev and
+            free_pages.get_device() == dev and free_head.get_device() == dev and
+            free_head_out.get_device() == dev and cu_new.get_device() == dev and
+            slot_map.get_device() == dev and workspace.get_device() == dev):
+        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
     B, T, n_free = new_len.numel(), slot_map.numel(), free_pages.numel()
-    _vectors(where, dev, (new_len, 0), (cache_len, B), (cache_len_out, B), (cu_new, B + 1), (slot_map, 0),
-             (position_ids, T), (free_pages, 0), (free_head, 1), (free_head_out, 1))
-    cols, stride = _table(where, dev, block_table, B)
+    if not (cache_len.numel() >= B and cache_len_out.numel() >= B and cu_new.numel() > B and
+            free_head.numel() and free_head_out.numel() and new_len.is_contiguous() and
+            cache_len.is_contiguous() and cache_len_out.is_contiguous() and free_pages.is_contiguous() and
+            cu_new.is_contiguous() and slot_map.is_contiguous() and workspace.is_contiguous()):
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+    pos = None
+    if position_ids is not None:
+        if position_ids.dtype is not _i32 or position_ids.get_device() != dev:
+            raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+        if position_ids.numel() < T or not position_ids.is_contiguous():
+            raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+        pos = position_ids.data_ptr()
+    cols, stride = _table(where, block_table, B)
     st = L.mis_paged_extend(B, T, page_size, n_pages, new_len.data_ptr(), cache_len.data_ptr(),
-                            cache_len_out.data_ptr(), block_table.data_ptr(), cols, stride, free_pages.data_ptr(), n_free, free_head.data_ptr(),
-                            free_head_out.data_ptr(), cu_new.data_ptr(), slot_map.data_ptr(),
-                            None if position_ids is None else position_ids.data_ptr(),
-                            workspace.data_ptr(), _workspace(where, dev, workspace), st)
+                            cache_len_out.data_ptr(), block_table.data_ptr(), cols, stride,
+                            free_pages.data_ptr(), n_free, free_head.data_ptr(), free_head_out.data_ptr(),
+                            cu_new.data_ptr(), slot_map.data_ptr(), pos, workspace.data_ptr(),
+                            workspace.numel(), st)
     if st:
         raise MisError(st, where)
 
@@ -717,16 +719,28 @@ def mis_paged_write_kv(cache: PagedCache, k, v, slot_map, workspace, position_id
     L = _lib or load()
     where = "mis_paged_write_kv"
     dev, st = _here(stream)
-    n = slot_map.numel()
-    _require(cache.device == dev, MIS_ERR_INVALID_ARG, where)  # noqa: F821
-    T = k.shape[0]
-    ks = _rows(where, dev, T, cache.Hkv, cache.D, k)
-    vs = _rows(where, dev, T, cache.Hkv, cache.D, v)
-    _vectors(where, dev, (slot_map, 0), (position_ids, n), (src_rows, n))
-    st = L.mis_paged_write_kv(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs, T,
-                              None if src_rows is None else src_rows.data_ptr(), slot_map.data_ptr(), n,
-                              None if position_ids is None else position_ids.data_ptr(), base,
-                              workspace.data_ptr(), _workspace(where, dev, workspace), st)
+    if not (cache.device == dev and k.dtype is _bf16 and v.dtype is _bf16 and slot_map.dtype is _i32 and
+            workspace.dtype is _u8 and k.get_device() == dev and v.get_device() == dev and
+            slot_map.get_device() == dev and workspace.get_device() == dev):
+        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    n, T = slot_map.numel(), k.shape[0]
+    ks = _row_stride(where, T, cache.Hkv, cache.D, k)
+    vs = _row_stride(where, T, cache.Hkv, cache.D, v)
+    pos = src = None
+    for t in (position_ids, src_rows):
+        if t is not None:
+            if t.dtype is not _i32 or t.get_device() != dev:
+                raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+            if t.numel() < n or not t.is_contiguous():
+                raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+            if t is position_ids:
+                pos = t.data_ptr()
+            if t is src_rows:
+                src = t.data_ptr()
+    if not (slot_map.is_contiguous() and workspace.is_contiguous()):
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+    st = L.mis_paged_write_kv(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs, T, src, slot_map.data_ptr(), n,
+                              pos, base, workspace.data_ptr(), workspace.numel(), st)
     if st:
         raise MisError(st, where)
 
@@ -741,20 +755,36 @@ def mis_tree_attention_fwd(desc: TreeDesc, q, k, v, o, lse, block_table, cache_l
     where = "mis_tree_attention_fwd"
     dev, st = _here(stream)
     c, T, B, Hq = desc.cache, desc.T, desc.B, desc.Hq
-    _require(c.device == dev, MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    if not (c.device == dev and q.dtype is _bf16 and k.dtype is _bf16 and v.dtype is _bf16 and
+            o.dtype is _bf16 and block_table.dtype is _i32 and cache_len.dtype is _i32 and
+            cu_nodes.dtype is _i32 and workspace.dtype is _u8 and q.get_device() == dev and
+            k.get_device() == dev and v.get_device() == dev and o.get_device() == dev and
+            block_table.get_device() == dev and cache_len.get_device() == dev and
+            cu_nodes.get_device() == dev and workspace.get_device() == dev):
+        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
     H, D = c.Hkv, c.D
-    qs, os_ = _rows(where, dev, T, Hq, D, q), _rows(where, dev, T, Hq, D, o)
-    ks, vs = _rows(where, dev, T, H, D, k), _rows(where, dev, T, H, D, v)
+    qs, os_ = _row_stride(where, T, Hq, D, q), _row_stride(where, T, Hq, D, o)
+    ks, vs = _row_stride(where, T, H, D, k), _row_stride(where, T, H, D, v)
+    cols, stride = _table(where, block_table, B)
+    if not (cache_len.numel() >= B and cu_nodes.numel() > B and cache_len.is_contiguous() and
+            cu_nodes.is_contiguous() and workspace.is_contiguous()):
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
     if lse is not None:
-        _require(lse.dtype is _torch.float32 and lse.get_device() == dev, MIS_ERR_INVALID_ARG, where)  # noqa: F821
-        _require(lse.shape == (Hq, T) and lse.is_contiguous(), MIS_ERR_SHAPE, where)  # noqa: F821
+        if lse.dtype is not _f32 or lse.get_device() != dev:
+            raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+        if lse.shape != (Hq, T) or not lse.is_contiguous():
+            raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
         lse = lse.data_ptr()
-    _vectors(where, dev, (cache_len, B), (cu_nodes, B + 1), (parents, T))
-    cols, stride = _table(where, dev, block_table, B)
+    if parents is not None:
+        if parents.dtype is not _i32 or parents.get_device() != dev:
+            raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+        if parents.numel() < T or not parents.is_contiguous():
+            raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+        parents = parents.data_ptr()
     st = L.mis_tree_attention_fwd(desc.ref, c.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                  lse, qs, ks, vs, os_, block_table.data_ptr(), cols, stride, cache_len.data_ptr(), cu_nodes.data_ptr(),
-                                  None if parents is None else parents.data_ptr(), workspace.data_ptr(),
-                                  _workspace(where, dev, workspace), st)
+                                  lse, qs, ks, vs, os_, block_table.data_ptr(), cols, stride,
+                                  cache_len.data_ptr(), cu_nodes.data_ptr(), parents, workspace.data_ptr(),
+                                  workspace.numel(), st)
     if st:
         raise MisError(st, where)
 
