@@ -568,10 +568,11 @@ mis_status_t mis_tree_attention_fwd(const mis_tree_desc* desc, const mis_paged_c
                                     void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
- * Device status of the last call that used `workspace` (a plan workspace or
- * a scoring workspace). Synchronises `stream`, then returns MIS_OK,
- * MIS_ERR_DEVICE_TIMEOUT or MIS_ERR_DEVICE_INDEX. Each call clears the word
- * when it starts.
+ * Device status of the last call that used `workspace` (a plan workspace, or
+ * one of scoring, of the paged cache or of tree attention). Synchronises
+ * `stream`, then returns MIS_OK, MIS_ERR_DEVICE_TIMEOUT, MIS_ERR_DEVICE_INDEX
+ * or MIS_ERR_DEVICE_PAGES, the first of these that applies. Each call that
+ * enqueues work sets the word anew.
  * ------------------------------------------------------------------------ */
 mis_status_t mis_get_device_status(const void* workspace, void* stream);
 

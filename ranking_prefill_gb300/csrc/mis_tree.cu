@@ -45,8 +45,8 @@
 
 namespace mis {
 
-CUtensorMap make_tmap_bf16(const void* base, int rank, const uint64_t* dims,
-                           const uint64_t* strides_bytes, const uint32_t* box, bool* ok);
+CUtensorMap encode_tmap_bf16(const void* base, int rank, const uint64_t* dims,
+                             const uint64_t* strides_bytes, const uint32_t* box, bool* ok);
 
 namespace {
 
@@ -1470,10 +1470,10 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     const int N = tile_rows(desc, cache), G = desc->Hq / cache->Hkv, npt = N / G;
     const uint32_t qb[3] = {64, (uint32_t)G, (uint32_t)npt};
     const CUtensorMap maps[7] = {
-        make_tmap_bf16(q, 3, qd, qst, qb, &ok),
-        make_tmap_bf16(cache->k, 4, cd, cs, cb, &ok), make_tmap_bf16(cache->v, 4, cd, cs, cb, &ok),
-        make_tmap_bf16(cache->k, 4, cd, cs, c8, &ok), make_tmap_bf16(cache->v, 4, cd, cs, c8, &ok),
-        make_tmap_bf16(k, 3, nd, nk, nb, &ok), make_tmap_bf16(v, 3, nd, nv, nb, &ok)};
+        encode_tmap_bf16(q, 3, qd, qst, qb, &ok),
+        encode_tmap_bf16(cache->k, 4, cd, cs, cb, &ok), encode_tmap_bf16(cache->v, 4, cd, cs, cb, &ok),
+        encode_tmap_bf16(cache->k, 4, cd, cs, c8, &ok), encode_tmap_bf16(cache->v, 4, cd, cs, c8, &ok),
+        encode_tmap_bf16(k, 3, nd, nk, nb, &ok), encode_tmap_bf16(v, 3, nd, nv, nb, &ok)};
     if (!ok) return MIS_ERR_CUDA;
     uint8_t* base = static_cast<uint8_t*>(workspace);
     TreeParams p;
