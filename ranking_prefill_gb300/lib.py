@@ -582,7 +582,7 @@ def _require(ok, status: int, where: str):
         raise MisError(status, where)
 
 
-_torch = _bf16 = _i32 = _u8 = _f32 = _device = _raw_stream = None
+_torch = _BF16 = _I32 = _U8 = _F32 = _device = _raw_stream = None
 
 
 def _here(stream):
@@ -590,7 +590,7 @@ def _here(stream):
     checks below compare every tensor's device with it. (The paged calls run
     once a layer and step; a look at a tensor costs 0.1 us and more, so each is
     made once, and what they share is not put into functions.)"""
-    global _torch, _bf16, _i32, _u8, _f32, _device, _raw_stream
+    global _torch, _BF16, _I32, _U8, _F32, _device, _raw_stream
     if _torch is None:
         import torch
         if torch.cuda.is_available():
@@ -598,7 +598,7 @@ def _here(stream):
             _device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
         else:
             _device, _raw_stream = (lambda: -1), (lambda dev: None)
-        _bf16, _i32, _u8, _f32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
+        _BF16, _I32, _U8, _F32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
         _torch = torch
     dev = _device()
     if stream is None:
@@ -676,10 +676,10 @@ def mis_paged_extend(new_len, cache_len, cache_len_out, block_table, free_pages,
     L = _lib or load()
     where = "mis_paged_extend"
     dev, st = _here(stream)
-    if not (new_len.dtype is _i32 and cache_len.dtype is _i32 and cache_len_out.dtype is _i32 and
-            block_table.dtype is _i32 and free_pages.dtype is _i32 and free_head.dtype is _i32 and
-            free_head_out.dtype is _i32 and cu_new.dtype is _i32 and slot_map.dtype is _i32 and
-            workspace.dtype is _u8 and new_len.get_device() == dev and cache_len.get_device() == dev and
+    if not (new_len.dtype is _I32 and cache_len.dtype is _I32 and cache_len_out.dtype is _I32 and
+            block_table.dtype is _I32 and free_pages.dtype is _I32 and free_head.dtype is _I32 and
+            free_head_out.dtype is _I32 and cu_new.dtype is _I32 and slot_map.dtype is _I32 and
+            workspace.dtype is _U8 and new_len.get_device() == dev and cache_len.get_device() == dev and
             cache_len_out.get_device() == dev and block_table.get_device() == dev and
             free_pages.get_device() == dev and free_head.get_device() == dev and
             free_head_out.get_device() == dev and cu_new.get_device() == dev and
@@ -693,7 +693,7 @@ def mis_paged_extend(new_len, cache_len, cache_len_out, block_table, free_pages,
         raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
     pos = None
     if position_ids is not None:
-        if position_ids.dtype is not _i32 or position_ids.get_device() != dev:
+        if position_ids.dtype is not _I32 or position_ids.get_device() != dev:
             raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
         if position_ids.numel() < T or not position_ids.is_contiguous():
             raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
@@ -719,8 +719,8 @@ def mis_paged_write_kv(cache: PagedCache, k, v, slot_map, workspace, position_id
     L = _lib or load()
     where = "mis_paged_write_kv"
     dev, st = _here(stream)
-    if not (cache.device == dev and k.dtype is _bf16 and v.dtype is _bf16 and slot_map.dtype is _i32 and
-            workspace.dtype is _u8 and k.get_device() == dev and v.get_device() == dev and
+    if not (cache.device == dev and k.dtype is _BF16 and v.dtype is _BF16 and slot_map.dtype is _I32 and
+            workspace.dtype is _U8 and k.get_device() == dev and v.get_device() == dev and
             slot_map.get_device() == dev and workspace.get_device() == dev):
         raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
     n, T = slot_map.numel(), k.shape[0]
@@ -729,7 +729,7 @@ def mis_paged_write_kv(cache: PagedCache, k, v, slot_map, workspace, position_id
     pos = src = None
     for t in (position_ids, src_rows):
         if t is not None:
-            if t.dtype is not _i32 or t.get_device() != dev:
+            if t.dtype is not _I32 or t.get_device() != dev:
                 raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
             if t.numel() < n or not t.is_contiguous():
                 raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
@@ -755,9 +755,9 @@ def mis_tree_attention_fwd(desc: TreeDesc, q, k, v, o, lse, block_table, cache_l
     where = "mis_tree_attention_fwd"
     dev, st = _here(stream)
     c, T, B, Hq = desc.cache, desc.T, desc.B, desc.Hq
-    if not (c.device == dev and q.dtype is _bf16 and k.dtype is _bf16 and v.dtype is _bf16 and
-            o.dtype is _bf16 and block_table.dtype is _i32 and cache_len.dtype is _i32 and
-            cu_nodes.dtype is _i32 and workspace.dtype is _u8 and q.get_device() == dev and
+    if not (c.device == dev and q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and
+            o.dtype is _BF16 and block_table.dtype is _I32 and cache_len.dtype is _I32 and
+            cu_nodes.dtype is _I32 and workspace.dtype is _U8 and q.get_device() == dev and
             k.get_device() == dev and v.get_device() == dev and o.get_device() == dev and
             block_table.get_device() == dev and cache_len.get_device() == dev and
             cu_nodes.get_device() == dev and workspace.get_device() == dev):
@@ -770,13 +770,13 @@ def mis_tree_attention_fwd(desc: TreeDesc, q, k, v, o, lse, block_table, cache_l
             cu_nodes.is_contiguous() and workspace.is_contiguous()):
         raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
     if lse is not None:
-        if lse.dtype is not _f32 or lse.get_device() != dev:
+        if lse.dtype is not _F32 or lse.get_device() != dev:
             raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
         if lse.shape != (Hq, T) or not lse.is_contiguous():
             raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
         lse = lse.data_ptr()
     if parents is not None:
-        if parents.dtype is not _i32 or parents.get_device() != dev:
+        if parents.dtype is not _I32 or parents.get_device() != dev:
             raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
         if parents.numel() < T or not parents.is_contiguous():
             raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
