@@ -17,7 +17,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmis_gb300.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
-CU_SOURCES = ["mis_attn.cu", "mis_score.cu", "mis_rope.cu", "mis_paged.cu", "mis_tree.cu"]
+CU_SOURCES = ["mis_attn.cu", "mis_score.cu", "mis_rope.cu", "mis_paged.cu", "mis_tree.cu",
+              "mis_tree_wide.cu"]
 CPP_SOURCES = ["mis_plan.cpp", "mis_abi.cpp"]
 
 

@@ -42,21 +42,23 @@
 
 #include "mis_internal.h"
 #include "mis_ptx.cuh"
+#include "mis_tree.cuh"
 
 namespace mis {
 
 CUtensorMap encode_tmap_bf16(const void* base, int rank, const uint64_t* dims,
                              const uint64_t* strides_bytes, const uint32_t* box, bool* ok);
 
+namespace tree {
+mis_status_t launch_wide(int D, const CUtensorMap* m, const TreeParams& p, int blocks, cudaStream_t st);
+}
+
 namespace {
 
 using namespace dev;
+using namespace tree;
 
-constexpr int kKeys = 128;                       // keys of a step
-constexpr float kGrow = 8.0f;                    // log2 units a score may pass the reference by
-constexpr float kSpread = 40.0f;                 // ... and maxima may differ under one reference
-constexpr float kEmpty = -1.0e30f;               // maximum of a column that has seen nothing
-constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kSpread = 40.0f;                 // log2 units maxima may differ by under one reference
 
 template <int D, int N>
 struct TreeCfg {
@@ -79,8 +81,7 @@ struct TreeCfg {
   static constexpr int kK = D == 128 ? (N == 128 ? 2 : 3) : (N == 128 ? 4 : 5);
   static constexpr int kV = D == 128 ? (N == 16 ? 3 : 2) : (N == 128 ? 4 : 5);
   static constexpr int kNW = N < 32 ? 1 : N / 32;       // mask words of a key: which columns see it
-  static constexpr int kNodes = N == 128 ? MIS_TREE_MAX_NODES : 64;   // N >= max_nodes * G below 128
-  static constexpr int kLanes = N == 128 ? 2 : 1;       // see TreeParams::lanes
+  static constexpr int kNodes = N == 128 ? 128 : 64;   // N >= max_nodes * G below 128
   // What a unit costs besides its steps (its first step, masks, epilogue), in
   // steps: blocks are given equal shares of both. Measured as the time blocks
   // took by their number of units: 8 us a unit at N = 128 (1.4 us a step), 2.8
@@ -103,130 +104,6 @@ struct TreeCfg {
   static constexpr int kSmem = kData + 4 * kWords + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
 };
-
-struct TreeParams {
-  const __nv_bfloat16* v;
-  __nv_bfloat16* o;
-  float* lse;
-  int64_t vs, os;
-  int32_t n_pages, page_shift, max_pages;
-  const int32_t* table;
-  int64_t table_stride;
-  const int32_t* cache_len;
-  const int32_t* cu;
-  const int32_t* parents;
-  int32_t B, T, Hkv, G, max_nodes;
-  int32_t npt;             // nodes of a row tile, N / G
-  int32_t lanes;           // row tiles rt, rt + lanes, ... of all requests form a lane, and the lanes lie
-                           // end to end: tiles that share K and V are worked on at the same time, by
-                           // blocks that start a lane's length apart, and meet in L2
-  uint32_t g_magic;        // ceil(2^32 / G): n / G = umulhi(n, magic) for n < N, 1 < G <= 128
-  float scale_log2;
-  uint32_t* cta_status;    // [blocks][2]
-  int4* meta;              // [blocks] the split unit that starts in the block: its first row of q,
-                           // columns, kv head, pieces
-  float2* ml;              // [2 * blocks][N] (max, sum) of a piece
-  float* part;             // [2 * blocks][N][D]
-  uint64_t wait_ns;
-  uint32_t stall;
-};
-
-// A bounded wait in few instructions (it stands at some thirty places): a wait
-// that runs out, or sees that another gave up, returns false. The site goes to
-// shared memory and to the status word when the block ends.
-struct Bound {
-  volatile uint32_t* gave_up;
-  uint64_t limit_ns;
-};
-__device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, const Bound& w, uint32_t where) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  do {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*w.gave_up) return false;
-  } while (globaltimer() - t0 <= w.limit_ns);
-  *w.gave_up = where;
-  return false;
-}
-
-// One request, checked. Its steps are the 128-key tiles of its cached rows,
-// then those of its new rows. When the new rows fit behind the last, partial
-// cache tile (from the next multiple of 8 rows, a copy's granularity) they
-// share its step: a decoded token costs no step of its own.
-struct Req {
-  int r0, n, L;
-  int nkt;                 // steps in all
-  int kt;                  // first step with new rows
-  int a;                   // their first key row in that step (0 unless it is shared)
-  int nrt;                 // row tiles
-  bool bad;
-};
-
-template <int N>
-__device__ __forceinline__ Req load_req(const TreeParams& p, int b) {
-  const int64_t r0 = p.cu[b], r1 = p.cu[b + 1], L = p.cache_len[b];
-  Req R;
-  R.bad = r0 < 0 || r1 < r0 || r1 > p.T || r1 - r0 > p.max_nodes || L < 0 ||
-          L > ((int64_t)p.max_pages << p.page_shift);
-  R.r0 = (int)r0;
-  R.n = R.bad ? 0 : (int)(r1 - r0);
-  R.L = (int)L;
-  const int nct = (int)((L + kKeys - 1) / kKeys);
-  const int off = (int)L & (kKeys - 1), a = (off + 7) & ~7;
-  const bool share = off > 0 && a + R.n <= kKeys;
-  R.a = share ? a : 0;
-  R.kt = share ? nct - 1 : nct;
-  R.nkt = share ? nct : nct + (R.n + kKeys - 1) / kKeys;
-  R.nrt = N < 128 ? 1 : (R.n + p.npt - 1) / p.npt;
-  return R;
-}
-
-// Row tiles of a request in lane z.
-__device__ __forceinline__ int lane_tiles(const TreeParams& p, const Req& R, int z) {
-  return R.n && R.nrt > z ? (R.nrt - z + p.lanes - 1) / p.lanes : 0;
-}
-
-// A unit of the block: request b's row tile rt for kv head h, steps [k0, k1);
-// k1 = 0 ends the list.
-struct Unit {
-  Req R;
-  int z, b, h, rt, k0, k1;
-  // key rows of step k: the products run over them, the rest of the tile is void
-  __device__ __forceinline__ int keys(int k) const {
-    return k < R.kt ? min(kKeys, R.L - k * kKeys) : min(kKeys, R.a + R.n - (k - R.kt) * kKeys);
-  }
-};
-constexpr int kUnits = 4;      // units the K producer may be ahead of the last reader
-
-// The unit behind u; left: the block's share not yet in a unit.
-template <int N, int kCost>
-__device__ __forceinline__ bool next_unit(const TreeParams& p, Unit& u, int& left) {
-  if (left <= 0) return false;
-  u.k0 = 0;
-  u.rt += p.lanes;
-  if (u.rt >= u.R.nrt) {
-    u.rt = u.z;
-    if (++u.h == p.Hkv) {
-      u.h = 0;
-      do {
-        if (++u.b >= p.B) {
-          u.b = 0;
-          u.rt = ++u.z;
-          if (u.z >= p.lanes) return false;
-        }
-        u.R = load_req<N>(p, u.b);
-      } while (u.R.n == 0 || u.R.nrt <= u.z);
-    }
-  }
-  u.k1 = min(u.R.nkt, left);
-  left -= u.R.nkt + kCost;
-  return true;
-}
-
-// Node (in its tile) of column n.
-__device__ __forceinline__ int over_g(const TreeParams& p, int n) {
-  return p.G == 1 ? n : (int)__umulhi((uint32_t)n, p.g_magic);
-}
 
 __device__ __forceinline__ float warp_max(float x) {       // NaN only if all are
   float r;
@@ -298,7 +175,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
   using C = TreeCfg<D, N>;
   constexpr int NB = C::kNB, NC = C::kNC, WG = C::kWG, KS = C::kK, VS = C::kV, QS = C::kQS;
-  constexpr int NW = C::kNW, LM = C::kLanes;
+  constexpr int NW = C::kNW;
   // barriers
   constexpr int bQF = 0, bQE = bQF + 2, bKF = bQE + 2, bKE = bKF + KS, bVF = bKE + KS,
                 bVE = bVF + VS, bSF = bVE + VS, bPF = bSF + 2, bPV = bPF + 1, bOF = bPV + 1,
@@ -328,7 +205,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + nBar);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   __shared__ Unit s_start, s_unit[kUnits];
-  __shared__ int s_sums[C::kLanes][C::kThreads / 32];
+  __shared__ int s_sums[1][C::kThreads / 32];
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -374,212 +251,23 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
 
   // ------------------------------------------------ this block's share of the steps
   uint32_t* status = p.cta_status + 2 * blockIdx.x;
-  const int per = (p.B + C::kThreads - 1) / C::kThreads;
-  const int rb0 = min(p.B, (int)threadIdx.x * per), rb1 = min(p.B, rb0 + per);
-  int mine[LM], incl[LM];                        // the host bounds the total below 2^31
-#pragma unroll
-  for (int z = 0; z < LM; ++z) mine[z] = 0;
-  bool bad_req = false;
-  Req R;
-#pragma unroll 1
-  for (int b = rb0; b < rb1; ++b) {
-    R = load_req<N>(p, b);
-    bad_req |= R.bad;
-#pragma unroll
-    for (int z = 0; z < LM; ++z) mine[z] += p.Hkv * lane_tiles(p, R, z) * (R.nkt + C::kUnitCost);
-  }
-#pragma unroll
-  for (int z = 0; z < LM; ++z) {
-    incl[z] = mine[z];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl[z], o);
-      if (lane >= o) incl[z] += y;
-    }
-    if (lane == 31) s_sums[z][warp] = incl[z];
-  }
-  if (threadIdx.x == 0) {
-    status[0] = 0;
-    status[1] = 0;
-    p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-  }
-  tc_fence_before();
-  const bool any_bad = __syncthreads_or(bad_req);
-  tc_fence_after();
-  int total = 0, before[LM];                     // before: steps ahead of this warp's, lane by lane
-#pragma unroll
-  for (int z = 0; z < LM; ++z)
-#pragma unroll
-    for (int w = 0; w < C::kThreads / 32; ++w) {
-      if (w == warp) before[z] = total;
-      total += s_sums[z][w];
-    }
-  if (any_bad && blockIdx.x == 0 && threadIdx.x == 0) raise_status(status, kDevIndex, 0x40);
-  // blocks [0, rem) take quo + 1 steps, the others quo
-  const int quo = total / (int)gridDim.x, rem = total - quo * (int)gridDim.x;
-  const int blk = (int)blockIdx.x;
-  const int f0 = blk * quo + min(blk, rem), steps = quo + (blk < rem ? 1 : 0);
-#pragma unroll
-  for (int z = 0; z < LM; ++z) {
-    int at = before[z] + incl[z] - mine[z];
-    if (steps > 0 && f0 >= at && f0 < at + mine[z]) {
-#pragma unroll 1
-      for (int b = rb0; b < rb1; ++b) {
-        if (per > 1) R = load_req<N>(p, b);
-        const int nt = lane_tiles(p, R, z), cost = R.nkt + C::kUnitCost, c = p.Hkv * nt * cost;
-        if (f0 >= at + c) { at += c; continue; }
-        const int off = f0 - at, u = off / cost;
-        Unit v;
-        v.R = R;
-        v.z = z;
-        v.b = b;
-        v.k0 = off - u * cost;              // from nkt on: the unit's steps are all done
-        v.k1 = min(R.nkt, v.k0 + steps);
-        v.h = N < 128 ? u : u / nt;
-        v.rt = z + (u - v.h * nt) * p.lanes;
-        s_start = v;
-        break;
-      }
-    }
-  }
-  __syncthreads();
+  const Share share = find_share<1, C::kThreads, C::kUnitCost>(p, status, &s_start, s_sums);
   const uint32_t tmem = *tmem_slot;
   const Bound W{abort_flag, p.wait_ns};
   auto colS = [](int s) { return (uint32_t)(s * N); };
   auto colO = [](int s) { return (uint32_t)((2 + s) * N); };
 
-  // a reader's next unit, number lu: copied, and its place given back
-  auto take = [&](int lu, Unit& u) -> bool {
-    const int s = lu % kUnits;
-    bool ok = spin(bar(bUF + s), (lu / kUnits) & 1, W, 0x900);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) return false;
-    u = s_unit[s];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(bUE + s));
-    return u.k1 > 0;
-  };
+  const UnitRing units_ring{s_unit, bar(bUF), bar(bUE)};
+  auto take = [&](int lu, Unit& u) -> bool { return tree::take(units_ring, lu, u, W); };
 
   if (warp < 4) {
     if constexpr (N >= 64) regs_dec<C::kRegCtl>();
     if (warp == 0 || warp == 3) {
-      // --------------------------- producers: warp 0 of K, warp 3 of Q and V.
-      // Each follows its own ring, so a K tile never waits behind a V tile
-      const int y = warp == 3;
-      const int depth = y ? VS : KS, full0 = y ? bVF : bKF, empty0 = y ? bVE : bKE;
-      const uint32_t ring = smem_u32(y ? sV : sK);
-      const CUtensorMap* const cmap = y ? &vcmap : &kcmap;
-      const CUtensorMap* const c8map = y ? &vc8map : &kc8map;
-      const CUtensorMap* const nmap = y ? &vmap : &kmap;
-      const int box_shift = min(p.page_shift, 7);
-      // a lane's copy of a step: box x of key-row group g by lane g * NB + x.
-      // Groups are whole boxes of a page, or 8 rows where new rows follow.
-      // The page id is asked for a step ahead of its use
-      const int g = lane / NB, x = lane % NB;
-      struct Copy { int page, row, h, key; bool fresh, cached, want; };
-      bool ok = true;
-      Unit w;
-      // the K producer also lays out the block's units for the other warps
-      int k = 0, lu = 0, left = steps;
-      bool begun = y || steps == 0;
-      w.k1 = 0;
-      auto advance = [&]() -> bool {
-        if (y) {
-          if (!take(lu, w)) return false;
-          // Q too, the rows of npt nodes (nodes behind the request's are
-          // columns that nobody reads)
-          const int sq = lu % QS;
-          if (lu >= QS) ok = spin(bar(bQE + sq), ((lu / QS) - 1) & 1, W, 0x600);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) return false;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(bQF + sq), (uint32_t)(NB * p.npt * p.G * 128));
-            for (int x = 0; x < NB; ++x)
-              tma_load_3d(smem_u32(sQ + sq * C::kQ) + x * C::kQBox, &qmap, bar(bQF + sq), x * 64,
-                          w.h * p.G, w.R.r0 + w.rt * p.npt);
-          }
-          __syncwarp();
-        } else {
-          bool more;
-          if (!begun) {
-            begun = true;
-            w = s_start;
-            left -= w.R.nkt + C::kUnitCost - w.k0;
-            more = w.k1 > w.k0 || next_unit<N, C::kUnitCost>(p, w, left);
-          } else {
-            more = steps > 0 && next_unit<N, C::kUnitCost>(p, w, left);
-          }
-          const int sl = lu % kUnits;
-          if (lu >= kUnits) {
-            ok = spin(bar(bUE + sl), ((lu / kUnits) - 1) & 1, W, 0x910);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) return false;
-          }
-          if (lane == 0) {
-            if (more) s_unit[sl] = w;
-            else s_unit[sl].k1 = 0;
-            mbar_arrive(bar(bUF + sl));
-          }
-          __syncwarp();
-          if (!more) return false;
-        }
-        k = w.k0;
-        ++lu;
-        return true;
-      };
-      auto fetch = [&](Copy& c) -> bool {
-        if (k >= w.k1 && !advance()) return false;
-        c.fresh = k >= w.R.kt;
-        c.h = w.h;
-        c.key = g << (c.fresh ? 3 : box_shift);
-        c.cached = !c.fresh || c.key < w.R.a;
-        c.want = c.key < w.keys(k);
-        c.page = 0;
-        c.row = w.R.r0 + (k - w.R.kt) * kKeys + c.key - w.R.a;
-        if (c.want && c.cached) {
-          const int at = k * kKeys + c.key;
-          c.page = p.table[(int64_t)w.b * p.table_stride + (at >> p.page_shift)];
-          c.row = at & ((1 << p.page_shift) - 1);
-        }
-        ++k;
-        return true;
-      };
-      // one copy is made while the next one's page id is on its way; the first
-      // round only asks
-      Copy cur, nxt;
-      cur.h = -1;
-      int t = 0, issued = 0;
-      for (bool more = true; more;) {
-        more = fetch(nxt);
-        if (cur.h < 0) { cur = nxt; continue; }
-        if (cur.cached && cur.want && (cur.page < 0 || cur.page >= p.n_pages)) {
-          cur.want = false;
-          raise_status(status, kDevIndex, 0x41);
-        }
-        const uint32_t each = 128u << (cur.fresh ? 3 : box_shift);
-        const uint32_t bytes = each * __popc(__ballot_sync(0xffffffffu, cur.want));
-        const int sl = t % depth;
-        if (t >= depth) {
-          ok = spin(bar(empty0 + sl), ((t / depth) - 1) & 1, W, 0x100 + y);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(bar(full0 + sl), bytes);
-        __syncwarp();
-        if (cur.want) {
-          const uint32_t d = ring + sl * C::kTile + (uint32_t)(x * C::kBox + cur.key * 128);
-          if (cur.cached) tma_load_4d(d, cur.fresh ? c8map : cmap, bar(full0 + sl), x * 64, cur.h, cur.row, cur.page);
-          else tma_load_3d(d, nmap, bar(full0 + sl), x * 64, cur.h, cur.row);
-        }
-        issued = ++t;
-        cur = nxt;
-      }
-      __syncwarp();
-      // drain: every copy has landed before the block exits
-      for (int i = max(0, issued - depth); i < issued; ++i)
-        wait_drain(bar(full0 + i % depth), (i / depth) & 1);
-      if (y)
-        for (int i = max(0, lu - QS); i < lu; ++i) wait_drain(bar(bQF + i % QS), (i / QS) & 1);
+      const bool y = warp == 3;
+      const Producer io{y ? &vcmap : &kcmap, y ? &vc8map : &kc8map, y ? &vmap : &kmap, &qmap,
+                        smem_u32(y ? sV : sK), smem_u32(sQ), bar(y ? bVF : bKF), bar(y ? bVE : bKE),
+                        bar(bQF), bar(bQE), y ? VS : KS, units_ring, &s_start};
+      produce<NB, 1, N, QS, C::kUnitCost>(p, io, y, share.steps, status, W);
     } else if (warp == 1) {
       // --------------------------------------------------------------- MMA
       // the warp walks together and one elected lane issues, so loop state and
@@ -759,52 +447,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                   atomicOr(&m[j * NW + x], bit_range(lo - 32 * x, hi - 32 * x));
             }
           }
-          // New rows whose V holds a NaN or an infinity (see the softmax). A few
-          // are read from memory, one trip that is over before their tile is
-          // there; more than that from the tiles the producer brought, which
-          // stay until the softmax has used this unit's masks (64 rows from
-          // memory took 20 us of the loaded HBM's latency; one decoded row
-          // from its tile 0.8 us more than this)
-          auto odd = [](const uint32_t* x) {
-            bool nf = false;
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              nf |= (x[y] & 0x7f80u) == 0x7f80u || (x[y] & 0x7f800000u) == 0x7f800000u;
-            return nf;
-          };
-          constexpr int LPR = D / 8, RPI = 32 / LPR, U = 4;   // lanes a row, rows a load, loads in flight
-          const bool few = w.R.n <= U * RPI;
-          if (few) {
-            const __nv_bfloat16* src = p.v + (int64_t)w.R.r0 * p.vs + w.h * D + lane % LPR * 8;
-            uint4 u[U];
-#pragma unroll
-            for (int e = 0; e < U; ++e)
-              u[e] = *reinterpret_cast<const uint4*>(src + (int64_t)min(e * RPI + lane / LPR, w.R.n - 1) * p.vs);
-#pragma unroll
-            for (int e = 0; e < U; ++e) {
-              const uint32_t x[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
-              if (odd(x)) atomicOr(&sNf[sm * 8], 1u << min(e * RPI + lane / LPR, w.R.n - 1));
-            }
-          }
-          for (int k = max(w.k0, w.R.kt); ok && !few && k < w.k1; ++k) {
-            const int t = t0 + k - w.k0, kv = w.keys(k), a = k == w.R.kt ? w.R.a : 0;
-            ok = spin(bar(bVF + t % VS), (t / VS) & 1, W, 0x620);
-            ok = __all_sync(0xffffffffu, ok);
-            const uint32_t tile = smem_u32(sV + (t % VS) * C::kTile);
-            for (int r = a + lane; ok && r < kv; r += 32) {
-              bool nf = false;
-#pragma unroll 4
-              for (int c = 0; c < 8 * NB; ++c) {               // any order: lanes spread over the banks
-                uint32_t x[4];
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                             : "r"(tile + (c >> 3) * C::kBox + r * 128 + (((c + r) & 7) << 4)) : "memory");
-                nf |= odd(x);
-              }
-              const int j = (k - w.R.kt) * kKeys + r - w.R.a;
-              if (nf) atomicOr(&sNf[sm * 8 + (j >> 5)], 1u << (j & 31));
-            }
-          }
+          ok = scan_new_rows<NB, VS>(p, w, sNf + sm * 8, t0, smem_u32(sV), bar(bVF), W);
           if (!ok) break;
         }
         t0 += w.k1 - w.k0;
@@ -1162,12 +805,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
             }
           }
         }
-        if (!whole && w.k0 == 0 && lane == 0) {
-          // the unit starts here at f1 - k1 and reaches into later blocks
-          const int last = f0 + steps - w.k1 + w.R.nkt - 1, cut = rem * (quo + 1);
-          const int lastb = last < cut ? last / (quo + 1) : rem + (last - cut) / quo;
-          p.meta[blockIdx.x] = make_int4(w.R.r0 + node0, rows, w.h, (int)(lastb - blockIdx.x + 1));
-        }
+        if (!whole && w.k0 == 0 && lane == 0)
+          p.meta[blockIdx.x] = make_int4(w.R.r0 + node0, rows, w.h, share.pieces(w));
       }
       float* inv = sInv + sw * N;
 #pragma unroll
@@ -1263,6 +902,7 @@ struct CombineParams {
 };
 
 constexpr int kCombineWarps = 8;
+constexpr int kNarrowMax = 128;
 
 template <int D, int N>
 __global__ void __launch_bounds__(32 * kCombineWarps) mis_tree_combine_kernel(const CombineParams p) {
@@ -1366,16 +1006,17 @@ mis_status_t check_desc(const mis_tree_desc* d, const mis_paged_cache* c) {
   return MIS_OK;
 }
 
-// Rows of a tile: the smallest that holds all rows of a request's kv head.
-int tile_rows(const mis_tree_desc* d, const mis_paged_cache* c) {
+// Rows of a unit: the smallest tile that holds all rows of a request's kv
+// head, or two tiles of 128.
+int unit_rows(const mis_tree_desc* d, const mis_paged_cache* c) {
   const int64_t rows = (int64_t)d->max_nodes * (d->Hq / c->Hkv);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= kNarrowMax ? 128 : 256;
 }
 
 struct TreeWs { size_t status, meta, ml, part, total; };
 
 TreeWs workspace_of(const mis_tree_desc* d, const mis_paged_cache* c) {
-  const size_t G = (size_t)num_sms(), N = (size_t)tile_rows(d, c);
+  const size_t G = (size_t)num_sms(), N = (size_t)unit_rows(d, c);
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   TreeWs w;
   w.status = kStatusBytes;
@@ -1389,12 +1030,17 @@ TreeWs workspace_of(const mis_tree_desc* d, const mis_paged_cache* c) {
 template <int D, int N>
 mis_status_t launch_tree(const CUtensorMap* m, const TreeParams& p, const CombineParams& c,
                          cudaStream_t st) {
-  using Cf = TreeCfg<D, N>;
-  auto kern = mis_tree_attn_kernel<D, N>;
-  if (!kernel_attr_once(reinterpret_cast<const void*>(kern), Cf::kSmem)) return MIS_ERR_CUDA;
-  if (launch_pdl(kern, dim3((unsigned)c.blocks), dim3(Cf::kThreads), Cf::kSmem, st, m[0],
-                 m[1], m[2], m[3], m[4], m[5], m[6], p) != cudaSuccess)
-    return MIS_ERR_CUDA;
+  if constexpr (N <= 128) {
+    using Cf = TreeCfg<D, N>;
+    auto kern = mis_tree_attn_kernel<D, N>;
+    if (!kernel_attr_once(reinterpret_cast<const void*>(kern), Cf::kSmem)) return MIS_ERR_CUDA;
+    if (launch_pdl(kern, dim3((unsigned)c.blocks), dim3(Cf::kThreads), Cf::kSmem, st, m[0],
+                   m[1], m[2], m[3], m[4], m[5], m[6], p) != cudaSuccess)
+      return MIS_ERR_CUDA;
+  } else {
+    const mis_status_t r = launch_wide(D, m, p, c.blocks, st);
+    if (r != MIS_OK) return r;
+  }
   return launch_pdl(mis_tree_combine_kernel<D, N>, dim3((unsigned)c.blocks, N / kCombineWarps),
                     dim3(32 * kCombineWarps), 0, st, c) == cudaSuccess
              ? MIS_OK
@@ -1467,7 +1113,7 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     // Q by the rows of a tile's nodes
     const uint64_t qd[3] = {(uint64_t)D, (uint64_t)desc->Hq, (uint64_t)desc->T};
     const uint64_t qst[2] = {(uint64_t)D * 2, (uint64_t)q_row_stride * 2};
-    const int N = tile_rows(desc, cache), G = desc->Hq / cache->Hkv, npt = N / G;
+    const int N = unit_rows(desc, cache), G = desc->Hq / cache->Hkv, npt = std::min(N, 128) / G;
     const uint32_t qb[3] = {64, (uint32_t)G, (uint32_t)npt};
     const CUtensorMap maps[7] = {
         encode_tmap_bf16(q, 3, qd, qst, qb, &ok),
@@ -1487,10 +1133,10 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     p.table = block_table; p.table_stride = block_table_stride;
     p.cache_len = cache_len; p.cu = cu_nodes; p.parents = parents;
     p.B = desc->B; p.T = desc->T; p.Hkv = cache->Hkv;
-    p.G = G; p.npt = npt;
+    p.G = G; p.npt = npt; p.npu = N > 128 ? 2 * npt : npt;
     p.g_magic = (uint32_t)((0xffffffffull + (uint64_t)p.G) / (uint64_t)p.G);
     p.max_nodes = desc->max_nodes;
-    p.lanes = N < 128 ? 1 : std::min((desc->max_nodes + npt - 1) / npt, 2);
+    p.lanes = std::min((desc->max_nodes + p.npu - 1) / p.npu, 2);
     p.scale_log2 = (desc->scale != 0.f ? desc->scale : 1.f / std::sqrt((float)D)) * 1.4426950408889634f;
     p.cta_status = reinterpret_cast<uint32_t*>(base + ws.status);
     p.meta = reinterpret_cast<int4*>(base + ws.meta);
@@ -1507,12 +1153,14 @@ extern "C" mis_status_t mis_tree_attention_fwd(
       if (N == 16) return launch_tree<128, 16>(maps, p, c, st);
       if (N == 32) return launch_tree<128, 32>(maps, p, c, st);
       if (N == 64) return launch_tree<128, 64>(maps, p, c, st);
-      return launch_tree<128, 128>(maps, p, c, st);
+      if (N == 128) return launch_tree<128, 128>(maps, p, c, st);
+      return launch_tree<128, 256>(maps, p, c, st);
     }
     if (N == 16) return launch_tree<64, 16>(maps, p, c, st);
     if (N == 32) return launch_tree<64, 32>(maps, p, c, st);
     if (N == 64) return launch_tree<64, 64>(maps, p, c, st);
-    return launch_tree<64, 128>(maps, p, c, st);
+    if (N == 128) return launch_tree<64, 128>(maps, p, c, st);
+    return launch_tree<64, 256>(maps, p, c, st);
   } catch (...) {
     return MIS_ERR_CUDA;
   }

@@ -1,0 +1,551 @@
+// Tree attention for requests with many rows a kv head (more than a tile of
+// 128), sm_103a: the products the usual way round,
+//     S [128 rows x 128 keys] = Q K^T,     O [128 rows x D] += P V,
+// for two row tiles that share every K and V tile. A thread owns a row: its
+// maximum, sum and reference stay in registers, P goes to tensor memory, and
+// one tile's softmax runs during the other's products.
+//
+// Everything else (units, shares, copies, pieces) is as in mis_tree.cu; a unit
+// is a pair of row tiles.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "mis_internal.h"
+#include "mis_ptx.cuh"
+#include "mis_tree.cuh"
+
+namespace mis {
+namespace tree {
+namespace {
+
+template <int D>
+struct WideCfg {
+  static constexpr int kNB = D / 64;             // 64-column boxes of a row
+  static constexpr int kThreads = 384;
+  // Register budgets of the warpgroups: their sum is the launch's, 384 x 168
+  static constexpr int kRegCtl = 88, kRegSoft = 208;
+  static_assert(128 * (kRegCtl + 2 * kRegSoft) <= kThreads * 168, "register split exceeds the launch allocation");
+  static constexpr int kBox = kKeys * 128;
+  static constexpr int kTile = kNB * kBox;       // of K, V and Q alike
+  static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 2 : 4;
+  static constexpr int kUnitCost = 4;            // see TreeCfg
+  static constexpr int kW = MIS_TREE_MAX_NODES / 32;    // words of a node's mask
+  static constexpr int oMask = 0;                       // [2][256][kW] new keys that a node sees
+  static constexpr int oDead = oMask + 2 * MIS_TREE_MAX_NODES * kW;   // [2][kW] unused nodes
+  static constexpr int oNf = oDead + 2 * kW;            // [2][kW] keys with a non-finite value
+  static constexpr int oPar = oNf + 2 * kW;             // [256] int16: parents
+  static constexpr int kWords = oPar + MIS_TREE_MAX_NODES / 2;
+  static constexpr int kData = (2 + kK + kV) * kTile;
+  static constexpr int kSmem = kData + 4 * kWords + 512 + 1024;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
+mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ CUtensorMap kcmap,
+                     const __grid_constant__ CUtensorMap vcmap,
+                     const __grid_constant__ CUtensorMap kc8map,
+                     const __grid_constant__ CUtensorMap vc8map,
+                     const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
+  using C = WideCfg<D>;
+  constexpr int NB = C::kNB, KS = C::kK, VS = C::kV, W8 = C::kW;
+  // barriers
+  constexpr int bQF = 0, bQE = bQF + 1, bKF = bQE + 1, bKE = bKF + KS, bVF = bKE + KS, bVE = bVF + VS,
+                bSF = bVE + VS, bPF = bSF + 2, bOF = bPF + 2, bSE = bOF + 2, bMF = bSE + 2,
+                bUF = bMF + 2, bUE = bUF + kUnits, bDR = bUE + kUnits, nBar = bDR + 1;
+  static_assert(nBar * 8 + 64 <= 512, "barrier space");
+
+  griddep_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + 2 * C::kTile;
+  uint8_t* sV = sK + KS * C::kTile;
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem + C::kData);
+  uint32_t* sMask = words + C::oMask;
+  uint32_t* sDead = words + C::oDead;
+  uint32_t* sNf = words + C::oNf;
+  int16_t* sPar = reinterpret_cast<int16_t*>(words + C::oPar);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(words + C::kWords);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + nBar);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  __shared__ Unit s_start, s_unit[kUnits];
+  __shared__ int s_sums[2][C::kThreads / 32];
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    mbar_init(bar(bQF), 1);
+    mbar_init(bar(bQE), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(bSF + s), 1);
+      mbar_init(bar(bPF + s), 4);
+      mbar_init(bar(bOF + s), 1);
+      mbar_init(bar(bSE + s), 8);
+      mbar_init(bar(bMF + s), 1);
+    }
+    for (int s = 0; s < KS; ++s) { mbar_init(bar(bKF + s), 1); mbar_init(bar(bKE + s), 1); }
+    for (int s = 0; s < VS; ++s) { mbar_init(bar(bVF + s), 1); mbar_init(bar(bVE + s), 1); }
+    mbar_init(bar(bDR), 1);
+    for (int s = 0; s < kUnits; ++s) {
+      mbar_init(bar(bUF + s), 1);
+      mbar_init(bar(bUE + s), 11);         // every warp but the K producer
+    }
+    fence_mbar_init();
+    fence_proxy_async();
+    tma_prefetch_desc(&qmap); tma_prefetch_desc(&kcmap); tma_prefetch_desc(&vcmap);
+    tma_prefetch_desc(&kc8map); tma_prefetch_desc(&vc8map);
+    tma_prefetch_desc(&kmap); tma_prefetch_desc(&vmap);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  griddep_wait();
+
+  uint32_t* status = p.cta_status + 2 * blockIdx.x;
+  const Share share = find_share<2, C::kThreads, C::kUnitCost>(p, status, &s_start, s_sums);
+  const uint32_t tmem = *tmem_slot;
+  const Bound W{abort_flag, p.wait_ns};
+  // tensor memory: S_0 | S_1 | O_0 | O_1; P, as bf16 pairs, in the first half of S
+  auto colS = [](int x) { return (uint32_t)(x * 128); };
+  auto colO = [](int x) { return (uint32_t)(256 + x * D); };
+  const UnitRing units_ring{s_unit, bar(bUF), bar(bUE)};
+  auto take = [&](int lu, Unit& u) -> bool { return tree::take(units_ring, lu, u, W); };
+
+  if (warp < 4) {
+    regs_dec<C::kRegCtl>();
+    if (warp == 0 || warp == 3) {
+      const bool y = warp == 3;
+      const Producer io{y ? &vcmap : &kcmap, y ? &vc8map : &kc8map, y ? &vmap : &kmap, &qmap,
+                        smem_u32(y ? sV : sK), smem_u32(sQ), bar(y ? bVF : bKF), bar(y ? bVE : bKE),
+                        bar(bQF), bar(bQE), y ? VS : KS, units_ring, &s_start};
+      produce<NB, 2, 128, 1, C::kUnitCost>(p, io, y, share.steps, status, W);
+    } else if (warp == 1) {
+      // --------------------------------------------------------------- MMA
+      // The warp walks together and one elected lane issues, so loop state and
+      // descriptors stay in uniform registers. A tile's S of the next step
+      // follows its PV at once; meanwhile the other tile's softmax goes on
+      constexpr uint32_t idS = idesc_bf16(128, 128, false);
+      constexpr uint32_t idO = idesc_bf16(128, D, true);
+      auto wait_all = [&](int b, uint32_t parity, uint32_t where) -> bool {
+        const bool r = spin(bar(b), parity, W, where);
+        return __all_sync(0xffffffffu, r);
+      };
+      bool ok = true;
+      if (p.stall) ok = wait_all(bDR, 0, 0x7ff);               // nothing arrives before the drain
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      struct Ring { int slot; uint32_t ph; };
+      auto turn = [](Ring& r, int depth) { if (++r.slot == depth) { r.slot = 0; r.ph ^= 1; } };
+      Ring rk{0, 0}, rv{0, 0};
+      uint32_t pf0 = 0, pf1 = 0, qf = 0;                       // phases of P and Q
+      // S of tile x with the K tile at rk; the last tile's releases it, the
+      // unit's last step Q
+      auto issue_s = [&](int x, bool done, bool last) {
+        tc_fence_after();
+        const uint32_t dst = tm + colS(x);
+        const uint64_t a = sdesc_sw128(smem_u32(sQ) + x * C::kTile, 16, 1024);
+        const uint64_t b = sdesc_sw128(smem_u32(sK) + rk.slot * C::kTile, 16, 1024);
+        if (elect_uniform()) {
+#pragma unroll
+          for (int e = 0; e < NB; ++e)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss(dst, a + ((e * C::kBox + ks * 32) >> 4), b + ((e * C::kBox + ks * 32) >> 4), idS,
+                     (e | ks) != 0);
+          mma_commit(bar(bSF + x));
+          if (done) mma_commit(bar(bKE + rk.slot));
+          if (done && last) mma_commit(bar(bQE));
+        }
+        __syncwarp();
+      };
+      // PV of tile x: V is MN-major, 8-key groups 1024 B apart, 64-column boxes
+      // kBox apart
+      auto issue_pv = [&](int x, uint32_t acc, int nks, bool done, bool last) {
+        tc_fence_after();
+        const uint32_t dst = tm + colO(x), a = tm + colS(x);
+        const uint64_t b = sdesc_sw128(smem_u32(sV) + rv.slot * C::kTile, C::kBox, 1024);
+        if (elect_uniform()) {
+          mma_ts(dst, a, b, idO, acc);
+          if (nks == kKeys / 16) {
+#pragma unroll
+            for (int ks = 1; ks < kKeys / 16; ++ks) mma_ts(dst, a + ks * 8, b + ks * 128, idO, 1u);
+          } else {
+#pragma unroll 1
+            for (int ks = 1; ks < nks; ++ks) mma_ts(dst, a + ks * 8, b + ks * 128, idO, 1u);
+          }
+          if (done) mma_commit(bar(bVE + rv.slot));
+          if (last) mma_commit(bar(bOF + x));
+        }
+        __syncwarp();
+      };
+      Unit w;
+      for (int lu = 0; ok && take(lu, w); ++lu) {
+        const int k0 = __shfl_sync(0xffffffffu, w.k0, 0), k1 = __shfl_sync(0xffffffffu, w.k1, 0);
+        const bool pair = __shfl_sync(0xffffffffu, w.R.n - w.rt * p.npu, 0) > p.npt;
+        ok = wait_all(bQF, qf, 0x200) && wait_all(bKF + rk.slot, rk.ph, 0x300);
+        if (!ok) break;
+        qf ^= 1;
+        issue_s(0, !pair, k0 + 1 == k1);
+        if (pair) issue_s(1, true, k0 + 1 == k1);
+        turn(rk, KS);
+        for (int k = k0; k < k1; ++k) {
+          const bool more = k + 1 < k1, last2 = k + 2 == k1;
+          const uint32_t acc = k > k0 ? 1u : 0u;
+          const int nks = (__shfl_sync(0xffffffffu, w.keys(k), 0) + 15) >> 4;
+          if (!(ok = wait_all(bVF + rv.slot, rv.ph, 0x310) && wait_all(bPF, pf0, 0x400))) break;
+          pf0 ^= 1;
+          issue_pv(0, acc, nks, !pair, !more);
+          if (more) {
+            if (!(ok = wait_all(bKF + rk.slot, rk.ph, 0x320))) break;
+            issue_s(0, !pair, last2);
+          }
+          if (pair) {
+            if (!(ok = wait_all(bPF + 1, pf1, 0x410))) break;
+            pf1 ^= 1;
+            issue_pv(1, acc, nks, true, !more);
+            if (more) issue_s(1, true, last2);
+          }
+          turn(rv, VS);
+          if (more) turn(rk, KS);
+        }
+      }
+      // drain: all tensor-core work of the elected lane completes before dealloc
+      if (elect_uniform()) mma_commit(bar(bDR));
+      __syncwarp();
+      wait_drain(bar(bDR), 0);
+    } else {
+      // ------------------------------------------------------ the tree's masks
+      int lu = 0, t0 = 0;                                // t0: steps of the units before
+      bool ok = true, bad = false;
+      Unit w;
+      while (ok && take(lu, w)) {
+        const int sm = lu & 1, n = w.R.n;
+        if (lu >= 2) ok = spin(bar(bSE + sm), ((lu >> 1) - 1) & 1, W, 0x610);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const bool tree = w.k1 > w.R.kt;
+        if (lane < W8) sNf[sm * W8 + lane] = 0;
+        __syncwarp();
+        // parents: the index, or -1 for roots, for children of unused nodes and
+        // for what is no index; unused nodes themselves -2. A node's ancestors
+        // among its batch of 32 are walked (they share a word), those before
+        // are the ancestors of the first one before the batch
+        uint32_t* m = sMask + sm * MIS_TREE_MAX_NODES * W8;
+#pragma unroll 1
+        for (int b0 = 0; b0 < MIS_TREE_MAX_NODES; b0 += 32) {
+          const int i = b0 + lane, wi = b0 >> 5;
+          int up = i - 1;
+          if (p.parents) {
+            up = MIS_TREE_ROOT;
+            if (i < n) {
+              up = p.parents[w.R.r0 + i];
+              if (up >= i || up < MIS_TREE_UNUSED) { up = MIS_TREE_ROOT; bad = true; }
+              if (up >= 0 && p.parents[w.R.r0 + up] == MIS_TREE_UNUSED) up = MIS_TREE_ROOT;
+            }
+            sPar[i] = (int16_t)up;
+          }
+          const bool dead = i < n && up == MIS_TREE_UNUSED;
+          const uint32_t dw = __ballot_sync(0xffffffffu, dead);
+          if (lane == 0) sDead[sm * W8 + wi] = dw;
+          if (!tree || b0 >= n) continue;
+          __syncwarp();
+          uint32_t own = 0;
+          int j = -1;
+          if (i < n && !dead) {
+            if (p.parents) {
+              for (j = i; j >= b0; j = sPar[j]) own |= 1u << (j & 31);
+            } else {
+              own = 0xffffffffu >> (31 - lane);
+              j = b0 - 1;
+            }
+          }
+          if (i < n) {
+#pragma unroll 1
+            for (int x = 0; x < W8; ++x) m[i * W8 + x] = x == wi ? own : x < wi && j >= 0 ? m[j * W8 + x] : 0u;
+          }
+          __syncwarp();
+        }
+        if (tree) ok = scan_new_rows<NB, VS>(p, w, sNf + sm * W8, t0, smem_u32(sV), bar(bVF), W);
+        if (!ok) break;
+        t0 += w.k1 - w.k0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bMF + sm));
+        ++lu;
+      }
+      __syncwarp();
+      if (bad) raise_status(status, kDevIndex, 0x42);
+    }
+  } else {
+    // ------------------------------------------------- softmax and epilogue
+    regs_inc<C::kRegSoft>();
+    const int x = (warp - 4) >> 2, sw = warp & 3, r = sw * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
+    const uint32_t tS = tl + colS(x), tO = tl + colO(x);
+    // scores are taken times the scale's sign, then scaled by its size
+    const float sa = fabsf(p.scale_log2);
+    const bool neg = p.scale_log2 < 0.f;
+    const uint64_t sax2 = f2_pack(__float_as_uint(sa), __float_as_uint(sa));
+    const int box_shift = min(p.page_shift, 7), boxes = kKeys >> box_shift;
+    Unit w;
+    uint32_t cs = 0, co = 0;                             // S tiles and units of this row tile so far
+    int lu = 0, tk = 0;                                  // tk: steps of the block's units so far
+    bool ok = true;
+    while (ok && take(lu, w)) {
+      const int slot = lu & 1, node0 = w.rt * p.npu + x * p.npt;
+      const int rows = min(p.npt, w.R.n - node0) * p.G;
+      if (rows <= 0) {
+        // no such tile in this unit; its masks' place is given back all the same
+        ok = spin(bar(bMF + slot), (lu >> 1) & 1, W, 0x701);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(bar(bSE + slot));
+        tk += w.k1 - w.k0;
+        ++lu;
+        continue;
+      }
+      const int i = over_g(p, min(r, rows - 1));         // the row's node
+      const uint32_t* mrow = sMask + (slot * MIS_TREE_MAX_NODES + node0 + i) * W8;
+      float m = kEmpty, l = 0.f;
+      // the page under box `lane` of a step, asked for a step ahead (0 where
+      // there is no cached row)
+      const int32_t* trow = p.table + (int64_t)w.b * p.table_stride;
+      auto page_of = [&](int k) {
+        const int at = k * kKeys + (lane << box_shift);
+        return k < w.k1 && lane < boxes && at < w.R.L ? trow[at >> p.page_shift] : 0;
+      };
+      int page = page_of(w.k0);
+#pragma unroll 1
+      for (int k = w.k0; k < w.k1; ++k, ++cs) {
+        const int kv = w.keys(k);
+        const bool fresh = k >= w.R.kt;
+        const uint32_t pages = __ballot_sync(0xffffffffu, page >= 0 && page < p.n_pages);
+        page = page_of(k + 1);
+        const bool plain = !fresh && kv == kKeys && pages == 0xffffffffu;
+        ok = spin(bar(bSF + x), cs & 1, W, 0x710);
+        if (ok && fresh) ok = spin(bar(bMF + slot), (lu >> 1) & 1, W, 0x720);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        // the whole row of scores in registers
+        uint32_t s[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) tmem_ld32(tS + c, s + c);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) reg_fence32(s + c);
+        if (neg) {
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) s[c] ^= 0x80000000u;
+        }
+        if (!plain) {
+          // keys by words of 32: cached rows on pages of the cache, then new row
+          // j0 + c for key c where the row's mask has it
+          const int j0 = (k - w.R.kt) * kKeys - w.R.a;
+          bool there = false;                            // key row r holds something
+#pragma unroll
+          for (int q = 0; q < kKeys / 32; ++q) {
+            uint32_t vis = bit_range(-32 * q, w.R.L - k * kKeys - 32 * q);
+            if (pages != 0xffffffffu) {
+#pragma unroll 1
+              for (int b = 0; b < boxes; ++b)
+                if (!((pages >> b) & 1u)) vis &= ~bit_range((b << box_shift) - 32 * q, ((b + 1) << box_shift) - 32 * q);
+            }
+            if (q == sw) there = (vis >> lane) & 1u;
+            if (fresh) {
+              const int at = j0 + 32 * q, wd = at >> 5;
+              const uint32_t lo = wd >= 0 && wd < W8 ? mrow[wd] : 0u;
+              const uint32_t hi = wd + 1 >= 0 && wd + 1 < W8 ? mrow[wd + 1] : 0u;
+              vis |= __funnelshift_r(lo, hi, at & 31);
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((vis >> c) & 1u)) s[32 * q + c] = 0xff800000u;
+          }
+          // a V row that nobody sees must not meet a zero probability with a NaN
+          // or an infinity; a new one that some rows see leaves its non-finite
+          // elements to the epilogue. The first tile's warps see to it, and the
+          // second tile's product comes behind the first's
+          const int j = j0 + r;
+          const bool node = fresh && j >= 0 && j < w.R.n;
+          const bool odd = node && ((sNf[slot * W8 + (j >> 5)] >> (j & 31)) & 1u);
+          if (x == 0 && r < ((kv + 15) & ~15) && (odd || !(node || there))) {
+            const int t = tk + k - w.k0;
+            ok = spin(bar(bVF + t % VS), (t / VS) & 1, W, 0x750);
+            if (ok) {
+              const uint32_t aV = smem_u32(sV + (t % VS) * C::kTile) + r * 128;
+#pragma unroll 2
+              for (int c = 0; c < 8 * NB; ++c) {
+                const uint32_t a = aV + (c >> 3) * C::kBox + (c & 7) * 16;
+                uint32_t u[4] = {0, 0, 0, 0};
+                if (odd) {
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(a) : "memory");
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    if ((u[e] & 0x7f80u) == 0x7f80u) u[e] &= 0xffff0000u;
+                    if ((u[e] & 0x7f800000u) == 0x7f800000u) u[e] &= 0x0000ffffu;
+                  }
+                }
+                st_shared_v4(a, u[0], u[1], u[2], u[3]);
+              }
+              fence_proxy_async();
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 2)
+          mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sa);
+        const bool grow = top > m + kGrow;
+        const bool any_grow = __any_sync(0xffffffffu, grow);
+        const float alpha = grow ? ex2(m - top) : 1.f;
+        if (grow) { l *= alpha; m = top; }
+        const uint64_t off = f2_pack(__float_as_uint(-m), __float_as_uint(-m));
+        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int k2 = hf * 64 + 2 * c;
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(s[k2], s[k2 + 1]), sax2, off), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            sum[c & 3] = f2_add(sum[c & 3], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
+            pk[c] = pack_bf16(p0, p1);
+          }
+          tmem_st32(tS + hf * 32, pk);
+        }
+        {
+          float a0, a1;
+          f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a0, a1);
+          l += a0 + a1;
+        }
+        if (any_grow && k > w.k0) {
+          // S of this step was issued behind the products of the steps before,
+          // so O holds them
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t ov[32];
+            tmem_ld32(tO + c, ov);
+            tmem_ld_wait();
+            reg_fence32(ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tmem_st32(tO + c, ov);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bPF + x));
+      }
+      if (!ok) break;
+      tk += w.k1 - w.k0;
+      // ---------------------------------------------------------- epilogue
+      ok = spin(bar(bMF + slot), (lu >> 1) & 1, W, 0x801);
+      if (ok) ok = spin(bar(bOF + x), co & 1, W, 0x810);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ++co;
+      tc_fence_after();
+      const bool whole = w.k0 == 0 && w.k1 == w.R.nkt, mine = r < rows;
+      if ((sDead[slot * W8 + ((node0 + i) >> 5)] >> ((node0 + i) & 31)) & 1u) { m = kEmpty; l = 0.f; }
+      const int g = r - i * p.G;
+      const int64_t piece = 2 * (int64_t)blockIdx.x + (w.k0 == 0 ? 1 : 0);
+      const int64_t prow = piece * 256 + x * p.npt * p.G + r;      // a piece's rows lie end to end
+      const int64_t orow = (int64_t)(w.R.r0 + node0 + i);
+      if (!whole) {
+        if (mine) p.ml[prow] = make_float2(m, l);
+        if (w.k0 == 0 && threadIdx.x == 128)
+          p.meta[blockIdx.x] = make_int4(w.R.r0 + node0, min(p.npu, w.R.n - node0) * p.G, w.h, share.pieces(w));
+      } else if (mine && p.lse) {
+        p.lse[(int64_t)(w.h * p.G + g) * p.T + orow] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      }
+      const float inv = l != 0.f ? 1.f / l : 0.f;                  // NaN stays
+      uint32_t nf = 0;
+      if (w.k1 > w.R.kt)
+        for (int q = 0; q < W8; ++q) nf |= sNf[slot * W8 + q];
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t ov[32];
+        __syncwarp();
+        tmem_ld32(tO + c, ov);
+        tmem_ld_wait();
+        reg_fence32(ov);
+        if (nf) {
+#pragma unroll 1
+          for (int q = 0; q < W8; ++q)
+#pragma unroll 1
+            for (uint32_t bits = sNf[slot * W8 + q] & mrow[q]; bits; bits &= bits - 1) {
+              const __nv_bfloat16* v = p.v + (int64_t)(w.R.r0 + q * 32 + __ffs(bits) - 1) * p.vs + w.h * D + c;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float val = __bfloat162float(v[e]);
+                if (!isfinite(val)) ov[e] = __float_as_uint(__uint_as_float(ov[e]) + val);
+              }
+            }
+          __syncwarp();
+        }
+        if (!mine) continue;
+        if (!whole) {
+          uint4* dst = reinterpret_cast<uint4*>(p.part + prow * D + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          continue;
+        }
+        uint4* dst = reinterpret_cast<uint4*>(p.o + orow * p.os + (int64_t)(w.h * p.G + g) * D + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t u[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            // an empty row is zero, whatever its accumulator holds
+            const float v0 = __uint_as_float(ov[8 * e + 2 * y]), v1 = __uint_as_float(ov[8 * e + 2 * y + 1]);
+            u[y] = inv != 0.f ? pack_bf16(v0 * inv, v1 * inv) : 0u;
+          }
+          dst[e] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+      if (lane == 0) mbar_arrive(bar(bSE + slot));
+      ++lu;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) raise_status(status, kDevTimeout, *abort_flag);
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+mis_status_t launch(const CUtensorMap* m, const TreeParams& p, int blocks, cudaStream_t st) {
+  using C = WideCfg<D>;
+  auto kern = mis_tree_wide_kernel<D>;
+  if (!kernel_attr_once(reinterpret_cast<const void*>(kern), C::kSmem)) return MIS_ERR_CUDA;
+  return launch_pdl(kern, dim3((unsigned)blocks), dim3(C::kThreads), C::kSmem, st, m[0], m[1], m[2], m[3],
+                    m[4], m[5], m[6], p) == cudaSuccess
+             ? MIS_OK
+             : MIS_ERR_CUDA;
+}
+
+}  // namespace
+
+mis_status_t launch_wide(int D, const CUtensorMap* m, const TreeParams& p, int blocks, cudaStream_t st) {
+  return D == 128 ? launch<128>(m, p, blocks, st) : launch<64>(m, p, blocks, st);
+}
+
+}  // namespace tree
+}  // namespace mis
