@@ -886,9 +886,12 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
   }
 }
 
-// Adds the pieces of split units in block order: blocks (c, y) take the unit
-// whose first piece block c of the attention left, a warp a column. Block (0,
-// 0) gathers the blocks' status words.
+// Adds the pieces of split units in block order: blocks (x, c) take the unit
+// whose first piece block c of the attention left, a warp four rows of it: the
+// pieces come from L2, and what is done once a row (weights, sums) bounds the
+// kernel, so 8 lanes a row do it for four rows at a time (a warp a row: 4 us
+// longer for the 36 MB of pieces of 16 requests with 64 nodes x 4 heads). Block
+// (0, 0) gathers the blocks' status words.
 struct CombineParams {
   const uint32_t* cta_status;
   const int4* meta;
@@ -901,17 +904,18 @@ struct CombineParams {
   int32_t T, G, blocks;
 };
 
-constexpr int kCombineWarps = 8;
+template <int N>
+constexpr int kCombineWarps = N < 32 ? N / 4 : 8;
 constexpr int kNarrowMax = 128;
 
 template <int D, int N>
-__global__ void __launch_bounds__(32 * kCombineWarps) mis_tree_combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(32 * kCombineWarps<N>) mis_tree_combine_kernel(const CombineParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x;
+  const int c = blockIdx.y;
   const int4 u = p.meta[c];
-  if (c == 0 && blockIdx.y == 0 && warp == 0) {
+  if (c == 0 && blockIdx.x == 0 && warp == 0) {
     uint32_t bits = 0, where = 0;
     for (int x = lane; x < p.blocks; x += 32) {
       const uint32_t s = p.cta_status[2 * x];
@@ -926,69 +930,75 @@ __global__ void __launch_bounds__(32 * kCombineWarps) mis_tree_combine_kernel(co
       p.status[1] = where;
     }
   }
-  const int n = blockIdx.y * kCombineWarps + warp, pieces = u.w;
-  if (pieces < 2 || n >= u.y) return;
+  const int n0 = (blockIdx.x * kCombineWarps<N> + warp) * 4, pieces = u.w;
+  if (pieces < 2 || n0 >= u.y) return;
+  const int sub = lane & 7, n = min(n0 + (lane >> 3), u.y - 1);
   // piece s: the first lies in block c's second slot, the others in the first
-  // slots of the blocks that follow. Lane s looks at piece s (of 32 at a
-  // time), while the first pieces' elements are on their way
+  // slots of the blocks that follow. A row's lane s looks at piece s (of 8 at
+  // a time), while the first pieces' elements are on their way
   auto at = [&](int s) { return (int64_t)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * N + n; };
-  constexpr int E = D / 32, A = 4;
-  auto load = [&](int s, float* y) {
-    const float* src = p.part + at(s) * D + lane * E;
-    if constexpr (E == 4) {
-      const float4 z = *reinterpret_cast<const float4*>(src);
-      y[0] = z.x; y[1] = z.y; y[2] = z.z; y[3] = z.w;
-    } else {
-      const float2 z = *reinterpret_cast<const float2*>(src);
-      y[0] = z.x; y[1] = z.y;
-    }
+  constexpr int E = D / 32, A = 2;        // float4s of a lane, pieces in flight
+  auto load = [&](int s, float4* y) {
+    const float4* src = reinterpret_cast<const float4*>(p.part + at(s) * D) + sub;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = src[8 * e];
   };
-  float y[A][E], acc[E];
+  float4 y[A][E], acc[E];
 #pragma unroll
   for (int s = 0; s < A; ++s) load(min(s, pieces - 1), y[s]);
   bool stuck = false;
   float m = kEmpty;
-  for (int s = lane; s < pieces; s += 32) {
+  for (int s = sub; s < pieces; s += 8) {
     m = fmaxf(m, p.ml[at(s)].x);
     stuck |= (p.cta_status[2 * (c + s)] & kDevTimeout) != 0;
   }
   if (__any_sync(0xffffffffu, stuck)) return;          // a piece is missing
-  m = warp_max(m);
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-  for (int s0 = 0; s0 < pieces; s0 += 32) {
+  for (int s0 = 0; s0 < pieces; s0 += 8) {
     float a = 0.f;
-    if (s0 + lane < pieces) {
-      const float2 x = p.ml[at(s0 + lane)];
+    if (s0 + sub < pieces) {
+      const float2 x = p.ml[at(s0 + sub)];
       a = ex2(x.x - m);
       l += a * x.y;
     }
     __syncwarp();
-    // a piece that saw nothing weighs nothing, whatever it holds
-    for (int s1 = 0; s1 < min(32, pieces - s0); s1 += A) {
+    for (int s1 = 0; s1 < min(8, pieces - s0); s1 += A) {
       if (s0 + s1 > 0) {
 #pragma unroll
         for (int s = 0; s < A; ++s) load(min(s0 + s1 + s, pieces - 1), y[s]);
       }
 #pragma unroll
       for (int s = 0; s < A; ++s) {
-        const float b = __shfl_sync(0xffffffffu, a, s1 + s);
+        // a piece that saw nothing weighs nothing, whatever it holds
+        const float b = __shfl_sync(0xffffffffu, a, (lane & 24) + s1 + s);
+        if (b != 0.f) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = b != 0.f ? fmaf(b, y[s][e], acc[e]) : acc[e];
+          for (int e = 0; e < E; ++e) {
+            acc[e].x = fmaf(b, y[s][e].x, acc[e].x);
+            acc[e].y = fmaf(b, y[s][e].y, acc[e].y);
+            acc[e].z = fmaf(b, y[s][e].z, acc[e].z);
+            acc[e].w = fmaf(b, y[s][e].w, acc[e].w);
+          }
+        }
       }
     }
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  for (int o = 4; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (n0 + (lane >> 3) >= u.y) return;
   const int i = n / p.G, h = u.z * p.G + n - i * p.G;
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (int64_t)(u.x + i) * p.os + (int64_t)h * D + lane * E);
+  uint2* dst = reinterpret_cast<uint2*>(p.o + (int64_t)(u.x + i) * p.os + (int64_t)h * D) + sub;
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    dst[e / 2] = inv != 0.f ? pack_bf16(acc[e] * inv, acc[e + 1] * inv) : 0u;
-  if (p.lse && lane == 0)
-    p.lse[(int64_t)h * p.T + u.x + i] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  for (int e = 0; e < E; ++e)
+    dst[8 * e] = inv != 0.f ? make_uint2(pack_bf16(acc[e].x * inv, acc[e].y * inv),
+                                         pack_bf16(acc[e].z * inv, acc[e].w * inv))
+                            : make_uint2(0u, 0u);
+  if (p.lse && sub == 0) p.lse[(int64_t)h * p.T + u.x + i] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -1041,8 +1051,9 @@ mis_status_t launch_tree(const CUtensorMap* m, const TreeParams& p, const Combin
     const mis_status_t r = launch_wide(D, m, p, c.blocks, st);
     if (r != MIS_OK) return r;
   }
-  return launch_pdl(mis_tree_combine_kernel<D, N>, dim3((unsigned)c.blocks, N / kCombineWarps),
-                    dim3(32 * kCombineWarps), 0, st, c) == cudaSuccess
+  constexpr int CW = kCombineWarps<N>;
+  return launch_pdl(mis_tree_combine_kernel<D, N>, dim3(N / (4 * CW), (unsigned)c.blocks), dim3(32 * CW), 0,
+                    st, c) == cudaSuccess
              ? MIS_OK
              : MIS_ERR_CUDA;
 }

@@ -263,6 +263,8 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Producer& io,
   constexpr int kTile = NB * kKeys * 128, kBox = kKeys * 128;
   const int lane = threadIdx.x & 31;
   const int box_shift = min(p.page_shift, 7);
+  // K and V pass through L2 once, unless the units of several lanes share them
+  const uint64_t policy = p.lanes > 1 ? policy_normal() : policy_once();
   // a lane's copy of a step: box x of key-row group g by lane g * NB + x.
   // Groups are whole boxes of a page, or 8 rows where new rows follow.
   // The page id is asked for a step ahead of its use
@@ -374,7 +376,8 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Producer& io,
     __syncwarp();
     if (cur.want) {
       const uint32_t d = io.ring + sl * kTile + (uint32_t)(x * kBox + cur.key * 128);
-      if (cur.cached) tma_load_4d(d, cur.fresh ? io.c8map : io.cmap, io.full + 8 * sl, x * 64, cur.h, cur.row, cur.page);
+      if (cur.cached)
+        tma_load_4d(d, cur.fresh ? io.c8map : io.cmap, io.full + 8 * sl, x * 64, cur.h, cur.row, cur.page, policy);
       else tma_load_3d(d, io.nmap, io.full + 8 * sl, x * 64, cur.h, cur.row);
     }
     issued = ++t;

@@ -40,6 +40,27 @@ struct WideCfg {
   static_assert(kSmem <= 232448, "shared memory");
 };
 
+// Four lanes exchange the four 16-byte pieces each holds of its row: piece e
+// becomes piece lane % 4 of row e of the four. A store then covers 64 bytes of
+// 8 rows (16 bytes of 32 rows took four times as long).
+__device__ __forceinline__ void spread4(uint32_t* u, int lane) {
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e & o) continue;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint32_t give = up ? u[4 * e + y] : u[4 * (e | o) + y];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, give, o);
+        if (up) u[4 * e + y] = got;
+        else u[4 * (e | o) + y] = got;
+      }
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(WideCfg<D>::kThreads, 1)
 mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -142,74 +163,72 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
       auto turn = [](Ring& r, int depth) { if (++r.slot == depth) { r.slot = 0; r.ph ^= 1; } };
       Ring rk{0, 0}, rv{0, 0};
       uint32_t pf0 = 0, pf1 = 0, qf = 0;                       // phases of P and Q
-      // S of tile x with the K tile at rk; the last tile's releases it, the
+      // PV of tile x for the step whose P is there (nks > 0), then S of the step
+      // behind it (more). V is MN-major: 8-key groups 1024 B apart, 64-column
+      // boxes kBox apart. The last tile's products release K and V, and in the
       // unit's last step Q
-      auto issue_s = [&](int x, bool done, bool last) {
+      auto step = [&](int x, uint32_t acc, int nks, bool done, bool more, bool last) {
         tc_fence_after();
-        const uint32_t dst = tm + colS(x);
-        const uint64_t a = sdesc_sw128(smem_u32(sQ) + x * C::kTile, 16, 1024);
-        const uint64_t b = sdesc_sw128(smem_u32(sK) + rk.slot * C::kTile, 16, 1024);
+        const uint32_t dO = tm + colO(x), dS = tm + colS(x);
+        const uint64_t v = sdesc_sw128(smem_u32(sV) + rv.slot * C::kTile, C::kBox, 1024);
+        const uint64_t q = sdesc_sw128(smem_u32(sQ) + x * C::kTile, 16, 1024);
+        const uint64_t kd = sdesc_sw128(smem_u32(sK) + rk.slot * C::kTile, 16, 1024);
         if (elect_uniform()) {
+          if (nks) {
+            mma_ts(dO, dS, v, idO, acc);
+            if (nks == kKeys / 16) {
 #pragma unroll
-          for (int e = 0; e < NB; ++e)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_ss(dst, a + ((e * C::kBox + ks * 32) >> 4), b + ((e * C::kBox + ks * 32) >> 4), idS,
-                     (e | ks) != 0);
-          mma_commit(bar(bSF + x));
-          if (done) mma_commit(bar(bKE + rk.slot));
-          if (done && last) mma_commit(bar(bQE));
-        }
-        __syncwarp();
-      };
-      // PV of tile x: V is MN-major, 8-key groups 1024 B apart, 64-column boxes
-      // kBox apart
-      auto issue_pv = [&](int x, uint32_t acc, int nks, bool done, bool last) {
-        tc_fence_after();
-        const uint32_t dst = tm + colO(x), a = tm + colS(x);
-        const uint64_t b = sdesc_sw128(smem_u32(sV) + rv.slot * C::kTile, C::kBox, 1024);
-        if (elect_uniform()) {
-          mma_ts(dst, a, b, idO, acc);
-          if (nks == kKeys / 16) {
-#pragma unroll
-            for (int ks = 1; ks < kKeys / 16; ++ks) mma_ts(dst, a + ks * 8, b + ks * 128, idO, 1u);
-          } else {
+              for (int ks = 1; ks < kKeys / 16; ++ks) mma_ts(dO, dS + ks * 8, v + ks * 128, idO, 1u);
+            } else {
 #pragma unroll 1
-            for (int ks = 1; ks < nks; ++ks) mma_ts(dst, a + ks * 8, b + ks * 128, idO, 1u);
+              for (int ks = 1; ks < nks; ++ks) mma_ts(dO, dS + ks * 8, v + ks * 128, idO, 1u);
+            }
+            if (done) mma_commit(bar(bVE + rv.slot));
+            if (!more) mma_commit(bar(bOF + x));
           }
-          if (done) mma_commit(bar(bVE + rv.slot));
-          if (last) mma_commit(bar(bOF + x));
+          if (more) {
+#pragma unroll
+            for (int e = 0; e < NB; ++e)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_ss(dS, q + ((e * C::kBox + ks * 32) >> 4), kd + ((e * C::kBox + ks * 32) >> 4), idS,
+                       (e | ks) != 0);
+            mma_commit(bar(bSF + x));
+            if (done) mma_commit(bar(bKE + rk.slot));
+            if (done && last) mma_commit(bar(bQE));
+          }
         }
         __syncwarp();
       };
       Unit w;
       for (int lu = 0; ok && take(lu, w); ++lu) {
         const int k0 = __shfl_sync(0xffffffffu, w.k0, 0), k1 = __shfl_sync(0xffffffffu, w.k1, 0);
+        const int kt = __shfl_sync(0xffffffffu, w.R.kt, 0), L = __shfl_sync(0xffffffffu, w.R.L, 0);
+        const int an = __shfl_sync(0xffffffffu, w.R.a + w.R.n, 0);
         const bool pair = __shfl_sync(0xffffffffu, w.R.n - w.rt * p.npu, 0) > p.npt;
-        ok = wait_all(bQF, qf, 0x200) && wait_all(bKF + rk.slot, rk.ph, 0x300);
-        if (!ok) break;
-        qf ^= 1;
-        issue_s(0, !pair, k0 + 1 == k1);
-        if (pair) issue_s(1, true, k0 + 1 == k1);
-        turn(rk, KS);
-        for (int k = k0; k < k1; ++k) {
-          const bool more = k + 1 < k1, last2 = k + 2 == k1;
+        // before the first step: S alone. Lanes wait for a barrier each: one
+        // trip for all that a product needs
+        for (int k = k0 - 1; k < k1; ++k) {
+          const bool begin = k < k0, more = k + 1 < k1, last = k + 2 == k1;
           const uint32_t acc = k > k0 ? 1u : 0u;
-          const int nks = (__shfl_sync(0xffffffffu, w.keys(k), 0) + 15) >> 4;
-          if (!(ok = wait_all(bVF + rv.slot, rv.ph, 0x310) && wait_all(bPF, pf0, 0x400))) break;
-          pf0 ^= 1;
-          issue_pv(0, acc, nks, !pair, !more);
-          if (more) {
-            if (!(ok = wait_all(bKF + rk.slot, rk.ph, 0x320))) break;
-            issue_s(0, !pair, last2);
-          }
+          const int kv = min(kKeys, k < kt ? L - k * kKeys : an - (k - kt) * kKeys);
+          const int nks = begin ? 0 : (kv + 15) >> 4;
+          const bool l1 = (lane & 1) != 0, l2 = more && (lane & 2);
+          const int wb = l1 ? (begin ? bQF : bVF + rv.slot) : l2 || begin ? bKF + rk.slot : bPF;
+          const uint32_t wp = l1 ? (begin ? qf : rv.ph) : l2 || begin ? rk.ph : pf0;
+          if (!(ok = wait_all(wb, wp, 0x400))) break;
+          step(0, acc, nks, !pair, more, last);
           if (pair) {
-            if (!(ok = wait_all(bPF + 1, pf1, 0x410))) break;
-            pf1 ^= 1;
-            issue_pv(1, acc, nks, true, !more);
-            if (more) issue_s(1, true, last2);
+            if (!begin && !(ok = wait_all(bPF + 1, pf1, 0x410))) break;
+            step(1, acc, nks, true, more, last);
           }
-          turn(rv, VS);
+          if (begin) {
+            qf ^= 1;
+          } else {
+            pf0 ^= 1;
+            if (pair) pf1 ^= 1;
+            turn(rv, VS);
+          }
           if (more) turn(rk, KS);
         }
       }
@@ -219,7 +238,7 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
       wait_drain(bar(bDR), 0);
     } else {
       // ------------------------------------------------------ the tree's masks
-      int lu = 0, t0 = 0;                                // t0: steps of the units before
+      int lu = 0;
       bool ok = true, bad = false;
       Unit w;
       while (ok && take(lu, w)) {
@@ -235,18 +254,30 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
         // among its batch of 32 are walked (they share a word), those before
         // are the ancestors of the first one before the batch
         uint32_t* m = sMask + sm * MIS_TREE_MAX_NODES * W8;
+        if (p.parents) {
+          int raw[W8];
+#pragma unroll
+          for (int q = 0; q < W8; ++q) raw[q] = q * 32 + lane < n ? p.parents[w.R.r0 + q * 32 + lane] : MIS_TREE_ROOT;
+#pragma unroll
+          for (int q = 0; q < W8; ++q) {
+            if (raw[q] >= q * 32 + lane || raw[q] < MIS_TREE_UNUSED) {
+              bad |= q * 32 + lane < n;
+              raw[q] = MIS_TREE_ROOT;
+            }
+            sPar[q * 32 + lane] = (int16_t)raw[q];
+          }
+          __syncwarp();
+        }
 #pragma unroll 1
         for (int b0 = 0; b0 < MIS_TREE_MAX_NODES; b0 += 32) {
           const int i = b0 + lane, wi = b0 >> 5;
           int up = i - 1;
           if (p.parents) {
-            up = MIS_TREE_ROOT;
-            if (i < n) {
-              up = p.parents[w.R.r0 + i];
-              if (up >= i || up < MIS_TREE_UNUSED) { up = MIS_TREE_ROOT; bad = true; }
-              if (up >= 0 && p.parents[w.R.r0 + up] == MIS_TREE_UNUSED) up = MIS_TREE_ROOT;
+            up = sPar[i];
+            if (up >= 0 && sPar[up] == MIS_TREE_UNUSED) {
+              up = MIS_TREE_ROOT;
+              sPar[i] = MIS_TREE_ROOT;
             }
-            sPar[i] = (int16_t)up;
           }
           const bool dead = i < n && up == MIS_TREE_UNUSED;
           const uint32_t dw = __ballot_sync(0xffffffffu, dead);
@@ -269,9 +300,6 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
           }
           __syncwarp();
         }
-        if (tree) ok = scan_new_rows<NB, VS>(p, w, sNf + sm * W8, t0, smem_u32(sV), bar(bVF), W);
-        if (!ok) break;
-        t0 += w.k1 - w.k0;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bMF + sm));
         ++lu;
@@ -371,26 +399,41 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
           // second tile's product comes behind the first's
           const int j = j0 + r;
           const bool node = fresh && j >= 0 && j < w.R.n;
-          const bool odd = node && ((sNf[slot * W8 + (j >> 5)] >> (j & 31)) & 1u);
-          if (x == 0 && r < ((kv + 15) & ~15) && (odd || !(node || there))) {
+          if (x == 0 && r < ((kv + 15) & ~15) && !there) {
             const int t = tk + k - w.k0;
             ok = spin(bar(bVF + t % VS), (t / VS) & 1, W, 0x750);
             if (ok) {
               const uint32_t aV = smem_u32(sV + (t % VS) * C::kTile) + r * 128;
-#pragma unroll 2
-              for (int c = 0; c < 8 * NB; ++c) {
-                const uint32_t a = aV + (c >> 3) * C::kBox + (c & 7) * 16;
-                uint32_t u[4] = {0, 0, 0, 0};
-                if (odd) {
-                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(a) : "memory");
+              // any order of the row's 16-byte chunks: lanes spread over the banks
+              auto chunk = [&](int c) { return aV + (c >> 3) * C::kBox + (((c + r) & 7) << 4); };
+              uint32_t top = 0x7f807f80u;                // the largest exponents, by half
+              if (node) {
+                top = 0;
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    if ((u[e] & 0x7f80u) == 0x7f80u) u[e] &= 0xffff0000u;
-                    if ((u[e] & 0x7f800000u) == 0x7f800000u) u[e] &= 0x0000ffffu;
-                  }
+                for (int c = 0; c < 8 * NB; ++c) {
+                  uint32_t u[4];
+                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(chunk(c)) : "memory");
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) top = __vmaxu2(top, u[e] & 0x7f807f80u);
                 }
-                st_shared_v4(a, u[0], u[1], u[2], u[3]);
+              }
+              if ((top & 0x7f80u) == 0x7f80u || (top >> 16) == 0x7f80u) {
+                if (node) atomicOr(&sNf[slot * W8 + (j >> 5)], 1u << (j & 31));
+#pragma unroll 1
+                for (int c = 0; c < 8 * NB; ++c) {
+                  uint32_t u[4] = {0, 0, 0, 0};
+                  if (node) {
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(chunk(c)) : "memory");
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      if ((u[e] & 0x7f80u) == 0x7f80u) u[e] &= 0xffff0000u;
+                      if ((u[e] & 0x7f800000u) == 0x7f800000u) u[e] &= 0x0000ffffu;
+                    }
+                  }
+                  st_shared_v4(chunk(c), u[0], u[1], u[2], u[3]);
+                }
               }
               fence_proxy_async();
             }
@@ -460,58 +503,76 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
       if ((sDead[slot * W8 + ((node0 + i) >> 5)] >> ((node0 + i) & 31)) & 1u) { m = kEmpty; l = 0.f; }
       const int g = r - i * p.G;
       const int64_t piece = 2 * (int64_t)blockIdx.x + (w.k0 == 0 ? 1 : 0);
-      const int64_t prow = piece * 256 + x * p.npt * p.G + r;      // a piece's rows lie end to end
+      const int pr = x * p.npt * p.G + r;                          // a piece's rows lie end to end
       const int64_t orow = (int64_t)(w.R.r0 + node0 + i);
       if (!whole) {
-        if (mine) p.ml[prow] = make_float2(m, l);
+        if (mine) p.ml[piece * 256 + pr] = make_float2(m, l);
         if (w.k0 == 0 && threadIdx.x == 128)
           p.meta[blockIdx.x] = make_int4(w.R.r0 + node0, min(p.npu, w.R.n - node0) * p.G, w.h, share.pieces(w));
       } else if (mine && p.lse) {
         p.lse[(int64_t)(w.h * p.G + g) * p.T + orow] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
       const float inv = l != 0.f ? 1.f / l : 0.f;                  // NaN stays
+      const int64_t oat = mine ? orow * p.os + (int64_t)(w.h * p.G + g) * D : -1;
       uint32_t nf = 0;
       if (w.k1 > w.R.kt)
         for (int q = 0; q < W8; ++q) nf |= sNf[slot * W8 + q];
+      if (nf) {
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t ov[32];
-        __syncwarp();
-        tmem_ld32(tO + c, ov);
-        tmem_ld_wait();
-        reg_fence32(ov);
-        if (nf) {
+        for (int c = 0; c < D; c += 8) {
+          uint32_t ov[8];
+          tmem_ld8(tO + c, ov);
+          tmem_ld_wait();
+          reg_fence8(ov);
 #pragma unroll 1
           for (int q = 0; q < W8; ++q)
 #pragma unroll 1
             for (uint32_t bits = sNf[slot * W8 + q] & mrow[q]; bits; bits &= bits - 1) {
               const __nv_bfloat16* v = p.v + (int64_t)(w.R.r0 + q * 32 + __ffs(bits) - 1) * p.vs + w.h * D + c;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
+              for (int e = 0; e < 8; ++e) {
                 const float val = __bfloat162float(v[e]);
                 if (!isfinite(val)) ov[e] = __float_as_uint(__uint_as_float(ov[e]) + val);
               }
             }
           __syncwarp();
+          tmem_st8(tO + c, ov);
         }
-        if (!mine) continue;
+        tmem_st_wait();
+      }
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t ov[32];
+        tmem_ld32(tO + c, ov);
+        tmem_ld_wait();
+        reg_fence32(ov);
         if (!whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.part + prow * D + c);
+          float* part = p.part + piece * 256 * D + c;
+          spread4(ov, lane);
+          spread4(ov + 16, lane);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+          for (int e = 0; e < 4; ++e) {
+            const int to = __shfl_sync(0xffffffffu, mine ? pr : -1, (lane & ~3) | e);
+            uint4* dst = reinterpret_cast<uint4*>(part + (int64_t)to * D) + (lane & 3);
+            if (to >= 0) dst[0] = make_uint4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+            if (to >= 0) dst[4] = make_uint4(ov[4 * e + 16], ov[4 * e + 17], ov[4 * e + 18], ov[4 * e + 19]);
+          }
           continue;
         }
-        uint4* dst = reinterpret_cast<uint4*>(p.o + orow * p.os + (int64_t)(w.h * p.G + g) * D + c);
+        uint32_t u[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          // an empty row is zero, whatever its accumulator holds
+          const float v0 = __uint_as_float(ov[2 * e]), v1 = __uint_as_float(ov[2 * e + 1]);
+          u[e] = inv != 0.f ? pack_bf16(v0 * inv, v1 * inv) : 0u;
+        }
+        spread4(u, lane);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          uint32_t u[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            // an empty row is zero, whatever its accumulator holds
-            const float v0 = __uint_as_float(ov[8 * e + 2 * y]), v1 = __uint_as_float(ov[8 * e + 2 * y + 1]);
-            u[y] = inv != 0.f ? pack_bf16(v0 * inv, v1 * inv) : 0u;
-          }
-          dst[e] = make_uint4(u[0], u[1], u[2], u[3]);
+          const int64_t to = __shfl_sync(0xffffffffu, oat, (lane & ~3) | e);
+          if (to >= 0)
+            *(reinterpret_cast<uint4*>(p.o + to + c) + (lane & 3)) =
+                make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
         }
       }
       __syncwarp();
