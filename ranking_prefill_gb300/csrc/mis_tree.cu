@@ -9,13 +9,12 @@
 // the wide side:
 //     S^T [128 keys x N rows] = K Q^T        (A = K tile, B = Q rows)
 //     O^T [D x N rows]       += V^T P^T      (A = V tile, MN-major, B = P)
-// with N = 16, 32, 64 or 128 rows a tile: a decoded token costs N = 16
-// columns of softmax instead of 128 rows, and one pass over K and V serves
-// every row of the tile.
+// with N = 16, 32 or 64 rows a tile: a decoded token costs N = 16 columns of
+// softmax instead of 128 rows, and one pass over K and V serves every row of
+// the tile. Requests with more rows go to mis_tree_wide.cu.
 //
 // A tile holds the G rows of N / G nodes (rounded down), so one TMA box loads
-// its Q.
-// Work is cut evenly: the (request, kv head, row tile) units are laid end to
+// its Q. Work is cut evenly: the (request, kv head) units are laid end to
 // end in 128-key steps and every block takes the same number of consecutive
 // steps, found on the device from the lengths (no host plan). A block that
 // holds a whole unit writes O; the pieces of a unit that several blocks share
@@ -63,30 +62,28 @@ constexpr float kSpread = 40.0f;                 // log2 units maxima may differ
 template <int D, int N>
 struct TreeCfg {
   static constexpr int kNB = D / 64;             // 64-column boxes of a row
-  static constexpr int kWG = N == 16 ? 1 : N == 128 ? 4 : 2;    // softmax warpgroups
+  static constexpr int kWG = N == 16 ? 1 : 2;    // softmax warpgroups
   static constexpr int kNC = N / kWG;            // columns of a softmax thread
   static constexpr int kThreads = 256 + 128 * kWG;
-  // Register budgets of the warpgroups (N >= 64): their sum is the launch's,
-  // 512 threads x 128 or 768 x 80
-  static constexpr int kRegCtl = N == 128 ? 64 : 80, kRegEpi = N == 128 ? 64 : 80;
-  static constexpr int kRegSoft = N == 128 ? 88 : 176;
-  static_assert(N < 64 || 128 * (kRegCtl + kRegEpi + kWG * kRegSoft) <= kThreads * (N == 128 ? 80 : 128),
+  // Register budgets of the warpgroups (N = 64): their sum is the launch's,
+  // 512 threads x 128
+  static constexpr int kRegCtl = 80, kRegEpi = 80, kRegSoft = 176;
+  static_assert(N < 64 || 128 * (kRegCtl + kRegEpi + kWG * kRegSoft) <= kThreads * 128,
                 "register split exceeds the launch allocation");
   static constexpr int kBox = kKeys * 128;       // 64 columns of a 128-key tile
   static constexpr int kTile = kNB * kBox;
   static constexpr int kQ = N * D * 2;
   static constexpr int kQBox = N * 128;
-  static constexpr int kQS = (N == 128 && D == 128) ? 1 : 2;
-  static constexpr int kP = kKeys * 128 * (N > 64 ? 2 : 1);
-  static constexpr int kK = D == 128 ? (N == 128 ? 2 : 3) : (N == 128 ? 4 : 5);
-  static constexpr int kV = D == 128 ? (N == 16 ? 3 : 2) : (N == 128 ? 4 : 5);
+  static constexpr int kQS = 2;
+  static constexpr int kP = kKeys * 128;
+  static constexpr int kK = D == 128 ? 3 : 5;
+  static constexpr int kV = D == 128 ? (N == 16 ? 3 : 2) : 5;
   static constexpr int kNW = N < 32 ? 1 : N / 32;       // mask words of a key: which columns see it
-  static constexpr int kNodes = N == 128 ? 128 : 64;   // N >= max_nodes * G below 128
+  static constexpr int kNodes = 64;              // N >= max_nodes * G
   // What a unit costs besides its steps (its first step, masks, epilogue), in
   // steps: blocks are given equal shares of both. Measured as the time blocks
-  // took by their number of units: 8 us a unit at N = 128 (1.4 us a step), 2.8
-  // at 64, 0.3 at 16
-  static constexpr int kUnitCost = N == 128 ? 7 : N == 64 ? 3 : 0;
+  // took by their number of units: 2.8 us a unit at N = 64, 0.3 at 16
+  static constexpr int kUnitCost = N == 64 ? 3 : 0;
   static constexpr int kTmem = N == 16 ? 64 : 4 * N;    // S_0 | S_1 | O_0 | O_1
   // floats / words behind the tiles
   static constexpr int oMask = 0;                       // [2][kNodes][kNW]
@@ -117,9 +114,9 @@ __device__ __forceinline__ float warp_min(float x) {
 }
 
 // Sums (or maxima) over the warp of NV columns, of which every lane brings one
-// value each: halve the columns lane bit by lane bit, then fold the lanes that
-// are left. Returns the first of the NV / 32 (at least one) columns that end up
-// in v[0], v[1], ... of this lane. (One redux a column took three times as long.)
+// value each, NV <= 32: halve the columns lane bit by lane bit, then fold the
+// lanes that are left. Returns the column that ends up in v[0] of this lane.
+// (One redux a column took three times as long.)
 template <int NV, bool kMax>
 __device__ __forceinline__ int fold_cols(float* v, int lane) {
   int cnt = NV, col = 0;
@@ -468,9 +465,6 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     // largest score is the largest product
     const float sa = fabsf(p.scale_log2), sign = p.scale_log2 < 0.f ? -1.f : 1.f, inv_sa = 1.f / sa;
     const uint64_t sax2 = f2_pack(__float_as_uint(sa), __float_as_uint(sa));
-    // columns in registers at a time: two pieces (N = 128) are read from
-    // tensor memory twice, once for the maximum and once for P
-    constexpr int CC = N == 128 ? 16 : NC;
     // this thread's row of P: chunk c of its columns
     const uint32_t aP = smem_u32(sP) + (c0 >> 6) * C::kBox + r * 128;
     const int cP = (c0 & 63) / 8;
@@ -559,21 +553,16 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           tmem_st_wait();
         }
         __syncwarp();
-        // columns q .. q + CC - 1 of the scores
-        uint32_t s[CC];
-        if (CC == NC && ok && active) ld_cols<CC>(tS, s);
+        uint32_t s[NC];
+        if (ok && active) ld_cols<NC>(tS, s);
         bool move = first;
         if (!first) {
           if (ok && active) {
             float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-            for (int q = 0; q < NC; q += CC) {
-              if (CC < NC) ld_cols<CC>(tS + q, s);
-#pragma unroll
-              for (int n = 0; n < CC; n += 4) {
-                x0 = max3(x0, __uint_as_float(s[n]), __uint_as_float(s[n + 1]));
-                x1 = max3(x1, __uint_as_float(s[n + 2]), __uint_as_float(s[n + 3]));
-              }
+            for (int n = 0; n < NC; n += 4) {
+              x0 = max3(x0, __uint_as_float(s[n]), __uint_as_float(s[n + 1]));
+              x1 = max3(x1, __uint_as_float(s[n + 2]), __uint_as_float(s[n + 3]));
             }
             over |= fmaf(fmaxf(x0, x1), sa, base) > kGrow;
           }
@@ -584,51 +573,36 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           // then every warp of the warpgroup leaves here)
           if (bar_any128(id, !ok)) { gone = true; break; }
           // the step's maximum of every column over this warp's keys
-#pragma unroll 1
-          for (int q = 0; q < NC; q += CC) {
-            float v[CC];
+          {
+            float v[NC];
 #pragma unroll
-            for (int n = 0; n < CC; ++n) v[n] = -INFINITY;
-            if (active) {
-              ld_cols<CC>(tS + q, s);
-#pragma unroll
-              for (int n = 0; n < CC; ++n) v[n] = __uint_as_float(s[n]);
-            }
-            const int n = q + fold_cols<CC, true>(v, lane);
+            for (int n = 0; n < NC; ++n) v[n] = active ? __uint_as_float(s[n]) : -INFINITY;
+            const int n = fold_cols<NC, true>(v, lane);
             float mine = v[0] * sa;
             if (!one && ref[n] < -kEmpty) mine -= ref[n];
             sMax[sw * N + c0 + n] = mine;
           }
           bar_sync128(id);
-          // every warp draws the same conclusion from the four warps' maxima
-          constexpr int NL = (NC + 31) / 32;
-          float old[NL], top[NL], hi = kEmpty, lo = INFINITY;
+          // every warp draws the same conclusion from the four warps' maxima,
+          // a lane for a column
+          const int n = min(lane, NC - 1);
+          const float old = first ? kEmpty : one ? -base : -ref[n];
+          float top = old;
 #pragma unroll
-          for (int x = 0; x < NL; ++x) {
-            const int n = min(x * 32 + lane, NC - 1);
-            old[x] = first ? kEmpty : one ? -base : -ref[n];
-            top[x] = old[x];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) top[x] = fmaxf(top[x], sMax[q * N + c0 + n]);
-            hi = fmaxf(hi, top[x]);
-            // columns without a row only count upwards, so that they never
-            // make the reference move step after step
-            if (c0 + n < rows) lo = fminf(lo, top[x]);
-          }
-          hi = warp_max(hi);
-          lo = warp_min(lo);
+          for (int q = 0; q < 4; ++q) top = fmaxf(top, sMax[q * N + c0 + n]);
+          // columns without a row only count upwards, so that they never make
+          // the reference move step after step
+          const float hi = warp_max(fmaxf(kEmpty, top));
+          const float lo = warp_min(c0 + n < rows ? top : INFINITY);
           const bool was = one;
           one = hi - lo <= kSpread || lo == INFINITY;
           base = one ? -hi : 0.f;
           __syncwarp();
           if (!(was && one)) {
             // the scores in tensor memory go from the old references to the new
-#pragma unroll
-            for (int x = 0; x < NL; ++x) {
-              const float from = was || old[x] <= kEmpty ? 0.f : old[x];
-              const float to = one || top[x] <= kEmpty ? 0.f : top[x];
-              if (x * 32 + lane < NC) al[x * 32 + lane] = (from - to) * inv_sa;
-            }
+            const float from = was || old <= kEmpty ? 0.f : old;
+            const float to = one || top <= kEmpty ? 0.f : top;
+            if (lane < NC) al[lane] = (from - to) * inv_sa;
             __syncwarp();
             if (active) {
 #pragma unroll 1
@@ -643,14 +617,10 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
             }
             __syncwarp();
           }
-#pragma unroll
-          for (int x = 0; x < NL; ++x) {
-            const int n = x * 32 + lane;
-            if (n < NC) {
-              const float to = one ? hi : top[x];
-              ref[n] = -to;
-              al[n] = ex2(old[x] - to);
-            }
+          if (lane < NC) {
+            const float to = one ? hi : top;
+            ref[lane] = -to;
+            al[lane] = ex2(old - to);
           }
           __syncwarp();
           if (!first) {
@@ -676,30 +646,26 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
             }
           }
         }
-        if (move && ok && active && CC == NC) ld_cols<CC>(tS, s);
+        if (move && ok && active) ld_cols<NC>(tS, s);
         if (ok && active) {
           const uint64_t basex2 = f2_pack(__float_as_uint(base), __float_as_uint(base));
+          uint32_t pk[NC / 2];
 #pragma unroll
-          for (int q = 0; q < NC; q += CC) {
-            if (CC < NC) ld_cols<CC>(tS + q, s);
-            uint32_t pk[CC / 2];
+          for (int n = 0; n < NC; n += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(s[n], s[n + 1]), sax2, basex2), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            l2[n / 2] = f2_add(l2[n / 2], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
+            pk[n / 2] = pack_bf16(p0, p1);
+          }
+          if (t > 0) {                                   // P of the step before has been read
+            ok = spin(bar(bPV), (t - 1) & 1, W, 0x740);
+            ok = __all_sync(0xffffffffu, ok);
+          }
+          if (ok) {
 #pragma unroll
-            for (int n = 0; n < CC; n += 2) {
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(s[n], s[n + 1]), sax2, basex2), x0, x1);
-              const float p0 = ex2(x0), p1 = ex2(x1);
-              l2[(q + n) / 2] = f2_add(l2[(q + n) / 2], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
-              pk[n / 2] = pack_bf16(p0, p1);
-            }
-            if (q == 0 && t > 0) {                       // P of the step before has been read
-              ok = spin(bar(bPV), (t - 1) & 1, W, 0x740);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-            }
-#pragma unroll
-            for (int c = 0; c < CC / 8; ++c)
-              st_shared_v4(aP + (((cP + q / 8 + c) ^ (r & 7)) << 4), pk[4 * c], pk[4 * c + 1],
-                           pk[4 * c + 2], pk[4 * c + 3]);
+            for (int c = 0; c < NC / 8; ++c)
+              st_shared_v4(aP + (((cP + c) ^ (r & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
           }
           // a V row that no row of the tile sees must not meet a zero
           // probability with a NaN or an infinity; one that some rows see
@@ -743,8 +709,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
       for (int n = 0; n < NC / 2; ++n) f2_unpack(l2[n], l[2 * n], l[2 * n + 1]);
       const int col = fold_cols<NC, false>(l, lane);
-#pragma unroll
-      for (int n = 0; n < (NC > 32 ? NC / 32 : 1); ++n) sL[(slot * 4 + sw) * N + c0 + col + n] = l[n];
+      sL[(slot * 4 + sw) * N + c0 + col] = l[0];
       if (sw == 0)
         for (int n = lane; n < NC; n += 32) sM[slot * N + c0 + n] = ref[n];
       __syncwarp();
@@ -906,7 +871,6 @@ struct CombineParams {
 
 template <int N>
 constexpr int kCombineWarps = N < 32 ? N / 4 : 8;
-constexpr int kNarrowMax = 128;
 
 template <int D, int N>
 __global__ void __launch_bounds__(32 * kCombineWarps<N>) mis_tree_combine_kernel(const CombineParams p) {
@@ -1017,10 +981,13 @@ mis_status_t check_desc(const mis_tree_desc* d, const mis_paged_cache* c) {
 }
 
 // Rows of a unit: the smallest tile that holds all rows of a request's kv
-// head, or two tiles of 128.
+// head, and from 65 rows on the two tiles of 128 of mis_tree_wide.cu. 16
+// requests of 2000 to 8000 cached rows (8 kv heads, D = 128): 64 rows 61 us in a
+// tile of 64, 65 us there; 128 rows 70 us in a tile of 128 columns here, 69 us
+// there, and 26 and 21 us over 100 to 600 cached rows.
 int unit_rows(const mis_tree_desc* d, const mis_paged_cache* c) {
   const int64_t rows = (int64_t)d->max_nodes * (d->Hq / c->Hkv);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= kNarrowMax ? 128 : 256;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256;
 }
 
 struct TreeWs { size_t status, meta, ml, part, total; };
@@ -1040,7 +1007,7 @@ TreeWs workspace_of(const mis_tree_desc* d, const mis_paged_cache* c) {
 template <int D, int N>
 mis_status_t launch_tree(const CUtensorMap* m, const TreeParams& p, const CombineParams& c,
                          cudaStream_t st) {
-  if constexpr (N <= 128) {
+  if constexpr (N <= 64) {
     using Cf = TreeCfg<D, N>;
     auto kern = mis_tree_attn_kernel<D, N>;
     if (!kernel_attr_once(reinterpret_cast<const void*>(kern), Cf::kSmem)) return MIS_ERR_CUDA;
@@ -1098,7 +1065,7 @@ extern "C" mis_status_t mis_tree_attention_fwd(
   // steps (with a unit's own cost) are counted in 32 bits
   const int64_t tiles = ((int64_t)max_pages * cache->page_size + kKeys - 1) / kKeys + 16;
   const int64_t rows = (int64_t)desc->max_nodes * (desc->Hq / cache->Hkv);
-  if ((double)tiles * desc->B * cache->Hkv * (rows > 128 ? 2.0 * ((rows + 127) / 128) : 1.0) >= 2147483648.0)
+  if ((double)tiles * desc->B * cache->Hkv * (rows > 64 ? 2.0 * ((rows + 127) / 128) : 1.0) >= 2147483648.0)
     return MIS_ERR_UNSUPPORTED;
   if (desc->T == 0)
     return cudaMemsetAsync(workspace, 0, 8, st) == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
@@ -1124,7 +1091,7 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     // Q by the rows of a tile's nodes
     const uint64_t qd[3] = {(uint64_t)D, (uint64_t)desc->Hq, (uint64_t)desc->T};
     const uint64_t qst[2] = {(uint64_t)D * 2, (uint64_t)q_row_stride * 2};
-    const int N = unit_rows(desc, cache), G = desc->Hq / cache->Hkv, npt = std::min(N, 128) / G;
+    const int N = unit_rows(desc, cache), G = desc->Hq / cache->Hkv, npt = (N == 256 ? 128 : N) / G;
     const uint32_t qb[3] = {64, (uint32_t)G, (uint32_t)npt};
     const CUtensorMap maps[7] = {
         encode_tmap_bf16(q, 3, qd, qst, qb, &ok),
@@ -1144,7 +1111,7 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     p.table = block_table; p.table_stride = block_table_stride;
     p.cache_len = cache_len; p.cu = cu_nodes; p.parents = parents;
     p.B = desc->B; p.T = desc->T; p.Hkv = cache->Hkv;
-    p.G = G; p.npt = npt; p.npu = N > 128 ? 2 * npt : npt;
+    p.G = G; p.npt = npt; p.npu = N == 256 ? 2 * npt : npt;
     p.g_magic = (uint32_t)((0xffffffffull + (uint64_t)p.G) / (uint64_t)p.G);
     p.max_nodes = desc->max_nodes;
     p.lanes = std::min((desc->max_nodes + p.npu - 1) / p.npu, 2);
@@ -1164,13 +1131,11 @@ extern "C" mis_status_t mis_tree_attention_fwd(
       if (N == 16) return launch_tree<128, 16>(maps, p, c, st);
       if (N == 32) return launch_tree<128, 32>(maps, p, c, st);
       if (N == 64) return launch_tree<128, 64>(maps, p, c, st);
-      if (N == 128) return launch_tree<128, 128>(maps, p, c, st);
       return launch_tree<128, 256>(maps, p, c, st);
     }
     if (N == 16) return launch_tree<64, 16>(maps, p, c, st);
     if (N == 32) return launch_tree<64, 32>(maps, p, c, st);
     if (N == 64) return launch_tree<64, 64>(maps, p, c, st);
-    if (N == 128) return launch_tree<64, 128>(maps, p, c, st);
     return launch_tree<64, 256>(maps, p, c, st);
   } catch (...) {
     return MIS_ERR_CUDA;
