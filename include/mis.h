@@ -545,7 +545,7 @@ mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const void* k, con
  * o and lse overlap no input. fp32 scores, statistics and accumulation;
  * probabilities are rounded to bf16 for the second product, o to bf16. The
  * same call gives the same bits. Two kernels. A wait inside the first can last
- * as long as a block works on one request, about 1.5 us per 128 cached rows
+ * as long as a block works on one request, about 2 us per 128 cached rows
  * (see mis_set_wait_limit_ns()). MIS_ERR_UNSUPPORTED also where B * Hkv *
  * max_pages * page_size / 128 steps would pass 32 bits.
  * Workspace: device, 256-byte aligned, >= mis_tree_attention_workspace_size()

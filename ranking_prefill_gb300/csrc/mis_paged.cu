@@ -7,8 +7,13 @@
 // over the batch and leaves a record per request; the rows' slots follow from
 // the record of their request (found by bisection of cu_new) and one page id.
 //
+// What bounds it is latency: a chain of dependent loads and the block's scans,
+// 4.3 us for 32 requests with a row each, 4.8 us for 16 with 187,165 rows, 7.3 us
+// for 256 with 997,692 (8.5 MB, 1.2 TB/s).
+//
 // mis_paged_write_kv is a copy: every kept row is read and written once, so
-// HBM bounds it (a decoding step: the launch).
+// HBM bounds it: 131,072 rows of 8 heads, D = 128, rotated (1.07 GB), 164.6 us,
+// 6.5 TB/s of 6.7 measured for a copy. A decoding step is the launch's 2 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -523,5 +528,3 @@ extern "C" mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const v
     return MIS_ERR_CUDA;
   }
 }
-
-

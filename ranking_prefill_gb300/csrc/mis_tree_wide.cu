@@ -1,12 +1,23 @@
-// Tree attention for requests with many rows a kv head (more than a tile of
-// 128), sm_103a: the products the usual way round,
+// Tree attention for requests with many rows a kv head (more than 64), sm_103a:
+// the products the usual way round,
 //     S [128 rows x 128 keys] = Q K^T,     O [128 rows x D] += P V,
 // for two row tiles that share every K and V tile. A thread owns a row: its
-// maximum, sum and reference stay in registers, P goes to tensor memory, and
-// one tile's softmax runs during the other's products.
+// maximum, sum and reference stay in registers (no exchange between threads),
+// P goes to tensor memory, and one tile's softmax runs during the other's
+// products. Everything else (units, shares, copies, pieces) is as in
+// mis_tree.cu; a unit is a pair of row tiles, or one tile where the request has
+// no more rows.
 //
-// Everything else (units, shares, copies, pieces) is as in mis_tree.cu; a unit
-// is a pair of row tiles.
+// What bounds it, at D = 128: a tile's round of a step is 1060 cycles of PV and
+// the next S, 320 until its scores are seen, 1130 of softmax (exponentials,
+// rounding and sums fill the issue slots of a tile's four warps) and 450 until
+// the products of its P go out: 2960, in which the other tile's 1060 fit. Tensor
+// memory holds no third tile. Two warps a row's half took longer (81 us, this
+// 77: the same SM partitions do the same exponentials). K and V alone, all
+// from L2, change little (2 us), so memory does not bound a step.
+// 16 requests of 2000 to 8000 cached rows, 64 nodes x 4 heads, 8 kv heads: 77 us
+// with the second kernel's 9, 4.5 TB/s and 1080 TFLOP/s (the tensor pipe is active
+// for 51% of this kernel's cycles).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,7 +39,8 @@ struct WideCfg {
   static constexpr int kBox = kKeys * 128;
   static constexpr int kTile = kNB * kBox;       // of K, V and Q alike
   static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 2 : 4;
-  static constexpr int kUnitCost = 4;            // see TreeCfg
+  // see TreeCfg; with 2, 3, 4 and 5 the pairs above took 79.4, 78.0, 77.7, 78.2 us
+  static constexpr int kUnitCost = 4;
   static constexpr int kW = MIS_TREE_MAX_NODES / 32;    // words of a node's mask
   static constexpr int oMask = 0;                       // [2][256][kW] new keys that a node sees
   static constexpr int oDead = oMask + 2 * MIS_TREE_MAX_NODES * kW;   // [2][kW] unused nodes
