@@ -800,6 +800,21 @@ def test_python_refusals():
 
 # ----------------------------------------------------- the operators together
 
+def test_python_refuses_outputs_over_inputs():
+    t = Tree([40], [3], 2, 2, 64, 16, None, seed=24).prepare()
+    for o in (t.q, t.k, t.v):
+        with pytest.raises(lib.MisError) as e:
+            lib.mis_tree_attention_fwd(t.desc, t.q, t.k, t.v, o, t.lse, t.d_table, t.d_len, t.d_cu, None, t.ws)
+        assert e.value.status == lib.MIS_ERR_INVALID_ARG
+    rows = t.kc.view(-1, 2, 64)                              # the cache's own rows as the source
+    other = torch.zeros_like(rows)
+    ws = workspace(256)
+    for k, v in ((rows, other), (other, t.vc.view(-1, 2, 64)), (other, rows)):
+        with pytest.raises(lib.MisError) as e:
+            lib.mis_paged_write_kv(t.cache, k, v, i32([1, 2]), ws)
+        assert e.value.status == lib.MIS_ERR_INVALID_ARG
+
+
 def test_prompt_draft_accept_decode():
     """A serving loop: prompts enter the cache, trees are drafted and attended,
     one path of each is accepted into the cache, then one token is decoded.
