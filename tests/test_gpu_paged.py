@@ -450,6 +450,19 @@ def test_large_trees_and_chains(hq, hkv, D, nodes, chain):
     Tree(lens, nodes, hq, hkv, D, 16, par, seed=nodes[0]).check()
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    rng = np.random.default_rng(100 + seed)
+    hq, hkv, D = HEADS[rng.integers(len(HEADS))]
+    B = int(rng.integers(2, 7))
+    nodes = rng.integers(1, int(2 ** rng.uniform(0, 7)) + 2, B)
+    lens = rng.integers(0, int(2 ** rng.uniform(2, 11)), B)
+    par = None if seed % 3 == 0 else random_parents(rng, nodes, 0.05, reach=20)
+    Tree(lens, nodes, hq, hkv, D, int(rng.choice([16, 32, 64, 128, 256])), par, seed=seed,
+         layout=["rows", "heads", "interleaved", "wide"][seed % 4], pad=8 * (seed % 3),
+         scale=[0.0, 0.3, -0.1][seed % 3]).check()
+
+
 def test_parents_of_a_chain_equal_no_parents():
     nodes = [5, 1, 40]
     par = np.concatenate([np.arange(-1, n - 1) for n in nodes])
