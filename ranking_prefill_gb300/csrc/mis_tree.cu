@@ -88,10 +88,12 @@ struct TreeCfg {
   static constexpr int kV = D == 128 ? (N == 16 ? 3 : 2) : 5;
   static constexpr int kNW = N < 32 ? 1 : N / 32;       // mask words of a key: which columns see it
   static constexpr int kNodes = 64;              // N >= max_nodes * G
+  static constexpr int kFew = D == 128 && N > 16 ? 8 : 16;     // new rows that the masks' warp reads itself
   // What a unit costs besides its steps (its first step, masks, epilogue), in
-  // steps: blocks are given equal shares of both. Measured as the time blocks
-  // took by their number of units: 2.8 us a unit at N = 64, 0.3 at 16
-  static constexpr int kUnitCost = N == 64 ? 3 : 0;
+  // steps: blocks are given equal shares of both. 8 trees of 8 to 32 nodes took
+  // 24.7, 25.8 and 26.3 us with 1, 2 and 3 at N = 64, over other lengths 24.4,
+  // 22.7 and 23.0; at N = 16 a unit costs 0.3 us, a third of a step
+  static constexpr int kUnitCost = N == 64 ? 2 : 0;
   static constexpr int kTmem = N == 16 ? 64 : 4 * N;    // S_0 | S_1 | O_0 | O_1
   // floats / words behind the tiles
   static constexpr int oMask = 0;                       // [2][kNodes][kNW]
@@ -400,7 +402,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       wait_drain(bar(bDR), 0);
     } else {
       // ------------------------------------------------------ the tree's masks
-      int lu = 0, t0 = 0;                                // t0: steps of the units before
+      int lu = 0;
       bool ok = true, bad = false;
       Unit w;
       while (ok && take(lu, w)) {
@@ -415,13 +417,25 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         const bool tree = w.k1 > w.R.kt;
         int16_t* par = sPar;
         if (p.parents) {
-#pragma unroll 2
-          for (int j = lane; j < w.R.n; j += 32) {
-            int up = p.parents[w.R.r0 + j];
-            if (up >= j || up < MIS_TREE_UNUSED) { up = -1; bad = true; }
-            if (up >= 0 && p.parents[w.R.r0 + up] == MIS_TREE_UNUSED) up = -1;
-            par[j] = (int16_t)up;
+          int raw[C::kNodes / 32];
+#pragma unroll
+          for (int x = 0; x < C::kNodes / 32; ++x) {
+            const int j = x * 32 + lane;
+            raw[x] = j < w.R.n ? p.parents[w.R.r0 + j] : MIS_TREE_ROOT;
           }
+#pragma unroll
+          for (int x = 0; x < C::kNodes / 32; ++x) {
+            const int j = x * 32 + lane;
+            if (raw[x] >= j || raw[x] < MIS_TREE_UNUSED) {
+              bad |= j < w.R.n;
+              raw[x] = MIS_TREE_ROOT;
+            }
+            par[j] = (int16_t)raw[x];
+          }
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < C::kNodes / 32; ++x)
+            if (raw[x] >= 0 && par[raw[x]] == MIS_TREE_UNUSED) par[x * 32 + lane] = MIS_TREE_ROOT;
           __syncwarp();
         }
         // columns of unused nodes
@@ -452,10 +466,27 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                   atomicOr(&m[j * NW + x], bit_range(lo - 32 * x, hi - 32 * x));
             }
           }
-          ok = scan_new_rows<NB, VS>(p, w, sNf + sm * 8, t0, smem_u32(sV), bar(bVF), W);
-          if (!ok) break;
+          // New rows whose V holds a NaN or an infinity (see the softmax): a few
+          // are read from memory here, one trip that is over before their tile is
+          // there (one decoded row from its tile: 0.8 us more); of more, the
+          // softmax looks over the tile
+          constexpr int LPR = D / 8, RPI = 32 / LPR;         // lanes a row, rows a load
+          __syncwarp();
+          if (w.R.n <= C::kFew) {
+            const __nv_bfloat16* src = p.v + (int64_t)w.R.r0 * p.vs + w.h * D + lane % LPR * 8;
+            uint4 u[C::kFew / RPI];
+#pragma unroll
+            for (int e = 0; e < C::kFew / RPI; ++e)
+              u[e] = *reinterpret_cast<const uint4*>(src + (int64_t)min(e * RPI + lane / LPR, w.R.n - 1) * p.vs);
+#pragma unroll
+            for (int e = 0; e < C::kFew / RPI; ++e) {
+              uint32_t top = __vmaxu2(__vmaxu2(u[e].x & 0x7f807f80u, u[e].y & 0x7f807f80u),
+                                      __vmaxu2(u[e].z & 0x7f807f80u, u[e].w & 0x7f807f80u));
+              if ((top & 0x7f80u) == 0x7f80u || (top >> 16) == 0x7f80u)
+                atomicOr(&sNf[sm * 8], 1u << min(e * RPI + lane / LPR, w.R.n - 1));
+            }
+          }
         }
-        t0 += w.k1 - w.k0;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bMF + sm));
         ++lu;
@@ -677,27 +708,11 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           // a V row that no row of the tile sees must not meet a zero
           // probability with a NaN or an infinity; one that some rows see
           // leaves its non-finite elements to the epilogue
+          const bool look = N > 16 && node && w.R.n > C::kFew;
           if (ok && !plain && wg == 0 && r < kv16 &&
-              (!seen || (node && ((sNf[slot * 8 + (j >> 5)] >> (j & 31)) & 1u)))) {
+              (!seen || look || (node && ((sNf[slot * 8 + (j >> 5)] >> (j & 31)) & 1u)))) {
             ok = spin(bar(bVF + t % VS), (t / VS) & 1, W, 0x750);
-            if (ok) {
-              const uint32_t aV = smem_u32(sV + (t % VS) * C::kTile) + r * 128;
-#pragma unroll 2
-              for (int c = 0; c < 8 * NB; ++c) {
-                const uint32_t a = aV + (c >> 3) * C::kBox + (c & 7) * 16;
-                uint32_t x[4] = {0, 0, 0, 0};
-                if (seen) {
-                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(a) : "memory");
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u;
-                    if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0x0000ffffu;
-                  }
-                }
-                st_shared_v4(a, x[0], x[1], x[2], x[3]);
-              }
-            }
+            if (ok) clean_row<NB>(smem_u32(sV + (t % VS) * C::kTile) + r * 128, r, seen, look, sNf + slot * 8, j);
           }
           ok = __all_sync(0xffffffffu, ok);
         } else if (ok && t > 0) {

@@ -1,6 +1,6 @@
 // Parts of the two tree-attention kernels that are alike: parameters, requests
-// and units, a block's share of the steps, the copies of Q, K and V, the look
-// over new V rows.
+// and units, a block's share of the steps, the copies of Q, K and V, the
+// cleaning of V rows.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -392,59 +392,43 @@ __device__ __forceinline__ void produce(const TreeParams& p, const Producer& io,
     for (int i = max(0, q_done - QS); i < q_done; ++i) wait_drain(io.qf + 8 * (i % QS), (i / QS) & 1);
 }
 
-// New rows whose V holds a NaN or an infinity (see the softmax). A few
-// are read from memory, one trip that is over before their tile is
-// there; more than that from the tiles the producer brought, which
-// stay until the softmax has used this unit's masks (64 rows from
-// memory took 20 us of the loaded HBM's latency; one decoded row
-// from its tile 0.8 us more than this)
-// nf_bits: a bit per new row; t0: the ring's number of the unit's first step.
-template <int NB, int VS>
-__device__ __forceinline__ bool scan_new_rows(const TreeParams& p, const Unit& w, uint32_t* nf_bits, int t0,
-                                    uint32_t sv, uint32_t vf, const Bound& W) {
-  const int lane = threadIdx.x & 31;
-  bool ok = true;
-  auto odd = [](const uint32_t* x) {
-    bool nf = false;
+// Key row r of a V tile (at address row) before its product: a new row (keep)
+// loses its NaN and infinite elements, which marks it in nf_bits as row j (the
+// epilogue adds them to the rows that see it); any other is zeroed. look: the
+// row is read first, and mostly left as it is.
+template <int NB>
+__device__ __forceinline__ void clean_row(uint32_t row, int r, bool keep, bool look, uint32_t* nf_bits, int j) {
+  // any order of the row's 16-byte chunks: lanes spread over the banks
+  auto chunk = [&](int c) { return row + (c >> 3) * kKeys * 128 + (((c + r) & 7) << 4); };
+  uint32_t top = 0x7f807f80u;                            // the largest exponents, by half
+  if (look) {
+    top = 0;
 #pragma unroll
-    for (int y = 0; y < 4; ++y)
-      nf |= (x[y] & 0x7f80u) == 0x7f80u || (x[y] & 0x7f800000u) == 0x7f800000u;
-    return nf;
-  };
-  constexpr int D = 64 * NB, LPR = D / 8, RPI = 32 / LPR, U = 4;   // lanes a row, rows a load, loads in flight
-  const bool few = w.R.n <= U * RPI;
-  if (few) {
-    const __nv_bfloat16* src = p.v + (int64_t)w.R.r0 * p.vs + w.h * D + lane % LPR * 8;
-    uint4 u[U];
+    for (int c = 0; c < 8 * NB; ++c) {
+      uint32_t x[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(chunk(c)) : "memory");
 #pragma unroll
-    for (int e = 0; e < U; ++e)
-      u[e] = *reinterpret_cast<const uint4*>(src + (int64_t)min(e * RPI + lane / LPR, w.R.n - 1) * p.vs);
-#pragma unroll
-    for (int e = 0; e < U; ++e) {
-      const uint32_t x[4] = {u[e].x, u[e].y, u[e].z, u[e].w};
-      if (odd(x)) atomicOr(nf_bits, 1u << min(e * RPI + lane / LPR, w.R.n - 1));
+      for (int e = 0; e < 4; ++e) top = __vmaxu2(top, x[e] & 0x7f807f80u);
     }
   }
-  for (int k = max(w.k0, w.R.kt); ok && !few && k < w.k1; ++k) {
-    const int t = t0 + k - w.k0, kv = w.keys(k), a = k == w.R.kt ? w.R.a : 0;
-    ok = spin(vf + 8 * (t % VS), (t / VS) & 1, W, 0x620);
-    ok = __all_sync(0xffffffffu, ok);
-    const uint32_t tile = sv + (t % VS) * (NB * kKeys * 128);
-    for (int r = a + lane; ok && r < kv; r += 32) {
-      bool nf = false;
-#pragma unroll 4
-      for (int c = 0; c < 8 * NB; ++c) {               // any order: lanes spread over the banks
-        uint32_t x[4];
+  if ((top & 0x7f80u) == 0x7f80u || (top >> 16) == 0x7f80u) {
+    if (keep) atomicOr(nf_bits + (j >> 5), 1u << (j & 31));
+#pragma unroll 1
+    for (int c = 0; c < 8 * NB; ++c) {
+      uint32_t x[4] = {0, 0, 0, 0};
+      if (keep) {
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                     : "r"(tile + (c >> 3) * kKeys * 128 + r * 128 + (((c + r) & 7) << 4)) : "memory");
-        nf |= odd(x);
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(chunk(c)) : "memory");
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u;
+          if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0x0000ffffu;
+        }
       }
-      const int j = (k - w.R.kt) * kKeys + r - w.R.a;
-      if (nf) atomicOr(nf_bits + (j >> 5), 1u << (j & 31));
+      st_shared_v4(chunk(c), x[0], x[1], x[2], x[3]);
     }
   }
-  return ok;
 }
 
 }  // namespace tree

@@ -415,38 +415,7 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
             const int t = tk + k - w.k0;
             ok = spin(bar(bVF + t % VS), (t / VS) & 1, W, 0x750);
             if (ok) {
-              const uint32_t aV = smem_u32(sV + (t % VS) * C::kTile) + r * 128;
-              // any order of the row's 16-byte chunks: lanes spread over the banks
-              auto chunk = [&](int c) { return aV + (c >> 3) * C::kBox + (((c + r) & 7) << 4); };
-              uint32_t top = 0x7f807f80u;                // the largest exponents, by half
-              if (node) {
-                top = 0;
-#pragma unroll
-                for (int c = 0; c < 8 * NB; ++c) {
-                  uint32_t u[4];
-                  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(chunk(c)) : "memory");
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) top = __vmaxu2(top, u[e] & 0x7f807f80u);
-                }
-              }
-              if ((top & 0x7f80u) == 0x7f80u || (top >> 16) == 0x7f80u) {
-                if (node) atomicOr(&sNf[slot * W8 + (j >> 5)], 1u << (j & 31));
-#pragma unroll 1
-                for (int c = 0; c < 8 * NB; ++c) {
-                  uint32_t u[4] = {0, 0, 0, 0};
-                  if (node) {
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(chunk(c)) : "memory");
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                      if ((u[e] & 0x7f80u) == 0x7f80u) u[e] &= 0xffff0000u;
-                      if ((u[e] & 0x7f800000u) == 0x7f800000u) u[e] &= 0x0000ffffu;
-                    }
-                  }
-                  st_shared_v4(chunk(c), u[0], u[1], u[2], u[3]);
-                }
-              }
+              clean_row<NB>(smem_u32(sV + (t % VS) * C::kTile) + r * 128, r, node, node, sNf + slot * W8, j);
               fence_proxy_async();
             }
           }
