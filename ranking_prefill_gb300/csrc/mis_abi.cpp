@@ -181,7 +181,7 @@ void free_plan(mis_plan_s* h) {
       return;
     }
   }
-  free_plan(h);
+  delete h;
 }
 
 }  // namespace

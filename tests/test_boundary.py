@@ -482,3 +482,16 @@ def test_layout_tile_map_and_walk_on_generated_batches(L):
         assert np.array_equal(np.sort(walk[walk >= 0]), np.arange(p.stats()["n_units"]))
 
     check()
+
+
+def test_more_plans_destroyed_than_are_kept(L):
+    s = synth.draw_shapes(synth.WORKLOADS["tiny"])
+    lay = lib.mis_build_layout(s.prefix_tokens, s.n_items, s.item_lens)
+    pl = _plan(lay)
+    plans = [C.c_void_p() for _ in range(8)]
+    for h in plans:
+        assert L.mis_plan_create(C.byref(pl.desc), None, 0, None, C.byref(h)) == lib.MIS_OK
+    assert len({h.value for h in plans}) == len(plans)
+    for h in plans:
+        assert L.mis_plan_destroy(h) == lib.MIS_OK
+    assert _plan(lay).workspace_size() > 0
