@@ -175,16 +175,19 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
       auto turn = [](Ring& r, int depth) { if (++r.slot == depth) { r.slot = 0; r.ph ^= 1; } };
       Ring rk{0, 0}, rv{0, 0};
       uint32_t pf0 = 0, pf1 = 0, qf = 0;                       // phases of P and Q
-      // PV of tile x for the step whose P is there (nks > 0), then S of the step
-      // behind it (more). V is MN-major: 8-key groups 1024 B apart, 64-column
-      // boxes kBox apart. The last tile's products release K and V, and in the
-      // unit's last step Q
-      auto step = [&](int x, uint32_t acc, int nks, bool done, bool more, bool last) {
-        tc_fence_after();
+      // Once barrier wb (a lane's own; none below 0) has passed phase wp: PV of tile
+      // x for the step whose P is there (nks > 0), then S of the step behind it
+      // (more). V is MN-major: 8-key groups 1024 B apart, 64-column boxes kBox
+      // apart. The last tile's products release K and V, and in the unit's last
+      // step Q. Descriptors are made before the wait
+      auto step = [&](int x, uint32_t acc, int nks, bool done, bool more, bool last, int wb, uint32_t wp) -> bool {
         const uint32_t dO = tm + colO(x), dS = tm + colS(x);
-        const uint64_t v = sdesc_sw128(smem_u32(sV) + rv.slot * C::kTile, C::kBox, 1024);
-        const uint64_t q = sdesc_sw128(smem_u32(sQ) + x * C::kTile, 16, 1024);
-        const uint64_t kd = sdesc_sw128(smem_u32(sK) + rk.slot * C::kTile, 16, 1024);
+        uint64_t v = sdesc_sw128(smem_u32(sV) + rv.slot * C::kTile, C::kBox, 1024);
+        uint64_t q = sdesc_sw128(smem_u32(sQ) + x * C::kTile, 16, 1024);
+        uint64_t kd = sdesc_sw128(smem_u32(sK) + rk.slot * C::kTile, 16, 1024);
+        asm volatile("" : "+l"(v), "+l"(q), "+l"(kd));
+        if (wb >= 0 && !wait_all(wb, wp, 0x400 + 0x10 * x)) return false;
+        tc_fence_after();
         if (elect_uniform()) {
           if (nks) {
             mma_ts(dO, dS, v, idO, acc);
@@ -211,6 +214,7 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
           }
         }
         __syncwarp();
+        return true;
       };
       Unit w;
       for (int lu = 0; ok && take(lu, w); ++lu) {
@@ -228,12 +232,8 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
           const bool l1 = (lane & 1) != 0, l2 = more && (lane & 2);
           const int wb = l1 ? (begin ? bQF : bVF + rv.slot) : l2 || begin ? bKF + rk.slot : bPF;
           const uint32_t wp = l1 ? (begin ? qf : rv.ph) : l2 || begin ? rk.ph : pf0;
-          if (!(ok = wait_all(wb, wp, 0x400))) break;
-          step(0, acc, nks, !pair, more, last);
-          if (pair) {
-            if (!begin && !(ok = wait_all(bPF + 1, pf1, 0x410))) break;
-            step(1, acc, nks, true, more, last);
-          }
+          if (!(ok = step(0, acc, nks, !pair, more, last, wb, wp))) break;
+          if (pair && !(ok = step(1, acc, nks, true, more, last, begin ? -1 : bPF + 1, pf1))) break;
           if (begin) {
             qf ^= 1;
           } else {
