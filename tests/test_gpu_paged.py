@@ -721,6 +721,44 @@ def test_two_streams_with_their_own_workspaces():
     b.compare(b.oracle())
 
 
+def test_two_host_threads_with_their_own_workspaces():
+    import threading
+    trees = [Tree([700, 300], [8, 3], 8, 2, 128, 32, None, seed=40).prepare(),
+             Tree([90, 500, 3], [70, 5, 30], 8, 2, 64, 16, None, seed=41).prepare()]
+    rows = [(randn(42, 300, 2, 64), randn(43, 300, 2, 64), 1e4), (randn(44, 300, 3, 128), randn(45, 300, 3, 128), 1e6)]
+    caches = [make_cache(20, 16, k.shape[1], k.shape[2]) for k, _, _ in rows]
+    slots = [np.random.default_rng(i).permutation(320)[:300] for i in range(2)]
+    d_slots, pos = [i32(s) for s in slots], i32(np.arange(300) * 7)
+    wws = [workspace(256) for _ in range(2)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            cache = lib.PagedCache(*caches[i])
+            for _ in range(40):
+                trees[i].call(stream=stream)
+                lib.mis_paged_write_kv(cache, rows[i][0], rows[i][1], d_slots[i], wws[i], position_ids=pos,
+                                       base=rows[i][2], stream=stream)
+            stream.synchronize()
+        except BaseException as e:                       # reported by the test, not by the thread
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for i in range(2):
+        trees[i].compare(trees[i].oracle())
+        k, v, base = rows[i]
+        kc, vc = (c.clone() for c in caches[i])
+        check_write(kc, vc, k, v, slots[i], pos=np.arange(300) * 7, base=base)       # the same again, alone
+        assert torch.equal(kc, caches[i][0]) and torch.equal(vc, caches[i][1])
+
+
 def test_rows_beyond_32_bit_element_offsets():
     # 2.3M cache rows of 1024 elements: offsets past 2^31 elements (and 2^32 bytes)
     H, D, ps = 8, 128, 64
