@@ -891,11 +891,10 @@ struct CombineParams {
   int32_t T, G, blocks;
 };
 
-template <int N>
-constexpr int kCombineWarps = N < 32 ? N / 4 : 8;
+constexpr int kCombineWarps = 4;
 
 template <int D, int N>
-__global__ void __launch_bounds__(32 * kCombineWarps<N>) mis_tree_combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(32 * kCombineWarps) mis_tree_combine_kernel(const CombineParams p) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -916,14 +915,14 @@ __global__ void __launch_bounds__(32 * kCombineWarps<N>) mis_tree_combine_kernel
       p.status[1] = where;
     }
   }
-  const int n0 = (blockIdx.x * kCombineWarps<N> + warp) * 4, pieces = u.w;
+  const int n0 = (blockIdx.x * kCombineWarps + warp) * 4, pieces = u.w;
   if (pieces < 2 || n0 >= u.y) return;
   const int sub = lane & 7, n = min(n0 + (lane >> 3), u.y - 1);
   // piece s: the first lies in block c's second slot, the others in the first
   // slots of the blocks that follow. A row's lane s looks at piece s (of 8 at
   // a time), while the first pieces' elements are on their way
   auto at = [&](int s) { return (int64_t)(s == 0 ? 2 * c + 1 : 2 * (c + s)) * N + n; };
-  constexpr int E = D / 32, A = 2;        // float4s of a lane, pieces in flight
+  constexpr int E = D / 32, A = 2;                     // float4s of a lane, pieces in flight
   auto load = [&](int s, float4* y) {
     const float4* src = reinterpret_cast<const float4*>(p.part + at(s) * D) + sub;
 #pragma unroll
@@ -1040,9 +1039,8 @@ mis_status_t launch_tree(const CUtensorMap* m, const TreeParams& p, const Combin
     const mis_status_t r = launch_wide(D, m, p, c.blocks, st);
     if (r != MIS_OK) return r;
   }
-  constexpr int CW = kCombineWarps<N>;
-  return launch_pdl(mis_tree_combine_kernel<D, N>, dim3(N / (4 * CW), (unsigned)c.blocks), dim3(32 * CW), 0,
-                    st, c) == cudaSuccess
+  return launch_pdl(mis_tree_combine_kernel<D, N>, dim3(N / (4 * kCombineWarps), (unsigned)c.blocks),
+                    dim3(32 * kCombineWarps), 0, st, c) == cudaSuccess
              ? MIS_OK
              : MIS_ERR_CUDA;
 }
