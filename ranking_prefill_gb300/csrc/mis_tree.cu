@@ -29,10 +29,10 @@
 // Any reference serves a column's softmax as long as its scores stay within
 // the exponent's reach of it. One reference for all columns of a warpgroup
 // stays in a register: it is the largest maximum, taken when the columns'
-// maxima lie within 2^40 of each other (else every column has its own, read
-// from shared memory). It is moved only when a score passes it by 2^8: one
-// vote per step replaces the exchange of maxima, and O in tensor memory is
-// rescaled only then.
+// maxima so far lie within 2^40 of each other (else every column has its own,
+// read from shared memory, at most 2^40 above its maximum). It is moved only
+// when a score passes it by 2^8: one vote per step replaces the exchange of
+// maxima, and O in tensor memory is rescaled only then.
 //
 // What bounds it: the stream of K and V. 64 decoded tokens over 512 to 4096 rows
 // (16 / 8 heads, D = 128, 562 MB): 94 us, 5.9 TB/s of 6.7 measured for a copy; 4
@@ -526,6 +526,9 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       bool one = true;                                   // one reference, -base, for all columns
                                                          // (else their scores are shifted, base 0)
       float base = 0.f;
+      // the largest score of column min(lane, NC - 1) in the steps that moved a
+      // reference: how far that column lies below a reference all columns share
+      float own = kEmpty;
       if (ok && lu >= 2) {
         ok = spin(bar(bSE + slot), ((lu >> 1) - 1) & 1, W, 0x700);
         ok = __all_sync(0xffffffffu, ok);
@@ -625,16 +628,18 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           // a lane for a column
           const int n = min(lane, NC - 1);
           const float old = first ? kEmpty : one ? -base : -ref[n];
-          float top = old;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) top = fmaxf(top, sMax[q * N + c0 + n]);
+          for (int q = 0; q < 4; ++q) own = fmaxf(own, sMax[q * N + c0 + n]);
           // columns without a row only count upwards, so that they never make
           // the reference move step after step
-          const float hi = warp_max(fmaxf(kEmpty, top));
-          const float lo = warp_min(c0 + n < rows ? top : INFINITY);
+          const float hi = warp_max(fmaxf(kEmpty, own));
+          const float lo = warp_min(c0 + n < rows ? own : INFINITY);
           const bool was = one;
           one = hi - lo <= kSpread || lo == INFINITY;
           base = one ? -hi : 0.f;
+          // a column that leaves the shared reference keeps it until its own
+          // scores pass it: references never go down
+          const float top = one ? hi : fmaxf(old, own);
           __syncwarp();
           if (!(was && one)) {
             // the scores in tensor memory go from the old references to the new
@@ -656,9 +661,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
             __syncwarp();
           }
           if (lane < NC) {
-            const float to = one ? hi : top;
-            ref[lane] = -to;
-            al[lane] = ex2(old - to);
+            ref[lane] = -top;
+            al[lane] = ex2(old - top);
           }
           __syncwarp();
           if (!first) {
