@@ -243,13 +243,6 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     tma_prefetch_desc(&kc8map); tma_prefetch_desc(&vc8map);
     tma_prefetch_desc(&kmap); tma_prefetch_desc(&vmap);
   }
-  // Q rows that no copy writes (G does not divide N): columns that nobody
-  // reads, but whose scores are looked at when references are drawn
-  for (int x = threadIdx.x; x < QS * NB * (N - p.npt * p.G) * 8; x += C::kThreads) {
-    const int row = x / 8 % (N - p.npt * p.G), box = x / 8 / (N - p.npt * p.G);
-    st_shared_v4(smem_u32(sQ) + box * C::kQBox + (p.npt * p.G + row) * 128 + x % 8 * 16, 0, 0, 0, 0);
-  }
-  fence_proxy_async();
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmem);
     tmem_relinquish();
@@ -519,7 +512,10 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         bar_any128(id, *abort_flag != 0);
         break;
       }
-      const int slot = lu & 1, rows = min(p.npt, w.R.n - w.rt * p.npt) * p.G;
+      // live: columns of this warpgroup that are rows of the unit. The others hold
+      // what Q's place held, other requests' rows mostly: nobody reads them, and
+      // their scores, whatever they are, move no reference
+      const int slot = lu & 1, rows = min(p.npt, w.R.n - w.rt * p.npt) * p.G, live = rows - c0;
       uint64_t l2[NC / 2];
 #pragma unroll
       for (int n = 0; n < NC / 2; ++n) l2[n] = 0ull;
@@ -571,7 +567,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
 #pragma unroll 1
           for (int q = 0; q < NC; q += 16) {
             const int c = c0 + q;
-            const uint32_t bits = node ? mk[c >> 5] >> (c & 31) : seen ? 0xffffu : 0u;
+            const uint32_t bits = node ? mk[c >> 5] >> (c & 31) : seen ? bit_range(0, live - q) : 0u;
             __syncwarp();
             uint32_t x[16];
             ld_cols<16>(tS + q, x);
@@ -601,9 +597,17 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           if (ok && active) {
             float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-            for (int n = 0; n < NC; n += 4) {
-              x0 = max3(x0, __uint_as_float(s[n]), __uint_as_float(s[n + 1]));
-              x1 = max3(x1, __uint_as_float(s[n + 2]), __uint_as_float(s[n + 3]));
+            for (int c = 0; c < NC; c += 8) {
+              if (c + 8 <= live) {
+#pragma unroll
+                for (int n = c; n < c + 8; n += 4) {
+                  x0 = max3(x0, __uint_as_float(s[n]), __uint_as_float(s[n + 1]));
+                  x1 = max3(x1, __uint_as_float(s[n + 2]), __uint_as_float(s[n + 3]));
+                }
+              } else if (c < live) {
+#pragma unroll
+                for (int n = c; n < c + 8; ++n) x0 = fmaxf(x0, n < live ? __uint_as_float(s[n]) : -INFINITY);
+              }
             }
             over |= fmaf(fmaxf(x0, x1), sa, base) > kGrow;
           }
@@ -617,7 +621,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           {
             float v[NC];
 #pragma unroll
-            for (int n = 0; n < NC; ++n) v[n] = active ? __uint_as_float(s[n]) : -INFINITY;
+            for (int n = 0; n < NC; ++n) v[n] = active && n < live ? __uint_as_float(s[n]) : -INFINITY;
             const int n = fold_cols<NC, true>(v, lane);
             float mine = v[0] * sa;
             if (!one && ref[n] < -kEmpty) mine -= ref[n];
@@ -630,10 +634,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           const float old = first ? kEmpty : one ? -base : -ref[n];
 #pragma unroll
           for (int q = 0; q < 4; ++q) own = fmaxf(own, sMax[q * N + c0 + n]);
-          // columns without a row only count upwards, so that they never make
-          // the reference move step after step
-          const float hi = warp_max(fmaxf(kEmpty, own));
-          const float lo = warp_min(c0 + n < rows ? own : INFINITY);
+          const float hi = warp_max(own);
+          const float lo = warp_min(n < live ? own : INFINITY);
           const bool was = one;
           one = hi - lo <= kSpread || lo == INFINITY;
           base = one ? -hi : 0.f;

@@ -128,3 +128,21 @@ def test_other_requests_climb(hq, D, n, low, climb):
     by_tile(t, 0, range(TILES))
     t.q.view(len(t.lens), n, hq, D)[1::2, :, :, 0] = climb
     check(t, [0, 1, 2, len(t.lens) - 2])
+
+
+@pytest.mark.parametrize("hq,D,n,low", KINDS)
+def test_bits_do_not_depend_on_other_requests_queries(hq, D, n, low):
+    t = batch(hq, D, n, low, 2, seed=5)
+    by_tile(t, 0, range(TILES))
+    t.prepare()
+    t.call()
+    q = t.q.view(len(t.lens), n, hq, D)
+    mine = lambda: (t.o.view(len(t.lens), n, hq, D)[::2].clone(),  # noqa: E731
+                    t.lse.view(hq, len(t.lens), n)[:, ::2].clone())
+    want = mine()
+    for x in (3.0, 20.0, 60.0, -60.0, float("inf"), float("nan")):
+        q[1::2, :, :, 0] = x
+        t.call()
+        assert lib.mis_get_device_status(t.ws) == lib.MIS_OK
+        for a, b in zip(mine(), want):
+            assert torch.equal(a, b), x
