@@ -523,7 +523,9 @@ mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const void* k, con
  *               most 128 query heads a kv head
  *   max_nodes — upper bound on a request's nodes, 1 .. MIS_TREE_MAX_NODES
  *   scale     — softmax scale of size 1e-20 to 1e20, of either sign; 0 selects
- *               1/sqrt(D)
+ *               1/sqrt(D). Products q_i k_j may be of any size that fp32 holds,
+ *               also where scale * q_i k_j passes fp32's range (lse is infinite
+ *               there)
  *   q, k, v, o, lse, row strides — as in mis_attention_fwd_plan (lse fp32
  *               [Hq, T] or NULL). Rows from cu_nodes[B] on are not written
  *   block_table — device int32 [B, max_pages], row stride in elements;

@@ -32,7 +32,10 @@
 // maxima so far lie within 2^40 of each other (else every column has its own,
 // read from shared memory, at most 2^40 above its maximum). It is moved only
 // when a score passes it by 2^8: one vote per step replaces the exchange of
-// maxima, and O in tensor memory is rescaled only then.
+// maxima, and O in tensor memory is rescaled only then. References are scores
+// before the scale (times its sign). scale * score - scale * reference in one
+// multiply-add is off by the rounding of scale * reference, so a reference that
+// is far from zero is taken off first, exactly where the score equals it.
 //
 // What bounds it: the stream of K and V. 64 decoded tokens over 512 to 4096 rows
 // (16 / 8 heads, D = 128, 562 MB): 94 us, 5.9 TB/s of 6.7 measured for a copy; 4
@@ -495,7 +498,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
     // scores are taken times the scale's sign, then scaled by its size: the
     // largest score is the largest product
-    const float sa = fabsf(p.scale_log2), sign = p.scale_log2 < 0.f ? -1.f : 1.f, inv_sa = 1.f / sa;
+    const float sa = fabsf(p.scale_log2), sign = p.scale_log2 < 0.f ? -1.f : 1.f;
     const uint64_t sax2 = f2_pack(__float_as_uint(sa), __float_as_uint(sa));
     // this thread's row of P: chunk c of its columns
     const uint32_t aP = smem_u32(sP) + (c0 >> 6) * C::kBox + r * 128;
@@ -519,7 +522,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       uint64_t l2[NC / 2];
 #pragma unroll
       for (int n = 0; n < NC / 2; ++n) l2[n] = 0ull;
-      bool one = true;                                   // one reference, -base, for all columns
+      bool one = true;                                   // one reference, -base / sa, for all columns
                                                          // (else their scores are shifted, base 0)
       float base = 0.f;
       // the largest score of column min(lane, NC - 1) in the steps that moved a
@@ -558,10 +561,11 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         const bool plain = __all_sync(0xffffffffu, seen && !node);
         // Steps that are not plain (new rows, a partial tile, a negative scale,
         // references by column) have their scores rewritten in tensor memory
-        // first: hidden ones -inf, the others times the scale's sign and less
-        // the column's reference. What follows is then the same short code for
-        // every step; unrolled for each kind, the kernel waited for instruction
-        // fetches more than for anything else.
+        // first: hidden ones -inf, the others times the scale's sign; and under
+        // references by column once more, less those, when they have been moved.
+        // What is left is then the same short code for every step; unrolled for
+        // each kind, the kernel waited for instruction fetches more than for
+        // anything else.
         bool over = !ok || first;
         if (ok && active && !(plain && one && sign > 0.f)) {
 #pragma unroll 1
@@ -571,20 +575,14 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
             __syncwarp();
             uint32_t x[16];
             ld_cols<16>(tS + q, x);
-            if (!(one && sign > 0.f)) {
-#pragma unroll
-              for (int n = 0; n < 16; ++n) {
-                const float b = one ? 0.f : ref[q + n];
-                float y = __uint_as_float(x[n]) * sign;
-                // a column that saw nothing so far has no reference to be taken off
-                if (b >= -kEmpty) over |= ((bits >> n) & 1u) && y > -INFINITY;
-                else y = fmaf(b, inv_sa, y);
-                x[n] = __float_as_uint(y);
-              }
-            }
 #pragma unroll
             for (int n = 0; n < 16; ++n)
-              if (!((bits >> n) & 1u)) x[n] = 0xff800000u;
+              x[n] = (bits >> n) & 1u ? __float_as_uint(__uint_as_float(x[n]) * sign) : 0xff800000u;
+            if (!one) {
+              // passes, too, in a column that saw nothing so far (kEmpty)
+#pragma unroll
+              for (int n = 0; n < 16; ++n) over |= (__uint_as_float(x[n]) + ref[q + n]) * sa > kGrow;
+            }
             tmem_st16(tS + q, x);
           }
           tmem_st_wait();
@@ -594,7 +592,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         if (ok && active) ld_cols<NC>(tS, s);
         bool move = first;
         if (!first) {
-          if (ok && active) {
+          if (ok && active && one) {
             float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
             for (int c = 0; c < NC; c += 8) {
@@ -623,48 +621,26 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
             for (int n = 0; n < NC; ++n) v[n] = active && n < live ? __uint_as_float(s[n]) : -INFINITY;
             const int n = fold_cols<NC, true>(v, lane);
-            float mine = v[0] * sa;
-            if (!one && ref[n] < -kEmpty) mine -= ref[n];
-            sMax[sw * N + c0 + n] = mine;
+            sMax[sw * N + c0 + n] = v[0];
           }
           bar_sync128(id);
           // every warp draws the same conclusion from the four warps' maxima,
           // a lane for a column
           const int n = min(lane, NC - 1);
-          const float old = first ? kEmpty : one ? -base : -ref[n];
+          const float old = first ? kEmpty : -ref[n];
 #pragma unroll
           for (int q = 0; q < 4; ++q) own = fmaxf(own, sMax[q * N + c0 + n]);
           const float hi = warp_max(own);
           const float lo = warp_min(n < live ? own : INFINITY);
-          const bool was = one;
-          one = hi - lo <= kSpread || lo == INFINITY;
-          base = one ? -hi : 0.f;
+          one = lo == INFINITY || (hi > kEmpty && (hi - lo) * sa <= kSpread && fabsf(hi) * sa <= kFar);
+          base = one && hi > kEmpty ? -hi * sa : 0.f;
           // a column that leaves the shared reference keeps it until its own
           // scores pass it: references never go down
-          const float top = one ? hi : fmaxf(old, own);
+          const float to = one ? hi : fmaxf(old, own);
           __syncwarp();
-          if (!(was && one)) {
-            // the scores in tensor memory go from the old references to the new
-            const float from = was || old <= kEmpty ? 0.f : old;
-            const float to = one || top <= kEmpty ? 0.f : top;
-            if (lane < NC) al[lane] = (from - to) * inv_sa;
-            __syncwarp();
-            if (active) {
-#pragma unroll 1
-              for (int q = 0; q < NC; q += 8) {
-                uint32_t x[8];
-                ld_cols<8>(tS + q, x);
-#pragma unroll
-                for (int n = 0; n < 8; ++n) x[n] = __float_as_uint(__uint_as_float(x[n]) + al[q + n]);
-                tmem_st8(tS + q, x);
-              }
-              tmem_st_wait();
-            }
-            __syncwarp();
-          }
           if (lane < NC) {
-            ref[lane] = -top;
-            al[lane] = ex2(old - top);
+            ref[lane] = -to;
+            al[lane] = ex2((old - to) * sa);
           }
           __syncwarp();
           if (!first) {
@@ -690,7 +666,19 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
             }
           }
         }
-        if (move && ok && active) ld_cols<NC>(tS, s);
+        if (!one && ok && active) {
+#pragma unroll 1
+          for (int q = 0; q < NC; q += 8) {
+            uint32_t x[8];
+            ld_cols<8>(tS + q, x);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) x[n] = __float_as_uint(__uint_as_float(x[n]) + ref[q + n]);
+            tmem_st8(tS + q, x);
+          }
+          tmem_st_wait();
+          __syncwarp();
+        }
+        if ((move || !one) && ok && active) ld_cols<NC>(tS, s);
         if (ok && active) {
           const uint64_t basex2 = f2_pack(__float_as_uint(base), __float_as_uint(base));
           uint32_t pk[NC / 2];
@@ -778,7 +766,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           const float* l = sL + slot * 4 * N + n;
           const bool dead = (sDead[slot * 4 + x] >> lane) & 1u;
           if (!dead) {
-            mx[x] = -sM[slot * N + n];
+            mx[x] = -sM[slot * N + n];                   // as the references: before the scale
             sum[x] = (l[0] + l[N]) + (l[2 * N] + l[3 * N]);
           }
         }
@@ -794,7 +782,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
             } else if (p.lse) {
               const int i = over_g(p, n), g = n - i * p.G;
               p.lse[(int64_t)(w.h * p.G + g) * p.T + w.R.r0 + node0 + i] =
-                  sum[x] != 0.f ? (mx[x] + log2f(sum[x])) * kLn2 : -INFINITY;
+                  sum[x] != 0.f ? fmaf(mx[x], fabsf(p.scale_log2), log2f(sum[x])) * kLn2 : -INFINITY;
             }
           }
         }
@@ -895,6 +883,7 @@ struct CombineParams {
   float* lse;
   int64_t os;
   int32_t T, G, blocks;
+  float scale_log2;        // its size
 };
 
 constexpr int kCombineWarps = 4;
@@ -953,7 +942,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) mis_tree_combine_kernel(co
     float a = 0.f;
     if (s0 + sub < pieces) {
       const float2 x = p.ml[at(s0 + sub)];
-      a = ex2(x.x - m);
+      a = ex2((x.x - m) * p.scale_log2);
       l += a * x.y;
     }
     __syncwarp();
@@ -989,7 +978,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) mis_tree_combine_kernel(co
     dst[8 * e] = inv != 0.f ? make_uint2(pack_bf16(acc[e].x * inv, acc[e].y * inv),
                                          pack_bf16(acc[e].z * inv, acc[e].w * inv))
                             : make_uint2(0u, 0u);
-  if (p.lse && sub == 0) p.lse[(int64_t)h * p.T + u.x + i] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (p.lse && sub == 0)
+    p.lse[(int64_t)h * p.T + u.x + i] = l != 0.f ? fmaf(m, p.scale_log2, log2f(l)) * kLn2 : -INFINITY;
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -1152,7 +1142,7 @@ extern "C" mis_status_t mis_tree_attention_fwd(
     c.cta_status = p.cta_status; c.meta = p.meta; c.ml = p.ml; c.part = p.part;
     c.status = reinterpret_cast<uint32_t*>(base);
     c.o = p.o; c.lse = lse; c.os = o_row_stride;
-    c.T = desc->T; c.G = G; c.blocks = num_sms();
+    c.T = desc->T; c.G = G; c.blocks = num_sms(); c.scale_log2 = std::fabs(p.scale_log2);
     if (D == 128) {
       if (N == 16) return launch_tree<128, 16>(maps, p, c, st);
       if (N == 32) return launch_tree<128, 32>(maps, p, c, st);

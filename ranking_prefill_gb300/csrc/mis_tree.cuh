@@ -14,7 +14,11 @@ using namespace dev;
 
 constexpr int kKeys = 128;                       // keys of a step
 constexpr float kGrow = 8.0f;                    // log2 units a score may pass the reference by
-constexpr float kEmpty = -1.0e30f;               // maximum of a row that has seen nothing
+constexpr float kEmpty = -3.402823466e38f;       // maximum of a row that has seen nothing: below any score
+// Scores are taken times the scale's sign, maxima and references kept before
+// its size. Scores this far from zero (log2 units) have their reference taken
+// off first: scale * reference rounds by half its last bit, 2^-15 here
+constexpr float kFar = 1024.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 struct TreeParams {
@@ -39,7 +43,7 @@ struct TreeParams {
   uint32_t* cta_status;    // [blocks][2]
   int4* meta;              // [blocks] the split unit that starts in the block: its first row of q,
                            // columns, kv head, pieces
-  float2* ml;              // [2 * blocks][rows of a unit] (max, sum) of a piece
+  float2* ml;              // [2 * blocks][rows of a unit] (max before the scale, sum) of a piece
   float* part;             // [2 * blocks][rows of a unit][D]
   uint64_t wait_ns;
   uint32_t stall;

@@ -349,7 +349,7 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
       }
       const int i = over_g(p, min(r, rows - 1));         // the row's node
       const uint32_t* mrow = sMask + (slot * MIS_TREE_MAX_NODES + node0 + i) * W8;
-      float m = kEmpty, l = 0.f;
+      float m = kEmpty, l = 0.f;                         // the row's reference and sum
       // the page under box `lane` of a step, asked for a step ahead (0 where
       // there is no cached row)
       const int32_t* trow = p.table + (int64_t)w.b * p.table_stride;
@@ -426,12 +426,22 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
 #pragma unroll
         for (int c = 0; c < kKeys; c += 2)
           mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-        const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sa);
-        const bool grow = top > m + kGrow;
+        const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        const bool grow = (top - m) * sa > kGrow;
         const bool any_grow = __any_sync(0xffffffffu, grow);
-        const float alpha = grow ? ex2(m - top) : 1.f;
+        const float alpha = grow ? ex2((m - top) * sa) : 1.f;
         if (grow) { l *= alpha; m = top; }
-        const uint64_t off = f2_pack(__float_as_uint(-m), __float_as_uint(-m));
+        // the reference after the scale, negated; one far from zero is taken off
+        // the scores instead (a row that saw nothing has no score to take it off)
+        const float scaled = -m * sa;
+        const bool far = fabsf(scaled) > kFar;
+        const float off = far ? 0.f : scaled;
+        if (__any_sync(0xffffffffu, far && m > kEmpty)) {
+          const float b = far ? -m : 0.f;
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) + b);
+        }
+        const uint64_t offx2 = f2_pack(__float_as_uint(off), __float_as_uint(off));
         uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -440,7 +450,7 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
           for (int c = 0; c < 32; ++c) {
             const int k2 = hf * 64 + 2 * c;
             float x0, x1;
-            f2_unpack(f2_fma(f2_pack(s[k2], s[k2 + 1]), sax2, off), x0, x1);
+            f2_unpack(f2_fma(f2_pack(s[k2], s[k2 + 1]), sax2, offx2), x0, x1);
             const float p0 = ex2(x0), p1 = ex2(x1);
             sum[c & 3] = f2_add(sum[c & 3], f2_pack(__float_as_uint(p0), __float_as_uint(p1)));
             pk[c] = pack_bf16(p0, p1);
@@ -491,7 +501,7 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
         if (w.k0 == 0 && threadIdx.x == 128)
           p.meta[blockIdx.x] = make_int4(w.R.r0 + node0, min(p.npu, w.R.n - node0) * p.G, w.h, share.pieces(w));
       } else if (mine && p.lse) {
-        p.lse[(int64_t)(w.h * p.G + g) * p.T + orow] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        p.lse[(int64_t)(w.h * p.G + g) * p.T + orow] = l != 0.f ? fmaf(m, sa, log2f(l)) * kLn2 : -INFINITY;
       }
       const float inv = l != 0.f ? 1.f / l : 0.f;                  // NaN stays
       const int64_t oat = mine ? orow * p.os + (int64_t)(w.h * p.G + g) * D : -1;

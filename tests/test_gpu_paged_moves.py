@@ -146,3 +146,39 @@ def test_bits_do_not_depend_on_other_requests_queries(hq, D, n, low):
         assert lib.mis_get_device_status(t.ws) == lib.MIS_OK
         for a, b in zip(mine(), want):
             assert torch.equal(a, b), x
+
+
+# scores of any size: (scale, power) of a head whose products with the keys are whole
+# numbers times 2^power, so exact in fp32
+SIZES = [(1.0, 9), (1.0, 24), (1.0, 31), (-1.0, 33), (1.0, 100), (-1.0, 118), (1e20, 0), (1e20, 60), (-1e20, 30),
+         (1e-20, 100)]
+
+
+@pytest.mark.parametrize("scale,power", SIZES)
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("hq,D,n,low", KINDS)
+def test_scores_of_any_size(hq, D, n, low, down, scale, power):
+    # keys of one tile tie, so do two tiles; the other heads see every key alike.
+    # Probabilities are 1 / m or 0, exactly, whatever the size
+    t = batch(hq, D, n, low, 1, seed=6, scale=scale)
+    for x in (t.q, t.k, t.kc):
+        x.zero_()
+    m = np.array([150, 100, 201, 7, 201, 200, 3, 9, 40, 201, 60, 61, 62, 63, 64, 1]) - (250 if down else 0)
+    by_tile(t, 0, m * np.sign(scale))
+    t.k[:, 0, 0] = (-255 if down else 0) * float(np.sign(scale))
+    t.q[:, 0, 0] = 2.0 ** power
+    t.prepare()
+    t.call()
+    assert lib.mis_get_device_status(t.ws) == lib.MIS_OK
+    got, gl = f64(t.o), f64(t.lse)
+    requests = some(t)
+    rows = np.concatenate([np.arange(t.cu[b], t.cu[b + 1]) for b in requests])
+    o, ls, a, _ = t.oracle(rows_of=requests)
+    tol = (2.0 ** -8 + 2.0 ** -12) * a + 2.0 ** -8 * (1 + 2.0 ** -8) * np.abs(o)
+    assert (np.abs(got - o)[rows] <= tol[rows]).all()
+    with np.errstate(over="ignore"):
+        want = ls[:, rows].astype(np.float32).astype(np.float64)        # past fp32's range: infinite
+    inf = np.isinf(want)
+    assert (gl[:, rows][inf] == want[inf]).all()
+    e = np.abs(gl[:, rows] - np.where(inf, 0, want))[~inf]
+    assert (e <= 2.0 ** -20 * (1 + np.abs(want[~inf]))).all(), e.max()
