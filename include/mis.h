@@ -538,8 +538,9 @@ mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const void* k, con
  *               -inf) and no row sees it, its children count as roots.
  *               NULL: every request is a chain (node i's parent is i - 1)
  * What a node does not see never reaches it, whatever its value (NaN and
- * infinities in unused cache rows or in other branches included). A row none
- * of whose visible scores is above -inf gets o = 0 and lse = -inf.
+ * infinities in unused cache rows or in other branches included); what it does
+ * see makes its element of o infinite or NaN, however small its probability. A
+ * row none of whose visible scores is above -inf gets o = 0 and lse = -inf.
  * Found on the device, reported as MIS_ERR_DEVICE_INDEX: a request with a
  * bad cache_len, more than max_nodes rows, or a bad cu_nodes range is
  * skipped (its rows are not written); a page id outside the cache hides its

@@ -944,6 +944,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) mis_tree_combine_kernel(co
       const float2 x = p.ml[at(s0 + sub)];
       a = ex2((x.x - m) * p.scale_log2);
       l += a * x.y;
+      // -0: a piece that saw something, but too far below the maximum to weigh
+      if (a == 0.f && x.y != 0.f) a = -0.f;
     }
     __syncwarp();
     for (int s1 = 0; s1 < min(8, pieces - s0); s1 += A) {
@@ -953,9 +955,19 @@ __global__ void __launch_bounds__(32 * kCombineWarps) mis_tree_combine_kernel(co
       }
 #pragma unroll
       for (int s = 0; s < A; ++s) {
-        // a piece that saw nothing weighs nothing, whatever it holds
+        // a piece that saw nothing weighs nothing, whatever it holds; of one
+        // that weighs too little, non-finite elements count, as where a block
+        // has the whole unit
         const float b = __shfl_sync(0xffffffffu, a, (lane & 24) + s1 + s);
-        if (b != 0.f) {
+        if (b == 0.f && signbit(b)) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            acc[e].x += isfinite(y[s][e].x) ? 0.f : y[s][e].x;
+            acc[e].y += isfinite(y[s][e].y) ? 0.f : y[s][e].y;
+            acc[e].z += isfinite(y[s][e].z) ? 0.f : y[s][e].z;
+            acc[e].w += isfinite(y[s][e].w) ? 0.f : y[s][e].w;
+          }
+        } else if (b != 0.f) {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             acc[e].x = fmaf(b, y[s][e].x, acc[e].x);

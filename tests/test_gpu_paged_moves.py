@@ -182,3 +182,44 @@ def test_scores_of_any_size(hq, D, n, low, down, scale, power):
     assert (gl[:, rows][inf] == want[inf]).all()
     e = np.abs(gl[:, rows] - np.where(inf, 0, want))[~inf]
     assert (e <= 2.0 ** -20 * (1 + np.abs(want[~inf]))).all(), e.max()
+
+
+@pytest.mark.parametrize("lens", [[100, 110], [20000, 30000]])           # whole units mostly, and pieces
+@pytest.mark.parametrize("where", ["node", "cache"])
+@pytest.mark.parametrize("hq,D,n,low", KINDS)
+def test_infinite_values_with_small_weights_reach_the_rows_that_see_them(hq, D, n, low, where, lens):
+    # one cached row's scores lie 300 powers of two above all others
+    nodes = [n, n]
+    par = np.concatenate([[-1], np.arange(n - 1) // 2, [-1], np.arange(n - 1) // 2]).astype(int)
+    t = T.Tree(lens, nodes, hq, 1, D, 64, par, seed=50, scale=LN2, max_nodes=max(n, -(-low // hq)))
+    t.q.mul_(0.125)
+    for x in (t.q, t.k, t.kc):
+        x[..., 0] = 0
+    t.q[..., 0] = 60.0
+    t.kc[int(t.table[0, 1]), 7, 0, 0] = 5.0
+    sees = np.zeros((2 * n, 2 * n), bool)
+    for b in range(2):
+        sees[b * n:b * n + n, b * n:b * n + n] = T.P.ancestors(par[b * n:b * n + n])
+    want = [x.copy() for x in t.oracle()]
+    if where == "node":
+        j = min(1, n - 1)
+        t.v[j, 0, 5], t.v[j, 0, 9] = float("inf"), float("nan")
+        hit = sees[:, j]
+    else:
+        page = int(t.table[0, (lens[0] - 1) // 64])
+        t.vc[page, 0, 0, 5], t.vc[page, 0, 0, 9] = float("inf"), float("nan")
+        hit = np.arange(2 * n) < n
+    t.prepare()
+    t.call()
+    assert lib.mis_get_device_status(t.ws) == lib.MIS_OK
+    got = f64(t.o)
+    if where == "node":
+        assert (got[hit][:, :, 5] == np.inf).all()
+    assert not np.isfinite(got[hit][:, :, 5]).any() and np.isnan(got[hit][:, :, 9]).all()
+    for d in (5, 9):
+        got[hit, :, d] = want[0][hit, :, d] = 0
+    assert np.isfinite(got).all()
+    d = 2.0 * D * 2.0 ** -24 * want[3] + 2.0 ** -20 * (1 + want[3])
+    tol = (2.0 ** -8 + 2.0 ** -12 + np.expm1(2 * d).T[:, :, None]) * want[2] + \
+        2.0 ** -8 * (1 + 2.0 ** -8) * np.abs(want[0])
+    assert (np.abs(got - want[0]) <= tol).all()
