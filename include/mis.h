@@ -463,7 +463,8 @@ typedef struct {
  *   position_ids  — device int32 [T] out or NULL: the row's position in its
  *                   request (cache_len[b] + d), 0 for rows from cu_new[B] on
  * cache_len_out may be cache_len and free_head_out free_head (in place);
- * other overlaps are not allowed. All pointers 4-byte aligned.
+ * another overlap of an output (the table and the workspace among them) with an
+ * argument is MIS_ERR_INVALID_ARG. All pointers 4-byte aligned.
  * Refused requests gain no rows and no pages (their lengths stay, cu_new
  * gives them no rows), the others are served:
  *   - a negative length, or one past max_pages * page_size rows, and a
@@ -489,7 +490,8 @@ mis_status_t mis_paged_extend(int32_t B, int32_t T, int32_t page_size, int32_t n
  *     cache row slot_map[i] = (rope(k[s_i], position_ids[i]), v[s_i]),
  *     s_i = src_rows[i], or i when src_rows is NULL,  i = 0 .. n-1.
  *   k, v          — device bf16 [T, Hkv, D], row strides in elements (>=
- *                   Hkv*D, multiples of 8), 16-byte aligned; not the cache
+ *                   Hkv*D, multiples of 8), 16-byte aligned; nothing read
+ *                   lies in the cache (MIS_ERR_INVALID_ARG)
  *   slot_map      — device int32 [n]; a negative slot skips its row (the
  *                   padding of mis_paged_extend). Slots must differ: two rows
  *                   at one slot leave pieces of either
@@ -545,7 +547,9 @@ mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const void* k, con
  * bad cache_len, more than max_nodes rows, or a bad cu_nodes range is
  * skipped (its rows are not written); a page id outside the cache hides its
  * rows; a parent out of range counts as MIS_TREE_ROOT.
- * o and lse overlap no input. fp32 scores, statistics and accumulation;
+ * o, lse and the workspace overlap no input, the cache among them, nor each
+ * other (MIS_ERR_INVALID_ARG; o may be columns of a buffer whose other columns
+ * are q, k or v, at one row stride). fp32 scores, statistics and accumulation;
  * probabilities are rounded to bf16 for the second product, o to bf16. The
  * same call gives the same bits. Two kernels. A wait inside the first can last
  * as long as a block works on one request, about 2 us per 128 cached rows

@@ -125,6 +125,27 @@ bool kernel_attr_once(const void* kernel, int smem_bytes);
 // Host-side checks of a paged cache's descriptor (mis_paged.cu).
 mis_status_t check_paged_cache(const mis_paged_cache* c);
 
+// An argument's memory: rows of `width` bytes, `stride` bytes apart.
+struct Span {
+  uint64_t lo, hi;         // its range; equal where there is none
+  int64_t rows, stride, width;
+  Span(const void* at, int64_t n, int64_t pitch, int64_t bytes) : rows(n), stride(pitch), width(bytes) {
+    lo = hi = reinterpret_cast<uintptr_t>(at);
+    if (!at || n < 1 || bytes < 1) return;
+    const auto end = (unsigned __int128)lo + (uint64_t)bytes + (unsigned __int128)(uint64_t)(n - 1) * (uint64_t)pitch;
+    hi = end > UINT64_MAX ? UINT64_MAX : (uint64_t)end;
+  }
+};
+// Whether the rows of two arguments whose ranges meet share bytes. Rows of one
+// stride may lie between each other (columns of one buffer); of two strides
+// they count as sharing.
+bool rows_meet(const Span& a, const Span& b);
+inline bool overlap(const Span& a, const Span& b) {
+  return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi && rows_meet(a, b);
+}
+// The first row of K or V (base) of a paged cache and all that follow it.
+Span cache_span(const mis_paged_cache* c, const void* base);
+
 // Process-wide wait limit for the kernels' bounded waits.
 uint64_t wait_limit_ns();
 // Process-wide failure-injection mask (bit 0: attention, bit 1: scoring).

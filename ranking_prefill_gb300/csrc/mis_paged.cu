@@ -417,6 +417,29 @@ mis_status_t check_paged_cache(const mis_paged_cache* c) {
   return MIS_OK;
 }
 
+bool rows_meet(const Span& a, const Span& b) {
+  if (a.rows > 1 && b.rows > 1 && a.stride != b.stride) return true;
+  const int64_t stride = a.rows > 1 ? a.stride : b.stride;
+  if ((a.rows == 1 && b.rows == 1) || stride < 1) return true;
+  // where b's rows begin in a's
+  const int64_t d = b.lo >= a.lo ? (int64_t)((b.lo - a.lo) % (uint64_t)stride)
+                                 : (stride - (int64_t)((a.lo - b.lo) % (uint64_t)stride)) % stride;
+  return d < a.width || d > stride - b.width;
+}
+
+Span cache_span(const mis_paged_cache* c, const void* base) {
+  auto reach = [](int64_t extent, int64_t stride) { return extent > 1 ? (extent - 1) * stride : 0; };
+  const int64_t heads = reach(c->Hkv, c->head_stride) + c->D;             // of one row
+  const int64_t page = reach(c->page_size, c->row_stride) + heads;
+  const int64_t all = reach(c->n_pages, c->page_stride) + page;
+  // rows at one stride; else pages at one; else all as one piece
+  const bool rows = c->n_pages == 1 || c->page_stride == c->page_size * c->row_stride;
+  if (rows && heads <= c->row_stride)
+    return {base, (int64_t)c->n_pages * c->page_size, c->row_stride * 2, heads * 2};
+  if (c->n_pages > 1 && page <= c->page_stride) return {base, c->n_pages, c->page_stride * 2, page * 2};
+  return {base, 1, all * 2, all * 2};
+}
+
 }  // namespace mis
 
 using namespace mis;
@@ -447,6 +470,22 @@ extern "C" mis_status_t mis_paged_extend(
     if (!aligned(ptr, 4)) return MIS_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < mis_paged_extend_workspace_size(B))
     return MIS_ERR_WORKSPACE;
+  {
+    auto ints = [](const int32_t* at, int64_t n) { return Span(at, 1, 0, 4 * n); };
+    const Span in[4] = {ints(new_len, B), ints(cache_len, B), ints(free_pages, n_free), ints(free_head, 1)};
+    const Span out[7] = {ints(cache_len_out, B), ints(free_head_out, 1), ints(cu_new, (int64_t)B + 1),
+                         ints(slot_map, T), ints(position_ids, T),
+                         Span{block_table, B, 4 * block_table_stride, 4 * (int64_t)max_pages},
+                         Span{workspace, 1, 0, (int64_t)mis_paged_extend_workspace_size(B)}};
+    for (int i = 0; i < 7; ++i) {
+      for (int j = 0; j < 4; ++j)
+        if (!(i == 0 && j == 1 && cache_len_out == cache_len) &&
+            !(i == 1 && j == 3 && free_head_out == free_head) && overlap(out[i], in[j]))
+          return MIS_ERR_INVALID_ARG;
+      for (int j = 0; j < i; ++j)
+        if (overlap(out[i], out[j])) return MIS_ERR_INVALID_ARG;
+    }
+  }
   ExtendParams p;
   p.page_shift = 31 - __builtin_clz((unsigned)page_size);
   p.vec = aligned(slot_map, 16) && aligned(position_ids, 16);
@@ -495,6 +534,12 @@ extern "C" mis_status_t mis_paged_write_kv(const mis_paged_cache* cache, const v
   if (!slot_map || !aligned(slot_map, 4) || !aligned(src_rows, 4) || !aligned(position_ids, 4))
     return MIS_ERR_INVALID_ARG;
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return MIS_ERR_INVALID_ARG;
+  for (const Span& out : {cache_span(cache, cache->k), cache_span(cache, cache->v),
+                          Span{workspace, 1, 0, (int64_t)kStatusBytes}})
+    for (const Span& in : {Span{k, T, 2 * k_row_stride, 2 * w}, Span{v, T, 2 * v_row_stride, 2 * w},
+                           Span{slot_map, 1, 0, 4 * (int64_t)n}, Span{src_rows, 1, 0, 4 * (int64_t)n},
+                           Span{position_ids, 1, 0, 4 * (int64_t)n}})
+      if (overlap(out, in)) return MIS_ERR_INVALID_ARG;
   WriteParams p;
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.v = static_cast<const __nv_bfloat16*>(v);

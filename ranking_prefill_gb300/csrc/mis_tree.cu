@@ -1095,6 +1095,21 @@ extern "C" mis_status_t mis_tree_attention_fwd(
   const int64_t rows = (int64_t)desc->max_nodes * (desc->Hq / cache->Hkv);
   if ((double)tiles * desc->B * cache->Hkv * (rows > 64 ? 2.0 * ((rows + 127) / 128) : 1.0) >= 2147483648.0)
     return MIS_ERR_UNSUPPORTED;
+  if (desc->T > 0) {                     // blocks still read what others write
+    const int64_t T = desc->T, B = desc->B;
+    const Span in[9] = {{q, T, 2 * q_row_stride, 2 * wq}, {k, T, 2 * k_row_stride, 2 * wk},
+                        {v, T, 2 * v_row_stride, 2 * wk}, cache_span(cache, cache->k),
+                        cache_span(cache, cache->v), {block_table, B, 4 * block_table_stride, 4 * (int64_t)max_pages},
+                        {cache_len, 1, 0, 4 * B}, {cu_nodes, 1, 0, 4 * B + 4}, {parents, 1, 0, 4 * T}};
+    const Span out[3] = {{o, T, 2 * o_row_stride, 2 * wq}, {lse, 1, 0, 4 * T * desc->Hq},
+                         {workspace, 1, 0, (int64_t)ws.total}};
+    for (int i = 0; i < 3; ++i) {
+      for (const Span& x : in)
+        if (overlap(out[i], x)) return MIS_ERR_INVALID_ARG;
+      for (int j = 0; j < i; ++j)
+        if (overlap(out[i], out[j])) return MIS_ERR_INVALID_ARG;
+    }
+  }
   if (desc->T == 0)
     return cudaMemsetAsync(workspace, 0, 8, st) == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
   try {

@@ -645,7 +645,7 @@ class PagedCache:
         self.desc = mis_paged_cache(_dptr(k), _dptr(v), self.n_pages, self.page_size, self.Hkv, self.D,
                                     k.stride(0), k.stride(1), k.stride(2))
         self.ref = C.byref(self.desc)
-        self.device, self.at = k.get_device(), (k.data_ptr(), v.data_ptr())
+        self.device = k.get_device()
 
 
 class TreeDesc:
@@ -743,10 +743,7 @@ def mis_paged_write_kv(cache: PagedCache, k, v, slot_map, workspace, position_id
                 src = t.data_ptr()
     if not (slot_map.is_contiguous() and workspace.is_contiguous()):
         raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
-    kp, vp = k.data_ptr(), v.data_ptr()
-    if n and (kp == cache.at[0] or kp == cache.at[1] or vp == cache.at[0] or vp == cache.at[1]):
-        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
-    st = L.mis_paged_write_kv(cache.ref, kp, vp, ks, vs, T, src, slot_map.data_ptr(), n,
+    st = L.mis_paged_write_kv(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs, T, src, slot_map.data_ptr(), n,
                               pos, base, workspace.data_ptr(), workspace.numel(), st)
     if st:
         raise MisError(st, where)
@@ -788,10 +785,8 @@ def mis_tree_attention_fwd(desc: TreeDesc, q, k, v, o, lse, block_table, cache_l
         if parents.numel() < T or not parents.is_contiguous():
             raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
         parents = parents.data_ptr()
-    qp, kp, vp, op = q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr()
-    if T and (op == qp or op == kp or op == vp):          # blocks still read what others write
-        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
-    st = L.mis_tree_attention_fwd(desc.ref, c.ref, qp, kp, vp, op, lse, qs, ks, vs, os_,
+    st = L.mis_tree_attention_fwd(desc.ref, c.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse,
+                                  qs, ks, vs, os_,
                                   block_table.data_ptr(), cols, stride, cache_len.data_ptr(),
                                   cu_nodes.data_ptr(), parents, workspace.data_ptr(), workspace.numel(), st)
     if st:
