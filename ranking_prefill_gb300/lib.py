@@ -597,7 +597,8 @@ def _here(stream):
             torch.cuda.init()
             _device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
         else:
-            _device, _raw_stream = (lambda: -1), (lambda dev: None)
+            # no device, so that no tensor is on it (a host tensor's get_device() is -1)
+            _device, _raw_stream = (lambda: None), (lambda dev: None)
         _BF16, _I32, _U8, _F32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
         _torch = torch
     dev = _device()
