@@ -100,16 +100,17 @@ struct TreeCfg {
   static constexpr int kTmem = N == 16 ? 64 : 4 * N;    // S_0 | S_1 | O_0 | O_1
   // floats / words behind the tiles
   static constexpr int oMask = 0;                       // [2][kNodes][kNW]
-  static constexpr int oDead = oMask + 2 * kNodes * kNW;   // [2][4] unused rows of the tile
-  static constexpr int oNf = oDead + 8;                 // [2][8] keys with a non-finite value
-  static constexpr int oM = oNf + 16;                   // [2][N] references, negated, for the epilogue
+  static constexpr int oDead = oMask + 2 * kNodes * kNW;   // [2][kNW] unused rows of the tile
+  static constexpr int kJW = kNodes / 32;               // words of a unit's new keys
+  static constexpr int oNf = oDead + 2 * kNW;           // [2][kJW] those with a non-finite value
+  static constexpr int oM = oNf + 2 * kJW;                  // [2][N] references, negated, for the epilogue
   static constexpr int oL = oM + 2 * N;                 // [2][4][N] sums of each softmax warp
   static constexpr int oMax = oL + 8 * N;               // [4][N] maxima of a step by warp
   static constexpr int oRef = oMax + 4 * N;             // [4][N] a warp's copy of the negated references
   static constexpr int oAl = oRef + 4 * N;              // [4][N] ... of the factors of a move
   static constexpr int oInv = oAl + 4 * N;              // [4][N] an epilogue warp's 1 / sum
-  static constexpr int oPar = oInv + 4 * N;             // [256] int16: parents
-  static constexpr int kWords = oPar + MIS_TREE_MAX_NODES / 2;
+  static constexpr int oPar = oInv + 4 * N;             // [kNodes] int16: parents
+  static constexpr int kWords = oPar + kNodes / 2;
   static constexpr int kData = kQS * kQ + kP + (kK + kV) * kTile;
   static constexpr int kSmem = kData + 4 * kWords + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
@@ -185,7 +186,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ CUtensorMap vmap, const TreeParams p) {
   using C = TreeCfg<D, N>;
   constexpr int NB = C::kNB, NC = C::kNC, WG = C::kWG, KS = C::kK, VS = C::kV, QS = C::kQS;
-  constexpr int NW = C::kNW;
+  constexpr int NW = C::kNW, JW = C::kJW;
   // barriers
   constexpr int bQF = 0, bQE = bQF + 2, bKF = bQE + 2, bKE = bKF + KS, bVF = bKE + KS,
                 bVE = bVF + VS, bSF = bVE + VS, bPF = bSF + 2, bPV = bPF + 1, bOF = bPV + 1,
@@ -435,13 +436,13 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           __syncwarp();
         }
         // columns of unused nodes
-        if (lane < 8) sNf[sm * 8 + lane] = 0;
+        if (lane < JW) sNf[sm * JW + lane] = 0;
 #pragma unroll 1
         for (int c0 = 0; c0 < N; c0 += 32) {
           const int n = c0 + lane;
           const bool dead = n < rows && p.parents && par[node0 + over_g(p, n)] == MIS_TREE_UNUSED;
           const uint32_t dw = __ballot_sync(0xffffffffu, dead);
-          if (lane == 0) sDead[sm * 4 + (c0 >> 5)] = dw;
+          if (lane == 0) sDead[sm * NW + (c0 >> 5)] = dw;
         }
         if (tree) {
           // who sees new key j: a bit a column
@@ -479,7 +480,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
               uint32_t top = __vmaxu2(__vmaxu2(u[e].x & 0x7f807f80u, u[e].y & 0x7f807f80u),
                                       __vmaxu2(u[e].z & 0x7f807f80u, u[e].w & 0x7f807f80u));
               if ((top & 0x7f80u) == 0x7f80u || (top >> 16) == 0x7f80u)
-                atomicOr(&sNf[sm * 8], 1u << min(e * RPI + lane / LPR, w.R.n - 1));
+                atomicOr(&sNf[sm * JW], 1u << min(e * RPI + lane / LPR, w.R.n - 1));
             }
           }
         }
@@ -501,8 +502,8 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
     const float sa = fabsf(p.scale_log2), sign = p.scale_log2 < 0.f ? -1.f : 1.f;
     const uint64_t sax2 = f2_pack(__float_as_uint(sa), __float_as_uint(sa));
     // this thread's row of P: chunk c of its columns
-    const uint32_t aP = smem_u32(sP) + (c0 >> 6) * C::kBox + r * 128;
-    const int cP = (c0 & 63) / 8;
+    const uint32_t aP = smem_u32(sP) + r * 128;
+    const int cP = c0 / 8;
     float* ref = sRef + sw * N + c0;                     // negated references, if not one for all
     float* al = sAl + sw * N + c0;
     Unit w;
@@ -704,9 +705,9 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
           // leaves its non-finite elements to the epilogue
           const bool look = N > 16 && node && w.R.n > C::kFew;
           if (ok && !plain && wg == 0 && r < kv16 &&
-              (!seen || look || (node && ((sNf[slot * 8 + (j >> 5)] >> (j & 31)) & 1u)))) {
+              (!seen || look || (node && ((sNf[slot * JW + (j >> 5)] >> (j & 31)) & 1u)))) {
             ok = spin(bar(bVF + t % VS), (t / VS) & 1, W, 0x750);
-            if (ok) clean_row<NB>(smem_u32(sV + (t % VS) * C::kTile) + r * 128, r, seen, look, sNf + slot * 8, j);
+            if (ok) clean_row<NB>(smem_u32(sV + (t % VS) * C::kTile) + r * 128, r, seen, look, sNf + slot * JW, j);
           }
           ok = __all_sync(0xffffffffu, ok);
         } else if (ok && t > 0) {
@@ -764,7 +765,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         sum[x] = 0.f;
         if (n < N) {
           const float* l = sL + slot * 4 * N + n;
-          const bool dead = (sDead[slot * 4 + x] >> lane) & 1u;
+          const bool dead = (sDead[slot * NW + x] >> lane) & 1u;
           if (!dead) {
             mx[x] = -sM[slot * N + n];                   // as the references: before the scale
             sum[x] = (l[0] + l[N]) + (l[2 * N] + l[3 * N]);
@@ -801,7 +802,7 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
       // non-finite values of the new rows, by key
       uint32_t nf = 0;
       if (w.k1 > w.R.kt)
-        for (int x = 0; x < 8; ++x) nf |= sNf[slot * 8 + x];
+        for (int x = 0; x < JW; ++x) nf |= sNf[slot * JW + x];
 #pragma unroll 1
       for (int q = 0; q < NE; q += CH) {
         uint32_t ov[CH];
@@ -813,8 +814,9 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         }
         if (e0 + q >= rows) continue;
         if (nf) {
-          for (int x = 0; x < 8; ++x)
-            for (uint32_t bits = sNf[slot * 8 + x]; bits; bits &= bits - 1) {
+#pragma unroll 1
+          for (int x = 0; x < JW; ++x)
+            for (uint32_t bits = sNf[slot * JW + x]; bits; bits &= bits - 1) {
               const int j = x * 32 + __ffs(bits) - 1;
               const float val = __bfloat162float(p.v[(int64_t)(w.R.r0 + j) * p.vs + w.h * D + d]);
               if (isfinite(val)) continue;
