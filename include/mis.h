@@ -499,8 +499,8 @@ mis_status_t mis_paged_extend(int32_t B, int32_t T, int32_t page_size, int32_t n
  *                   store, e.g. the accepted nodes of a drafted tree; repeats ok
  *   position_ids  — device int32 [n] or NULL for no rotation. Rotate-half
  *                   form of mis_rope_qk: the pair (x[i], x[i + D/2]) turns by
- *                   p * rope_base^(-2i/D); the angle is kept as a 64-bit
- *                   fraction of a turn, so far positions lose nothing
+ *                   p * rope_base^(-2i/D), kept as a 64-bit fraction of a
+ *                   turn: off by p * 2^-54 of a turn before the sine's own 2^-21
  *   rope_base     — > 1, read only with position_ids
  * A slot past the cache or a source row outside [0, T) stores nothing and
  * sets MIS_ERR_DEVICE_INDEX. One kernel; n = 0 enqueues nothing and leaves

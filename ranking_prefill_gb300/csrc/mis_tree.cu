@@ -38,9 +38,9 @@
 // is far from zero is taken off first, exactly where the score equals it.
 //
 // What bounds it: the stream of K and V. 64 decoded tokens over 512 to 4096 rows
-// (16 / 8 heads, D = 128, 562 MB): 94 us, 5.9 TB/s of 6.7 measured for a copy; 4
-// requests of 64K to 128K rows with 1 to 8 nodes x 4 heads (1.9 GB): 278 to 285
-// us, 6.7 TB/s. Short ones are bound by the way there: launch and schedule 2 us,
+// (16 / 8 heads, D = 128, 562 MB): 94 to 96 us, 5.9 TB/s of 6.7 measured for a
+// copy; 4 requests of 64K to 128K rows with 1 to 8 nodes x 4 heads (1.9 GB): 278
+// to 286 us, 6.7 TB/s. Short ones are bound by the way there: launch and schedule 2 us,
 // the first copies 3.5, the second kernel 2; 8 trees of 8 to 32 nodes over 512 to
 // 4096 rows (79 MB): 26 us. K and V are marked to leave L2 first, which keeps
 // the pieces, the tables and the code in it: 1 us of those 26 and 94.
@@ -93,9 +93,12 @@ struct TreeCfg {
   static constexpr int kNodes = 64;              // N >= max_nodes * G
   static constexpr int kFew = D == 128 && N > 16 ? 8 : 16;     // new rows that the masks' warp reads itself
   // What a unit costs besides its steps (its first step, masks, epilogue), in
-  // steps: blocks are given equal shares of both. 8 trees of 8 to 32 nodes took
-  // 24.7, 25.8 and 26.3 us with 1, 2 and 3 at N = 64, over other lengths 24.4,
-  // 22.7 and 23.0; at N = 16 a unit costs 0.3 us, a third of a step
+  // steps: blocks are given equal shares of both. N = 64, with 1, 2 and 3: 8 trees
+  // of 17 to 32 nodes 24.7, 23.6, 24.9 us, 32 of them over 100 to 600 rows 34.6,
+  // 33.0, 32.7. N = 16 and 32, with 0, 1 and 2: 4 decoded tokens 10.5, 11.0, 10.9;
+  // 5 small trees 11.0, 11.4, 11.3; 64 decoded tokens 103.6, 102.8, 101.9. So none
+  // for the small batches; 256 tokens over 100 to 600 rows (130, 118, 115) and 32
+  // trees of 9 to 16 nodes over as many (33.5, 26.9, 25.4) would rather have 2
   static constexpr int kUnitCost = N == 64 ? 2 : 0;
   static constexpr int kTmem = N == 16 ? 64 : 4 * N;    // S_0 | S_1 | O_0 | O_1
   // floats / words behind the tiles
@@ -595,17 +598,25 @@ mis_tree_attn_kernel(const __grid_constant__ CUtensorMap qmap,
         if (!first) {
           if (ok && active && one) {
             float x0 = -INFINITY, x1 = -INFINITY;
+            auto fold8 = [&](int c) {
 #pragma unroll
-            for (int c = 0; c < NC; c += 8) {
-              if (c + 8 <= live) {
+              for (int n = c; n < c + 8; n += 4) {
+                x0 = max3(x0, __uint_as_float(s[n]), __uint_as_float(s[n + 1]));
+                x1 = max3(x1, __uint_as_float(s[n + 2]), __uint_as_float(s[n + 3]));
+              }
+            };
+            if (live >= NC) {
 #pragma unroll
-                for (int n = c; n < c + 8; n += 4) {
-                  x0 = max3(x0, __uint_as_float(s[n]), __uint_as_float(s[n + 1]));
-                  x1 = max3(x1, __uint_as_float(s[n + 2]), __uint_as_float(s[n + 3]));
+              for (int c = 0; c < NC; c += 8) fold8(c);
+            } else {
+#pragma unroll
+              for (int c = 0; c < NC; c += 8) {
+                if (c + 8 <= live) {
+                  fold8(c);
+                } else if (c < live) {
+#pragma unroll
+                  for (int n = c; n < c + 8; ++n) x0 = fmaxf(x0, n < live ? __uint_as_float(s[n]) : -INFINITY);
                 }
-              } else if (c < live) {
-#pragma unroll
-                for (int n = c; n < c + 8; ++n) x0 = fmaxf(x0, n < live ? __uint_as_float(s[n]) : -INFINITY);
               }
             }
             over |= fmaf(fmaxf(x0, x1), sa, base) > kGrow;
@@ -1013,9 +1024,10 @@ mis_status_t check_desc(const mis_tree_desc* d, const mis_paged_cache* c) {
 
 // Rows of a unit: the smallest tile that holds all rows of a request's kv
 // head, and from 65 rows on the two tiles of 128 of mis_tree_wide.cu. 16
-// requests of 2000 to 8000 cached rows (8 kv heads, D = 128): 64 rows 61 us in a
-// tile of 64, 65 us there; 128 rows 70 us in a tile of 128 columns here, 69 us
-// there, and 26 and 21 us over 100 to 600 cached rows.
+// requests of 2000 to 8000 cached rows (8 kv heads, D = 128): 32 nodes x 2 heads
+// 63 us in a tile of 64, 68 us there, 64 x 1 65 and 68, at D = 64 56 and 55; over
+// 100 to 600 rows 32 and 21, but lengths are not known here. 128 rows 70 us in a
+// tile of 128 columns, 69 us there, and 26 and 21 us over 100 to 600 rows.
 int unit_rows(const mis_tree_desc* d, const mis_paged_cache* c) {
   const int64_t rows = (int64_t)d->max_nodes * (d->Hq / c->Hkv);
   return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 256;

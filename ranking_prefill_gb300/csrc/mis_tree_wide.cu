@@ -8,16 +8,17 @@
 // mis_tree.cu; a unit is a pair of row tiles, or one tile where the request has
 // no more rows.
 //
-// What bounds it, at D = 128: a tile's round of a step is 1060 cycles of PV and
-// the next S, 320 until its scores are seen, 1130 of softmax (exponentials,
-// rounding and sums fill the issue slots of a tile's four warps) and 450 until
-// the products of its P go out: 2960, in which the other tile's 1060 fit. Tensor
-// memory holds no third tile. Two warps a row's half took longer (81 us, this
-// 77: the same SM partitions do the same exponentials). K and V alone, all
-// from L2, change little (2 us), so memory does not bound a step.
-// 16 requests of 2000 to 8000 cached rows, 64 nodes x 4 heads, 8 kv heads: 77 us
-// with the second kernel's 9, 4.5 TB/s and 1080 TFLOP/s (the tensor pipe is active
-// for 51% of this kernel's cycles).
+// What bounds it, at D = 128: a tile's round of a step is about 1060 cycles of PV
+// and the next S, 320 until its scores are seen, 1130 of softmax and 450 until
+// the products of its P go out: 2960, in which the other tile's 1060 fit. No pipe
+// is full: the tensor pipe is active for 52% of the cycles, issue slots for 37%,
+// exponentials for 27%, memory for 57%; a round is a chain of latencies, and
+// tensor memory holds no third tile to fill it. Two warps a row's half took longer
+// (81 us, one 77). K and V alone, all from L2, change little (2 us).
+// 16 requests of 2000 to 8000 cached rows, 64 nodes x 4 heads, 8 kv heads: 77 to
+// 78 us with the second kernel's 9, 4.5 TB/s and 1080 TFLOP/s. D = 64 is alike:
+// 64 us where K and V take 26 (tensor pipe 30%, issue 41%, exponentials 30%,
+// memory 41%).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -39,7 +40,9 @@ struct WideCfg {
   static constexpr int kBox = kKeys * 128;
   static constexpr int kTile = kNB * kBox;       // of K, V and Q alike
   static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 2 : 4;
-  // see TreeCfg; with 2, 3, 4 and 5 the pairs above took 79.4, 78.0, 77.7, 78.2 us
+  // see TreeCfg; with 2, 3, 4 and 5: the pairs above 79.4, 78.0, 77.7, 78.2 us, over
+  // other lengths 80.3, 79.4, 79.5, 79.5; 32 pairs over 100 to 600 rows 38.1, 40.1,
+  // 39.5, 40.7; 16 single tiles 70.6, 70.5, 71.8, 71.9; pairs at D = 64 39.5, 39.8, 39.3, 40.1
   static constexpr int kUnitCost = 4;
   static constexpr int kW = MIS_TREE_MAX_NODES / 32;    // words of a node's mask
   static constexpr int oMask = 0;                       // [2][256][kW] new keys that a node sees
@@ -326,7 +329,7 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
     const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
     const uint32_t tS = tl + colS(x), tO = tl + colO(x);
     // scores are taken times the scale's sign, then scaled by its size
-    const float sa = fabsf(p.scale_log2);
+    const float sa = fabsf(p.scale_log2), grow_by = kGrow / sa;
     const bool neg = p.scale_log2 < 0.f;
     const uint64_t sax2 = f2_pack(__float_as_uint(sa), __float_as_uint(sa));
     const int box_shift = min(p.page_shift, 7), boxes = kKeys >> box_shift;
@@ -427,7 +430,7 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
         for (int c = 0; c < kKeys; c += 2)
           mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
         const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-        const bool grow = (top - m) * sa > kGrow;
+        const bool grow = top > m + grow_by;
         const bool any_grow = __any_sync(0xffffffffu, grow);
         const float alpha = grow ? ex2((m - top) * sa) : 1.f;
         if (grow) { l *= alpha; m = top; }
@@ -436,10 +439,9 @@ mis_tree_wide_kernel(const __grid_constant__ CUtensorMap qmap,
         const float scaled = -m * sa;
         const bool far = fabsf(scaled) > kFar;
         const float off = far ? 0.f : scaled;
-        if (__any_sync(0xffffffffu, far && m > kEmpty)) {
-          const float b = far ? -m : 0.f;
+        if (far && m > kEmpty) {
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) + b);
+          for (int c = 0; c < kKeys; ++c) s[c] = __float_as_uint(__uint_as_float(s[c]) - m);
         }
         const uint64_t offx2 = f2_pack(__float_as_uint(off), __float_as_uint(off));
         uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
