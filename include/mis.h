@@ -575,6 +575,141 @@ mis_status_t mis_tree_attention_fwd(const mis_tree_desc* desc, const mis_paged_c
                                     void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Per-head norms of Q and K with the rotary embedding in the same pass, as the
+ * Qwen3 family has them before attention (mis_rope_qk without the norms):
+ *     y = w * x / sqrt(mean(x^2) + eps)   over the D elements of a (row, head),
+ *     the pair (y[i], y[i + D/2]) turns by p * rope_base^(-2i/D).
+ *   q, k, q_out, k_out — device bf16 [T, heads, D], row strides in elements
+ *                  (>= heads*D, multiples of 8), 16-byte aligned. Hq = 0 or
+ *                  Hkv = 0 leaves that tensor out (its pointers are not read).
+ *                  An output may be its own input at the same row stride (in
+ *                  place); another overlap of an output with an argument is
+ *                  MIS_ERR_INVALID_ARG. Columns of one buffer at one row stride
+ *                  (the parts of a projection's output) do not overlap
+ *   q_weight, k_weight — device bf16 [D], 16-byte aligned, or NULL: no norm of
+ *                  that tensor
+ *   eps          — 0 to 1, read only with a weight
+ *   position_ids — device int32 [T] (any value), or NULL for no rotation. The
+ *                  angle is kept as a 64-bit fraction of a turn: off by
+ *                  p * 2^-54 of a turn, its sine and cosine by 2^-22
+ *   rope_base    — > 1, read only with position_ids
+ * fp32 throughout, rounded once to bf16. Infinities and NaN stay in their (row,
+ * head). One kernel, no workspace; T = 0 enqueues nothing.
+ * ------------------------------------------------------------------------ */
+mis_status_t mis_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
+                              int64_t q_row_stride, int64_t k_row_stride, int64_t q_out_row_stride,
+                              int64_t k_out_row_stride, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                              const void* q_weight, const void* k_weight, float eps,
+                              const int32_t* position_ids, double rope_base, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit paged K/V cache: the paged cache above at half its bytes. Slots, pages,
+ * block tables and mis_paged_extend() are the same. A row of a kv head is held
+ * as D e4m3 codes and one exponent byte e + 127; it stands for code * 2^e:
+ *     a = max |finite x|, e = the least integer in [-56, 120] with
+ *     a <= 448 * 2^e, code = e4m3(x * 2^-e) (nearest, ties to even).
+ * Elements that are infinite or NaN are kept as NaN. Elements below 2^(e - 10)
+ * become zero, so a row whose largest element is below 2^-66 is kept as zeros.
+ * Every value is exact in bf16, but for those that elements above 248 * 2^120
+ * round to, 2^128, which bf16 holds as infinity. An exponent byte outside [71, 247] counts as
+ * the nearest one inside.
+ *   k, v         — device codes, a byte each. Row r of page p, head h starts at
+ *                  byte p*page_stride + r*row_stride + h*head_stride of either
+ *                  buffer; its D codes are contiguous
+ *   k_exp, v_exp — device exponent bytes [n_pages][Hkv][page_size], contiguous
+ *   page_size, n_pages, D — as in mis_paged_cache
+ *   strides      — in bytes, multiples of 16, K and V alike; no two rows may
+ *                  overlap (a stride whose extent is 1 is not used)
+ * All pointers 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_exp;
+  uint8_t* v_exp;
+  int32_t n_pages, page_size, Hkv, D;
+  int64_t page_stride, row_stride, head_stride;
+} mis_paged_cache_q8;
+
+/* mis_paged_write_kv() into an 8-bit cache, K normed on the way if asked:
+ *     cache row slot_map[i] = quantised (rope(norm(k[s_i]), position_ids[i]), v[s_i]).
+ * Arguments as there, and
+ *   k_weight — device bf16 [D], 16-byte aligned, or NULL for no norm
+ *   eps      — 0 to 1, read only with k_weight
+ * with the norm and rotation of mis_qk_norm_rope() in fp32, rounded once to the
+ * codes. No buffer of the cache and not the workspace overlaps another of them
+ * or an argument (MIS_ERR_INVALID_ARG); K and V rows may lie between each other
+ * in one buffer. A slot past the cache or a source row outside [0, T) stores
+ * nothing and sets MIS_ERR_DEVICE_INDEX. n = 0 enqueues nothing and leaves the
+ * status word. Workspace: device, 256-byte aligned, >=
+ * mis_paged_write_workspace_size(). */
+mis_status_t mis_paged_write_kv_q8(const mis_paged_cache_q8* cache, const void* k, const void* v,
+                                   int64_t k_row_stride, int64_t v_row_stride, int32_t T,
+                                   const int32_t* src_rows, const int32_t* slot_map, int32_t n,
+                                   const int32_t* position_ids, double rope_base, const void* k_weight,
+                                   float eps, void* workspace, size_t ws_bytes, void* stream);
+
+/* Rows of an 8-bit cache as bf16, e.g. a cached prefix for
+ * mis_attention_fwd_cached(): k_out[i], v_out[i] = the values at slot_map[i].
+ *   slot_map     — device int32 [n]; repeats ok; a negative slot leaves its row
+ *                  of k_out and v_out as it was
+ *   k_out, v_out — device bf16 [n, Hkv, D], row strides in elements (>= Hkv*D,
+ *                  multiples of 8), 16-byte aligned; they overlap neither the
+ *                  cache nor another argument (MIS_ERR_INVALID_ARG)
+ * A slot past the cache leaves its row too and sets MIS_ERR_DEVICE_INDEX.
+ * n = 0 and the workspace as in mis_paged_write_kv_q8(). */
+mis_status_t mis_paged_read_kv_q8(const mis_paged_cache_q8* cache, const int32_t* slot_map, int32_t n,
+                                  void* k_out, void* v_out, int64_t k_row_stride, int64_t v_row_stride,
+                                  void* workspace, size_t ws_bytes, void* stream);
+
+/* Attention of the newest rows of each request over an 8-bit cache that holds
+ * them already (mis_paged_extend, mis_paged_write_kv_q8): a decoded token, a
+ * drafted chain, a short chunk. Request b has cache_len[b] cached rows, the last
+ * n_b = cu_rows[b+1] - cu_rows[b] of them being its rows of q; row i of n_b sees
+ * the keys j < cache_len[b] - n_b + i + 1 (itself and all before it):
+ *     o_i = sum_j p_ij v_j,  p_ij = softmax_j(scale * q_i k_j).
+ *   B, T      — requests, rows of q and o (>= 0); Hq a multiple of Hkv, at most
+ *               128 query heads a kv head
+ *   max_rows  — upper bound on a request's new rows, 1 .. MIS_PAGED_MAX_ROWS
+ *   scale     — softmax scale of size 1e-20 to 1e20, of either sign; 0 selects
+ *               1/sqrt(D). scale * q_i k_j has to stay within fp32's range
+ *   q, o, lse, row strides — as in mis_attention_fwd_plan (lse fp32 [Hq, T] or
+ *               NULL). Rows from cu_rows[B] on are not written
+ *   block_table — device int32 [B, max_pages], row stride in elements;
+ *               max_pages * page_size <= 2^31 - 256
+ *   cache_len — device int32 [B], n_b .. max_pages * page_size
+ *   cu_rows   — device int32 [B+1], non-decreasing, within [0, T]
+ * What a row does not see never reaches it, whatever its value (NaN in unused
+ * cache rows or in later new rows included); NaN that it does see makes its
+ * element of o (from a value) or its row (from a key) NaN. Infinities and NaN in
+ * q make their own row undefined and no other.
+ * Found on the device, reported as MIS_ERR_DEVICE_INDEX: a request with a bad
+ * cache_len, more than max_rows rows, or a bad cu_rows range is skipped (its
+ * rows are not written); a page id outside the cache hides its rows, and a row
+ * that sees nothing then gets o = 0 and lse = -inf.
+ * o, lse and the workspace overlap no input, the cache among them, nor each
+ * other (MIS_ERR_INVALID_ARG; o may be columns of a buffer whose other columns
+ * are q, at one row stride). fp32 scores, statistics and accumulation;
+ * probabilities are rounded to 11 bits for the second product, o to bf16. The
+ * same call gives the same bits. Two kernels, which wait on nothing but their
+ * stream. Workspace: device, 256-byte aligned, >=
+ * mis_paged_attention_q8_workspace_size() (0 for an invalid descriptor); one
+ * call at a time may use it. */
+#define MIS_PAGED_MAX_ROWS 256
+typedef struct {
+  int32_t B, T, Hq, max_rows;
+  float scale;
+} mis_paged_attn_desc;
+size_t mis_paged_attention_q8_workspace_size(const mis_paged_attn_desc* desc,
+                                             const mis_paged_cache_q8* cache);
+mis_status_t mis_paged_attention_q8_fwd(const mis_paged_attn_desc* desc, const mis_paged_cache_q8* cache,
+                                        const void* q, void* o, float* lse, int64_t q_row_stride,
+                                        int64_t o_row_stride, const int32_t* block_table,
+                                        int32_t max_pages, int64_t block_table_stride,
+                                        const int32_t* cache_len, const int32_t* cu_rows,
+                                        void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Device status of the last call that used `workspace` (a plan workspace, or
  * one of scoring, of the paged cache or of tree attention). Synchronises
  * `stream`, then returns MIS_OK, MIS_ERR_DEVICE_TIMEOUT, MIS_ERR_DEVICE_INDEX

@@ -124,6 +124,11 @@ bool kernel_attr_once(const void* kernel, int smem_bytes);
 
 // Host-side checks of a paged cache's descriptor (mis_paged.cu).
 mis_status_t check_paged_cache(const mis_paged_cache* c);
+// Page sizes that the paged calls take (mis_paged.cu).
+bool page_size_ok(int32_t ps);
+// base^(-2i/D) / (2 pi) as 64-bit fractions of a turn, i < D/2, zeros up to 64
+// (mis_paged.cu).
+void fill_turns(double base, int D, uint64_t* turn);
 
 // An argument's memory: rows of `width` bytes, `stride` bytes apart.
 struct Span {
@@ -145,6 +150,11 @@ inline bool overlap(const Span& a, const Span& b) {
 }
 // The first row of K or V (base) of a paged cache and all that follow it.
 Span cache_span(const mis_paged_cache* c, const void* base);
+
+// The same of an 8-bit cache (mis_q8.cu): its checks, its codes' rows, its exponent bytes.
+mis_status_t check_paged_cache_q8(const mis_paged_cache_q8* c);
+Span codes_span(const mis_paged_cache_q8* c, const void* base);
+Span exps_span(const mis_paged_cache_q8* c, const void* base);
 
 // Process-wide wait limit for the kernels' bounded waits.
 uint64_t wait_limit_ns();

@@ -1,0 +1,166 @@
+// Per-head root mean square norms of Q and K with the rotary embedding in the
+// same pass, sm_103a (the Qwen3 family normalises each head's query and key
+// before the rotation).
+//
+//   y = w * x / sqrt(mean(x^2) + eps) over the D elements of a (row, head),
+//   the pair (y[i], y[i + D/2]) turns by p * base^(-2i/D), i < D/2.
+//
+// fp32 from the loaded bf16 values on, one rounding at the end. Every element is
+// read and written once, so HBM bounds it. D / 16 lanes share a head: a lane
+// holds 8 pairs, so the mean takes 2 or 3 exchanges and the rotation none. The
+// angles of a lane's 8 pairs serve every head that its thread takes.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "mis_internal.h"
+#include "mis_ptx.cuh"
+#include "mis_rows.cuh"
+
+namespace mis {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 256;
+
+struct NormParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  __nv_bfloat16* qo;
+  __nv_bfloat16* ko;
+  int64_t qs, ks, qos, kos;        // row strides, elements
+  const __nv_bfloat16* qw;         // or null: no norm
+  const __nv_bfloat16* kw;
+  const int32_t* pos;              // or null: no rotation
+  float eps;
+  int32_t T, Hq, Hkv, hpt;         // hpt: heads of a thread
+  uint64_t turn[64];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+mis_qk_norm_rope_kernel(const __grid_constant__ NormParams p) {
+  constexpr int HALF = D / 2, NC = D / 16;
+  griddep_wait();
+  const int H = p.Hq + p.Hkv, NG = (H + p.hpt - 1) / p.hpt;
+  const int64_t gid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int c = (int)(gid % NC);
+  const int64_t cell = gid / NC;
+  const int grp = (int)(cell % NG);
+  const int64_t t = cell / NG;
+  if (t >= p.T) return;                          // the lanes of a row leave together
+  const uint32_t lanes = row_lanes<NC>();
+  float sn[8], cs[8];
+  if (p.pos) {
+    const int pos = p.pos[t];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sincos_quarters(pos, p.turn[c * 8 + e], sn[e], cs[e]);
+  }
+  // heads [h0, h1) of one tensor
+  auto pass = [&](const __nv_bfloat16* src, __nv_bfloat16* dst, const __nv_bfloat16* w, int h0, int h1) {
+    if (h0 >= h1) return;
+    float wx[8], wy[8];
+    if (w) {
+      bf16x8_to_float(*reinterpret_cast<const uint4*>(w + c * 8), wx);
+      bf16x8_to_float(*reinterpret_cast<const uint4*>(w + HALF + c * 8), wy);
+    }
+    src += c * 8;
+    dst += c * 8;
+#pragma unroll 2
+    for (int h = h0; h < h1; ++h) {
+      float x[8], y[8];
+      const uint4 a = ld_row16(src + (int64_t)h * D), b = ld_row16(src + (int64_t)h * D + HALF);
+      bf16x8_to_float(a, x);
+      bf16x8_to_float(b, y);
+      if (w) norm_row<D>(x, y, wx, wy, p.eps, lanes);
+      if (p.pos) rotate_row(x, y, sn, cs);
+      uint32_t u[4], v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+        v[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+      }
+      *reinterpret_cast<uint4*>(dst + (int64_t)h * D) = make_uint4(u[0], u[1], u[2], u[3]);
+      *reinterpret_cast<uint4*>(dst + (int64_t)h * D + HALF) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  };
+  const int h0 = grp * p.hpt, h1 = min(h0 + p.hpt, H);
+  pass(p.q + t * p.qs, p.qo + t * p.qos, p.qw, h0, min(h1, p.Hq));
+  pass(p.k + t * p.ks, p.ko + t * p.kos, p.kw, max(h0 - p.Hq, 0), h1 - p.Hq);
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+}  // namespace mis
+
+using namespace mis;
+
+extern "C" mis_status_t mis_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
+                                         int64_t q_row_stride, int64_t k_row_stride,
+                                         int64_t q_out_row_stride, int64_t k_out_row_stride, int32_t T,
+                                         int32_t Hq, int32_t Hkv, int32_t D, const void* q_weight,
+                                         const void* k_weight, float eps, const int32_t* position_ids,
+                                         double rope_base, void* stream) {
+  if (T < 0 || Hq < 0 || Hkv < 0 || Hq + (int64_t)Hkv < 1) return MIS_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return MIS_ERR_UNSUPPORTED;
+  if ((int64_t)Hq + Hkv > 65536) return MIS_ERR_UNSUPPORTED;
+  if ((q_weight || k_weight) && !(eps >= 0.f && eps <= 1.f)) return MIS_ERR_INVALID_ARG;
+  if (position_ids && (!(rope_base > 1.0) || !std::isfinite(rope_base))) return MIS_ERR_INVALID_ARG;
+  const int64_t wq = (int64_t)Hq * D, wk = (int64_t)Hkv * D;
+  if (Hq > 0 && (q_row_stride < wq || q_out_row_stride < wq || ((q_row_stride | q_out_row_stride) & 7)))
+    return MIS_ERR_SHAPE;
+  if (Hkv > 0 && (k_row_stride < wk || k_out_row_stride < wk || ((k_row_stride | k_out_row_stride) & 7)))
+    return MIS_ERR_SHAPE;
+  if (T == 0) return MIS_OK;
+  if ((Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out))) return MIS_ERR_INVALID_ARG;
+  for (const void* x : {q, k, (const void*)q_out, (const void*)k_out, q_weight, k_weight})
+    if (!aligned(x, 16)) return MIS_ERR_INVALID_ARG;
+  if (!aligned(position_ids, 4)) return MIS_ERR_INVALID_ARG;
+  {
+    const Span in[5] = {{q, Hq ? T : 0, 2 * q_row_stride, 2 * wq}, {k, Hkv ? T : 0, 2 * k_row_stride, 2 * wk},
+                        {q_weight, 1, 0, 2 * (int64_t)D}, {k_weight, 1, 0, 2 * (int64_t)D},
+                        {position_ids, 1, 0, 4 * (int64_t)T}};
+    const Span out[2] = {{q_out, Hq ? T : 0, 2 * q_out_row_stride, 2 * wq},
+                         {k_out, Hkv ? T : 0, 2 * k_out_row_stride, 2 * wk}};
+    // in place: the same rows, each element read and written by one thread
+    const bool same[2] = {q_out == q && q_out_row_stride == q_row_stride,
+                          k_out == k && k_out_row_stride == k_row_stride};
+    for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 5; ++j)
+        if (!(i == j && same[i]) && overlap(out[i], in[j])) return MIS_ERR_INVALID_ARG;
+    if (overlap(out[0], out[1])) return MIS_ERR_INVALID_ARG;
+  }
+  NormParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.qo = static_cast<__nv_bfloat16*>(q_out);
+  p.ko = static_cast<__nv_bfloat16*>(k_out);
+  p.qs = q_row_stride; p.ks = k_row_stride; p.qos = q_out_row_stride; p.kos = k_out_row_stride;
+  p.qw = static_cast<const __nv_bfloat16*>(q_weight);
+  p.kw = static_cast<const __nv_bfloat16*>(k_weight);
+  p.pos = position_ids;
+  p.eps = eps;
+  p.T = T; p.Hq = Hq; p.Hkv = Hkv;
+  if (position_ids) fill_turns(rope_base, D, p.turn);
+  const int H = Hq + Hkv;
+  // an angle serves all heads of a thread; a row's heads are split over
+  // threads only while its lanes alone would leave SMs idle
+  const int64_t cells = (int64_t)T * (D / 16), want = 1024 * (int64_t)num_sms();
+  const int64_t split = std::max<int64_t>(1, std::min<int64_t>(H, want / cells));
+  p.hpt = (int32_t)((H + split - 1) / split);
+  const int64_t threads = cells * ((H + p.hpt - 1) / p.hpt);
+  const int64_t blocks = (threads + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffff) return MIS_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  try {
+    const cudaError_t e =
+        D == 128 ? launch_pdl(mis_qk_norm_rope_kernel<128>, dim3((unsigned)blocks), dim3(kThreads), 0, st, p)
+                 : launch_pdl(mis_qk_norm_rope_kernel<64>, dim3((unsigned)blocks), dim3(kThreads), 0, st, p);
+    return e == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
+  } catch (...) {
+    return MIS_ERR_CUDA;
+  }
+}

@@ -370,6 +370,10 @@ mis_paged_write_kernel(const WriteParams p) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+mis_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MIS_OK : MIS_ERR_CUDA; }
+
+}  // namespace
+
 bool page_size_ok(int32_t ps) {
   return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256;
 }
@@ -393,10 +397,6 @@ void fill_turns(double base, int D, uint64_t* turn) {
   }
   for (int i = 0; i < 64; ++i) turn[i] = kept.turn[i];
 }
-
-mis_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MIS_OK : MIS_ERR_CUDA; }
-
-}  // namespace
 
 mis_status_t check_paged_cache(const mis_paged_cache* c) {
   if (!c || !c->k || !c->v) return MIS_ERR_INVALID_ARG;

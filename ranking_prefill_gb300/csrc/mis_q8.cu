@@ -1,0 +1,436 @@
+// 8-bit paged K/V cache, sm_103a: rows quantised as they are stored (K normed
+// and rotated on the way), and rows read back as bf16.
+//
+// A (row, kv head) is held as D e4m3 codes and one exponent e:
+//   a = max |finite x|,  e = least integer in [-56, 120] with a <= 448 * 2^e,
+//   code = e4m3(x * 2^-e) (nearest, ties to even), value = code * 2^e.
+// The scale is a power of two because e4m3 is a float: a finer scale would not
+// make its codes finer, while this one is a byte, x * 2^-e is exact, and the
+// value is exact in bf16 (and the code in fp16, which attention computes with).
+//
+// Both kernels touch every byte once, so HBM bounds them: D / 16 lanes share a
+// row of a head in the store (maximum and mean in 2 or 3 exchanges, as the
+// rotation's pairs lie in a lane), and D / 16 lanes read one back.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "mis_internal.h"
+#include "mis_ptx.cuh"
+#include "mis_rows.cuh"
+
+namespace mis {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 256;
+// Rows up to which one block looks over every index beside the copy. Beyond,
+// the status word is cleared by a copy engine's node and the rows' own threads
+// raise it, so that no single block bounds the call.
+constexpr int kCheckRows = 8192;
+
+struct Q8Cache {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* ke;                       // exponent bytes [page][head][row]
+  uint8_t* ve;
+  int64_t page_stride, row_stride, head_stride;
+  int64_t n_slots;
+  int32_t page_shift, Hkv;
+};
+
+__device__ __forceinline__ int64_t code_at(const Q8Cache& c, int s) {
+  return (int64_t)(s >> c.page_shift) * c.page_stride +
+         (int64_t)(s & ((1 << c.page_shift) - 1)) * c.row_stride;
+}
+__device__ __forceinline__ int64_t exp_at(const Q8Cache& c, int s, int h) {
+  return (((int64_t)(s >> c.page_shift) * c.Hkv + h) << c.page_shift) + (s & ((1 << c.page_shift) - 1));
+}
+
+// One block looks over every index and writes the status word, 16 loads in
+// flight a thread.
+__device__ __forceinline__ void check_rows(const int32_t* slot, const int32_t* src, int n, int64_t n_slots,
+                                           int T, uint32_t* status, uint32_t where) {
+  constexpr int U = 16;
+  uint32_t bad = 0;
+  for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
+    int s[U], r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      s[u] = i < n ? slot[i] : -1;
+      r[u] = src && i < n ? src[i] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s[u] >= 0 && (s[u] >= n_slots || r[u] < 0 || r[u] >= T)) bad = 1;
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) {
+    status[0] = bad ? kDevIndex : 0u;
+    status[1] = bad ? where : 0u;
+  }
+}
+
+struct StoreParams {
+  Q8Cache c;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t ks, vs;                    // source row strides, elements
+  const int32_t* src;                // or null
+  const int32_t* slot;
+  const int32_t* pos;                // or null: no rotation
+  const __nv_bfloat16* kw;           // or null: no norm
+  float eps;
+  int32_t n, T, hpt;                 // hpt: heads of a thread
+  int32_t own_check;                 // block 0 looks over the indices
+  uint32_t* status;
+  uint64_t turn[64];
+};
+
+// Quantises a lane's 8 + 8 elements of a row and stores them.
+template <int D>
+__device__ __forceinline__ void put_row(float* x, float* y, uint8_t* code, uint8_t* exp, bool first,
+                                        uint32_t lanes) {
+  float m = 0.f, sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    m = fmaxf(m, fmaxf(fabsf(x[e]), fabsf(y[e])));
+    sum += fabsf(x[e]) + fabsf(y[e]);
+  }
+  if (!(sum <= 3.0e38f)) {           // infinities or NaN, or nearly: the finite ones count, the others become NaN
+    m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (isfinite(x[e])) m = fmaxf(m, fabsf(x[e])); else x[e] = __int_as_float(0x7fffffff);
+      if (isfinite(y[e])) m = fmaxf(m, fabsf(y[e])); else y[e] = __int_as_float(0x7fffffff);
+    }
+  }
+  const int ex = q8_exp_of(row_max<D / 16>(m, lanes));
+  const float r = pow2(-ex);
+  uint2 a, b;
+  a.x = e4m3x4(x[0] * r, x[1] * r, x[2] * r, x[3] * r);
+  a.y = e4m3x4(x[4] * r, x[5] * r, x[6] * r, x[7] * r);
+  b.x = e4m3x4(y[0] * r, y[1] * r, y[2] * r, y[3] * r);
+  b.y = e4m3x4(y[4] * r, y[5] * r, y[6] * r, y[7] * r);
+  *reinterpret_cast<uint2*>(code) = a;
+  *reinterpret_cast<uint2*>(code + D / 2) = b;
+  if (first) *exp = (uint8_t)(ex + 127);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+mis_paged_write_q8_kernel(const __grid_constant__ StoreParams p) {
+  constexpr int HALF = D / 2, NC = D / 16;
+  griddep_wait();
+  if (p.own_check && blockIdx.x == 0) {
+    check_rows(p.slot, p.src, p.n, p.c.n_slots, p.T, p.status, 0x40);
+    return;
+  }
+  const int64_t gid = (int64_t)(blockIdx.x - p.own_check) * kThreads + threadIdx.x;
+  const int c = (int)(gid % NC);
+  const int64_t cell = gid / NC;
+  const int groups = (p.c.Hkv + p.hpt - 1) / p.hpt;
+  const int grp = (int)(cell % groups);
+  const int64_t i = cell / groups;
+  if (i >= p.n) return;
+  const int s = p.slot[i];
+  if (s < 0) return;
+  const int r = p.src ? p.src[i] : (int)i;
+  if (s >= p.c.n_slots || r < 0 || r >= p.T) {
+    if (!p.own_check) raise_status(p.status, kDevIndex, 0x40);
+    return;
+  }
+  const uint32_t lanes = row_lanes<NC>();
+  const int h0 = grp * p.hpt, h1 = min(h0 + p.hpt, p.c.Hkv);
+  const __nv_bfloat16* ks = p.k + (int64_t)r * p.ks + c * 8;
+  const __nv_bfloat16* vs = p.v + (int64_t)r * p.vs + c * 8;
+  const int64_t at = code_at(p.c, s) + c * 8;
+  float sn[8], cs[8], wx[8], wy[8];
+  if (p.pos) {
+    const int pos = p.pos[i];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sincos_quarters(pos, p.turn[c * 8 + e], sn[e], cs[e]);
+  }
+  if (p.kw) {
+    bf16x8_to_float(*reinterpret_cast<const uint4*>(p.kw + c * 8), wx);
+    bf16x8_to_float(*reinterpret_cast<const uint4*>(p.kw + HALF + c * 8), wy);
+  }
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    const int64_t from = (int64_t)h * D, to = at + (int64_t)h * p.c.head_stride, ex = exp_at(p.c, s, h);
+    const uint4 ka = ld_row16(ks + from), kb = ld_row16(ks + from + HALF);
+    const uint4 va = ld_row16(vs + from), vb = ld_row16(vs + from + HALF);
+    float x[8], y[8];
+    bf16x8_to_float(ka, x);
+    bf16x8_to_float(kb, y);
+    if (p.kw) norm_row<D>(x, y, wx, wy, p.eps, lanes);
+    if (p.pos) rotate_row(x, y, sn, cs);
+    put_row<D>(x, y, p.c.k + to, p.c.ke + ex, c == 0, lanes);
+    bf16x8_to_float(va, x);
+    bf16x8_to_float(vb, y);
+    put_row<D>(x, y, p.c.v + to, p.c.ve + ex, c == 0, lanes);
+  }
+}
+
+struct ReadParams {
+  Q8Cache c;
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  int64_t ks, vs;
+  const int32_t* slot;
+  int32_t n, own_check;
+  uint32_t* status;
+};
+
+// 16 codes times 2^e as bf16.
+__device__ __forceinline__ void put_values(const uint4& codes, float scale, __nv_bfloat16* dst) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t h = e4m3x2_to_half2((uint16_t)(w[i] >> (16 * j)));
+      float lo, hi;
+      asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}"
+          : "=f"(lo), "=f"(hi) : "r"(h));
+      o[2 * i + j] = pack_bf16(lo * scale, hi * scale);
+    }
+  }
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+mis_paged_read_q8_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int NC = D / 16;
+  griddep_wait();
+  if (p.own_check && blockIdx.x == 0) {
+    check_rows(p.slot, nullptr, p.n, p.c.n_slots, 0x7fffffff, p.status, 0x50);
+    return;
+  }
+  const int64_t gid = (int64_t)(blockIdx.x - p.own_check) * kThreads + threadIdx.x;
+  const int c = (int)(gid % NC);
+  const int64_t cell = gid / NC;
+  const int h = (int)(cell % p.c.Hkv);
+  const int64_t i = cell / p.c.Hkv;
+  if (i >= p.n) return;
+  const int s = p.slot[i];
+  if (s < 0) return;
+  if (s >= p.c.n_slots) {
+    if (!p.own_check) raise_status(p.status, kDevIndex, 0x50);
+    return;
+  }
+  const int64_t at = code_at(p.c, s) + (int64_t)h * p.c.head_stride + c * 16, ex = exp_at(p.c, s, h);
+  const uint4 kc = *reinterpret_cast<const uint4*>(p.c.k + at);
+  const uint4 vc = *reinterpret_cast<const uint4*>(p.c.v + at);
+  const int ke = q8_exp(p.c.ke[ex]), ve = q8_exp(p.c.ve[ex]);
+  const int64_t to = (int64_t)h * D + c * 16;
+  put_values(kc, pow2(ke), p.k + i * p.ks + to);
+  put_values(vc, pow2(ve), p.v + i * p.vs + to);
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+Q8Cache cache_of(const mis_paged_cache_q8* c) {
+  Q8Cache d;
+  d.k = static_cast<uint8_t*>(c->k);
+  d.v = static_cast<uint8_t*>(c->v);
+  d.ke = c->k_exp;
+  d.ve = c->v_exp;
+  d.page_stride = c->page_stride; d.row_stride = c->row_stride; d.head_stride = c->head_stride;
+  d.n_slots = (int64_t)c->n_pages * c->page_size;
+  d.page_shift = 31 - __builtin_clz((unsigned)c->page_size);
+  d.Hkv = c->Hkv;
+  return d;
+}
+
+}  // namespace
+
+mis_status_t check_paged_cache_q8(const mis_paged_cache_q8* c) {
+  if (!c || !c->k || !c->v || !c->k_exp || !c->v_exp) return MIS_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)c->k, (const void*)c->v, (const void*)c->k_exp, (const void*)c->v_exp})
+    if (!aligned(x, 16)) return MIS_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->Hkv < 1) return MIS_ERR_INVALID_ARG;
+  if (!page_size_ok(c->page_size) || (c->D != 64 && c->D != 128)) return MIS_ERR_UNSUPPORTED;
+  if ((int64_t)c->n_pages * c->page_size > 0x7fffffff) return MIS_ERR_SHAPE;
+  // the strides in use, smallest first, each past the extent of the ones below
+  int64_t st[3] = {c->row_stride, c->page_stride, c->head_stride};
+  int64_t ex[3] = {c->page_size, c->n_pages, c->Hkv};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (st[j] < st[i]) { std::swap(st[i], st[j]); std::swap(ex[i], ex[j]); }
+  int64_t width = c->D;
+  for (int i = 0; i < 3; ++i) {
+    if (ex[i] == 1) continue;
+    if (st[i] < width || (st[i] & 15) || st[i] >= (int64_t)1 << 38) return MIS_ERR_SHAPE;
+    width = st[i] * (ex[i] - 1) + width;
+  }
+  return MIS_OK;
+}
+
+Span codes_span(const mis_paged_cache_q8* c, const void* base) {
+  auto reach = [](int64_t extent, int64_t stride) { return extent > 1 ? (extent - 1) * stride : 0; };
+  const int64_t heads = reach(c->Hkv, c->head_stride) + c->D;             // of one row
+  const int64_t page = reach(c->page_size, c->row_stride) + heads;
+  const int64_t all = reach(c->n_pages, c->page_stride) + page;
+  // rows at one stride; else pages at one; else all as one piece
+  const bool rows = c->n_pages == 1 || c->page_stride == c->page_size * c->row_stride;
+  if (rows && heads <= c->row_stride) return {base, (int64_t)c->n_pages * c->page_size, c->row_stride, heads};
+  if (c->n_pages > 1 && page <= c->page_stride) return {base, c->n_pages, c->page_stride, page};
+  return {base, 1, all, all};
+}
+
+// Whether rows of K and rows of V (the same strides, `apart` bytes on) share
+// bytes. The strides lie past each other's extents, so of each, largest first,
+// only the two multiples around what is left can bring the rest near zero.
+static bool rows_at(const int64_t* st, const int64_t* ex, int i, int64_t apart, int64_t D) {
+  if (i < 0) return apart > -D && apart < D;
+  if (ex[i] == 1) return rows_at(st, ex, i - 1, apart, D);
+  int64_t d = apart / st[i] - (apart % st[i] < 0);
+  for (int x = 0; x < 2; ++x, ++d)
+    if (d > -ex[i] && d < ex[i] && rows_at(st, ex, i - 1, apart - d * st[i], D)) return true;
+  return false;
+}
+static bool kv_rows_meet(const mis_paged_cache_q8* c) {
+  int64_t st[3] = {c->row_stride, c->page_stride, c->head_stride};
+  int64_t ex[3] = {c->page_size, c->n_pages, c->Hkv};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (ex[i] == 1 ? false : ex[j] == 1 || st[j] < st[i]) { std::swap(st[i], st[j]); std::swap(ex[i], ex[j]); }
+  const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(c->v) - reinterpret_cast<uintptr_t>(c->k));
+  return rows_at(st, ex, 2, apart, c->D);
+}
+
+Span exps_span(const mis_paged_cache_q8* c, const void* base) {
+  return {base, 1, 0, (int64_t)c->n_pages * c->page_size * c->Hkv};
+}
+
+}  // namespace mis
+
+using namespace mis;
+
+extern "C" mis_status_t mis_paged_write_kv_q8(const mis_paged_cache_q8* cache, const void* k, const void* v,
+                                              int64_t k_row_stride, int64_t v_row_stride, int32_t T,
+                                              const int32_t* src_rows, const int32_t* slot_map, int32_t n,
+                                              const int32_t* position_ids, double rope_base,
+                                              const void* k_weight, float eps, void* workspace,
+                                              size_t ws_bytes, void* stream) {
+  const mis_status_t cs = check_paged_cache_q8(cache);
+  if (cs != MIS_OK) return cs;
+  if (T < 0 || n < 0) return MIS_ERR_INVALID_ARG;
+  if (position_ids && (!(rope_base > 1.0) || !std::isfinite(rope_base))) return MIS_ERR_INVALID_ARG;
+  if (k_weight && !(eps >= 0.f && eps <= 1.f)) return MIS_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < mis_paged_write_workspace_size())
+    return MIS_ERR_WORKSPACE;
+  if (!src_rows && n > T) return MIS_ERR_SHAPE;
+  const int64_t w = (int64_t)cache->Hkv * cache->D;
+  if (k_row_stride < w || v_row_stride < w || ((k_row_stride | v_row_stride) & 7)) return MIS_ERR_SHAPE;
+  if (n == 0) return MIS_OK;
+  if (!slot_map || !aligned(slot_map, 4) || !aligned(src_rows, 4) || !aligned(position_ids, 4))
+    return MIS_ERR_INVALID_ARG;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_weight, 16)) return MIS_ERR_INVALID_ARG;
+  {
+    const Span out[5] = {codes_span(cache, cache->k), codes_span(cache, cache->v),
+                         exps_span(cache, cache->k_exp), exps_span(cache, cache->v_exp),
+                         Span{workspace, 1, 0, (int64_t)kStatusBytes}};
+    const Span in[6] = {{k, T, 2 * k_row_stride, 2 * w}, {v, T, 2 * v_row_stride, 2 * w},
+                        {slot_map, 1, 0, 4 * (int64_t)n}, {src_rows, 1, 0, 4 * (int64_t)n},
+                        {position_ids, 1, 0, 4 * (int64_t)n}, {k_weight, 1, 0, 2 * (int64_t)cache->D}};
+    for (int i = 0; i < 5; ++i) {
+      for (const Span& x : in)
+        if (overlap(out[i], x)) return MIS_ERR_INVALID_ARG;
+      for (int j = i < 2 ? i : 0; j < i; ++j)
+        if (overlap(out[i], out[j])) return MIS_ERR_INVALID_ARG;
+    }
+    if (kv_rows_meet(cache)) return MIS_ERR_INVALID_ARG;
+  }
+  StoreParams p;
+  p.c = cache_of(cache);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.ks = k_row_stride; p.vs = v_row_stride;
+  p.src = src_rows; p.slot = slot_map; p.pos = position_ids;
+  p.kw = static_cast<const __nv_bfloat16*>(k_weight);
+  p.eps = eps;
+  p.n = n; p.T = T;
+  p.status = static_cast<uint32_t*>(workspace);
+  p.own_check = n <= kCheckRows;
+  const int D = cache->D, Hkv = cache->Hkv;
+  if (position_ids) fill_turns(rope_base, D, p.turn);
+  // an angle serves all heads of a thread; a row's heads are split over
+  // threads only while its lanes alone would leave SMs idle
+  const int64_t cells = (int64_t)n * (D / 16), want = 1024 * (int64_t)num_sms();
+  const int64_t split = std::max<int64_t>(1, std::min<int64_t>(Hkv, want / cells));
+  p.hpt = (int32_t)((Hkv + split - 1) / split);
+  const int64_t threads = cells * ((Hkv + p.hpt - 1) / p.hpt);
+  const int64_t blocks = p.own_check + (threads + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffff) return MIS_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  try {
+    if (!p.own_check && cudaMemsetAsync(workspace, 0, 8, st) != cudaSuccess) return MIS_ERR_CUDA;
+    const cudaError_t e =
+        D == 128 ? launch_pdl(mis_paged_write_q8_kernel<128>, dim3((unsigned)blocks), dim3(kThreads), 0, st, p)
+                 : launch_pdl(mis_paged_write_q8_kernel<64>, dim3((unsigned)blocks), dim3(kThreads), 0, st, p);
+    return e == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
+  } catch (...) {
+    return MIS_ERR_CUDA;
+  }
+}
+
+extern "C" mis_status_t mis_paged_read_kv_q8(const mis_paged_cache_q8* cache, const int32_t* slot_map,
+                                             int32_t n, void* k_out, void* v_out, int64_t k_row_stride,
+                                             int64_t v_row_stride, void* workspace, size_t ws_bytes,
+                                             void* stream) {
+  const mis_status_t cs = check_paged_cache_q8(cache);
+  if (cs != MIS_OK) return cs;
+  if (n < 0) return MIS_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < mis_paged_write_workspace_size())
+    return MIS_ERR_WORKSPACE;
+  const int64_t w = (int64_t)cache->Hkv * cache->D;
+  if (k_row_stride < w || v_row_stride < w || ((k_row_stride | v_row_stride) & 7)) return MIS_ERR_SHAPE;
+  if (n == 0) return MIS_OK;
+  if (!slot_map || !aligned(slot_map, 4)) return MIS_ERR_INVALID_ARG;
+  if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16)) return MIS_ERR_INVALID_ARG;
+  {
+    const Span out[3] = {{k_out, n, 2 * k_row_stride, 2 * w}, {v_out, n, 2 * v_row_stride, 2 * w},
+                         {workspace, 1, 0, (int64_t)kStatusBytes}};
+    const Span in[5] = {codes_span(cache, cache->k), codes_span(cache, cache->v),
+                        exps_span(cache, cache->k_exp), exps_span(cache, cache->v_exp),
+                        Span{slot_map, 1, 0, 4 * (int64_t)n}};
+    for (int i = 0; i < 3; ++i) {
+      for (const Span& x : in)
+        if (overlap(out[i], x)) return MIS_ERR_INVALID_ARG;
+      for (int j = 0; j < i; ++j)
+        if (overlap(out[i], out[j])) return MIS_ERR_INVALID_ARG;
+    }
+  }
+  ReadParams p;
+  p.c = cache_of(cache);
+  p.k = static_cast<__nv_bfloat16*>(k_out);
+  p.v = static_cast<__nv_bfloat16*>(v_out);
+  p.ks = k_row_stride; p.vs = v_row_stride;
+  p.slot = slot_map;
+  p.n = n;
+  p.own_check = n <= kCheckRows;
+  p.status = static_cast<uint32_t*>(workspace);
+  const int64_t threads = (int64_t)n * (cache->D / 16) * cache->Hkv;
+  const int64_t blocks = p.own_check + (threads + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffff) return MIS_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  try {
+    if (!p.own_check && cudaMemsetAsync(workspace, 0, 8, st) != cudaSuccess) return MIS_ERR_CUDA;
+    const cudaError_t e = cache->D == 128 ? launch_pdl(mis_paged_read_q8_kernel<128>, dim3((unsigned)blocks),
+                                                       dim3(kThreads), 0, st, p)
+                                          : launch_pdl(mis_paged_read_q8_kernel<64>, dim3((unsigned)blocks),
+                                                       dim3(kThreads), 0, st, p);
+    return e == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
+  } catch (...) {
+    return MIS_ERR_CUDA;
+  }
+}

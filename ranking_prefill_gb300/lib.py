@@ -39,7 +39,9 @@ EXPORTS = ["mis_status_string", "mis_abi_version", "mis_layout_size", "mis_build
            "mis_attention_fwd_cached", "mis_attention_fwd_plan_rope", "mis_rope_k_plan",
            "mis_plan_exec_tiles", "mis_paged_extend_workspace_size", "mis_paged_extend",
            "mis_paged_write_workspace_size", "mis_paged_write_kv",
-           "mis_tree_attention_workspace_size", "mis_tree_attention_fwd"]
+           "mis_tree_attention_workspace_size", "mis_tree_attention_fwd",
+           "mis_qk_norm_rope", "mis_paged_write_kv_q8", "mis_paged_read_kv_q8",
+           "mis_paged_attention_q8_workspace_size", "mis_paged_attention_q8_fwd"]
 
 
 class MisError(RuntimeError):
@@ -71,6 +73,17 @@ class mis_paged_cache(C.Structure):
 
 class mis_tree_desc(C.Structure):
     _fields_ = [("B", C.c_int32), ("T", C.c_int32), ("Hq", C.c_int32), ("max_nodes", C.c_int32),
+                ("scale", C.c_float)]
+
+
+class mis_paged_cache_q8(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_exp", C.c_void_p), ("v_exp", C.c_void_p),
+                ("n_pages", C.c_int32), ("page_size", C.c_int32), ("Hkv", C.c_int32), ("D", C.c_int32),
+                ("page_stride", C.c_int64), ("row_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class mis_paged_attn_desc(C.Structure):
+    _fields_ = [("B", C.c_int32), ("T", C.c_int32), ("Hq", C.c_int32), ("max_rows", C.c_int32),
                 ("scale", C.c_float)]
 
 
@@ -149,6 +162,17 @@ def load(path: str = LIB_PATH):
                                                    C.POINTER(mis_paged_cache)]),
         "mis_tree_attention_fwd": (C.c_int, [C.POINTER(mis_tree_desc), C.POINTER(mis_paged_cache)] +
                                    [vp] * 5 + [i64] * 4 + [vp, C.c_int32, i64] + [vp] * 4 + [sz, vp]),
+        "mis_qk_norm_rope": (C.c_int, [vp] * 4 + [i64] * 4 + [C.c_int32] * 4 + [vp, vp, C.c_float, vp,
+                                                                               C.c_double, vp]),
+        "mis_paged_write_kv_q8": (C.c_int, [C.POINTER(mis_paged_cache_q8), vp, vp, i64, i64, C.c_int32, vp,
+                                            vp, C.c_int32, vp, C.c_double, vp, C.c_float, vp, sz, vp]),
+        "mis_paged_read_kv_q8": (C.c_int, [C.POINTER(mis_paged_cache_q8), vp, C.c_int32, vp, vp, i64, i64,
+                                           vp, sz, vp]),
+        "mis_paged_attention_q8_workspace_size": (sz, [C.POINTER(mis_paged_attn_desc),
+                                                       C.POINTER(mis_paged_cache_q8)]),
+        "mis_paged_attention_q8_fwd": (C.c_int, [C.POINTER(mis_paged_attn_desc),
+                                                 C.POINTER(mis_paged_cache_q8)] + [vp] * 3 + [i64] * 2 +
+                                       [vp, C.c_int32, i64] + [vp] * 3 + [sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -790,6 +814,196 @@ def mis_tree_attention_fwd(desc: TreeDesc, q, k, v, o, lse, block_table, cache_l
                                   qs, ks, vs, os_,
                                   block_table.data_ptr(), cols, stride, cache_len.data_ptr(),
                                   cu_nodes.data_ptr(), parents, workspace.data_ptr(), workspace.numel(), st)
+    if st:
+        raise MisError(st, where)
+
+
+# -------------------------------------------- per-head norms, 8-bit paged cache
+
+PAGED_MAX_ROWS = 256
+
+
+def _weight(where: str, t, D: int, dev) -> int:
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    if t.shape != (D,) or not t.is_contiguous():
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+    return t.data_ptr()
+
+
+def mis_qk_norm_rope(q, k, q_out, k_out, position_ids=None, q_weight=None, k_weight=None,
+                     eps: float = 1.0e-6, base: float = 1.0e6, stream=None):
+    """Root mean square norms of the heads of q [T, Hq, D] and k [T, Hkv, D] (each
+    with its weight [D]; without one, no norm of that tensor), then the rotation
+    at position_ids [T] int32 (None: no rotation), in one pass. q or k (with its
+    output) may be None; an output may be its input."""
+    L = _lib or load()
+    where = "mis_qk_norm_rope"
+    dev, st = _here(stream)
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (q is None and k is None):
+        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    x = q if q is not None else k
+    if len(x.shape) != 3:
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+    T, _, D = x.shape
+    at, strides, heads = [], [], []
+    for t, o in ((q, q_out), (k, k_out)):
+        if t is None:
+            at += [None, None]
+            strides += [0, 0]
+            heads.append(0)
+            continue
+        if not (t.dtype is _BF16 and o.dtype is _BF16 and t.get_device() == dev and o.get_device() == dev):
+            raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+        if len(t.shape) != 3 or t.shape[0] != T or o.shape[0] != T:
+            raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+        H = t.shape[1]
+        strides += [_row_stride(where, T, H, D, t), _row_stride(where, T, H, D, o)]
+        at += [t.data_ptr(), o.data_ptr()]
+        heads.append(H)
+    qw = None if q_weight is None else _weight(where, q_weight, D, dev)
+    kw = None if k_weight is None else _weight(where, k_weight, D, dev)
+    pos = None
+    if position_ids is not None:
+        if position_ids.dtype is not _I32 or position_ids.get_device() != dev:
+            raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+        if position_ids.numel() < T or not position_ids.is_contiguous():
+            raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+        pos = position_ids.data_ptr()
+    st = L.mis_qk_norm_rope(at[0], at[2], at[1], at[3], strides[0], strides[2], strides[1], strides[3], T,
+                            heads[0], heads[1], D, qw, kw, eps, pos, base, st)
+    if st:
+        raise MisError(st, where)
+
+
+class PagedCacheQ8:
+    """An 8-bit paged K/V cache: k and v codes (uint8 or float8_e4m3fn) [n_pages,
+    page_size, Hkv, D] with equal strides and contiguous head rows (a [n_pages,
+    Hkv, page_size, D] buffer passes as its transpose(1, 2)), k_exp and v_exp
+    exponent bytes, uint8 [n_pages, Hkv, page_size]. Keeps the tensors alive."""
+
+    def __init__(self, k, v, k_exp, v_exp):
+        import torch
+        where = "PagedCacheQ8"
+        dev, _ = _here(0)
+        codes = (torch.uint8, torch.float8_e4m3fn)
+        _require(k.dtype in codes and k.dtype == v.dtype and k_exp.dtype == v_exp.dtype == torch.uint8 and
+                 all(t.get_device() == dev for t in (k, v, k_exp, v_exp)),
+                 MIS_ERR_INVALID_ARG, where)  # noqa: F821
+        _require(k.dim() == 4 and k.shape == v.shape and k.stride() == v.stride() and k.stride(3) == 1,
+                 MIS_ERR_SHAPE, where)  # noqa: F821
+        self.n_pages, self.page_size, self.Hkv, self.D = k.shape
+        _require(k_exp.shape == v_exp.shape == (self.n_pages, self.Hkv, self.page_size) and
+                 k_exp.is_contiguous() and v_exp.is_contiguous(), MIS_ERR_SHAPE, where)  # noqa: F821
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.desc = mis_paged_cache_q8(_dptr(k), _dptr(v), _dptr(k_exp), _dptr(v_exp), self.n_pages,
+                                       self.page_size, self.Hkv, self.D, k.stride(0), k.stride(1),
+                                       k.stride(2))
+        self.ref = C.byref(self.desc)
+        self.device = k.get_device()
+
+
+class PagedAttentionDesc:
+    """Sizes of a mis_paged_attention_q8_fwd call over `cache`."""
+
+    def __init__(self, cache: PagedCacheQ8, B: int, T: int, Hq: int, max_rows: int, scale: float = 0.0):
+        self.cache, self.B, self.T, self.Hq, self.max_rows = cache, B, T, Hq, max_rows
+        self.desc = mis_paged_attn_desc(B, T, Hq, max_rows, scale)
+        self.ref = C.byref(self.desc)
+
+    def workspace_size(self) -> int:
+        n = int(load().mis_paged_attention_q8_workspace_size(self.ref, self.cache.ref))
+        if n == 0:   # ask the call itself for the reason (no pointer is looked at before it)
+            st = load().mis_paged_attention_q8_fwd(self.ref, self.cache.ref, *([None] * 3), 0, 0, None, 0, 0,
+                                                   *([None] * 3), 0, None)
+            _check(st or lib_status_unknown(), "mis_paged_attention_q8_workspace_size")
+        return n
+
+
+def mis_paged_write_kv_q8(cache: PagedCacheQ8, k, v, slot_map, workspace, position_ids=None,
+                          base: float = 1.0e6, src_rows=None, k_weight=None, eps: float = 1.0e-6,
+                          stream=None):
+    """mis_paged_write_kv into an 8-bit cache; K normed first if k_weight [D] is given."""
+    L = _lib or load()
+    where = "mis_paged_write_kv_q8"
+    dev, st = _here(stream)
+    if not (cache.device == dev and k.dtype is _BF16 and v.dtype is _BF16 and slot_map.dtype is _I32 and
+            workspace.dtype is _U8 and k.get_device() == dev and v.get_device() == dev and
+            slot_map.get_device() == dev and workspace.get_device() == dev):
+        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    n, T, D = slot_map.numel(), k.shape[0], cache.D
+    ks = _row_stride(where, T, cache.Hkv, D, k)
+    vs = _row_stride(where, T, cache.Hkv, D, v)
+    pos = src = None
+    for t in (position_ids, src_rows):
+        if t is not None:
+            if t.dtype is not _I32 or t.get_device() != dev:
+                raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+            if t.numel() < n or not t.is_contiguous():
+                raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+            if t is position_ids:
+                pos = t.data_ptr()
+            if t is src_rows:
+                src = t.data_ptr()
+    if not (slot_map.is_contiguous() and workspace.is_contiguous()):
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+    kw = None if k_weight is None else _weight(where, k_weight, D, dev)
+    st = L.mis_paged_write_kv_q8(cache.ref, k.data_ptr(), v.data_ptr(), ks, vs, T, src, slot_map.data_ptr(),
+                                 n, pos, base, kw, eps, workspace.data_ptr(), workspace.numel(), st)
+    if st:
+        raise MisError(st, where)
+
+
+def mis_paged_read_kv_q8(cache: PagedCacheQ8, slot_map, k_out, v_out, workspace, stream=None):
+    """Rows at the slots of slot_map [n] (negative: the row stays) as bf16 rows of
+    k_out, v_out [n, Hkv, D]."""
+    L = _lib or load()
+    where = "mis_paged_read_kv_q8"
+    dev, st = _here(stream)
+    if not (cache.device == dev and k_out.dtype is _BF16 and v_out.dtype is _BF16 and
+            slot_map.dtype is _I32 and workspace.dtype is _U8 and k_out.get_device() == dev and
+            v_out.get_device() == dev and slot_map.get_device() == dev and workspace.get_device() == dev):
+        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    n = slot_map.numel()
+    ks = _row_stride(where, n, cache.Hkv, cache.D, k_out)
+    vs = _row_stride(where, n, cache.Hkv, cache.D, v_out)
+    if not (slot_map.is_contiguous() and workspace.is_contiguous()):
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+    st = L.mis_paged_read_kv_q8(cache.ref, slot_map.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(), ks,
+                                vs, workspace.data_ptr(), workspace.numel(), st)
+    if st:
+        raise MisError(st, where)
+
+
+def mis_paged_attention_q8_fwd(desc: PagedAttentionDesc, q, o, lse, block_table, cache_len, cu_rows,
+                               workspace, stream=None):
+    """Attention of q [T, Hq, D], the newest rows [cu_rows[b], cu_rows[b+1]) of each
+    request, over its cached rows of block_table [B, max_pages] up to cache_len [B]
+    (they are among these); o like q, lse fp32 [Hq, T] or None."""
+    L = _lib or load()
+    where = "mis_paged_attention_q8_fwd"
+    dev, st = _here(stream)
+    c, T, B, Hq = desc.cache, desc.T, desc.B, desc.Hq
+    if not (c.device == dev and q.dtype is _BF16 and o.dtype is _BF16 and block_table.dtype is _I32 and
+            cache_len.dtype is _I32 and cu_rows.dtype is _I32 and workspace.dtype is _U8 and
+            q.get_device() == dev and o.get_device() == dev and block_table.get_device() == dev and
+            cache_len.get_device() == dev and cu_rows.get_device() == dev and
+            workspace.get_device() == dev):
+        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    qs, os_ = _row_stride(where, T, Hq, c.D, q), _row_stride(where, T, Hq, c.D, o)
+    cols, stride = _table(where, block_table, B)
+    if not (cache_len.numel() >= B and cu_rows.numel() > B and cache_len.is_contiguous() and
+            cu_rows.is_contiguous() and workspace.is_contiguous()):
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+    if lse is not None:
+        if lse.dtype is not _F32 or lse.get_device() != dev:
+            raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+        if lse.shape != (Hq, T) or not lse.is_contiguous():
+            raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+        lse = lse.data_ptr()
+    st = L.mis_paged_attention_q8_fwd(desc.ref, c.ref, q.data_ptr(), o.data_ptr(), lse, qs, os_,
+                                      block_table.data_ptr(), cols, stride, cache_len.data_ptr(),
+                                      cu_rows.data_ptr(), workspace.data_ptr(), workspace.numel(), st)
     if st:
         raise MisError(st, where)
 
