@@ -195,8 +195,7 @@ __device__ __forceinline__ void put_values(const uint4& codes, float scale, __nv
     for (int j = 0; j < 2; ++j) {
       const uint32_t h = e4m3x2_to_half2((uint16_t)(w[i] >> (16 * j)));
       float lo, hi;
-      asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}"
-          : "=f"(lo), "=f"(hi) : "r"(h));
+      half2_to_float(h, lo, hi);
       o[2 * i + j] = pack_bf16(lo * scale, hi * scale);
     }
   }

@@ -44,10 +44,10 @@ namespace {
 
 using namespace dev;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;              // keys of a warp's step
+constexpr int kJoinWarps = 8;
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kNone = -3.0e38f;      // reference of a row that has seen nothing
 
 struct AttnParams {
   const __nv_bfloat16* q;
@@ -70,60 +70,55 @@ struct AttnParams {
   uint32_t* status;
   uint32_t* flags;                     // [blocks]
   int64_t* first;                      // [B + 1]: steps before each request
-  float2* rl;                          // [2 * blocks][unit rows]: (r, l) of a piece's rows
-  float* part;                         // [2 * blocks][unit rows][D]
+  float2* rl;                          // [2 * blocks][slot rows]: (r, l) of a piece's rows
+  float* part;                         // [2 * blocks][slot rows][D]
 };
 
-struct Request {
-  int32_t len, row0, n;                // cached rows; first new row, new rows
-  bool ok;
-};
-
-__device__ __forceinline__ Request request_of(const AttnParams& p, int b) {
-  Request r;
-  r.len = p.cache_len[b];
-  r.row0 = p.cu[b];
-  const int end = p.cu[b + 1];
-  r.ok = r.row0 >= 0 && end >= r.row0 && end <= p.T && end - r.row0 <= p.max_rows && r.len >= 0 &&
-         r.len <= (int64_t)p.max_pages << p.page_shift && end - r.row0 <= r.len;
-  r.n = r.ok ? end - r.row0 : 0;
-  if (!r.ok) r.len = 0;
-  return r;
-}
-
-// Rows of a unit: what the block's warps hold together. A unit with fewer rows
-// uses RG warps for its rows (a power of two) and splits its keys over the
-// other kWarps / RG; it counts RG per step of 32 keys.
+// A block's warps by their width (8 or 16 rows).
 template <int NT>
 struct Shape {
+  static constexpr int kWarps = 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = 3;
   static constexpr int kWarpRows = 8 * NT;
-  static constexpr int kUnitRows = kWarps * kWarpRows;
+  static constexpr int kSlotRows = kWarps * kWarpRows;     // rows that a block holds at once
 };
+
+// A request's work. The n * G rows of a kv head are cut into tiles of a warp's
+// rows; (kv head, tile) are its columns. A unit is cg columns, a warp each, over
+// all keys, so that the heads of a cached row are read together (a row's 128
+// bytes of one head alone are too short for HBM: 64 decoded tokens 97 us by
+// single heads). Where cg leaves warps free, kWarps / cg groups of them split
+// the keys. A step of 32 keys of a unit counts cg.
+struct Job {
+  int len, row0, n;                    // cached rows; first new row, new rows
+  int steps, tiles, cols, cg, units;
+  bool ok;
+  __device__ __forceinline__ int64_t unit() const { return (int64_t)steps * cg; }
+  __device__ __forceinline__ int64_t cost() const { return unit() * units; }
+};
+
 template <int NT>
-__device__ __forceinline__ int row_groups(int rows) {
-  const int tiles = (rows + Shape<NT>::kWarpRows - 1) / Shape<NT>::kWarpRows;
-  return tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
+__device__ __forceinline__ Job job_of(const AttnParams& p, int b) {
+  constexpr int W = Shape<NT>::kWarps, WR = Shape<NT>::kWarpRows;
+  Job j;
+  j.len = p.cache_len[b];
+  j.row0 = p.cu[b];
+  const int end = p.cu[b + 1];
+  j.ok = j.row0 >= 0 && end >= j.row0 && end <= p.T && end - j.row0 <= p.max_rows && j.len >= 0 &&
+         j.len <= (int64_t)p.max_pages << p.page_shift && end - j.row0 <= j.len;
+  j.n = j.ok ? end - j.row0 : 0;
+  j.steps = j.n ? (j.len + kStep - 1) / kStep : 0;
+  j.tiles = (j.n * p.G + WR - 1) / WR;
+  j.cols = j.tiles * p.Hkv;
+  j.units = (j.cols + W - 1) / W;
+  j.cg = j.units > 1 ? (j.cols + j.units - 1) / j.units : j.cols;
+  return j;
 }
 
-// Cost of a request's heads, each: its full units, then a partial one.
-struct Cost {
-  int64_t head;                        // one kv head
-  int32_t steps, full, rest;           // steps of 32 keys; full units; rows of the last one
-};
-template <int NT>
-__device__ __forceinline__ Cost cost_of(const AttnParams& p, const Request& r) {
-  Cost c;
-  const int rows = r.n * p.G;
-  c.steps = (r.len + kStep - 1) / kStep;
-  c.full = rows / Shape<NT>::kUnitRows;
-  c.rest = rows - c.full * Shape<NT>::kUnitRows;
-  c.head = (int64_t)c.steps * (c.full * kWarps + (c.rest ? row_groups<NT>(c.rest) : 0));
-  return c;
-}
-
-// Blocks that take part: none has less than a step for each of its warps.
+// Blocks that take part: none has less than 8 steps.
 __device__ __forceinline__ int blocks_for(int64_t total, int blocks) {
-  return (int)min((int64_t)blocks, max((int64_t)1, total / kWarps));
+  return (int)min((int64_t)blocks, max((int64_t)1, total / 8));
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
@@ -176,8 +171,9 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-template <int D, int NT, int STAGES>
+template <int D, int NT>
 struct Cfg {
+  static constexpr int kWarps = Shape<NT>::kWarps, STAGES = Shape<NT>::kStages;
   static constexpr int KC = D / 64;            // 64-wide chunks of a K row
   static constexpr int VB = D / 8;             // bytes of a V row that a lane takes
   static constexpr int MT = D / 16;            // 16-wide tiles of O^T
@@ -188,72 +184,52 @@ struct Cfg {
   static_assert(Shape<NT>::kWarpRows * D * 4 <= kStage, "a warp's rows fit a step");
 };
 
-// Walks the steps of 32 keys that one warp takes in its block's share.
+// Walks the pieces of units that a block's share holds.
 template <int NT>
 struct Walk {
-  int64_t pos, end;                    // of the block's share, in costs
-  int b, h, u;                         // request, kv head, unit of the head
-  Request r;
-  Cost c;
-  int64_t head0;                       // where the current head starts
-  // the current piece
-  int rows, groups, k0, k1;            // rows of the unit; its key steps [k0, k1)
-  int64_t unit0, unit1;
+  int64_t left;                        // of the share from this piece on, in costs
+  int64_t off;                         // of the unit before this piece
+  int b, u;                            // request, its unit
+  int k0, k1;                          // key steps of the piece
+  Job j;
 
-  __device__ __forceinline__ void enter(const AttnParams& p, int b_, int64_t request0) {
+  __device__ __forceinline__ void enter(const AttnParams& p, int b_, int64_t from) {
     b = b_;
-    r = request_of(p, b);
-    c = cost_of<NT>(p, r);
-    if (pos < end) {
-      while (c.head == 0) {            // requests without rows
-        r = request_of(p, ++b);
-        c = cost_of<NT>(p, r);
-      }
-      h = (int)((pos - request0) / c.head);
-      head0 = request0 + (int64_t)h * c.head;
-      u = (int)min((int64_t)c.full, (pos - head0) / ((int64_t)c.steps * kWarps));
-      piece();
-    }
+    j = job_of<NT>(p, b);
+    u = (int)(from / j.unit());
+    off = from - u * j.unit();
+    piece();
   }
-  // sets the piece that starts at pos
   __device__ __forceinline__ void piece() {
-    rows = u < c.full ? Shape<NT>::kUnitRows : c.rest;
-    groups = row_groups<NT>(rows);
-    unit0 = head0 + (int64_t)u * c.steps * kWarps;
-    unit1 = unit0 + (int64_t)c.steps * groups;
-    k0 = (int)(pos - unit0) / groups;
-    k1 = end >= unit1 ? c.steps : (int)(end - unit0) / groups;
+    k0 = (int)(off / j.cg);
+    k1 = ends() ? j.steps : (int)((off + left) / j.cg);
   }
+  // whether the piece reaches the unit's end
+  __device__ __forceinline__ bool ends() const { return off + left >= j.unit(); }
   // the next piece; false at the end of the share
   __device__ __forceinline__ bool next(const AttnParams& p) {
-    pos = unit1;
-    if (pos >= end) return false;
-    ++u;
-    if (u > c.full || (u == c.full && !c.rest)) {
+    left -= j.unit() - off;
+    if (left <= 0) return false;
+    off = 0;
+    if (++u == j.units) {
       u = 0;
-      ++h;
-      head0 = pos;
-      if (h == p.Hkv) {
-        h = 0;
-        do {
-          r = request_of(p, ++b);
-          c = cost_of<NT>(p, r);
-        } while (c.head == 0);
-      }
+      do j = job_of<NT>(p, ++b);
+      while (j.cost() == 0);
     }
     piece();
     return true;
   }
 };
 
-template <int D, int NT, int STAGES>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int NT>
+__global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
 mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
-  using C = Cfg<D, NT, STAGES>;
-  constexpr int WR = Shape<NT>::kWarpRows, UR = Shape<NT>::kUnitRows;
+  using C = Cfg<D, NT>;
+  constexpr int kWarps = Shape<NT>::kWarps, kThreads = Shape<NT>::kThreads, STAGES = Shape<NT>::kStages;
+  constexpr int WR = Shape<NT>::kWarpRows, SR = Shape<NT>::kSlotRows;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_sum[kWarps];
-  __shared__ int64_t s_req0;
+  __shared__ int64_t s_from;
   __shared__ int s_req;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -267,9 +243,9 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
   int64_t mine = 0;
   bool bad = false;
   for (int b = rb0; b < rb1; ++b) {
-    const Request r = request_of(p, b);
-    bad |= !r.ok;
-    mine += cost_of<NT>(p, r).head * p.Hkv;
+    const Job j = job_of<NT>(p, b);
+    bad |= !j.ok;
+    mine += j.cost();
   }
   int64_t upto = mine;
 #pragma unroll
@@ -288,39 +264,42 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
   }
   const int blocks = blocks_for(total, p.blocks);
   Walk<NT> f;                          // of the copies, ahead of the products
-  f.pos = total * min((int)blockIdx.x, blocks) / blocks;
-  f.end = total * min((int)blockIdx.x + 1, blocks) / blocks;
+  const int64_t share0 = total * min((int)blockIdx.x, blocks) / blocks;
+  f.left = total * min((int)blockIdx.x + 1, blocks) / blocks - share0;
   {
     int64_t at = upto - mine;
-    const bool here = f.pos >= at && f.pos < upto;
+    const bool here = share0 >= at && share0 < upto;
     if (here || blockIdx.x == 0)
       for (int b = rb0; b < rb1; ++b) {
-        const int64_t next = at + cost_of<NT>(p, request_of(p, b)).head * p.Hkv;
-        if (here && f.pos >= at && f.pos < next) { s_req = b; s_req0 = at; }
+        const int64_t next = at + job_of<NT>(p, b).cost();
+        if (here && share0 >= at && share0 < next) { s_req = b; s_from = share0 - at; }
         if (blockIdx.x == 0) p.first[b] = at;
         at = next;
       }
     if (blockIdx.x == 0 && tid == 0) p.first[p.B] = total;
   }
   __syncthreads();
-  if (f.pos >= f.end) {
+  if (f.left <= 0) {
     if (tid == 0) p.flags[blockIdx.x] = bad ? kDevIndex : 0u;
     return;
   }
-  const int64_t share0 = f.pos;
-  f.enter(p, s_req, s_req0);
+  f.enter(p, s_req, s_from);
   Walk<NT> w = f;                      // of the products
+  const int64_t share_left = f.left;
 
   const uint32_t ring = smem_u32(smem) + warp * (STAGES * C::kStage);
   float2* s_rl = reinterpret_cast<float2*>(smem + C::kRing);      // [warp][row]
 
   // ---- copies: the step at hand, whose page ids were asked for a step ago
   bool f_on = true;                    // a step is at hand
-  int f_step = 0, f_h = 0, f_len = 0, id0 = 0, id1 = 0;
+  int f_step = 0, f_h = 0, f_kgs = 1, f_head = 0, f_len = 0, id0 = 0, id1 = 0;
   uint32_t hidden = 0;                 // two bits a stage: strips without rows or page
   bool bad_page = false;
-  auto first_step = [&] {              // none where the unit has no rows for the warp
-    return warp % f.groups * WR < f.rows ? f.k0 + warp / f.groups : f.k1;
+  auto first_step = [&] {              // none where the unit has no column for the warp
+    const int kg = warp / f.j.cg, col = f.u * f.j.cg + warp - kg * f.j.cg;
+    f_h = col / f.j.tiles;
+    f_kgs = kWarps / f.j.cg;
+    return kg < f_kgs && col < f.j.cols ? f.k0 + kg : f.k1;
   };
   auto find = [&](int step) {          // from this step on: the next one that the warp takes, and its ids
     for (;;) {
@@ -332,9 +311,9 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
     const int32_t* row = p.table + (int64_t)f.b * p.table_stride;
     const int key = step * kStep;
     id0 = row[key >> p.page_shift];
-    id1 = key + 16 < f.r.len ? row[(key + 16) >> p.page_shift] : id0;
-    f_len = f.r.len;
-    f_h = f.h;
+    id1 = key + 16 < f.j.len ? row[(key + 16) >> p.page_shift] : id0;
+    f_len = f.j.len;
+    f_head = f_h;
   };
   auto copy = [&](int stage) {
     uint32_t hide = 0;
@@ -348,7 +327,7 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
         if (key + 16 * s >= f_len) { hide |= 1u << s; continue; }
         if (off) { hide |= 1u << s; bad_page = true; continue; }
         const int in = (key + 16 * s) & ((1 << p.page_shift) - 1);
-        const int64_t from = (int64_t)id * p.page_stride + (int64_t)in * p.row_stride + (int64_t)f_h * p.head_stride;
+        const int64_t from = (int64_t)id * p.page_stride + (int64_t)in * p.row_stride + (int64_t)f_head * p.head_stride;
         const uint32_t dst = at + s * (16 * D) + lane * 16;
 #pragma unroll
         for (int c = 0; c < C::KC; ++c) {
@@ -364,11 +343,11 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
           else cp8(vdst + e * (32 * C::VB), src);
         }
         if (lane < 2) {
-          const int64_t ex = (((int64_t)id * p.Hkv + f_h) << p.page_shift) + in;
+          const int64_t ex = (((int64_t)id * p.Hkv + f_head) << p.page_shift) + in;
           cp16(at + C::kKBytes + C::kVBytes + 32 * s + 16 * lane, (lane ? p.ve : p.ke) + ex);
         }
       }
-      find(f_step + kWarps / f.groups);
+      find(f_step + f_kgs);
     }
     hidden = (hidden & ~(3u << (2 * stage))) | hide << (2 * stage);
     cp_commit();
@@ -380,10 +359,11 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
 
   // ---- products, piece by piece
   for (;;) {
-    const int groups = w.groups, tile = warp % groups;
-    const int row_first = w.u * UR + tile * WR;           // of the kv head's n * G rows
-    const int rows = min(WR, w.rows - tile * WR);         // may be <= 0: the warp has none
-    const int len = w.r.len, n = w.r.n;
+    const int cg = w.j.cg, kgs = kWarps / cg, kg = warp / cg, col = w.u * cg + warp - kg * cg;
+    const int head = col / w.j.tiles;                     // kv head
+    const int row_first = (col - head * w.j.tiles) * WR;  // of its n * G rows
+    const int rows = kg < kgs && col < w.j.cols ? min(WR, w.j.n * p.G - row_first) : 0;
+    const int len = w.j.len, n = w.j.n;
     // Q of the warp's rows as half floats, each row in units of its own power
     // of two (its largest element in [2^14, 2^15), so nothing that counts is lost)
     uint32_t qf[NT][4 * C::KC][2];
@@ -397,7 +377,7 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
       float m = 0.f;
       if (live) {
         const int at = row_first + row, i = at / p.G;
-        const __nv_bfloat16* src = p.q + (int64_t)(w.r.row0 + i) * p.qs + (int64_t)(w.h * p.G + at - i * p.G) * D + 16 * t;
+        const __nv_bfloat16* src = p.q + (int64_t)(w.j.row0 + i) * p.qs + (int64_t)(head * p.G + at - i * p.G) * D + 16 * t;
 #pragma unroll
         for (int c = 0; c < C::KC; ++c) {
           x[2 * c] = *reinterpret_cast<const uint4*>(src + 64 * c);
@@ -441,7 +421,7 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
     float o[NT][C::MT][4], r[NT][2], l[NT][2];
 #pragma unroll
     for (int a = 0; a < NT; ++a) {
-      r[a][0] = r[a][1] = -INFINITY;
+      r[a][0] = r[a][1] = kNone;
       l[a][0] = l[a][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < C::MT; ++j)
@@ -449,7 +429,7 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
         for (int e = 0; e < 4; ++e) o[a][j][e] = 0.f;
     }
 
-    for (int step = rows > 0 ? w.k0 + warp / groups : w.k1; step < w.k1; step += kWarps / groups) {
+    for (int step = rows > 0 ? w.k0 + kg : w.k1; step < w.k1; step += kgs) {
       __syncwarp();                    // every lane is done with the step before
       copy(stage_in);
       stage_in = stage_in + 1 == STAGES ? 0 : stage_in + 1;
@@ -513,9 +493,13 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int a = 0; a < NT; ++a)
+        for (int x = 0; x < 2; ++x) {
+          const float most = 37.f - (float)ev[k][x];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) over |= s[k][a][e] - r[a][e & 1] + (float)ev[k][e >> 1] > 37.f;
+          for (int a = 0; a < NT; ++a)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) over |= s[k][a][2 * x + e] - r[a][e] > most;
+        }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int a = 0; a < NT; ++a)
@@ -547,8 +531,7 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float ref = r[a][e & 1] == -INFINITY ? 0.f : r[a][e & 1];
-            const float y = ex2(s[k][a][e] - ref);
+            const float y = ex2(s[k][a][e] - r[a][e & 1]);
             l[a][e & 1] += y;
             x[e] = y * vs[k][e >> 1];
           }
@@ -648,6 +631,7 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
           x += __shfl_xor_sync(0xffffffffu, x, 8);
           x += __shfl_xor_sync(0xffffffffu, x, 16);
           const int row = 8 * a + 2 * t + e;
+          if (row >= rows) continue;
           if (g == 0) s_rl[warp * WR + row] = make_float2(r[a][e], x);
           float4* d4 = reinterpret_cast<float4*>(dst + row * D + g * (2 * C::MT));
 #pragma unroll
@@ -657,40 +641,42 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
       if (lane == 0) s_sum[warp] = stage_in;
     }
     __syncthreads();
-    const bool whole = w.pos == w.unit0 && w.end >= w.unit1;
-    const int slot = 2 * blockIdx.x + (share0 < w.unit0 ? 1 : 0);
-    const int parts = kWarps / groups;
-    for (int x = tid; x < w.rows * (D / 4); x += kThreads) {
-      const int row = x / (D / 4), c4 = x % (D / 4), tl = row / WR, in = row % WR;
-      float m = -INFINITY;
-      for (int y = 0; y < parts; ++y) m = fmaxf(m, s_rl[(y * groups + tl) * WR + in].x);
-      const float ref = m == -INFINITY ? 0.f : m;
+    const bool first = w.left == share_left, whole = w.off == 0 && w.ends();
+    const int slot = 2 * blockIdx.x + (first ? 0 : 1);
+    const int height = min(WR, n * p.G);                  // of a column
+    for (int x = tid; x < cg * height * (D / 4); x += kThreads) {
+      const int c4 = x % (D / 4), y = x / (D / 4), wc = y / height, in = y - wc * height;
+      const int ocol = w.u * cg + wc, ohead = ocol / w.j.tiles, row = (ocol - ohead * w.j.tiles) * WR + in;
+      if (ocol >= w.j.cols || row >= n * p.G) continue;
+      float m = kNone;
+      for (int z = 0; z < kgs; ++z) m = fmaxf(m, s_rl[(z * cg + wc) * WR + in].x);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f;
-      for (int y = 0; y < parts; ++y) {
-        const int from = y * groups + tl;
+      for (int z = 0; z < kgs; ++z) {
+        const int from = z * cg + wc;
         const float2 rl = s_rl[from * WR + in];
-        const float f1 = ex2(rl.x - ref);
-        const float4 z = *reinterpret_cast<const float4*>(smem + from * (STAGES * C::kStage) +
-                                                          (int)s_sum[from] * C::kStage + (in * D + 4 * c4) * 4);
+        const float f1 = ex2(rl.x - m);
+        const float4 v4 = *reinterpret_cast<const float4*>(smem + from * (STAGES * C::kStage) +
+                                                           (int)s_sum[from] * C::kStage + (in * D + 4 * c4) * 4);
         sum += f1 * rl.y;
-        acc.x += f1 * z.x;
-        acc.y += f1 * z.y;
-        acc.z += f1 * z.z;
-        acc.w += f1 * z.w;
+        acc.x += f1 * v4.x;
+        acc.y += f1 * v4.y;
+        acc.z += f1 * v4.z;
+        acc.w += f1 * v4.w;
       }
       if (whole) {
-        const int at = w.u * UR + row, i = at / p.G, head = w.h * p.G + at - i * p.G;
+        const int i = row / p.G, qh = ohead * p.G + row - i * p.G;
         // the products' weights carry 2^-22
         const float inv = sum != 0.f ? 4194304.f / sum : 0.f;
-        *reinterpret_cast<uint2*>(p.o + (int64_t)(w.r.row0 + i) * p.os + (int64_t)head * D + 4 * c4) =
+        *reinterpret_cast<uint2*>(p.o + (int64_t)(w.j.row0 + i) * p.os + (int64_t)qh * D + 4 * c4) =
             sum != 0.f ? make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv))
                        : make_uint2(0u, 0u);
         if (p.lse && c4 == 0)
-          p.lse[(int64_t)head * p.T + w.r.row0 + i] = sum != 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+          p.lse[(int64_t)qh * p.T + w.j.row0 + i] = sum != 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
       } else {
-        *reinterpret_cast<float4*>(p.part + ((int64_t)slot * UR + row) * D + 4 * c4) = acc;
-        if (c4 == 0) p.rl[(int64_t)slot * UR + row] = make_float2(m, sum);
+        const int64_t at = (int64_t)slot * SR + wc * WR + in;
+        *reinterpret_cast<float4*>(p.part + at * D + 4 * c4) = acc;
+        if (c4 == 0) p.rl[at] = make_float2(m, sum);
       }
     }
     __syncthreads();
@@ -701,12 +687,15 @@ mis_q8_attn_kernel(const __grid_constant__ AttnParams p) {
   if (tid == 0) p.flags[blockIdx.x] = bad || bad_page ? kDevIndex : 0u;
 }
 
-// Joins the pieces of units that several blocks hold: a warp a row, in block
-// order. Grid: (request, kv head) by groups of kWarps rows.
+// Joins the pieces of units that several blocks hold, in block order. Grid:
+// (request, kv head) by groups of rows; `share` warps (a power of two) take a
+// row's pieces in turn, so that a single long request's many pieces do not
+// queue behind one warp (8192 rows of 8 heads: 63 us by one).
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads)
-mis_q8_join_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int UR = Shape<NT>::kUnitRows, E = D / 32;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
+  constexpr int SR = Shape<NT>::kSlotRows, WR = Shape<NT>::kWarpRows, E = D / 32;
+  __shared__ float s_acc[kJoinWarps][D + 1];
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
@@ -719,61 +708,73 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p) {
     }
   }
   const int b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv;
-  const int row = blockIdx.y * kWarps + warp;
-  const Request r = request_of(p, b);
-  if (row >= r.n * p.G) return;
-  const Cost c = cost_of<NT>(p, r);
+  const int sub = warp & (share - 1), row = blockIdx.y * (kJoinWarps / share) + warp / share;
+  const Job j = job_of<NT>(p, b);
+  if ((int)blockIdx.y * (kJoinWarps / share) >= j.n * p.G) return;
   const int64_t total = p.first[p.B];
   const int blocks = blocks_for(total, p.blocks);
-  const int u = row / UR;
-  const int64_t u0 = p.first[b] + h * c.head + (int64_t)u * c.steps * kWarps;
-  const int64_t u1 = u0 + (int64_t)c.steps * (u < c.full ? kWarps : row_groups<NT>(c.rest));
-  // the blocks that hold the unit's first and last step
+  // the blocks that hold the first and last step of the row's unit
   auto holder = [&](int64_t x) {
     int y = (int)(x * blocks / total);
     while (total * (y + 1) / blocks <= x) ++y;
     while (total * y / blocks > x) --y;
     return y;
   };
-  const int c0 = holder(u0), c1 = holder(u1 - 1);
-  if (c0 == c1) return;
-  const int in = row - u * UR;
-  auto piece = [&](int y) {
-    return (int64_t)(2 * y + (total * y / blocks < u0 ? 1 : 0)) * UR + in;
-  };
-  float m = -INFINITY;
-  for (int y = c0 + lane; y <= c1; y += 32) m = fmaxf(m, p.rl[piece(y)].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = m == -INFINITY ? 0.f : m;
-  float acc[E], sum = 0.f;
+  const bool live = row < j.n * p.G;
+  const int col = h * j.tiles + (live ? row : 0) / WR, u = col / j.cg;
+  const int64_t u0 = p.first[b] + u * j.unit();
+  const int c0 = holder(u0), c1 = holder(u0 + j.unit() - 1);
+  const bool split = live && c0 != c1;
+  const int64_t in = (col - u * j.cg) * WR + row % WR;
+  // the first block's piece is its last one where its share starts before the unit
+  const int64_t at0 = (2 * c0 + (total * c0 / blocks < u0 ? 1 : 0)) * (int64_t)SR + in;
+  auto piece = [&](int y) { return y == c0 ? at0 : (int64_t)(2 * y) * SR + in; };
+  float m = kNone, sum = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  if (split) {
+    for (int y = c0 + lane; y <= c1; y += 32) m = fmaxf(m, p.rl[piece(y)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll 4
-  for (int y = c0; y <= c1; ++y) {
-    const int64_t at = piece(y);
-    const float2 rl = p.rl[at];
-    const float f1 = ex2(rl.x - ref);
-    sum += f1 * rl.y;
-    const float* z = p.part + at * D + lane * E;
-    if constexpr (E == 4) {
-      const float4 z4 = *reinterpret_cast<const float4*>(z);
-      acc[0] += f1 * z4.x; acc[1] += f1 * z4.y; acc[2] += f1 * z4.z; acc[3] += f1 * z4.w;
-    } else {
-      const float2 z2 = *reinterpret_cast<const float2*>(z);
-      acc[0] += f1 * z2.x; acc[1] += f1 * z2.y;
+    for (int y = c0 + sub; y <= c1; y += share) {
+      const int64_t at = piece(y);
+      const float2 rl = p.rl[at];
+      const float f1 = ex2(rl.x - m);
+      sum += f1 * rl.y;
+      const float* z = p.part + at * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 z4 = *reinterpret_cast<const float4*>(z);
+        acc[0] += f1 * z4.x; acc[1] += f1 * z4.y; acc[2] += f1 * z4.z; acc[3] += f1 * z4.w;
+      } else {
+        const float2 z2 = *reinterpret_cast<const float2*>(z);
+        acc[0] += f1 * z2.x; acc[1] += f1 * z2.y;
+      }
     }
   }
+  if (share > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_acc[warp][e * 32 + lane] = acc[e];
+    if (lane == 0) s_acc[warp][D] = sum;
+    __syncthreads();
+    if (sub) return;
+    for (int y = 1; y < share; ++y) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += s_acc[warp + y][e * 32 + lane];
+      sum += s_acc[warp + y][D];
+    }
+  }
+  if (!split) return;
   const int i = row / p.G, head = h * p.G + row - i * p.G;
   const float inv = sum != 0.f ? 4194304.f / sum : 0.f;
   uint32_t out[E / 2];
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) out[e] = sum != 0.f ? pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv) : 0u;
-  __nv_bfloat16* dst = p.o + (int64_t)(r.row0 + i) * p.os + (int64_t)head * D + lane * E;
+  __nv_bfloat16* dst = p.o + (int64_t)(j.row0 + i) * p.os + (int64_t)head * D + lane * E;
   if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
   else *reinterpret_cast<uint32_t*>(dst) = out[0];
   if (p.lse && lane == 0)
-    p.lse[(int64_t)head * p.T + r.row0 + i] = sum != 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+    p.lse[(int64_t)head * p.T + j.row0 + i] = sum != 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -788,7 +789,8 @@ mis_status_t check_desc(const mis_paged_attn_desc* d, const mis_paged_cache_q8* 
   if (d->max_rows > MIS_PAGED_MAX_ROWS) return MIS_ERR_UNSUPPORTED;
   if (d->Hq % c->Hkv) return MIS_ERR_SHAPE;
   if (d->Hq / c->Hkv > 128) return MIS_ERR_UNSUPPORTED;
-  if ((int64_t)d->B * c->Hkv > 0x7fffffff) return MIS_ERR_UNSUPPORTED;
+  // columns, and the join's grid, are counted in 32 bits
+  if ((int64_t)d->B * c->Hkv > 0x7fffffff || (int64_t)d->max_rows * d->Hq > 0x7fffffff) return MIS_ERR_UNSUPPORTED;
   return MIS_OK;
 }
 
@@ -797,28 +799,29 @@ int head_rows(const mis_paged_attn_desc* d, const mis_paged_cache_q8* c) { retur
 struct AttnWs { size_t flags, first, rl, part, total; };
 
 AttnWs workspace_of(const mis_paged_attn_desc* d, const mis_paged_cache_q8* c) {
-  const size_t G = (size_t)num_sms(), UR = kWarps * (head_rows(d, c) <= 8 ? 8 : 16);
+  const size_t G = (size_t)num_sms(), SR = head_rows(d, c) <= 8 ? Shape<1>::kSlotRows : Shape<2>::kSlotRows;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   AttnWs w;
   w.flags = kStatusBytes;
   w.first = w.flags + up(G * 4);
   w.rl = w.first + up(((size_t)d->B + 1) * 8);
-  w.part = w.rl + up(2 * G * UR * sizeof(float2));
-  w.total = w.part + 2 * G * UR * (size_t)c->D * sizeof(float);
+  w.part = w.rl + up(2 * G * SR * sizeof(float2));
+  w.total = w.part + 2 * G * SR * (size_t)c->D * sizeof(float);
   return w;
 }
 
 template <int D, int NT>
 mis_status_t launch(const AttnParams& p, cudaStream_t st) {
-  constexpr int STAGES = 3;
-  using C = Cfg<D, NT, STAGES>;
-  auto kern = mis_q8_attn_kernel<D, NT, STAGES>;
+  using C = Cfg<D, NT>;
+  auto kern = mis_q8_attn_kernel<D, NT>;
   if (!kernel_attr_once(reinterpret_cast<const void*>(kern), C::kSmem)) return MIS_ERR_CUDA;
-  if (launch_pdl(kern, dim3((unsigned)p.blocks), dim3(kThreads), C::kSmem, st, p) != cudaSuccess)
+  if (launch_pdl(kern, dim3((unsigned)p.blocks), dim3(Shape<NT>::kThreads), C::kSmem, st, p) != cudaSuccess)
     return MIS_ERR_CUDA;
-  const unsigned rows = (unsigned)((p.max_rows * p.G + kWarps - 1) / kWarps);
-  return launch_pdl(mis_q8_join_kernel<D, NT>, dim3((unsigned)(p.B * p.Hkv), rows), dim3(kThreads), 0, st, p) ==
-                 cudaSuccess
+  // warps of a row: all of a block's while the rows are few
+  const int64_t rows = (int64_t)p.max_rows * p.G, most = 4 * (int64_t)num_sms() / (p.B * (int64_t)p.Hkv * rows) + 1;
+  const int share = most >= 8 ? 8 : most >= 4 ? 4 : most >= 2 ? 2 : 1, per = kJoinWarps / share;
+  return launch_pdl(mis_q8_join_kernel<D, NT>, dim3((unsigned)(p.B * p.Hkv), (unsigned)((rows + per - 1) / per)),
+                    dim3(32 * kJoinWarps), 0, st, p, share) == cudaSuccess
              ? MIS_OK
              : MIS_ERR_CUDA;
 }

@@ -122,5 +122,9 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint16_t codes) {
   return h;
 }
 
+__device__ __forceinline__ void half2_to_float(uint32_t h, float& lo, float& hi) {
+  asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(lo), "=f"(hi) : "r"(h));
+}
+
 }  // namespace dev
 }  // namespace mis
