@@ -78,9 +78,10 @@ int g_tmap_n = 0, g_tmap_next = 0;
 
 }  // namespace
 
-// bf16 tiled tensor map with 128-byte swizzle; dims/box innermost first.
-CUtensorMap encode_tmap_bf16(const void* base, int rank, const uint64_t* dims,
-                             const uint64_t* strides_bytes, const uint32_t* box, bool* ok) {
+// Tiled tensor map; dims/box innermost first.
+static CUtensorMap encode_tmap(CUtensorMapDataType type, CUtensorMapSwizzle swizzle,
+                               CUtensorMapL2promotion promotion, const void* base, int rank, const uint64_t* dims,
+                               const uint64_t* strides_bytes, const uint32_t* box, bool* ok) {
   CUtensorMap m;
   std::memset(&m, 0, sizeof(m));
   auto fn = encode_fn();
@@ -91,9 +92,8 @@ CUtensorMap encode_tmap_bf16(const void* base, int rank, const uint64_t* dims,
   for (int i = 0; i < rank; ++i) { gd[i] = dims[i]; bx[i] = box[i]; es[i] = 1; }
   for (int i = 0; i + 1 < rank; ++i) gs[i] = strides_bytes[i];
   auto encode = [&] {
-    return fn(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), gd, gs,
-              bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return fn(&m, type, (cuuint32_t)rank, const_cast<void*>(base), gd, gs, bx, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   CUresult r = encode();
   if (r != CUDA_SUCCESS) {
@@ -106,7 +106,22 @@ CUtensorMap encode_tmap_bf16(const void* base, int rank, const uint64_t* dims,
   return m;
 }
 
-// The same, kept from call to call.
+// bf16 tiled tensor map with 128-byte swizzle.
+CUtensorMap encode_tmap_bf16(const void* base, int rank, const uint64_t* dims,
+                             const uint64_t* strides_bytes, const uint32_t* box, bool* ok) {
+  return encode_tmap(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, base,
+                     rank, dims, strides_bytes, box, ok);
+}
+
+// Of bytes: the swizzle is as wide as the box, 128 or 64 bytes. L2 fetches no more
+// than that: what lies behind a head's row is another head's.
+CUtensorMap encode_tmap_u8(const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                           const uint32_t* box, bool* ok) {
+  return encode_tmap(CU_TENSOR_MAP_DATA_TYPE_UINT8, box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     box[0] == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B, base, rank, dims, strides_bytes, box, ok);
+}
+
+// The same as encode_tmap_bf16, kept from call to call.
 CUtensorMap make_tmap_bf16(const void* base, int rank, const uint64_t* dims,
                            const uint64_t* strides_bytes, const uint32_t* box, bool* ok) {
   TmapKey key;

@@ -113,8 +113,9 @@ class Batch:
         """Every row against the oracle. A score is a sum of D products in fp32 (D
         roundings of at most the sum of their sizes, and the tensor core may cut
         instead of round: twice that), scaled by three more; the exponential is
-        good to 2^-21. P is rounded to 11 bits (2^-11 of its size, and of the
-        largest weighted value 2^-34 where it falls below fp16's range), o to bf16."""
+        good to 2^-21. P is rounded to 11 bits (2^-11 of its size); held in steps
+        of 2^-17 where its largest is 2^6 at least, it is off by at most 2^-24 of
+        the largest weight for every key that weighs little. o is rounded to bf16."""
         o, lse, q = f64(self.o), f64(self.lse), f64(self.q)
         scale = self.scale or 1.0 / math.sqrt(self.D)
         for b, (l, n) in enumerate(zip(self.lens, self.ns)):
@@ -125,7 +126,7 @@ class Batch:
             k, v = self.gathered(b)
             ro, rl, av, big = Q.attention(q[r0:r0 + n], k, v, n, scale)
             ds = big * ((2 * self.D + 8) * 2.0 ** -24) + 2.0 ** -20      # of a score, natural logarithm
-            tol = 2.0 ** -8 * np.abs(ro) + av * (2.0 ** -11 + 2 * ds[..., None]) + l * 2.0 ** -34 * np.nan_to_num(
+            tol = 2.0 ** -8 * np.abs(ro) + av * (2.0 ** -11 + 2 * ds[..., None]) + l * 2.0 ** -24 * np.nan_to_num(
                 np.abs(v)).max(initial=0.0) + 1e-30
             got = o[r0:r0 + n]
             assert (np.isnan(got) == np.isnan(ro)).all(), (b, np.isnan(got).sum(), np.isnan(ro).sum())
