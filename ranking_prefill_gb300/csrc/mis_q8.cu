@@ -25,11 +25,11 @@ namespace {
 
 using namespace dev;
 
-constexpr int kThreads = 256;
-// Rows up to which one block looks over every index beside the copy. Beyond,
-// the status word is cleared by a copy engine's node and the rows' own threads
-// raise it, so that no single block bounds the call.
-constexpr int kCheckRows = 8192;
+constexpr int kThreads = 256, kStoreThreads = 128;
+// One block looks over every index beside the copy where that takes no longer
+// than the copy. Else the status word is cleared by a node of its own and the
+// rows' own threads raise it.
+constexpr int kCheckRows = 8192, kCheckCells = 512;
 
 struct Q8Cache {
   uint8_t* k;
@@ -55,11 +55,12 @@ __device__ __forceinline__ void check_rows(const int32_t* slot, const int32_t* s
                                            int T, uint32_t* status, uint32_t where) {
   constexpr int U = 16;
   uint32_t bad = 0;
-  for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
+  const int step = (int)blockDim.x;
+  for (int i0 = threadIdx.x; i0 < n; i0 += U * step) {
     int s[U], r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads;
+      const int i = i0 + u * step;
       s[u] = i < n ? slot[i] : -1;
       r[u] = src && i < n ? src[i] : 0;
     }
@@ -90,17 +91,13 @@ struct StoreParams {
   uint64_t turn[64];
 };
 
-// Quantises a lane's 8 + 8 elements of a row and stores them.
-template <int D>
-__device__ __forceinline__ void put_row(float* x, float* y, uint8_t* code, uint8_t* exp, bool first,
-                                        uint32_t lanes) {
-  float m = 0.f, sum = 0.f;
+// Largest finite size of a lane's 8 + 8 elements; what is not finite becomes NaN
+// (a maximum passes over NaN, so only infinities need a look at each).
+__device__ __forceinline__ float lane_max(float* x, float* y) {
+  float m = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    m = fmaxf(m, fmaxf(fabsf(x[e]), fabsf(y[e])));
-    sum += fabsf(x[e]) + fabsf(y[e]);
-  }
-  if (!(sum <= 3.0e38f)) {           // infinities or NaN, or nearly: the finite ones count, the others become NaN
+  for (int e = 0; e < 8; ++e) m = max3(m, fabsf(x[e]), fabsf(y[e]));
+  if (m == INFINITY) {
     m = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -108,7 +105,14 @@ __device__ __forceinline__ void put_row(float* x, float* y, uint8_t* code, uint8
       if (isfinite(y[e])) m = fmaxf(m, fabsf(y[e])); else y[e] = __int_as_float(0x7fffffff);
     }
   }
-  const int ex = q8_exp_of(row_max<D / 16>(m, lanes));
+  return m;
+}
+
+// Quantises a lane's 8 + 8 elements of a row with largest element m and stores them.
+template <int D>
+__device__ __forceinline__ void put_row(const float* x, const float* y, float m, uint8_t* code, uint8_t* exp,
+                                        bool first) {
+  const int ex = q8_exp_of(m);
   const float r = pow2(-ex);
   uint2 a, b;
   a.x = e4m3x4(x[0] * r, x[1] * r, x[2] * r, x[3] * r);
@@ -120,8 +124,9 @@ __device__ __forceinline__ void put_row(float* x, float* y, uint8_t* code, uint8
   if (first) *exp = (uint8_t)(ex + 127);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads)
+// U heads of a row at a time: nothing of one waits for another
+template <int D, int U>
+__global__ void __launch_bounds__(kStoreThreads, 4)
 mis_paged_write_q8_kernel(const __grid_constant__ StoreParams p) {
   constexpr int HALF = D / 2, NC = D / 16;
   griddep_wait();
@@ -129,7 +134,7 @@ mis_paged_write_q8_kernel(const __grid_constant__ StoreParams p) {
     check_rows(p.slot, p.src, p.n, p.c.n_slots, p.T, p.status, 0x40);
     return;
   }
-  const int64_t gid = (int64_t)(blockIdx.x - p.own_check) * kThreads + threadIdx.x;
+  const int64_t gid = (int64_t)(blockIdx.x - p.own_check) * kStoreThreads + threadIdx.x;
   const int c = (int)(gid % NC);
   const int64_t cell = gid / NC;
   const int groups = (p.c.Hkv + p.hpt - 1) / p.hpt;
@@ -148,6 +153,18 @@ mis_paged_write_q8_kernel(const __grid_constant__ StoreParams p) {
   const __nv_bfloat16* ks = p.k + (int64_t)r * p.ks + c * 8;
   const __nv_bfloat16* vs = p.v + (int64_t)r * p.vs + c * 8;
   const int64_t at = code_at(p.c, s) + c * 8;
+  uint4 ka[U], kb[U], va[U], vb[U];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int64_t from = (int64_t)min(h + j, h1 - 1) * D;
+      ka[j] = ld_row16(ks + from);
+      kb[j] = ld_row16(ks + from + HALF);
+      va[j] = ld_row16(vs + from);
+      vb[j] = ld_row16(vs + from + HALF);
+    }
+  };
+  if (U == 1) load(h0);                          // in flight while the angles are taken
   float sn[8], cs[8], wx[8], wy[8];
   if (p.pos) {
     const int pos = p.pos[i];
@@ -159,19 +176,36 @@ mis_paged_write_q8_kernel(const __grid_constant__ StoreParams p) {
     bf16x8_to_float(*reinterpret_cast<const uint4*>(p.kw + HALF + c * 8), wy);
   }
 #pragma unroll 1
-  for (int h = h0; h < h1; ++h) {
-    const int64_t from = (int64_t)h * D, to = at + (int64_t)h * p.c.head_stride, ex = exp_at(p.c, s, h);
-    const uint4 ka = ld_row16(ks + from), kb = ld_row16(ks + from + HALF);
-    const uint4 va = ld_row16(vs + from), vb = ld_row16(vs + from + HALF);
-    float x[8], y[8];
-    bf16x8_to_float(ka, x);
-    bf16x8_to_float(kb, y);
-    if (p.kw) norm_row<D>(x, y, wx, wy, p.eps, lanes);
-    if (p.pos) rotate_row(x, y, sn, cs);
-    put_row<D>(x, y, p.c.k + to, p.c.ke + ex, c == 0, lanes);
-    bf16x8_to_float(va, x);
-    bf16x8_to_float(vb, y);
-    put_row<D>(x, y, p.c.v + to, p.c.ve + ex, c == 0, lanes);
+  for (int hh = h0; hh < h1; hh += U) {
+    if (U != 1 || hh != h0) load(hh);
+    float x[U][8], y[U][8], m[2 * U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      bf16x8_to_float(ka[i], x[i]);
+      bf16x8_to_float(kb[i], y[i]);
+    }
+    if (p.kw) norm_rows<D, U>(x, y, wx, wy, p.eps, lanes);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (p.pos) rotate_row(x[i], y[i], sn, cs);
+      m[i] = lane_max(x[i], y[i]);
+    }
+    float vx[U][8], vy[U][8];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      bf16x8_to_float(va[i], vx[i]);
+      bf16x8_to_float(vb[i], vy[i]);
+      m[U + i] = lane_max(vx[i], vy[i]);
+    }
+    row_maxima<NC, 2 * U>(m, lanes);
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = hh + i;
+      if (h >= h1) break;
+      const int64_t to = at + (int64_t)h * p.c.head_stride, ex = exp_at(p.c, s, h);
+      put_row<D>(x[i], y[i], m[i], p.c.k + to, p.c.ke + ex, c == 0);
+      put_row<D>(vx[i], vy[i], m[U + i], p.c.v + to, p.c.ve + ex, c == 0);
+    }
   }
 }
 
@@ -359,23 +393,23 @@ extern "C" mis_status_t mis_paged_write_kv_q8(const mis_paged_cache_q8* cache, c
   p.eps = eps;
   p.n = n; p.T = T;
   p.status = static_cast<uint32_t*>(workspace);
-  p.own_check = n <= kCheckRows;
+  p.own_check = n <= kCheckRows || cache->Hkv * cache->D >= kCheckCells;
   const int D = cache->D, Hkv = cache->Hkv;
   if (position_ids) fill_turns(rope_base, D, p.turn);
   // an angle serves all heads of a thread; a row's heads are split over
   // threads only while its lanes alone would leave SMs idle
-  const int64_t cells = (int64_t)n * (D / 16), want = 1024 * (int64_t)num_sms();
+  const int64_t cells = (int64_t)n * (D / 16), want = 512 * (int64_t)num_sms();
   const int64_t split = std::max<int64_t>(1, std::min<int64_t>(Hkv, want / cells));
   p.hpt = (int32_t)((Hkv + split - 1) / split);
   const int64_t threads = cells * ((Hkv + p.hpt - 1) / p.hpt);
-  const int64_t blocks = p.own_check + (threads + kThreads - 1) / kThreads;
+  const int64_t blocks = p.own_check + (threads + kStoreThreads - 1) / kStoreThreads;
   if (blocks > 0x7fffffff) return MIS_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   try {
     if (!p.own_check && cudaMemsetAsync(workspace, 0, 8, st) != cudaSuccess) return MIS_ERR_CUDA;
-    const cudaError_t e =
-        D == 128 ? launch_pdl(mis_paged_write_q8_kernel<128>, dim3((unsigned)blocks), dim3(kThreads), 0, st, p)
-                 : launch_pdl(mis_paged_write_q8_kernel<64>, dim3((unsigned)blocks), dim3(kThreads), 0, st, p);
+    auto kern = D == 128 ? (p.hpt > 1 ? mis_paged_write_q8_kernel<128, 2> : mis_paged_write_q8_kernel<128, 1>)
+                         : (p.hpt > 1 ? mis_paged_write_q8_kernel<64, 2> : mis_paged_write_q8_kernel<64, 1>);
+    const cudaError_t e = launch_pdl(kern, dim3((unsigned)blocks), dim3(kStoreThreads), 0, st, p);
     return e == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
   } catch (...) {
     return MIS_ERR_CUDA;
@@ -416,7 +450,7 @@ extern "C" mis_status_t mis_paged_read_kv_q8(const mis_paged_cache_q8* cache, co
   p.ks = k_row_stride; p.vs = v_row_stride;
   p.slot = slot_map;
   p.n = n;
-  p.own_check = n <= kCheckRows;
+  p.own_check = n <= kCheckRows || cache->Hkv * cache->D >= kCheckCells;
   p.status = static_cast<uint32_t*>(workspace);
   const int64_t threads = (int64_t)n * (cache->D / 16) * cache->Hkv;
   const int64_t blocks = p.own_check + (threads + kThreads - 1) / kThreads;

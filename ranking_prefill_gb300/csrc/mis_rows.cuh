@@ -50,37 +50,54 @@ __device__ __forceinline__ void sincos_quarters(int32_t p, uint64_t f, float& sn
   cs = (quarter + 1) & 2 ? -v : v;
 }
 
-// Sum or maximum over the N lanes (a power of two, aligned) that share a row.
+// The N lanes (a power of two, aligned) that share a row, and sums and maxima over
+// them
 template <int N>
 __device__ __forceinline__ uint32_t row_lanes() {
   return N == 32 ? 0xffffffffu : ((1u << N) - 1u) << ((threadIdx.x & 31) & ~(N - 1));
 }
-template <int N>
-__device__ __forceinline__ float row_sum(float x, uint32_t lanes) {
+// of U values, their exchanges side by side
+template <int N, int U>
+__device__ __forceinline__ void row_sums(float* x, uint32_t lanes) {
 #pragma unroll
-  for (int o = N / 2; o; o >>= 1) x += __shfl_xor_sync(lanes, x, o);
-  return x;
+  for (int o = N / 2; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < U; ++i) x[i] += __shfl_xor_sync(lanes, x[i], o);
+}
+template <int N, int U>
+__device__ __forceinline__ void row_maxima(float* x, uint32_t lanes) {
+#pragma unroll
+  for (int o = N / 2; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < U; ++i) x[i] = fmaxf(x[i], __shfl_xor_sync(lanes, x[i], o));
 }
 template <int N>
 __device__ __forceinline__ float row_max(float x, uint32_t lanes) {
-#pragma unroll
-  for (int o = N / 2; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(lanes, x, o));
+  row_maxima<N, 1>(&x, lanes);
   return x;
 }
 
-// A lane's 8 + 8 elements of a row (x: of its first half, y: of its second)
-// times w / sqrt(mean(x^2) + eps).
-template <int D>
-__device__ __forceinline__ void norm_row(float* x, float* y, const float* wx, const float* wy, float eps,
-                                         uint32_t lanes) {
-  float s = 0.f;
+// A lane's 8 + 8 elements of U rows (x: of their first halves, y: of their
+// second) times w / sqrt(mean(x^2) + eps).
+template <int D, int U>
+__device__ __forceinline__ void norm_rows(float (*x)[8], float (*y)[8], const float* wx, const float* wy, float eps,
+                                          uint32_t lanes) {
+  float s[U];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s = fmaf(x[e], x[e], fmaf(y[e], y[e], s));
-  const float r = __frsqrt_rn(fmaf(row_sum<D / 16>(s, lanes), 1.f / D, eps));
+  for (int i = 0; i < U; ++i) {
+    s[i] = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = x[e] * r * wx[e];
-    y[e] = y[e] * r * wy[e];
+    for (int e = 0; e < 8; ++e) s[i] = fmaf(x[i][e], x[i][e], fmaf(y[i][e], y[i][e], s[i]));
+  }
+  row_sums<D / 16, U>(s, lanes);
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const float r = __frsqrt_rn(fmaf(s[i], 1.f / D, eps));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[i][e] = x[i][e] * r * wx[e];
+      y[i][e] = y[i][e] * r * wy[e];
+    }
   }
 }
 
