@@ -58,6 +58,7 @@ using namespace dev;
 
 constexpr int kKeys = 128;             // of a step
 constexpr int kJoinWarps = 4;
+constexpr int kAhead = 4;              // steps whose scores may be out: as many places of S
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNone = -3.0e38f;      // reference of a row that has seen nothing
 constexpr float kDead = 3.0e38f;       // ... of a column that is no row: its weights are zero
@@ -75,7 +76,7 @@ struct AttnParams {
   int64_t table_stride;
   const int32_t* cache_len;
   const int32_t* cu;
-  int32_t n_pages, page_shift, max_pages;
+  int32_t n_pages, page_shift, most;       // most: rows that a table row can name
   int32_t B, T, Hkv, G, max_rows, blocks;
   float scale_log2;
   uint64_t wait_ns;
@@ -88,13 +89,22 @@ struct AttnParams {
   float* part;                         // [2 * blocks][N][D]
 };
 
+// What steps and units count in a block's share, so that shares take alike: a
+// step in two streams kStep, one of more rows than that kWide; a unit what its
+// beginning and end take besides, where blocks have some steps each (in small
+// batches the longest share is what counts, and that is one step).
+constexpr int kStep = 4, kWide = 5, kUnit = 12;
+
 // A request's work: units of N of a kv head's n * G rows, the tiles of a head
-// side by side. A step of 128 keys of a unit counts one.
+// side by side.
 struct Job {
   int len, row0, n;                    // cached rows; first new row, new rows
-  int steps, tiles, units;
+  int steps, tiles, units;             // 128-key steps of a unit
+  int step;                            // what one counts
   bool ok;
-  __device__ __forceinline__ int64_t cost() const { return (int64_t)steps * units; }
+  // what it counts, and a unit of it; the host bounds the sum
+  __device__ __forceinline__ int unit(int own) const { return steps * step + own; }
+  __device__ __forceinline__ int cost(int own) const { return unit(own) * units; }
 };
 
 // What a request brings, as read.
@@ -108,54 +118,77 @@ __device__ __forceinline__ Job job_of(const AttnParams& p, const Given& g) {
   j.len = g.len;
   j.row0 = g.row0;
   j.ok = j.row0 >= 0 && g.end >= j.row0 && g.end <= p.T && g.end - j.row0 <= p.max_rows && j.len >= 0 &&
-         j.len <= (int64_t)p.max_pages << p.page_shift && g.end - j.row0 <= j.len;
+         j.len <= p.most && g.end - j.row0 <= j.len;
   j.n = j.ok ? g.end - j.row0 : 0;
-  j.steps = j.n ? (j.len + kKeys - 1) / kKeys : 0;
+  j.steps = (j.len + kKeys - 1) / kKeys;
   j.tiles = (j.n * p.G + N - 1) / N;
   j.units = j.tiles * p.Hkv;
+  j.step = N == 16 || j.n * p.G <= 16 ? kStep : kWide;
   return j;
 }
 template <int N>
 __device__ __forceinline__ Job job_of(const AttnParams& p, int b) { return job_of<N>(p, given(p, b)); }
 
-// Blocks that take part.
-__device__ __forceinline__ int blocks_for(int64_t total, int blocks) {
-  return (int)min((int64_t)blocks, max((int64_t)1, total));
-}
+// A block's share: [from, from + size) of all units laid end to end; blocks
+// [0, rem) take quo + 1, the others quo. So few take part that a share holds a
+// unit's own cost and a step (`least`).
+struct Share {
+  int quo, rem, from, size;
+  __device__ __forceinline__ Share(int total, int blocks, int b, int least) {
+    blocks = min(blocks, max(1, total / least));
+    quo = total / blocks;
+    rem = total - quo * blocks;
+    from = b * quo + min(b, rem);
+    size = b < blocks ? quo + (b < rem ? 1 : 0) : 0;
+  }
+  __device__ __forceinline__ int holder(int at) const {
+    const int cut = rem * (quo + 1);
+    return at < cut ? at / (quo + 1) : rem + (at - cut) / quo;
+  }
+};
 
-// Walks the pieces of units that a block's share holds.
+// Walks the pieces of units that a block's share holds. A step is in the share
+// that holds the last of what it counts.
 template <int N>
 struct Walk {
-  int64_t left;                        // steps of the share from this piece on
+  int left, off, own;                  // of the share from this piece on; of the unit before it; a unit's own
   int b, u;                            // request, its unit
   int k0, k1;                          // steps of the piece
   Job j;
   Given g;                             // of the request behind, asked for ahead of its turn
 
-  __device__ __forceinline__ void enter(const AttnParams& p, int b_, int64_t from, int64_t share) {
+  // the first piece; false where the share has none
+  __device__ __forceinline__ bool enter(const AttnParams& p, int b_, int from, int share, int own_) {
     b = b_;
     left = share;
+    own = own_;
     j = job_of<N>(p, b);
     g = given(p, b + 1);
-    u = (int)(from / j.steps);
-    k0 = (int)(from - (int64_t)u * j.steps);
-    k1 = (int)min((int64_t)j.steps, k0 + left);
+    u = from / j.unit(own);
+    off = from - u * j.unit(own);
+    k0 = off / j.step;
+    if (k0 >= j.steps) return next(p);
+    k1 = min(j.steps, (off + left) / j.step);
+    return k1 > k0;
   }
   // the next piece; false at the end of the share
   __device__ __forceinline__ bool next(const AttnParams& p) {
-    left -= k1 - k0;
-    if (left <= 0) return false;
+    left -= j.unit(own) - off;
+    if (left < kStep) return false;
+    off = 0;
     if (++u == j.units) {
       u = 0;
       do {
         j = job_of<N>(p, g);
         g = given(p, ++b + 1);
-      } while (j.cost() == 0);
+      } while (j.units == 0);
     }
     k0 = 0;
-    k1 = (int)min((int64_t)j.steps, left);
-    return true;
+    k1 = min(j.steps, left / j.step);
+    return k1 > 0;
   }
+  // the end of the unit's steps, counted from the piece on
+  __device__ __forceinline__ int ahead() const { return j.steps * j.step - off; }
   __device__ __forceinline__ int head() const { return j.tiles == 1 ? u : u / j.tiles; }
   __device__ __forceinline__ int row0(int h) const { return (u - h * j.tiles) * N; }   // of the kv head's rows
   // keys that every row of the unit sees
@@ -169,15 +202,18 @@ struct Bound {
   volatile uint32_t* gave_up;
   uint64_t limit_ns;
 };
-__device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, const Bound& w, uint32_t where) {
-  if (mbar_try_wait(bar, parity)) return true;
+static __device__ __noinline__ bool spin_on(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up,
+                                            uint64_t limit_ns, uint32_t where) {
   const uint64_t t0 = globaltimer();
   do {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*w.gave_up) return false;
-  } while (globaltimer() - t0 <= w.limit_ns);
-  *w.gave_up = where;
+    if (*gave_up) return false;
+  } while (globaltimer() - t0 <= limit_ns);
+  *gave_up = where;
   return false;
+}
+__device__ __forceinline__ bool spin(uint32_t bar, uint32_t parity, const Bound& w, uint32_t where) {
+  return mbar_try_wait(bar, parity) || spin_on(bar, parity, w.gave_up, w.limit_ns, where);
 }
 __device__ __forceinline__ bool spin_all(uint32_t bar, uint32_t parity, const Bound& w, uint32_t where) {
   const bool ok = spin(bar, parity, w, where);
@@ -263,19 +299,17 @@ __device__ __forceinline__ int fold16(float* v, int lane) {
 
 template <int D, int N>
 struct Cfg {
-  static constexpr int kCG = N / 16;                   // softmax warpgroups of a stream
-  static constexpr int kST = 3 - kCG;                  // streams
   static constexpr int kThreads = 512;
   static constexpr int kCodes = kKeys * D;             // a tile of codes
-  static constexpr int kK = D == 128 ? 5 : 8, kV = D == 128 ? 6 : 8;     // stages
+  static constexpr int kK = D == 128 ? 5 : 8, kV = D == 64 ? 8 : N == 16 ? 6 : 5;     // stages
   static constexpr int kQS = N == 16 ? 4 : 2;          // units of Q
   static constexpr int kQ = 2 * N * D;                 // both parts of a unit's rows
   static constexpr int kPW = N == 16 ? 64 : 128;       // bytes of a key's row of P (3N used)
   static constexpr int kP = kKeys * kPW;
   static constexpr int kE = kK + 4;                    // exponents of a step: 128 of K, 128 of V, hidden boxes
   static constexpr int kEBytes = 272;
-  static constexpr int kTmem = 512;                    // S of the streams (2N each), O by unit and stream (3N)
-  static constexpr int oV = kK * kCodes, oP = oV + kV * kCodes, oQ = oP + kST * kP, oE = oQ + kQS * kQ,
+  static constexpr int kTmem = 512;                    // S of kAhead steps (2N each), O by unit (96)
+  static constexpr int oV = kK * kCodes, oP = oV + kV * kCodes, oQ = oP + 2 * kP, oE = oQ + kQS * kQ,
                        oW = oE + kE * kEBytes;
   // words
   static constexpr int wCq = 0;                        // [kQS][N] scale of a column's scores
@@ -284,7 +318,7 @@ struct Cfg {
   static constexpr int wR = wAt + kQS * N;             // [2][2][N] references for the epilogue, by unit and stream
   static constexpr int wL = wR + 4 * N;                // [2][2][4][N] sums of each softmax warp
   static constexpr int wMax = wL + 16 * N;             // [2][4][N] maxima of a step by stream and warp
-  static constexpr int wRef = wMax + 8 * N;            // [2][4][N] a warp's copy of the references
+  static constexpr int wRef = wMax + 8 * N;            // [2][4][N] a warp's copy of the references, negated
   static constexpr int wAl = wRef + 8 * N;             // [2][4][N] ... of the factors of a move
   static constexpr int wWt = wAl + 8 * N;              // [4][2][N] an epilogue warp's weights of the streams
   static constexpr int wNf = wWt + 8 * N;              // [2][2] NaN taken out of V tiles, by unit and stream
@@ -292,7 +326,7 @@ struct Cfg {
   static constexpr int oBar = oW + 4 * kWords;
   static constexpr int kSmem = oBar + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(4 * N + 12 * N <= 512, "tensor memory");
+  static_assert(2 * N * kAhead + 2 * 96 <= 512, "tensor memory");
 };
 
 template <int D, int N>
@@ -300,10 +334,10 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1)
 mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ AttnParams p) {
   using C = Cfg<D, N>;
-  constexpr int CG = C::kCG, ST = C::kST, KS = C::kK, VS = C::kV, QS = C::kQS;
+  constexpr int KS = C::kK, VS = C::kV, QS = C::kQS;
   // barriers
-  constexpr int bQF = 0, bKF = bQF + QS, bKE = bKF + KS, bVF = bKE + KS, bVE = bVF + VS, bSF = bVE + VS, bPF = bSF + 2,
-                bPV = bPF + 2, bOF = bPV + 2, bOE = bOF + 2, bST = bOE + 2, bSE = bST + 2, bDR = bSE + QS, nBar = bDR + 1;
+  constexpr int bQF = 0, bKF = bQF + QS, bKE = bKF + KS, bVF = bKE + KS, bVE = bVF + VS, bSF = bVE + VS, bPF = bSF + kAhead,
+                bPV = bPF + 4, bOF = bPV + 2, bOE = bOF + 2, bST = bOE + 2, bSE = bST + 2, bDR = bSE + QS, nBar = bDR + 1;
   static_assert(nBar * 8 + 16 <= 512, "barrier space");
   griddep_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
@@ -314,9 +348,8 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::oBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + nBar);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  __shared__ int64_t s_sum[C::kThreads / 32];
-  __shared__ int64_t s_from;
-  __shared__ int s_req;
+  __shared__ int2 s_sum[C::kThreads / 32];
+  __shared__ int s_from, s_req;
   __shared__ uint32_t s_bad;
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -326,13 +359,14 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     s_bad = 0;
     for (int s = 0; s < 4; ++s) sNf[s] = 0;
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(bSF + s), 1);
-      mbar_init(bar(bPF + s), 4 * CG);
+      mbar_init(bar(bPF + s), 4);
+      mbar_init(bar(bPF + 2 + s), 4);
       mbar_init(bar(bPV + s), 1);
       mbar_init(bar(bOF + s), 1);
       mbar_init(bar(bOE + s), 4);
-      mbar_init(bar(bST + s), 4 * CG * ST);
+      mbar_init(bar(bST + s), 8);
     }
+    for (int s = 0; s < kAhead; ++s) mbar_init(bar(bSF + s), 1);
     for (int s = 0; s < QS; ++s) { mbar_init(bar(bQF + s), 1); mbar_init(bar(bSE + s), 4); }
     for (int s = 0; s < KS; ++s) { mbar_init(bar(bKF + s), 1); mbar_init(bar(bKE + s), 1); }
     for (int s = 0; s < VS; ++s) { mbar_init(bar(bVF + s), 1); mbar_init(bar(bVE + s), 1); }
@@ -352,53 +386,56 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   // finds the request that its share starts in.
   const int run = (p.B + C::kThreads - 1) / C::kThreads;
   const int rb0 = min(p.B, tid * run), rb1 = min(p.B, rb0 + run);
-  int64_t mine = 0;
+  int mine = 0, units = 0;             // steps' counts, units
   bool bad = false;
   for (int b = rb0; b < rb1; ++b) {
     const Job j = job_of<N>(p, b);
     bad |= !j.ok;
-    mine += j.cost();
+    mine += j.cost(0);
+    units += j.units;
   }
-  int64_t upto = mine;
+  int upto = mine, uptou = units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += x;
+    const int x = __shfl_up_sync(0xffffffffu, upto, o), y = __shfl_up_sync(0xffffffffu, uptou, o);
+    if (lane >= o) { upto += x; uptou += y; }
   }
-  if (lane == 31) s_sum[warp] = upto;
+  if (lane == 31) s_sum[warp] = make_int2(upto, uptou);
   tc_fence_before();
   bad = __syncthreads_or(bad);
   tc_fence_after();
-  int64_t total = 0;
+  int total = 0, totalu = 0;
 #pragma unroll
   for (int w = 0; w < C::kThreads / 32; ++w) {
-    if (w < warp) upto += s_sum[w];
-    total += s_sum[w];
+    if (w < warp) { upto += s_sum[w].x; uptou += s_sum[w].y; }
+    total += s_sum[w].x;
+    totalu += s_sum[w].y;
   }
-  const int blocks = blocks_for(total, p.blocks);
-  const int64_t share0 = total * min((int)blockIdx.x, blocks) / blocks;
-  const int64_t share = total * min((int)blockIdx.x + 1, blocks) / blocks - share0;
+  const int own = total >= 8 * kStep * p.blocks ? kUnit : 0;
+  const Share share(total + own * totalu, p.blocks, blockIdx.x, (N == 16 ? kStep : kWide) + own);
   if (tid == 0) p.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
-  {
-    int64_t at = upto - mine;
-    const bool here = share0 >= at && share0 < upto;
-    if (here)
-      for (int b = rb0; b < rb1; ++b) {
-        const int64_t next = at + job_of<N>(p, b).cost();
-        if (share0 >= at && share0 < next) { s_req = b; s_from = share0 - at; }
-        at = next;
-      }
+  upto += own * uptou;
+  mine += own * units;
+  if (share.size > 0 && share.from >= upto - mine && share.from < upto) {
+    int at = upto - mine;
+    for (int b = rb0; b < rb1; ++b) {
+      const int next = at + job_of<N>(p, b).cost(own);
+      if (share.from >= at && share.from < next) { s_req = b; s_from = share.from - at; }
+      at = next;
+    }
   }
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
   const Bound W{abort_flag, p.wait_ns};
   const int box_shift = min(p.page_shift, 7);
   auto colS = [](int s) { return (uint32_t)(s * 2 * N); };
-  auto colO = [](int unit, int stream) { return (uint32_t)(4 * N + (ST * unit + stream) * 3 * N); };
+  // the streams of a unit lie side by side, three parts of 16 columns each; a
+  // unit of more rows has three parts of 32
+  auto colO = [](int unit, int stream) { return (uint32_t)(2 * N * kAhead + unit * 96 + stream * 48); };
+  auto two_streams = [](int rows) { return N == 16 || rows <= 16; };
 
-  if (share > 0) {
-    Walk<N> w;
-    w.enter(p, s_req, s_from, share);
+  Walk<N> w;
+  if (share.size > 0 && w.enter(p, s_req, s_from, share.size, own)) {
     if (warp == 0 || warp == 3) {
       // ------------------------------------------------- copies of K (V): a lane a box of a page
       const bool y = warp == 3;
@@ -474,100 +511,120 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     } else if (warp == 1) {
       // --------------------------------------------------------------- products
       constexpr uint32_t idS = (1u << 4) | ((uint32_t)(2 * N >> 3) << 17) | (8u << 24);
-      constexpr uint32_t idO = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(3 * N >> 3) << 17) | (8u << 24);
+      constexpr uint32_t idO = (1u << 4) | (1u << 15) | (1u << 16) | (8u << 24), idO48 = idO | (48u >> 3) << 17, idO96 = idO | (96u >> 3) << 17;
       bool ok = true;
       if (p.stall) ok = spin_all(bar(bDR), 0, W, 0x7ff);       // nothing arrives before the drain
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      // S runs two steps ahead: O of step t and S of step t + 2, which takes the
-      // place of S of t, go out together once P of t is there. One wait a step
-      // (a lane a barrier): this warp's own instructions are a long chain of a
-      // short step. What it counts has to be uniform over the warp for the
-      // compiler too (shuffled where it comes from memory): the products'
-      // operands are uniform registers
+      // S of a step goes out as soon as its K is there, up to kAhead steps before
+      // its O, so that the softmax finds its scores waiting; O once V and P are.
+      // A lane a barrier looks for both at once: this warp's own instructions are
+      // a long chain of a short step. What it counts has to be uniform over the
+      // warp for the compiler too (shuffled where it comes from memory): the
+      // products' operands are uniform registers
       int sk = 0, sv = 0, sq = 0, lu = 0;              // slots of K, V and Q; units
-      uint32_t pk = 0, pv = 0, pq = 0, pp = 0;         // phases of K, V, Q and (a bit a stream) P
+      uint32_t pk = 0, pv = 0, pq = 0;                 // their phases
       int ts = 0, to = 0;                              // steps whose S (O) has gone out
-      struct Step { int kv, unit; uint32_t first, open, last; } st[2] = {};     // those between, by parity
-      int k = 0, k0 = 0, k1 = 0, len = 0;
+      // the steps between: unit << 7 | two streams << 6 | products of O << 3 |
+      // last << 2 | opens its unit << 1 | first of its stream
+      uint32_t wait[kAhead] = {};
+      int k = 0, k0 = 0, k1 = 0, len = 0, two = 0;
       bool have = ok;
-      uint64_t qd = 0;
+      uint32_t pp = 0;                                 // phases of P, by warpgroup and place
       auto enter = [&] {
         k = k0 = __shfl_sync(0xffffffffu, w.k0, 0);
         k1 = __shfl_sync(0xffffffffu, w.k1, 0);
         len = __shfl_sync(0xffffffffu, w.j.len, 0);
+        two = __shfl_sync(0xffffffffu, two_streams(w.j.n * p.G - w.row0(w.head())) ? 1 : 0, 0);
       };
       enter();
-      auto scores = [&] {                              // by the elected lane
-        const uint32_t d = tm + colS(ts & 1);
-        const uint64_t a = rows_desc<D>(base + sk * C::kCodes, 0);
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) mma_e4m3(d, a + 2 * x, qd + 2 * x, idS, x != 0);
-        mma_commit(bar(bSF + (ts & 1)));
-        mma_commit(bar(bKE + sk));
-      };
-      auto counted = [&] {                             // S of a step has gone out
-        const Step x{min(kKeys, len - k * kKeys), lu, k < k0 + ST, k == k0, k + 1 == k1};
-        if (ts & 1) st[1] = x; else st[0] = x;
-        ++ts;
-        if (++sk == KS) { sk = 0; pk ^= 1; }
-        if (++k == k1) {
-          if (++sq == QS) { sq = 0; pq ^= 1; }
-          ++lu;
-          have = __shfl_sync(0xffffffffu, w.next(p), 0);
-          if (have) enter();
-        }
-      };
-      auto next_scores = [&]() -> bool {
-        if (k == k0) {
-          if (!spin_all(bar(bQF + sq), pq, W, 0x400)) return false;
-          qd = rows_desc<D>(base + C::oQ + sq * C::kQ, 0);
-        }
-        if (!spin_all(bar(bKF + sk), pk, W, 0x401)) return false;
-        tc_fence_after();
-        if (elect_uniform()) scores();
-        __syncwarp();
-        counted();
-        return true;
-      };
-      if (have) ok = next_scores();
-      if (ok && have) ok = next_scores();
+      uint32_t idle = 0;
+      uint64_t t0 = 0;
 #pragma unroll 1
-      while (ok && to < ts) {
-        const Step x = to & 1 ? st[1] : st[0];
-        const int s0 = ST == 2 ? to & 1 : 0;
+      while (ok && (have || to < ts)) {
+        const uint32_t x = wait[0];
+        const bool both = N > 16 && !(x & 64);         // both warpgroups have a part of P
+        const int unit = x >> 7, pb = to & 1, s0 = both ? 0 : pb;         // place of P, stream
         // O's place: the unit before the last must have been read out
-        if (x.open && x.unit >= 2) ok = spin_all(bar(bOE + (x.unit & 1)), ((x.unit >> 1) - 1) & 1, W, 0x410);
-        ok = ok && spin_all(lane & 1 ? bar(bVF + sv) : bar(bPF + s0), lane & 1 ? pv : (pp >> s0) & 1, W, 0x411);
-        if (!ok) break;
-        const bool both = have && k != k0 && __all_sync(0xffffffffu, mbar_test_wait(bar(bKF + sk), pk));
-        tc_fence_after();
-        // V [key][d] and P [key][part, row], both MN-major, 32 keys a product.
-        // D = 64 repeats its 64 columns (stride 0): rows 64..127 of O^T equal
-        // rows 0..63.
-        const uint32_t d = tm + colO(x.unit & 1, s0);
-        const uint64_t a = rows_desc<D>(base + C::oV + sv * C::kCodes, 0);
-        const uint64_t b = rows_desc<C::kPW>(base + C::oP + s0 * C::kP, 0);
-        const int nks = (x.kv + 31) >> 5;
-        if (elect_uniform()) {
-          mma_e4m3(d, a, b, idO, x.first ^ 1u);
-          if (nks == kKeys / 32) {
-#pragma unroll
-            for (int y = 1; y < kKeys / 32; ++y) mma_e4m3(d, a + y * (2 * D), b + y * (2 * C::kPW), idO, 1u);
-          } else {
-#pragma unroll 1
-            for (int y = 1; y < nks; ++y) mma_e4m3(d, a + y * (2 * D), b + y * (2 * C::kPW), idO, 1u);
+        const bool place = (x & 2) && unit >= 2;
+        int b = bPF + 2 * s0 + pb;
+        uint32_t ph = (pp >> (2 * s0 + pb)) & 1;
+        if (lane == 1) { b = bVF + sv; ph = pv; }
+        if (lane == 2) { b = bKF + sk; ph = pk; }
+        if (lane == 3) { b = bQF + sq; ph = pq; }
+        if (lane == 5) { b = bPF + 2 + pb; ph = (pp >> (2 + pb)) & 1; }
+        if (lane == 4) { b = bOE + (unit & 1); ph = ((unit >> 1) - 1) & 1; }
+        const uint32_t here = __ballot_sync(0xffffffffu, mbar_test_wait(bar(b), ph));
+        const bool o_due = to < ts && (here & 3) == 3 && (!place || (here & 16)) && (!both || (here & 32));
+        const bool s_due = have && ts - to < kAhead && (here & 4) && (k != k0 || (here & 8));
+        if (!o_due && !s_due) {
+          // bounded: the clock is read every 64 fruitless rounds
+          if ((++idle & 63) == 0) {
+            const uint64_t now = globaltimer();
+            if (idle == 64) t0 = now;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            if (__any_sync(0xffffffffu, now - t0 > p.wait_ns && idle > 64)) {
+              if (lane == 0) *abort_flag = 0x400;
+              break;
+            }
           }
-          mma_commit(bar(bPV + s0));
-          if (x.last) mma_commit(bar(bOF + (x.unit & 1)));
-          if (both) scores();
-          mma_commit(bar(bVE + sv));
+          continue;
+        }
+        idle = 0;
+        tc_fence_after();
+        if (elect_uniform()) {
+          if (o_due) {
+            // V [key][d] and P [key][part, row], both MN-major, 32 keys a
+            // product. D = 64 repeats its 64 columns (stride 0): rows 64..127 of
+            // O^T equal rows 0..63.
+            const uint32_t d = tm + colO(unit & 1, s0);
+            const uint64_t a = rows_desc<D>(base + C::oV + sv * C::kCodes, 0);
+            const uint64_t b2 = rows_desc<C::kPW>(base + C::oP + pb * C::kP, 0);
+            const int nks = (x >> 3) & 7;
+            const uint32_t id = both ? idO96 : idO48;
+            mma_e4m3(d, a, b2, id, (x & 1) ^ 1u);
+            if (nks == kKeys / 32) {
+#pragma unroll
+              for (int y = 1; y < kKeys / 32; ++y) mma_e4m3(d, a + y * (2 * D), b2 + y * (2 * C::kPW), id, 1u);
+            } else {
+#pragma unroll 1
+              for (int y = 1; y < nks; ++y) mma_e4m3(d, a + y * (2 * D), b2 + y * (2 * C::kPW), id, 1u);
+            }
+            mma_commit(bar(bPV + pb));
+            if (x & 4) mma_commit(bar(bOF + (unit & 1)));
+          }
+          if (s_due) {
+            const uint32_t d = tm + colS(ts % kAhead);
+            const uint64_t a = rows_desc<D>(base + sk * C::kCodes, 0), q = rows_desc<D>(base + C::oQ + sq * C::kQ, 0);
+#pragma unroll
+            for (int y = 0; y < D / 32; ++y) mma_e4m3(d, a + 2 * y, q + 2 * y, idS, y != 0);
+            mma_commit(bar(bSF + ts % kAhead));
+            mma_commit(bar(bKE + sk));
+          }
+          if (o_due) mma_commit(bar(bVE + sv));
         }
         __syncwarp();
-        if (++sv == VS) { sv = 0; pv ^= 1; }
-        pp ^= 1u << s0;
-        ++to;
-        if (both) counted();
-        else if (have) ok = next_scores();
+        if (o_due) {
+          if (++sv == VS) { sv = 0; pv ^= 1; }
+          pp ^= both ? 5u << pb : 1u << (2 * s0 + pb);
+          ++to;
+#pragma unroll
+          for (int i = 0; i + 1 < kAhead; ++i) wait[i] = wait[i + 1];
+        }
+        if (s_due) {
+          const uint32_t y = (uint32_t)lu << 7 | (uint32_t)two << 6 | (uint32_t)((min(kKeys, len - k * kKeys) + 31) >> 5) << 3 |
+                             (k + 1 == k1 ? 4u : 0u) | (k == k0 ? 2u : 0u) | (k < k0 + 1 + two ? 1u : 0u);
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+            if (ts - to == i) wait[i] = y;
+          ++ts;
+          if (++sk == KS) { sk = 0; pk ^= 1; }
+          if (++k == k1) {
+            if (++sq == QS) { sq = 0; pq ^= 1; }
+            ++lu;
+            have = __shfl_sync(0xffffffffu, w.next(p), 0);
+            if (have) enter();
+          }
+        }
       }
       // drain: all tensor-core work of the elected lane completes before dealloc
       if (elect_uniform()) mma_commit(bar(bDR));
@@ -575,19 +632,24 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       wait_drain(bar(bDR), 0);
     } else if (warp == 2) {
       // ------------------------------------------------- Q and what its columns are
-      // A row by D / 16 lanes, 16 elements each. Rows that are none keep what
-      // was there: nobody reads their columns. The next unit's first rows come
-      // while this one's are turned
+      // A row by D / 16 lanes, 16 elements each, RI rows at a time. Rows that are
+      // none keep what was there: nobody reads their columns. The next rows come
+      // while these are turned
       constexpr int LR = D / 16, RI = 32 / LR;
-      const int c = lane % LR, n0 = lane / LR;
-      int lu = 0;
+      const int c = lane % LR;
+      int lu = 0, n = lane / LR;
+      struct Rows { int h, first, rows, row0, see; } a, cur;
       bool more = true;
-      struct Rows { int h, first, rows, row0, see; };
+      uint4 x, y;
+      int at;
       auto of = [&] {
-        const int h = w.head(), first = w.row0(h);
-        return Rows{h, first, min(N, w.j.n * p.G - first), w.j.row0, w.j.len - w.j.n + 1};
+        a.h = w.head();
+        a.first = w.row0(a.h);
+        a.rows = min(N, w.j.n * p.G - a.first);
+        a.row0 = w.j.row0;
+        a.see = w.j.len - w.j.n + 1;
       };
-      auto load = [&](const Rows& a, int n, uint4& x, uint4& y, int& at) {
+      auto load = [&] {                                // row n of unit a
         x = y = make_uint4(0u, 0u, 0u, 0u);
         at = 0;
         if (n >= a.rows) return;
@@ -597,60 +659,60 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         x = src[0];
         y = src[1];
       };
-      Rows cur = of();
-      uint4 x, y;
-      int at;
-      load(cur, n0, x, y, at);
-      while (true) {
-        const Rows a = cur;
-        uint4 xa = x, ya = y;
-        int ata = at;
-        more = w.next(p);
-        if (more) {
-          cur = of();
-          load(cur, n0, x, y, at);
-        }
-        const int sl = lu % QS;
-        // what the unit before left there has been read
-        if (lu >= QS && !spin_all(bar(bSE + sl), ((lu / QS) - 1) & 1, W, 0x200)) break;
+      of();
+      load();
 #pragma unroll 1
-        for (int n = n0; n - n0 < a.rows; n += RI) {
-          if (n >= RI) load(a, n, xa, ya, ata);
-          float f[16];
-          bf16x8_to_float(xa, f);
-          bf16x8_to_float(ya, f + 8);
-          float m = 0.f;
+      while (true) {
+        // these rows, and the next ones' loads
+        const uint4 xa = x, ya = y;
+        const int ata = at, na = n, sl = lu % QS, n0 = n - lane / LR;
+        cur = a;
+        const bool begins = n0 == 0, ends = n0 + RI >= a.rows;
+        if (!ends) {
+          n += RI;
+        } else {
+          n = lane / LR;
+          more = w.next(p);
+          of();
+        }
+        if (more) load();
+        // what the unit before left there has been read
+        if (begins && lu >= QS && !spin_all(bar(bSE + sl), ((lu / QS) - 1) & 1, W, 0x200)) break;
+        float f[16];
+        bf16x8_to_float(xa, f);
+        bf16x8_to_float(ya, f + 8);
+        float m = 0.f;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(f[e]));
-          m = row_max<LR>(m, 0xffffffffu);
-          // m * 2^-ex in [128, 256); a row with infinities is NaN
-          const int ex = m > 0.f ? max((__float_as_int(m) >> 23) - 127 - 7, -126) : 0;
-          const float unit = m <= 3.4e38f ? pow2(-ex) : __int_as_float(0x7fffffff);
-          uint32_t hi[4], lo[4];
+        for (int e = 0; e < 16; e += 2) m = max3(m, fabsf(f[e]), fabsf(f[e + 1]));
+        m = row_max<LR>(m, 0xffffffffu);
+        // m * 2^-ex in [128, 256); a row with infinities is NaN
+        const int ex = m > 0.f ? max((__float_as_int(m) >> 23) - 127 - 7, -126) : 0;
+        const float unit = m <= 3.4e38f ? pow2(-ex) : __int_as_float(0x7fffffff);
+        uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float z[4], b[4];
+        for (int q = 0; q < 4; ++q) {
+          float z[4], b[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] = f[4 * q + e] * unit;
-            hi[q] = e4m3x4(z[0], z[1], z[2], z[3]);
-            half2_to_float(e4m3x2_to_half2((uint16_t)hi[q]), b[0], b[1]);
-            half2_to_float(e4m3x2_to_half2((uint16_t)(hi[q] >> 16)), b[2], b[3]);
+          for (int e = 0; e < 4; ++e) z[e] = f[4 * q + e] * unit;
+          hi[q] = e4m3x4(z[0], z[1], z[2], z[3]);
+          half2_to_float(e4m3x2_to_half2((uint16_t)hi[q]), b[0], b[1]);
+          half2_to_float(e4m3x2_to_half2((uint16_t)(hi[q] >> 16)), b[2], b[3]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] = (z[e] - b[e]) * 32.f;
-            lo[q] = e4m3x4(z[0], z[1], z[2], z[3]);
-          }
-          const uint32_t q0 = base + C::oQ + sl * C::kQ;
-          if (n < a.rows) {
-            st_shared_v4(q0 + chunk_at<D>(n, c), hi[0], hi[1], hi[2], hi[3]);
-            st_shared_v4(q0 + N * D + chunk_at<D>(n, c), lo[0], lo[1], lo[2], lo[3]);
-            if (c == 0) {
-              words[C::wCq + sl * N + n] = pow2(min(ex, 127)) * p.scale_log2;
-              reinterpret_cast<int*>(words)[C::wLim + sl * N + n] = a.see + (ata >> 8);
-              reinterpret_cast<int*>(words)[C::wAt + sl * N + n] = ata;
-            }
+          for (int e = 0; e < 4; ++e) z[e] = (z[e] - b[e]) * 32.f;
+          lo[q] = e4m3x4(z[0], z[1], z[2], z[3]);
+        }
+        const uint32_t q0 = base + C::oQ + sl * C::kQ;
+        if (na < cur.rows) {
+          st_shared_v4(q0 + chunk_at<D>(na, c), hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(q0 + N * D + chunk_at<D>(na, c), lo[0], lo[1], lo[2], lo[3]);
+          if (c == 0) {
+            words[C::wCq + sl * N + na] = pow2(min(ex, 127)) * p.scale_log2;
+            reinterpret_cast<int*>(words)[C::wLim + sl * N + na] = cur.see + (ata >> 8);
+            reinterpret_cast<int*>(words)[C::wAt + sl * N + na] = ata;
           }
         }
-        if (lane >= a.rows && lane < N) {
+        if (!ends) continue;
+        if (lane >= cur.rows && lane < N) {
           words[C::wCq + sl * N + lane] = 0.f;
           reinterpret_cast<int*>(words)[C::wLim + sl * N + lane] = 0;
         }
@@ -662,18 +724,19 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       }
     } else if (warp < 12) {
       // --------------------------------------------------------------- softmax
-      const int wg = (warp - 4) >> 2, str = wg / CG, cg = wg % CG, sw = warp & 3, r = sw * 32 + lane;
-      const int c0 = cg * 16, id = 1 + wg;
+      const int wg = (warp - 4) >> 2, sw = warp & 3, r = sw * 32 + lane, id = 1 + wg;
       const uint32_t tl = tmem + ((uint32_t)(sw * 32) << 16);
-      const uint32_t aP = base + C::oP + str * C::kP;
-      float* ref = words + C::wRef + (str * 4 + sw) * N + c0;
-      float* al = words + C::wAl + (str * 4 + sw) * N + c0;
-      float* mx = words + C::wMax + str * 4 * N + c0;
       int t = 0, lu = 0;                               // steps of both streams, units
       bool ok = true, more = true, gone = false;
       while (more) {
         const int slot = lu & 1, sq = lu % QS, first_row = w.row0(w.head()), rows = w.j.n * p.G - first_row;
         const int len = w.j.len, see = w.all_see(p, first_row);
+        // every other step and all columns, or every step and its 16 of 32
+        const bool two = two_streams(rows);
+        const int str = two ? wg : 0, c0 = two ? 0 : 16 * wg, parts = two ? 16 : 32;
+        float* ref = words + C::wRef + (str * 4 + sw) * N + c0;
+        float* al = words + C::wAl + (str * 4 + sw) * N + c0;
+        float* mx = words + C::wMax + str * 4 * N + c0;
         ok = spin(bar(bQF + sq), (lu / QS) & 1, W, 0x700) &&
              (lu < 2 || spin(bar(bSE + (lu - 2) % QS), ((lu - 2) / QS) & 1, W, 0x701));
         // one vote of the warpgroup: all go on, or all leave
@@ -684,13 +747,14 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 #pragma unroll
         for (int n = 0; n < 8; ++n) l2[n] = 0ull;
         bool first = true, nan = false;
-        // the stream's steps: every other one of the share
         int k = w.k0;
-        if (ST == 2 && ((t ^ str) & 1)) { ++k; ++t; }
+        const int stride = two ? 2 : 1;
+        if (two && ((t ^ str) & 1)) { ++k; ++t; }
 #pragma unroll 1
-        for (; k < w.k1; k += ST, t += ST) {
-          const uint32_t before = (uint32_t)(t / ST - 1) & 1u, tS = tl + colS(t & 1) + c0;      // phase of its last product
-          ok = spin_all(bar(bSF + (t & 1)), (t >> 1) & 1, W, 0x710);
+        for (; k < w.k1; k += stride, t += stride) {
+          const int pb = t & 1;
+          const uint32_t tS = tl + colS(t % kAhead) + c0;
+          ok = spin_all(bar(bSF + t % kAhead), (t / kAhead) & 1, W, 0x710);
           tc_fence_after();
           uint32_t s[16], x[16];
           if (ok) {
@@ -734,8 +798,8 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             for (int n = 0; n < 16; n += 4) {
               const float4 c = *reinterpret_cast<const float4*>(ref + n);
               float y0, y1, y2, y3;
-              f2_unpack(f2_fma(f2_pack(s[n], s[n + 1]), k2, f2_pack(__float_as_uint(-c.x), __float_as_uint(-c.y))), y0, y1);
-              f2_unpack(f2_fma(f2_pack(s[n + 2], s[n + 3]), k2, f2_pack(__float_as_uint(-c.z), __float_as_uint(-c.w))), y2, y3);
+              f2_unpack(f2_fma(f2_pack(s[n], s[n + 1]), k2, f2_pack(__float_as_uint(c.x), __float_as_uint(c.y))), y0, y1);
+              f2_unpack(f2_fma(f2_pack(s[n + 2], s[n + 3]), k2, f2_pack(__float_as_uint(c.z), __float_as_uint(c.w))), y2, y3);
               x[n] = __float_as_uint(y0); x[n + 1] = __float_as_uint(y1);
               x[n + 2] = __float_as_uint(y2); x[n + 3] = __float_as_uint(y3);
             }
@@ -763,22 +827,22 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             bar_sync128(id);
             // every warp draws the same conclusion from the four warps' maxima
             if (lane < 16) {
-              const float old = first ? kNone : ref[lane];
+              const float old = first ? kNone : -ref[lane];
               float to = old;
 #pragma unroll
               for (int q = 0; q < 4; ++q) to = fmaxf(to, mx[q * N + lane]);
               if (c0 + lane >= rows) to = kDead;
               al[lane] = to > old ? ex2(old - to) : 1.f;
-              ref[lane] = to;
+              ref[lane] = -to;
             }
             __syncwarp();
             if (!first) {
-              ok = spin_all(bar(bPV + str), before, W, 0x730);    // O holds every step before
+              ok = spin_all(bar(bPV + ((t - stride) & 1)), ((t - stride) >> 1) & 1, W, 0x730);    // O holds every step before
               tc_fence_after();
               if (ok) {
 #pragma unroll 1
                 for (int q = 0; q < 3; ++q) {
-                  const uint32_t tO = tl + colO(slot, str) + q * N + c0;
+                  const uint32_t tO = tl + colO(slot, str) + q * parts + c0;
                   tmem_ld16(tO, x);
                   tmem_ld_wait();
                   reg_fence16(x);
@@ -820,14 +884,14 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 #pragma unroll
             for (int q = 0; q < 3; ++q) part3[q][n] = __byte_perm(lo[q], hi[q], 0x5410);
           }
-          if (ok && t >= ST) ok = spin_all(bar(bPV + str), before, W, 0x740);   // its last P has been read
+          if (ok && t >= 2) ok = spin_all(bar(bPV + pb), ((t - 2) >> 1) & 1, W, 0x740);   // what was there has been read
           if (ok) {
 #pragma unroll
             for (int q = 0; q < 3; ++q)
-              st_shared_v4(aP + chunk_at<C::kPW>(r, q * CG + cg), part3[q][0], part3[q][1], part3[q][2], part3[q][3]);
+              st_shared_v4(base + C::oP + pb * C::kP + chunk_at<C::kPW>(r, two ? q : 2 * q + wg), part3[q][0], part3[q][1], part3[q][2], part3[q][3]);
             // V rows that nobody sees hold anything; NaN that only some rows see
             // is left to the epilogue (0 x NaN would reach all)
-            if (!plain && cg == 0 && r < ((len - k * kKeys + 31) & ~31) && (gone_key || key >= see)) {
+            if (!plain && (two || wg == 0) && r < ((len - k * kKeys + 31) & ~31) && (gone_key || key >= see)) {
               const int sv = t % VS;
               ok = spin(bar(bVF + sv), (t / VS) & 1, W, 0x750);
               const uint32_t row = base + C::oV + sv * C::kCodes;
@@ -852,7 +916,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           fence_proxy_async();
           tc_fence_before();
           __syncwarp();
-          if (ok && lane == 0) mbar_arrive(bar(bPF + str));
+          if (ok && lane == 0) mbar_arrive(bar(bPF + 2 * wg + pb));
         }
         if (gone) break;
         t += w.k1 - k;                                 // the next unit's first step
@@ -862,8 +926,8 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         for (int n = 0; n < 8; ++n) f2_unpack(l2[n], l[2 * n], l[2 * n + 1]);
         const int col = fold16<false>(l, lane);
         words[C::wL + ((slot * 2 + str) * 4 + sw) * N + c0 + col] = l[0];
-        if (sw == 0 && lane < 16) words[C::wR + (slot * 2 + str) * N + c0 + lane] = first ? kNone : ref[lane];
-        if (cg == 0 && __any_sync(0xffffffffu, nan) && lane == 0) sNf[slot * 2 + str] = 1u + (uint32_t)lu;
+        if (sw == 0 && lane < 16) words[C::wR + (slot * 2 + str) * N + c0 + lane] = first ? kNone : -ref[lane];
+        if (__any_sync(0xffffffffu, nan) && lane == 0) sNf[slot * 2 + str] = 1u + (uint32_t)lu;
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(bar(bST + slot));
         ++lu;
@@ -882,7 +946,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       bool ok = true, more = true;
       while (more) {
         const int slot = lu & 1, h = w.head(), first = w.row0(h), rows = min(N, w.j.n * p.G - first);
-        const bool whole = w.k0 == 0 && w.k1 == w.j.steps;
+        const bool whole = w.k0 == 0 && w.k1 == w.j.steps, two = two_streams(rows);
         ok = spin_all(bar(bST + slot), (lu >> 1) & 1, W, 0x800);
         if (!ok) break;
         const int piece = 2 * blockIdx.x + (lu ? 1 : 0), sq = lu % QS;
@@ -891,12 +955,12 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         float mx = kNone, sum = 0.f;
         if (lane < N) {
           const float* l0 = words + C::wL + slot * 8 * N + lane;
-          const float* l1 = l0 + (ST - 1) * 4 * N;
-          const float r0 = words[C::wR + slot * 2 * N + lane], r1 = ST == 2 ? words[C::wR + (slot * 2 + 1) * N + lane] : kNone;
+          const float* l1 = l0 + 4 * N;
+          const float r0 = words[C::wR + slot * 2 * N + lane], r1 = two ? words[C::wR + (slot * 2 + 1) * N + lane] : kNone;
           mx = fmaxf(r0, r1);
           const float a0 = ex2(r0 - mx), a1 = ex2(r1 - mx);
           sum = a0 * ((l0[0] + l0[N]) + (l0[2 * N] + l0[3 * N]));
-          if (ST == 2) sum += a1 * ((l1[0] + l1[N]) + (l1[2 * N] + l1[3 * N]));
+          if (two) sum += a1 * ((l1[0] + l1[N]) + (l1[2 * N] + l1[3 * N]));
           // the products' weights carry 2^-26; NaN stays
           const float inv = whole ? (sum != 0.f ? 67108864.f / sum : 0.f) : 1.f;
           wt[lane] = a0 * inv;
@@ -904,10 +968,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         if (sw == 0 && lane == 0 && !whole && w.k0 == 0) {
           // the block that holds its last step
-          const int64_t last = share0 + share + w.j.steps - w.k1 - 1;
-          int c = (int)(last * blocks / total);
-          while (total * (c + 1) / blocks <= last) ++c;
-          while (total * c / blocks > last) --c;
+          const int c = share.holder(share.from + share.size - w.left + w.ahead() - 1);
           p.meta[2 * blockIdx.x] = make_int4(c - (int)blockIdx.x + 1, rows, h, first);
           p.meta[2 * blockIdx.x + 1] = make_int4(w.j.row0, lu ? 1 : 0, 0, 0);
         }
@@ -924,9 +985,10 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         ok = spin_all(bar(bOF + slot), (lu >> 1) & 1, W, 0x810);
         if (!ok) break;
         tc_fence_after();
-        const bool nf = sNf[slot * 2] == 1u + (uint32_t)lu || (ST == 2 && sNf[slot * 2 + 1] == 1u + (uint32_t)lu);
+        const bool nf = sNf[slot * 2] == 1u + (uint32_t)lu || (two && sNf[slot * 2 + 1] == 1u + (uint32_t)lu);
         // streams that had a step: both, or the one of a single step
-        const bool use0 = ST == 1 || w.k1 - w.k0 > 1 || !(t & 1), use1 = ST == 2 && (w.k1 - w.k0 > 1 || (t & 1));
+        const bool use0 = !two || w.k1 - w.k0 > 1 || !(t & 1), use1 = two && (w.k1 - w.k0 > 1 || (t & 1));
+        const int parts = two ? 16 : 32;
         t += w.k1 - w.k0;
         // the columns in use; what no row needs is given back unread
         const int used = min(NE, rows - e0);
@@ -940,12 +1002,16 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           float ov[CH];
 #pragma unroll
           for (int n = 0; n < CH; ++n) ov[n] = 0.f;
-          uint32_t y[ST][3][CH];                       // the parts of the streams' accumulators
+          uint32_t y[2][3][CH];                        // the parts of the streams' accumulators
 #pragma unroll
-          for (int i = 0; i < 3 * ST; ++i) tmem_ld8(tl + colO(slot, i / 3) + (i % 3) * N + e0 + q, y[i / 3][i % 3]);
+          for (int i = 0; i < 3; ++i) tmem_ld8(tl + colO(slot, 0) + i * parts + e0 + q, y[0][i]);
+          if (two) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) tmem_ld8(tl + colO(slot, 1) + i * parts + e0 + q, y[1][i]);
+          }
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 3 * ST; ++i) reg_fence8(y[i / 3][i % 3]);
+          for (int i = 0; i < 6; ++i) reg_fence8(y[i / 3][i % 3]);
           auto add = [&](int stream) {
 #pragma unroll
             for (int n = 0; n < CH; ++n) {
@@ -955,9 +1021,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             }
           };
           if (use0) add(0);
-          if constexpr (ST == 2) {
-            if (use1) add(1);
-          }
+          if (use1) add(1);
           if (q + CH >= used) {
             tc_fence_before();
             __syncwarp();
@@ -1194,6 +1258,9 @@ extern "C" mis_status_t mis_paged_attention_q8_fwd(
         if (overlap(out[i], out[j])) return MIS_ERR_INVALID_ARG;
     }
   }
+  // what steps and units count is counted in 32 bits
+  const double tiles = (double)((head_rows(desc, cache) + 15) / 16) * cache->Hkv;
+  if ((((double)max_pages * cache->page_size / kKeys + 1) * kWide + kUnit) * tiles * desc->B >= 2147483648.0) return MIS_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (desc->T == 0) return cudaMemsetAsync(workspace, 0, 8, st) == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
   uint8_t* base = static_cast<uint8_t*>(workspace);
@@ -1212,7 +1279,7 @@ extern "C" mis_status_t mis_paged_attention_q8_fwd(
   p.cache_len = cache_len; p.cu = cu_rows;
   p.n_pages = cache->n_pages;
   p.page_shift = 31 - __builtin_clz((unsigned)cache->page_size);
-  p.max_pages = max_pages;
+  p.most = max_pages << p.page_shift;
   p.B = desc->B; p.T = desc->T; p.Hkv = cache->Hkv; p.G = desc->Hq / cache->Hkv;
   p.max_rows = desc->max_rows;
   p.blocks = num_sms();
