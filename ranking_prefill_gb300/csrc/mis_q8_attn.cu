@@ -120,8 +120,8 @@ __device__ __forceinline__ Job job_of(const AttnParams& p, const Given& g) {
   j.ok = j.row0 >= 0 && g.end >= j.row0 && g.end <= p.T && g.end - j.row0 <= p.max_rows && j.len >= 0 &&
          j.len <= p.most && g.end - j.row0 <= j.len;
   j.n = j.ok ? g.end - j.row0 : 0;
-  j.steps = (j.len + kKeys - 1) / kKeys;
-  j.tiles = (j.n * p.G + N - 1) / N;
+  j.steps = (uint32_t)(j.len + kKeys - 1) / kKeys;
+  j.tiles = (uint32_t)(j.n * p.G + N - 1) / N;
   j.units = j.tiles * p.Hkv;
   j.step = N == 16 || j.n * p.G <= 16 ? kStep : kWide;
   return j;
@@ -135,15 +135,15 @@ __device__ __forceinline__ Job job_of(const AttnParams& p, int b) { return job_o
 struct Share {
   int quo, rem, from, size;
   __device__ __forceinline__ Share(int total, int blocks, int b, int least) {
-    blocks = min(blocks, max(1, total / least));
-    quo = total / blocks;
+    if (total < blocks * least) blocks = max(1u, (uint32_t)total / (uint32_t)least);
+    quo = (uint32_t)total / (uint32_t)blocks;
     rem = total - quo * blocks;
     from = b * quo + min(b, rem);
     size = b < blocks ? quo + (b < rem ? 1 : 0) : 0;
   }
   __device__ __forceinline__ int holder(int at) const {
     const int cut = rem * (quo + 1);
-    return at < cut ? at / (quo + 1) : rem + (at - cut) / quo;
+    return at < cut ? (uint32_t)at / (uint32_t)(quo + 1) : rem + (uint32_t)(at - cut) / (uint32_t)quo;
   }
 };
 
@@ -164,11 +164,11 @@ struct Walk {
     own = own_;
     j = job_of<N>(p, b);
     g = given(p, b + 1);
-    u = from / j.unit(own);
+    u = (uint32_t)from / (uint32_t)j.unit(own);
     off = from - u * j.unit(own);
-    k0 = off / j.step;
+    k0 = (uint32_t)off / (uint32_t)j.step;
     if (k0 >= j.steps) return next(p);
-    k1 = min(j.steps, (off + left) / j.step);
+    k1 = min(j.steps, (int)((uint32_t)(off + left) / (uint32_t)j.step));
     return k1 > k0;
   }
   // the next piece; false at the end of the share
@@ -184,12 +184,12 @@ struct Walk {
       } while (j.units == 0);
     }
     k0 = 0;
-    k1 = min(j.steps, left / j.step);
+    k1 = min(j.steps, (int)((uint32_t)left / (uint32_t)j.step));
     return k1 > 0;
   }
   // the end of the unit's steps, counted from the piece on
   __device__ __forceinline__ int ahead() const { return j.steps * j.step - off; }
-  __device__ __forceinline__ int head() const { return j.tiles == 1 ? u : u / j.tiles; }
+  __device__ __forceinline__ int head() const { return j.tiles == 1 ? u : (int)((uint32_t)u / (uint32_t)j.tiles); }
   __device__ __forceinline__ int row0(int h) const { return (u - h * j.tiles) * N; }   // of the kv head's rows
   // keys that every row of the unit sees
   __device__ __forceinline__ int all_see(const AttnParams& p, int first) const { return j.len - j.n + first / p.G + 1; }
@@ -1085,20 +1085,24 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   }
 }
 
-// Joins the pieces of a unit that several blocks hold, in block order: a block of
-// four warps a row of the unit that starts in block blockIdx.x, the warps taking
-// the pieces in turn. What it needs lies in one place, since its time is that of
-// the trips to L2 it makes one behind the other (found by bisection of the
-// requests' steps: 10 us for 64 decoded tokens).
+// Joins the pieces of a unit that several blocks hold, in block order: block
+// (c, y) takes rows of the unit that starts in block c, a row by `share` of its
+// four warps, which take the pieces in turn. What it needs lies in one place,
+// since its time is that of the trips to L2 it makes one behind the other (units
+// found by bisection of the requests' steps: 10 us for 64 decoded tokens), and
+// that of its blocks' launch, which the attention's registers leave no room for
+// before its own blocks end: no more of them than there can be rows.
 template <int D, int N>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-mis_q8_join_kernel(const __grid_constant__ AttnParams p) {
+mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
   constexpr int E = D / 32;
   __shared__ float s_acc[kJoinWarps][D + 1];
+  griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x, n = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
+  const int sub = warp & (share - 1), n = blockIdx.y * (kJoinWarps / share) + warp / share;
   const int4 u = p.meta[2 * c], v = p.meta[2 * c + 1];
-  if (c == 0 && n == 0 && warp == 0) {
+  if (c == 0 && blockIdx.y == 0 && warp == 0) {
     uint32_t f = 0, where = 0;
     for (int x = lane; x < p.blocks; x += 32) {
       const uint32_t y = p.flags[2 * x];
@@ -1114,10 +1118,11 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p) {
     }
   }
   const int pieces = u.x;
-  if (pieces < 2 || n >= u.y) return;
+  if (pieces < 2) return;
+  const bool live = n < u.y;
   // the first piece lies in block c's first or second slot, the others in the
   // first slots of the blocks that follow
-  auto at = [&](int y) { return (int64_t)(2 * (c + y) + (y == 0 ? v.y : 0)) * N + n; };
+  auto at = [&](int y) { return (int64_t)(2 * (c + y) + (y == 0 ? v.y : 0)) * N + (live ? n : 0); };
   float acc[E], sum = 0.f, m = kNone;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -1130,7 +1135,7 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll 4
-  for (int y = warp; y < pieces; y += kJoinWarps) {
+  for (int y = sub; y < pieces; y += share) {
     const float2 rl = p.rl[at(y)];
     const float f1 = ex2(rl.x - m);
     sum += f1 * rl.y;
@@ -1143,16 +1148,19 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p) {
       acc[0] += f1 * z2.x; acc[1] += f1 * z2.y;
     }
   }
+  if (share > 1) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_acc[warp][e * 32 + lane] = acc[e];
-  if (lane == 0) s_acc[warp][D] = sum;
-  __syncthreads();
-  if (warp) return;
-  for (int y = 1; y < min(kJoinWarps, pieces); ++y) {
+    for (int e = 0; e < E; ++e) s_acc[warp][e * 32 + lane] = acc[e];
+    if (lane == 0) s_acc[warp][D] = sum;
+    __syncthreads();
+    if (sub) return;
+    for (int y = 1; y < min(share, pieces); ++y) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += s_acc[y][e * 32 + lane];
-    sum += s_acc[y][D];
+      for (int e = 0; e < E; ++e) acc[e] += s_acc[warp + y][e * 32 + lane];
+      sum += s_acc[warp + y][D];
+    }
   }
+  if (!live) return;
   const int i = (u.w + n) / p.G, head = u.z * p.G + u.w + n - i * p.G;
   // the products' weights carry 2^-26
   const float inv = sum != 0.f ? 67108864.f / sum : 0.f;
@@ -1210,7 +1218,9 @@ mis_status_t launch(const CUtensorMap& km, const CUtensorMap& vm, const AttnPara
   if (!kernel_attr_once(reinterpret_cast<const void*>(kern), C::kSmem)) return MIS_ERR_CUDA;
   if (launch_pdl(kern, dim3((unsigned)p.blocks), dim3(C::kThreads), C::kSmem, st, km, vm, p) != cudaSuccess)
     return MIS_ERR_CUDA;
-  return launch_pdl(mis_q8_join_kernel<D, N>, dim3((unsigned)p.blocks, N), dim3(32 * kJoinWarps), 0, st, p) == cudaSuccess
+  const int rows = std::min(N, p.max_rows * p.G), share = rows <= 8 ? kJoinWarps : 1;
+  return launch_pdl(mis_q8_join_kernel<D, N>, dim3((unsigned)p.blocks, (unsigned)(rows * share + kJoinWarps - 1) / kJoinWarps),
+                    dim3(32 * kJoinWarps), 0, st, p, share) == cudaSuccess
              ? MIS_OK
              : MIS_ERR_CUDA;
 }
