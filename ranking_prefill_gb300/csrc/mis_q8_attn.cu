@@ -1126,6 +1126,22 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
   float acc[E], sum = 0.f, m = kNone;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  auto load = [&](int y, float* z, float2& rl) {
+    const float* from = p.part + at(y) * D + lane * E;
+    rl = p.rl[at(y)];
+    if constexpr (E == 4) {
+      const float4 z4 = *reinterpret_cast<const float4*>(from);
+      z[0] = z4.x; z[1] = z4.y; z[2] = z4.z; z[3] = z4.w;
+    } else {
+      const float2 z2 = *reinterpret_cast<const float2*>(from);
+      z[0] = z2.x; z[1] = z2.y;
+    }
+  };
+  // the first pieces come while the maximum is taken
+  float z0[E], z1[E];
+  float2 rl0, rl1;
+  load(min(sub, pieces - 1), z0, rl0);
+  load(min(sub + share, pieces - 1), z1, rl1);
   bool stuck = false;
   for (int y = lane; y < pieces; y += 32) {
     m = fmaxf(m, p.rl[at(y)].x);
@@ -1134,19 +1150,19 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
   if (__any_sync(0xffffffffu, stuck)) return;          // a piece is missing: every warp sees it
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll 4
-  for (int y = sub; y < pieces; y += share) {
-    const float2 rl = p.rl[at(y)];
-    const float f1 = ex2(rl.x - m);
-    sum += f1 * rl.y;
-    const float* z = p.part + at(y) * D + lane * E;
-    if constexpr (E == 4) {
-      const float4 z4 = *reinterpret_cast<const float4*>(z);
-      acc[0] += f1 * z4.x; acc[1] += f1 * z4.y; acc[2] += f1 * z4.z; acc[3] += f1 * z4.w;
-    } else {
-      const float2 z2 = *reinterpret_cast<const float2*>(z);
-      acc[0] += f1 * z2.x; acc[1] += f1 * z2.y;
+#pragma unroll 1
+  for (int y = sub; y < pieces; y += 2 * share) {
+    const float f0 = ex2(rl0.x - m), f1 = y + share < pieces ? ex2(rl1.x - m) : 0.f;
+    sum += f0 * rl0.y;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += f0 * z0[e];
+    if (y + share < pieces) {
+      sum += f1 * rl1.y;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += f1 * z1[e];
     }
+    load(min(y + 2 * share, pieces - 1), z0, rl0);
+    load(min(y + 3 * share, pieces - 1), z1, rl1);
   }
   if (share > 1) {
 #pragma unroll

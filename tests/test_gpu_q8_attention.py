@@ -225,6 +225,54 @@ def test_two_streams_at_once():
         b.check()
 
 
+def test_a_stalled_call_ends_and_the_next_one_is_right():
+    b = Batch([3000, 40, 700], [1, 3, 2], 8, 2, 128, 16, seed=40).put()
+    limit = lib.mis_set_wait_limit_ns(2_000_000)
+    try:
+        lib.mis_inject_stall(1)
+        b.call()
+        assert lib.mis_get_device_status(b.ws) == lib.MIS_ERR_DEVICE_TIMEOUT
+        assert (b.o == 7).all()
+    finally:
+        lib.mis_inject_stall(0)
+        lib.mis_set_wait_limit_ns(limit)
+    b.call()
+    assert lib.mis_get_device_status(b.ws) == lib.MIS_OK
+    b.check()
+
+
+@pytest.mark.parametrize("ns", [[1, 3, 2], [9, 2, 12]])
+def test_waits_that_run_out_anywhere_end_the_call(ns):
+    b = Batch([20000, 40, 3000], ns, 8, 2, 128, 16, seed=41).put()
+    # The limit is looked at between two tries, and a try may itself hold for longer
+    # than the limit: whether a given wait runs out is the machine's affair. What holds
+    # for each call is that it ends, and that one that reports no timeout is right.
+    limit = lib.mis_set_wait_limit_ns(0)
+    try:
+        for ns_ in [0, 100, 300, 500, 700, 900] + list(range(1000, 9000, 500)):
+            lib.mis_set_wait_limit_ns(ns_)
+            b.call()
+            status = lib.mis_get_device_status(b.ws)
+            assert status in (lib.MIS_OK, lib.MIS_ERR_DEVICE_TIMEOUT)
+            if status == lib.MIS_OK:
+                b.check()
+    finally:
+        lib.mis_set_wait_limit_ns(limit)
+    b.call()
+    assert lib.mis_get_device_status(b.ws) == lib.MIS_OK
+    b.check()
+
+
+def test_narrow_and_wide_units_in_turn():
+    """Units of up to 16 rows take their steps in two streams, wider ones in one:
+    the products' places pass from one to the other."""
+    r = np.random.default_rng(42)
+    for seed in range(6):
+        ns = r.choice([1, 2, 3, 4, 5, 6, 7, 8], 9)
+        lens = ns + r.integers(0, 1500, 9)
+        Batch(lens, ns, 8, 2, int(r.choice([64, 128])), 32, seed=seed, max_rows=8).run().check()
+
+
 def random_batch(r, most=4096):
     hkv = int(r.integers(1, 5))
     G = int(r.choice([1, 1, 2, 3, 4, 5, 8, 16, 20]))
