@@ -831,6 +831,21 @@ def _weight(where: str, t, D: int, dev) -> int:
     return t.data_ptr()
 
 
+def _heads_pair(where: str, t, o, dev):
+    """(T, heads, D, addresses and row strides) of [T, heads, D] rows and an output like them."""
+    if not (t.dtype is _BF16 and o.dtype is _BF16 and t.get_device() == dev and o.get_device() == dev):
+        raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
+    sh, st, so = t.shape, t.stride(), o.stride()
+    if len(sh) != 3 or o.shape != sh:
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+    T, H, D = sh
+    if st[2] != 1 or so[2] != 1 or (H > 1 and (st[1] != D or so[1] != D)):
+        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
+    if T <= 1:
+        return T, H, D, t.data_ptr(), o.data_ptr(), H * D, H * D
+    return T, H, D, t.data_ptr(), o.data_ptr(), st[0], so[0]
+
+
 def mis_qk_norm_rope(q, k, q_out, k_out, position_ids=None, q_weight=None, k_weight=None,
                      eps: float = 1.0e-6, base: float = 1.0e6, stream=None):
     """Root mean square norms of the heads of q [T, Hq, D] and k [T, Hkv, D] (each
@@ -842,25 +857,15 @@ def mis_qk_norm_rope(q, k, q_out, k_out, position_ids=None, q_weight=None, k_wei
     dev, st = _here(stream)
     if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (q is None and k is None):
         raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
-    x = q if q is not None else k
-    if len(x.shape) != 3:
-        raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
-    T, _, D = x.shape
-    at, strides, heads = [], [], []
-    for t, o in ((q, q_out), (k, k_out)):
-        if t is None:
-            at += [None, None]
-            strides += [0, 0]
-            heads.append(0)
-            continue
-        if not (t.dtype is _BF16 and o.dtype is _BF16 and t.get_device() == dev and o.get_device() == dev):
-            raise MisError(MIS_ERR_INVALID_ARG, where)  # noqa: F821
-        if len(t.shape) != 3 or t.shape[0] != T or o.shape[0] != T:
+    T, hq, hk, D, qa, qoa, qs, qos = None, 0, 0, None, None, None, 0, 0
+    ka, koa, ks, kos = None, None, 0, 0
+    if q is not None:
+        T, hq, D, qa, qoa, qs, qos = _heads_pair(where, q, q_out, dev)
+    if k is not None:
+        Tk, hk, Dk, ka, koa, ks, kos = _heads_pair(where, k, k_out, dev)
+        if q is not None and (Tk != T or Dk != D):
             raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
-        H = t.shape[1]
-        strides += [_row_stride(where, T, H, D, t), _row_stride(where, T, H, D, o)]
-        at += [t.data_ptr(), o.data_ptr()]
-        heads.append(H)
+        T, D = Tk, Dk
     qw = None if q_weight is None else _weight(where, q_weight, D, dev)
     kw = None if k_weight is None else _weight(where, k_weight, D, dev)
     pos = None
@@ -870,8 +875,7 @@ def mis_qk_norm_rope(q, k, q_out, k_out, position_ids=None, q_weight=None, k_wei
         if position_ids.numel() < T or not position_ids.is_contiguous():
             raise MisError(MIS_ERR_SHAPE, where)  # noqa: F821
         pos = position_ids.data_ptr()
-    st = L.mis_qk_norm_rope(at[0], at[2], at[1], at[3], strides[0], strides[2], strides[1], strides[3], T,
-                            heads[0], heads[1], D, qw, kw, eps, pos, base, st)
+    st = L.mis_qk_norm_rope(qa, ka, qoa, koa, qs, ks, qos, kos, T, hq, hk, D, qw, kw, eps, pos, base, st)
     if st:
         raise MisError(st, where)
 

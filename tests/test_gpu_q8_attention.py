@@ -1,4 +1,6 @@
 """Attention of the newest rows over an 8-bit paged cache, against the oracle."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -271,6 +273,58 @@ def test_narrow_and_wide_units_in_turn():
         ns = r.choice([1, 2, 3, 4, 5, 6, 7, 8], 9)
         lens = ns + r.integers(0, 1500, 9)
         Batch(lens, ns, 8, 2, int(r.choice([64, 128])), 32, seed=seed, max_rows=8).run().check()
+
+
+def test_two_captured_graphs_share_a_workspace():
+    """Replayed in turn on one stream: a narrow call and a wide one over one workspace."""
+    jobs = [Batch([4000, 70], [1, 2], 8, 2, 128, 16, seed=50).put(), Batch([900, 33, 2000], [9, 2, 12], 8, 2, 128, 16, seed=51).put()]
+    ws = max((b.ws for b in jobs), key=lambda w: w.numel())
+    graphs = []
+    for b in jobs:
+        b.ws = ws
+        b.call()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.call()
+        graphs.append(g)
+    for _ in range(3):
+        for b, g in zip(jobs, graphs):
+            b.o.fill_(7.0)
+            b.lse.fill_(7.0)
+            g.replay()
+            assert lib.mis_get_device_status(ws) == lib.MIS_OK
+            b.check()
+
+
+def test_two_host_threads():
+    jobs = [Batch([1500 + 70 * i, 60], [1 + 4 * i, 2], 8, 2, 64, 16, seed=60 + i).put() for i in range(2)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(b):
+        try:
+            st = torch.cuda.Stream()
+            for _ in range(50):
+                b.call(stream=st)
+            st.synchronize()
+        except Exception as e:                             # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(b,)) for b in jobs]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failed
+    for b in jobs:
+        b.check()
+
+
+@pytest.mark.parametrize("ns", [[1, 1, 2], [5, 9, 3]])
+def test_requests_share_pages(ns):
+    """A common prefix: the first pages of every request are the same ones."""
+    b = Batch([700, 500, 360], ns, 8, 2, 128, 32, seed=70)
+    b.table[1:, :10] = b.table[0, :10]
+    b.run().check()
 
 
 def random_batch(r, most=4096):

@@ -284,6 +284,45 @@ def test_bad_slots_and_rows(n):
         assert lib.mis_get_device_status(s) == lib.MIS_OK
 
 
+@pytest.mark.parametrize("n", [40, 9000])
+@pytest.mark.parametrize("bad", ["slot", "row"])
+def test_bad_indices_of_wide_rows(n, bad):
+    """Rows wide enough that one block looks over the indices of any number of them."""
+    n_pages = n // 256 + 2
+    r = np.random.default_rng(6)
+    k = draw(r, n, 4, 128).cuda()
+    for i in (0, n // 2, n - 1):
+        ca, s = Cache(n_pages, 256, 4, 128), ws()
+        slots, rows = np.arange(n), np.arange(n)[::-1].copy()
+        (slots if bad == "slot" else rows)[i] = n_pages * 256 if bad == "slot" else n
+        lib.mis_paged_write_kv_q8(ca.c, k, k, i32(slots), s, src_rows=i32(rows))
+        assert lib.mis_get_device_status(s) == lib.MIS_ERR_DEVICE_INDEX
+        kc, ke, _, _ = ca.rows()
+        good = np.delete(np.arange(n), i)
+        check_exact(kc[good], ke[good], f64(k)[rows[good]])
+        assert (kc[i] == 0x55).all()
+        if bad == "slot":
+            out = torch.full((n, 4, 128), 7.0, dtype=BF16).cuda()
+            lib.mis_paged_read_kv_q8(ca.c, i32(slots), out, out.clone(), s)
+            assert lib.mis_get_device_status(s) == lib.MIS_ERR_DEVICE_INDEX
+            assert (out[i] == 7).all()
+
+
+def test_repeated_rows_and_slots():
+    """One source row at many slots, one slot read many times."""
+    r = np.random.default_rng(7)
+    x, ca, s = draw(r, 5, 3, 64), Cache(8, 16, 3, 64), ws()
+    rows = r.integers(0, 5, 100)
+    lib.mis_paged_write_kv_q8(ca.c, x.cuda(), x.cuda(), i32(np.arange(100)), s, src_rows=i32(rows))
+    slots = r.integers(0, 100, 500)
+    k, v = (torch.empty(500, 3, 64, dtype=BF16, device="cuda") for _ in range(2))
+    lib.mis_paged_read_kv_q8(ca.c, i32(slots), k, v, s)
+    assert lib.mis_get_device_status(s) == lib.MIS_OK
+    e = Q.exponent(f64(x))
+    held = Q.values(Q.codes(f64(x), e), e + 127)[rows][slots]
+    assert np.array_equal(f64(k), held) and np.array_equal(f64(v), held)
+
+
 def test_slots_past_four_gigabytes():
     """A cache whose byte offsets pass 32 bits: rows at its far end, stored, read and attended."""
     n_pages, page, hkv, D = 1100, 256, 128, 128                  # 4.6 GB a buffer

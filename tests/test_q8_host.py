@@ -146,6 +146,14 @@ def test_attention(L, kw, st):
     assert attn(L, **kw) == st
 
 
+def test_attention_of_more_steps_than_are_counted(L):
+    """(16-row pages: 2^27 - 16 of them make 16,777,214 steps of 128 rows, which count 5 each.)"""
+    pages = (0x7fffff00 // 16)
+    kw = dict(max_pages=pages, stride=pages, table=1 << 44)
+    assert attn(L, d=dict(B=13), **kw) == UNSUP            # 13 requests x 2 kv heads
+    assert attn(L, d=dict(B=13), **dict(kw, max_pages=pages + 16, stride=pages + 16)) == SHAPE
+
+
 @pytest.mark.parametrize("kw,st", [
     (dict(T=-1), ARG), (dict(Hq=-1), ARG), (dict(Hq=0, Hkv=0), ARG), (dict(D=32), UNSUP), (dict(Hq=65537, qs=1 << 23, qos=1 << 23), UNSUP),
     (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG), (dict(base=0.5), ARG), (dict(base=float("inf")), ARG), (dict(qs=248), SHAPE),
