@@ -689,10 +689,17 @@ mis_status_t mis_paged_read_kv_q8(const mis_paged_cache_q8* cache, const int32_t
  * that sees nothing then gets o = 0 and lse = -inf.
  * o, lse and the workspace overlap no input, the cache among them, nor each
  * other (MIS_ERR_INVALID_ARG; o may be columns of a buffer whose other columns
- * are q, at one row stride). fp32 scores, statistics and accumulation;
- * probabilities are rounded to 11 bits for the second product, o to bf16. The
- * same call gives the same bits. Two kernels, which wait on nothing but their
- * stream. Workspace: device, 256-byte aligned, >=
+ * are q, at one row stride). fp32 scores, statistics and accumulation. Elements
+ * of q count as they are down to 2^-14 of their row's largest, and to within
+ * 2^-22 of it below that; a key's weight (its probability times the scale of its
+ * value row) is rounded to 11 bits, and to within 2^-24 of the row's largest
+ * weight where it is below 2^-17 of that; o is rounded to bf16. The same call
+ * gives the same bits. Two kernels. A wait inside the first can last as long as
+ * a block works on one request, about 1 us per 128 cached rows (see
+ * mis_set_wait_limit_ns()); one that runs out leaves rows that its block has a
+ * part in unwritten. MIS_ERR_UNSUPPORTED also where the steps of 128 rows that
+ * B requests of max_pages pages and max_rows rows can make pass 32 bits.
+ * Workspace: device, 256-byte aligned, >=
  * mis_paged_attention_q8_workspace_size() (0 for an invalid descriptor); one
  * call at a time may use it. */
 #define MIS_PAGED_MAX_ROWS 256
@@ -711,7 +718,7 @@ mis_status_t mis_paged_attention_q8_fwd(const mis_paged_attn_desc* desc, const m
 
 /* ------------------------------------------------------------------------
  * Device status of the last call that used `workspace` (a plan workspace, or
- * one of scoring, of the paged cache or of tree attention). Synchronises
+ * one of scoring, of a paged cache, or of tree or paged attention). Synchronises
  * `stream`, then returns MIS_OK, MIS_ERR_DEVICE_TIMEOUT, MIS_ERR_DEVICE_INDEX
  * or MIS_ERR_DEVICE_PAGES, the first of these that applies. Each call that
  * enqueues work sets the word anew.

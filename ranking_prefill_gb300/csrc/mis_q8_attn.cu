@@ -15,11 +15,19 @@
 // units of a power of two of each row: exact for bf16 elements down to 2^-14 of
 // the row's largest, within 2^-22 of that below. P is rounded to fp16 (11 bits)
 // and split into 4 bits, 16 times the next 4, 256 times the last 3: exact, but
-// that weights below 2^-17 of the largest lose bits, to within 2^-25 of it. The
+// that weights below 2^-17 of the largest lose bits, to within 2^-24 of it. The
 // parts' products stand in columns of their own and are added when they are read.
-// (V converted to fp16 by a warpgroup of its own, P in one part: 64 decoded
-// tokens 74 us. By mma.sync with K and V converted in registers: 73 us, and
-// three times that for 64 rows a kv head.)
+// (64 decoded tokens over 512 to 4096 rows take 54 to 61 us this way, 4 requests
+// of 117K rows 174. V converted to fp16 by a warpgroup of its own, P in one part:
+// 74 and 224. mma.sync with K and V converted in registers: 73 and 270.)
+//
+// What bounds it: the K/V stream in long caches (5.5 TB/s of 6.8 at 117K rows, 4.7
+// at 64 x 2.2K, which loses 6 us before the first product and 5 in the join); the
+// softmax of a step where a unit has more than 16 rows (1,750 cycles for 32 KB of
+// K and V: 32 requests of 32 rows a kv head 100 us, their stream 21); what a unit
+// takes to begin and end where it has a few steps (256 requests of 100 to 600 rows
+// 76 us, their stream 27); the chain of one step and the second launch in small
+// batches (4 requests of 100 to 300 rows 11.5 us).
 //
 // A row's key scale multiplies its score, its value scale its probability. The
 // softmax keeps two things per row: a reference r below which weights are
@@ -92,7 +100,10 @@ struct AttnParams {
 // What steps and units count in a block's share, so that shares take alike: a
 // step in two streams kStep, one of more rows than that kWide; a unit what its
 // beginning and end take besides, where blocks have some steps each (in small
-// batches the longest share is what counts, and that is one step).
+// batches the longest share is what counts, and that is one step: 1 to 2 us more
+// with it). 4 long requests of 12 to 32 rows a kv head: 177 us, with kWide = kStep
+// 200 (requests of 64 rows alone, whose shares that leaves the same size, 100 and
+// 96). kUnit = 12 and 0: 256 short requests 76 and 90, 32 of 64 rows 100 and 124.
 constexpr int kStep = 4, kWide = 5, kUnit = 12;
 
 // A request's work: units of N of a kv head's n * G rows, the tiles of a head
@@ -1087,7 +1098,8 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 
 // Joins the pieces of a unit that several blocks hold, in block order: block
 // (c, y) takes rows of the unit that starts in block c, a row by `share` of its
-// four warps, which take the pieces in turn. What it needs lies in one place,
+// four warps, which take the pieces in turn (all four where rows are few: one
+// request of 8192 rows, 2 a kv head, 13.5 us, by one warp 15.8; 16 rows 38.8 and 37.2). What it needs lies in one place,
 // since its time is that of the trips to L2 it makes one behind the other (units
 // found by bisection of the requests' steps: 10 us for 64 decoded tokens), and
 // that of its blocks' launch, which the attention's registers leave no room for
@@ -1210,7 +1222,9 @@ mis_status_t check_desc(const mis_paged_attn_desc* d, const mis_paged_cache_q8* 
 int head_rows(const mis_paged_attn_desc* d, const mis_paged_cache_q8* c) { return d->max_rows * (d->Hq / c->Hkv); }
 
 // Rows of a unit. More than 32 rows of a kv head are several units over the same
-// keys.
+// keys. Units of 16 and of 32: 64 requests of 16 rows 37.2 and 39.4 us, 256 short
+// ones of 2 rows 76 and 94; 32 of 32 rows a kv head 109 and 100 (4 long ones, of
+// which one has 32 rows and the others fewer than 17, 171 and 177).
 int unit_rows(const mis_paged_attn_desc* d, const mis_paged_cache_q8* c) { return head_rows(d, c) <= 16 ? 16 : 32; }
 
 struct AttnWs { size_t flags, meta, rl, part, total; };
