@@ -14,8 +14,8 @@
 // what gets split. Q's parts are its leading 4 bits and 32 times the rest, in
 // units of a power of two of each row: exact for bf16 elements down to 2^-14 of
 // the row's largest, within 2^-22 of that below. P is rounded to fp16 (11 bits)
-// and split into 4 bits, 16 times the next 4, 256 times the last 3: exact, but
-// that weights below 2^-17 of the largest lose bits, to within 2^-24 of it. The
+// and split into 4 bits, 16 times the next 4, 1024 times the last 3: exact, but
+// that weights below 2^-13 of the largest lose bits, to within 2^-24 of it. The
 // parts' products stand in columns of their own and are added when they are read.
 // (64 decoded tokens over 512 to 4096 rows take 54 to 61 us this way, 4 requests
 // of 117K rows 174. V converted to fp16 by a warpgroup of its own, P in one part:
@@ -31,10 +31,11 @@
 //
 // A row's key scale multiplies its score, its value scale its probability. The
 // softmax keeps two things per row: a reference r below which weights are
-// taken, and l = sum 2^(s - r). Products use P = 2^(s - r + e_v - 26): r is the
-// largest s + e_v - 32 seen, moved only when one passes it by 2^2.5, so P lies
-// below e4m3's 448 and its largest above 2^6, whatever the spread of the value
-// scales; 2^(s - r) stays within fp32 for every e_v in [-56, 120].
+// taken, and l = sum 2^(s - r). Products use P = 2^(s - r + e_v - 28): r is the
+// largest s + e_v - 32 seen, moved only when one passes it by 2^4, so P stays below
+// 2^8 (where 16 and 64 times the rests stay within e4m3) and its largest above 2^4,
+// whatever the spread of the value scales; 2^(s - r) stays within fp32 for every e_v
+// in [-56, 120].
 //
 // Work is cut evenly between blocks, not at requests: every block adds up the
 // 128-key steps of all units (request, kv head, row tile) from the lengths on
@@ -247,11 +248,11 @@ __device__ __forceinline__ uint16_t e4m3x2_of_half2(uint32_t h) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
   return c;
 }
-// 16 (p - c), for the codes c of p: exact.
-__device__ __forceinline__ uint32_t rest16(uint32_t p, uint16_t codes) {
+// times (p - c), for the codes c of p: exact.
+__device__ __forceinline__ uint32_t rest(uint32_t p, uint16_t codes, uint32_t times) {
   uint32_t d;
   asm("{.reg .b32 t; sub.rn.f16x2 t, %1, %2; mul.rn.f16x2 %0, t, %3;}"
-      : "=r"(d) : "r"(p), "r"(e4m3x2_to_half2(codes)), "r"(0x4c004c00u));
+      : "=r"(d) : "r"(p), "r"(e4m3x2_to_half2(codes)), "r"(times));
   return d;
 }
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
@@ -776,7 +777,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           const uint32_t hide = *reinterpret_cast<const uint32_t*>(e + 256);
           const float kf = pow2(q8_exp(e[r]));
           const int ev = q8_exp(e[128 + r]);
-          const float vs = pow2(ev - 26), most = 34.5f - (float)ev;
+          const float vs = pow2(ev - 28), most = 36.f - (float)ev;
           const int key = k * kKeys + r;
           if (ok) {
             tmem_ld_wait();
@@ -885,9 +886,9 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
               f2_unpack(f2_mul(w2, v2), p0, p1);
               const uint32_t h = half2_of(p0, p1);
               const uint16_t a = e4m3x2_of_half2(h);
-              const uint32_t h1 = rest16(h, a);
+              const uint32_t h1 = rest(h, a, 0x4c004c00u);          // 16
               const uint16_t b = e4m3x2_of_half2(h1);
-              const uint16_t c = e4m3x2_of_half2(rest16(h1, b));
+              const uint16_t c = e4m3x2_of_half2(rest(h1, b, 0x54005400u));     // 64
               (y ? hi : lo)[0] = a;
               (y ? hi : lo)[1] = b;
               (y ? hi : lo)[2] = c;
@@ -972,8 +973,8 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           const float a0 = ex2(r0 - mx), a1 = ex2(r1 - mx);
           sum = a0 * ((l0[0] + l0[N]) + (l0[2 * N] + l0[3 * N]));
           if (two) sum += a1 * ((l1[0] + l1[N]) + (l1[2 * N] + l1[3 * N]));
-          // the products' weights carry 2^-26; NaN stays
-          const float inv = whole ? (sum != 0.f ? 67108864.f / sum : 0.f) : 1.f;
+          // the products' weights carry 2^-28; NaN stays
+          const float inv = whole ? (sum != 0.f ? 268435456.f / sum : 0.f) : 1.f;
           wt[lane] = a0 * inv;
           wt[N + lane] = a1 * inv;
         }
@@ -1026,7 +1027,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           auto add = [&](int stream) {
 #pragma unroll
             for (int n = 0; n < CH; ++n) {
-              const float x = fmaf(__uint_as_float(y[stream][2][n]), 0.00390625f,
+              const float x = fmaf(__uint_as_float(y[stream][2][n]), 0.0009765625f,
                                    fmaf(__uint_as_float(y[stream][1][n]), 0.0625f, __uint_as_float(y[stream][0][n])));
               ov[n] = fmaf(wt[stream * N + e0 + q + n], x, ov[n]);
             }
@@ -1190,8 +1191,8 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
   }
   if (!live) return;
   const int i = (u.w + n) / p.G, head = u.z * p.G + u.w + n - i * p.G;
-  // the products' weights carry 2^-26
-  const float inv = sum != 0.f ? 67108864.f / sum : 0.f;
+  // the products' weights carry 2^-28
+  const float inv = sum != 0.f ? 268435456.f / sum : 0.f;
   uint32_t out[E / 2];
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) out[e] = sum != 0.f ? pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv) : 0u;
