@@ -204,7 +204,7 @@ struct Walk {
   __device__ __forceinline__ int head() const { return j.tiles == 1 ? u : (int)((uint32_t)u / (uint32_t)j.tiles); }
   __device__ __forceinline__ int row0(int h) const { return (u - h * j.tiles) * N; }   // of the kv head's rows
   // keys that every row of the unit sees
-  __device__ __forceinline__ int all_see(const AttnParams& p, int first) const { return j.len - j.n + first / p.G + 1; }
+  __device__ __forceinline__ int all_see(const AttnParams& p, int first) const { return j.len - j.n + (first ? first / p.G : 0) + 1; }
 };
 
 // A bounded wait in few instructions: one that runs out, or sees that another
@@ -800,9 +800,15 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           const bool plain = k * kKeys + kKeys <= see && !hide;
           const bool gone_key = key >= len || ((hide >> (r >> box_shift)) & 1u);
           if (!plain) {
+            const int seen = gone_key ? 0x7fffffff : key;
 #pragma unroll
-            for (int n = 0; n < 16; ++n)
-              if (gone_key || key >= lim[n]) s[n] = 0xff800000u;
+            for (int n = 0; n < 16; n += 4) {
+              const int4 m = *reinterpret_cast<const int4*>(lim + n);
+              if (seen >= m.x) s[n] = 0xff800000u;
+              if (seen >= m.y) s[n + 1] = 0xff800000u;
+              if (seen >= m.z) s[n + 2] = 0xff800000u;
+              if (seen >= m.w) s[n + 3] = 0xff800000u;
+            }
           }
           auto weigh = [&] {                           // x = s * kf - r
             const uint64_t k2 = f2_pack(__float_as_uint(kf), __float_as_uint(kf));
@@ -907,20 +913,26 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
               const int sv = t % VS;
               ok = spin(bar(bVF + sv), (t / VS) & 1, W, 0x750);
               const uint32_t row = base + C::oV + sv * C::kCodes;
-#pragma unroll 1
-              for (int c = 0; c < D / 16 && ok; ++c) {
-                const uint32_t at = row + chunk_at<D>(r, c);
-                uint4 u = lds16(at);
-                uint32_t* y = reinterpret_cast<uint32_t*>(&u);
-                uint32_t any = 0;
+              if (gone_key) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const uint32_t nn = nan_codes(y[q]);
-                  any |= nn;
-                  y[q] = gone_key ? 0u : y[q] & ~((nn >> 7) * 0xffu);
+                for (int c = 0; c < D / 16; ++c)
+                  if (ok) st_shared_v4(row + chunk_at<D>(r, c), 0u, 0u, 0u, 0u);
+              } else {
+#pragma unroll 1
+                for (int c = 0; c < D / 16 && ok; ++c) {
+                  const uint32_t at = row + chunk_at<D>(r, c);
+                  uint4 u = lds16(at);
+                  uint32_t* y = reinterpret_cast<uint32_t*>(&u);
+                  uint32_t any = 0;
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    const uint32_t nn = nan_codes(y[q]);
+                    any |= nn;
+                    y[q] &= ~((nn >> 7) * 0xffu);
+                  }
+                  if (any) st_shared_v4(at, u.x, u.y, u.z, u.w);
+                  nan |= any != 0;
                 }
-                if (gone_key || any) st_shared_v4(at, u.x, u.y, u.z, u.w);
-                nan |= any && !gone_key;
               }
             }
             ok = __all_sync(0xffffffffu, ok);
