@@ -971,6 +971,12 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       while (more) {
         const int slot = lu & 1, h = w.head(), first = w.row0(h), rows = min(N, w.j.n * p.G - first);
         const bool whole = w.k0 == 0 && w.k1 == w.j.steps, two = two_streams(rows);
+        if (sw == 0 && lane == 0 && !whole && w.k0 == 0) {
+          // the block that holds its last step; while there is nothing else to do
+          const int c = share.holder(share.from + share.size - w.left + w.ahead() - 1);
+          p.meta[2 * blockIdx.x] = make_int4(c - (int)blockIdx.x + 1, rows, h, first);
+          p.meta[2 * blockIdx.x + 1] = make_int4(w.j.row0, lu ? 1 : 0, 0, 0);
+        }
         ok = spin_all(bar(bST + slot), (lu >> 1) & 1, W, 0x800);
         if (!ok) break;
         const int piece = 2 * blockIdx.x + (lu ? 1 : 0), sq = lu % QS;
@@ -986,15 +992,9 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           sum = a0 * ((l0[0] + l0[N]) + (l0[2 * N] + l0[3 * N]));
           if (two) sum += a1 * ((l1[0] + l1[N]) + (l1[2 * N] + l1[3 * N]));
           // the products' weights carry 2^-28; NaN stays
-          const float inv = whole ? (sum != 0.f ? 268435456.f / sum : 0.f) : 1.f;
+          const float inv = whole ? (sum != 0.f ? __fdividef(268435456.f, sum) : 0.f) : 1.f;
           wt[lane] = a0 * inv;
           wt[N + lane] = a1 * inv;
-        }
-        if (sw == 0 && lane == 0 && !whole && w.k0 == 0) {
-          // the block that holds its last step
-          const int c = share.holder(share.from + share.size - w.left + w.ahead() - 1);
-          p.meta[2 * blockIdx.x] = make_int4(c - (int)blockIdx.x + 1, rows, h, first);
-          p.meta[2 * blockIdx.x + 1] = make_int4(w.j.row0, lu ? 1 : 0, 0, 0);
         }
         const int* at = reinterpret_cast<const int*>(words) + C::wAt + sq * N;
         const int* lim = reinterpret_cast<const int*>(words) + C::wLim + sq * N;
@@ -1003,7 +1003,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             p.rl[(int64_t)piece * N + lane] = make_float2(mx, sum);
           else if (p.lse)
             p.lse[(int64_t)(h * p.G + (at[lane] & 255)) * p.T + w.j.row0 + (at[lane] >> 8)] =
-                sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+                sum != 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
         }
         __syncwarp();
         ok = spin_all(bar(bOF + slot), (lu >> 1) & 1, W, 0x810);
@@ -1204,7 +1204,7 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
   if (!live) return;
   const int i = (u.w + n) / p.G, head = u.z * p.G + u.w + n - i * p.G;
   // the products' weights carry 2^-28
-  const float inv = sum != 0.f ? 268435456.f / sum : 0.f;
+  const float inv = sum != 0.f ? __fdividef(268435456.f, sum) : 0.f;
   uint32_t out[E / 2];
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) out[e] = sum != 0.f ? pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv) : 0u;
@@ -1212,7 +1212,7 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
   if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
   else *reinterpret_cast<uint32_t*>(dst) = out[0];
   if (p.lse && lane == 0)
-    p.lse[(int64_t)head * p.T + v.x + i] = sum != 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+    p.lse[(int64_t)head * p.T + v.x + i] = sum != 0.f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
