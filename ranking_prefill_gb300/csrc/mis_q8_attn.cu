@@ -105,18 +105,18 @@ struct AttnParams {
 // with it). 4 long requests of 12 to 32 rows a kv head: 177 us, with kWide = kStep
 // 200 (requests of 64 rows alone, whose shares that leaves the same size, 100 and
 // 96). kUnit = 12 and 0: 256 short requests 76 and 90, 32 of 64 rows 100 and 124.
-constexpr int kStep = 4, kWide = 5, kUnit = 12;
+constexpr int kStep = 4, kWide = 5, kUnit = 8, kUnitWide = 20;
 
 // A request's work: units of N of a kv head's n * G rows, the tiles of a head
 // side by side.
 struct Job {
   int len, row0, n;                    // cached rows; first new row, new rows
   int steps, tiles, units;             // 128-key steps of a unit
-  int step;                            // what one counts
+  int step, own;                       // what one counts, and a unit besides
   bool ok;
-  // what it counts, and a unit of it; the host bounds the sum
-  __device__ __forceinline__ int unit(int own) const { return steps * step + own; }
-  __device__ __forceinline__ int cost(int own) const { return unit(own) * units; }
+  // what a unit counts, and all of them; the host bounds the sum
+  __device__ __forceinline__ int unit() const { return steps * step + own; }
+  __device__ __forceinline__ int cost() const { return unit() * units; }
 };
 
 // What a request brings, as read.
@@ -125,7 +125,7 @@ __device__ __forceinline__ Given given(const AttnParams& p, int b) {
   return b < p.B ? Given{p.cache_len[b], p.cu[b], p.cu[b + 1]} : Given{0, 0, 0};
 }
 template <int N>
-__device__ __forceinline__ Job job_of(const AttnParams& p, const Given& g) {
+__device__ __forceinline__ Job job_of(const AttnParams& p, const Given& g, bool big) {
   Job j;
   j.len = g.len;
   j.row0 = g.row0;
@@ -135,11 +135,11 @@ __device__ __forceinline__ Job job_of(const AttnParams& p, const Given& g) {
   j.steps = (uint32_t)(j.len + kKeys - 1) / kKeys;
   j.tiles = (uint32_t)(j.n * p.G + N - 1) / N;
   j.units = j.tiles * p.Hkv;
-  j.step = N == 16 || j.n * p.G <= 16 ? kStep : kWide;
+  const bool wide = N > 16 && j.n * p.G > 16;
+  j.step = big && wide ? kWide : kStep;
+  j.own = big ? (wide ? kUnitWide : kUnit) : 0;
   return j;
 }
-template <int N>
-__device__ __forceinline__ Job job_of(const AttnParams& p, int b) { return job_of<N>(p, given(p, b)); }
 
 // A block's share: [from, from + size) of all units laid end to end; blocks
 // [0, rem) take quo + 1, the others quo. So few take part that a share holds a
@@ -163,21 +163,22 @@ struct Share {
 // that holds the last of what it counts.
 template <int N>
 struct Walk {
-  int left, off, own;                  // of the share from this piece on; of the unit before it; a unit's own
+  int left, off;                       // of the share from this piece on; of the unit before it
+  bool big;
   int b, u;                            // request, its unit
   int k0, k1;                          // steps of the piece
   Job j;
   Given g;                             // of the request behind, asked for ahead of its turn
 
   // the first piece; false where the share has none
-  __device__ __forceinline__ bool enter(const AttnParams& p, int b_, int from, int share, int own_) {
+  __device__ __forceinline__ bool enter(const AttnParams& p, int b_, int from, int share, bool big_) {
     b = b_;
     left = share;
-    own = own_;
-    j = job_of<N>(p, b);
+    big = big_;
+    j = job_of<N>(p, given(p, b), big);
     g = given(p, b + 1);
-    u = (uint32_t)from / (uint32_t)j.unit(own);
-    off = from - u * j.unit(own);
+    u = (uint32_t)from / (uint32_t)j.unit();
+    off = from - u * j.unit();
     k0 = (uint32_t)off / (uint32_t)j.step;
     if (k0 >= j.steps) return next(p);
     k1 = min(j.steps, (int)((uint32_t)(off + left) / (uint32_t)j.step));
@@ -185,13 +186,13 @@ struct Walk {
   }
   // the next piece; false at the end of the share
   __device__ __forceinline__ bool next(const AttnParams& p) {
-    left -= j.unit(own) - off;
+    left -= j.unit() - off;
     if (left < kStep) return false;
     off = 0;
     if (++u == j.units) {
       u = 0;
       do {
-        j = job_of<N>(p, g);
+        j = job_of<N>(p, g, big);
         g = given(p, ++b + 1);
       } while (j.units == 0);
     }
@@ -398,40 +399,40 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   // finds the request that its share starts in.
   const int run = (p.B + C::kThreads - 1) / C::kThreads;
   const int rb0 = min(p.B, tid * run), rb1 = min(p.B, rb0 + run);
-  int mine = 0, units = 0;             // steps' counts, units
+  int mine = 0, mineb = 0;             // what they count in a small batch and in a big one
   bool bad = false;
   for (int b = rb0; b < rb1; ++b) {
-    const Job j = job_of<N>(p, b);
+    const Given g = given(p, b);
+    const Job j = job_of<N>(p, g, false);
     bad |= !j.ok;
-    mine += j.cost(0);
-    units += j.units;
+    mine += j.cost();
+    mineb += job_of<N>(p, g, true).cost();
   }
-  int upto = mine, uptou = units;
+  int upto = mine, uptob = mineb;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, upto, o), y = __shfl_up_sync(0xffffffffu, uptou, o);
-    if (lane >= o) { upto += x; uptou += y; }
+    const int x = __shfl_up_sync(0xffffffffu, upto, o), y = __shfl_up_sync(0xffffffffu, uptob, o);
+    if (lane >= o) { upto += x; uptob += y; }
   }
-  if (lane == 31) s_sum[warp] = make_int2(upto, uptou);
+  if (lane == 31) s_sum[warp] = make_int2(upto, uptob);
   tc_fence_before();
   bad = __syncthreads_or(bad);
   tc_fence_after();
-  int total = 0, totalu = 0;
+  int total = 0, totalb = 0;
 #pragma unroll
   for (int w = 0; w < C::kThreads / 32; ++w) {
-    if (w < warp) { upto += s_sum[w].x; uptou += s_sum[w].y; }
+    if (w < warp) { upto += s_sum[w].x; uptob += s_sum[w].y; }
     total += s_sum[w].x;
-    totalu += s_sum[w].y;
+    totalb += s_sum[w].y;
   }
-  const int own = total >= 8 * kStep * p.blocks ? kUnit : 0;
-  const Share share(total + own * totalu, p.blocks, blockIdx.x, (N == 16 ? kStep : kWide) + own);
+  const bool big = total >= 8 * kStep * p.blocks;
+  const Share share(big ? totalb : total, p.blocks, blockIdx.x, !big ? kStep : N == 16 ? kStep + kUnit : kWide + kUnitWide);
   if (tid == 0) p.meta[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
-  upto += own * uptou;
-  mine += own * units;
+  if (big) { upto = uptob; mine = mineb; }
   if (share.size > 0 && share.from >= upto - mine && share.from < upto) {
     int at = upto - mine;
     for (int b = rb0; b < rb1; ++b) {
-      const int next = at + job_of<N>(p, b).cost(own);
+      const int next = at + job_of<N>(p, given(p, b), big).cost();
       if (share.from >= at && share.from < next) { s_req = b; s_from = share.from - at; }
       at = next;
     }
@@ -447,7 +448,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   auto two_streams = [](int rows) { return N == 16 || rows <= 16; };
 
   Walk<N> w;
-  if (share.size > 0 && w.enter(p, s_req, s_from, share.size, own)) {
+  if (share.size > 0 && w.enter(p, s_req, s_from, share.size, big)) {
     if (warp == 0 || warp == 3) {
       // ------------------------------------------------- copies of K (V): a lane a box of a page
       const bool y = warp == 3;
@@ -1313,7 +1314,7 @@ extern "C" mis_status_t mis_paged_attention_q8_fwd(
   }
   // what steps and units count is counted in 32 bits
   const double tiles = (double)((head_rows(desc, cache) + 15) / 16) * cache->Hkv;
-  if ((((double)max_pages * cache->page_size / kKeys + 1) * kWide + kUnit) * tiles * desc->B >= 2147483648.0) return MIS_ERR_UNSUPPORTED;
+  if ((((double)max_pages * cache->page_size / kKeys + 1) * kWide + kUnitWide) * tiles * desc->B >= 2147483648.0) return MIS_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (desc->T == 0) return cudaMemsetAsync(workspace, 0, 8, st) == cudaSuccess ? MIS_OK : MIS_ERR_CUDA;
   uint8_t* base = static_cast<uint8_t*>(workspace);
