@@ -314,7 +314,7 @@ template <int D, int N>
 struct Cfg {
   static constexpr int kThreads = 512;
   static constexpr int kCodes = kKeys * D;             // a tile of codes
-  static constexpr int kK = D == 128 ? 5 : 8, kV = D == 64 ? 8 : N == 16 ? 6 : 5;     // stages
+  static constexpr int kK = D == 128 ? 4 : 8, kV = kK;    // stages: 64 KB of each
   static constexpr int kQS = N == 16 ? 4 : 2;          // units of Q
   static constexpr int kQ = 2 * N * D;                 // both parts of a unit's rows
   static constexpr int kPW = N == 16 ? 64 : 128;       // bytes of a key's row of P (3N used)
