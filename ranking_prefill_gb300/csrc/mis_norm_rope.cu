@@ -9,8 +9,9 @@
 // read and written once, so HBM bounds it. D / 16 lanes share a head: a lane
 // holds 8 pairs, so the mean takes 2 or 3 exchanges and the rotation none. The
 // angles of a lane's 8 pairs serve every head that its thread takes. 128K tokens
-// of 24 heads, 128 wide, take 254 us (6.3 TB/s of the 6.8 that a copy reaches), one
-// head at a time 314; 4,099 of 16 heads, 64 wide, 7.2 us; 32 tokens 3.0, a launch.
+// of 24 heads, 128 wide, take 241 us (6.7 TB/s of the 6.8 that a copy reaches),
+// without the next heads' way to L2 254, one head at a time 314; 4,099 of 16 heads,
+// 64 wide, 7.2 us; 32 tokens 3.0, a launch.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -70,6 +71,14 @@ mis_qk_norm_rope_kernel(const __grid_constant__ NormParams p) {
       b[i] = ld_row16(at + HALF);
     }
   };
+  // the U heads from h on come to L2, a lane a line of 128 bytes: loads of the
+  // next ones in registers would cost half the blocks
+  auto ahead = [&](int h) {
+    constexpr int LH = D / 64, W = NC / LH;
+    const int x = h + c / LH;
+    const __nv_bfloat16* at = (x < p.Hq ? p.q + t * p.qs : p.k + t * p.ks - (int64_t)p.Hq * D) + (int64_t)x * D + (c % LH) * 64;
+    if (x < h1 && c / LH < U) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+  };
   if (U == 2) load(h0);
   float sn[8], cs[8];
   if (p.pos) {
@@ -87,6 +96,7 @@ mis_qk_norm_rope_kernel(const __grid_constant__ NormParams p) {
 #pragma unroll 1
     for (int h = g0; h < g1; h += U) {
       if (U != 2 || h != h0) load(h);
+      if (h + U < h1) ahead(h + U);
       float x[U][8], y[U][8];
 #pragma unroll
       for (int i = 0; i < U; ++i) {

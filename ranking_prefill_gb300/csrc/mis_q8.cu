@@ -11,7 +11,7 @@
 // Both kernels touch every byte once, so HBM bounds them: D / 16 lanes share a
 // row of a head in the store (maximum and mean in 2 or 3 exchanges, as the
 // rotation's pairs lie in a lane), and D / 16 lanes read one back. 128K rows of 8
-// heads, 128 wide, are stored in 158 us and read back in 136 (5.1 and 5.9 TB/s of
+// heads, 128 wide, are stored in 146 us and read back in 135 (5.5 and 6.0 TB/s of
 // the 6.8 that a copy reaches); a few rows cost a launch, 2.3 to 2.9 us. Narrow rows
 // are bound by their angles: 128K rows of one head 42 us both ways, their bytes 15.
 #include <cuda_runtime.h>
@@ -130,9 +130,10 @@ __device__ __forceinline__ void put_row(const float* x, const float* y, float m,
 }
 
 // U heads of a row at a time: nothing of one waits for another. Two where a thread
-// has more than one, stored and read back: 128K rows of 8 x 128 292 us, one at a
-// time 317; one where it has one: 32 rows 4.7 us and 5.1, 128K rows of 1 x 64 42
-// and 47. Blocks of 128: 292 us, of 256 299 to 307 (more of them stay resident).
+// has more than one, stored and read back: 128K rows of 8 x 128 290 us, one at a
+// time 317 (before the lines that are asked for ahead: 278); one where it has one:
+// 32 rows 4.7 us and 5.1, 128K rows of 1 x 64 42 and 47. Blocks of 128: 292 us, of
+// 256 299 to 307 (more of them stay resident).
 template <int D, int U>
 __global__ void __launch_bounds__(kStoreThreads, 4)
 mis_paged_write_q8_kernel(const __grid_constant__ StoreParams p) {
@@ -172,6 +173,15 @@ mis_paged_write_q8_kernel(const __grid_constant__ StoreParams p) {
       vb[j] = ld_row16(vs + from + HALF);
     }
   };
+  // heads h and h + 1 of K and V come to L2, a lane a line of 128 bytes (128K rows
+  // of 8 x 128 are stored in 146 us, without that in 158)
+  auto ahead = [&](int h) {
+    constexpr int LH = D / 64;
+    const int x = h + c / (2 * LH);
+    const __nv_bfloat16* at = ((c / LH) & 1 ? p.v + (int64_t)r * p.vs : p.k + (int64_t)r * p.ks) + (int64_t)x * D + (c % LH) * 64;
+    if (x < h1) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+  };
+  if (U == 2) ahead(h0 + U);
   if (U == 1) load(h0);                          // in flight while the angles are taken
   float sn[8], cs[8], wx[8], wy[8];
   if (p.pos) {
@@ -186,6 +196,7 @@ mis_paged_write_q8_kernel(const __grid_constant__ StoreParams p) {
 #pragma unroll 1
   for (int hh = h0; hh < h1; hh += U) {
     if (U != 1 || hh != h0) load(hh);
+    if (U == 2 && hh + 2 * U < h1) ahead(hh + 2 * U);
     float x[U][8], y[U][8], m[2 * U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
