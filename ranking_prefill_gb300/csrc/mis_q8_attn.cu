@@ -17,17 +17,19 @@
 // and split into 4 bits, 16 times the next 4, 1024 times the last 3: exact, but
 // that weights below 2^-13 of the largest lose bits, to within 2^-24 of it. The
 // parts' products stand in columns of their own and are added when they are read.
-// (64 decoded tokens over 512 to 4096 rows take 54 to 61 us this way, 4 requests
-// of 117K rows 174. V converted to fp16 by a warpgroup of its own, P in one part:
-// 74 and 224. mma.sync with K and V converted in registers: 73 and 270.)
+// (V converted to fp16 by a warpgroup of its own and P in one part took 64 decoded
+// tokens over 512 to 4096 rows 74 us and 4 requests of 117K rows 224; mma.sync with
+// K and V converted in registers 73 and 270; this form took 57 and 178 before the
+// steps noted below, 51 to 55 and 161 to 170 with them, by the GPU.)
 //
-// What bounds it: the K/V stream in long caches (5.5 TB/s of 6.8 at 117K rows, 4.7
-// at 64 x 2.2K, which loses 6 us before the first product and 5 in the join); the
-// softmax of a step where a unit has more than 16 rows (1,750 cycles for 32 KB of
-// K and V: 32 requests of 32 rows a kv head 100 us, their stream 21); what a unit
-// takes to begin and end where it has a few steps (256 requests of 100 to 600 rows
-// 76 us, their stream 27); the chain of one step and the second launch in small
-// batches (4 requests of 100 to 300 rows 11.5 us).
+// What bounds it: the K/V stream in long caches (4 single tokens over 65K to 131K
+// rows 146 to 166 us, 5.8 to 6.6 TB/s where a copy reaches 6.8; 5.1 to 5.5 at 64 x
+// 2.2K rows, which lose 6 us before the first product and 5 in the join); the
+// softmax's chain of a step where a unit has more than 16 rows (1,700 cycles for the
+// 32 KB of K and V that HBM brings in 1,440: 32 requests of 64 rows a kv head 85 us,
+// their stream 21); what a unit takes to begin and end where it has a few steps (256
+// requests of 100 to 600 rows 67 us, their stream 27); the chain of one step and the
+// second launch in small batches (4 requests of 100 to 300 rows 10.2 us).
 //
 // A row's key scale multiplies its score, its value scale its probability. The
 // softmax keeps two things per row: a reference r below which weights are
@@ -67,7 +69,9 @@ using namespace dev;
 
 constexpr int kKeys = 128;             // of a step
 constexpr int kJoinWarps = 4;
-constexpr int kAhead = 4;              // steps whose scores may be out: as many places of S
+// Steps whose scores may be out, as many places of S (3 of them: units of 16 rows
+// 36.3 us instead of 35.5, 4 long requests of 32 rows a kv head 191 instead of 187).
+constexpr int kAhead = 4;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNone = -3.0e38f;      // reference of a row that has seen nothing
 constexpr float kDead = 3.0e38f;       // ... of a column that is no row: its weights are zero
@@ -100,11 +104,12 @@ struct AttnParams {
 
 // What steps and units count in a block's share, so that shares take alike: a
 // step in two streams kStep, one of more rows than that kWide; a unit what its
-// beginning and end take besides, where blocks have some steps each (in small
-// batches the longest share is what counts, and that is one step: 1 to 2 us more
-// with it). 4 long requests of 12 to 32 rows a kv head: 177 us, with kWide = kStep
-// 200 (requests of 64 rows alone, whose shares that leaves the same size, 100 and
-// 96). kUnit = 12 and 0: 256 short requests 76 and 90, 32 of 64 rows 100 and 124.
+// beginning and end take besides. 4 long requests of 12 to 32 rows a kv head 180 us,
+// with kWide = kStep 194 (requests of 64 rows alone, whose shares that leaves alike,
+// 87 and 85.5). With kUnit and kUnitWide zero: requests of 64 rows 111 us instead of
+// 87, units of 16 rows 36.6 and 35.5, 256 short requests 68.2 and 67.6. Where blocks
+// have few steps each the longest share is what counts, and that is one step: there
+// a step counts kStep and a unit nothing (5 small requests 11.6 us, otherwise 14.6).
 constexpr int kStep = 4, kWide = 5, kUnit = 8, kUnitWide = 20;
 
 // A request's work: units of N of a kv head's n * G rows, the tiles of a head
@@ -314,7 +319,10 @@ template <int D, int N>
 struct Cfg {
   static constexpr int kThreads = 512;
   static constexpr int kCodes = kKeys * D;             // a tile of codes
-  static constexpr int kK = D == 128 ? 4 : 8, kV = kK;    // stages: 64 KB of each
+  // Stages, 64 KB of K and of V. More in flight than that and HBM reads slower: with
+  // 80 and 96 KB 4 single tokens over 65K to 131K rows take 180 us instead of 166 (on
+  // another GPU 160 and 146), with 48 and 48 148, with 32 and 48 166.
+  static constexpr int kK = D == 128 ? 4 : 8, kV = kK;
   static constexpr int kQS = N == 16 ? 4 : 2;          // units of Q
   static constexpr int kQ = 2 * N * D;                 // both parts of a unit's rows
   static constexpr int kPW = N == 16 ? 64 : 128;       // bytes of a key's row of P (3N used)
@@ -1113,11 +1121,12 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 // Joins the pieces of a unit that several blocks hold, in block order: block
 // (c, y) takes rows of the unit that starts in block c, a row by `share` of its
 // four warps, which take the pieces in turn (all four where rows are few: one
-// request of 8192 rows, 2 a kv head, 13.5 us, by one warp 15.8; 16 rows 38.8 and 37.2). What it needs lies in one place,
-// since its time is that of the trips to L2 it makes one behind the other (units
-// found by bisection of the requests' steps: 10 us for 64 decoded tokens), and
-// that of its blocks' launch, which the attention's registers leave no room for
-// before its own blocks end: no more of them than there can be rows.
+// request of 8192 rows, 2 a kv head, 13.5 us, by one warp 15.7; units of 16 rows 36.6
+// and 35.5). What it needs lies in one place, since its time is that of the trips to
+// L2 it makes one behind the other (units found by bisection of the requests' steps:
+// 10 us for 64 decoded tokens), and that of its blocks' launch, which the attention's
+// registers leave no room for before its own blocks end: no more of them than there
+// can be rows.
 template <int D, int N>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
@@ -1236,9 +1245,9 @@ mis_status_t check_desc(const mis_paged_attn_desc* d, const mis_paged_cache_q8* 
 int head_rows(const mis_paged_attn_desc* d, const mis_paged_cache_q8* c) { return d->max_rows * (d->Hq / c->Hkv); }
 
 // Rows of a unit. More than 32 rows of a kv head are several units over the same
-// keys. Units of 16 and of 32: 64 requests of 16 rows 37.2 and 39.4 us, 256 short
-// ones of 2 rows 76 and 94; 32 of 32 rows a kv head 109 and 100 (4 long ones, of
-// which one has 32 rows and the others fewer than 17, 171 and 177).
+// keys. Units of 16 and of 32: 64 requests of 16 rows 35.4 and 37.6 us, 256 short
+// ones of 2 rows 67 and 79; 4 long ones of 32 rows 349 and 186, 32 of 64 rows 99 and
+// 87 (4 long ones, of which one has 32 rows and the others fewer than 17, 169 and 176).
 int unit_rows(const mis_paged_attn_desc* d, const mis_paged_cache_q8* c) { return head_rows(d, c) <= 16 ? 16 : 32; }
 
 struct AttnWs { size_t flags, meta, rl, part, total; };
