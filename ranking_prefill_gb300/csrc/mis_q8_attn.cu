@@ -33,11 +33,12 @@
 //
 // A row's key scale multiplies its score, its value scale its probability. The
 // softmax keeps two things per row: a reference r below which weights are
-// taken, and l = sum 2^(s - r). Products use P = 2^(s - r + e_v - 28): r is the
-// largest s + e_v - 32 seen, moved only when one passes it by 2^4, so P stays below
+// taken, and l = sum 2^(s - r). Products use P = 2^(s - r + e_v - 16): r is the
+// largest s + e_v - 20 seen, moved only when one passes it by 2^4, so P stays below
 // 2^8 (where 16 and 64 times the rests stay within e4m3) and its largest above 2^4,
-// whatever the spread of the value scales; 2^(s - r) stays within fp32 for every e_v
-// in [-56, 120].
+// whatever the spread of the value scales. 2^(s - r) lies between 2^-100 and 2^80
+// for the largest of every e_v in [-56, 120], with room in fp32 for sums and for
+// what adds 24 bits below; s - r is about 20 - e_v, rounded at that size.
 //
 // Work is cut evenly between blocks, not at requests: every block adds up the
 // 128-key steps of all units (request, kv head, row tile) from the lengths on
@@ -313,6 +314,11 @@ __device__ __forceinline__ int fold16(float* v, int lane) {
   const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
   v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
   return col;
+}
+
+// ln(sum * 2^r), 2^20 taken out of the sum: near 1 the logarithm's bits are finest
+__device__ __forceinline__ float lse_of(float r, float sum) {
+  return ((r + 20.f) + log2f(sum * 9.5367431640625e-7f)) * kLn2;
 }
 
 template <int D, int N>
@@ -786,7 +792,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           const uint32_t hide = *reinterpret_cast<const uint32_t*>(e + 256);
           const float kf = pow2(q8_exp(e[r]));
           const int ev = q8_exp(e[128 + r]);
-          const float vs = pow2(ev - 28), most = 36.f - (float)ev;
+          const float vs = pow2(ev - 16), most = 24.f - (float)ev;
           const int key = k * kKeys + r;
           if (ok) {
             tmem_ld_wait();
@@ -847,7 +853,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             {
               float v[16];
 #pragma unroll
-              for (int n = 0; n < 16; ++n) v[n] = fmaf(__uint_as_float(s[n]), kf, (float)(ev - 32));
+              for (int n = 0; n < 16; ++n) v[n] = fmaf(__uint_as_float(s[n]), kf, (float)(ev - 20));
               const int n = fold16<true>(v, lane);
               mx[sw * N + n] = v[0];
             }
@@ -1000,8 +1006,8 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           const float a0 = ex2(r0 - mx), a1 = ex2(r1 - mx);
           sum = a0 * ((l0[0] + l0[N]) + (l0[2 * N] + l0[3 * N]));
           if (two) sum += a1 * ((l1[0] + l1[N]) + (l1[2 * N] + l1[3 * N]));
-          // the products' weights carry 2^-28; NaN stays
-          const float inv = whole ? (sum != 0.f ? __fdividef(268435456.f, sum) : 0.f) : 1.f;
+          // the products' weights carry 2^-16; NaN stays
+          const float inv = whole ? (sum != 0.f ? __fdividef(65536.f, sum) : 0.f) : 1.f;
           wt[lane] = a0 * inv;
           wt[N + lane] = a1 * inv;
         }
@@ -1012,7 +1018,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             p.rl[(int64_t)piece * N + lane] = make_float2(mx, sum);
           else if (p.lse)
             p.lse[(int64_t)(h * p.G + (at[lane] & 255)) * p.T + w.j.row0 + (at[lane] >> 8)] =
-                sum != 0.f ? (mx + __log2f(sum)) * kLn2 : -INFINITY;
+                sum != 0.f ? lse_of(mx, sum) : -INFINITY;
         }
         __syncwarp();
         ok = spin_all(bar(bOF + slot), (lu >> 1) & 1, W, 0x810);
@@ -1213,8 +1219,8 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
   }
   if (!live) return;
   const int i = (u.w + n) / p.G, head = u.z * p.G + u.w + n - i * p.G;
-  // the products' weights carry 2^-28
-  const float inv = sum != 0.f ? __fdividef(268435456.f, sum) : 0.f;
+  // the products' weights carry 2^-16
+  const float inv = sum != 0.f ? __fdividef(65536.f, sum) : 0.f;
   uint32_t out[E / 2];
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) out[e] = sum != 0.f ? pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv) : 0u;
@@ -1222,7 +1228,7 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
   if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
   else *reinterpret_cast<uint32_t*>(dst) = out[0];
   if (p.lse && lane == 0)
-    p.lse[(int64_t)head * p.T + v.x + i] = sum != 0.f ? (m + __log2f(sum)) * kLn2 : -INFINITY;
+    p.lse[(int64_t)head * p.T + v.x + i] = sum != 0.f ? lse_of(m, sum) : -INFINITY;
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

@@ -477,6 +477,51 @@ def held(c, slots, which):
     return codes[slots], exps[slots]
 
 
+def test_layers_back_to_back_are_the_same_as_one_call_at_a_time():
+    """Norms, store and attention of 12 layers over reused buffers, each layer's
+    output the next one's queries: every call starts before the one before has ended."""
+    r = np.random.default_rng(11)
+    B, hq, hkv, D, page = 5, 8, 4, 128, 32
+    lens = [300, 77, 1500, 33, 640]
+    pages = [-(-n // page) for n in lens]
+    table = np.full((B, max(pages)), -1, np.int32)
+    perm, at = r.permutation(sum(pages)), 0
+    for b, n in enumerate(pages):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    shape = (sum(pages), page, hkv, D)
+    start = [torch.as_tensor(r.integers(0, 0x7E, shape, dtype=np.uint8)).cuda() for _ in range(2)]
+    exps = torch.full((shape[0], hkv, page), 127 - 6, dtype=torch.uint8).cuda()
+    caches = [lib.PagedCacheQ8(*(x.clone() for x in start), exps.clone(), exps.clone()) for _ in range(12)]
+    pos = i32([n - 1 for n in lens])
+    slots = i32([table[b, (n - 1) // page] * page + (n - 1) % page for b, n in enumerate(lens)])
+    q0, k, v = (draw(r, B, h, D).cuda() for h in (hq, hkv, hkv))
+    w = draw(r, D).cuda()
+    desc = lib.PagedAttentionDesc(caches[0], B=B, T=B, Hq=hq, max_rows=1)
+    descs = [lib.PagedAttentionDesc(c, B=B, T=B, Hq=hq, max_rows=1) for c in caches]
+    w2, s = torch.empty(desc.workspace_size(), dtype=torch.uint8, device="cuda"), ws()
+    dt, dl, dc = i32(table), i32(lens), i32(np.arange(B + 1))
+
+    def layers(pause):
+        q, o, lse = q0.clone(), torch.empty_like(q0), torch.empty(hq, B, device="cuda")
+        torch.cuda.synchronize()
+        for c, d in zip(caches, descs):
+            lib.mis_qk_norm_rope(q, None, q, None, pos, w)
+            pause()
+            lib.mis_paged_write_kv_q8(c, k, v, slots, s, pos, BASE, None, w, EPS)
+            pause()
+            lib.mis_paged_attention_q8_fwd(d, q, o, lse, dt, dl, dc, w2)
+            pause()
+            q, o = o, q
+        torch.cuda.synchronize()
+        return q.clone(), lse.clone()
+    want = layers(torch.cuda.synchronize)
+    assert torch.isfinite(want[0].float()).all()
+    for _ in range(10):
+        got = layers(lambda: None)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_calls_on_a_stream_of_their_own():
     r = np.random.default_rng(8)
     st = torch.cuda.Stream()
