@@ -11,9 +11,9 @@
 // Both kernels touch every byte once, so HBM bounds them: D / 16 lanes share a
 // row of a head in the store (maximum and mean in 2 or 3 exchanges, as the
 // rotation's pairs lie in a lane), and D / 16 lanes read one back. 128K rows of 8
-// heads, 128 wide, are stored in 146 us and read back in 135 (5.5 and 6.0 TB/s of
-// the 6.8 that a copy reaches); a few rows cost a launch, 2.3 to 2.9 us. Narrow rows
-// are bound by their angles: 128K rows of one head 42 us both ways, their bytes 15.
+// heads, 128 wide, are stored in 146 us and read back in 120 (5.5 and 6.7 TB/s of
+// the 6.8 that a copy reaches); a few rows cost a launch, 2.3 to 2.5 us. Narrow rows
+// are bound by their angles: 128K rows of one head 40 us both ways, their bytes 15.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -238,12 +238,12 @@ struct ReadParams {
   uint32_t* status;
 };
 
-// 16 codes times 2^e as bf16.
-__device__ __forceinline__ void put_values(const uint4& codes, float scale, __nv_bfloat16* dst) {
-  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t o[8];
+// 8 codes times 2^e as bf16.
+__device__ __forceinline__ void put_values(const uint2& codes, float scale, __nv_bfloat16* dst) {
+  const uint32_t w[2] = {codes.x, codes.y};
+  uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t h = e4m3x2_to_half2((uint16_t)(w[i] >> (16 * j)));
@@ -252,9 +252,7 @@ __device__ __forceinline__ void put_values(const uint4& codes, float scale, __nv
       o[2 * i + j] = pack_bf16(lo * scale, hi * scale);
     }
   }
-  uint4* d = reinterpret_cast<uint4*>(dst);
-  d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <int D>
@@ -278,13 +276,18 @@ mis_paged_read_q8_kernel(const __grid_constant__ ReadParams p) {
     if (!p.own_check) raise_status(p.status, kDevIndex, 0x50);
     return;
   }
-  const int64_t at = code_at(p.c, s) + (int64_t)h * p.c.head_stride + c * 16, ex = exp_at(p.c, s, h);
-  const uint4 kc = *reinterpret_cast<const uint4*>(p.c.k + at);
-  const uint4 vc = *reinterpret_cast<const uint4*>(p.c.v + at);
-  const int ke = q8_exp(p.c.ke[ex]), ve = q8_exp(p.c.ve[ex]);
-  const int64_t to = (int64_t)h * D + c * 16;
-  put_values(kc, pow2(ke), p.k + i * p.ks + to);
-  put_values(vc, pow2(ve), p.v + i * p.vs + to);
+  // a lane's 8 elements of each half of the head: its 16 bytes of a store lie beside
+  // its neighbours' (16 elements a lane, every other 16 bytes a store: 135 us, not 120)
+  const int64_t at = code_at(p.c, s) + (int64_t)h * p.c.head_stride + c * 8, ex = exp_at(p.c, s, h);
+  const uint2 ka = *reinterpret_cast<const uint2*>(p.c.k + at), kb = *reinterpret_cast<const uint2*>(p.c.k + at + D / 2);
+  const uint2 va = *reinterpret_cast<const uint2*>(p.c.v + at), vb = *reinterpret_cast<const uint2*>(p.c.v + at + D / 2);
+  const float ke = pow2(q8_exp(p.c.ke[ex])), ve = pow2(q8_exp(p.c.ve[ex]));
+  __nv_bfloat16* k = p.k + i * p.ks + (int64_t)h * D + c * 8;
+  __nv_bfloat16* v = p.v + i * p.vs + (int64_t)h * D + c * 8;
+  put_values(ka, ke, k);
+  put_values(kb, ke, k + D / 2);
+  put_values(va, ve, v);
+  put_values(vb, ve, v + D / 2);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
