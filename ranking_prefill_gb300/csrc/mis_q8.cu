@@ -32,8 +32,8 @@ constexpr int kThreads = 256, kStoreThreads = 128;
 // One block looks over every index beside the copy where that takes no longer
 // than the copy. Else the status word is cleared by a node of its own and the
 // rows' own threads raise it. Both ways, stored and read back: 32 rows of 8 x 128
-// 4.7 and 11.8 us, 8,192 of 1 x 64 7.4 and 12.7; 131,072 of 1 x 64 101 and 42, of
-// 2 x 128 134 and 102, of 4 x 128 166 and 167, of 8 x 128 292 and 300.
+// 4.5 and 11.0 us, 8,192 of 1 x 64 7.2 and 12.6; 131,072 of 1 x 64 99 and 39, of
+// 2 x 128 133 and 100, of 4 x 128 160 and 158, of 8 x 128 263 and 272.
 constexpr int kCheckRows = 8192, kCheckCells = 512;
 
 struct Q8Cache {
@@ -130,10 +130,9 @@ __device__ __forceinline__ void put_row(const float* x, const float* y, float m,
 }
 
 // U heads of a row at a time: nothing of one waits for another. Two where a thread
-// has more than one, stored and read back: 128K rows of 8 x 128 290 us, one at a
-// time 317 (before the lines that are asked for ahead: 278); one where it has one:
-// 32 rows 4.7 us and 5.1, 128K rows of 1 x 64 42 and 47. Blocks of 128: 292 us, of
-// 256 299 to 307 (more of them stay resident).
+// has more than one, stored and read back: 128K rows of 8 x 128 263 us, one at a
+// time 300; one where it has one: 32 rows 4.5 us, 5.1 by two, 128K rows of 1 x 64 39
+// and 46. Blocks of 128: 263 us, of 256 268 (more of them stay resident).
 template <int D, int U>
 __global__ void __launch_bounds__(kStoreThreads, 4)
 mis_paged_write_q8_kernel(const __grid_constant__ StoreParams p) {
