@@ -692,8 +692,11 @@ mis_status_t mis_paged_read_kv_q8(const mis_paged_cache_q8* cache, const int32_t
  * are q, at one row stride). fp32 scores, statistics and accumulation. Elements
  * of q count as they are down to 2^-14 of their row's largest, and to within
  * 2^-22 of it below that; a key's weight (its probability times the scale of its
- * value row) is rounded to 11 bits, and to within 2^-24 of the row's largest
- * weight where it is below 2^-13 of that; o is rounded to bf16. The same call
+ * value row) is rounded to 11 bits, and to within 2^-36 of the row's largest
+ * weight where it is below 2^-25 of that (beside value rows with elements above
+ * 2^118 it is zero there); the products are added by the tensor core in fp32,
+ * which cuts each some 25 bits below the sum, so that n keys may together be off
+ * by n * 2^-25 of the largest weighted value; o is rounded to bf16. The same call
  * gives the same bits. Two kernels. A wait inside the first can last as long as
  * a block works on one request, about 1 us per 128 cached rows (see
  * mis_set_wait_limit_ns()); one that runs out leaves rows that its block has a

@@ -9,14 +9,23 @@
 // side of the products, as in mis_tree.cu:
 //     S^T [128 keys x 2N] = K Q^T        (A = K tile, B = Q in two parts)
 //     O^T [D x 3N]       += V^T P^T      (A = V tile, MN-major, B = P in three)
-// with N = 16 or 32 rows a tile, all of it e4m3: K and V go from the cache to
+// with N = 16 or 32 rows a tile, all of it in 8 bits: K and V go from the cache to
 // the tensor core as they lie there, and what the softmax computes anyway is
-// what gets split. Q's parts are its leading 4 bits and 32 times the rest, in
-// units of a power of two of each row: exact for bf16 elements down to 2^-14 of
-// the row's largest, within 2^-22 of that below. P is rounded to fp16 (11 bits)
-// and split into 4 bits, 16 times the next 4, 1024 times the last 3: exact, but
-// that weights below 2^-13 of the largest lose bits, to within 2^-24 of it. The
-// parts' products stand in columns of their own and are added when they are read.
+// what gets split. Q's parts are its leading 4 bits and 32 times the rest, both
+// e4m3, in units of a power of two of each row: exact for bf16 elements down to
+// 2^-14 of the row's largest, within 2^-22 of that below. P is rounded to fp16 and
+// split into its nearest e5m2, 16 times what is left, 16 times what that leaves:
+// exact for every fp16 up to 2^15, subnormals too (a code has 3 bits, so its rest is
+// a bit and more shorter than what is below them: 11, 7, 3 bits). The largest
+// weight of a row lies in [2^11, 2^15], so one keeps 11 bits down to 2^-25 of it and
+// is within 2^-36 of it below that (values above 2^118: weights below 2^-26 are
+// zero, 2^(s - r) having left fp32). Three e4m3 parts, at the same times, lost bits
+// from 2^-13 on and all below 2^-24, which the sum of the weights kept: 131,072 keys
+// 2^-24.6 of one more left o 0.5% off. What stays is the tensor core's: products
+// are added in fp32 and cut some 25 bits below the sum, so n weights that small
+// beside one lose up to n 2^-25 of its value (1M of 2^-26 beside one of the same
+// value in one block: o 1.1% off). The parts' products stand in columns of their
+// own and are added when they are read.
 // (V converted to fp16 by a warpgroup of its own and P in one part took 64 decoded
 // tokens over 512 to 4096 rows 74 us and 4 requests of 117K rows 224; mma.sync with
 // K and V converted in registers 73 and 270; this form took 57 and 178 before the
@@ -33,9 +42,9 @@
 //
 // A row's key scale multiplies its score, its value scale its probability. The
 // softmax keeps two things per row: a reference r below which weights are
-// taken, and l = sum 2^(s - r). Products use P = 2^(s - r + e_v - 16): r is the
+// taken, and l = sum 2^(s - r). Products use P = 2^(s - r + e_v - 9): r is the
 // largest s + e_v - 20 seen, moved only when one passes it by 2^4, so P stays below
-// 2^8 (where 16 and 64 times the rests stay within e4m3) and its largest above 2^4,
+// 2^15 (where 16 times the rests stay within e5m2) and its largest above 2^11,
 // whatever the spread of the value scales. 2^(s - r) lies between 2^-100 and 2^80
 // for the largest of every e_v in [-56, 120], with room in fp32 for sums and for
 // what adds 24 bits below; s - r is about 20 - e_v, rounded at that size.
@@ -249,17 +258,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
-// Two half floats as e4m3 codes (the low 16 bits).
-__device__ __forceinline__ uint16_t e4m3x2_of_half2(uint32_t h) {
+// Two half floats as e5m2 codes (the low 16 bits), to the nearest.
+__device__ __forceinline__ uint16_t e5m2x2_of_half2(uint32_t h) {
   uint16_t c;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
   return c;
 }
-// times (p - c), for the codes c of p: exact.
-__device__ __forceinline__ uint32_t rest(uint32_t p, uint16_t codes, uint32_t times) {
+// 16 (p - c), for the codes c of p (a code is the upper byte of its half float): exact.
+__device__ __forceinline__ uint32_t rest(uint32_t p, uint16_t codes) {
   uint32_t d;
   asm("{.reg .b32 t; sub.rn.f16x2 t, %1, %2; mul.rn.f16x2 %0, t, %3;}"
-      : "=r"(d) : "r"(p), "r"(e4m3x2_to_half2(codes)), "r"(times));
+      : "=r"(d) : "r"(p), "r"(__byte_perm(codes, 0u, 0x1404)), "r"(0x4c004c00u));
   return d;
 }
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
@@ -272,8 +281,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// kind::f8f6f4, e4m3 both, fp32 accumulate.
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// kind::f8f6f4, fp32 accumulate.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -538,7 +547,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     } else if (warp == 1) {
       // --------------------------------------------------------------- products
       constexpr uint32_t idS = (1u << 4) | ((uint32_t)(2 * N >> 3) << 17) | (8u << 24);
-      constexpr uint32_t idO = (1u << 4) | (1u << 15) | (1u << 16) | (8u << 24), idO48 = idO | (48u >> 3) << 17, idO96 = idO | (96u >> 3) << 17;
+      constexpr uint32_t idO = (1u << 4) | (1u << 10) | (1u << 15) | (1u << 16) | (8u << 24), idO48 = idO | (48u >> 3) << 17, idO96 = idO | (96u >> 3) << 17;
       bool ok = true;
       if (p.stall) ok = spin_all(bar(bDR), 0, W, 0x7ff);       // nothing arrives before the drain
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -608,13 +617,13 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const uint64_t b2 = rows_desc<C::kPW>(base + C::oP + pb * C::kP, 0);
             const int nks = (x >> 3) & 7;
             const uint32_t id = both ? idO96 : idO48;
-            mma_e4m3(d, a, b2, id, (x & 1) ^ 1u);
+            mma_f8(d, a, b2, id, (x & 1) ^ 1u);
             if (nks == kKeys / 32) {
 #pragma unroll
-              for (int y = 1; y < kKeys / 32; ++y) mma_e4m3(d, a + y * (2 * D), b2 + y * (2 * C::kPW), id, 1u);
+              for (int y = 1; y < kKeys / 32; ++y) mma_f8(d, a + y * (2 * D), b2 + y * (2 * C::kPW), id, 1u);
             } else {
 #pragma unroll 1
-              for (int y = 1; y < nks; ++y) mma_e4m3(d, a + y * (2 * D), b2 + y * (2 * C::kPW), id, 1u);
+              for (int y = 1; y < nks; ++y) mma_f8(d, a + y * (2 * D), b2 + y * (2 * C::kPW), id, 1u);
             }
             mma_commit(bar(bPV + pb));
             if (x & 4) mma_commit(bar(bOF + (unit & 1)));
@@ -623,7 +632,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const uint32_t d = tm + colS(ts % kAhead);
             const uint64_t a = rows_desc<D>(base + sk * C::kCodes, 0), q = rows_desc<D>(base + C::oQ + sq * C::kQ, 0);
 #pragma unroll
-            for (int y = 0; y < D / 32; ++y) mma_e4m3(d, a + 2 * y, q + 2 * y, idS, y != 0);
+            for (int y = 0; y < D / 32; ++y) mma_f8(d, a + 2 * y, q + 2 * y, idS, y != 0);
             mma_commit(bar(bSF + ts % kAhead));
             mma_commit(bar(bKE + sk));
           }
@@ -792,7 +801,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           const uint32_t hide = *reinterpret_cast<const uint32_t*>(e + 256);
           const float kf = pow2(q8_exp(e[r]));
           const int ev = q8_exp(e[128 + r]);
-          const float vs = pow2(ev - 16), most = 24.f - (float)ev;
+          const float vs = pow2(ev - 9), most = 24.f - (float)ev;
           const int key = k * kKeys + r;
           if (ok) {
             tmem_ld_wait();
@@ -906,10 +915,10 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
               float p0, p1;
               f2_unpack(f2_mul(w2, v2), p0, p1);
               const uint32_t h = half2_of(p0, p1);
-              const uint16_t a = e4m3x2_of_half2(h);
-              const uint32_t h1 = rest(h, a, 0x4c004c00u);          // 16
-              const uint16_t b = e4m3x2_of_half2(h1);
-              const uint16_t c = e4m3x2_of_half2(rest(h1, b, 0x54005400u));     // 64
+              const uint16_t a = e5m2x2_of_half2(h);
+              const uint32_t h1 = rest(h, a);
+              const uint16_t b = e5m2x2_of_half2(h1);
+              const uint16_t c = e5m2x2_of_half2(rest(h1, b));
               (y ? hi : lo)[0] = a;
               (y ? hi : lo)[1] = b;
               (y ? hi : lo)[2] = c;
@@ -1006,8 +1015,8 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           const float a0 = ex2(r0 - mx), a1 = ex2(r1 - mx);
           sum = a0 * ((l0[0] + l0[N]) + (l0[2 * N] + l0[3 * N]));
           if (two) sum += a1 * ((l1[0] + l1[N]) + (l1[2 * N] + l1[3 * N]));
-          // the products' weights carry 2^-16; NaN stays
-          const float inv = whole ? (sum != 0.f ? __fdividef(65536.f, sum) : 0.f) : 1.f;
+          // the products' weights carry 2^-9; NaN stays
+          const float inv = whole ? (sum != 0.f ? __fdividef(512.f, sum) : 0.f) : 1.f;
           wt[lane] = a0 * inv;
           wt[N + lane] = a1 * inv;
         }
@@ -1054,7 +1063,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           auto add = [&](int stream) {
 #pragma unroll
             for (int n = 0; n < CH; ++n) {
-              const float x = fmaf(__uint_as_float(y[stream][2][n]), 0.0009765625f,
+              const float x = fmaf(__uint_as_float(y[stream][2][n]), 0.00390625f,
                                    fmaf(__uint_as_float(y[stream][1][n]), 0.0625f, __uint_as_float(y[stream][0][n])));
               ov[n] = fmaf(wt[stream * N + e0 + q + n], x, ov[n]);
             }
@@ -1219,8 +1228,8 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
   }
   if (!live) return;
   const int i = (u.w + n) / p.G, head = u.z * p.G + u.w + n - i * p.G;
-  // the products' weights carry 2^-16
-  const float inv = sum != 0.f ? __fdividef(65536.f, sum) : 0.f;
+  // the products' weights carry 2^-9
+  const float inv = sum != 0.f ? __fdividef(512.f, sum) : 0.f;
   uint32_t out[E / 2];
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) out[e] = sum != 0.f ? pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv) : 0u;

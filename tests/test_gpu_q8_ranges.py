@@ -35,3 +35,52 @@ def test_as_many_indices_as_32_bits_count():
         lib.mis_paged_write_kv_q8(ca.c, x.cuda(), x.cuda(), slots, s, src_rows=rows)
         assert lib.mis_get_device_status(s) == lib.MIS_ERR_DEVICE_INDEX
         where[n - 1] = was
+
+
+# ------------------------------------------------------------------- attention
+
+def shared(kc, ke, vc, ve, q, lens, ns, scale):
+    """Requests whose tables name the same pages. Returns o and lse."""
+    c = lib.PagedCacheQ8(kc, vc, ke, ve)
+    B, T, hq = len(lens), int(sum(ns)), q.shape[1]
+    desc = lib.PagedAttentionDesc(c, B=B, T=T, Hq=hq, max_rows=max(ns), scale=scale)
+    w = torch.full((desc.workspace_size(),), 0xA5, dtype=torch.uint8, device="cuda")
+    o, lse = torch.full_like(q, 7.0), torch.full((hq, T), 7.0, device="cuda")
+    lib.mis_paged_attention_q8_fwd(desc, q, o, lse, i32(np.tile(np.arange(c.n_pages), (B, 1))), i32(lens),
+                                   i32(np.concatenate([[0], np.cumsum(ns)])), w)
+    assert lib.mis_get_device_status(w) == lib.MIS_OK
+    return f64(o), f64(lse)
+
+
+@pytest.mark.parametrize("hq,D", [(8, 128), (8, 64), (160, 128), (160, 64)])
+@pytest.mark.parametrize("at", [5, 70000, 131071])
+def test_a_key_that_rules_a_long_cache(hq, D, at):
+    """One key 2^24 to 2^26 above 131,071 others: these weigh half a percent together,
+    with values that share a mean. More units than blocks, so that a block takes a
+    unit whole. Off by: o's rounding; the weights' (2^-11 of their size) and their
+    arguments' (2^-17); the sum of weights, of which a thread adds up to 1,024 (2^-14);
+    131,071 products that the tensor core may cut at 2^-24 of a sum of at most 2^-3.5:
+    2^-10.5, whatever the weights. So no error that grows with their number is let by."""
+    L, hkv, B, page = 131072, 8, 20, 256
+    g = torch.Generator(device="cuda").manual_seed(at)
+    lut = torch.tensor([0x30, 0x38, 0x3C, 0x38], dtype=torch.uint8, device="cuda")       # 0.5, 1, 1.5, 1
+    vc = lut[torch.randint(0, 4, (L // page, page, hkv, D), generator=g, device="cuda")]
+    v0 = torch.tensor([0x00, 0x08, 0x10, 0x18, 0x88, 0x94], dtype=torch.uint8, device="cuda").repeat(D)[:D]   # |v| <= 2^-4
+    vc[at // page, at % page] = v0
+    kc = torch.zeros_like(vc)
+    kc[at // page, at % page, :, 0] = 0x38
+    ke, ve = (torch.full((L // page, hkv, page), 127, dtype=torch.uint8, device="cuda") for _ in range(2))
+    v = vc.view(torch.float8_e4m3fn).float()
+    first = f64(v0.view(torch.float8_e4m3fn).float())
+    others = np.repeat(f64(v.double().sum(dim=(0, 1))) - first, hq // hkv, axis=0)
+    q = torch.zeros(B, hq, D, dtype=BF16, device="cuda")
+    q[..., 0] = 1.0
+    for p in (24.2, 24.6, 25.3, 26.0):
+        scale = float(np.float32(p * np.log(2.0)))
+        o, lse = shared(kc, ke, vc, ve, q, [L] * B, [1] * B, scale)
+        w = np.exp(-scale)
+        total = 1 + w * (L - 1)
+        ref, av = (first + w * others) / total, (np.abs(first) + w * others) / total
+        tol = 2.0 ** -8 * np.abs(ref) + av * (2.0 ** -11 + 2.0 ** -17 + 2.0 ** -14) + 2.0 ** -10.5
+        assert (np.abs(o - ref) <= tol).all(), (p, np.abs(o - ref).max(), tol.min())
+        assert np.abs(lse - (scale + np.log(total))).max() <= 2.0 ** -13
