@@ -47,7 +47,10 @@
 // 2^15 (where 16 times the rests stay within e5m2) and its largest above 2^11,
 // whatever the spread of the value scales. 2^(s - r) lies between 2^-100 and 2^80
 // for the largest of every e_v in [-56, 120], with room in fp32 for sums and for
-// what adds 24 bits below; s - r is about 20 - e_v, rounded at that size.
+// what adds 24 bits below; s - r is about 20 - e_v, rounded at that size. r can move
+// by more than fp32's exponents hold (a row of zeros, e_v = -56, and one of 2^80
+// behind it): l of before, 2^76 a key, then still counts, so its factor is taken as
+// a root that multiplies twice. What O held is 2^-126 of what comes and may go.
 //
 // Work is cut evenly between blocks, not at requests: every block adds up the
 // 128-key steps of all units (request, kv head, row tile) from the lengths on
@@ -356,7 +359,8 @@ struct Cfg {
   static constexpr int wMax = wL + 16 * N;             // [2][4][N] maxima of a step by stream and warp
   static constexpr int wRef = wMax + 8 * N;            // [2][4][N] a warp's copy of the references, negated
   static constexpr int wAl = wRef + 8 * N;             // [2][4][N] ... of the factors of a move
-  static constexpr int wWt = wAl + 8 * N;              // [4][2][N] an epilogue warp's weights of the streams
+  static constexpr int wAh = wAl + 8 * N;              // [2][4][N] ... of their roots
+  static constexpr int wWt = wAh + 8 * N;              // [4][2][N] an epilogue warp's weights of the streams
   static constexpr int wNf = wWt + 8 * N;              // [2][2] NaN taken out of V tiles, by unit and stream
   static constexpr int kWords = wNf + 4;
   static constexpr int oBar = oW + 4 * kWords;
@@ -772,6 +776,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const int str = two ? wg : 0, c0 = two ? 0 : 16 * wg, parts = two ? 16 : 32;
         float* ref = words + C::wRef + (str * 4 + sw) * N + c0;
         float* al = words + C::wAl + (str * 4 + sw) * N + c0;
+        float* ah = words + C::wAh + (str * 4 + sw) * N + c0;
         float* mx = words + C::wMax + str * 4 * N + c0;
         ok = spin(bar(bQF + sq), (lu / QS) & 1, W, 0x700) &&
              (lu < 2 || spin(bar(bSE + (lu - 2) % QS), ((lu - 2) / QS) & 1, W, 0x701));
@@ -874,7 +879,9 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 #pragma unroll
               for (int q = 0; q < 4; ++q) to = fmaxf(to, mx[q * N + lane]);
               if (c0 + lane >= rows) to = kDead;
-              al[lane] = to > old ? ex2(old - to) : 1.f;
+              const float root = to > old ? ex2(0.5f * (old - to)) : 1.f;
+              al[lane] = root * root;
+              ah[lane] = root;
               ref[lane] = -to;
             }
             __syncwarp();
@@ -894,8 +901,10 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
                 tmem_st_wait();
 #pragma unroll
-                for (int n = 0; n < 8; ++n)
-                  l2[n] = f2_mul(l2[n], f2_pack(__float_as_uint(al[2 * n]), __float_as_uint(al[2 * n + 1])));
+                for (int n = 0; n < 8; ++n) {
+                  const uint64_t root = f2_pack(__float_as_uint(ah[2 * n]), __float_as_uint(ah[2 * n + 1]));
+                  l2[n] = f2_mul(f2_mul(l2[n], root), root);
+                }
               }
             }
             weigh();
@@ -1012,9 +1021,9 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           const float* l1 = l0 + 4 * N;
           const float r0 = words[C::wR + slot * 2 * N + lane], r1 = two ? words[C::wR + (slot * 2 + 1) * N + lane] : kNone;
           mx = fmaxf(r0, r1);
-          const float a0 = ex2(r0 - mx), a1 = ex2(r1 - mx);
-          sum = a0 * ((l0[0] + l0[N]) + (l0[2 * N] + l0[3 * N]));
-          if (two) sum += a1 * ((l1[0] + l1[N]) + (l1[2 * N] + l1[3 * N]));
+          const float h0 = ex2(0.5f * (r0 - mx)), h1 = ex2(0.5f * (r1 - mx)), a0 = h0 * h0, a1 = h1 * h1;
+          sum = h0 * (h0 * ((l0[0] + l0[N]) + (l0[2 * N] + l0[3 * N])));
+          if (two) sum += h1 * (h1 * ((l1[0] + l1[N]) + (l1[2 * N] + l1[3 * N])));
           // the products' weights carry 2^-9; NaN stays
           const float inv = whole ? (sum != 0.f ? __fdividef(512.f, sum) : 0.f) : 1.f;
           wt[lane] = a0 * inv;
@@ -1202,12 +1211,13 @@ mis_q8_join_kernel(const __grid_constant__ AttnParams p, int share) {
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll 1
   for (int y = sub; y < pieces; y += 2 * share) {
-    const float f0 = ex2(rl0.x - m), f1 = y + share < pieces ? ex2(rl1.x - m) : 0.f;
-    sum += f0 * rl0.y;
+    const float h0 = ex2(0.5f * (rl0.x - m)), h1 = y + share < pieces ? ex2(0.5f * (rl1.x - m)) : 0.f;
+    const float f0 = h0 * h0, f1 = h1 * h1;
+    sum += h0 * (h0 * rl0.y);
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] += f0 * z0[e];
     if (y + share < pieces) {
-      sum += f1 * rl1.y;
+      sum += h1 * (h1 * rl1.y);
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] += f1 * z1[e];
     }

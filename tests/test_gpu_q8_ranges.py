@@ -84,3 +84,28 @@ def test_a_key_that_rules_a_long_cache(hq, D, at):
         tol = 2.0 ** -8 * np.abs(ref) + av * (2.0 ** -11 + 2.0 ** -17 + 2.0 ** -14) + 2.0 ** -10.5
         assert (np.abs(o - ref) <= tol).all(), (p, np.abs(o - ref).max(), tol.min())
         assert np.abs(lse - (scale + np.log(total))).max() <= 2.0 ** -13
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,hkv,B", [(2, 2, 1), (1, 1, 1), (8, 8, 20), (160, 8, 20), (24, 1, 1)])
+@pytest.mark.parametrize("L", [2, 130, 300, 2001, 20001])
+def test_values_at_both_ends_of_the_exponents(hq, hkv, B, D, L):
+    """Rows of tiny or no values, then one of far larger ones, all with the same score:
+    every key has a share in the sum, in streams, steps, blocks and their join. Off by:
+    the weights and o, each rounded; L roundings of the sum at most."""
+    page = 64
+    n_pages = -(-L // page)
+    kc = torch.zeros(n_pages, page, hkv, D, dtype=torch.uint8, device="cuda")
+    ke = torch.full((n_pages, hkv, page), 127, dtype=torch.uint8, device="cuda")
+    q = torch.zeros(B, hq, D, dtype=BF16, device="cuda")
+    for low, high, code in ((71, 207, 0x00), (71, 247, 0x38), (71, 198, 0x00), (100, 247, 0x38)):
+        for at in sorted({0, L // 2, L - 1}):
+            vc = torch.full_like(kc, code)
+            ve = torch.full_like(ke, low)
+            vc[at // page, at % page] = 0x38
+            ve[at // page, :, at % page] = high
+            o, lse = shared(kc, ke, vc, ve, q, [L] * B, [1] * B, 1.0)
+            ref = (2.0 ** (high - 127) + (L - 1) * (2.0 ** (low - 127) if code else 0.0)) / L
+            slack = 2.0 ** -8 + 2.0 ** -11 + L * 2.0 ** -24
+            assert (np.abs(o - ref) <= slack * ref).all(), (low, high, at, o.ravel()[0] / ref)
+            assert np.abs(lse - np.log(L)).max() <= L * 2.0 ** -24 + 2.0 ** -17, (low, high, at)
