@@ -593,8 +593,10 @@ mis_status_t mis_tree_attention_fwd(const mis_tree_desc* desc, const mis_paged_c
  *                  angle is kept as a 64-bit fraction of a turn: off by
  *                  p * 2^-54 of a turn, its sine and cosine by 2^-22
  *   rope_base    — > 1, read only with position_ids
- * fp32 throughout, rounded once to bf16. Infinities and NaN stay in their (row,
- * head). One kernel, no workspace; T = 0 enqueues nothing.
+ * fp32 throughout, rounded once to bf16; heads whose squares leave fp32 are scaled
+ * by a power of two first, so that one of any size comes out right (of zeros
+ * alone with eps = 0: NaN). Infinities and NaN stay in their (row, head). One
+ * kernel, no workspace; T = 0 enqueues nothing.
  * ------------------------------------------------------------------------ */
 mis_status_t mis_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
                               int64_t q_row_stride, int64_t k_row_stride, int64_t q_out_row_stride,

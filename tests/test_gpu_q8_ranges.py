@@ -5,9 +5,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import q8_oracle as Q
 from q8_helpers import BF16, f64, i32
 from ranking_prefill_gb300 import lib
-from test_gpu_q8_rows import Cache, check_exact, draw, ws
+from test_gpu_q8_rows import BASE, Cache, check_exact, check_near, draw, near_bf16, positions, ws
 
 pytestmark = pytest.mark.gpu
 
@@ -35,6 +36,55 @@ def test_as_many_indices_as_32_bits_count():
         lib.mis_paged_write_kv_q8(ca.c, x.cuda(), x.cuda(), slots, s, src_rows=rows)
         assert lib.mis_get_device_status(s) == lib.MIS_ERR_DEVICE_INDEX
         where[n - 1] = was
+
+
+# ----------------------------------------------------------------------- norms
+
+SIZES = [2.0 ** p for p in (0, 40, 61, 63, 64, 90, 124, -30, -55, -60, -74, -90, -110)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [len(SIZES), 1000 * len(SIZES)])
+@pytest.mark.parametrize("eps", [0.0, 1e-37, 1e-30, 1e-6])
+def test_norms_of_rows_whose_squares_leave_fp32(D, T, eps):
+    """Every size beside every other one in a row's heads; normed in both forms and on the way
+    to the cache. Errors as in the ordinary range (2^-18); elements 2^60 below their
+    row's size may lose bits at fp32's least ones."""
+    r = np.random.default_rng(D)
+    hq, hkv = 7, 4
+    x = draw(r, T, hq + hkv, D, spread=0.0).double()
+    size = np.stack([np.roll(SIZES, h)[np.arange(T) % len(SIZES)] for h in range(hq + hkv)], axis=1)
+    x = (x.clamp(-8, 8) * torch.as_tensor(size)[..., None]).to(BF16)
+    x[:, 1, ::3] = 0.0
+    qw, kw = draw(r, D, spread=0.0), draw(r, D, spread=0.0)
+    pos = positions(r, T)
+    qo, ko = torch.empty(T, hq, D, dtype=BF16).cuda(), torch.empty(T, hkv, D, dtype=BF16).cuda()
+    d = x.cuda()
+    lib.mis_qk_norm_rope(d[:, :hq], d[:, hq:], qo, ko, i32(pos), qw.cuda(), kw.cuda(), eps=eps, base=BASE)
+    for got, rows, w in ((qo, x[:, :hq], qw), (ko, x[:, hq:], kw)):
+        ref, pair = Q.rope(Q.norm(f64(rows), f64(w), eps), pos, BASE)
+        near_bf16(got, ref, pair * 2.0 ** -18)
+    ca, s = Cache(T // 16 + 1, 16, hkv, D), ws()
+    k = d[:, hq:].contiguous()
+    lib.mis_paged_write_kv_q8(ca.c, k, k, i32(np.arange(T)), s, i32(pos), BASE, k_weight=kw.cuda(), eps=eps)
+    kc, ke, vc, ve = ca.rows()
+    check_near(kc[:T], ke[:T], ref, pair * 2.0 ** -18 + 1e-38)
+    check_exact(vc[:T], ve[:T], f64(k))
+
+
+def test_norms_without_eps_of_rows_of_zeros_and_infinities():
+    """0 / 0 and inf / inf are NaN, what stands beside an infinity is zero, and no other row is touched."""
+    x = torch.full((4, 8, 128), 3.0, dtype=BF16)
+    x[0, 2] = 0.0
+    x[1, 3, 7] = float("inf")
+    x[2, 4, 100] = float("nan")
+    x[3, 5] = torch.finfo(BF16).max
+    w, o = torch.ones(128, dtype=BF16).cuda(), torch.empty(4, 8, 128, dtype=BF16).cuda()
+    lib.mis_qk_norm_rope(x.cuda(), None, o, None, None, w, eps=0.0)
+    want = torch.ones(4, 8, 128)
+    want[0, 2], want[1, 3], want[2, 4] = float("nan"), 0.0, float("nan")
+    want[1, 3, 7] = float("nan")
+    assert np.array_equal(f64(o), f64(want), equal_nan=True)
 
 
 # ------------------------------------------------------------------- attention
