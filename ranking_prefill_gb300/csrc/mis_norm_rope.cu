@@ -139,6 +139,9 @@ extern "C" mis_status_t mis_qk_norm_rope(const void* q, const void* k, void* q_o
                                          const void* k_weight, float eps, const int32_t* position_ids,
                                          double rope_base, void* stream) {
   if (T < 0 || Hq < 0 || Hkv < 0 || Hq + (int64_t)Hkv < 1) return MIS_ERR_INVALID_ARG;
+  // a tensor without heads: nothing of it is looked at
+  if (Hq == 0) { q = q_out = nullptr; q_weight = nullptr; q_row_stride = q_out_row_stride = 0; }
+  if (Hkv == 0) { k = k_out = nullptr; k_weight = nullptr; k_row_stride = k_out_row_stride = 0; }
   if (D != 64 && D != 128) return MIS_ERR_UNSUPPORTED;
   if ((int64_t)Hq + Hkv > 65536) return MIS_ERR_UNSUPPORTED;
   if ((q_weight || k_weight) && !(eps >= 0.f && eps <= 1.f)) return MIS_ERR_INVALID_ARG;

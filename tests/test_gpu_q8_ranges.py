@@ -87,6 +87,22 @@ def test_norms_without_eps_of_rows_of_zeros_and_infinities():
     assert np.array_equal(f64(o), f64(want), equal_nan=True)
 
 
+@pytest.mark.parametrize("left_out", ["q", "k"])
+def test_nothing_of_a_tensor_without_heads_is_looked_at(left_out):
+    """Its addresses, its weight's and its strides may be anything."""
+    r = np.random.default_rng(3)
+    x, w, pos = draw(r, 33, 3, 64).cuda(), draw(r, 64).cuda(), i32(np.arange(33))
+    want, got = torch.empty_like(x), torch.full_like(x, 7.0)
+    lib.mis_qk_norm_rope(x, None, want, None, pos, w)
+    live = (x.data_ptr(), got.data_ptr(), 3 * 64, 3 * 64, 3, w.data_ptr())
+    none = (0x1002, 0x2001, -5, 3, 0, 0x3004)
+    q, k = (none, live) if left_out == "q" else (live, none)
+    st = lib.load().mis_qk_norm_rope(q[0], k[0], q[1], k[1], q[2], k[2], q[3], k[3], 33, q[4], k[4], 64, q[5], k[5], 1e-6,
+                                     pos.data_ptr(), BASE, None)
+    torch.cuda.synchronize()
+    assert st == lib.MIS_OK and torch.equal(got, want)
+
+
 # ------------------------------------------------------------------- attention
 
 def shared(kc, ke, vc, ve, q, lens, ns, scale):
