@@ -8,7 +8,7 @@ import torch
 from oracle import q8_oracle as Q
 from q8_helpers import BF16, f64, i32
 from ranking_prefill_gb300 import lib
-from test_gpu_q8_rows import BASE, Cache, check_exact, check_near, draw, near_bf16, positions, ws
+from test_gpu_q8_rows import BASE, Cache, check_exact, check_near, draw, near_bf16, positions, transform, ws
 
 pytestmark = pytest.mark.gpu
 
@@ -39,6 +39,33 @@ def test_as_many_indices_as_32_bits_count():
 
 
 # ----------------------------------------------------------------------- norms
+
+@pytest.mark.parametrize("hq,hkv", [(13, 3), (10, 6), (5, 6), (8, 8), (3, 9)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompts_normed_four_heads_at_a_time(hq, hkv, D):
+    """Tokens so many that a thread takes all heads of one: groups of four that end in a
+    tensor, at its end and past it, apart from the input and over it."""
+    T = 10000 + hq
+    r = np.random.default_rng(hq)
+    qkv = draw(r, T, hq + hkv + 1, D).cuda()
+    q, k, rest = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:].clone()
+    qw, kw, pos = draw(r, D).cuda(), draw(r, D).cuda(), positions(r, T)
+    qo, ko = torch.full((T, hq, D), 7.0, dtype=BF16).cuda(), torch.full((T, hkv, D), 7.0, dtype=BF16).cuda()
+    lib.mis_qk_norm_rope(q, k, qo, ko, i32(pos), qw, kw, base=BASE)
+    near_bf16(qo, *transform(q, qw, pos))
+    near_bf16(ko, *transform(k, kw, pos))
+    if hkv >= 8:
+        k1 = torch.zeros_like(ko)
+        lib.mis_qk_norm_rope(None, k, None, k1, i32(pos), k_weight=kw, base=BASE)
+        assert torch.equal(k1, ko)
+    # one tensor normed, the other turned alone
+    q2, k2 = torch.empty_like(qo), torch.empty_like(ko)
+    lib.mis_qk_norm_rope(q, k, q2, k2, i32(pos), None, kw, base=BASE)
+    near_bf16(q2, *transform(q, None, pos))
+    assert torch.equal(k2, ko)
+    lib.mis_qk_norm_rope(q, k, q, k, i32(pos), qw, kw, base=BASE)
+    assert torch.equal(q, qo) and torch.equal(k, ko) and torch.equal(qkv[:, hq + hkv:], rest)
+
 
 SIZES = [2.0 ** p for p in (0, 40, 61, 63, 64, 90, 124, -30, -55, -60, -74, -90, -110)]
 
