@@ -1031,13 +1031,7 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         const int* at = reinterpret_cast<const int*>(words) + C::wAt + sq * N;
         const int* lim = reinterpret_cast<const int*>(words) + C::wLim + sq * N;
-        if (sw == 0 && lane < rows) {
-          if (!whole)
-            p.rl[(int64_t)piece * N + lane] = make_float2(mx, sum);
-          else if (p.lse)
-            p.lse[(int64_t)(h * p.G + (at[lane] & 255)) * p.T + w.j.row0 + (at[lane] >> 8)] =
-                sum != 0.f ? lse_of(mx, sum) : -INFINITY;
-        }
+        if (sw == 0 && lane < rows && !whole) p.rl[(int64_t)piece * N + lane] = make_float2(mx, sum);
         __syncwarp();
         ok = spin_all(bar(bOF + slot), (lu >> 1) & 1, W, 0x810);
         if (!ok) break;
@@ -1122,6 +1116,10 @@ mis_q8_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             }
           }
         }
+        // not before O was there: a sum whose waits ran out on the way is not written
+        if (sw == 0 && lane < rows && whole && p.lse)
+          p.lse[(int64_t)(h * p.G + (at[lane] & 255)) * p.T + w.j.row0 + (at[lane] >> 8)] =
+              sum != 0.f ? lse_of(mx, sum) : -INFINITY;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bSE + sq));
         ++lu;

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from oracle import q8_oracle as Q
-from q8_helpers import BF16, f64, i32
+from q8_helpers import BF16, Batch, f64, i32
 from ranking_prefill_gb300 import lib
 from test_gpu_q8_rows import BASE, Cache, check_exact, check_near, draw, near_bf16, positions, transform, ws
 
@@ -202,3 +202,27 @@ def test_values_at_both_ends_of_the_exponents(hq, hkv, B, D, L):
             slack = 2.0 ** -8 + 2.0 ** -11 + L * 2.0 ** -24
             assert (np.abs(o - ref) <= slack * ref).all(), (low, high, at, o.ravel()[0] / ref)
             assert np.abs(lse - np.log(L)).max() <= L * 2.0 ** -24 + 2.0 ** -17, (low, high, at)
+
+
+@pytest.mark.parametrize("ns", [[1, 3, 2, 1], [9, 2, 12, 5]])
+def test_what_is_written_beside_waits_that_run_out_is_right(ns):
+    """Limits of 0 to 9 us: every element of o and lse is either as it was or as in a
+    call whose waits last, to the bit, whatever the status."""
+    b = Batch([20000, 40, 3000, 500], ns, 8, 2, 128, 16, seed=80).run().check()
+    o, lse = b.o.clone(), b.lse.clone()
+    assert not o.isnan().any() and not lse.isnan().any()
+    limit = lib.mis_set_wait_limit_ns(0)
+    try:
+        for t in list(range(0, 2000, 50)) + list(range(2000, 9000, 250)):
+            lib.mis_set_wait_limit_ns(t)
+            b.o.fill_(float("nan"))
+            b.lse.fill_(float("nan"))
+            b.call()
+            status = lib.mis_get_device_status(b.ws)
+            assert status in (lib.MIS_OK, lib.MIS_ERR_DEVICE_TIMEOUT)
+            for got, want in ((b.o, o), (b.lse, lse)):
+                there = ~got.isnan()
+                assert torch.equal(got[there], want[there])
+                assert status != lib.MIS_OK or there.all()
+    finally:
+        lib.mis_set_wait_limit_ns(limit)
