@@ -581,7 +581,8 @@ mis_status_t mis_tree_attention_fwd(const mis_tree_desc* desc, const mis_paged_c
  *     the pair (y[i], y[i + D/2]) turns by p * rope_base^(-2i/D).
  *   q, k, q_out, k_out — device bf16 [T, heads, D], row strides in elements
  *                  (>= heads*D, multiples of 8), 16-byte aligned. Hq = 0 or
- *                  Hkv = 0 leaves that tensor out (its pointers are not read).
+ *                  Hkv = 0 leaves that tensor out (its addresses, strides and
+ *                  weight are not looked at).
  *                  An output may be its own input at the same row stride (in
  *                  place); another overlap of an output with an argument is
  *                  MIS_ERR_INVALID_ARG. Columns of one buffer at one row stride
@@ -674,7 +675,8 @@ mis_status_t mis_paged_read_kv_q8(const mis_paged_cache_q8* cache, const int32_t
  *               128 query heads a kv head
  *   max_rows  — upper bound on a request's new rows, 1 .. MIS_PAGED_MAX_ROWS
  *   scale     — softmax scale of size 1e-20 to 1e20, of either sign; 0 selects
- *               1/sqrt(D). scale * q_i k_j has to stay within fp32's range
+ *               1/sqrt(D). scale * q_i k_j has to stay within fp32's range,
+ *               and so has its size over the 2^e of k_j
  *   q, o, lse, row strides — as in mis_attention_fwd_plan (lse fp32 [Hq, T] or
  *               NULL). Rows from cu_rows[B] on are not written
  *   block_table — device int32 [B, max_pages], row stride in elements;

@@ -11,7 +11,7 @@
 // angles of a lane's 8 pairs serve every head that its thread takes. 128K tokens
 // of 24 heads, 128 wide, take 241 us (6.7 TB/s of the 6.8 that a copy reaches),
 // without the next heads' way to L2 254, one head at a time 314; 4,099 of 16 heads,
-// 64 wide, 7.2 us; 32 tokens 3.0, a launch.
+// 64 wide, 7.5 us; 32 tokens 3.0, a launch.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -74,7 +74,7 @@ mis_qk_norm_rope_kernel(const __grid_constant__ NormParams p) {
   // the U heads from h on come to L2, a lane a line of 128 bytes: loads of the
   // next ones in registers would cost half the blocks
   auto ahead = [&](int h) {
-    constexpr int LH = D / 64, W = NC / LH;
+    constexpr int LH = D / 64;
     const int x = h + c / LH;
     const __nv_bfloat16* at = (x < p.Hq ? p.q + t * p.qs : p.k + t * p.ks - (int64_t)p.Hq * D) + (int64_t)x * D + (c % LH) * 64;
     if (x < h1 && c / LH < U) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
@@ -185,7 +185,7 @@ extern "C" mis_status_t mis_qk_norm_rope(const void* q, const void* k, void* q_o
   const int H = Hq + Hkv;
   // an angle serves all heads of a thread; a row's heads are split over
   // threads only while its lanes alone would leave SMs idle (4,099 tokens of 16
-  // heads: 512 threads an SM 7.2 us, 1,024 8.1)
+  // heads, 64 wide: 512 threads an SM 7.5 us, 1,024 8.4)
   const int64_t cells = (int64_t)T * (D / 16), want = 512 * (int64_t)num_sms();
   const int64_t split = std::max<int64_t>(1, std::min<int64_t>(H, want / cells));
   p.hpt = (int32_t)((H + split - 1) / split);
@@ -194,8 +194,11 @@ extern "C" mis_status_t mis_qk_norm_rope(const void* q, const void* k, void* q_o
   if (blocks > 0x7fffffff) return MIS_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   try {
-    // four heads at a time where a thread has that many: 128K tokens of 24 heads
-    // 252 us, two at a time 270; 4,099 tokens of 16 heads, two a thread, 10.7 and 8.2
+    // four heads at a time where a thread has eight or more: 128K tokens of 24 heads
+    // 241 us, two at a time 256, of 8 heads 96 and 101, 16K of 24 36.6 and 38.2. Below,
+    // the last four are mostly not full: 128K of 6 heads 88 and 81, 2,400 of 24, six a
+    // thread, 11.3 and 10.3 (of 7 heads 92 and 96; 4,099 of 16, four a thread, 7.1 and
+    // 7.6; 9 heads of 128K 115 either way)
     const bool many = p.hpt >= 8;
     auto kern = D == 128 ? (many ? mis_qk_norm_rope_kernel<128, 4> : mis_qk_norm_rope_kernel<128, 2>)
                          : (many ? mis_qk_norm_rope_kernel<64, 4> : mis_qk_norm_rope_kernel<64, 2>);

@@ -13,7 +13,10 @@
 // rotation's pairs lie in a lane), and D / 16 lanes read one back. 128K rows of 8
 // heads, 128 wide, are stored in 146 us and read back in 120 (5.5 and 6.7 TB/s of
 // the 6.8 that a copy reaches); a few rows cost a launch, 2.3 to 2.5 us. Narrow rows
-// are bound by their angles: 128K rows of one head 40 us both ways, their bytes 15.
+// are bound by one chain a thread (slot, row, exchange, store) at 512 threads an SM:
+// 128K rows of 1 x 64 are stored in 25 us, 19 without norm and angles, and read in 13,
+// where the bytes take 7.6 each way; of 4 x 128 by the look at the indices, 97 and 90
+// (60).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -32,8 +35,8 @@ constexpr int kThreads = 256, kStoreThreads = 128;
 // One block looks over every index beside the copy where that takes no longer
 // than the copy. Else the status word is cleared by a node of its own and the
 // rows' own threads raise it. Both ways, stored and read back: 32 rows of 8 x 128
-// 4.5 and 11.0 us, 8,192 of 1 x 64 7.2 and 12.6; 131,072 of 1 x 64 99 and 39, of
-// 2 x 128 133 and 100, of 4 x 128 160 and 158, of 8 x 128 263 and 272.
+// 4.5 and 11.0 us, 8,192 of 1 x 64 7.2 and 12.6; 131,072 of 1 x 64 99 and 40, of
+// 2 x 128 133 and 101, of 4 x 128 159 and 158, of 8 x 128 264 and 272.
 constexpr int kCheckRows = 8192, kCheckCells = 512;
 
 struct Q8Cache {
@@ -132,9 +135,9 @@ __device__ __forceinline__ void put_row(const float* x, const float* y, float m,
 }
 
 // U heads of a row at a time: nothing of one waits for another. Two where a thread
-// has more than one, stored and read back: 128K rows of 8 x 128 263 us, one at a
-// time 300; one where it has one: 32 rows 4.5 us, 5.1 by two, 128K rows of 1 x 64 39
-// and 46. Blocks of 128: 263 us, of 256 268 (more of them stay resident).
+// has more than one, stored and read back: 128K rows of 8 x 128 264 us, one at a
+// time 300; one where it has one: 32 rows 4.5 us, 5.1 by two, 128K rows of 1 x 64 40
+// and 46. Blocks of 128: 264 us, of 256 269 (more of them stay resident).
 template <int D, int U>
 __global__ void __launch_bounds__(kStoreThreads, 4)
 mis_paged_write_q8_kernel(const __grid_constant__ StoreParams p) {

@@ -29,16 +29,18 @@
 // (V converted to fp16 by a warpgroup of its own and P in one part took 64 decoded
 // tokens over 512 to 4096 rows 74 us and 4 requests of 117K rows 224; mma.sync with
 // K and V converted in registers 73 and 270; this form took 57 and 178 before the
-// steps noted below, 51 to 55 and 161 to 170 with them, by the GPU.)
+// steps noted below, 51 to 56 and 161 to 170 with them, by the GPU.)
 //
 // What bounds it: the K/V stream in long caches (4 single tokens over 65K to 131K
-// rows 146 to 166 us, 5.8 to 6.6 TB/s where a copy reaches 6.8; 5.1 to 5.5 at 64 x
+// rows 146 to 168 us, 5.7 to 6.6 TB/s where a copy reaches 6.7; 5.1 to 5.5 at 64 x
 // 2.2K rows, which lose 6 us before the first product and 5 in the join); the
 // softmax's chain of a step where a unit has more than 16 rows (1,700 cycles for the
-// 32 KB of K and V that HBM brings in 1,440: 32 requests of 64 rows a kv head 85 us,
-// their stream 21); what a unit takes to begin and end where it has a few steps (256
-// requests of 100 to 600 rows 67 us, their stream 27); the chain of one step and the
-// second launch in small batches (4 requests of 100 to 300 rows 10.2 us).
+// 32 KB of K and V that HBM brings in 1,440: 32 requests of 64 rows a kv head 86 us,
+// their stream 21; of 128 155, of 256 288, every 32 rows walking the keys again); the
+// same chain at D = 64, where a step brings half the bytes (64 tokens over 512 to 8192
+// rows 75 us, their stream 40); what a unit takes to begin and end where it has a few
+// steps (256 requests of 100 to 600 rows 68 us, their stream 27); the chain of one step
+// and the second launch in small batches (4 requests of 100 to 300 rows 10.3 us).
 //
 // A row's key scale multiplies its score, its value scale its probability. The
 // softmax keeps two things per row: a reference r below which weights are

@@ -114,8 +114,9 @@ class Batch:
         roundings of at most the sum of their sizes, and the tensor core may cut
         instead of round: twice that), scaled by three more; the exponential is
         good to 2^-21. P is rounded to 11 bits (2^-11 of its size); held in steps
-        of 2^-17 where its largest is 2^6 at least, it is off by at most 2^-24 of
-        the largest weight for every key that weighs little. o is rounded to bf16."""
+        of 2^-24 where its largest is 2^11 at least, it is off by 2^-36 of the largest
+        weight for keys that weigh little. Each of l products may be cut at 2^-24 of
+        the largest as fp32 adds it. o is rounded to bf16."""
         o, lse, q = f64(self.o), f64(self.lse), f64(self.q)
         scale = self.scale or 1.0 / math.sqrt(self.D)
         for b, (l, n) in enumerate(zip(self.lens, self.ns)):
